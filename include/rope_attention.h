@@ -2,7 +2,7 @@
  * rope_attention.h -- C ABI of librope_attention.so, the GB300 (sm_103a)
  * attention-prologue hot path.
  *
- * Two operators:
+ * Two operators of the prologue, and (c) - (e) the attention that follows it:
  *
  *  (a) qkv_cte_mx: the fused QKV projection of the AWS Neuron page "Kernel
  *      reference: qkv_cte -- Wan2.2 additions to the NKI Library QKV CTE MXFP8
@@ -20,6 +20,12 @@
  *      (3) quantisation, (4) scatter, (5) is_output_kv; parameter table;
  *      cache/index constraint table), modes V1 (combined kv) and V2
  *      (separate kv with v_optional).
+ *
+ *  (c) packed_attention: softmax attention over whole prompts, on the columns
+ *      that (a) leaves in HBM.  (d) paged_attention: new tokens of sequences
+ *      against the caches that (b) fills.  (e) kv_cache_read: rows of those
+ *      caches gathered by slot and dequantised.  The pages end at the prologue;
+ *      these three take the layouts, dtypes and parameters of (a) and (b).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -39,8 +45,8 @@
  *    kv_rms_norm_rope_cache_status, dev_error_count).
  *  - bf16 values are passed as their 16-bit patterns (uint16_t).
  *  - qkv_cte_mx, qkv_cte_mx_project, qkv_cte_mx_norm_rope, row_quantize_e4m3,
- *    row_quantize_e4m3_packed, qkv_cte_mx_pack_weight and kv_rms_norm_rope_cache
- *    launch kernels only (no allocation, no synchronisation), so after one
+ *    row_quantize_e4m3_packed, qkv_cte_mx_pack_weight, kv_rms_norm_rope_cache,
+ *    packed_attention, paged_attention and kv_cache_read launch kernels only (no allocation, no synchronisation), so after one
  *    eager call per device they can be captured into a CUDA graph and
  *    replayed; the status readers synchronise and cannot be captured.
  */
@@ -375,6 +381,152 @@ ra_status kv_rms_norm_rope_cache_status(void* stream, int32_t* device_status);
  * reports RA_ERR_TIMEOUT.  Nothing is in flight when the waits give up.  The
  * caches of that call are undefined.  Applies to one call, then clears itself. */
 void ra_test_stall_next_kv_cache(void);
+
+/* ========================================================================
+ * (c) packed_attention
+ * ======================================================================== */
+
+/* Attention over B sequences whose tokens lie one after another:
+ *   out[i, h] = sum_j softmax_j(softmax_scale * q[i, h] . k[j, h / g]) v[j, h / g],
+ *   g = num_heads / num_kv_heads,
+ * over the keys j of query i's own sequence; with `causal`, query i of a sequence
+ * of Lq queries and Lk keys sees the keys j <= i + Lk - Lq (the last query sees
+ * every key).  A query that sees no key gives zeros (lse -inf). */
+typedef struct {
+  int64_t B;              /* sequences                                                 */
+  int64_t total_q;        /* query tokens (rows of q and out), >= 1, < 2^31            */
+  int64_t total_k;        /* key tokens (rows of k and v), >= 1, < 2^31                */
+  int32_t num_heads;      /* query heads; a multiple of num_kv_heads; <= 65535         */
+  int32_t num_kv_heads;
+  int32_t head_dim;       /* multiple of 16 up to 128                                  */
+  int32_t dtype;          /* RA_BF16 or RA_FP16, of q, k, v and out                    */
+  int32_t causal;         /* 0 or 1                                                    */
+  float softmax_scale;    /* finite, > 0 (head_dim^-0.5 as a rule)                     */
+  /* strides, in elements: element (token, head, c) of q is at
+   * token * q_token_stride + head * q_head_stride + c; k, v and out likewise.
+   * Multiples of 8, at least 0; every byte offset below 2^40.  In a BSD output of
+   * qkv_cte_mx the token stride is I and the head stride head_dim; in NBSd
+   * head_dim and B*S*head_dim. */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+} packed_attention_params;
+
+/* Workspace bytes of packed_attention (a status word and scratch).  Zero-fill it
+ * once after allocation.  Calls that may overlap need workspaces of their own. */
+ra_status packed_attention_workspace_bytes(const packed_attention_params* p, size_t* bytes);
+
+/* One call.
+ *   q, k, v       strided as above, 16-byte aligned; out likewise, no two elements of
+ *                 out in one place.  Every row of q, k and v inside a sequence must be
+ *                 finite; rows outside every sequence may hold anything and the
+ *                 matching rows of out (and lse) are left as they were.
+ *   lse           [total_q, num_heads] fp32: log of the sum of the exponentials, or NULL.
+ *   cu_seqlens_q  [B + 1] int32 on the device: sequence b has the query tokens
+ *                 cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (non-decreasing, at most
+ *                 total_q; values outside are clamped); NULL: every sequence has
+ *                 total_q / B tokens (total_q must be a multiple of B).
+ *   cu_seqlens_k  likewise for the keys; a sequence may have none.
+ *   workspace     >= packed_attention_workspace_bytes, 16-byte aligned.
+ * A device wait that ran out is reported by attention_status. */
+ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, const uint16_t* k,
+                           const uint16_t* v, uint16_t* out, float* lse, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ========================================================================
+ * (d) paged_attention
+ * ======================================================================== */
+
+/* Attention of new tokens (one per sequence when decoding, or a chunk) over the
+ * caches that kv_rms_norm_rope_cache writes, described by the same parameter
+ * struct.  Of `cache` the call uses N, Dkv, Dv, rope_size, variant, cache_mode,
+ * block_num, block_size, kv_dtype, k_cache_dtype, ckv_cache_dtype, cache_seq_len
+ * and the two scalar flags, and in NORM mode B.
+ *   V2: key = k_cache row [Dkv], value = ckv_cache row [Dv], N heads.
+ *   V1: key = (ckv_cache row, k_cache row) [Dkv], value = ckv_cache row [Dv]: the
+ *       latent row serves every head, so q holds the absorbed latent part first and
+ *       the rotated part behind it.
+ * A quantised element x is read as (code - offset) / scale (scales finite, not 0).
+ * The new tokens' own rows must already be in the cache: the Lq query tokens of a
+ * sequence are its last Lq positions, and with `causal` query i sees the
+ * positions <= seq_len - Lq + i.  A query that sees no key gives zeros (lse -inf).
+ * Built for V1 with Dv <= 512 (a multiple of 64) and rope_size <= 64 (a multiple
+ * of 16), and V2 with Dkv <= 256 and Dv <= 256 (multiples of 16): others are
+ * RA_ERR_UNSUPPORTED. */
+typedef struct {
+  int64_t B;                  /* sequences (in NORM mode the cache's B)                */
+  int64_t total_q;            /* query tokens, >= 1, < 2^31                            */
+  int32_t num_heads;          /* query heads; a multiple of the cache's N              */
+  int32_t causal;             /* 0 or 1                                                */
+  float softmax_scale;        /* finite, > 0                                           */
+  int32_t reserved;           /* 0                                                     */
+  int64_t max_seq_len;        /* no seq_lens value is larger (larger ones are clamped) */
+  int64_t block_table_stride; /* entries per row of block_table; 0 in NORM mode        */
+} paged_attention_params;
+
+/* Workspace bytes of paged_attention: a status word and the partial results of
+ * sequences that several blocks share (at most 64 MiB).  Zero-fill it once after
+ * allocation.  Calls that may overlap need workspaces of their own. */
+ra_status paged_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache,
+                                          const paged_attention_params* p, size_t* bytes);
+
+/* One call.
+ *   q             [total_q, num_heads, Dkv] kv_dtype, 16-byte aligned.
+ *   k_cache, ckv_cache  as kv_rms_norm_rope_cache leaves them; only the rows of the
+ *                 sequences' own positions are read.
+ *   seq_lens      [B] int32: positions in the cache, the new tokens included; 0 allowed.
+ *   block_table   [B, block_table_stride] int32 in the PA modes: position j of sequence
+ *                 b is in page block_table[b, j / block_size] at j % block_size.
+ *                 Entries behind a sequence's last page are not read.  NULL in NORM mode
+ *                 (position j is row j of the sequence's cache).
+ *   cu_seqlens_q  [B + 1] int32 as in packed_attention; NULL: total_q / B tokens each.
+ *   k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset  as given to
+ *                 kv_rms_norm_rope_cache.
+ *   out           [total_q, num_heads, Dv] kv_dtype, 16-byte aligned.
+ *   lse           [total_q, num_heads] fp32, or NULL.
+ *   dev_error_count  optional int32 device counter, raised when a page number that a
+ *                 sequence needs is outside [0, block_num): that page's keys are left out.
+ * A device wait that ran out is reported by attention_status. */
+ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                          const uint16_t* q, const void* k_cache, const void* ckv_cache,
+                          const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                          const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
+                          const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Synchronises `stream`, reads and clears the status word of a workspace of
+ * packed_attention or paged_attention and stores it in *device_status (0 = fine).
+ * Returns RA_ERR_TIMEOUT if a pipeline wait gave up since the last read (the
+ * outputs of that call are then undefined), else RA_OK. */
+ra_status attention_status(void* workspace, void* stream, int32_t* device_status);
+
+/* Test hook for failure detection.  The next packed_attention or paged_attention
+ * launch issues no loads, so its waits run out after the time limit of
+ * ra_set_wait_timeout_ns; every block records it in the workspace status word and
+ * exits, and attention_status reports RA_ERR_TIMEOUT.  Nothing is in flight when
+ * the waits give up.  Applies to one launch, then clears itself. */
+void ra_test_stall_next_attention(void);
+
+/* ========================================================================
+ * (e) kv_cache_read
+ * ======================================================================== */
+
+/* Reads rows back from the caches of kv_rms_norm_rope_cache: token (b, s) comes
+ * from the slot that a call with the same parameters and index would write it to,
+ *   k_out[b, n, s, :] = k_cache row,  c_kv_out[b, n, s, :] = ckv_cache row,
+ * as kv_dtype; a quantised element x as (code - offset) / scale in fp32, rounded
+ * once.  Of `p` the call uses B, N, S, Dkv, Dv, rope_size, variant, the cache
+ * fields, the dtypes and the scalar flags.
+ *   index         as in kv_rms_norm_rope_cache (here a slot may come several times).
+ *                 A token whose index is -1 gives zeros; so does one whose slot is
+ *                 outside the cache, which dev_error_count (optional) counts.
+ *   k_out         [B, N, S, k_w], c_kv_out [B, N, S, c_w], 16-byte aligned (k_w, c_w: the
+ *                 caches' row widths); either may be NULL, and is then not read.
+ * Asynchronous on `stream`, allocates nothing. */
+ra_status kv_cache_read(const kv_rms_norm_rope_cache_params* p, const int64_t* index, const void* k_cache,
+                        const void* ckv_cache, const float* k_rope_scale, const float* c_kv_scale,
+                        const float* k_rope_offset, const float* c_kv_offset, uint16_t* k_out,
+                        uint16_t* c_kv_out, int32_t* dev_error_count, void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "rope_attention.h"
+#include "attention.h"
 #include "internal.h"
 #include "kv_cache.h"
 #include "row_quant.h"
@@ -34,6 +35,7 @@ std::atomic<int64_t> g_wait_ns{2000000000LL};
 std::atomic<int> g_stall_next{0};  // ra_test_stall_next_projection
 std::atomic<int> g_stall_next_kv{0};  // ra_test_stall_next_kv_cache
 std::atomic<int> g_stall_next_norm{0};  // ra_test_stall_next_norm_rope
+std::atomic<int> g_stall_next_attn{0};  // ra_test_stall_next_attention
 std::atomic<int> g_validate_only{0};    // ra_test_validate_only
 
 // ra_test_validate_only: a call that passed its host checks returns here, before
@@ -260,6 +262,175 @@ ra_status run_norm_rope(const qkv_cte_mx_params* p, const QkvShape& s, const flo
   cudaError_t e = ra::launch_qk_norm_rope(L, st);
   if (e != cudaSuccess) return cuda_fail(e, "norm/rope launch");
   return RA_OK;
+}
+
+// ---------------------------------------------------------------- attention and the cache read
+int32_t quant_kind(int32_t dtype) {
+  return dtype == RA_INT8 ? ra::kQuantInt8 : dtype == RA_FP8_E4M3 ? ra::kQuantE4m3 : dtype == RA_FP8_E5M2 ? ra::kQuantE5m2 : -1;
+}
+
+// The caches of kv_rms_norm_rope_cache as a reader sees them: the checks of the
+// parameters that describe them, and their row widths and types.
+struct CacheShape {
+  int32_t kw, vw, kq, vq;
+};
+ra_status check_cache(const kv_rms_norm_rope_cache_params* p, const float* k_scale, const float* v_scale,
+                      const float* k_offset, const float* v_offset, CacheShape* s) {
+  if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "cache params is NULL");
+  if (p->kv_dtype != RA_BF16 && p->kv_dtype != RA_FP16) return fail(RA_ERR_INVALID_ARG, "kv dtype must be bf16 or fp16");
+  if (p->rope_size < 8 || p->rope_size % 8 != 0 || p->rope_size > 256)
+    return fail(RA_ERR_INVALID_ARG, "rope_size must be a multiple of 8 in [8, 256]");
+  if (p->Dkv < 8 || p->Dkv % 8 != 0 || p->Dkv > 4096 || p->Dv < 8 || p->Dv % 8 != 0 || p->Dv > 1024)
+    return fail(RA_ERR_INVALID_ARG, "Dkv and Dv must be positive multiples of 8 (Dv <= 1024)");
+  if (p->variant == 1) {
+    if (p->N != 1) return fail(RA_ERR_INVALID_ARG, "V1 (combined kv) supports N == 1 only");
+    if (p->Dv != p->Dkv - p->rope_size) return fail(RA_ERR_INVALID_ARG, "V1 needs Dv == Dkv - rope_size");
+  } else if (p->variant == 2) {
+    if (!(p->N == 1 || p->N == 2 || p->N == 4 || p->N == 8))
+      return fail(RA_ERR_INVALID_ARG, "V2 (separate kv) supports N in {1, 2, 4, 8}");
+    if (p->rope_size > p->Dkv) return fail(RA_ERR_INVALID_ARG, "rope_size exceeds Dkv");
+  } else {
+    return fail(RA_ERR_INVALID_ARG, "variant must be 1 or 2");
+  }
+  const int64_t rms = p->variant == 1 ? p->Dv : p->Dkv;
+  if (rms > 1024) return fail(RA_ERR_INVALID_ARG, "rms_size must be in [8, 1024]");
+  if ((k_offset && !k_scale) || (v_offset && !v_scale))
+    return fail(RA_ERR_INVALID_ARG, "an offset without its scale is illegal");
+  s->kq = k_scale ? quant_kind(p->k_cache_dtype) : 0;
+  s->vq = v_scale ? quant_kind(p->ckv_cache_dtype) : 0;
+  if (k_scale ? s->kq < 0 : p->k_cache_dtype != p->kv_dtype)
+    return fail(RA_ERR_INVALID_ARG, "k_cache dtype must be int8 or fp8 with a k scale, else equal to the kv dtype");
+  if (v_scale ? s->vq < 0 : p->ckv_cache_dtype != p->kv_dtype)
+    return fail(RA_ERR_INVALID_ARG, "ckv_cache dtype must be int8 or fp8 with a c_kv scale, else equal to the kv dtype");
+  const int32_t mode = p->cache_mode;
+  if (mode == RA_CACHE_PA_NZ || mode == RA_CACHE_PA_BLK_NZ)
+    return fail(RA_ERR_UNSUPPORTED, "FRACTAL_NZ cache modes are not built");
+  if (mode != RA_CACHE_NORM && mode != RA_CACHE_PA && mode != RA_CACHE_PA_BNSD && mode != RA_CACHE_PA_BLK_BNSD)
+    return fail(RA_ERR_INVALID_ARG, "unknown cache_mode");
+  if (mode == RA_CACHE_NORM) {
+    if (p->cache_seq_len < 1 || p->cache_seq_len > (1LL << 31))
+      return fail(RA_ERR_INVALID_ARG, "NORM mode needs cache_seq_len in [1, 2^31]");
+    if (p->variant == 1 && (k_scale || v_scale))
+      return fail(RA_ERR_INVALID_ARG, "V1 in NORM mode takes no quantisation parameters");
+  } else {
+    if (p->block_num < 1 || p->block_num > 0x7fffffffLL || p->block_size <= 1 || p->block_size > 0x7fffffffLL)
+      return fail(RA_ERR_INVALID_ARG, "block_num >= 1 and block_size > 1 (both below 2^31) are required");
+    if ((k_scale || v_scale) && p->block_size % 32 != 0)
+      return fail(RA_ERR_INVALID_ARG, "1-byte caches need block_size %% 32 == 0");
+    if ((!k_scale || !v_scale) && p->block_size % 16 != 0)
+      return fail(RA_ERR_INVALID_ARG, "2-byte caches need block_size %% 16 == 0");
+    if (p->block_num * p->block_size > (1LL << 40)) return fail(RA_ERR_INVALID_ARG, "too many cache slots");
+  }
+  if ((p->k_quant_scalar != 0 && p->k_quant_scalar != 1) || (p->c_kv_quant_scalar != 0 && p->c_kv_quant_scalar != 1))
+    return fail(RA_ERR_INVALID_ARG, "k_quant_scalar and c_kv_quant_scalar must be 0 or 1");
+  if (p->variant == 2 && (p->k_quant_scalar || p->c_kv_quant_scalar))
+    return fail(RA_ERR_INVALID_ARG, "V2 quantisation parameters are [N, D]; the [1] form is V1 only");
+  if ((p->k_quant_scalar && !k_scale) || (p->c_kv_quant_scalar && !v_scale))
+    return fail(RA_ERR_INVALID_ARG, "a [1] quantisation parameter flag needs its scale");
+  if ((k_scale && !aligned16(k_scale)) || (v_scale && !aligned16(v_scale)) || (k_offset && !aligned16(k_offset)) ||
+      (v_offset && !aligned16(v_offset)))
+    return fail(RA_ERR_ALIGNMENT, "scales and offsets must be 16-byte aligned");
+  s->kw = static_cast<int32_t>(p->variant == 1 ? p->rope_size : p->Dkv);
+  s->vw = static_cast<int32_t>(p->Dv);
+  return RA_OK;
+}
+
+bool good_scale(float s) { return std::isfinite(s) && s > 0.f; }
+
+ra_status check_packed(const packed_attention_params* p) {
+  if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "params is NULL");
+  if (p->B < 1 || p->total_q < 1 || p->total_k < 1)
+    return fail(RA_ERR_INVALID_ARG, "B, total_q and total_k must be >= 1 (no empty tensors)");
+  if (p->total_q > 0x7fffff00LL || p->total_k > 0x7fffff00LL || p->B > 0x00ffffffLL)
+    return fail(RA_ERR_INVALID_ARG, "too many tokens or sequences for 32-bit tile coordinates");
+  if (p->num_kv_heads < 1 || p->num_heads < 1 || p->num_heads % p->num_kv_heads != 0 || p->num_heads > 65535)
+    return fail(RA_ERR_INVALID_ARG, "num_heads must be a positive multiple of num_kv_heads, at most 65535");
+  if (p->head_dim < 16 || p->head_dim % 16 != 0)
+    return fail(RA_ERR_INVALID_ARG, "head_dim must be a positive multiple of 16");
+  if (p->head_dim > 128) return fail(RA_ERR_UNSUPPORTED, "packed_attention is built for head_dim up to 128");
+  if (p->dtype != RA_BF16 && p->dtype != RA_FP16) return fail(RA_ERR_INVALID_ARG, "dtype must be bf16 or fp16");
+  if (p->causal != 0 && p->causal != 1) return fail(RA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!good_scale(p->softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  const int64_t tokens[4] = {p->total_q, p->total_k, p->total_k, p->total_q};
+  const int64_t heads[4] = {p->num_heads, p->num_kv_heads, p->num_kv_heads, p->num_heads};
+  const int64_t ts[4] = {p->q_token_stride, p->k_token_stride, p->v_token_stride, p->out_token_stride};
+  const int64_t hs[4] = {p->q_head_stride, p->k_head_stride, p->v_head_stride, p->out_head_stride};
+  for (int i = 0; i < 4; ++i) {
+    if (ts[i] < 0 || hs[i] < 0) return fail(RA_ERR_INVALID_ARG, "strides must not be negative");
+    if (ts[i] % 8 != 0 || hs[i] % 8 != 0)
+      return fail(RA_ERR_ALIGNMENT, "strides must be multiples of 8 elements (16 bytes)");
+    if ((tokens[i] > 1 && ts[i] == 0) || (heads[i] > 1 && hs[i] == 0))
+      return fail(RA_ERR_INVALID_ARG, "an axis of more than one element needs a stride");
+    if ((tokens[i] > 1 && ts[i] >= (1LL << 39) / tokens[i]) || (heads[i] > 1 && hs[i] >= (1LL << 39) / heads[i]))
+      return fail(RA_ERR_INVALID_ARG, "a stride reaches past 2^40 bytes");
+  }
+  const int64_t d = p->head_dim, to = p->out_token_stride, ho = p->out_head_stride;
+  const bool apart = (p->num_heads == 1 || ho >= d) && (p->total_q == 1 || to >= d) &&
+                     (p->num_heads == 1 || p->total_q == 1 || to >= (p->num_heads - 1) * ho + d ||
+                      ho >= (p->total_q - 1) * to + d);
+  if (!apart) return fail(RA_ERR_INVALID_ARG, "out strides put two elements in one place");
+  return RA_OK;
+}
+
+ra_status check_attn_workspace(const void* workspace, size_t have, size_t need) {
+  if (!workspace) return fail(RA_ERR_INVALID_ARG, "workspace is required");
+  if (!aligned16(workspace)) return fail(RA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (have < need) return fail(RA_ERR_WORKSPACE, "workspace too small: %zu < %zu", have, need);
+  return RA_OK;
+}
+
+ra_status check_paged(const kv_rms_norm_rope_cache_params* c, const paged_attention_params* p, const CacheShape& s) {
+  if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "params is NULL");
+  if (p->B < 1 || p->total_q < 1) return fail(RA_ERR_INVALID_ARG, "B and total_q must be >= 1 (no empty tensors)");
+  if (p->num_heads < 1 || p->num_heads % c->N != 0)
+    return fail(RA_ERR_INVALID_ARG, "num_heads must be a positive multiple of the cache's N");
+  if (p->B > 0x00ffffffLL || p->total_q > 0x7fffffffLL || p->total_q * p->num_heads > 0x7fffffffLL)
+    return fail(RA_ERR_INVALID_ARG, "too many sequences or query rows (total_q * num_heads must stay below 2^31)");
+  if (p->causal != 0 && p->causal != 1) return fail(RA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (p->reserved != 0) return fail(RA_ERR_INVALID_ARG, "reserved must be 0");
+  if (!good_scale(p->softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (p->max_seq_len < 0 || p->max_seq_len > 0x7fffff00LL)
+    return fail(RA_ERR_INVALID_ARG, "max_seq_len must be in [0, 2^31 - 256]");
+  if (c->cache_mode == RA_CACHE_NORM) {
+    if (c->B != p->B) return fail(RA_ERR_INVALID_ARG, "NORM mode: the cache's B must equal the call's B");
+    if (p->block_table_stride != 0) return fail(RA_ERR_INVALID_ARG, "NORM mode takes no block table");
+  } else if (p->block_table_stride < 1 || p->block_table_stride > (1LL << 31)) {
+    return fail(RA_ERR_INVALID_ARG, "block_table_stride must be in [1, 2^31]");
+  }
+  if (c->variant == 1 ? (c->Dv > 512 || c->Dv % 64 != 0 || c->rope_size > 64 || c->rope_size % 16 != 0)
+                      : (c->Dkv > 256 || c->Dkv % 16 != 0 || c->Dv > 256 || c->Dv % 16 != 0))
+    return fail(RA_ERR_UNSUPPORTED,
+                "paged_attention is built for V1 with Dv a multiple of 64 up to 512 and rope_size 16..64, and V2 with "
+                "Dkv and Dv multiples of 16 up to 256");
+  (void)s;
+  return RA_OK;
+}
+
+ra::PagedLaunch paged_launch(const kv_rms_norm_rope_cache_params* c, const paged_attention_params* p,
+                             const CacheShape& s) {
+  ra::PagedLaunch L{};
+  L.B = p->B;
+  L.total_q = p->total_q;
+  L.N = c->N;
+  L.heads = p->num_heads;
+  L.Dkv = static_cast<int32_t>(c->Dkv);
+  L.Dv = static_cast<int32_t>(c->Dv);
+  L.R = c->rope_size;
+  L.variant = c->variant;
+  L.mode = c->cache_mode;
+  L.f16 = c->kv_dtype == RA_FP16;
+  L.kq = s.kq;
+  L.vq = s.vq;
+  L.k_scalar = c->k_quant_scalar;
+  L.v_scalar = c->c_kv_quant_scalar;
+  L.causal = p->causal;
+  L.scale = p->softmax_scale;
+  L.max_seq_len = p->max_seq_len;
+  L.block_num = c->block_num;
+  L.block_size = c->cache_mode == RA_CACHE_NORM ? 1 : c->block_size;
+  L.cache_seq = c->cache_seq_len;
+  L.table_stride = p->block_table_stride;
+  return L;
 }
 
 }  // namespace
@@ -597,6 +768,200 @@ ra_status kv_rms_norm_rope_cache_status(void* stream, int32_t* device_status) {
   if (e != cudaSuccess) return cuda_fail(e, "KV status read");
   *device_status = v;
   if (v != 0) return fail(RA_ERR_TIMEOUT, "a KV cache pipeline wait ran out of time (status %d)", v);
+  return ok();
+}
+
+void ra_test_stall_next_attention(void) { g_stall_next_attn.store(1); }
+
+ra_status packed_attention_workspace_bytes(const packed_attention_params* p, size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  const ra_status st = check_packed(p);
+  if (st != RA_OK) return st;
+  *bytes = ra::kAttnHeader;
+  return ok();
+}
+
+ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, const uint16_t* k,
+                           const uint16_t* v, uint16_t* out, float* lse, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
+  ra_status st = check_packed(p);
+  if (st != RA_OK) return st;
+  if (!q || !k || !v || !out) return fail(RA_ERR_INVALID_ARG, "q, k, v and out are required");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+    return fail(RA_ERR_ALIGNMENT, "q, k, v and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3u))
+    return fail(RA_ERR_ALIGNMENT, "lse and cu_seqlens must be 4-byte aligned");
+  if (!cu_seqlens_q && p->total_q % p->B != 0)
+    return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_q, total_q must be a multiple of B");
+  if (!cu_seqlens_k && p->total_k % p->B != 0)
+    return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_k, total_k must be a multiple of B");
+  st = check_attn_workspace(workspace, workspace_bytes, ra::kAttnHeader);
+  if (st != RA_OK) return st;
+  if (validate_only()) return ok();
+  ra::PackedLaunch L{};
+  L.q = q;
+  L.k = k;
+  L.v = v;
+  L.out = out;
+  L.lse = lse;
+  L.cu_q = cu_seqlens_q;
+  L.cu_k = cu_seqlens_k;
+  L.B = p->B;
+  L.total_q = p->total_q;
+  L.total_k = p->total_k;
+  L.q_ts = p->q_token_stride;
+  L.q_hs = p->q_head_stride;
+  L.k_ts = p->k_token_stride;
+  L.k_hs = p->k_head_stride;
+  L.v_ts = p->v_token_stride;
+  L.v_hs = p->v_head_stride;
+  L.o_ts = p->out_token_stride;
+  L.o_hs = p->out_head_stride;
+  L.nq = p->num_heads;
+  L.nkv = p->num_kv_heads;
+  L.d = p->head_dim;
+  L.causal = p->causal;
+  L.f16 = p->dtype == RA_FP16;
+  L.scale = p->softmax_scale;
+  L.status = static_cast<int32_t*>(workspace);
+  L.wait_ns = g_wait_ns.load();
+  L.stall_loads = g_stall_next_attn.exchange(0);
+  const char* why = "launch failed";
+  const cudaError_t e = ra::launch_packed_attention(L, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "packed_attention: %s (%s)", why, cudaGetErrorString(e));
+  return ok();
+}
+
+ra_status paged_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache,
+                                          const paged_attention_params* p, size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  if (cache == nullptr) return fail(RA_ERR_INVALID_ARG, "cache params is NULL");
+  // the scales are not at hand: a quantised dtype stands for its scale
+  const float* given = reinterpret_cast<const float*>(uintptr_t{16});
+  CacheShape s;
+  ra_status st = check_cache(cache, quant_kind(cache->k_cache_dtype) > 0 ? given : nullptr,
+                             quant_kind(cache->ckv_cache_dtype) > 0 ? given : nullptr, nullptr, nullptr, &s);
+  if (st == RA_OK) st = check_paged(cache, p, s);
+  if (st != RA_OK) return st;
+  *bytes = ra::paged_attention_workspace(paged_launch(cache, p, s));
+  return ok();
+}
+
+ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                          const uint16_t* q, const void* k_cache, const void* ckv_cache,
+                          const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                          const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
+                          const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  CacheShape s;
+  ra_status st = check_cache(cache, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, &s);
+  if (st == RA_OK) st = check_paged(cache, p, s);
+  if (st != RA_OK) return st;
+  if (!q || !k_cache || !ckv_cache || !seq_lens || !out)
+    return fail(RA_ERR_INVALID_ARG, "q, k_cache, ckv_cache, seq_lens and out are required");
+  if ((cache->cache_mode == RA_CACHE_NORM) != (block_table == nullptr))
+    return fail(RA_ERR_INVALID_ARG, "the PA modes need a block_table, NORM mode takes none");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(ckv_cache) || !aligned16(out))
+    return fail(RA_ERR_ALIGNMENT, "q, out and the caches must be 16-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(seq_lens) |
+        reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
+        reinterpret_cast<uintptr_t>(dev_error_count)) & 3u) != 0)
+    return fail(RA_ERR_ALIGNMENT, "lse, seq_lens, block_table, cu_seqlens_q and dev_error_count must be 4-byte aligned");
+  if (!cu_seqlens_q && p->total_q % p->B != 0)
+    return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_q, total_q must be a multiple of B");
+  ra::PagedLaunch L = paged_launch(cache, p, s);
+  st = check_attn_workspace(workspace, workspace_bytes, ra::paged_attention_workspace(L));
+  if (st != RA_OK) return st;
+  if (validate_only()) return ok();
+  L.q = q;
+  L.out = out;
+  L.lse = lse;
+  L.k_cache = k_cache;
+  L.v_cache = ckv_cache;
+  L.k_scale = k_rope_scale;
+  L.k_offset = k_rope_offset;
+  L.v_scale = c_kv_scale;
+  L.v_offset = c_kv_offset;
+  L.cu_q = cu_seqlens_q;
+  L.seq_lens = seq_lens;
+  L.table = block_table;
+  L.err_count = dev_error_count;
+  L.status = static_cast<int32_t*>(workspace);
+  L.partials = static_cast<uint8_t*>(workspace) + ra::kAttnHeader;
+  L.wait_ns = g_wait_ns.load();
+  L.stall_loads = g_stall_next_attn.exchange(0);
+  const char* why = "launch failed";
+  const cudaError_t e = ra::launch_paged_attention(L, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "paged_attention: %s (%s)", why, cudaGetErrorString(e));
+  return ok();
+}
+
+ra_status attention_status(void* workspace, void* stream, int32_t* device_status) {
+  if (!device_status) return fail(RA_ERR_INVALID_ARG, "device_status is required");
+  if (!workspace) return fail(RA_ERR_INVALID_ARG, "workspace is required");
+  if (!aligned16(workspace)) return fail(RA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (validate_only()) {
+    *device_status = 0;
+    return ok();
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int32_t v = 0;
+  cudaError_t e = cudaMemcpyAsync(&v, workspace, sizeof(v), cudaMemcpyDeviceToHost, cs);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
+  if (e == cudaSuccess && v != 0) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), cs);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
+  if (e != cudaSuccess) return cuda_fail(e, "attention status read");
+  *device_status = v;
+  if (v != 0) return fail(RA_ERR_TIMEOUT, "an attention pipeline wait ran out of time (status %d)", v);
+  return ok();
+}
+
+ra_status kv_cache_read(const kv_rms_norm_rope_cache_params* p, const int64_t* index, const void* k_cache,
+                        const void* ckv_cache, const float* k_rope_scale, const float* c_kv_scale,
+                        const float* k_rope_offset, const float* c_kv_offset, uint16_t* k_out,
+                        uint16_t* c_kv_out, int32_t* dev_error_count, void* stream) {
+  CacheShape s;
+  const ra_status st = check_cache(p, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, &s);
+  if (st != RA_OK) return st;
+  if (p->B < 1 || p->S < 1) return fail(RA_ERR_INVALID_ARG, "empty tensors are not supported");
+  if (p->S > (1LL << 31) || p->B > (1LL << 31) || p->B * p->N * p->S > (1LL << 40)) return fail(RA_ERR_INVALID_ARG, "too many rows");
+  if (!index || (!k_out && !c_kv_out) || (k_out && !k_cache) || (c_kv_out && !ckv_cache))
+    return fail(RA_ERR_INVALID_ARG, "index, and an output with its cache, are required");
+  if ((reinterpret_cast<uintptr_t>(index) & 7u) != 0 || !aligned16(k_cache) || !aligned16(ckv_cache) ||
+      !aligned16(k_out) || !aligned16(c_kv_out))
+    return fail(RA_ERR_ALIGNMENT, "caches and outputs must be 16-byte aligned (index 8-byte)");
+  if ((reinterpret_cast<uintptr_t>(dev_error_count) & 3u) != 0)
+    return fail(RA_ERR_ALIGNMENT, "dev_error_count must be 4-byte aligned");
+  if (validate_only()) return ok();
+  ra::ReadLaunch L{};
+  L.index = index;
+  L.k_cache = k_cache;
+  L.v_cache = ckv_cache;
+  L.k_scale = k_rope_scale;
+  L.k_offset = k_rope_offset;
+  L.v_scale = c_kv_scale;
+  L.v_offset = c_kv_offset;
+  L.k_out = k_out;
+  L.v_out = c_kv_out;
+  L.err_count = dev_error_count;
+  L.B = p->B;
+  L.N = p->N;
+  L.S = p->S;
+  L.block_num = p->block_num;
+  L.block_size = p->cache_mode == RA_CACHE_NORM ? 1 : p->block_size;
+  L.cache_seq = p->cache_seq_len;
+  L.kw = s.kw;
+  L.vw = s.vw;
+  L.mode = p->cache_mode;
+  L.f16 = p->kv_dtype == RA_FP16;
+  L.kq = s.kq;
+  L.vq = s.vq;
+  L.k_scalar = p->k_quant_scalar;
+  L.v_scalar = p->c_kv_quant_scalar;
+  L.variant = p->variant;
+  const cudaError_t e = ra::launch_cache_read(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_read launch");
   return ok();
 }
 

@@ -1,0 +1,906 @@
+// Attention of new tokens over the paged caches of kv_rms_norm_rope_cache.
+//
+//   out[i, h] = sum_j softmax_j(scale q[i, h] . k_j) v_j   over the cached positions j <
+//   seq_len (causal: j <= seq_len - Lq + i), k_j / v_j read through the block table.
+//
+// Quantised caches.  An element is x = (code - o) / s per channel, so
+//   q . k_j = sum_c (q_c / s_c) code_jc - sum_c q_c o_c / s_c:
+// the second sum does not depend on j and leaves the softmax (it enters the lse), and
+//   out_c = (sum_j p_j code_jc / sum_j p_j - o_c) / s_c.
+// The codes themselves (int8, E4M3, E5M2: all exact in fp16) are the tensor core's
+// operands; q / s is rounded to fp16 behind a power of two per row that brings the row's
+// largest element to [2^9, 2^10), so it keeps 11 bits whatever the scales.
+//
+// GB300 mapping.  A work item is one row tile of a sequence and kv head: NR rows, a row
+// being (token, head of the group), against all the sequence's keys in 64-key tiles.
+// The tiles of all items, laid end to end, are cut into equal runs, one per block, so
+// blocks finish together whatever the lengths; an item cut in two or more has its pieces'
+// (max, sum, accumulator) joined by a second kernel, in a fixed order.
+//  * The rows are few (one token: 1..128 heads), so the second product is transposed:
+//    O^T[channel, row] += V^T P^T puts the channels on the MMA's 128 rows and the NR rows
+//    on its N, which costs tensor time and TMEM for NR columns instead of 128.  The
+//    first, S = Q K^T, keeps rows on TMEM lanes so that a softmax row is one thread's;
+//    its A operand is addressed as 128 rows although only NR are stored: the other lanes
+//    of S come from whatever follows in shared memory and are never read.
+//  * V1's value row is the first part of its key row: one tile in shared memory serves
+//    both products (K-major for S, MN-major for O^T).
+//  * Warps 4-7 gather rows with 16-byte cp.async (absent rows zero-filled), straight into
+//    the swizzled operand tile for 16-bit caches, or into a staging ring from which each
+//    thread converts the codes that it copied itself; warps 0-3 are the softmax, the
+//    rescaling and the epilogue; warp 8 issues the MMAs, taking whichever of the next
+//    S = Q K^T and the next O^T += V^T P^T is ready first.
+// Every wait is bounded in time (status word).
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "attention.h"
+#include "attn_ptx.cuh"
+#include "internal.h"
+#include "kv_cache.h"
+
+namespace ra {
+namespace {
+
+constexpr int kKeys = 64;                 // keys per tile: one 128-byte swizzled row of P
+constexpr int kSlab = kKeys * 128;        // 64 keys x 64 channels of 16 bits
+constexpr int kThreads = 288;
+constexpr int kSoftmax = 128, kProducers = 128;
+constexpr int kMmaWarp = 8;
+constexpr int kValidRing = 16;            // > tiles between a producer and the softmax
+constexpr int kMaxStages = 6;
+constexpr int kMinTiles = 4;              // tiles per block below which a split costs more than it gives
+constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int kSmemMax = 232448;
+constexpr int kMaxBlocks = 160;           // blocks that a workspace has room for (a GB300 has 152 SMs)
+constexpr int kSCols = 2 * kKeys;         // TMEM: two S buffers, then O^T
+
+struct Params {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *k_offset, *v_scale, *v_offset;
+  const int32_t *cu_q, *seq_lens, *table;
+  int32_t* err_count;
+  int32_t* status;
+  float4* stats;                // [2 G][NR] (m in log2 units, l, lse constant, -) of partial pieces
+  float* parts;                 // [2 G][NR][Dv]
+  int32_t* meta;                // [G][8]
+  int64_t table_stride, cap;    // cap: positions that a sequence can have
+  int64_t block_num, cache_seq;
+  int32_t B, total_q, N, heads, g, NR, block_size, bs_shift;
+  int32_t Dk, Dv, Dko;          // key width, value width, width of a k_cache row
+  int32_t v1, mode, f16, kq, vq, k_scalar, v_scalar, causal;
+  int32_t ca, nc, magic;        // 16-byte chunks of a v row, of both rows; idx / nc = idx * magic >> 20
+  int32_t vslabs, kslabs, qslabs, kslab0;
+  int32_t ns, nsg;              // operand stages, staging stages (0: 16-bit caches)
+  int32_t stage_bytes, staging_bytes;
+  int32_t off_p, off_ring, off_staging, off_misc;
+  float sl2, scale;
+  uint64_t wait_ns;
+  int32_t stall_loads;
+};
+
+struct Misc {                   // behind the tiles in shared memory
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
+  uint64_t valid[kValidRing];
+  int64_t row_index[2][kKeys];
+  int64_t scan[kThreads / 32];
+  int64_t start_off;
+  int32_t start_b;
+  uint32_t tmem;
+  int32_t abort;
+  // followed by per-row arrays of NR: int32 out_row, float row_scale, row_const, fac[2], inv_sum
+};
+__host__ __device__ constexpr int row_arrays_bytes(int nr) { return nr * (4 + 5 * 4); }
+
+__device__ __forceinline__ int32_t seq_len_of(const Params& p, int32_t b) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(max(__ldg(p.seq_lens + b), 0)), p.cap));
+}
+__device__ __forceinline__ void q_span(const Params& p, int32_t b, int32_t& start, int32_t& len) {
+  if (p.cu_q == nullptr) {
+    len = p.total_q / p.B;
+    start = b * len;
+    return;
+  }
+  const int32_t lo = min(max(__ldg(p.cu_q + b), 0), p.total_q), hi = min(max(__ldg(p.cu_q + b + 1), lo), p.total_q);
+  start = lo;
+  len = hi - lo;
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t len) { return max(1, (len + kKeys - 1) / kKeys); }
+__device__ __forceinline__ int64_t seq_work(const Params& p, int32_t b) {
+  int32_t s, lq;
+  q_span(p, b, s, lq);
+  const int64_t rows = static_cast<int64_t>(lq) * p.g;
+  return (rows + p.NR - 1) / p.NR * p.N * tiles_of(seq_len_of(p, b));
+}
+
+// One block's share of an item: key tiles [ta, tb) of row tile rt of (b, n).
+struct Piece {
+  int32_t b, n, rt, rows, q_start, Lq, len;
+  int32_t t0, take, T;          // nominal tiles: [t0, t0 + take) of T
+  int32_t ta, tb;               // those that any of its rows sees
+  __device__ bool whole() const { return take == T; }
+};
+// Walks the pieces of a run of tiles.
+struct Walker {
+  int32_t b;
+  int64_t off, rem;             // position inside sequence b, tiles left
+  __device__ bool next(const Params& p, Piece& w) {
+    while (rem > 0 && b < p.B) {
+      int32_t qs, lq;
+      q_span(p, b, qs, lq);
+      const int32_t len = seq_len_of(p, b), T = tiles_of(len);
+      const int64_t rows = static_cast<int64_t>(lq) * p.g;
+      const int64_t rts = (rows + p.NR - 1) / p.NR;
+      if (off >= rts * p.N * T) {
+        off -= rts * p.N * T;
+        ++b;
+        continue;
+      }
+      const int64_t item = off / T;
+      w.b = b;
+      w.t0 = static_cast<int32_t>(off - item * T);
+      w.T = T;
+      w.take = static_cast<int32_t>(min(static_cast<int64_t>(T - w.t0), rem));
+      w.n = static_cast<int32_t>(item / rts);
+      w.rt = static_cast<int32_t>(item - w.n * rts);
+      w.rows = static_cast<int32_t>(min(static_cast<int64_t>(p.NR), rows - static_cast<int64_t>(w.rt) * p.NR));
+      w.q_start = qs;
+      w.Lq = lq;
+      w.len = len;
+      const int32_t last = static_cast<int32_t>((static_cast<int64_t>(w.rt) * p.NR + w.rows - 1) / p.g);
+      const int32_t seen = p.causal ? min(len, max(0, len - lq + last + 1)) : len;
+      const int32_t vt = (seen + kKeys - 1) / kKeys;
+      w.ta = min(w.t0, vt);
+      w.tb = min(w.t0 + w.take, vt);
+      off += w.take;
+      rem -= w.take;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ uint32_t bar_or(uint32_t id, uint32_t pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred), "r"(id)
+      : "memory");
+  return r;
+}
+__device__ __forceinline__ void bar_128(uint32_t id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// four codes -> four fp16 values, exactly
+__device__ __forceinline__ uint2 codes_to_half(uint32_t c, int32_t kind) {
+  uint2 r;
+  if (kind == kQuantInt8) {
+    // 0x6400 | u is the fp16 number 1024 + u; with u = code + 128, subtract 1152
+    c ^= 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t lo = __byte_perm(c, 0x64646464u, 0x4140), hi = __byte_perm(c, 0x64646464u, 0x4342);
+    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), off), b = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+    r.x = *reinterpret_cast<uint32_t*>(&a);
+    r.y = *reinterpret_cast<uint32_t*>(&b);
+  } else if (kind == kQuantE5m2) {  // the upper byte of an fp16 number
+    r.x = __byte_perm(c, 0, 0x1404);
+    r.y = __byte_perm(c, 0, 0x3424);
+  } else {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
+    r.x = a.x | (static_cast<uint32_t>(a.y) << 16);
+    r.y = b.x | (static_cast<uint32_t>(b.y) << 16);
+  }
+  return r;
+}
+
+__device__ __forceinline__ float load_half(const uint16_t* p, bool f16) {
+  const uint16_t u = *p;
+  return f16 ? __half2float(__ushort_as_half(u)) : __uint_as_float(static_cast<uint32_t>(u) << 16);
+}
+__device__ __forceinline__ uint16_t to_half(float x, bool f16) {
+  return f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+__device__ __forceinline__ uint32_t pair16(uint16_t lo, uint16_t hi) { return lo | (static_cast<uint32_t>(hi) << 16); }
+// scale and offset of one channel of a cache row (1 and 0 for a 16-bit cache)
+__device__ __forceinline__ float2 channel_quant(const float* scale, const float* offset, int32_t at, int32_t scalar) {
+  if (scale == nullptr) return make_float2(1.f, 0.f);
+  const int32_t i = scalar ? 0 : at;
+  return make_float2(__ldg(scale + i), offset ? __ldg(offset + i) : 0.f);
+}
+// the quantisation of key channel c of head n: V1's key is the ckv row, then the k row
+__device__ __forceinline__ float2 key_quant(const Params& p, int32_t n, int32_t c) {
+  if (p.v1)
+    return c < p.Dv ? channel_quant(p.v_scale, p.v_offset, c, p.v_scalar)
+                    : channel_quant(p.k_scale, p.k_offset, c - p.Dv, p.k_scalar);
+  return channel_quant(p.k_scale, p.k_offset, n * p.Dk + c, 0);
+}
+__device__ __forceinline__ float2 value_quant(const Params& p, int32_t n, int32_t c) {
+  return channel_quant(p.v_scale, p.v_offset, p.v1 ? c : n * p.Dv + c, p.v_scalar);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc& ms = *reinterpret_cast<Misc*>(smem + p.off_misc);
+  const int NR = p.NR;
+  int32_t* out_row = reinterpret_cast<int32_t*>(&ms + 1);  // row of q and out, -1: none
+  float* row_scale = reinterpret_cast<float*>(out_row + NR);
+  float* row_const = row_scale + NR;
+  float* fac = row_const + NR;              // [2][NR]
+  float* inv_sum = fac + 2 * NR;
+  const uint32_t s0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this block's run of tiles
+  const int32_t chunk = (p.B + kThreads - 1) / kThreads;
+  const int32_t b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk), b_hi = min(p.B, b_lo + chunk);
+  int64_t mine = 0;
+  for (int32_t b = b_lo; b < b_hi; ++b) mine += seq_work(p, b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) ms.scan[warp] = incl;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ns; ++s) {
+      mbar_init(smem_u32(&ms.kv_full[s]), kProducers);
+      mbar_init(smem_u32(&ms.kv_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ms.s_full[0]), 1);
+    mbar_init(smem_u32(&ms.s_full[1]), 1);
+    mbar_init(smem_u32(&ms.p_ready), kSoftmax);
+    mbar_init(smem_u32(&ms.pv_done), 1);
+    mbar_init(smem_u32(&ms.q_ready), kSoftmax);
+    mbar_init(smem_u32(&ms.drain), 1);
+    ms.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int64_t before = incl - mine, W = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int64_t t = ms.scan[w];
+    if (w < warp) before += t;
+    W += t;
+  }
+  const int64_t G = gridDim.x;
+  const int64_t per = max((W + G - 1) / G, static_cast<int64_t>(kMinTiles));
+  const int64_t start = per * blockIdx.x;
+  if (threadIdx.x == 0) p.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
+  if (start >= W) return;
+  if (before <= start && start < before + mine) {
+    int32_t b = b_lo;
+    int64_t off = start - before;
+    for (int64_t w; b < b_hi && off >= (w = seq_work(p, b)); ++b) off -= w;
+    ms.start_b = b;
+    ms.start_off = off;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ms.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  volatile int* abort_flag = &ms.abort;
+  Walker walk{ms.start_b, ms.start_off, min(per, W - start)};
+  Piece w;
+
+  if (warp >= 4 && warp < kMmaWarp) {
+    // ------------------------------------------------------------ producers
+    const int tid = threadIdx.x - kSoftmax;
+    const int chunks = kKeys * p.nc;
+    const int64_t v_row = static_cast<int64_t>(p.ca) * 16, k_row = static_cast<int64_t>(p.nc - p.ca) * 16;
+    // this thread's key of tile t of piece w, as a cache row (-1: none)
+    auto row_of = [&](const Piece& x, int32_t t) -> int64_t {
+      const int32_t pos = t * kKeys + tid;
+      if (tid >= kKeys || pos >= x.len) return -1;
+      if (p.mode == kModeNorm) return (static_cast<int64_t>(x.b) * p.N + x.n) * p.cache_seq + pos;
+      const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
+      const int32_t in = pos - pg * p.block_size;
+      const int64_t page = __ldg(p.table + x.b * p.table_stride + pg);
+      if (page < 0 || page >= p.block_num) {
+        if (p.err_count) atomicAdd(p.err_count, 1);
+        return -1;
+      }
+      return p.mode == kModePa ? (page * p.block_size + in) * p.N + x.n : (page * p.N + x.n) * p.block_size + in;
+    };
+    bool ok = !p.stall_loads;
+    int32_t issued = 0, completed = 0;
+    bool more = walk.next(p, w);
+    while (more && w.ta >= w.tb) more = walk.next(p, w);
+    int32_t t = more ? w.ta : 0;
+    int64_t row = more && ok ? row_of(w, t) : -1;
+    auto complete = [&]() {  // convert the oldest staged tile into its operand stage
+      const int st = completed % p.ns, sg = completed % p.nsg;
+      if (!bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((completed / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag)) return false;
+      uint8_t* stage = smem + p.off_ring + st * p.stage_bytes;
+      const uint8_t* from = smem + p.off_staging + sg * p.staging_bytes;
+      for (int i = tid; i < chunks; i += kProducers) {
+        const int key = (i * p.magic) >> 20, c = i - key * p.nc;
+        const bool is_v = c < p.ca;
+        const int cc = is_v ? c : c - p.ca;
+        const int32_t kind = is_v ? p.vq : p.kq;
+        uint8_t* slab0 = stage + (is_v ? 0 : p.vslabs * kSlab) + key * 128;
+        const uint4 u = *reinterpret_cast<const uint4*>(from + i * 16);
+        if (kind == kQuantNone) {
+          *reinterpret_cast<uint4*>(slab0 + (cc >> 3) * kSlab + (((cc & 7) ^ (key & 7)) << 4)) = u;
+        } else {
+          const uint2 a = codes_to_half(u.x, kind), b = codes_to_half(u.y, kind);
+          const uint2 d = codes_to_half(u.z, kind), e = codes_to_half(u.w, kind);
+          uint8_t* slab = slab0 + (cc >> 2) * kSlab;
+          const int c8 = (cc & 3) * 2;
+          *reinterpret_cast<uint4*>(slab + ((c8 ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(slab + (((c8 + 1) ^ (key & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&ms.kv_full[st]));
+      ++completed;
+      return true;
+    };
+    while (more && !p.stall_loads) {
+      int64_t* rows = ms.row_index[issued & 1];
+      if (tid < kKeys) {
+        rows[tid] = row;
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane == 0) reinterpret_cast<uint32_t*>(&ms.valid[issued % kValidRing])[tid >> 5] = live;
+      }
+      // the next tile's rows: its table entry is on the way while this tile is issued
+      bool next_more = true;
+      if (++t >= w.tb) {
+        next_more = walk.next(p, w);
+        while (next_more && w.ta >= w.tb) next_more = walk.next(p, w);
+        t = w.ta;
+      }
+      const int64_t next_row = next_more ? row_of(w, t) : -1;
+      // a warp whose wait gave up leaves with the others, not them at the barrier
+      if (bar_or(2, ok ? 0u : 1u)) break;
+      uint32_t dst0;
+      const int st = issued % p.ns;
+      if (p.nsg == 0) {
+        if (!bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((issued / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag)) ok = false;
+        dst0 = s0 + p.off_ring + st * p.stage_bytes;
+      } else {
+        dst0 = s0 + p.off_staging + (issued % p.nsg) * p.staging_bytes;
+      }
+      if (ok) {
+        for (int i = tid; i < chunks; i += kProducers) {
+          const int key = (i * p.magic) >> 20, c = i - key * p.nc;
+          const bool is_v = c < p.ca;
+          const int cc = is_v ? c : c - p.ca;
+          const int64_t r = rows[key];
+          const uint8_t* src = is_v ? p.v_cache : p.k_cache;
+          if (r >= 0) src += r * (is_v ? v_row : k_row) + cc * 16;
+          const uint32_t dst = p.nsg == 0 ? dst0 + ((is_v ? 0 : p.vslabs) + (cc >> 3)) * kSlab + key * 128 +
+                                                (((cc & 7) ^ (key & 7)) << 4)
+                                          : dst0 + i * 16;
+          cp_async16(dst, src, r >= 0 ? 16 : 0);
+        }
+        if (p.nsg == 0) {
+          cp_async_mbar_arrive(smem_u32(&ms.kv_full[st]));
+        } else {
+          cp_async_commit();
+          if (issued + 1 - completed == p.nsg) {
+            switch (p.nsg) {  // the oldest of the nsg tiles in flight has landed
+              case 1: cp_async_wait<0>(); break;
+              case 2: cp_async_wait<1>(); break;
+              case 3: cp_async_wait<2>(); break;
+              default: cp_async_wait<3>(); break;
+            }
+            ok = complete();
+          }
+        }
+        ++issued;
+      }
+      more = next_more;
+      row = next_row;
+    }
+    if (p.nsg != 0) {
+      cp_async_commit();
+      cp_async_wait<0>();
+      while (ok && completed < issued) ok = complete();
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const bool bf = !p.f16;
+      const uint32_t id_s_v = idesc_f16(bf && p.vq == 0, false, false, 128, kKeys);   // V1: the latent part of the key
+      const uint32_t id_s_k = idesc_f16(bf && p.kq == 0, false, false, 128, kKeys);
+      const uint32_t id_o = idesc_f16(bf && p.vq == 0, true, false, 128, static_cast<uint32_t>(NR));
+      const uint64_t q_desc = sdesc_kmajor_sw128(s0);
+      const uint64_t k_desc = sdesc_kmajor_sw128(s0 + p.off_ring + p.kslab0 * kSlab);
+      const uint64_t v_desc = sdesc_mnmajor_sw128(s0 + p.off_ring, kSlab);
+      const uint64_t p_desc = sdesc_kmajor_sw128(s0 + p.off_p);
+      const int v_chunks = (p.Dv + 127) / 128;
+      const int q_step = NR * 128 >> 4;
+      int32_t jt = 0, pieces = 0;
+      bool ok = true;
+      while (ok && walk.next(p, w)) {
+        const int32_t n = w.tb - w.ta;
+        if (n <= 0) continue;
+        if (!bounded_wait_one(smem_u32(&ms.q_ready), pieces & 1, p.wait_ns, abort_flag)) break;
+        ++pieces;
+        int32_t qk = 0, pv = 0;
+        uint64_t t_start = 0;
+        uint32_t spins = 0;
+        while (pv < n) {
+          if (qk < n && qk - pv < 2) {
+            const int32_t u = jt + qk;
+            const int st = u % p.ns;
+            if (mbar_test_wait(smem_u32(&ms.kv_full[st]), (u / p.ns) & 1)) {
+              // the tile was written through the generic proxy by the producers
+              fence_proxy_async_smem();
+              tc_fence_after();
+              const uint64_t kb = k_desc + static_cast<uint64_t>(st * (p.stage_bytes >> 4));
+              const uint32_t d = tmem + (u & 1) * kKeys;
+              for (int sl = 0; sl < p.qslabs; ++sl) {
+                const uint32_t id = p.v1 && sl < p.vslabs ? id_s_v : id_s_k;
+                const int steps = min(4, (p.Dk - sl * 64) / 16);
+                for (int k = 0; k < steps; ++k)
+                  mma_f16_ss(d, q_desc + sl * q_step + 2 * k, kb + sl * (kSlab >> 4) + 2 * k, id, sl + k > 0);
+              }
+              tc_commit(smem_u32(&ms.s_full[u & 1]));
+              ++qk;
+              spins = 0;
+              continue;
+            }
+          }
+          if (pv < qk && mbar_test_wait(smem_u32(&ms.p_ready), (jt + pv) & 1)) {
+            tc_fence_after();
+            const int st = (jt + pv) % p.ns;
+            const uint64_t va = v_desc + static_cast<uint64_t>(st * (p.stage_bytes >> 4));
+            for (int c = 0; c < v_chunks; ++c)
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_f16_ss(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4) + 128 * k, p_desc + 2 * k, id_o,
+                           pv > 0 || k > 0);
+            tc_commit(smem_u32(&ms.kv_empty[st]));
+            tc_commit(smem_u32(&ms.pv_done));
+            ++pv;
+            spins = 0;
+            continue;
+          }
+          if ((++spins & 31u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (spins == 32u) t_start = now;
+            else if (*abort_flag || now - t_start > p.wait_ns) {
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        jt += n;
+      }
+      tc_commit(smem_u32(&ms.drain));  // every product must finish before TMEM is released
+      bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, rescaling, epilogue
+    const int tid = threadIdx.x;                     // also the row this thread owns
+    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
+    const int v_chunks = (p.Dv + 127) / 128;
+    const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
+    const bool p_f16 = p.f16 || p.vq != 0;           // P has the type of V's operand
+    const int tpr = kSoftmax / NR;                   // threads that prepare one row of Q
+    int32_t jt = 0, piece = 0;
+    bool ok = true;
+    for (; ok && walk.next(p, w); ++piece) {
+      const int32_t n = w.tb - w.ta;
+      const int64_t first_row = static_cast<int64_t>(w.rt) * NR;
+      bar_128(1);                                    // the previous piece's row arrays are done with
+      if (tid < NR) {
+        const int64_t rr = first_row + tid;
+        const int64_t tok = rr / p.g;
+        out_row[tid] =
+            tid < w.rows ? static_cast<int32_t>((w.q_start + tok) * p.heads + static_cast<int64_t>(w.n) * p.g + (rr - tok * p.g)) : -1;
+      }
+      bar_128(1);
+      {  // Q rows into the swizzled operand, 8 channels at a time
+        const int r = tid / tpr, sub = tid - r * tpr;
+        const int64_t at = out_row[r];
+        const uint16_t* src = p.q + (at < 0 ? 0 : at) * p.Dk;
+        const int nck = p.Dk / 8;
+        float up = 1.f, shift = 0.f;
+        if (k_quant) {
+          float amax = 0.f;
+          if (at >= 0)
+            for (int c = sub; c < nck; c += tpr)
+              for (int e = 0; e < 8; ++e) {
+                const float2 so = key_quant(p, w.n, c * 8 + e);
+                const float x = load_half(src + c * 8 + e, p.f16) / so.x;
+                amax = fmaxf(amax, fabsf(x));
+                shift = fmaf(x, so.y, shift);
+              }
+          for (int o = 1; o < tpr; o <<= 1) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            shift += __shfl_xor_sync(0xffffffffu, shift, o);
+          }
+          up = amax > 0.f ? exp2_int(-(scale_exponent(amax) + 5)) : 1.f;  // amax * up in [2^9, 2^10)
+        }
+        if (sub == 0) {
+          row_scale[r] = p.sl2 / up;
+          row_const[r] = -shift * p.scale;
+        }
+        if (at >= 0) {
+          for (int c = sub; c < nck; c += tpr) {
+            uint4 u = *reinterpret_cast<const uint4*>(src + c * 8);
+            if (k_quant) {
+              const bool quant = (p.v1 && c * 8 < p.Dv) ? p.vq != 0 : p.kq != 0;
+              uint16_t h[8];
+              for (int e = 0; e < 8; ++e) {
+                const float2 so = key_quant(p, w.n, c * 8 + e);
+                h[e] = to_half(load_half(src + c * 8 + e, p.f16) / so.x * up, quant || p.f16);
+              }
+              u = make_uint4(pair16(h[0], h[1]), pair16(h[2], h[3]), pair16(h[4], h[5]), pair16(h[6], h[7]));
+            }
+            *reinterpret_cast<uint4*>(smem + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      bar_128(1);
+      if (n > 0) mbar_arrive(smem_u32(&ms.q_ready));
+
+      const bool live = tid < w.rows;
+      const float sl2 = live ? row_scale[tid] : 1.f;
+      const float lazy = kLazy / sl2;
+      int32_t seen = w.len;
+      if (p.causal && live) {
+        const int32_t tok = static_cast<int32_t>((first_row + tid) / p.g);
+        seen = min(w.len, max(0, w.len - w.Lq + tok + 1));
+      }
+      float m = neg_inf(), l = 0.f;
+      for (int32_t j = 0; j < n; ++j) {
+        const int32_t u = jt + j;
+        if (!bounded_wait_warp(smem_u32(&ms.s_full[u & 1]), (u >> 1) & 1, p.wait_ns, abort_flag)) ok = false;
+        tc_fence_after();
+        uint32_t s[kKeys];
+        float f = 1.f;
+        uint32_t grow = 0;
+        const bool rows_here = warp * 32 < w.rows;   // uniform in the warp
+        if (ok && rows_here) {
+          tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys, s);
+          tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys + 32, s + 32);
+          tmem_ld_wait();
+          const int32_t nv = seen - (w.ta + j) * kKeys;
+          uint64_t mask = ms.valid[u % kValidRing];
+          if (nv < kKeys) mask &= nv <= 0 ? 0ull : (1ull << nv) - 1;
+          if (__any_sync(0xffffffffu, mask != ~0ull)) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (!((mask >> c) & 1)) s[c] = __float_as_uint(neg_inf());
+          }
+          float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e])));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (live && top > m + lazy) {
+            f = ex2((m - top) * sl2);
+            l *= f;
+            m = top;
+            grow = 1;
+          }
+        }
+        if (tid < NR) fac[(u & 1) * NR + tid] = f;
+        // a row's maximum grew, or a wait gave up: then the group leaves together
+        const uint32_t any = bar_or(1, grow | (ok ? 0u : 1u));
+        if (any && bar_or(1, ok ? 0u : 1u)) {
+          ok = false;
+          break;
+        }
+        if (j > 0) {  // P's buffer is free, and the accumulator complete, once the last product is
+          if (!bounded_wait_warp(smem_u32(&ms.pv_done), (u - 1) & 1, p.wait_ns, abort_flag)) ok = false;
+          tc_fence_after();
+        }
+        if (ok && any && j > 0) {
+          const float* fr = fac + (u & 1) * NR;
+          for (int c = 0; c < v_chunks; ++c) {
+            if (c * 128 + warp * 32 >= p.Dv) continue;
+            for (int col = 0; col < NR; col += 16) {
+              const uint32_t at = tmem + lane_base + kSCols + c * NR + col;
+              uint32_t o[16];
+              tmem_ld_x16(at, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr[col + e]);
+              tmem_st_x16(at, o);
+            }
+          }
+          tmem_st_wait();
+        }
+        if (ok && rows_here) {
+          const float neg = m == neg_inf() ? 0.f : -m * sl2;
+          const float2 sc = make_float2(sl2, sl2), ng = make_float2(neg, neg);
+          float2 acc = make_float2(0.f, 0.f);
+          uint8_t* prow = smem + p.off_p + tid * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = 8 * c + 2 * e;
+              float2 x = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc, ng);
+              x.x = ex2(x.x), x.y = ex2(x.y);
+              acc = __fadd2_rn(acc, x);
+              h[e] = p_f16 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+            }
+            if (live) *reinterpret_cast<uint4*>(prow + ((c ^ (tid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          l += acc.x + acc.y;
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ms.p_ready));
+      }
+      if (ok && n > 0) ok = bounded_wait_warp(smem_u32(&ms.pv_done), (jt + n - 1) & 1, p.wait_ns, abort_flag);
+      ok = bar_or(1, ok ? 0u : 1u) == 0;
+      if (!ok) break;
+      tc_fence_after();
+      jt += n;
+
+      // ---- epilogue: final rows, or the piece's statistics and accumulator
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1);
+      if (tid < NR) inv_sum[tid] = l > 0.f ? 1.f / l : 0.f;
+      if (live) {
+        if (w.whole()) {
+          if (p.lse)
+            p.lse[out_row[tid]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + row_const[tid] : neg_inf();
+        } else {
+          p.stats[slot * NR + tid] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, row_const[tid], 0.f);
+        }
+      }
+      if (piece == 0 && tid == 0) {
+        // the block behind the first cut through an item joins the item's pieces
+        const int64_t item0 = start - w.t0;
+        const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
+        int32_t* mt = p.meta + 8 * blockIdx.x;
+        mt[1] = first;
+        mt[2] = last;
+        mt[3] = w.rows;
+        mt[4] = w.q_start;
+        mt[5] = w.n;
+        mt[6] = w.rt;
+        mt[0] = w.t0 > 0 && first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+      }
+      bar_128(1);
+      for (int c = 0; c < v_chunks; ++c) {
+        const int ch = c * 128 + tid;                 // this lane's channel
+        if (c * 128 + warp * 32 >= p.Dv) continue;
+        const float2 so = value_quant(p, w.n, min(ch, p.Dv - 1));
+        const float inv_s = 1.f / so.x;
+        for (int col = 0; col < w.rows; col += 16) {
+          uint32_t o[16];
+          if (n > 0) {
+            tmem_ld_x16(tmem + lane_base + kSCols + c * NR + col, o);
+            tmem_ld_wait();
+          }
+          if (ch < p.Dv) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int r = col + e;
+              if (r >= w.rows) continue;
+              if (w.whole()) {
+                const float inv = inv_sum[r];
+                const float y = inv > 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
+                p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half(y, p.f16);
+              } else if (n > 0) {
+                p.parts[(slot * NR + r) * p.Dv + ch] = __uint_as_float(o[e]);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the items that a cut runs through: block (c, r) row r of the item
+// whose first cut lies before block c's run.
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ Params p) {
+  const int32_t* mt = p.meta + 8 * blockIdx.x;
+  const int r = blockIdx.y;
+  if (mt[0] == 0 || r >= mt[3]) return;
+  const int32_t first = mt[1], last = mt[2], NR = p.NR;
+  const int64_t rr = static_cast<int64_t>(mt[6]) * NR + r, tok = rr / p.g;
+  const int64_t row = (mt[4] + tok) * p.heads + static_cast<int64_t>(mt[5]) * p.g + (rr - tok * p.g);
+  // the item's piece is the last of its first block, the first of the others
+  auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == first ? 1 : 0); };
+  float m = neg_inf();
+  for (int32_t c = first; c <= last; ++c) m = fmaxf(m, p.stats[slot(c) * NR + r].x);
+  float l = 0.f, k0 = 0.f;
+  for (int32_t c = first; c <= last; ++c) {
+    const float4 s = p.stats[slot(c) * NR + r];
+    if (s.y > 0.f) l += s.y * ex2(s.x - m);
+    k0 = s.z;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
+  for (int ch = threadIdx.x; ch < p.Dv; ch += blockDim.x) {
+    float acc = 0.f;
+    for (int32_t c = first; c <= last; ++c) {
+      const float4 s = p.stats[slot(c) * NR + r];
+      if (s.y > 0.f) acc += p.parts[(slot(c) * NR + r) * p.Dv + ch] * ex2(s.x - m);
+    }
+    const float2 so = value_quant(p, mt[5], ch);
+    p.out[row * p.Dv + ch] = to_half(l > 0.f ? (acc * inv - so.y) / so.x : 0.f, p.f16);
+  }
+}
+
+struct Plan {
+  int32_t NR, G;
+  int32_t ns, nsg;
+  int32_t vslabs, kslabs, qslabs, kslab0, stage, staging, off_p, off_ring, off_staging, off_misc, smem;
+};
+
+// The rows of a tile: as many as a sequence's tokens and heads fill on average, so that a
+// decode step does not pay for 128, within what shared memory leaves for two stages.
+bool plan(const PagedLaunch& L, Plan* pl) {
+  const bool v1 = L.variant == 1;
+  const int g = L.heads / static_cast<int32_t>(L.N);
+  pl->vslabs = (L.Dv + 63) / 64;
+  pl->kslabs = ((v1 ? L.R : L.Dkv) + 63) / 64;
+  pl->qslabs = v1 ? pl->vslabs + pl->kslabs : pl->kslabs;
+  pl->kslab0 = v1 ? 0 : pl->vslabs;
+  pl->stage = (pl->vslabs + pl->kslabs) * kSlab;
+  const int rows_bytes = (v1 ? L.R : L.Dkv) * (L.kq ? 1 : 2) + L.Dv * (L.vq ? 1 : 2);
+  const bool staged = L.kq != 0 || L.vq != 0;
+  pl->staging = staged ? kKeys * rows_bytes : 0;
+  const int64_t mean = (L.total_q + L.B - 1) / L.B * g;
+  int nr = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  const int chunks = (L.Dv + 127) / 128;
+  for (;; nr >>= 1) {
+    if (nr < 16) return false;
+    if (kSCols + chunks * nr > 512) continue;
+    const int fixed = pl->qslabs * nr * 128 + nr * 128 + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
+    const int left = kSmemMax - fixed;
+    if (!staged) {
+      pl->nsg = 0;
+      pl->ns = std::min(kMaxStages, left / pl->stage);
+      if (pl->ns < 2) continue;
+    } else {
+      if (left < pl->stage + pl->staging) continue;
+      pl->ns = left >= 2 * pl->stage + 2 * pl->staging ? 2 : 1;
+      pl->nsg = std::min(4, (left - pl->ns * pl->stage) / pl->staging);
+    }
+    break;
+  }
+  pl->NR = nr;
+  pl->off_p = pl->qslabs * nr * 128;
+  pl->off_ring = pl->off_p + nr * 128;
+  pl->off_staging = pl->off_ring + pl->ns * pl->stage;
+  pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
+  pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
+  // one block per SM, and no more than there are runs of kMinTiles at the largest lengths
+  const int64_t rts = std::min<int64_t>(L.total_q * g, (L.total_q * g) / nr + L.B);
+  const int64_t T = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
+  const int64_t runs = (rts * L.N * T + kMinTiles - 1) / kMinTiles;
+  pl->G = static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs)));
+  return true;
+}
+
+size_t meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
+size_t stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
+
+}  // namespace
+
+size_t paged_attention_workspace(const PagedLaunch& L) {
+  Plan pl;
+  if (!plan(L, &pl)) return 0;
+  return kAttnHeader + meta_bytes(pl.G) + stats_bytes(pl.G, pl.NR) +
+         static_cast<size_t>(pl.G) * 2 * pl.NR * L.Dv * sizeof(float);
+}
+
+cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why) {
+  Plan pl;
+  if (!plan(L, &pl)) {
+    *why = "no tile shape fits";
+    return cudaErrorInvalidValue;
+  }
+  uint8_t* const stats = L.partials + meta_bytes(pl.G);
+  uint8_t* const parts = stats + stats_bytes(pl.G, pl.NR);
+  pl.G = std::min(pl.G, device_sm_count());
+  Params p{};
+  p.q = L.q;
+  p.out = L.out;
+  p.lse = L.lse;
+  p.k_cache = static_cast<const uint8_t*>(L.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(L.v_cache);
+  p.k_scale = L.k_scale;
+  p.k_offset = L.k_offset;
+  p.v_scale = L.v_scale;
+  p.v_offset = L.v_offset;
+  p.cu_q = L.cu_q;
+  p.seq_lens = L.seq_lens;
+  p.table = L.table;
+  p.err_count = L.err_count;
+  p.status = L.status;
+  p.meta = reinterpret_cast<int32_t*>(L.partials);
+  p.stats = reinterpret_cast<float4*>(stats);
+  p.parts = reinterpret_cast<float*>(parts);
+  p.table_stride = L.table_stride;
+  const int64_t room = L.mode == kModeNorm ? L.cache_seq : L.table_stride * L.block_size;
+  p.cap = std::min<int64_t>(room, L.max_seq_len);
+  p.block_num = L.block_num;
+  p.cache_seq = L.cache_seq;
+  p.B = static_cast<int32_t>(L.B);
+  p.total_q = static_cast<int32_t>(L.total_q);
+  p.N = static_cast<int32_t>(L.N);
+  p.heads = L.heads;
+  p.g = L.heads / static_cast<int32_t>(L.N);
+  p.NR = pl.NR;
+  p.block_size = static_cast<int32_t>(L.block_size);
+  p.bs_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if ((int64_t(1) << s) == L.block_size) p.bs_shift = s;
+  p.v1 = L.variant == 1;
+  p.Dk = L.Dkv;
+  p.Dv = L.Dv;
+  p.Dko = p.v1 ? L.R : L.Dkv;
+  p.mode = L.mode;
+  p.f16 = L.f16;
+  p.kq = L.kq;
+  p.vq = L.vq;
+  p.k_scalar = L.k_scalar;
+  p.v_scalar = L.v_scalar;
+  p.causal = L.causal;
+  p.ca = L.Dv * (L.vq ? 1 : 2) / 16;
+  p.nc = p.ca + p.Dko * (L.kq ? 1 : 2) / 16;
+  p.magic = ((1 << 20) + p.nc - 1) / p.nc;  // exact for idx < 64 nc: the error idx * nc / 2^20 stays below 1 / nc
+  p.vslabs = pl.vslabs;
+  p.kslabs = pl.kslabs;
+  p.qslabs = pl.qslabs;
+  p.kslab0 = pl.kslab0;
+  p.ns = pl.ns;
+  p.nsg = pl.nsg;
+  p.stage_bytes = pl.stage;
+  p.staging_bytes = pl.staging;
+  p.off_p = pl.off_p;
+  p.off_ring = pl.off_ring;
+  p.off_staging = pl.off_staging;
+  p.off_misc = pl.off_misc;
+  p.scale = L.scale;
+  p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
+  p.wait_ns = static_cast<uint64_t>(L.wait_ns);
+  p.stall_loads = L.stall_loads;
+
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  paged_attention_kernel<<<pl.G, kThreads, pl.smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || pl.G == 1) return e;
+  paged_join_kernel<<<dim3(pl.G, pl.NR), 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ra

@@ -33,7 +33,9 @@ EXPORTS = ["ra_last_error", "ra_abi_version", "ra_set_wait_timeout_ns", "ra_test
            "qkv_cte_mx", "qkv_cte_mx_project", "qkv_cte_mx_norm_rope", "qkv_cte_mx_status",
            "qkv_cte_mx_noalloc", "kv_rms_norm_rope_cache", "kv_rms_norm_rope_cache_status",
            "ra_test_stall_next_kv_cache", "ra_test_stall_next_norm_rope", "row_quantize_e4m3",
-           "row_quantize_e4m3_packed", "ra_test_validate_only"]
+           "row_quantize_e4m3_packed", "ra_test_validate_only", "packed_attention_workspace_bytes",
+           "packed_attention", "paged_attention_workspace_bytes", "paged_attention", "attention_status",
+           "ra_test_stall_next_attention", "kv_cache_read"]
 
 
 class RAError(RuntimeError):
@@ -60,6 +62,23 @@ class KvRmsNormRopeCacheParams(ctypes.Structure):
                 ("is_output_kv", ctypes.c_int32), ("rope_s_broadcast", ctypes.c_int32),
                 ("cache_seq_len", ctypes.c_int64), ("k_quant_scalar", ctypes.c_int32),
                 ("c_kv_quant_scalar", ctypes.c_int32)]
+
+
+class PackedAttentionParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class PagedAttentionParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("total_q", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("max_seq_len", ctypes.c_int64), ("block_table_stride", ctypes.c_int64)]
 
 
 _LIB = None
@@ -97,6 +116,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "row_quantize_e4m3": (i32, [P, i64, i64, P, P, P]),
         "row_quantize_e4m3_packed": (i32, [P, i64, i64, P, P]),
         "ra_test_validate_only": (None, [i32]),
+        "packed_attention_workspace_bytes": (i32, [ctypes.POINTER(PackedAttentionParams), ctypes.POINTER(sz)]),
+        "packed_attention": (i32, [ctypes.POINTER(PackedAttentionParams), P, P, P, P, P, P, P, P, sz, P]),
+        "paged_attention_workspace_bytes": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams),
+                                                  ctypes.POINTER(PagedAttentionParams), ctypes.POINTER(sz)]),
+        "paged_attention": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), ctypes.POINTER(PagedAttentionParams),
+                                  P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "attention_status": (i32, [P, P, ctypes.POINTER(i32)]),
+        "ra_test_stall_next_attention": (None, []),
+        "kv_cache_read": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), P, P, P, P, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -377,3 +405,198 @@ def row_quantize_e4m3_packed(x: torch.Tensor, packed: torch.Tensor, stream=None)
     _need(packed, T * (H + 4), "packed")
     _check(load().row_quantize_e4m3_packed(_ptr(x, torch.bfloat16, "x"), T, H,
                                            _ptr(packed, torch.uint8, "packed"), _stream(stream)))
+
+
+# ---------------------------------------------------------------- attention and the cache read
+_HALF = {RA_BF16: torch.bfloat16, RA_FP16: torch.float16}
+_STORED = {RA_BF16: (torch.bfloat16,), RA_FP16: (torch.float16,), RA_INT8: (torch.int8,),
+           RA_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), RA_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
+
+
+def ra_test_stall_next_attention() -> None:
+    """Test hook: the next packed or paged attention issues no loads, so its waits time out."""
+    load().ra_test_stall_next_attention()
+
+
+def _one_device(**tensors) -> None:
+    """The calls run on the current device's stream: every tensor has to be there."""
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _half_tensor(t: torch.Tensor, code: int, name: str) -> None:
+    want = _HALF.get(code)
+    if want is not None and t.dtype != want:
+        raise ValueError(f"{name}: expected {want}, got {t.dtype}")
+
+
+def _stored_tensor(t: torch.Tensor | None, code: int, name: str) -> None:
+    want = _STORED.get(code)
+    if t is not None and want is not None and t.dtype not in want:
+        raise ValueError(f"{name}: expected {want[-1]}, got {t.dtype}")
+
+
+def packed_attention_params(q, k, v, out, *, B: int = 1, causal: bool = False,
+                            softmax_scale: float | None = None) -> PackedAttentionParams:
+    """Parameters of packed_attention for tensors of shape [tokens, heads, head_dim] with any
+    token and head strides: views of a qkv_cte_mx output, for example
+    ``qkv.view(T, heads, d)[:, :num_heads]`` (BSD) or ``planes[:num_heads].transpose(0, 1)``
+    (NBSd).  softmax_scale defaults to head_dim ** -0.5."""
+    for name, t, other in (("q", q, q), ("k", k, k), ("v", v, k), ("out", out, q)):
+        if t.dim() != 3:
+            raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
+        if t.shape != other.shape or t.shape[2] != q.shape[2]:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {tuple(other.shape)}")
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name}: expected {q.dtype}, got {t.dtype}")
+        if t.shape[2] > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+    codes = {torch.bfloat16: RA_BF16, torch.float16: RA_FP16}
+    if q.dtype not in codes:
+        raise ValueError(f"q: expected bfloat16 or float16, got {q.dtype}")
+    d = q.shape[2]
+    return PackedAttentionParams(
+        B=B, total_q=q.shape[0], total_k=k.shape[0], num_heads=q.shape[1], num_kv_heads=k.shape[1],
+        head_dim=d, dtype=codes[q.dtype], causal=1 if causal else 0,
+        softmax_scale=d ** -0.5 if softmax_scale is None else softmax_scale,
+        q_token_stride=q.stride(0), q_head_stride=q.stride(1), k_token_stride=k.stride(0),
+        k_head_stride=k.stride(1), v_token_stride=v.stride(0), v_head_stride=v.stride(1),
+        out_token_stride=out.stride(0), out_head_stride=out.stride(1))
+
+
+def packed_extents(p: PackedAttentionParams) -> dict[str, int]:
+    """Bytes that each tensor argument of packed_attention spans, from its first element:
+    the strided extent of q, k, v and out, and [total_q, num_heads], [B + 1] for the others."""
+    def span(tokens, heads, ts, hs):
+        return ((max(tokens, 1) - 1) * ts + (max(heads, 1) - 1) * hs + p.head_dim) * 2
+    return {"q": span(p.total_q, p.num_heads, p.q_token_stride, p.q_head_stride),
+            "k": span(p.total_k, p.num_kv_heads, p.k_token_stride, p.k_head_stride),
+            "v": span(p.total_k, p.num_kv_heads, p.v_token_stride, p.v_head_stride),
+            "out": span(p.total_q, p.num_heads, p.out_token_stride, p.out_head_stride),
+            "lse": p.total_q * p.num_heads * 4, "cu_seqlens_q": (p.B + 1) * 4, "cu_seqlens_k": (p.B + 1) * 4}
+
+
+def _strided_ptr(t: torch.Tensor, nbytes: int, name: str) -> int:
+    """Pointer of a strided 16-bit tensor whose storage holds `nbytes` from its first element."""
+    held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+    if held < nbytes:
+        raise ValueError(f"{name}: the call needs {nbytes} bytes, the tensor's storage holds {held}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def packed_attention_workspace_bytes(params: PackedAttentionParams) -> int:
+    n = ctypes.c_size_t()
+    _check(load().packed_attention_workspace_bytes(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def packed_attention(params, q, k, v, out, workspace, lse=None, cu_seqlens_q=None, cu_seqlens_k=None,
+                     stream=None) -> None:
+    """Attention over packed prompts (header: packed_attention); q, k, v and out as the
+    tensors that ``packed_attention_params`` was given, or others with the same strides."""
+    ext = packed_extents(params)
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _half_tensor(t, params.dtype, name)
+    for name, t in (("lse", lse), ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
+        _need(t, ext[name], name)
+    ptrs = [_strided_ptr(t, ext[name], name) for name, t in (("q", q), ("k", k), ("v", v), ("out", out))]
+    _one_device(q=q, k=k, v=v, out=out, workspace=workspace, lse=lse, cu_seqlens_q=cu_seqlens_q,
+                cu_seqlens_k=cu_seqlens_k)
+    _check(load().packed_attention(
+        ctypes.byref(params), *ptrs, _ptr(lse, torch.float32, "lse"),
+        _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"), _ptr(cu_seqlens_k, torch.int32, "cu_seqlens_k"),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)))
+
+
+def paged_extents(cache: KvRmsNormRopeCacheParams, p: PagedAttentionParams) -> dict[str, int]:
+    """Bytes that each tensor argument of paged_attention spans, from the call's parameters."""
+    kv = kv_extents(cache)
+    rows = max(p.total_q, 0) * max(p.num_heads, 0)
+    return {"q": rows * max(cache.Dkv, 0) * 2, "out": rows * max(cache.Dv, 0) * 2, "lse": rows * 4,
+            "seq_lens": p.B * 4, "block_table": p.B * p.block_table_stride * 4, "cu_seqlens_q": (p.B + 1) * 4,
+            "dev_error_count": 4,
+            **{n: kv[n] for n in ("k_cache", "ckv_cache", "k_rope_scale", "c_kv_scale", "k_rope_offset",
+                                  "c_kv_offset")}}
+
+
+def paged_attention_workspace_bytes(cache: KvRmsNormRopeCacheParams, params: PagedAttentionParams) -> int:
+    n = ctypes.c_size_t()
+    _check(load().paged_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention(cache, params, q, k_cache, ckv_cache, seq_lens, out, workspace, block_table=None,
+                    cu_seqlens_q=None, k_rope_scale=None, c_kv_scale=None, k_rope_offset=None,
+                    c_kv_offset=None, lse=None, dev_error_count=None, stream=None) -> None:
+    """Attention of new tokens over the caches of kv_rms_norm_rope_cache (header:
+    paged_attention).  ``cache`` is that call's parameter struct; block_table is [B, pages],
+    and its width is taken as ``block_table_stride`` where that is 0."""
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != params.B:
+            raise ValueError(f"block_table: expected [{params.B}, pages], got {tuple(block_table.shape)}")
+        if params.block_table_stride == 0:
+            params = PagedAttentionParams(params.B, params.total_q, params.num_heads, params.causal,
+                                          params.softmax_scale, params.reserved, params.max_seq_len,
+                                          block_table.shape[1])
+    _need_all(paged_extents(cache, params), q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, out=out,
+              block_table=block_table, cu_seqlens_q=cu_seqlens_q, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale,
+              k_rope_offset=k_rope_offset, c_kv_offset=c_kv_offset, lse=lse, dev_error_count=dev_error_count)
+    _half_tensor(q, cache.kv_dtype, "q")
+    _half_tensor(out, cache.kv_dtype, "out")
+    _stored_tensor(k_cache, cache.k_cache_dtype, "k_cache")
+    _stored_tensor(ckv_cache, cache.ckv_cache_dtype, "ckv_cache")
+    _one_device(q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, out=out, workspace=workspace,
+                block_table=block_table, cu_seqlens_q=cu_seqlens_q, lse=lse)
+    _check(load().paged_attention(
+        ctypes.byref(cache), ctypes.byref(params), _ptr(q, None, "q"), _ptr(k_cache, None, "k_cache"),
+        _ptr(ckv_cache, None, "ckv_cache"), _ptr(seq_lens, torch.int32, "seq_lens"),
+        _ptr(block_table, torch.int32, "block_table"), _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+        _ptr(k_rope_scale, torch.float32, "k_rope_scale"), _ptr(c_kv_scale, torch.float32, "c_kv_scale"),
+        _ptr(k_rope_offset, torch.float32, "k_rope_offset"), _ptr(c_kv_offset, torch.float32, "c_kv_offset"),
+        _ptr(out, None, "out"), _ptr(lse, torch.float32, "lse"),
+        _ptr(dev_error_count, torch.int32, "dev_error_count"), _ptr(workspace, torch.uint8, "workspace"),
+        workspace.numel(), _stream(stream)))
+
+
+def attention_status(workspace: torch.Tensor, stream=None) -> int:
+    """Synchronises the stream; returns the workspace's status word (0 = fine) and clears it."""
+    v = ctypes.c_int32()
+    st = load().attention_status(_ptr(workspace, torch.uint8, "workspace"), _stream(stream), ctypes.byref(v))
+    if st not in (RA_OK, -6):
+        _check(st)
+    return v.value
+
+
+def read_extents(p: KvRmsNormRopeCacheParams) -> dict[str, int]:
+    """Bytes that each tensor argument of kv_cache_read spans, from the call's parameters."""
+    kv = kv_extents(p)
+    kw, cw = (p.rope_size, p.Dkv - p.rope_size) if p.variant == 1 else (p.Dkv, p.Dv)
+    rows = max(p.B, 0) * max(p.N, 0) * max(p.S, 0)
+    return {"k_out": rows * max(kw, 0) * 2, "c_kv_out": rows * max(cw, 0) * 2, "dev_error_count": 4,
+            **{n: kv[n] for n in ("index", "k_cache", "ckv_cache", "k_rope_scale", "c_kv_scale", "k_rope_offset",
+                                  "c_kv_offset")}}
+
+
+def kv_cache_read(params, index, k_cache, ckv_cache, k_out=None, c_kv_out=None, k_rope_scale=None,
+                  c_kv_scale=None, k_rope_offset=None, c_kv_offset=None, dev_error_count=None,
+                  stream=None) -> None:
+    """Rows of the caches of kv_rms_norm_rope_cache read back (header: kv_cache_read)."""
+    _need_all(read_extents(params), index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_out=k_out,
+              c_kv_out=c_kv_out, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale, k_rope_offset=k_rope_offset,
+              c_kv_offset=c_kv_offset, dev_error_count=dev_error_count)
+    for name, t in (("k_out", k_out), ("c_kv_out", c_kv_out)):
+        if t is not None:
+            _half_tensor(t, params.kv_dtype, name)
+    _stored_tensor(k_cache, params.k_cache_dtype, "k_cache")
+    _stored_tensor(ckv_cache, params.ckv_cache_dtype, "ckv_cache")
+    _one_device(index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_out=k_out, c_kv_out=c_kv_out)
+    _check(load().kv_cache_read(
+        ctypes.byref(params), _ptr(index, torch.int64, "index"), _ptr(k_cache, None, "k_cache"),
+        _ptr(ckv_cache, None, "ckv_cache"), _ptr(k_rope_scale, torch.float32, "k_rope_scale"),
+        _ptr(c_kv_scale, torch.float32, "c_kv_scale"), _ptr(k_rope_offset, torch.float32, "k_rope_offset"),
+        _ptr(c_kv_offset, torch.float32, "c_kv_offset"), _ptr(k_out, None, "k_out"),
+        _ptr(c_kv_out, None, "c_kv_out"), _ptr(dev_error_count, torch.int32, "dev_error_count"),
+        _stream(stream)))

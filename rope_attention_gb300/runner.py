@@ -136,3 +136,64 @@ class KvRun:
             self.params, self.kv, self.gamma, self.cos, self.sin, self.index, self.k_cache,
             self.ckv_cache, self.k_scale, self.v_scale, self.k_offset, self.v_offset, self.v,
             self.k_rope, self.c_kv, self.err, stream)
+
+
+class PackedAttentionRun:
+    """packed_attention on the output of a QkvRun: its Q, K and V columns as they lie, each
+    batch element one sequence (or ``starts``, the first token of each and the total)."""
+
+    def __init__(self, qkv: QkvRun, causal: bool = False, starts: list[int] | None = None, scale: float | None = None):
+        c = qkv.case
+        nq, nkv, d = c.num_heads, c.num_kv_heads, c.head_dim
+        if qkv.params.output_layout == native.RA_LAYOUT_BSD:
+            heads = qkv.out.view(c.T, c.I // d, d)
+        else:
+            heads = qkv.out.transpose(0, 1)
+        self.q, self.k, self.v = heads[:, :nq], heads[:, nq:nq + nkv], heads[:, nq + nkv:]
+        device = qkv.out.device
+        self.out = torch.empty(c.T, nq, d, dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty(c.T, nq, dtype=torch.float32, device=device)
+        self.starts = None if starts is None else torch.tensor(starts, dtype=torch.int32, device=device)
+        self.params = native.packed_attention_params(self.q, self.k, self.v, self.out,
+                                                     B=c.B if starts is None else len(starts) - 1, causal=causal,
+                                                     softmax_scale=scale)
+        self.workspace = torch.zeros(native.packed_attention_workspace_bytes(self.params), dtype=torch.uint8,
+                                     device=device)
+
+    def run(self, stream=None) -> None:
+        native.packed_attention(self.params, self.q, self.k, self.v, self.out, self.workspace, self.lse,
+                                self.starts, self.starts, stream)
+
+    def status(self, stream=None) -> int:
+        return native.attention_status(self.workspace, stream)
+
+
+class PagedAttentionRun:
+    """paged_attention of query tokens q [total_q, heads, Dkv] over the caches of a KvRun.
+    ``table`` [B, pages] int32 (None in Norm mode), ``lens`` [B] and ``starts`` [B + 1] lists."""
+
+    def __init__(self, kv: KvRun, q: torch.Tensor, lens: list[int], table=None, starts: list[int] | None = None,
+                 causal: bool = True, scale: float | None = None):
+        c, device = kv.case, q.device
+        self.kv, self.q = kv, q
+        i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).to(device)
+        self.lens, self.table = i32(lens), None if table is None else i32(table)
+        self.starts = None if starts is None else i32(starts)
+        self.out = torch.empty(q.shape[0], q.shape[1], c.ckv_width, dtype=q.dtype, device=device)
+        self.lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.params = native.PagedAttentionParams(
+            B=len(lens), total_q=q.shape[0], num_heads=q.shape[1], causal=1 if causal else 0,
+            softmax_scale=c.Dkv ** -0.5 if scale is None else scale, max_seq_len=max(lens),
+            block_table_stride=0 if table is None else self.table.shape[1])
+        self.workspace = torch.zeros(native.paged_attention_workspace_bytes(kv.params, self.params),
+                                     dtype=torch.uint8, device=device)
+
+    def run(self, stream=None) -> None:
+        k = self.kv
+        native.paged_attention(k.params, self.params, self.q, k.k_cache, k.ckv_cache, self.lens, self.out,
+                               self.workspace, self.table, self.starts, k.k_scale, k.v_scale, k.k_offset,
+                               k.v_offset, self.lse, self.err, stream)
+
+    def status(self, stream=None) -> int:
+        return native.attention_status(self.workspace, stream)
