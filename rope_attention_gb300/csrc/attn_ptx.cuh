@@ -1,5 +1,5 @@
 // Inline-PTX helpers of the attention kernels (sm_103a): one-CTA tcgen05 MMAs on 16-bit
-// operands, TMEM loads and stores, TMA tile loads and cp.async, each written from the PTX
+// operands, TMEM loads and stores and TMA tile loads, each written from the PTX
 // ISA, and the bounded waits' bookkeeping that those kernels share.
 #pragma once
 
@@ -97,6 +97,35 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// true in one lane, always the same one.  The whole warp must be there; operands computed
+// inside the branch it guards stay in uniform registers, where the MMA takes them from.
+// (Measured: M = 128, N = 64 MMAs in a loop go out every 50 cycles, the tensor core's own
+// rate; behind a comparison of the thread index every 74, and one by one every 170-200.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// `steps` (1..4) consecutive K = 16 steps of D[tmem] (+)= A[smem] B[smem], the descriptors
+// SA and SB further in 16-byte units at each step; `acc` 0 starts D anew.
+template <int SA, int SB>
+__device__ __forceinline__ void mma4_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                            uint32_t steps) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1, p2, p3, on;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.gt.u32 p1, %5, 1;\n\tsetp.gt.u32 p2, %5, 2;\n\tsetp.gt.u32 p3, %5, 3;\n\t"
+      "setp.eq.b32 on, 0, 0;\n\t"
+      "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %7;\n\t"
+      "add.s64 a2, %1, %8;\n\tadd.s64 b2, %2, %9;\n\t"
+      "add.s64 a3, %1, %10;\n\tadd.s64 b3, %2, %11;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+      "@p1 tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, on;\n\t"
+      "@p2 tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, on;\n\t"
+      "@p3 tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, on;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(steps), "n"(SA), "n"(SB), "n"(2 * SA), "n"(2 * SB), "n"(3 * SA),
+      "n"(3 * SB)
+      : "memory");
+}
 // arrive on the mbarrier once every tcgen05 operation this thread issued so far has completed
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -117,21 +146,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint3
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// 16 bytes global -> shared, the part beyond `bytes` (0 or 16) zero-filled
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// this thread's arrival on the mbarrier once its cp.async copies so far have landed (the
-// arrival is one of the barrier's expected count)
-__device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // ---------------------------------------------------------------- registers
 // every warp of the warpgroup; the shares of a block add up to what it was launched with
 template <int N>
@@ -147,13 +161,43 @@ __device__ __forceinline__ void set_max_regs_dec() {
 // 2^x, flushing subnormal results: the probabilities they stand for are below 2^-126
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   if constexpr (BF16) return pack_bf16x2(lo, hi);
   else return pack_f16x2(lo, hi);
+}
+// 32 probabilities 2^(s scale + neg): their pairs rounded to 16 bits in w, their fp32 sums in
+// acc.  All the exponentials of a batch go out before the first result is used: a warp
+// issues in order, and with each used at once 64 elements took 827 cycles (one warp per
+// scheduler; 882 for two), against 353 (615) in batches of 32, near the rate of the
+// exponential unit (8 lanes a cycle: 256, 512).
+template <bool BF16>
+__device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float2 neg, float2 (&acc)[4], uint32_t* w) {
+  float2 t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    t[i] = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale, neg);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    t[i].x = ex2(t[i].x);
+    t[i].y = ex2(t[i].y);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    acc[i & 3] = __fadd2_rn(acc[i & 3], t[i]);
+    if constexpr (BF16)
+      asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t[i].y), "f"(t[i].x));
+    else
+      asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t[i].y), "f"(t[i].x));
+  }
 }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(static_cast<int>(0xff800000u)); }
 

@@ -215,17 +215,17 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attention_kernel(const __g
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0 && n_max > 0) {
+    if (n_max > 0) {
       constexpr uint32_t id_s = idesc_f16(BF16, false, false, kRows, kKeys);
       constexpr uint32_t id_o = idesc_f16(BF16, false, true, kRows, DP);
       const uint64_t ring_k = sdesc_kmajor_sw128(s0 + SH::kRing);
       const uint64_t ring_v = sdesc_mnmajor_sw128(s0 + SH::kRing, SH::kSlabBytes);
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t par) {
-        if (ok) ok = bounded_wait_one(bar, par, p.wait_ns, abort_flag);
+        if (ok) ok = bounded_wait_warp(bar, par, p.wait_ns, abort_flag);
         return ok;
       };
-      auto issue_s = [&](int i, int st) {
+      auto issue_s = [&](int i, int st) {  // one lane
         const uint64_t a = sdesc_kmajor_sw128(s0 + i * SH::kTileBytes);
         const uint64_t bd = ring_k + static_cast<uint64_t>(st * (SH::kTileBytes >> 4));
 #pragma unroll
@@ -235,38 +235,46 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attention_kernel(const __g
         }
         tc_commit(s_full(i));
       };
-      auto issue_o = [&](int i, int st, bool first) {
-        const uint64_t bd = ring_v + static_cast<uint64_t>(st * (SH::kTileBytes >> 4));
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_f16_ts(o_col(i), s_col(i) + 8 * k, bd + 128 * k, id_o, !first || k > 0);
-      };
       if (wait(full(0), 0)) {
         for (int i = 0; i < 2; ++i)
           if (n_tiles[i] > 0 && wait(q_full(i), 0)) {
             tc_fence_after();
-            issue_s(i, 0);
+            if (elect_one()) issue_s(i, 0);
+            __syncwarp();
           }
-        if (ok) tc_commit(empty(0));
+        if (ok && elect_one()) tc_commit(empty(0));
+        __syncwarp();
       }
+      int sv = 1, sk = 2;                        // ring stages of V j and K j + 1
+      uint32_t par_v = 0, par_k = 0;
       for (int32_t j = 0; ok && j < n_max; ++j) {
-        const int32_t uv = 2 * j + 1, uk = 2 * j + 2;
-        const int sv = uv % SH::kStages, sk = uk % SH::kStages;
-        if (!wait(full(sv), (uv / SH::kStages) & 1)) break;
-        if (j + 1 < n_max && !wait(full(sk), (uk / SH::kStages) & 1)) break;
+        if (!wait(full(sv), par_v)) break;
+        if (j + 1 < n_max && !wait(full(sk), par_k)) break;
         for (int i = 0; i < 2; ++i) {
           if (j >= n_tiles[i]) continue;
           if (!wait(p_ready(i), j & 1)) break;
           tc_fence_after();
-          issue_o(i, sv, j == 0);
-          if (j + 1 < n_tiles[i]) issue_s(i, sk);
-          else tc_commit(o_done(i));
+          if (elect_one()) {
+            const uint64_t bd = ring_v + static_cast<uint64_t>(sv * (SH::kTileBytes >> 4));
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_f16_ts(o_col(i), s_col(i) + 8 * k, bd + 128 * k, id_o, j > 0 || k > 0);
+            if (j + 1 < n_tiles[i]) issue_s(i, sk);
+            else tc_commit(o_done(i));
+          }
+          __syncwarp();
         }
         if (!ok) break;
-        tc_commit(empty(sv));
-        if (j + 1 < n_max) tc_commit(empty(sk));
+        if (elect_one()) {
+          tc_commit(empty(sv));
+          if (j + 1 < n_max) tc_commit(empty(sk));
+        }
+        __syncwarp();
+        if ((sv += 2) >= SH::kStages) sv -= SH::kStages, par_v ^= 1u;
+        if ((sk += 2) >= SH::kStages) sk -= SH::kStages, par_k ^= 1u;
       }
-      tc_commit(drain_bar);  // every product must finish before TMEM is released
+      if (elect_one()) tc_commit(drain_bar);  // every product must finish before TMEM is released
+      __syncwarp();
       bounded_drain(drain_bar, 0, kDrainNs);
     }
     __syncwarp();
@@ -325,24 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attention_kernel(const __g
       }
       const float neg = m == neg_inf() ? 0.f : -m * p.sl2;
       const float2 sl = make_float2(p.sl2, p.sl2), ng = make_float2(neg, neg);
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const int k = 64 * h + 2 * c;
-          float2 a = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sl, ng);
-          float2 d = __ffma2_rn(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), sl, ng);
-          a.x = ex2(a.x), a.y = ex2(a.y), d.x = ex2(d.x), d.y = ex2(d.y);
-          acc0 = __fadd2_rn(acc0, a);
-          acc1 = __fadd2_rn(acc1, d);
-          w[c] = pack_half2<BF16>(a.x, a.y);
-          w[c + 1] = pack_half2<BF16>(d.x, d.y);
-        }
-        tmem_st_x32(s_addr + 32 * h, w);  // P takes the place of S: 64 columns of pairs
+      for (int h = 0; h < 4; ++h) {
+        uint32_t w[16];
+        exp_batch<BF16>(s + 32 * h, sl, ng, acc, w);
+        tmem_st_x16(s_addr + 16 * h, w);  // P takes the place of S: 64 columns of pairs
       }
-      l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+      const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      l += sum.x + sum.y;
       if ((j + 1) * kKeys > Lk) {
         // V rows behind the sequence's end meet P = 0, but 0 times a stray NaN or
         // infinity is NaN: zero them in shared memory

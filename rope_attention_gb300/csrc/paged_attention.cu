@@ -24,11 +24,13 @@
 //    of S come from whatever follows in shared memory and are never read.
 //  * V1's value row is the first part of its key row: one tile in shared memory serves
 //    both products (K-major for S, MN-major for O^T).
-//  * Warps 4-7 gather rows with 16-byte cp.async (absent rows zero-filled), straight into
-//    the swizzled operand tile for 16-bit caches, or into a staging ring from which each
-//    thread converts the codes that it copied itself; warps 0-3 are the softmax, the
-//    rescaling and the epilogue; warp 8 issues the MMAs, taking whichever of the next
-//    S = Q K^T and the next O^T += V^T P^T is ready first.
+//  * Warp 9 reads the block table and issues TMA boxes of 16, 32 or 64 rows (what divides
+//    a page), 64 channels wide: straight into the swizzled operand tile for 16-bit caches,
+//    or as codes into a staging ring that warps 4-7 convert from.  Rows behind a
+//    sequence's end and rows of absent pages are zeroed in shared memory (0 times a
+//    stray NaN is NaN) and masked in S.  Warps 0-3 are the softmax, the rescaling and the
+//    epilogue; warp 8 issues the MMAs, taking whichever of the next S = Q K^T and the
+//    next O^T += V^T P^T is ready first.
 // Every wait is bounded in time (status word).
 #include <cuda_fp8.h>
 
@@ -46,10 +48,11 @@ namespace {
 
 constexpr int kKeys = 64;                 // keys per tile: one 128-byte swizzled row of P
 constexpr int kSlab = kKeys * 128;        // 64 keys x 64 channels of 16 bits
-constexpr int kThreads = 288;
-constexpr int kSoftmax = 128, kProducers = 128;
-constexpr int kMmaWarp = 8;
-constexpr int kValidRing = 16;            // > tiles between a producer and the softmax
+constexpr int kCodeSlab = kKeys * 64;      // the same of codes
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 128, kConverters = 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kValidRing = 16;            // > tiles between the loads and the softmax
 constexpr int kMaxStages = 6;
 constexpr int kMinTiles = 4;              // tiles per block below which a split costs more than it gives
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
@@ -59,6 +62,7 @@ constexpr int kMaxBlocks = 160;           // blocks that a workspace has room fo
 constexpr int kSCols = 2 * kKeys;         // TMEM: two S buffers, then O^T
 
 struct Params {
+  CUtensorMap tk, tv;           // the caches' rows: 64 channels x 1 x box_rows boxes
   const uint16_t* q;
   uint16_t* out;
   float* lse;
@@ -72,10 +76,10 @@ struct Params {
   int32_t* meta;                // [G][8]
   int64_t table_stride, cap;    // cap: positions that a sequence can have
   int64_t block_num, cache_seq;
-  int32_t B, total_q, N, heads, g, NR, block_size, bs_shift;
+  int32_t B, total_q, N, heads, g, NR, nr_shift, block_size, bs_shift;
   int32_t Dk, Dv, Dko;          // key width, value width, width of a k_cache row
   int32_t v1, mode, f16, kq, vq, k_scalar, v_scalar, causal;
-  int32_t ca, nc, magic;        // 16-byte chunks of a v row, of both rows; idx / nc = idx * magic >> 20
+  int32_t box_rows;
   int32_t vslabs, kslabs, qslabs, kslab0;
   int32_t ns, nsg;              // operand stages, staging stages (0: 16-bit caches)
   int32_t stage_bytes, staging_bytes;
@@ -87,9 +91,9 @@ struct Params {
 
 struct Misc {                   // behind the tiles in shared memory
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t code_full[kMaxStages], code_empty[kMaxStages];
   uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
   uint64_t valid[kValidRing];
-  int64_t row_index[2][kKeys];
   int64_t scan[kThreads / 32];
   int64_t start_off;
   int32_t start_b;
@@ -116,8 +120,8 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len) { return max(1, (len + 
 __device__ __forceinline__ int64_t seq_work(const Params& p, int32_t b) {
   int32_t s, lq;
   q_span(p, b, s, lq);
-  const int64_t rows = static_cast<int64_t>(lq) * p.g;
-  return (rows + p.NR - 1) / p.NR * p.N * tiles_of(seq_len_of(p, b));
+  const int64_t row_tiles = (static_cast<uint32_t>(lq * p.g) + p.NR - 1) >> p.nr_shift;  // lq * g < 2^31
+  return row_tiles * p.N * tiles_of(seq_len_of(p, b));
 }
 
 // One block's share of an item: key tiles [ta, tb) of row tile rt of (b, n).
@@ -136,25 +140,27 @@ struct Walker {
       int32_t qs, lq;
       q_span(p, b, qs, lq);
       const int32_t len = seq_len_of(p, b), T = tiles_of(len);
-      const int64_t rows = static_cast<int64_t>(lq) * p.g;
-      const int64_t rts = (rows + p.NR - 1) / p.NR;
-      if (off >= rts * p.N * T) {
-        off -= rts * p.N * T;
+      const int32_t rows = lq * p.g;
+      const int32_t rts = (static_cast<uint32_t>(rows) + p.NR - 1) >> p.nr_shift;
+      const int64_t work = static_cast<int64_t>(rts) * p.N * T;
+      if (off >= work) {
+        off -= work;
         ++b;
         continue;
       }
-      const int64_t item = off / T;
+      // (a 64-bit division is a hundred instructions: only for what needs it)
+      const int64_t item = work >> 32 ? off / T : static_cast<int64_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(T));
       w.b = b;
       w.t0 = static_cast<int32_t>(off - item * T);
       w.T = T;
       w.take = static_cast<int32_t>(min(static_cast<int64_t>(T - w.t0), rem));
-      w.n = static_cast<int32_t>(item / rts);
-      w.rt = static_cast<int32_t>(item - w.n * rts);
-      w.rows = static_cast<int32_t>(min(static_cast<int64_t>(p.NR), rows - static_cast<int64_t>(w.rt) * p.NR));
+      w.n = static_cast<int32_t>(static_cast<uint32_t>(item) / static_cast<uint32_t>(rts));  // item < rts * N <= 2^31
+      w.rt = static_cast<int32_t>(item - static_cast<int64_t>(w.n) * rts);
+      w.rows = min(p.NR, rows - w.rt * p.NR);
       w.q_start = qs;
       w.Lq = lq;
       w.len = len;
-      const int32_t last = static_cast<int32_t>((static_cast<int64_t>(w.rt) * p.NR + w.rows - 1) / p.g);
+      const int32_t last = static_cast<int32_t>(static_cast<uint32_t>(w.rt * p.NR + w.rows - 1) / static_cast<uint32_t>(p.g));
       const int32_t seen = p.causal ? min(len, max(0, len - lq + last + 1)) : len;
       const int32_t vt = (seen + kKeys - 1) / kKeys;
       w.ta = min(w.t0, vt);
@@ -201,31 +207,136 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t c, int32_t kind) {
   return r;
 }
 
-__device__ __forceinline__ float load_half(const uint16_t* p, bool f16) {
-  const uint16_t u = *p;
-  return f16 ? __half2float(__ushort_as_half(u)) : __uint_as_float(static_cast<uint32_t>(u) << 16);
+template <bool F16>
+__device__ __forceinline__ float half_to_float(uint32_t u) {
+  return F16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u))) : __uint_as_float(u << 16);
 }
-__device__ __forceinline__ uint16_t to_half(float x, bool f16) {
-  return f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+template <bool F16>
+__device__ __forceinline__ uint16_t to_half(float x) {
+  return F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
-__device__ __forceinline__ uint32_t pair16(uint16_t lo, uint16_t hi) { return lo | (static_cast<uint32_t>(hi) << 16); }
 // scale and offset of one channel of a cache row (1 and 0 for a 16-bit cache)
 __device__ __forceinline__ float2 channel_quant(const float* scale, const float* offset, int32_t at, int32_t scalar) {
   if (scale == nullptr) return make_float2(1.f, 0.f);
   const int32_t i = scalar ? 0 : at;
   return make_float2(__ldg(scale + i), offset ? __ldg(offset + i) : 0.f);
 }
-// the quantisation of key channel c of head n: V1's key is the ckv row, then the k row
-__device__ __forceinline__ float2 key_quant(const Params& p, int32_t n, int32_t c) {
-  if (p.v1)
-    return c < p.Dv ? channel_quant(p.v_scale, p.v_offset, c, p.v_scalar)
-                    : channel_quant(p.k_scale, p.k_offset, c - p.Dv, p.k_scalar);
-  return channel_quant(p.k_scale, p.k_offset, n * p.Dk + c, 0);
+// the scales of key channels c..c+7 of head n: V1's key is the ckv row, then the k row
+__device__ __forceinline__ void key_scales(const Params& p, int32_t n, int32_t c, float (&s)[8]) {
+  const bool latent = p.v1 && c < p.Dv;
+  const float* scale = latent ? p.v_scale : p.k_scale;
+  const bool one = latent ? p.v_scalar : p.k_scalar;
+  const int32_t at = latent ? c : p.v1 ? c - p.Dv : n * p.Dk + c;
+  if (scale == nullptr || one || c >= p.Dk) {
+    const float x = scale != nullptr && one ? __ldg(scale) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = x;
+    return;
+  }
+  const float4 a = __ldg(reinterpret_cast<const float4*>(scale + at)), b = __ldg(reinterpret_cast<const float4*>(scale + at) + 1);
+  s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w, s[4] = b.x, s[5] = b.y, s[6] = b.z, s[7] = b.w;
+}
+__device__ __forceinline__ float key_offset(const Params& p, int32_t n, int32_t c) {
+  if (p.v1 && c < p.Dv) return channel_quant(p.v_scale, p.v_offset, c, p.v_scalar).y;
+  return channel_quant(p.k_scale, p.k_offset, p.v1 ? c - p.Dv : n * p.Dk + c, p.k_scalar).y;
 }
 __device__ __forceinline__ float2 value_quant(const Params& p, int32_t n, int32_t c) {
   return channel_quant(p.v_scale, p.v_offset, p.v1 ? c : n * p.Dv + c, p.v_scalar);
 }
 
+// The piece's rows of q in the swizzled operand; where the key is codes, over the key's
+// scales and behind a power of two that keeps the row's elements below 2^15: 2^29 above
+// fp16's subnormals, so that a bound on the largest element (the largest |q| times the
+// largest 1 / s) serves as well as the element itself.  row_scale gets the softmax scale
+// that undoes the power, row_const the lse's share of the offsets.  A warp takes a row, a
+// lane the 8-channel chunks lane, lane + 32, lane + 64.
+template <bool F16>
+__device__ __forceinline__ void load_q(const Params& p, int32_t n, int32_t rows, uint8_t* smem, const int32_t* out_row,
+                                       float* row_scale, float* row_const, bool scaled, int warp, int lane) {
+  const int nck = p.Dk / 8;
+  float inv_s[3][8], top = 0.f;
+  if (scaled) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = (lane + 32 * i) * 8;
+      float s[8];
+      key_scales(p, n, c, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        inv_s[i][e] = c < p.Dk ? rcp(s[e]) : 0.f;
+        top = fmaxf(top, fabsf(inv_s[i][e]));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  constexpr int kBatch = 4;  // rows whose loads are in flight together
+#pragma unroll 1
+  for (int r0 = warp; r0 < rows; r0 += 4 * kBatch) {
+    uint4 x[kBatch][3];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int r = r0 + 4 * t;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;
+        x[t][i] = r < rows && c < nck
+                      ? __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(out_row[r]) * p.Dk + c * 8))
+                      : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int r = r0 + 4 * t;
+      if (r >= rows) break;
+      float up = 1.f;
+      if (scaled) {
+        uint32_t big = 0;  // |q| as bits orders like the value in either type
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          big = __vmaxu2(__vmaxu2(big, x[t][i].x & 0x7FFF7FFFu), x[t][i].y & 0x7FFF7FFFu);
+          big = __vmaxu2(__vmaxu2(big, x[t][i].z & 0x7FFF7FFFu), x[t][i].w & 0x7FFF7FFFu);
+        }
+        big = __reduce_max_sync(0xffffffffu, max(big & 0xFFFFu, big >> 16));
+        const float amax = half_to_float<F16>(big);
+        // amax < 2^(e + 15), top < 2^(f + 15): amax * top * up < 2^15
+        up = exp2_int(max(-100, min(100, -(scale_exponent(amax) + scale_exponent(top) + 15))));
+      }
+      if (lane == 0) {
+        row_scale[r] = p.sl2 / up;
+        row_const[r] = 0.f;
+      }
+      float shift = 0.f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;
+        if (c >= nck) continue;
+        if (scaled) {
+          // V1's key can be codes in one part and 16-bit values in the other
+          const bool f16 = F16 || ((p.v1 && c * 8 < p.Dv) ? p.vq != 0 : p.kq != 0);
+          uint32_t u[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = half_to_float<F16>(u[e] & 0xFFFFu) * inv_s[i][2 * e];
+            const float b = half_to_float<F16>(u[e] >> 16) * inv_s[i][2 * e + 1];
+            if (p.lse) shift += a * key_offset(p, n, c * 8 + 2 * e) + b * key_offset(p, n, c * 8 + 2 * e + 1);
+            u[e] = f16 ? pack_f16x2(a * up, b * up) : pack_bf16x2(a * up, b * up);
+          }
+          x[t][i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        *reinterpret_cast<uint4*>(smem + (c >> 3) * p.NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[t][i];
+      }
+      if (scaled && p.lse) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) shift += __shfl_xor_sync(0xffffffffu, shift, o);
+        if (lane == 0) row_const[r] = -shift * p.scale;
+      }
+    }
+  }
+}
+
+// F16: q, out and 16-bit caches are fp16, not bf16; P16: P is fp16 (V's operand is)
+template <bool F16, bool P16>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + p.off_misc);
@@ -252,8 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   if (lane == 31) ms.scan[warp] = incl;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ns; ++s) {
-      mbar_init(smem_u32(&ms.kv_full[s]), kProducers);
+      // one arrival with the bytes of a 16-bit cache, one from each thread that converts codes
+      mbar_init(smem_u32(&ms.kv_full[s]), (p.vq == 0 || p.kq == 0 ? 1 : 0) + (p.nsg != 0 ? kConverters : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
+    }
+    for (int s = 0; s < p.nsg; ++s) {
+      mbar_init(smem_u32(&ms.code_full[s]), 1);
+      mbar_init(smem_u32(&ms.code_empty[s]), kConverters);
     }
     mbar_init(smem_u32(&ms.s_full[0]), 1);
     mbar_init(smem_u32(&ms.s_full[1]), 1);
@@ -294,200 +410,206 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   const uint32_t tmem = ms.tmem;
   volatile int* abort_flag = &ms.abort;
   Walker walk{ms.start_b, ms.start_off, min(per, W - start)};
-  Piece w;
+  Piece w{};
 
-  if (warp >= 4 && warp < kMmaWarp) {
-    // ------------------------------------------------------------ producers
-    const int tid = threadIdx.x - kSoftmax;
-    const int chunks = kKeys * p.nc;
-    const int64_t v_row = static_cast<int64_t>(p.ca) * 16, k_row = static_cast<int64_t>(p.nc - p.ca) * 16;
-    // this thread's key of tile t of piece w, as a cache row (-1: none)
-    auto row_of = [&](const Piece& x, int32_t t) -> int64_t {
-      const int32_t pos = t * kKeys + tid;
-      if (tid >= kKeys || pos >= x.len) return -1;
-      if (p.mode == kModeNorm) return (static_cast<int64_t>(x.b) * p.N + x.n) * p.cache_seq + pos;
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    const int groups = kKeys / p.box_rows;
+    const bool direct = p.vq == 0 || p.kq == 0, staged = p.vq != 0 || p.kq != 0;
+    const uint32_t direct_bytes = ((p.vq ? 0 : p.vslabs) + (p.kq ? 0 : p.kslabs)) * p.box_rows * 128;
+    const uint32_t staged_bytes = ((p.vq ? p.vslabs : 0) + (p.kq ? p.kslabs : 0)) * p.box_rows * 64;
+    uint32_t armed[2] = {0, 0}, armed_parity[2] = {0, 0};   // copies in flight, by ring
+    // this lane's group of rows of tile t: the cache row it starts at (-1: none)
+    auto row_of = [&](int32_t t) -> int64_t {
+      const int32_t pos = t * kKeys + lane * p.box_rows;
+      if (lane >= groups || pos >= w.len) return -1;
+      if (p.mode == kModeNorm) return (static_cast<int64_t>(w.b) * p.N + w.n) * p.cache_seq + pos;
       const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
       const int32_t in = pos - pg * p.block_size;
-      const int64_t page = __ldg(p.table + x.b * p.table_stride + pg);
+      const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
       if (page < 0 || page >= p.block_num) {
         if (p.err_count) atomicAdd(p.err_count, 1);
         return -1;
       }
-      return p.mode == kModePa ? (page * p.block_size + in) * p.N + x.n : (page * p.N + x.n) * p.block_size + in;
+      return p.mode == kModePa ? page * p.block_size + in : (page * p.N + w.n) * p.block_size + in;
     };
-    bool ok = !p.stall_loads;
-    int32_t issued = 0, completed = 0;
-    bool more = walk.next(p, w);
+    bool more = !p.stall_loads && walk.next(p, w);
     while (more && w.ta >= w.tb) more = walk.next(p, w);
-    int32_t t = more ? w.ta : 0;
-    int64_t row = more && ok ? row_of(w, t) : -1;
-    auto complete = [&]() {  // convert the oldest staged tile into its operand stage
-      const int st = completed % p.ns, sg = completed % p.nsg;
-      if (!bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((completed / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag)) return false;
-      uint8_t* stage = smem + p.off_ring + st * p.stage_bytes;
-      const uint8_t* from = smem + p.off_staging + sg * p.staging_bytes;
-      for (int i = tid; i < chunks; i += kProducers) {
-        const int key = (i * p.magic) >> 20, c = i - key * p.nc;
-        const bool is_v = c < p.ca;
-        const int cc = is_v ? c : c - p.ca;
-        const int32_t kind = is_v ? p.vq : p.kq;
-        uint8_t* slab0 = stage + (is_v ? 0 : p.vslabs * kSlab) + key * 128;
-        const uint4 u = *reinterpret_cast<const uint4*>(from + i * 16);
-        if (kind == kQuantNone) {
-          *reinterpret_cast<uint4*>(slab0 + (cc >> 3) * kSlab + (((cc & 7) ^ (key & 7)) << 4)) = u;
-        } else {
-          const uint2 a = codes_to_half(u.x, kind), b = codes_to_half(u.y, kind);
-          const uint2 d = codes_to_half(u.z, kind), e = codes_to_half(u.w, kind);
-          uint8_t* slab = slab0 + (cc >> 2) * kSlab;
-          const int c8 = (cc & 3) * 2;
-          *reinterpret_cast<uint4*>(slab + ((c8 ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(slab + (((c8 + 1) ^ (key & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&ms.kv_full[st]));
-      ++completed;
-      return true;
-    };
-    while (more && !p.stall_loads) {
-      int64_t* rows = ms.row_index[issued & 1];
-      if (tid < kKeys) {
-        rows[tid] = row;
-        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-        if (lane == 0) reinterpret_cast<uint32_t*>(&ms.valid[issued % kValidRing])[tid >> 5] = live;
-      }
-      // the next tile's rows: its table entry is on the way while this tile is issued
-      bool next_more = true;
+    int32_t t = more ? w.ta : 0, u = 0;
+    int64_t row = more ? row_of(t) : -1;
+    bool ok = true;
+    while (more) {
+      const int st = u % p.ns, sg = staged ? u % p.nsg : 0;
+      const int32_t head = p.mode == kModePa ? w.n : 0;
+      // which keys of the tile exist
+      const int32_t have = row >= 0 ? min(p.box_rows, w.len - t * kKeys - lane * p.box_rows) : 0;
+      uint64_t bits = have > 0 ? (~0ull >> (64 - have)) << (lane * p.box_rows) : 0;
+      bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
+      bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
+      // the next tile's rows: its table entry is on the way while this tile waits
+      const int64_t this_row = row;
       if (++t >= w.tb) {
-        next_more = walk.next(p, w);
-        while (next_more && w.ta >= w.tb) next_more = walk.next(p, w);
+        more = walk.next(p, w);
+        while (more && w.ta >= w.tb) more = walk.next(p, w);
         t = w.ta;
       }
-      const int64_t next_row = next_more ? row_of(w, t) : -1;
-      // a warp whose wait gave up leaves with the others, not them at the barrier
-      if (bar_or(2, ok ? 0u : 1u)) break;
-      uint32_t dst0;
-      const int st = issued % p.ns;
-      if (p.nsg == 0) {
-        if (!bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((issued / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag)) ok = false;
-        dst0 = s0 + p.off_ring + st * p.stage_bytes;
-      } else {
-        dst0 = s0 + p.off_staging + (issued % p.nsg) * p.staging_bytes;
+      if (more) row = row_of(t);
+      const uint32_t par_d = (u / p.ns) & 1, par_s = staged ? (u / p.nsg) & 1 : 0;
+      if (direct) ok = bounded_wait_warp(smem_u32(&ms.kv_empty[st]), par_d ^ 1u, p.wait_ns, abort_flag);
+      if (ok && staged) ok = bounded_wait_warp(smem_u32(&ms.code_empty[sg]), par_s ^ 1u, p.wait_ns, abort_flag);
+      if (!ok) break;
+      const uint32_t bar_d = smem_u32(&ms.kv_full[st]), bar_s = smem_u32(&ms.code_full[sg]);
+      const uint32_t live = __popc(__ballot_sync(0xffffffffu, this_row >= 0));
+      if (lane == 0) {
+        ms.valid[u % kValidRing] = bits;
+        if (direct) mbar_arrive_expect_tx(bar_d, live * direct_bytes);
+        if (staged) mbar_arrive_expect_tx(bar_s, live * staged_bytes);
       }
-      if (ok) {
-        for (int i = tid; i < chunks; i += kProducers) {
-          const int key = (i * p.magic) >> 20, c = i - key * p.nc;
-          const bool is_v = c < p.ca;
-          const int cc = is_v ? c : c - p.ca;
-          const int64_t r = rows[key];
-          const uint8_t* src = is_v ? p.v_cache : p.k_cache;
-          if (r >= 0) src += r * (is_v ? v_row : k_row) + cc * 16;
-          const uint32_t dst = p.nsg == 0 ? dst0 + ((is_v ? 0 : p.vslabs) + (cc >> 3)) * kSlab + key * 128 +
-                                                (((cc & 7) ^ (key & 7)) << 4)
-                                          : dst0 + i * 16;
-          cp_async16(dst, src, r >= 0 ? 16 : 0);
-        }
-        if (p.nsg == 0) {
-          cp_async_mbar_arrive(smem_u32(&ms.kv_full[st]));
-        } else {
-          cp_async_commit();
-          if (issued + 1 - completed == p.nsg) {
-            switch (p.nsg) {  // the oldest of the nsg tiles in flight has landed
-              case 1: cp_async_wait<0>(); break;
-              case 2: cp_async_wait<1>(); break;
-              case 3: cp_async_wait<2>(); break;
-              default: cp_async_wait<3>(); break;
-            }
-            ok = complete();
+      __syncwarp();
+      if (this_row >= 0) {
+        const int32_t at = static_cast<int32_t>(this_row);
+        const uint32_t operand = s0 + p.off_ring + st * p.stage_bytes + lane * p.box_rows * 128;
+        const uint32_t codes = s0 + p.off_staging + sg * p.staging_bytes + lane * p.box_rows * 64;
+        for (int c = 0; c < p.vslabs; ++c)
+          tma_load_3d(p.vq ? codes + c * kCodeSlab : operand + c * kSlab, &p.tv, p.vq ? bar_s : bar_d, 64 * c, head, at);
+        const uint32_t k_codes = codes + (p.vq ? p.vslabs : 0) * kCodeSlab;
+        for (int c = 0; c < p.kslabs; ++c)
+          tma_load_3d(p.kq ? k_codes + c * kCodeSlab : operand + (p.vslabs + c) * kSlab, &p.tk, p.kq ? bar_s : bar_d,
+                      64 * c, head, at);
+      }
+      if (direct) {
+        armed[0] |= 1u << st;
+        armed_parity[0] = (armed_parity[0] & ~(1u << st)) | (par_d << st);
+      }
+      if (staged) {
+        armed[1] |= 1u << sg;
+        armed_parity[1] = (armed_parity[1] & ~(1u << sg)) | (par_s << sg);
+      }
+      ++u;
+    }
+    if (lane == 0 && (!ok || *abort_flag))  // let every copy in flight land before the block leaves
+      for (int i = 0; i < kMaxStages; ++i) {
+        // (a stage that converters share may stay open for them: then nothing is in flight after the limit)
+        if (armed[0] & (1u << i)) bounded_drain(smem_u32(&ms.kv_full[i]), (armed_parity[0] >> i) & 1u, kDrainNs);
+        if (armed[1] & (1u << i)) bounded_drain(smem_u32(&ms.code_full[i]), (armed_parity[1] >> i) & 1u, kDrainNs);
+      }
+    __syncwarp();
+  } else if (warp >= 4 && warp < kMmaWarp) {
+    // ------------------------------------------------------------ codes to fp16 operands
+    const int tid = threadIdx.x - kSoftmax;
+    const int sl0 = p.vq ? 0 : p.vslabs, sl1 = p.vslabs + (p.kq ? p.kslabs : 0);  // the slabs that hold codes
+    bool ok = p.nsg != 0 && !p.stall_loads;
+    int32_t u = 0;
+    while (ok && walk.next(p, w)) {
+      for (int32_t t = w.ta; ok && t < w.tb; ++t, ++u) {
+        const int st = u % p.ns, sg = u % p.nsg;
+        ok = bounded_wait_warp(smem_u32(&ms.code_full[sg]), (u / p.nsg) & 1, p.wait_ns, abort_flag) &&
+             bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((u / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag);
+        if (!ok) break;
+        uint8_t* stage = smem + p.off_ring + st * p.stage_bytes;
+        const uint8_t* from = smem + p.off_staging + sg * p.staging_bytes;
+        const uint64_t valid = ms.valid[u % kValidRing];
+        // 64 keys x 4 chunks of 16 codes per slab, two rounds of 128 threads; two slabs' loads
+        // are in flight together
+        for (int sl = sl0; sl < sl1; sl += 2) {
+          uint4 x[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int key = (tid >> 2) + 32 * (h & 1), c = tid & 3;
+            x[h] = make_uint4(0, 0, 0, 0);
+            if (sl + (h >> 1) < sl1 && ((valid >> key) & 1))
+              x[h] = *reinterpret_cast<const uint4*>(from + (sl - sl0 + (h >> 1)) * kCodeSlab + key * 64 + c * 16);
+          }
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            if (sl + (h >> 1) >= sl1) break;
+            const int key = (tid >> 2) + 32 * (h & 1), c = tid & 3;
+            const int32_t kind = sl + (h >> 1) < p.vslabs ? p.vq : p.kq;
+            const uint2 a = codes_to_half(x[h].x, kind), b = codes_to_half(x[h].y, kind);
+            const uint2 d = codes_to_half(x[h].z, kind), e = codes_to_half(x[h].w, kind);
+            uint8_t* dst = stage + (sl + (h >> 1)) * kSlab + key * 128;
+            *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
           }
         }
-        ++issued;
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&ms.kv_full[st]));
+        mbar_arrive(smem_u32(&ms.code_empty[sg]));
       }
-      more = next_more;
-      row = next_row;
     }
-    if (p.nsg != 0) {
-      cp_async_commit();
-      cp_async_wait<0>();
-      while (ok && completed < issued) ok = complete();
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      const bool bf = !p.f16;
-      const uint32_t id_s_v = idesc_f16(bf && p.vq == 0, false, false, 128, kKeys);   // V1: the latent part of the key
-      const uint32_t id_s_k = idesc_f16(bf && p.kq == 0, false, false, 128, kKeys);
-      const uint32_t id_o = idesc_f16(bf && p.vq == 0, true, false, 128, static_cast<uint32_t>(NR));
-      const uint64_t q_desc = sdesc_kmajor_sw128(s0);
-      const uint64_t k_desc = sdesc_kmajor_sw128(s0 + p.off_ring + p.kslab0 * kSlab);
-      const uint64_t v_desc = sdesc_mnmajor_sw128(s0 + p.off_ring, kSlab);
-      const uint64_t p_desc = sdesc_kmajor_sw128(s0 + p.off_p);
-      const int v_chunks = (p.Dv + 127) / 128;
-      const int q_step = NR * 128 >> 4;
-      int32_t jt = 0, pieces = 0;
-      bool ok = true;
-      while (ok && walk.next(p, w)) {
-        const int32_t n = w.tb - w.ta;
-        if (n <= 0) continue;
-        if (!bounded_wait_one(smem_u32(&ms.q_ready), pieces & 1, p.wait_ns, abort_flag)) break;
-        ++pieces;
-        int32_t qk = 0, pv = 0;
-        uint64_t t_start = 0;
-        uint32_t spins = 0;
-        while (pv < n) {
-          if (qk < n && qk - pv < 2) {
-            const int32_t u = jt + qk;
-            const int st = u % p.ns;
-            if (mbar_test_wait(smem_u32(&ms.kv_full[st]), (u / p.ns) & 1)) {
-              // the tile was written through the generic proxy by the producers
-              fence_proxy_async_smem();
-              tc_fence_after();
-              const uint64_t kb = k_desc + static_cast<uint64_t>(st * (p.stage_bytes >> 4));
-              const uint32_t d = tmem + (u & 1) * kKeys;
-              for (int sl = 0; sl < p.qslabs; ++sl) {
-                const uint32_t id = p.v1 && sl < p.vslabs ? id_s_v : id_s_k;
-                const int steps = min(4, (p.Dk - sl * 64) / 16);
-                for (int k = 0; k < steps; ++k)
-                  mma_f16_ss(d, q_desc + sl * q_step + 2 * k, kb + sl * (kSlab >> 4) + 2 * k, id, sl + k > 0);
-              }
-              tc_commit(smem_u32(&ms.s_full[u & 1]));
-              ++qk;
-              spins = 0;
-              continue;
-            }
+    const bool bf = !p.f16;
+    const uint32_t id_s_v = idesc_f16(bf && p.vq == 0, false, false, 128, kKeys);   // V1: the latent part of the key
+    const uint32_t id_s_k = idesc_f16(bf && p.kq == 0, false, false, 128, kKeys);
+    const uint32_t id_o = idesc_f16(bf && p.vq == 0, true, false, 128, static_cast<uint32_t>(NR));
+    const uint64_t q_desc = sdesc_kmajor_sw128(s0);
+    const uint64_t k_desc = sdesc_kmajor_sw128(s0 + p.off_ring + p.kslab0 * kSlab);
+    const uint64_t v_desc = sdesc_mnmajor_sw128(s0 + p.off_ring, kSlab);
+    const uint64_t p_desc = sdesc_kmajor_sw128(s0 + p.off_p);
+    const int v_chunks = (p.Dv + 127) / 128;
+    const int q_step = NR * 128 >> 4;
+    int32_t jt = 0, pieces = 0;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      const int32_t n = w.tb - w.ta;
+      if (n <= 0) continue;
+      if (!bounded_wait_warp(smem_u32(&ms.q_ready), pieces & 1, p.wait_ns, abort_flag)) break;
+      ++pieces;
+      int32_t qk = 0, pv = 0;
+      uint64_t t_start = 0;
+      uint32_t spins = 0;
+      while (pv < n) {  // whichever product is ready next; the whole warp goes the same way
+        const int32_t u = jt + qk, v = jt + pv;
+        const int st_s = u % p.ns, st_o = v % p.ns;
+        const bool go_s = qk < n && qk - pv < 2 && mbar_test_wait(smem_u32(&ms.kv_full[st_s]), (u / p.ns) & 1);
+        if (__all_sync(0xffffffffu, go_s)) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t kb = k_desc + static_cast<uint64_t>(st_s * (p.stage_bytes >> 4));
+            const uint32_t d = tmem + (u & 1) * kKeys;
+            for (int sl = 0; sl < p.qslabs; ++sl)
+              mma4_f16_ss<2, 2>(d, q_desc + sl * q_step, kb + sl * (kSlab >> 4), p.v1 && sl < p.vslabs ? id_s_v : id_s_k,
+                                sl > 0, min(4, (p.Dk - sl * 64) / 16));
+            tc_commit(smem_u32(&ms.s_full[u & 1]));
           }
-          if (pv < qk && mbar_test_wait(smem_u32(&ms.p_ready), (jt + pv) & 1)) {
-            tc_fence_after();
-            const int st = (jt + pv) % p.ns;
-            const uint64_t va = v_desc + static_cast<uint64_t>(st * (p.stage_bytes >> 4));
+          __syncwarp();
+          ++qk;
+          spins = 0;
+          continue;
+        }
+        const bool go_o = pv < qk && mbar_test_wait(smem_u32(&ms.p_ready), v & 1);
+        if (__all_sync(0xffffffffu, go_o)) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t va = v_desc + static_cast<uint64_t>(st_o * (p.stage_bytes >> 4));
             for (int c = 0; c < v_chunks; ++c)
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                mma_f16_ss(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4) + 128 * k, p_desc + 2 * k, id_o,
-                           pv > 0 || k > 0);
-            tc_commit(smem_u32(&ms.kv_empty[st]));
+              mma4_f16_ss<128, 2>(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4), p_desc, id_o, pv > 0, 4);
+            tc_commit(smem_u32(&ms.kv_empty[st_o]));
             tc_commit(smem_u32(&ms.pv_done));
-            ++pv;
-            spins = 0;
-            continue;
           }
-          if ((++spins & 31u) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (spins == 32u) t_start = now;
-            else if (*abort_flag || now - t_start > p.wait_ns) {
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
+          __syncwarp();
+          ++pv;
+          spins = 0;
+          continue;
+        }
+        if ((++spins & 31u) == 0) {
+          const uint64_t now = globaltimer_ns();
+          int give_up = 0;
+          if (spins == 32u) t_start = now;
+          else give_up = *abort_flag || now - t_start > p.wait_ns;
+          if (__any_sync(0xffffffffu, give_up)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
           }
         }
-        jt += n;
       }
-      tc_commit(smem_u32(&ms.drain));  // every product must finish before TMEM is released
-      bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
+      jt += n;
     }
+    if (elect_one()) tc_commit(smem_u32(&ms.drain));  // every product must finish before TMEM is released
+    __syncwarp();
+    bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, rescaling, epilogue
@@ -495,63 +617,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
     const int v_chunks = (p.Dv + 127) / 128;
     const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
-    const bool p_f16 = p.f16 || p.vq != 0;           // P has the type of V's operand
-    const int tpr = kSoftmax / NR;                   // threads that prepare one row of Q
     int32_t jt = 0, piece = 0;
     bool ok = true;
     for (; ok && walk.next(p, w); ++piece) {
       const int32_t n = w.tb - w.ta;
-      const int64_t first_row = static_cast<int64_t>(w.rt) * NR;
+      const uint32_t first_row = w.rt * NR;
       bar_128(1);                                    // the previous piece's row arrays are done with
       if (tid < NR) {
-        const int64_t rr = first_row + tid;
-        const int64_t tok = rr / p.g;
-        out_row[tid] =
-            tid < w.rows ? static_cast<int32_t>((w.q_start + tok) * p.heads + static_cast<int64_t>(w.n) * p.g + (rr - tok * p.g)) : -1;
+        const uint32_t rr = first_row + tid, tok = rr / static_cast<uint32_t>(p.g);
+        out_row[tid] = tid < w.rows ? static_cast<int32_t>((w.q_start + tok) * p.heads + w.n * p.g + (rr - tok * p.g)) : -1;
       }
       bar_128(1);
-      {  // Q rows into the swizzled operand, 8 channels at a time
-        const int r = tid / tpr, sub = tid - r * tpr;
-        const int64_t at = out_row[r];
-        const uint16_t* src = p.q + (at < 0 ? 0 : at) * p.Dk;
-        const int nck = p.Dk / 8;
-        float up = 1.f, shift = 0.f;
-        if (k_quant) {
-          float amax = 0.f;
-          if (at >= 0)
-            for (int c = sub; c < nck; c += tpr)
-              for (int e = 0; e < 8; ++e) {
-                const float2 so = key_quant(p, w.n, c * 8 + e);
-                const float x = load_half(src + c * 8 + e, p.f16) / so.x;
-                amax = fmaxf(amax, fabsf(x));
-                shift = fmaf(x, so.y, shift);
-              }
-          for (int o = 1; o < tpr; o <<= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            shift += __shfl_xor_sync(0xffffffffu, shift, o);
-          }
-          up = amax > 0.f ? exp2_int(-(scale_exponent(amax) + 5)) : 1.f;  // amax * up in [2^9, 2^10)
-        }
-        if (sub == 0) {
-          row_scale[r] = p.sl2 / up;
-          row_const[r] = -shift * p.scale;
-        }
-        if (at >= 0) {
-          for (int c = sub; c < nck; c += tpr) {
-            uint4 u = *reinterpret_cast<const uint4*>(src + c * 8);
-            if (k_quant) {
-              const bool quant = (p.v1 && c * 8 < p.Dv) ? p.vq != 0 : p.kq != 0;
-              uint16_t h[8];
-              for (int e = 0; e < 8; ++e) {
-                const float2 so = key_quant(p, w.n, c * 8 + e);
-                h[e] = to_half(load_half(src + c * 8 + e, p.f16) / so.x * up, quant || p.f16);
-              }
-              u = make_uint4(pair16(h[0], h[1]), pair16(h[2], h[3]), pair16(h[4], h[5]), pair16(h[6], h[7]));
-            }
-            *reinterpret_cast<uint4*>(smem + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
-          }
-        }
-      }
+      load_q<F16>(p, w.n, w.rows, smem, out_row, row_scale, row_const, k_quant, warp, lane);
       fence_proxy_async_smem();
       bar_128(1);
       if (n > 0) mbar_arrive(smem_u32(&ms.q_ready));
@@ -561,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       const float lazy = kLazy / sl2;
       int32_t seen = w.len;
       if (p.causal && live) {
-        const int32_t tok = static_cast<int32_t>((first_row + tid) / p.g);
+        const int32_t tok = static_cast<int32_t>((first_row + tid) / static_cast<uint32_t>(p.g));
         seen = min(w.len, max(0, w.len - w.Lq + tok + 1));
       }
       float m = neg_inf(), l = 0.f;
@@ -629,24 +706,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (ok && rows_here) {
           const float neg = m == neg_inf() ? 0.f : -m * sl2;
           const float2 sc = make_float2(sl2, sl2), ng = make_float2(neg, neg);
-          float2 acc = make_float2(0.f, 0.f);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint8_t* prow = smem + p.off_p + tid * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t h[4];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[16];
+            exp_batch<!P16>(s + 32 * h, sc, ng, acc, x);
+            if (live)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 8 * c + 2 * e;
-              float2 x = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc, ng);
-              x.x = ex2(x.x), x.y = ex2(x.y);
-              acc = __fadd2_rn(acc, x);
-              h[e] = p_f16 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
-            }
-            if (live) *reinterpret_cast<uint4*>(prow + ((c ^ (tid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(prow + (((4 * h + c) ^ (tid & 7)) << 4)) =
+                    make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
           }
-          l += acc.x + acc.y;
-          fence_proxy_async_smem();
+          const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l += sum.x + sum.y;
         }
+        if (ok && p.vq == 0) {
+          const uint64_t valid = ms.valid[u % kValidRing];
+          if (valid != ~0ull) {  // zero the value rows that do not exist, two threads per row
+            const int key = tid >> 1;
+            if (!((valid >> key) & 1)) {
+              uint8_t* vrow = smem + p.off_ring + (u % p.ns) * p.stage_bytes + key * 128 + (tid & 1) * 64;
+              for (int c = 0; c < p.vslabs; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4*>(vrow + c * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(smem_u32(&ms.p_ready));
       }
@@ -700,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
               if (w.whole()) {
                 const float inv = inv_sum[r];
                 const float y = inv > 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
-                p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half(y, p.f16);
+                p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
               } else if (n > 0) {
                 p.parts[(slot * NR + r) * p.Dv + ch] = __uint_as_float(o[e]);
               }
@@ -718,35 +806,65 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the items that a cut runs through: block (c, r) row r of the item
-// whose first cut lies before block c's run.
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ Params p) {
+// Joins the pieces of the items that a cut runs through: the blocks (c, *) take the rows of
+// the item whose first cut lies before block c's run.  The pieces' weights come first, one
+// thread each; then four groups of 128 threads sum every fourth piece, and the groups' sums
+// are added in a fixed order.
+constexpr int kJoinThreads = 512, kJoinGroups = 4;
+template <bool F16>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Params p) {
+  __shared__ float weight[kMaxBlocks], red[2][kJoinThreads / 32];
+  __shared__ float sum[kJoinGroups][512];
   const int32_t* mt = p.meta + 8 * blockIdx.x;
-  const int r = blockIdx.y;
-  if (mt[0] == 0 || r >= mt[3]) return;
-  const int32_t first = mt[1], last = mt[2], NR = p.NR;
-  const int64_t rr = static_cast<int64_t>(mt[6]) * NR + r, tok = rr / p.g;
-  const int64_t row = (mt[4] + tok) * p.heads + static_cast<int64_t>(mt[5]) * p.g + (rr - tok * p.g);
+  if (mt[0] == 0) return;
+  const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3], NR = p.NR;
+  const int tid = threadIdx.x, group = tid / 128;
   // the item's piece is the last of its first block, the first of the others
-  auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == first ? 1 : 0); };
-  float m = neg_inf();
-  for (int32_t c = first; c <= last; ++c) m = fmaxf(m, p.stats[slot(c) * NR + r].x);
-  float l = 0.f, k0 = 0.f;
-  for (int32_t c = first; c <= last; ++c) {
-    const float4 s = p.stats[slot(c) * NR + r];
-    if (s.y > 0.f) l += s.y * ex2(s.x - m);
-    k0 = s.z;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
-  for (int ch = threadIdx.x; ch < p.Dv; ch += blockDim.x) {
-    float acc = 0.f;
-    for (int32_t c = first; c <= last; ++c) {
-      const float4 s = p.stats[slot(c) * NR + r];
-      if (s.y > 0.f) acc += p.parts[(slot(c) * NR + r) * p.Dv + ch] * ex2(s.x - m);
+  auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int64_t rr = static_cast<int64_t>(mt[6]) * NR + r, tok = rr / p.g;
+    const int64_t row = (mt[4] + tok) * p.heads + static_cast<int64_t>(mt[5]) * p.g + (rr - tok * p.g);
+    const float4 st = tid < n ? p.stats[slot(tid) * NR + r] : make_float4(neg_inf(), 0.f, 0.f, 0.f);
+    float m = st.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) red[0][tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[0][i]);
+    const float wt = st.y > 0.f ? ex2(st.x - m) : 0.f;
+    if (tid < n) weight[tid] = wt;
+    float l = st.y * wt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((tid & 31) == 0) red[1][tid >> 5] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
+    const int ch = (tid & 127) * 4;
+    if (ch < p.Dv) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int i = group; i < n; i += kJoinGroups) {
+        if (weight[i] == 0.f) continue;  // a piece that saw nothing stored no accumulator
+        const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + r) * p.Dv + ch);
+        acc.x = fmaf(x.x, weight[i], acc.x);
+        acc.y = fmaf(x.y, weight[i], acc.y);
+        acc.z = fmaf(x.z, weight[i], acc.z);
+        acc.w = fmaf(x.w, weight[i], acc.w);
+      }
+      *reinterpret_cast<float4*>(&sum[group][ch]) = acc;
     }
-    const float2 so = value_quant(p, mt[5], ch);
-    p.out[row * p.Dv + ch] = to_half(l > 0.f ? (acc * inv - so.y) / so.x : 0.f, p.f16);
+    __syncthreads();
+    if (tid == 0 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + st.z : neg_inf();
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    for (int c = tid; c < p.Dv; c += kJoinThreads) {
+      const float acc = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
+      const float2 so = value_quant(p, mt[5], c);
+      p.out[row * p.Dv + c] = to_half<F16>(l > 0.f ? (acc * inv - so.y) / so.x : 0.f);
+    }
+    __syncthreads();
   }
 }
 
@@ -766,9 +884,8 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   pl->qslabs = v1 ? pl->vslabs + pl->kslabs : pl->kslabs;
   pl->kslab0 = v1 ? 0 : pl->vslabs;
   pl->stage = (pl->vslabs + pl->kslabs) * kSlab;
-  const int rows_bytes = (v1 ? L.R : L.Dkv) * (L.kq ? 1 : 2) + L.Dv * (L.vq ? 1 : 2);
   const bool staged = L.kq != 0 || L.vq != 0;
-  pl->staging = staged ? kKeys * rows_bytes : 0;
+  pl->staging = ((L.vq ? pl->vslabs : 0) + (L.kq ? pl->kslabs : 0)) * kCodeSlab;
   const int64_t mean = (L.total_q + L.B - 1) / L.B * g;
   int nr = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
   const int chunks = (L.Dv + 127) / 128;
@@ -783,7 +900,9 @@ bool plan(const PagedLaunch& L, Plan* pl) {
       if (pl->ns < 2) continue;
     } else {
       if (left < pl->stage + pl->staging) continue;
-      pl->ns = left >= 2 * pl->stage + 2 * pl->staging ? 2 : 1;
+      // as many operand stages as leave two staging ones (a tile on its way, one being converted)
+      pl->ns = std::max(1, std::min(4, (left - 2 * pl->staging) / pl->stage));
+      if (pl->ns == 1 && left >= 2 * pl->stage + pl->staging) pl->ns = 2;
       pl->nsg = std::min(4, (left - pl->ns * pl->stage) / pl->staging);
     }
     break;
@@ -802,8 +921,46 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   return true;
 }
 
+// A cache's rows as a 3-D map: PA (channels, heads, slots), the others (channels, 1, rows);
+// boxes of 64 channels x box_rows rows, swizzled like an MMA operand unless they are codes
+bool make_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32_t width, int32_t quant, int32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const uint64_t row = static_cast<uint64_t>(width) * (quant ? 1 : 2);
+  const bool pa = L.mode == kModePa;
+  const uint64_t slots = L.mode == kModeNorm ? static_cast<uint64_t>(L.B) * L.cache_seq
+                                             : static_cast<uint64_t>(L.block_num) * L.block_size;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), pa ? static_cast<cuuint64_t>(L.N) : 1, pa ? slots : slots * L.N};
+  cuuint64_t strides[2] = {row, pa ? row * L.N : row};
+  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
 size_t stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
+
+template <bool F16, bool P16>
+cudaError_t launch(const Params& p, int blocks, int smem, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto kernel = paged_attention_kernel<F16, P16>;
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  kernel<<<blocks, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || blocks == 1) return e;
+  paged_join_kernel<F16><<<dim3(blocks, std::min(p.NR, 16)), kJoinThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -852,6 +1009,7 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.heads = L.heads;
   p.g = L.heads / static_cast<int32_t>(L.N);
   p.NR = pl.NR;
+  p.nr_shift = pl.NR == 16 ? 4 : pl.NR == 32 ? 5 : pl.NR == 64 ? 6 : 7;
   p.block_size = static_cast<int32_t>(L.block_size);
   p.bs_shift = -1;
   for (int s = 0; s < 31; ++s)
@@ -867,9 +1025,11 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.k_scalar = L.k_scalar;
   p.v_scalar = L.v_scalar;
   p.causal = L.causal;
-  p.ca = L.Dv * (L.vq ? 1 : 2) / 16;
-  p.nc = p.ca + p.Dko * (L.kq ? 1 : 2) / 16;
-  p.magic = ((1 << 20) + p.nc - 1) / p.nc;  // exact for idx < 64 nc: the error idx * nc / 2^20 stays below 1 / nc
+  p.box_rows = L.mode == kModeNorm || L.block_size % 64 == 0 ? 64 : L.block_size % 32 == 0 ? 32 : 16;
+  if (!make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
+    *why = "cuTensorMapEncodeTiled failed or is unavailable";
+    return cudaErrorInvalidValue;
+  }
   p.vslabs = pl.vslabs;
   p.kslabs = pl.kslabs;
   p.qslabs = pl.qslabs;
@@ -887,20 +1047,8 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);
   p.stall_loads = L.stall_loads;
 
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(ready.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) ready.fetch_or(1ull << dev);
-  }
-  paged_attention_kernel<<<pl.G, kThreads, pl.smem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || pl.G == 1) return e;
-  paged_join_kernel<<<dim3(pl.G, pl.NR), 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (L.f16) return launch<true, true>(p, pl.G, pl.smem, stream);
+  return L.vq ? launch<false, true>(p, pl.G, pl.smem, stream) : launch<false, false>(p, pl.G, pl.smem, stream);
 }
 
 }  // namespace ra
