@@ -397,6 +397,8 @@ ra_status check_paged(const kv_rms_norm_rope_cache_params* c, const paged_attent
   } else if (p->block_table_stride < 1 || p->block_table_stride > (1LL << 31)) {
     return fail(RA_ERR_INVALID_ARG, "block_table_stride must be in [1, 2^31]");
   }
+  if ((c->cache_mode == RA_CACHE_NORM ? p->B * c->cache_seq_len : c->block_num * c->block_size) * c->N > 0x7fffffffLL)
+    return fail(RA_ERR_UNSUPPORTED, "paged_attention addresses cache rows with 31 bits (slots * N)");
   if (c->variant == 1 ? (c->Dv > 512 || c->Dv % 64 != 0 || c->rope_size > 64 || c->rope_size % 16 != 0)
                       : (c->Dkv > 256 || c->Dkv % 16 != 0 || c->Dv > 256 || c->Dv % 16 != 0))
     return fail(RA_ERR_UNSUPPORTED,

@@ -49,7 +49,10 @@ namespace {
 constexpr int kKeys = 64;                 // keys per tile: one 128-byte swizzled row of P
 constexpr int kSlab = kKeys * 128;        // 64 keys x 64 channels of 16 bits
 constexpr int kCodeSlab = kKeys * 64;      // the same of codes
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;              // three warpgroups
+// Registers per thread: launched with 168 each, then moved to the softmax:
+// 232 + 184 + 88 = 3 x 168
+constexpr int kRegsSoftmax = 232, kRegsConvert = 184, kRegsRest = 88;
 constexpr int kSoftmax = 128, kConverters = 128;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kValidRing = 16;            // > tiles between the loads and the softmax
@@ -63,6 +66,7 @@ constexpr int kSCols = 2 * kKeys;         // TMEM: two S buffers, then O^T
 
 struct Params {
   CUtensorMap tk, tv;           // the caches' rows: 64 channels x 1 x box_rows boxes
+  CUtensorMap tq;               // (channels, heads, tokens): boxes of 64 x hb x tb, a row tile
   const uint16_t* q;
   uint16_t* out;
   float* lse;
@@ -76,10 +80,11 @@ struct Params {
   int32_t* meta;                // [G][8]
   int64_t table_stride, cap;    // cap: positions that a sequence can have
   int64_t block_num, cache_seq;
-  int32_t B, total_q, N, heads, g, NR, nr_shift, block_size, bs_shift;
+  int32_t B, total_q, N, heads, g, NR, block_size, bs_shift;
   int32_t Dk, Dv, Dko;          // key width, value width, width of a k_cache row
   int32_t v1, mode, f16, kq, vq, k_scalar, v_scalar, causal;
-  int32_t box_rows;
+  int32_t box_rows, box_shift;
+  int32_t hb, tb, hblocks;      // a row tile: tb tokens x hb heads; tiles that a token's heads take
   int32_t vslabs, kslabs, qslabs, kslab0;
   int32_t ns, nsg;              // operand stages, staging stages (0: 16-bit caches)
   int32_t stage_bytes, staging_bytes;
@@ -92,7 +97,7 @@ struct Params {
 struct Misc {                   // behind the tiles in shared memory
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t code_full[kMaxStages], code_empty[kMaxStages];
-  uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
+  uint64_t s_full[2], p_ready, pv_done, q_full, q_ready, q_empty, drain;
   uint64_t valid[kValidRing];
   int64_t scan[kThreads / 32];
   int64_t start_off;
@@ -117,16 +122,32 @@ __device__ __forceinline__ void q_span(const Params& p, int32_t b, int32_t& star
   len = hi - lo;
 }
 __device__ __forceinline__ int32_t tiles_of(int32_t len) { return max(1, (len + kKeys - 1) / kKeys); }
+// row tiles of lq tokens and one kv head (lq * heads < 2^31)
+__device__ __forceinline__ int32_t row_tiles_of(const Params& p, int32_t lq) {
+  return p.hblocks > 1 ? lq * p.hblocks : static_cast<int32_t>(static_cast<uint32_t>(lq + p.tb - 1) / static_cast<uint32_t>(p.tb));
+}
 __device__ __forceinline__ int64_t seq_work(const Params& p, int32_t b) {
   int32_t s, lq;
   q_span(p, b, s, lq);
-  const int64_t row_tiles = (static_cast<uint32_t>(lq * p.g) + p.NR - 1) >> p.nr_shift;  // lq * g < 2^31
-  return row_tiles * p.N * tiles_of(seq_len_of(p, b));
+  return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * tiles_of(seq_len_of(p, b));
 }
+
+// A position in a ring of stages: the stage, and the parity of its barriers' phase.  (A
+// division by the number of stages costs a lone warp 150 cycles or more.)
+struct Ring {
+  int32_t stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int32_t stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // One block's share of an item: key tiles [ta, tb) of row tile rt of (b, n).
 struct Piece {
-  int32_t b, n, rt, rows, q_start, Lq, len;
+  int32_t b, n, tok, head, rows, q_start, Lq, len;  // the tile's first token (of its sequence) and head
   int32_t t0, take, T;          // nominal tiles: [t0, t0 + take) of T
   int32_t ta, tb;               // those that any of its rows sees
   __device__ bool whole() const { return take == T; }
@@ -140,8 +161,7 @@ struct Walker {
       int32_t qs, lq;
       q_span(p, b, qs, lq);
       const int32_t len = seq_len_of(p, b), T = tiles_of(len);
-      const int32_t rows = lq * p.g;
-      const int32_t rts = (static_cast<uint32_t>(rows) + p.NR - 1) >> p.nr_shift;
+      const int32_t rts = row_tiles_of(p, lq);
       const int64_t work = static_cast<int64_t>(rts) * p.N * T;
       if (off >= work) {
         off -= work;
@@ -155,12 +175,21 @@ struct Walker {
       w.T = T;
       w.take = static_cast<int32_t>(min(static_cast<int64_t>(T - w.t0), rem));
       w.n = static_cast<int32_t>(static_cast<uint32_t>(item) / static_cast<uint32_t>(rts));  // item < rts * N <= 2^31
-      w.rt = static_cast<int32_t>(item - static_cast<int64_t>(w.n) * rts);
-      w.rows = min(p.NR, rows - w.rt * p.NR);
+      const int32_t rt = static_cast<int32_t>(item - static_cast<int64_t>(w.n) * rts);
+      if (p.hblocks > 1) {
+        w.tok = rt / p.hblocks;
+        const int32_t h = (rt - w.tok * p.hblocks) * p.hb;
+        w.head = w.n * p.g + h;
+        w.rows = min(p.hb, p.g - h);
+      } else {
+        w.tok = rt * p.tb;
+        w.head = w.n * p.g;
+        w.rows = min(p.tb, lq - w.tok) * p.g;
+      }
       w.q_start = qs;
       w.Lq = lq;
       w.len = len;
-      const int32_t last = static_cast<int32_t>(static_cast<uint32_t>(w.rt * p.NR + w.rows - 1) / static_cast<uint32_t>(p.g));
+      const int32_t last = p.hblocks > 1 ? w.tok : min(w.tok + p.tb, lq) - 1;
       const int32_t seen = p.causal ? min(len, max(0, len - lq + last + 1)) : len;
       const int32_t vt = (seen + kKeys - 1) / kKeys;
       w.ta = min(w.t0, vt);
@@ -244,95 +273,90 @@ __device__ __forceinline__ float2 value_quant(const Params& p, int32_t n, int32_
   return channel_quant(p.v_scale, p.v_offset, p.v1 ? c : n * p.Dv + c, p.v_scalar);
 }
 
-// The piece's rows of q in the swizzled operand; where the key is codes, over the key's
+// Where the key is codes: the piece's rows of q, in their swizzled operand, over the key's
 // scales and behind a power of two that keeps the row's elements below 2^15: 2^29 above
 // fp16's subnormals, so that a bound on the largest element (the largest |q| times the
 // largest 1 / s) serves as well as the element itself.  row_scale gets the softmax scale
 // that undoes the power, row_const the lse's share of the offsets.  A warp takes a row, a
-// lane the 8-channel chunks lane, lane + 32, lane + 64.
+// lane the 8-channel chunks lane, lane + 32, lane + 64.  Rolled loops: at the start of a
+// block each line of code comes from L2, at several hundred cycles.
 template <bool F16>
-__device__ __forceinline__ void load_q(const Params& p, int32_t n, int32_t rows, uint8_t* smem, const int32_t* out_row,
-                                       float* row_scale, float* row_const, bool scaled, int warp, int lane) {
+__device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows, uint8_t* smem, float* row_scale,
+                                        float* row_const, int warp, int lane, uint32_t q_full, uint32_t parity,
+                                        volatile int* abort_flag) {
   const int nck = p.Dk / 8;
   float inv_s[3][8], top = 0.f;
-  if (scaled) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = (lane + 32 * i) * 8;
+    key_scales(p, n, c, inv_s[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      inv_s[i][e] = c < p.Dk ? rcp(inv_s[i][e]) : 0.f;
+      top = fmaxf(top, fabsf(inv_s[i][e]));
+    }
+  }
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: bits order like values
+  if (!bounded_wait_warp(q_full, parity, p.wait_ns, abort_flag)) return false;
+#pragma unroll 1
+  for (int r = warp; r < rows; r += 4) {
+    uint8_t* row = smem + r * 128;
+    uint4 x[3];
+    uint32_t big = 0;  // |q| as bits orders like the value in either type
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const int c = (lane + 32 * i) * 8;
-      float s[8];
-      key_scales(p, n, c, s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        inv_s[i][e] = c < p.Dk ? rcp(s[e]) : 0.f;
-        top = fmaxf(top, fabsf(inv_s[i][e]));
-      }
+      const int c = lane + 32 * i;
+      x[i] = c < nck ? *reinterpret_cast<const uint4*>(row + (c >> 3) * p.NR * 128 + (((c & 7) ^ (r & 7)) << 4))
+                     : make_uint4(0, 0, 0, 0);
+      big = __vmaxu2(__vmaxu2(big, x[i].x & 0x7FFF7FFFu), x[i].y & 0x7FFF7FFFu);
+      big = __vmaxu2(__vmaxu2(big, x[i].z & 0x7FFF7FFFu), x[i].w & 0x7FFF7FFFu);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  constexpr int kBatch = 4;  // rows whose loads are in flight together
-#pragma unroll 1
-  for (int r0 = warp; r0 < rows; r0 += 4 * kBatch) {
-    uint4 x[kBatch][3];
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int r = r0 + 4 * t;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int c = lane + 32 * i;
-        x[t][i] = r < rows && c < nck
-                      ? __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(out_row[r]) * p.Dk + c * 8))
-                      : make_uint4(0, 0, 0, 0);
-      }
+    big = __reduce_max_sync(0xffffffffu, max(big & 0xFFFFu, big >> 16));
+    // |q| < 2^(e + 15), 1 / s < 2^(f + 15) with e, f the exponents below: |q| / s * up < 2^15
+    const int k = max(-100, min(100, -(scale_exponent(half_to_float<F16>(big)) + scale_exponent(top) + 15)));
+    const float up = exp2_int(k);
+    if (lane == 0) {
+      row_scale[r] = p.sl2 * exp2_int(-k);
+      row_const[r] = 0.f;
     }
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int r = r0 + 4 * t;
-      if (r >= rows) break;
-      float up = 1.f;
-      if (scaled) {
-        uint32_t big = 0;  // |q| as bits orders like the value in either type
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          big = __vmaxu2(__vmaxu2(big, x[t][i].x & 0x7FFF7FFFu), x[t][i].y & 0x7FFF7FFFu);
-          big = __vmaxu2(__vmaxu2(big, x[t][i].z & 0x7FFF7FFFu), x[t][i].w & 0x7FFF7FFFu);
-        }
-        big = __reduce_max_sync(0xffffffffu, max(big & 0xFFFFu, big >> 16));
-        const float amax = half_to_float<F16>(big);
-        // amax < 2^(e + 15), top < 2^(f + 15): amax * top * up < 2^15
-        up = exp2_int(max(-100, min(100, -(scale_exponent(amax) + scale_exponent(top) + 15))));
-      }
-      if (lane == 0) {
-        row_scale[r] = p.sl2 / up;
-        row_const[r] = 0.f;
-      }
+    if (p.lse) {
       float shift = 0.f;
+#pragma unroll 1
+      for (int c = lane; c < nck; c += 32) {
+        const uint4 z = *reinterpret_cast<const uint4*>(row + (c >> 3) * p.NR * 128 + (((c & 7) ^ (r & 7)) << 4));
+        const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+        float sc[8];
+        key_scales(p, n, c * 8, sc);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int c = lane + 32 * i;
-        if (c >= nck) continue;
-        if (scaled) {
-          // V1's key can be codes in one part and 16-bit values in the other
-          const bool f16 = F16 || ((p.v1 && c * 8 < p.Dv) ? p.vq != 0 : p.kq != 0);
-          uint32_t u[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = half_to_float<F16>(u[e] & 0xFFFFu) * inv_s[i][2 * e];
-            const float b = half_to_float<F16>(u[e] >> 16) * inv_s[i][2 * e + 1];
-            if (p.lse) shift += a * key_offset(p, n, c * 8 + 2 * e) + b * key_offset(p, n, c * 8 + 2 * e + 1);
-            u[e] = f16 ? pack_f16x2(a * up, b * up) : pack_bf16x2(a * up, b * up);
-          }
-          x[t][i] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-        *reinterpret_cast<uint4*>(smem + (c >> 3) * p.NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[t][i];
+        for (int e = 0; e < 8; ++e)
+          shift += half_to_float<F16>((u[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) / sc[e] * key_offset(p, n, c * 8 + e);
       }
-      if (scaled && p.lse) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) shift += __shfl_xor_sync(0xffffffffu, shift, o);
-        if (lane == 0) row_const[r] = -shift * p.scale;
+      for (int o = 16; o > 0; o >>= 1) shift += __shfl_xor_sync(0xffffffffu, shift, o);
+      if (lane == 0) row_const[r] = -shift * p.scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = lane + 32 * i;
+      // V1's key can be codes in one part and 16-bit values in the other
+      const bool f16 = F16 || ((p.v1 && c * 8 < p.Dv) ? p.vq != 0 : p.kq != 0);
+      const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t y[4];
+      float a[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        a[e] = half_to_float<F16>((u[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * (inv_s[i][e] * up);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(a[2 * e], a[2 * e + 1]);
+      if (!f16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
       }
+      if (c < nck)
+        *reinterpret_cast<uint4*>(row + (c >> 3) * p.NR * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
+  return true;
 }
 
 // F16: q, out and 16-bit caches are fp16, not bf16; P16: P is fp16 (V's operand is)
@@ -375,10 +399,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     mbar_init(smem_u32(&ms.s_full[1]), 1);
     mbar_init(smem_u32(&ms.p_ready), kSoftmax);
     mbar_init(smem_u32(&ms.pv_done), 1);
+    mbar_init(smem_u32(&ms.q_full), 1);
     mbar_init(smem_u32(&ms.q_ready), kSoftmax);
+    mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
     fence_mbar_init();
+    prefetch_tensormap(&p.tq);
+    prefetch_tensormap(&p.tk);
+    prefetch_tensormap(&p.tv);
   }
   __syncthreads();
   int64_t before = incl - mine, W = 0;
@@ -408,103 +437,217 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
+  const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
   volatile int* abort_flag = &ms.abort;
   Walker walk{ms.start_b, ms.start_off, min(per, W - start)};
   Piece w{};
 
+  if (warp >= kMmaWarp) {
+    set_max_regs_dec<kRegsRest>();
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
-    const int groups = kKeys / p.box_rows;
+    const int groups = kKeys >> p.box_shift;
     const bool direct = p.vq == 0 || p.kq == 0, staged = p.vq != 0 || p.kq != 0;
     const uint32_t direct_bytes = ((p.vq ? 0 : p.vslabs) + (p.kq ? 0 : p.kslabs)) * p.box_rows * 128;
     const uint32_t staged_bytes = ((p.vq ? p.vslabs : 0) + (p.kq ? p.kslabs : 0)) * p.box_rows * 64;
-    uint32_t armed[2] = {0, 0}, armed_parity[2] = {0, 0};   // copies in flight, by ring
-    // this lane's group of rows of tile t: the cache row it starts at (-1: none)
-    auto row_of = [&](int32_t t) -> int64_t {
-      const int32_t pos = t * kKeys + lane * p.box_rows;
-      if (lane >= groups || pos >= w.len) return -1;
-      if (p.mode == kModeNorm) return (static_cast<int64_t>(w.b) * p.N + w.n) * p.cache_seq + pos;
-      const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
-      const int32_t in = pos - pg * p.block_size;
-      const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
-      if (page < 0 || page >= p.block_num) {
-        if (p.err_count) atomicAdd(p.err_count, 1);
-        return -1;
-      }
-      return p.mode == kModePa ? page * p.block_size + in : (page * p.N + w.n) * p.block_size + in;
-    };
-    bool more = !p.stall_loads && walk.next(p, w);
-    while (more && w.ta >= w.tb) more = walk.next(p, w);
-    int32_t t = more ? w.ta : 0, u = 0;
-    int64_t row = more ? row_of(t) : -1;
-    bool ok = true;
-    while (more) {
-      const int st = u % p.ns, sg = staged ? u % p.nsg : 0;
-      const int32_t head = p.mode == kModePa ? w.n : 0;
-      // which keys of the tile exist
-      const int32_t have = row >= 0 ? min(p.box_rows, w.len - t * kKeys - lane * p.box_rows) : 0;
-      uint64_t bits = have > 0 ? (~0ull >> (64 - have)) << (lane * p.box_rows) : 0;
-      bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
-      bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
-      // the next tile's rows: its table entry is on the way while this tile waits
-      const int64_t this_row = row;
-      if (++t >= w.tb) {
-        more = walk.next(p, w);
-        while (more && w.ta >= w.tb) more = walk.next(p, w);
-        t = w.ta;
-      }
-      if (more) row = row_of(t);
-      const uint32_t par_d = (u / p.ns) & 1, par_s = staged ? (u / p.nsg) & 1 : 0;
-      if (direct) ok = bounded_wait_warp(smem_u32(&ms.kv_empty[st]), par_d ^ 1u, p.wait_ns, abort_flag);
-      if (ok && staged) ok = bounded_wait_warp(smem_u32(&ms.code_empty[sg]), par_s ^ 1u, p.wait_ns, abort_flag);
+    uint32_t armed[3] = {0, 0, 0}, armed_parity[3] = {0, 0, 0};   // copies in flight: operands, codes, Q
+    int32_t u = 0, pieces = 0;
+    Ring kv, code;
+    bool ok = !p.stall_loads;
+    while (ok && walk.next(p, w)) {
+      if (w.ta >= w.tb) continue;
+      // the row tile of Q, once the products of the last one are through with it
+      ok = bounded_wait_warp(smem_u32(&ms.q_empty), (pieces & 1) ^ 1u, p.wait_ns, abort_flag);
       if (!ok) break;
-      const uint32_t bar_d = smem_u32(&ms.kv_full[st]), bar_s = smem_u32(&ms.code_full[sg]);
-      const uint32_t live = __popc(__ballot_sync(0xffffffffu, this_row >= 0));
-      if (lane == 0) {
-        ms.valid[u % kValidRing] = bits;
-        if (direct) mbar_arrive_expect_tx(bar_d, live * direct_bytes);
-        if (staged) mbar_arrive_expect_tx(bar_s, live * staged_bytes);
+      if (elect_one()) {
+        const uint32_t bar = smem_u32(&ms.q_full);
+        mbar_arrive_expect_tx(bar, p.qslabs * p.hb * p.tb * 128);
+        for (int c = 0; c < p.qslabs; ++c) tma_load_3d(s0 + c * NR * 128, &p.tq, bar, 64 * c, w.head, w.q_start + w.tok);
       }
       __syncwarp();
-      if (this_row >= 0) {
-        const int32_t at = static_cast<int32_t>(this_row);
-        const uint32_t operand = s0 + p.off_ring + st * p.stage_bytes + lane * p.box_rows * 128;
-        const uint32_t codes = s0 + p.off_staging + sg * p.staging_bytes + lane * p.box_rows * 64;
-        for (int c = 0; c < p.vslabs; ++c)
-          tma_load_3d(p.vq ? codes + c * kCodeSlab : operand + c * kSlab, &p.tv, p.vq ? bar_s : bar_d, 64 * c, head, at);
-        const uint32_t k_codes = codes + (p.vq ? p.vslabs : 0) * kCodeSlab;
-        for (int c = 0; c < p.kslabs; ++c)
-          tma_load_3d(p.kq ? k_codes + c * kCodeSlab : operand + (p.vslabs + c) * kSlab, &p.tk, p.kq ? bar_s : bar_d,
-                      64 * c, head, at);
+      armed[2] = 1;
+      armed_parity[2] = pieces & 1;
+      ++pieces;
+      // Cache rows.  Lane i holds where group `base + i` of the piece starts: 32 groups of
+      // box_rows keys per trip to the block table.
+      const int32_t g_end = w.tb * groups, head = p.mode == kModePa ? w.n : 0;
+      int64_t row = -1;
+      int32_t base = w.ta * groups - 32;
+      for (int32_t t = w.ta; t < w.tb; ++t, ++u) {
+        if (t * groups >= base + 32) {
+          base += 32;
+          const int32_t pos = (base + lane) << p.box_shift;
+          row = -1;
+          if (base + lane < g_end && pos < w.len) {
+            if (p.mode == kModeNorm) {
+              row = (static_cast<int64_t>(w.b) * p.N + w.n) * p.cache_seq + pos;
+            } else {
+              const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
+              const int32_t in = pos - pg * p.block_size;
+              const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
+              if (page >= 0 && page < p.block_num)
+                row = p.mode == kModePa ? page * p.block_size + in : (page * p.N + w.n) * p.block_size + in;
+              else if (p.err_count)
+                atomicAdd(p.err_count, 1);
+            }
+          }
+        }
+        const int st = kv.stage, sg = code.stage;
+        const uint32_t par_d = kv.parity, par_s = code.parity;
+        if (direct) ok = bounded_wait_warp(smem_u32(&ms.kv_empty[st]), par_d ^ 1u, p.wait_ns, abort_flag);
+        if (ok && staged) ok = bounded_wait_warp(smem_u32(&ms.code_empty[sg]), par_s ^ 1u, p.wait_ns, abort_flag);
+        if (!ok) break;
+        // the starts of this tile's groups (at most four), and which of its keys exist
+        int32_t at[4];
+        uint64_t bits = 0;
+        uint32_t live = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          at[i] = -1;
+          if (i < groups) {
+            at[i] = __shfl_sync(0xffffffffu, static_cast<int32_t>(row), t * groups - base + i);
+            const int32_t have = min(p.box_rows, w.len - (t * kKeys + (i << p.box_shift)));
+            if (at[i] >= 0) {
+              bits |= (~0ull >> (64 - have)) << (i << p.box_shift);
+              ++live;
+            }
+          }
+        }
+        if (elect_one()) {
+          const uint32_t bar_d = smem_u32(&ms.kv_full[st]), bar_s = smem_u32(&ms.code_full[sg]);
+          ms.valid[u % kValidRing] = bits;
+          if (direct) mbar_arrive_expect_tx(bar_d, live * direct_bytes);
+          if (staged) mbar_arrive_expect_tx(bar_s, live * staged_bytes);
+          const uint32_t operand = s0 + p.off_ring + st * p.stage_bytes, codes = s0 + p.off_staging + sg * p.staging_bytes;
+          const uint32_t k_codes = codes + (p.vq ? p.vslabs : 0) * kCodeSlab;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (at[i] < 0) continue;
+            const uint32_t od = (i << p.box_shift) * 128, cd = (i << p.box_shift) * 64;
+            for (int c = 0; c < p.vslabs; ++c)
+              tma_load_3d(p.vq ? codes + cd + c * kCodeSlab : operand + od + c * kSlab, &p.tv, p.vq ? bar_s : bar_d, 64 * c,
+                          head, at[i]);
+            for (int c = 0; c < p.kslabs; ++c)
+              tma_load_3d(p.kq ? k_codes + cd + c * kCodeSlab : operand + od + (p.vslabs + c) * kSlab, &p.tk,
+                          p.kq ? bar_s : bar_d, 64 * c, head, at[i]);
+          }
+        }
+        __syncwarp();
+        if (direct) {
+          armed[0] |= 1u << st;
+          armed_parity[0] = (armed_parity[0] & ~(1u << st)) | (par_d << st);
+        }
+        if (staged) {
+          armed[1] |= 1u << sg;
+          armed_parity[1] = (armed_parity[1] & ~(1u << sg)) | (par_s << sg);
+        }
+        kv.next(p.ns);
+        code.next(p.nsg);
       }
-      if (direct) {
-        armed[0] |= 1u << st;
-        armed_parity[0] = (armed_parity[0] & ~(1u << st)) | (par_d << st);
-      }
-      if (staged) {
-        armed[1] |= 1u << sg;
-        armed_parity[1] = (armed_parity[1] & ~(1u << sg)) | (par_s << sg);
-      }
-      ++u;
     }
-    if (lane == 0 && (!ok || *abort_flag))  // let every copy in flight land before the block leaves
+    if (!p.stall_loads && (!ok || *abort_flag)) {  // let every copy in flight land before the block leaves
       for (int i = 0; i < kMaxStages; ++i) {
         // (a stage that converters share may stay open for them: then nothing is in flight after the limit)
         if (armed[0] & (1u << i)) bounded_drain(smem_u32(&ms.kv_full[i]), (armed_parity[0] >> i) & 1u, kDrainNs);
         if (armed[1] & (1u << i)) bounded_drain(smem_u32(&ms.code_full[i]), (armed_parity[1] >> i) & 1u, kDrainNs);
       }
+      if (armed[2]) bounded_drain(smem_u32(&ms.q_full), armed_parity[2], kDrainNs);
+    }
     __syncwarp();
-  } else if (warp >= 4 && warp < kMmaWarp) {
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    const bool bf = !p.f16;
+    const uint32_t id_s_v = idesc_f16(bf && p.vq == 0, false, false, 128, kKeys);   // V1: the latent part of the key
+    const uint32_t id_s_k = idesc_f16(bf && p.kq == 0, false, false, 128, kKeys);
+    const uint32_t id_o = idesc_f16(bf && p.vq == 0, true, false, 128, static_cast<uint32_t>(NR));
+    const uint64_t q_desc = sdesc_kmajor_sw128(s0);
+    const uint64_t k_desc = sdesc_kmajor_sw128(s0 + p.off_ring + p.kslab0 * kSlab);
+    const uint64_t v_desc = sdesc_mnmajor_sw128(s0 + p.off_ring, kSlab);
+    const uint64_t p_desc = sdesc_kmajor_sw128(s0 + p.off_p);
+    const int v_chunks = (p.Dv + 127) / 128;
+    const int q_step = NR * 128 >> 4;
+    int32_t jt = 0, pieces = 0;
+    Ring ring_s, ring_o;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      const int32_t n = w.tb - w.ta;
+      if (n <= 0) continue;
+      if (!bounded_wait_warp(smem_u32(k_quant ? &ms.q_ready : &ms.q_full), pieces & 1, p.wait_ns, abort_flag)) break;
+      // the accumulator's last readers (the epilogue of the piece before) are waited for at
+      // this piece's first P, which they write
+      ++pieces;
+      int32_t qk = 0, pv = 0;
+      uint64_t t_start = 0;
+      uint32_t spins = 0;
+      while (pv < n) {  // whichever product is ready next; the whole warp goes the same way
+        const int32_t u = jt + qk, v = jt + pv;
+        const int st_s = ring_s.stage, st_o = ring_o.stage;
+        const bool go_s = qk < n && qk - pv < 2 && mbar_test_wait(smem_u32(&ms.kv_full[st_s]), ring_s.parity);
+        if (__all_sync(0xffffffffu, go_s)) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t kb = k_desc + static_cast<uint64_t>(st_s * (p.stage_bytes >> 4));
+            const uint32_t d = tmem + (u & 1) * kKeys;
+            for (int sl = 0; sl < p.qslabs; ++sl)
+              mma4_f16_ss<2, 2>(d, q_desc + sl * q_step, kb + sl * (kSlab >> 4), p.v1 && sl < p.vslabs ? id_s_v : id_s_k,
+                                sl > 0, min(4, (p.Dk - sl * 64) / 16));
+            tc_commit(smem_u32(&ms.s_full[u & 1]));
+            if (qk + 1 == n) tc_commit(smem_u32(&ms.q_empty));
+          }
+          __syncwarp();
+          ring_s.next(p.ns);
+          ++qk;
+          spins = 0;
+          continue;
+        }
+        const bool go_o = pv < qk && mbar_test_wait(smem_u32(&ms.p_ready), v & 1);
+        if (__all_sync(0xffffffffu, go_o)) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t va = v_desc + static_cast<uint64_t>(st_o * (p.stage_bytes >> 4));
+            for (int c = 0; c < v_chunks; ++c)
+              mma4_f16_ss<128, 2>(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4), p_desc, id_o, pv > 0, 4);
+            tc_commit(smem_u32(&ms.kv_empty[st_o]));
+            tc_commit(smem_u32(&ms.pv_done));
+          }
+          __syncwarp();
+          ring_o.next(p.ns);
+          ++pv;
+          spins = 0;
+          continue;
+        }
+        if ((++spins & 31u) == 0) {
+          const uint64_t now = globaltimer_ns();
+          int give_up = 0;
+          if (spins == 32u) t_start = now;
+          else give_up = *abort_flag || now - t_start > p.wait_ns;
+          if (__any_sync(0xffffffffu, give_up)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+        }
+      }
+      jt += n;
+    }
+    if (elect_one()) tc_commit(smem_u32(&ms.drain));  // every product must finish before TMEM is released
+    __syncwarp();
+    bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
+    __syncwarp();
+  }
+  } else if (warp >= 4) {
+    set_max_regs_inc<kRegsConvert>();
     // ------------------------------------------------------------ codes to fp16 operands
     const int tid = threadIdx.x - kSoftmax;
     const int sl0 = p.vq ? 0 : p.vslabs, sl1 = p.vslabs + (p.kq ? p.kslabs : 0);  // the slabs that hold codes
     bool ok = p.nsg != 0 && !p.stall_loads;
     int32_t u = 0;
+    Ring kv, code;
     while (ok && walk.next(p, w)) {
       for (int32_t t = w.ta; ok && t < w.tb; ++t, ++u) {
-        const int st = u % p.ns, sg = u % p.nsg;
-        ok = bounded_wait_warp(smem_u32(&ms.code_full[sg]), (u / p.nsg) & 1, p.wait_ns, abort_flag) &&
-             bounded_wait_warp(smem_u32(&ms.kv_empty[st]), ((u / p.ns) & 1) ^ 1u, p.wait_ns, abort_flag);
+        const int st = kv.stage, sg = code.stage;
+        ok = bounded_wait_warp(smem_u32(&ms.code_full[sg]), code.parity, p.wait_ns, abort_flag) &&
+             bounded_wait_warp(smem_u32(&ms.kv_empty[st]), kv.parity ^ 1u, p.wait_ns, abort_flag);
         if (!ok) break;
         uint8_t* stage = smem + p.off_ring + st * p.stage_bytes;
         const uint8_t* from = smem + p.off_staging + sg * p.staging_bytes;
@@ -535,112 +678,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&ms.kv_full[st]));
         mbar_arrive(smem_u32(&ms.code_empty[sg]));
+        kv.next(p.ns);
+        code.next(p.nsg);
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ products
-    const bool bf = !p.f16;
-    const uint32_t id_s_v = idesc_f16(bf && p.vq == 0, false, false, 128, kKeys);   // V1: the latent part of the key
-    const uint32_t id_s_k = idesc_f16(bf && p.kq == 0, false, false, 128, kKeys);
-    const uint32_t id_o = idesc_f16(bf && p.vq == 0, true, false, 128, static_cast<uint32_t>(NR));
-    const uint64_t q_desc = sdesc_kmajor_sw128(s0);
-    const uint64_t k_desc = sdesc_kmajor_sw128(s0 + p.off_ring + p.kslab0 * kSlab);
-    const uint64_t v_desc = sdesc_mnmajor_sw128(s0 + p.off_ring, kSlab);
-    const uint64_t p_desc = sdesc_kmajor_sw128(s0 + p.off_p);
-    const int v_chunks = (p.Dv + 127) / 128;
-    const int q_step = NR * 128 >> 4;
-    int32_t jt = 0, pieces = 0;
-    bool ok = true;
-    while (ok && walk.next(p, w)) {
-      const int32_t n = w.tb - w.ta;
-      if (n <= 0) continue;
-      if (!bounded_wait_warp(smem_u32(&ms.q_ready), pieces & 1, p.wait_ns, abort_flag)) break;
-      ++pieces;
-      int32_t qk = 0, pv = 0;
-      uint64_t t_start = 0;
-      uint32_t spins = 0;
-      while (pv < n) {  // whichever product is ready next; the whole warp goes the same way
-        const int32_t u = jt + qk, v = jt + pv;
-        const int st_s = u % p.ns, st_o = v % p.ns;
-        const bool go_s = qk < n && qk - pv < 2 && mbar_test_wait(smem_u32(&ms.kv_full[st_s]), (u / p.ns) & 1);
-        if (__all_sync(0xffffffffu, go_s)) {
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t kb = k_desc + static_cast<uint64_t>(st_s * (p.stage_bytes >> 4));
-            const uint32_t d = tmem + (u & 1) * kKeys;
-            for (int sl = 0; sl < p.qslabs; ++sl)
-              mma4_f16_ss<2, 2>(d, q_desc + sl * q_step, kb + sl * (kSlab >> 4), p.v1 && sl < p.vslabs ? id_s_v : id_s_k,
-                                sl > 0, min(4, (p.Dk - sl * 64) / 16));
-            tc_commit(smem_u32(&ms.s_full[u & 1]));
-          }
-          __syncwarp();
-          ++qk;
-          spins = 0;
-          continue;
-        }
-        const bool go_o = pv < qk && mbar_test_wait(smem_u32(&ms.p_ready), v & 1);
-        if (__all_sync(0xffffffffu, go_o)) {
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t va = v_desc + static_cast<uint64_t>(st_o * (p.stage_bytes >> 4));
-            for (int c = 0; c < v_chunks; ++c)
-              mma4_f16_ss<128, 2>(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4), p_desc, id_o, pv > 0, 4);
-            tc_commit(smem_u32(&ms.kv_empty[st_o]));
-            tc_commit(smem_u32(&ms.pv_done));
-          }
-          __syncwarp();
-          ++pv;
-          spins = 0;
-          continue;
-        }
-        if ((++spins & 31u) == 0) {
-          const uint64_t now = globaltimer_ns();
-          int give_up = 0;
-          if (spins == 32u) t_start = now;
-          else give_up = *abort_flag || now - t_start > p.wait_ns;
-          if (__any_sync(0xffffffffu, give_up)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-        }
-      }
-      jt += n;
-    }
-    if (elect_one()) tc_commit(smem_u32(&ms.drain));  // every product must finish before TMEM is released
-    __syncwarp();
-    bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
-    __syncwarp();
   } else {
+    set_max_regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax, rescaling, epilogue
     const int tid = threadIdx.x;                     // also the row this thread owns
     const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
     const int v_chunks = (p.Dv + 127) / 128;
-    const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
-    int32_t jt = 0, piece = 0;
+    int32_t jt = 0, piece = 0, loaded = 0;
+    Ring kv;
     bool ok = true;
     for (; ok && walk.next(p, w); ++piece) {
       const int32_t n = w.tb - w.ta;
-      const uint32_t first_row = w.rt * NR;
       bar_128(1);                                    // the previous piece's row arrays are done with
-      if (tid < NR) {
-        const uint32_t rr = first_row + tid, tok = rr / static_cast<uint32_t>(p.g);
-        out_row[tid] = tid < w.rows ? static_cast<int32_t>((w.q_start + tok) * p.heads + w.n * p.g + (rr - tok * p.g)) : -1;
-      }
-      bar_128(1);
-      load_q<F16>(p, w.n, w.rows, smem, out_row, row_scale, row_const, k_quant, warp, lane);
-      fence_proxy_async_smem();
-      bar_128(1);
-      if (n > 0) mbar_arrive(smem_u32(&ms.q_ready));
-
       const bool live = tid < w.rows;
-      const float sl2 = live ? row_scale[tid] : 1.f;
-      const float lazy = kLazy / sl2;
-      int32_t seen = w.len;
-      if (p.causal && live) {
-        const int32_t tok = static_cast<int32_t>((first_row + tid) / static_cast<uint32_t>(p.g));
-        seen = min(w.len, max(0, w.len - w.Lq + tok + 1));
+      const int32_t my_tok = w.tok + (p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(tid) / static_cast<uint32_t>(p.hb)));
+      if (tid < NR)
+        out_row[tid] = live ? (w.q_start + my_tok) * p.heads + w.head + tid - (my_tok - w.tok) * p.hb : -1;
+      if (k_quant && n > 0) {
+        ok = scale_q<F16>(p, w.n, w.rows, smem, row_scale, row_const, warp, lane, smem_u32(&ms.q_full), loaded & 1, abort_flag);
+        fence_proxy_async_smem();
+        ok = bar_or(1, ok ? 0u : 1u) == 0;
+        if (!ok) break;
+        mbar_arrive(smem_u32(&ms.q_ready));
+        ++loaded;
       }
+      const float sl2 = live && k_quant && n > 0 ? row_scale[tid] : p.sl2;
+      const float lazy = kLazy / sl2;
+      const int32_t seen = p.causal && live ? min(w.len, max(0, w.len - w.Lq + my_tok + 1)) : w.len;
       float m = neg_inf(), l = 0.f;
       for (int32_t j = 0; j < n; ++j) {
         const int32_t u = jt + j;
@@ -689,16 +757,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         }
         if (ok && any && j > 0) {
           const float* fr = fac + (u & 1) * NR;
+#pragma unroll 1
           for (int c = 0; c < v_chunks; ++c) {
-            if (c * 128 + warp * 32 >= p.Dv) continue;
-            for (int col = 0; col < NR; col += 16) {
+            if (c * 128 + warp * 32 >= p.Dv) break;
+#pragma unroll 1
+            for (int col = 0; col < w.rows; col += 8) {
               const uint32_t at = tmem + lane_base + kSCols + c * NR + col;
-              uint32_t o[16];
-              tmem_ld_x16(at, o);
+              uint32_t o[8];
+              tmem_ld_x8(at, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr[col + e]);
-              tmem_st_x16(at, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr[col + e]);
+              tmem_st_x8(at, o);
             }
           }
           tmem_st_wait();
@@ -726,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           if (valid != ~0ull) {  // zero the value rows that do not exist, two threads per row
             const int key = tid >> 1;
             if (!((valid >> key) & 1)) {
-              uint8_t* vrow = smem + p.off_ring + (u % p.ns) * p.stage_bytes + key * 128 + (tid & 1) * 64;
+              uint8_t* vrow = smem + p.off_ring + kv.stage * p.stage_bytes + key * 128 + (tid & 1) * 64;
               for (int c = 0; c < p.vslabs; ++c)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -737,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(smem_u32(&ms.p_ready));
+        kv.next(p.ns);
       }
       if (ok && n > 0) ok = bounded_wait_warp(smem_u32(&ms.pv_done), (jt + n - 1) & 1, p.wait_ns, abort_flag);
       ok = bar_or(1, ok ? 0u : 1u) == 0;
@@ -750,9 +821,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       if (live) {
         if (w.whole()) {
           if (p.lse)
-            p.lse[out_row[tid]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + row_const[tid] : neg_inf();
+            p.lse[out_row[tid]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + (k_quant ? row_const[tid] : 0.f) : neg_inf();
         } else {
-          p.stats[slot * NR + tid] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, row_const[tid], 0.f);
+          p.stats[slot * NR + tid] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, k_quant && n > 0 ? row_const[tid] : 0.f, 0.f);
         }
       }
       if (piece == 0 && tid == 0) {
@@ -763,35 +834,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         mt[1] = first;
         mt[2] = last;
         mt[3] = w.rows;
-        mt[4] = w.q_start;
+        mt[4] = w.q_start + w.tok;
         mt[5] = w.n;
-        mt[6] = w.rt;
+        mt[6] = w.head;
         mt[0] = w.t0 > 0 && first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
       }
       bar_128(1);
+      // Rolled loops over eight rows at a time: this code runs once a piece, and each line of
+      // it comes from L2 (unrolled over 16 rows it took 21k cycles, now NEW_EPI).
+      const bool whole = w.whole();
+#pragma unroll 1
       for (int c = 0; c < v_chunks; ++c) {
         const int ch = c * 128 + tid;                 // this lane's channel
-        if (c * 128 + warp * 32 >= p.Dv) continue;
-        const float2 so = value_quant(p, w.n, min(ch, p.Dv - 1));
+        if (c * 128 + warp * 32 >= p.Dv) break;
+        float2 so = make_float2(1.f, 0.f);
+        if (whole && p.vq) so = value_quant(p, w.n, min(ch, p.Dv - 1));
         const float inv_s = 1.f / so.x;
-        for (int col = 0; col < w.rows; col += 16) {
-          uint32_t o[16];
+        float* part = p.parts + slot * NR * p.Dv + ch;
+#pragma unroll 1
+        for (int col = 0; col < w.rows; col += 8) {
+          uint32_t o[8];
           if (n > 0) {
-            tmem_ld_x16(tmem + lane_base + kSCols + c * NR + col, o);
+            tmem_ld_x8(tmem + lane_base + kSCols + c * NR + col, o);
             tmem_ld_wait();
           }
-          if (ch < p.Dv) {
+          if (ch >= p.Dv || (!whole && n == 0)) continue;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int r = col + e;
-              if (r >= w.rows) continue;
-              if (w.whole()) {
-                const float inv = inv_sum[r];
-                const float y = inv > 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
-                p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
-              } else if (n > 0) {
-                p.parts[(slot * NR + r) * p.Dv + ch] = __uint_as_float(o[e]);
-              }
+          for (int e = 0; e < 8; ++e) {
+            const int r = col + e;
+            if (r >= w.rows) break;
+            if (whole) {
+              const float inv = inv_sum[r];
+              const float y = inv > 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
+              p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
+            } else {
+              part[r * p.Dv] = __uint_as_float(o[e]);
             }
           }
         }
@@ -806,70 +883,105 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the items that a cut runs through: the blocks (c, *) take the rows of
-// the item whose first cut lies before block c's run.  The pieces' weights come first, one
-// thread each; then four groups of 128 threads sum every fourth piece, and the groups' sums
-// are added in a fixed order.
-constexpr int kJoinThreads = 512, kJoinGroups = 4;
+// Joins the pieces of the items that a cut runs through.  Blocks (x, *) take the x-th,
+// x + gridDim.x-th, ... block of the main kernel that says so in `meta`.  A unit is a row's
+// 128 channels: a warp sums an item of few pieces, the block's eight warps every eighth
+// piece of one with many, and their sums are added in a fixed order.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFew = 12;                // pieces up to which a warp takes a unit alone
+constexpr int kJoinLoads = (kMaxBlocks + 31) / 32;
 template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Params p) {
-  __shared__ float weight[kMaxBlocks], red[2][kJoinThreads / 32];
-  __shared__ float sum[kJoinGroups][512];
-  const int32_t* mt = p.meta + 8 * blockIdx.x;
-  if (mt[0] == 0) return;
-  const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3], NR = p.NR;
-  const int tid = threadIdx.x, group = tid / 128;
-  // the item's piece is the last of its first block, the first of the others
-  auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    const int64_t rr = static_cast<int64_t>(mt[6]) * NR + r, tok = rr / p.g;
-    const int64_t row = (mt[4] + tok) * p.heads + static_cast<int64_t>(mt[5]) * p.g + (rr - tok * p.g);
-    const float4 st = tid < n ? p.stats[slot(tid) * NR + r] : make_float4(neg_inf(), 0.f, 0.f, 0.f);
-    float m = st.x;
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Params p, int32_t blocks) {
+  __shared__ float4 sum[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NR = p.NR, slices = (p.Dv + 127) / 128;
+  int32_t skip = blockIdx.x;                // items before this block's next one
+  for (int32_t c0 = 0; c0 < blocks; c0 += 32) {
+    uint32_t has = __ballot_sync(0xffffffffu, c0 + lane < blocks && p.meta[8 * (c0 + lane)] != 0);
+    while (has) {
+      const int32_t c = c0 + __ffs(has) - 1;
+      has &= has - 1;
+      if (skip-- != 0) continue;
+      skip += gridDim.x;
+      const int32_t* mt = p.meta + 8 * c;
+      const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3], kv_head = mt[5];
+      const bool few = n <= kJoinFew;
+      // the item's piece is the last of its first block, the first of the others
+      auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+      const int32_t units = rows * slices, group = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+      const int32_t groups = few ? gridDim.y * kJoinWarps : gridDim.y;
+      for (int32_t unit = group; unit < units; unit += groups) {
+        const int32_t r = unit / slices, ch = (unit - r * slices) * 128 + lane * 4;
+        const int32_t t = r / p.hb;
+        const int64_t row = static_cast<int64_t>(mt[4] + t) * p.heads + mt[6] + (r - t * p.hb);
+        // every lane holds the statistics of pieces lane, lane + 32, ...
+        float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
+        float4 st[kJoinLoads];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) red[0][tid >> 5] = m;
-    __syncthreads();
+        for (int i = 0; i < kJoinLoads; ++i) {
+          st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+          if (32 * i < n && 32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + r];
+          m = fmaxf(m, st[i].x);
+          if (st[i].y > 0.f) k0 = st[i].z;  // the same in every piece that saw a key
+        }
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[0][i]);
-    const float wt = st.y > 0.f ? ex2(st.x - m) : 0.f;
-    if (tid < n) weight[tid] = wt;
-    float l = st.y * wt;
+        for (int o = 16; o > 0; o >>= 1) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if ((tid & 31) == 0) red[1][tid >> 5] = l;
-    __syncthreads();
-    l = 0.f;
+        for (int i = 0; i < kJoinLoads; ++i) {
+          wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
+          l = fmaf(st[i].y, wt[i], l);
+        }
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
-    const int ch = (tid & 127) * 4;
-    if (ch < p.Dv) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int i = group; i < n; i += kJoinGroups) {
-        if (weight[i] == 0.f) continue;  // a piece that saw nothing stored no accumulator
-        const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + r) * p.Dv + ch);
-        acc.x = fmaf(x.x, weight[i], acc.x);
-        acc.y = fmaf(x.y, weight[i], acc.y);
-        acc.z = fmaf(x.z, weight[i], acc.z);
-        acc.w = fmaf(x.w, weight[i], acc.w);
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+          if (32 * i >= n) break;
+#pragma unroll 4
+          for (int e = few ? 0 : warp; e < 32; e += few ? 1 : kJoinWarps) {
+            const float weight = __shfl_sync(0xffffffffu, wt[i], e);
+            if (weight == 0.f || ch >= p.Dv) continue;  // a piece that saw nothing stored no accumulator
+            const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + r) * p.Dv + ch);
+            acc.x = fmaf(x.x, weight, acc.x);
+            acc.y = fmaf(x.y, weight, acc.y);
+            acc.z = fmaf(x.z, weight, acc.z);
+            acc.w = fmaf(x.w, weight, acc.w);
+          }
+        }
+        if (!few) {
+          sum[warp][lane] = acc;
+          __syncthreads();
+          acc = sum[0][lane];
+#pragma unroll
+          for (int i = 1; i < kJoinWarps; ++i) {
+            const float4 x = sum[i][lane];
+            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+          }
+          __syncthreads();
+        }
+        if (few || warp == 0) {
+          if (lane == 0 && ch < 128 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float y[4] = {acc.x, acc.y, acc.z, acc.w};
+          if (ch < p.Dv) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 so = value_quant(p, kv_head, ch + e);
+              p.out[row * p.Dv + ch + e] = to_half<F16>(l > 0.f ? (y[e] * inv - so.y) / so.x : 0.f);
+            }
+          }
+        }
       }
-      *reinterpret_cast<float4*>(&sum[group][ch]) = acc;
     }
-    __syncthreads();
-    if (tid == 0 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + st.z : neg_inf();
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int c = tid; c < p.Dv; c += kJoinThreads) {
-      const float acc = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
-      const float2 so = value_quant(p, mt[5], c);
-      p.out[row * p.Dv + c] = to_half<F16>(l > 0.f ? (acc * inv - so.y) / so.x : 0.f);
-    }
-    __syncthreads();
   }
 }
 
 struct Plan {
-  int32_t NR, G;
+  int32_t NR, G, hb, tb, hblocks;
+  int64_t items;                // at most
   int32_t ns, nsg;
   int32_t vslabs, kslabs, qslabs, kslab0, stage, staging, off_p, off_ring, off_staging, off_misc, smem;
 };
@@ -914,7 +1026,12 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
   // one block per SM, and no more than there are runs of kMinTiles at the largest lengths
-  const int64_t rts = std::min<int64_t>(L.total_q * g, (L.total_q * g) / nr + L.B);
+  pl->hb = std::min(g, nr);
+  pl->tb = nr / pl->hb;
+  pl->hblocks = g > nr ? (g + nr - 1) / nr : 1;
+  if (pl->hblocks > 1) pl->tb = 1;
+  const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
+  pl->items = rts * L.N;
   const int64_t T = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
   const int64_t runs = (rts * L.N * T + kMinTiles - 1) / kMinTiles;
   pl->G = static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs)));
@@ -940,11 +1057,24 @@ bool make_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32_t wi
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q as (channels, heads, tokens), boxes of one row tile's 64 channels
+bool make_q_map(CUtensorMap* m, const PagedLaunch& L, const Plan& pl) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(L.Dkv), static_cast<cuuint64_t>(L.heads), static_cast<cuuint64_t>(L.total_q)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(L.Dkv) * 2, static_cast<cuuint64_t>(L.Dkv) * 2 * L.heads};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(pl.hb), static_cast<cuuint32_t>(pl.tb)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(L.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
 size_t stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
 
 template <bool F16, bool P16>
-cudaError_t launch(const Params& p, int blocks, int smem, cudaStream_t stream) {
+cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -958,7 +1088,10 @@ cudaError_t launch(const Params& p, int blocks, int smem, cudaStream_t stream) {
   kernel<<<blocks, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || blocks == 1) return e;
-  paged_join_kernel<F16><<<dim3(blocks, std::min(p.NR, 16)), kJoinThreads, 0, stream>>>(p);
+  // cuts there are, at most; and blocks for each that fill the SMs about twice
+  const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), units = p.NR * ((p.Dv + 127) / 128);
+  const int y = std::max(1, std::min(units, (2 * device_sm_count() + cuts - 1) / cuts));
+  paged_join_kernel<F16><<<dim3(cuts, y), kJoinThreads, 0, stream>>>(p, blocks);
   return cudaGetLastError();
 }
 
@@ -1009,7 +1142,6 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.heads = L.heads;
   p.g = L.heads / static_cast<int32_t>(L.N);
   p.NR = pl.NR;
-  p.nr_shift = pl.NR == 16 ? 4 : pl.NR == 32 ? 5 : pl.NR == 64 ? 6 : 7;
   p.block_size = static_cast<int32_t>(L.block_size);
   p.bs_shift = -1;
   for (int s = 0; s < 31; ++s)
@@ -1025,8 +1157,12 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.k_scalar = L.k_scalar;
   p.v_scalar = L.v_scalar;
   p.causal = L.causal;
+  p.hb = pl.hb;
+  p.tb = pl.tb;
+  p.hblocks = pl.hblocks;
   p.box_rows = L.mode == kModeNorm || L.block_size % 64 == 0 ? 64 : L.block_size % 32 == 0 ? 32 : 16;
-  if (!make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
+  p.box_shift = p.box_rows == 64 ? 6 : p.box_rows == 32 ? 5 : 4;
+  if (!make_q_map(&p.tq, L, pl) || !make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
@@ -1047,8 +1183,8 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);
   p.stall_loads = L.stall_loads;
 
-  if (L.f16) return launch<true, true>(p, pl.G, pl.smem, stream);
-  return L.vq ? launch<false, true>(p, pl.G, pl.smem, stream) : launch<false, false>(p, pl.G, pl.smem, stream);
+  if (L.f16) return launch<true, true>(p, pl.G, pl.items, pl.smem, stream);
+  return L.vq ? launch<false, true>(p, pl.G, pl.items, pl.smem, stream) : launch<false, false>(p, pl.G, pl.items, pl.smem, stream);
 }
 
 }  // namespace ra

@@ -408,7 +408,7 @@ def row_quantize_e4m3_packed(x: torch.Tensor, packed: torch.Tensor, stream=None)
 
 
 # ---------------------------------------------------------------- attention and the cache read
-_HALF = {RA_BF16: torch.bfloat16, RA_FP16: torch.float16}
+_I32, _I64, _F32, _U8 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.uint8,)
 _STORED = {RA_BF16: (torch.bfloat16,), RA_FP16: (torch.float16,), RA_INT8: (torch.int8,),
            RA_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), RA_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
 
@@ -418,23 +418,28 @@ def ra_test_stall_next_attention() -> None:
     load().ra_test_stall_next_attention()
 
 
-def _one_device(**tensors) -> None:
+def _arg(t: torch.Tensor | None, nbytes: int, dtypes, name: str) -> int | None:
+    """Pointer of a contiguous tensor of one of ``dtypes`` and of at least ``nbytes`` bytes."""
+    if t is None:
+        return None
+    size = t.numel() * t.element_size()
+    if size < nbytes:
+        raise ValueError(f"{name}: the call needs {nbytes} bytes, the tensor holds {size}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {dtypes[-1]}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _place(**tensors) -> None:
     """The calls run on the current device's stream: every tensor has to be there."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
     for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _half_tensor(t: torch.Tensor, code: int, name: str) -> None:
-    want = _HALF.get(code)
-    if want is not None and t.dtype != want:
-        raise ValueError(f"{name}: expected {want}, got {t.dtype}")
-
-
-def _stored_tensor(t: torch.Tensor | None, code: int, name: str) -> None:
-    want = _STORED.get(code)
-    if t is not None and want is not None and t.dtype not in want:
-        raise ValueError(f"{name}: expected {want[-1]}, got {t.dtype}")
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError(f"{name}: expected a CUDA tensor")
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{dev}")
 
 
 def packed_attention_params(q, k, v, out, *, B: int = 1, causal: bool = False,
@@ -443,26 +448,23 @@ def packed_attention_params(q, k, v, out, *, B: int = 1, causal: bool = False,
     token and head strides: views of a qkv_cte_mx output, for example
     ``qkv.view(T, heads, d)[:, :num_heads]`` (BSD) or ``planes[:num_heads].transpose(0, 1)``
     (NBSd).  softmax_scale defaults to head_dim ** -0.5."""
-    for name, t, other in (("q", q, q), ("k", k, k), ("v", v, k), ("out", out, q)):
+    qs, ks = q.shape, k.shape
+    for name, t, want in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)):
         if t.dim() != 3:
             raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
-        if t.shape != other.shape or t.shape[2] != q.shape[2]:
-            raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {tuple(other.shape)}")
+        if t.shape != want or want[2] != qs[2]:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {tuple(want if t.shape != want else qs)}")
         if t.dtype != q.dtype:
             raise ValueError(f"{name}: expected {q.dtype}, got {t.dtype}")
-        if t.shape[2] > 1 and t.stride(2) != 1:
+        if want[2] > 1 and t.stride(2) != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-    codes = {torch.bfloat16: RA_BF16, torch.float16: RA_FP16}
-    if q.dtype not in codes:
+    code = RA_BF16 if q.dtype == torch.bfloat16 else RA_FP16 if q.dtype == torch.float16 else None
+    if code is None:
         raise ValueError(f"q: expected bfloat16 or float16, got {q.dtype}")
-    d = q.shape[2]
-    return PackedAttentionParams(
-        B=B, total_q=q.shape[0], total_k=k.shape[0], num_heads=q.shape[1], num_kv_heads=k.shape[1],
-        head_dim=d, dtype=codes[q.dtype], causal=1 if causal else 0,
-        softmax_scale=d ** -0.5 if softmax_scale is None else softmax_scale,
-        q_token_stride=q.stride(0), q_head_stride=q.stride(1), k_token_stride=k.stride(0),
-        k_head_stride=k.stride(1), v_token_stride=v.stride(0), v_head_stride=v.stride(1),
-        out_token_stride=out.stride(0), out_head_stride=out.stride(1))
+    d = qs[2]
+    return PackedAttentionParams(B, qs[0], ks[0], qs[1], ks[1], d, code, 1 if causal else 0,
+                                 d ** -0.5 if softmax_scale is None else softmax_scale,
+                                 *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
 
 
 def packed_extents(p: PackedAttentionParams) -> dict[str, int]:
@@ -477,13 +479,16 @@ def packed_extents(p: PackedAttentionParams) -> dict[str, int]:
             "lse": p.total_q * p.num_heads * 4, "cu_seqlens_q": (p.B + 1) * 4, "cu_seqlens_k": (p.B + 1) * 4}
 
 
-def _strided_ptr(t: torch.Tensor, nbytes: int, name: str) -> int:
-    """Pointer of a strided 16-bit tensor whose storage holds `nbytes` from its first element."""
-    held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
-    if held < nbytes:
-        raise ValueError(f"{name}: the call needs {nbytes} bytes, the tensor's storage holds {held}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+def _strided_arg(t: torch.Tensor, tokens: int, heads: int, d: int, ts: int, hs: int, dtypes, name: str) -> int:
+    """Pointer of a strided 16-bit tensor [tokens, heads, d]: one with these sizes and strides
+    holds what the call addresses, any other has to in its storage."""
+    if t.shape != (tokens, heads, d) or t.stride() != (ts, hs, 1):
+        need = ((max(tokens, 1) - 1) * ts + (max(heads, 1) - 1) * hs + d) * 2
+        held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+        if held < need:
+            raise ValueError(f"{name}: the call needs {need} bytes, the tensor's storage holds {held}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {dtypes[-1]}, got {t.dtype}")
     return t.data_ptr()
 
 
@@ -497,29 +502,35 @@ def packed_attention(params, q, k, v, out, workspace, lse=None, cu_seqlens_q=Non
                      stream=None) -> None:
     """Attention over packed prompts (header: packed_attention); q, k, v and out as the
     tensors that ``packed_attention_params`` was given, or others with the same strides."""
-    ext = packed_extents(params)
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _half_tensor(t, params.dtype, name)
-    for name, t in (("lse", lse), ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
-        _need(t, ext[name], name)
-    ptrs = [_strided_ptr(t, ext[name], name) for name, t in (("q", q), ("k", k), ("v", v), ("out", out))]
-    _one_device(q=q, k=k, v=v, out=out, workspace=workspace, lse=lse, cu_seqlens_q=cu_seqlens_q,
-                cu_seqlens_k=cu_seqlens_k)
-    _check(load().packed_attention(
-        ctypes.byref(params), *ptrs, _ptr(lse, torch.float32, "lse"),
-        _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"), _ptr(cu_seqlens_k, torch.int32, "cu_seqlens_k"),
-        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)))
+    p, half = params, _STORED.get(params.dtype, (torch.bfloat16, torch.float16))
+    tq, tk, nq, nk, d, cu = p.total_q, p.total_k, p.num_heads, p.num_kv_heads, p.head_dim, (p.B + 1) * 4
+    args = (_strided_arg(q, tq, nq, d, p.q_token_stride, p.q_head_stride, half, "q"),
+            _strided_arg(k, tk, nk, d, p.k_token_stride, p.k_head_stride, half, "k"),
+            _strided_arg(v, tk, nk, d, p.v_token_stride, p.v_head_stride, half, "v"),
+            _strided_arg(out, tq, nq, d, p.out_token_stride, p.out_head_stride, half, "out"),
+            _arg(lse, tq * nq * 4, _F32, "lse"), _arg(cu_seqlens_q, cu, _I32, "cu_seqlens_q"),
+            _arg(cu_seqlens_k, cu, _I32, "cu_seqlens_k"), _arg(workspace, 0, _U8, "workspace"))
+    _place(q=q, k=k, v=v, out=out, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, workspace=workspace)
+    _check(load().packed_attention(ctypes.byref(p), *args, workspace.numel(), _stream(stream)))
+
+
+def _cache_extents(p: KvRmsNormRopeCacheParams) -> dict[str, int]:
+    """The part of kv_extents that a reader of the caches shares with their writer."""
+    v1, N = p.variant == 1, p.N
+    kw, cw = (p.rope_size, p.Dkv - p.rope_size) if v1 else (p.Dkv, p.Dv)
+    rows = (p.B * p.cache_seq_len if p.cache_mode == RA_CACHE_NORM else p.block_num * p.block_size) * N
+    qk, qv = (1 if p.k_quant_scalar else kw, 1 if p.c_kv_quant_scalar else cw) if v1 else (N * kw, N * cw)
+    return {"k_cache": rows * kw * _CACHE_BYTES.get(p.k_cache_dtype, 1),
+            "ckv_cache": rows * cw * _CACHE_BYTES.get(p.ckv_cache_dtype, 1),
+            "k_rope_scale": qk * 4, "k_rope_offset": qk * 4, "c_kv_scale": qv * 4, "c_kv_offset": qv * 4}
 
 
 def paged_extents(cache: KvRmsNormRopeCacheParams, p: PagedAttentionParams) -> dict[str, int]:
     """Bytes that each tensor argument of paged_attention spans, from the call's parameters."""
-    kv = kv_extents(cache)
     rows = max(p.total_q, 0) * max(p.num_heads, 0)
     return {"q": rows * max(cache.Dkv, 0) * 2, "out": rows * max(cache.Dv, 0) * 2, "lse": rows * 4,
             "seq_lens": p.B * 4, "block_table": p.B * p.block_table_stride * 4, "cu_seqlens_q": (p.B + 1) * 4,
-            "dev_error_count": 4,
-            **{n: kv[n] for n in ("k_cache", "ckv_cache", "k_rope_scale", "c_kv_scale", "k_rope_offset",
-                                  "c_kv_offset")}}
+            "dev_error_count": 4, **_cache_extents(cache)}
 
 
 def paged_attention_workspace_bytes(cache: KvRmsNormRopeCacheParams, params: PagedAttentionParams) -> int:
@@ -541,24 +552,18 @@ def paged_attention(cache, params, q, k_cache, ckv_cache, seq_lens, out, workspa
             params = PagedAttentionParams(params.B, params.total_q, params.num_heads, params.causal,
                                           params.softmax_scale, params.reserved, params.max_seq_len,
                                           block_table.shape[1])
-    _need_all(paged_extents(cache, params), q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, out=out,
-              block_table=block_table, cu_seqlens_q=cu_seqlens_q, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale,
-              k_rope_offset=k_rope_offset, c_kv_offset=c_kv_offset, lse=lse, dev_error_count=dev_error_count)
-    _half_tensor(q, cache.kv_dtype, "q")
-    _half_tensor(out, cache.kv_dtype, "out")
-    _stored_tensor(k_cache, cache.k_cache_dtype, "k_cache")
-    _stored_tensor(ckv_cache, cache.ckv_cache_dtype, "ckv_cache")
-    _one_device(q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, out=out, workspace=workspace,
-                block_table=block_table, cu_seqlens_q=cu_seqlens_q, lse=lse)
-    _check(load().paged_attention(
-        ctypes.byref(cache), ctypes.byref(params), _ptr(q, None, "q"), _ptr(k_cache, None, "k_cache"),
-        _ptr(ckv_cache, None, "ckv_cache"), _ptr(seq_lens, torch.int32, "seq_lens"),
-        _ptr(block_table, torch.int32, "block_table"), _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
-        _ptr(k_rope_scale, torch.float32, "k_rope_scale"), _ptr(c_kv_scale, torch.float32, "c_kv_scale"),
-        _ptr(k_rope_offset, torch.float32, "k_rope_offset"), _ptr(c_kv_offset, torch.float32, "c_kv_offset"),
-        _ptr(out, None, "out"), _ptr(lse, torch.float32, "lse"),
-        _ptr(dev_error_count, torch.int32, "dev_error_count"), _ptr(workspace, torch.uint8, "workspace"),
-        workspace.numel(), _stream(stream)))
+    ext, half = paged_extents(cache, params), _STORED.get(cache.kv_dtype)
+    arg = lambda t, name, dtypes: None if t is None else _arg(t, ext[name], dtypes, name)
+    args = (arg(q, "q", half), arg(k_cache, "k_cache", _STORED.get(cache.k_cache_dtype)),
+            arg(ckv_cache, "ckv_cache", _STORED.get(cache.ckv_cache_dtype)), arg(seq_lens, "seq_lens", _I32),
+            arg(block_table, "block_table", _I32), arg(cu_seqlens_q, "cu_seqlens_q", _I32),
+            arg(k_rope_scale, "k_rope_scale", _F32), arg(c_kv_scale, "c_kv_scale", _F32),
+            arg(k_rope_offset, "k_rope_offset", _F32), arg(c_kv_offset, "c_kv_offset", _F32), arg(out, "out", half),
+            arg(lse, "lse", _F32), arg(dev_error_count, "dev_error_count", _I32), _arg(workspace, 0, _U8, "workspace"))
+    _place(q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, block_table=block_table,
+           cu_seqlens_q=cu_seqlens_q, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale, k_rope_offset=k_rope_offset,
+           c_kv_offset=c_kv_offset, out=out, lse=lse, dev_error_count=dev_error_count, workspace=workspace)
+    _check(load().paged_attention(ctypes.byref(cache), ctypes.byref(params), *args, workspace.numel(), _stream(stream)))
 
 
 def attention_status(workspace: torch.Tensor, stream=None) -> int:
@@ -572,31 +577,25 @@ def attention_status(workspace: torch.Tensor, stream=None) -> int:
 
 def read_extents(p: KvRmsNormRopeCacheParams) -> dict[str, int]:
     """Bytes that each tensor argument of kv_cache_read spans, from the call's parameters."""
-    kv = kv_extents(p)
     kw, cw = (p.rope_size, p.Dkv - p.rope_size) if p.variant == 1 else (p.Dkv, p.Dv)
-    rows = max(p.B, 0) * max(p.N, 0) * max(p.S, 0)
-    return {"k_out": rows * max(kw, 0) * 2, "c_kv_out": rows * max(cw, 0) * 2, "dev_error_count": 4,
-            **{n: kv[n] for n in ("index", "k_cache", "ckv_cache", "k_rope_scale", "c_kv_scale", "k_rope_offset",
-                                  "c_kv_offset")}}
+    rows, bs = p.B * p.N * p.S, max(p.block_size, 1)
+    n_index = p.B * (-(-p.S // bs)) if p.cache_mode == RA_CACHE_PA_BLK_BNSD else p.B * p.S
+    return {"k_out": rows * kw * 2, "c_kv_out": rows * cw * 2, "index": n_index * 8, "dev_error_count": 4,
+            **_cache_extents(p)}
 
 
 def kv_cache_read(params, index, k_cache, ckv_cache, k_out=None, c_kv_out=None, k_rope_scale=None,
                   c_kv_scale=None, k_rope_offset=None, c_kv_offset=None, dev_error_count=None,
                   stream=None) -> None:
     """Rows of the caches of kv_rms_norm_rope_cache read back (header: kv_cache_read)."""
-    _need_all(read_extents(params), index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_out=k_out,
-              c_kv_out=c_kv_out, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale, k_rope_offset=k_rope_offset,
-              c_kv_offset=c_kv_offset, dev_error_count=dev_error_count)
-    for name, t in (("k_out", k_out), ("c_kv_out", c_kv_out)):
-        if t is not None:
-            _half_tensor(t, params.kv_dtype, name)
-    _stored_tensor(k_cache, params.k_cache_dtype, "k_cache")
-    _stored_tensor(ckv_cache, params.ckv_cache_dtype, "ckv_cache")
-    _one_device(index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_out=k_out, c_kv_out=c_kv_out)
-    _check(load().kv_cache_read(
-        ctypes.byref(params), _ptr(index, torch.int64, "index"), _ptr(k_cache, None, "k_cache"),
-        _ptr(ckv_cache, None, "ckv_cache"), _ptr(k_rope_scale, torch.float32, "k_rope_scale"),
-        _ptr(c_kv_scale, torch.float32, "c_kv_scale"), _ptr(k_rope_offset, torch.float32, "k_rope_offset"),
-        _ptr(c_kv_offset, torch.float32, "c_kv_offset"), _ptr(k_out, None, "k_out"),
-        _ptr(c_kv_out, None, "c_kv_out"), _ptr(dev_error_count, torch.int32, "dev_error_count"),
-        _stream(stream)))
+    ext, half = read_extents(params), _STORED.get(params.kv_dtype)
+    arg = lambda t, name, dtypes: None if t is None else _arg(t, ext[name], dtypes, name)
+    args = (arg(index, "index", _I64), arg(k_cache, "k_cache", _STORED.get(params.k_cache_dtype)),
+            arg(ckv_cache, "ckv_cache", _STORED.get(params.ckv_cache_dtype)), arg(k_rope_scale, "k_rope_scale", _F32),
+            arg(c_kv_scale, "c_kv_scale", _F32), arg(k_rope_offset, "k_rope_offset", _F32),
+            arg(c_kv_offset, "c_kv_offset", _F32), arg(k_out, "k_out", half), arg(c_kv_out, "c_kv_out", half),
+            arg(dev_error_count, "dev_error_count", _I32))
+    _place(index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale,
+           k_rope_offset=k_rope_offset, c_kv_offset=c_kv_offset, k_out=k_out, c_kv_out=c_kv_out,
+           dev_error_count=dev_error_count)
+    _check(load().kv_cache_read(ctypes.byref(params), *args, _stream(stream)))
