@@ -25,7 +25,7 @@ LIB_NAME = "librope_attention.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "qkv_project.cu", "qk_norm_rope.cu", "kv_cache.cu", "noalloc.cu", "row_quant.cu",
-           "packed_attention.cu", "paged_attention.cu", "cache_read.cu"]
+           "packed_attention.cu", "paged_attention.cu", "paged_tile.cu", "cache_read.cu"]
 
 
 def nvcc() -> str:

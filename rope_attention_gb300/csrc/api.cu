@@ -335,6 +335,28 @@ ra_status check_cache(const kv_rms_norm_rope_cache_params* p, const float* k_sca
   return RA_OK;
 }
 
+ra::PackedLaunch packed_launch(const packed_attention_params* p) {
+  ra::PackedLaunch L{};
+  L.B = p->B;
+  L.total_q = p->total_q;
+  L.total_k = p->total_k;
+  L.q_ts = p->q_token_stride;
+  L.q_hs = p->q_head_stride;
+  L.k_ts = p->k_token_stride;
+  L.k_hs = p->k_head_stride;
+  L.v_ts = p->v_token_stride;
+  L.v_hs = p->v_head_stride;
+  L.o_ts = p->out_token_stride;
+  L.o_hs = p->out_head_stride;
+  L.nq = p->num_heads;
+  L.nkv = p->num_kv_heads;
+  L.d = p->head_dim;
+  L.causal = p->causal;
+  L.f16 = p->dtype == RA_FP16;
+  L.scale = p->softmax_scale;
+  return L;
+}
+
 bool good_scale(float s) { return std::isfinite(s) && s > 0.f; }
 
 ra_status check_packed(const packed_attention_params* p) {
@@ -779,7 +801,7 @@ ra_status packed_attention_workspace_bytes(const packed_attention_params* p, siz
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
   const ra_status st = check_packed(p);
   if (st != RA_OK) return st;
-  *bytes = ra::kAttnHeader;
+  *bytes = ra::packed_attention_workspace(packed_launch(p));
   return ok();
 }
 
@@ -798,10 +820,10 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
     return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_q, total_q must be a multiple of B");
   if (!cu_seqlens_k && p->total_k % p->B != 0)
     return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_k, total_k must be a multiple of B");
-  st = check_attn_workspace(workspace, workspace_bytes, ra::kAttnHeader);
+  ra::PackedLaunch L = packed_launch(p);
+  st = check_attn_workspace(workspace, workspace_bytes, ra::packed_attention_workspace(L));
   if (st != RA_OK) return st;
   if (validate_only()) return ok();
-  ra::PackedLaunch L{};
   L.q = q;
   L.k = k;
   L.v = v;
@@ -809,24 +831,8 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
   L.lse = lse;
   L.cu_q = cu_seqlens_q;
   L.cu_k = cu_seqlens_k;
-  L.B = p->B;
-  L.total_q = p->total_q;
-  L.total_k = p->total_k;
-  L.q_ts = p->q_token_stride;
-  L.q_hs = p->q_head_stride;
-  L.k_ts = p->k_token_stride;
-  L.k_hs = p->k_head_stride;
-  L.v_ts = p->v_token_stride;
-  L.v_hs = p->v_head_stride;
-  L.o_ts = p->out_token_stride;
-  L.o_hs = p->out_head_stride;
-  L.nq = p->num_heads;
-  L.nkv = p->num_kv_heads;
-  L.d = p->head_dim;
-  L.causal = p->causal;
-  L.f16 = p->dtype == RA_FP16;
-  L.scale = p->softmax_scale;
   L.status = static_cast<int32_t*>(workspace);
+  L.partials = static_cast<uint8_t*>(workspace) + ra::kAttnHeader;
   L.wait_ns = g_wait_ns.load();
   L.stall_loads = g_stall_next_attn.exchange(0);
   const char* why = "launch failed";

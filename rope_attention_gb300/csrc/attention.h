@@ -21,9 +21,12 @@ struct PackedLaunch {
   int32_t causal, f16;
   float scale;
   int32_t* status;
+  uint8_t* partials;           // workspace behind the header
   int64_t wait_ns;
   int32_t stall_loads;
 };
+// Bytes of workspace (header included) of any call with these sizes.
+size_t packed_attention_workspace(const PackedLaunch& L);
 cudaError_t launch_packed_attention(const PackedLaunch& L, cudaStream_t stream, const char** why);
 
 struct PagedLaunch {
@@ -49,6 +52,11 @@ struct PagedLaunch {
 // Bytes of workspace (header included) of any call with these sizes.
 size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
+// The kernel for many rows per sequence and kv head (paged_tile.cu): whether it takes the
+// call, its part of the workspace, and the launch.
+bool paged_tile_serves(const PagedLaunch& L);
+size_t paged_tile_workspace(const PagedLaunch& L);
+cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
 struct ReadLaunch {
   const int64_t* index;

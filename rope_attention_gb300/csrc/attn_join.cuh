@@ -1,0 +1,199 @@
+// Work shared out in runs of key tiles, and the joining of what a run cuts in two.
+//
+// Both attention kernels lay the key tiles of all their work items end to end and give
+// each block an equal run, so blocks finish together whatever the lengths.  A block that
+// gets a part of an item stores the part's (max, sum, accumulator) in the workspace; the
+// second kernel here joins an item's parts in the order of the blocks, so results do not
+// depend on which block finished first.
+#pragma once
+
+#include <algorithm>
+
+#include "attn_ptx.cuh"
+#include "internal.h"
+
+namespace ra {
+namespace {
+
+constexpr int kMaxBlocks = 160;           // blocks that a workspace has room for (a GB300 has 152 SMs)
+
+// a position in a ring of stages: the stage, and the parity of its barriers' phase.  (A
+// division by the number of stages costs a lone warp 150 cycles or more.)
+struct Ring {
+  int32_t stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int32_t stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// A part of block c is its first piece (slot 2 c) where the item began before the block's
+// run, else its last (2 c + 1).
+struct JoinParams {
+  float4* stats;                // [2 G][NR] (max in log2 units, sum, the lse's share of the key offsets, -)
+  float* parts;                 // [2 G][NR][Dv] unscaled accumulators
+  int32_t* meta;                // [G][8]: an item to join (0 / 1), its first and last block, rows of its one or
+                                // two subtiles, first token (of all), first head, kv head
+  uint16_t* out;
+  float* lse;
+  const float *v_scale, *v_offset;
+  int64_t o_ts, o_hs;           // strides of out
+  int32_t heads, hb, tb;        // a subtile: tb tokens x hb heads
+  int32_t Dv, NR, sub;          // rows of a part, rows of a subtile (NR or NR / 2)
+  int32_t per_head, v_scalar;   // the value's quantisation: [N, Dv], or [Dv] ([1])
+};
+
+template <bool F16>
+__device__ __forceinline__ uint16_t to_half(float x) {
+  return F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+// scale and offset of one channel of a cache row (1 and 0 for a 16-bit cache)
+__device__ __forceinline__ float2 channel_quant(const float* scale, const float* offset, int32_t at, int32_t scalar) {
+  if (scale == nullptr) return make_float2(1.f, 0.f);
+  const int32_t i = scalar ? 0 : at;
+  return make_float2(__ldg(scale + i), offset ? __ldg(offset + i) : 0.f);
+}
+
+// Blocks (x, *) take the x-th, x + gridDim.x-th, ... block of the main kernel that says in
+// `meta` that an item's first cut lies before it.  A unit is a row's 128 channels: a warp
+// sums an item of few pieces, the block's eight warps every eighth piece of one with many,
+// and their sums are added in a fixed order.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFew = 12;                // pieces up to which a warp takes a unit alone
+constexpr int kJoinLoads = (kMaxBlocks + 31) / 32;
+template <bool F16>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t blocks) {
+  __shared__ float4 sum[kJoinWarps][32];
+  grid_dependency_wait();                   // launched while the main kernel's last blocks still run
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NR = p.NR, slices = (p.Dv + 127) / 128;
+  int32_t skip = blockIdx.x;                // items before this block's next one
+  for (int32_t c0 = 0; c0 < blocks; c0 += 32) {
+    uint32_t has = __ballot_sync(0xffffffffu, c0 + lane < blocks && p.meta[8 * (c0 + lane)] != 0);
+    while (has) {
+      const int32_t c = c0 + __ffs(has) - 1;
+      has &= has - 1;
+      if (skip-- != 0) continue;
+      skip += gridDim.x;
+      const int32_t* mt = p.meta + 8 * c;
+      const int32_t first = mt[1], n = mt[2] - first + 1, rows0 = mt[3], rows1 = mt[4], kv_head = mt[7];
+      const bool few = n <= kJoinFew;
+      auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+      const int32_t units = (rows0 + rows1) * slices, group = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+      const int32_t groups = few ? gridDim.y * kJoinWarps : gridDim.y;
+      for (int32_t unit = group; unit < units; unit += groups) {
+        int32_t r = unit / slices;
+        const int32_t ch = (unit - r * slices) * 128 + lane * 4;
+        const int32_t in = r < rows0 ? r : r - rows0;      // row of its subtile
+        const int32_t t = in / p.hb, h = in - t * p.hb;
+        const int64_t token = mt[5] + (r < rows0 ? 0 : p.tb) + t, head = mt[6] + h;
+        r = r < rows0 ? r : p.sub + in;
+        // every lane holds the statistics of pieces lane, lane + 32, ...
+        float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
+        float4 st[kJoinLoads];
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+          st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+          if (32 * i < n && 32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + r];
+          m = fmaxf(m, st[i].x);
+          if (st[i].y > 0.f) k0 = st[i].z;  // the same in every piece that saw a key
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+          wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
+          l = fmaf(st[i].y, wt[i], l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+          if (32 * i >= n) break;
+#pragma unroll 4
+          for (int e = few ? 0 : warp; e < 32; e += few ? 1 : kJoinWarps) {
+            const float weight = __shfl_sync(0xffffffffu, wt[i], e);
+            if (weight == 0.f || ch >= p.Dv) continue;  // a piece that saw nothing stored no accumulator
+            const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + r) * p.Dv + ch);
+            acc.x = fmaf(x.x, weight, acc.x);
+            acc.y = fmaf(x.y, weight, acc.y);
+            acc.z = fmaf(x.z, weight, acc.z);
+            acc.w = fmaf(x.w, weight, acc.w);
+          }
+        }
+        if (!few) {
+          sum[warp][lane] = acc;
+          __syncthreads();
+          acc = sum[0][lane];
+#pragma unroll
+          for (int i = 1; i < kJoinWarps; ++i) {
+            const float4 x = sum[i][lane];
+            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+          }
+          __syncthreads();
+        }
+        if (few || warp == 0) {
+          if (lane == 0 && ch < 128 && p.lse)
+            p.lse[token * p.heads + head] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+          if (ch < p.Dv) {
+            if (p.v_scale) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 so = channel_quant(p.v_scale, p.v_offset, (p.per_head ? kv_head * p.Dv : 0) + ch + e, p.v_scalar);
+                y[e] = l > 0.f ? (y[e] - so.y) / so.x : 0.f;
+              }
+            }
+            uint2 w;
+            w.x = pack_half2<!F16>(y[0], y[1]);
+            w.y = pack_half2<!F16>(y[2], y[3]);
+            *reinterpret_cast<uint2*>(p.out + token * p.o_ts + head * p.o_hs + ch) = w;
+          }
+        }
+      }
+    }
+  }
+}
+
+// The join behind a main kernel of `blocks` blocks over at most `items` items; it is put in
+// place while that kernel still runs (programmatic stream serialisation).
+inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
+  if (blocks < 2) return cudaSuccess;
+  // the cuts that there can be, and blocks for each that fill the SMs
+  const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), units = p.NR * ((p.Dv + 127) / 128);
+  const int y = std::max(1, std::min(units, (8 * device_sm_count() + cuts - 1) / cuts));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(cuts, y);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, p, static_cast<int32_t>(blocks))
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, p, static_cast<int32_t>(blocks));
+}
+
+inline size_t join_meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
+inline size_t join_stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
+inline size_t join_bytes(int G, int NR, int Dv) {
+  return join_meta_bytes(G) + join_stats_bytes(G, NR) + static_cast<size_t>(G) * 2 * NR * Dv * sizeof(float);
+}
+// sets the pointers of a join whose workspace was sized for G blocks
+inline void join_place(JoinParams* j, uint8_t* at, int G) {
+  j->meta = reinterpret_cast<int32_t*>(at);
+  j->stats = reinterpret_cast<float4*>(at + join_meta_bytes(G));
+  j->parts = reinterpret_cast<float*>(at + join_meta_bytes(G) + join_stats_bytes(G, j->NR));
+}
+
+}  // namespace
+}  // namespace ra

@@ -24,24 +24,26 @@
 //    of S come from whatever follows in shared memory and are never read.
 //  * V1's value row is the first part of its key row: one tile in shared memory serves
 //    both products (K-major for S, MN-major for O^T).
-//  * Warp 9 reads the block table and issues TMA boxes of 16, 32 or 64 rows (what divides
+//  * Warp 13 reads the block table and issues TMA boxes of 16, 32 or 64 rows (what divides
 //    a page), 64 channels wide: straight into the swizzled operand tile for 16-bit caches,
-//    or as codes into a staging ring that warps 4-7 convert from.  Rows behind a
+//    or as codes into a staging ring that warps 8-11 convert from.  Rows behind a
 //    sequence's end and rows of absent pages are zeroed in shared memory (0 times a
-//    stray NaN is NaN) and masked in S.  Warps 0-3 are the softmax, the rescaling and the
-//    epilogue; warp 8 issues the MMAs, taking whichever of the next S = Q K^T and the
+//    stray NaN is NaN) and masked in S.  Warps 0-7 are the softmax, the rescaling and the
+//    epilogue, two threads to a row of S with 32 of its 64 columns each (with one thread
+//    a 64-key tile took 1740 cycles, more than its products); warp 12 issues the MMAs, taking whichever of the next S = Q K^T and the
 //    next O^T += V^T P^T is ready first.
 // Every wait is bounded in time (status word).
-#include <cuda_fp8.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 
 #include "attention.h"
+#include "attn_join.cuh"
 #include "attn_ptx.cuh"
 #include "internal.h"
 #include "kv_cache.h"
+#include "paged_codes.cuh"
+#include "paged_maps.cuh"
 
 namespace ra {
 namespace {
@@ -49,19 +51,18 @@ namespace {
 constexpr int kKeys = 64;                 // keys per tile: one 128-byte swizzled row of P
 constexpr int kSlab = kKeys * 128;        // 64 keys x 64 channels of 16 bits
 constexpr int kCodeSlab = kKeys * 64;      // the same of codes
-constexpr int kThreads = 384;              // three warpgroups
-// Registers per thread: launched with 168 each, then moved to the softmax:
-// 232 + 184 + 88 = 3 x 168
-constexpr int kRegsSoftmax = 232, kRegsConvert = 184, kRegsRest = 88;
-constexpr int kSoftmax = 128, kConverters = 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 512;              // four warpgroups
+// Registers per thread: launched with 128 each, then moved to the softmax:
+// 2 x 160 + 120 + 72 = 4 x 128
+constexpr int kRegsSoftmax = 160, kRegsConvert = 120, kRegsRest = 72;
+constexpr int kSoftmax = 256, kSoftmaxWarps = kSoftmax / 32, kConvertWarps = 4;
+constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kValidRing = 16;            // > tiles between the loads and the softmax
 constexpr int kMaxStages = 6;
 constexpr int kMinTiles = 4;              // tiles per block below which a split costs more than it gives
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSmemMax = 232448;
-constexpr int kMaxBlocks = 160;           // blocks that a workspace has room for (a GB300 has 152 SMs)
 constexpr int kSCols = 2 * kKeys;         // TMEM: two S buffers, then O^T
 
 struct Params {
@@ -75,9 +76,7 @@ struct Params {
   const int32_t *cu_q, *seq_lens, *table;
   int32_t* err_count;
   int32_t* status;
-  float4* stats;                // [2 G][NR] (m in log2 units, l, lse constant, -) of partial pieces
-  float* parts;                 // [2 G][NR][Dv]
-  int32_t* meta;                // [G][8]
+  JoinParams join;
   int64_t table_stride, cap;    // cap: positions that a sequence can have
   int64_t block_num, cache_seq;
   int32_t B, total_q, N, heads, g, NR, block_size, bs_shift;
@@ -104,7 +103,7 @@ struct Misc {                   // behind the tiles in shared memory
   int32_t start_b;
   uint32_t tmem;
   int32_t abort;
-  // followed by per-row arrays of NR: int32 out_row, float row_scale, row_const, fac[2], inv_sum
+  // followed by per-row arrays of NR: int32 out_row, float row_scale, row_const, xch[2], inv_sum
 };
 __host__ __device__ constexpr int row_arrays_bytes(int nr) { return nr * (4 + 5 * 4); }
 
@@ -131,19 +130,6 @@ __device__ __forceinline__ int64_t seq_work(const Params& p, int32_t b) {
   q_span(p, b, s, lq);
   return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * tiles_of(seq_len_of(p, b));
 }
-
-// A position in a ring of stages: the stage, and the parity of its barriers' phase.  (A
-// division by the number of stages costs a lone warp 150 cycles or more.)
-struct Ring {
-  int32_t stage = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next(int32_t stages) {
-    if (++stage == stages) {
-      stage = 0;
-      parity ^= 1u;
-    }
-  }
-};
 
 // One block's share of an item: key tiles [ta, tb) of row tile rt of (b, n).
 struct Piece {
@@ -202,53 +188,21 @@ struct Walker {
   }
 };
 
-__device__ __forceinline__ uint32_t bar_or(uint32_t id, uint32_t pred) {
+// over the softmax warps
+__device__ __forceinline__ uint32_t bar_or(uint32_t pred) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(pred), "r"(id)
+      : "r"(pred)
       : "memory");
   return r;
 }
-__device__ __forceinline__ void bar_128(uint32_t id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// four codes -> four fp16 values, exactly
-__device__ __forceinline__ uint2 codes_to_half(uint32_t c, int32_t kind) {
-  uint2 r;
-  if (kind == kQuantInt8) {
-    // 0x6400 | u is the fp16 number 1024 + u; with u = code + 128, subtract 1152
-    c ^= 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    uint32_t lo = __byte_perm(c, 0x64646464u, 0x4140), hi = __byte_perm(c, 0x64646464u, 0x4342);
-    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), off), b = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
-    r.x = *reinterpret_cast<uint32_t*>(&a);
-    r.y = *reinterpret_cast<uint32_t*>(&b);
-  } else if (kind == kQuantE5m2) {  // the upper byte of an fp16 number
-    r.x = __byte_perm(c, 0, 0x1404);
-    r.y = __byte_perm(c, 0, 0x3424);
-  } else {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
-    r.x = a.x | (static_cast<uint32_t>(a.y) << 16);
-    r.y = b.x | (static_cast<uint32_t>(b.y) << 16);
-  }
-  return r;
-}
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool F16>
 __device__ __forceinline__ float half_to_float(uint32_t u) {
   return F16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u))) : __uint_as_float(u << 16);
-}
-template <bool F16>
-__device__ __forceinline__ uint16_t to_half(float x) {
-  return F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-// scale and offset of one channel of a cache row (1 and 0 for a 16-bit cache)
-__device__ __forceinline__ float2 channel_quant(const float* scale, const float* offset, int32_t at, int32_t scalar) {
-  if (scale == nullptr) return make_float2(1.f, 0.f);
-  const int32_t i = scalar ? 0 : at;
-  return make_float2(__ldg(scale + i), offset ? __ldg(offset + i) : 0.f);
 }
 // the scales of key channels c..c+7 of head n: V1's key is the ckv row, then the k row
 __device__ __forceinline__ void key_scales(const Params& p, int32_t n, int32_t c, float (&s)[8]) {
@@ -299,7 +253,7 @@ __device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: bits order like values
   if (!bounded_wait_warp(q_full, parity, p.wait_ns, abort_flag)) return false;
 #pragma unroll 1
-  for (int r = warp; r < rows; r += 4) {
+  for (int r = warp; r < rows; r += kSoftmaxWarps) {
     uint8_t* row = smem + r * 128;
     uint4 x[3];
     uint32_t big = 0;  // |q| as bits orders like the value in either type
@@ -368,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   int32_t* out_row = reinterpret_cast<int32_t*>(&ms + 1);  // row of q and out, -1: none
   float* row_scale = reinterpret_cast<float*>(out_row + NR);
   float* row_const = row_scale + NR;
-  float* fac = row_const + NR;              // [2][NR]
-  float* inv_sum = fac + 2 * NR;
+  float* xch = row_const + NR;              // [2][NR] what the two threads of a row exchange
+  float* inv_sum = xch + 2 * NR;
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -387,20 +341,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   if (lane == 31) ms.scan[warp] = incl;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ns; ++s) {
-      // one arrival with the bytes of a 16-bit cache, one from each thread that converts codes
-      mbar_init(smem_u32(&ms.kv_full[s]), (p.vq == 0 || p.kq == 0 ? 1 : 0) + (p.nsg != 0 ? kConverters : 0));
+      // one arrival with the bytes of a 16-bit cache, one from each warp that converts codes
+      mbar_init(smem_u32(&ms.kv_full[s]), (p.vq == 0 || p.kq == 0 ? 1 : 0) + (p.nsg != 0 ? kConvertWarps : 0));
       mbar_init(smem_u32(&ms.kv_empty[s]), 1);
     }
     for (int s = 0; s < p.nsg; ++s) {
       mbar_init(smem_u32(&ms.code_full[s]), 1);
-      mbar_init(smem_u32(&ms.code_empty[s]), kConverters);
+      mbar_init(smem_u32(&ms.code_empty[s]), kConvertWarps);
     }
     mbar_init(smem_u32(&ms.s_full[0]), 1);
     mbar_init(smem_u32(&ms.s_full[1]), 1);
-    mbar_init(smem_u32(&ms.p_ready), kSoftmax);
+    mbar_init(smem_u32(&ms.p_ready), kSoftmaxWarps);
     mbar_init(smem_u32(&ms.pv_done), 1);
     mbar_init(smem_u32(&ms.q_full), 1);
-    mbar_init(smem_u32(&ms.q_ready), kSoftmax);
+    mbar_init(smem_u32(&ms.q_ready), kSoftmaxWarps);
     mbar_init(smem_u32(&ms.q_empty), 1);
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
@@ -420,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   const int64_t G = gridDim.x;
   const int64_t per = max((W + G - 1) / G, static_cast<int64_t>(kMinTiles));
   const int64_t start = per * blockIdx.x;
-  if (threadIdx.x == 0) p.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
+  grid_launch_dependents();
+  if (threadIdx.x == 0) p.join.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
   if (start >= W) return;
   if (before <= start && start < before + mine) {
     int32_t b = b_lo;
@@ -635,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     bounded_drain(smem_u32(&ms.drain), 0, kDrainNs);
     __syncwarp();
   }
-  } else if (warp >= 4) {
-    set_max_regs_inc<kRegsConvert>();
+  } else if (warp >= kSoftmaxWarps) {
+    set_max_regs_dec<kRegsConvert>();
     // ------------------------------------------------------------ codes to fp16 operands
     const int tid = threadIdx.x - kSoftmax;
     const int sl0 = p.vq ? 0 : p.vslabs, sl1 = p.vslabs + (p.kq ? p.kslabs : 0);  // the slabs that hold codes
@@ -676,8 +631,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&ms.kv_full[st]));
-        mbar_arrive(smem_u32(&ms.code_empty[sg]));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ms.kv_full[st]));
+          mbar_arrive(smem_u32(&ms.code_empty[sg]));
+        }
         kv.next(p.ns);
         code.next(p.nsg);
       }
@@ -685,174 +643,176 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   } else {
     set_max_regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax, rescaling, epilogue
-    const int tid = threadIdx.x;                     // also the row this thread owns
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
+    const int tid = threadIdx.x, quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;                // the row this thread owns, with the other half's
+    const int col0 = half * 32;                      // its columns of S
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const int v_chunks = (p.Dv + 127) / 128;
     int32_t jt = 0, piece = 0, loaded = 0;
     Ring kv;
     bool ok = true;
     for (; ok && walk.next(p, w); ++piece) {
       const int32_t n = w.tb - w.ta;
-      bar_128(1);                                    // the previous piece's row arrays are done with
-      const bool live = tid < w.rows;
-      const int32_t my_tok = w.tok + (p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(tid) / static_cast<uint32_t>(p.hb)));
-      if (tid < NR)
-        out_row[tid] = live ? (w.q_start + my_tok) * p.heads + w.head + tid - (my_tok - w.tok) * p.hb : -1;
+      bar_softmax();                                 // the previous piece's row arrays are done with
+      const bool live = row < w.rows;
+      const int32_t my_tok = w.tok + (p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.hb)));
+      if (half == 0 && row < NR)
+        out_row[row] = live ? (w.q_start + my_tok) * p.heads + w.head + row - (my_tok - w.tok) * p.hb : -1;
+      if (piece == 0 && tid == 0 && w.t0 > 0) {
+        // the block behind the first cut through an item joins the item's pieces
+        const int64_t item0 = start - w.t0;
+        const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
+        int32_t* mt = p.join.meta + 8 * blockIdx.x;
+        mt[1] = first;
+        mt[2] = last;
+        mt[3] = w.rows;
+        mt[4] = 0;
+        mt[5] = w.q_start + w.tok;
+        mt[6] = w.head;
+        mt[7] = w.n;
+        mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+      }
       if (k_quant && n > 0) {
         ok = scale_q<F16>(p, w.n, w.rows, smem, row_scale, row_const, warp, lane, smem_u32(&ms.q_full), loaded & 1, abort_flag);
         fence_proxy_async_smem();
-        ok = bar_or(1, ok ? 0u : 1u) == 0;
+        ok = bar_or(ok ? 0u : 1u) == 0;
         if (!ok) break;
-        mbar_arrive(smem_u32(&ms.q_ready));
+        if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
         ++loaded;
       }
-      const float sl2 = live && k_quant && n > 0 ? row_scale[tid] : p.sl2;
+      const float sl2 = live && k_quant && n > 0 ? row_scale[row] : p.sl2;
       const float lazy = kLazy / sl2;
       const int32_t seen = p.causal && live ? min(w.len, max(0, w.len - w.Lq + my_tok + 1)) : w.len;
+      const bool rows_here = quad * 32 < w.rows;     // uniform in the warp
       float m = neg_inf(), l = 0.f;
       for (int32_t j = 0; j < n; ++j) {
         const int32_t u = jt + j;
         if (!bounded_wait_warp(smem_u32(&ms.s_full[u & 1]), (u >> 1) & 1, p.wait_ns, abort_flag)) ok = false;
         tc_fence_after();
-        uint32_t s[kKeys];
-        float f = 1.f;
-        uint32_t grow = 0;
-        const bool rows_here = warp * 32 < w.rows;   // uniform in the warp
+        uint32_t s[32];
+        float top = neg_inf();
+        const uint64_t valid = ms.valid[u % kValidRing];
         if (ok && rows_here) {
-          tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys, s);
-          tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys + 32, s + 32);
+          tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys + col0, s);
           tmem_ld_wait();
-          const int32_t nv = seen - (w.ta + j) * kKeys;
-          uint64_t mask = ms.valid[u % kValidRing];
-          if (nv < kKeys) mask &= nv <= 0 ? 0ull : (1ull << nv) - 1;
-          if (__any_sync(0xffffffffu, mask != ~0ull)) {
+          const int32_t nv = seen - (w.ta + j) * kKeys - col0;  // keys of these 32 that the row sees
+          uint32_t mask = static_cast<uint32_t>(valid >> col0);
+          if (nv < 32) mask &= nv <= 0 ? 0u : (1u << nv) - 1;
+          if (__any_sync(0xffffffffu, mask != ~0u)) {
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c)
+            for (int c = 0; c < 32; ++c)
               if (!((mask >> c) & 1)) s[c] = __float_as_uint(neg_inf());
           }
           float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 8)
+          for (int c = 0; c < 32; c += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
+        // a row's maximum grew, or a wait gave up
+        const uint32_t any = bar_or((live && top > m + lazy) || !ok ? 1u : 0u);
+        if (j > 0) {  // P's buffer is free, and the accumulator complete, once the last product is
+          if (ok && !bounded_wait_warp(smem_u32(&ms.pv_done), (u - 1) & 1, p.wait_ns, abort_flag)) ok = false;
+          tc_fence_after();
+        }
+        if (any) {
+          if (row < NR) xch[half * NR + row] = top;
+          if (bar_or(ok ? 0u : 1u)) {  // the group leaves together
+            ok = false;
+            break;
+          }
+          float f = 1.f;
+          if (live) top = fmaxf(top, xch[(half ^ 1) * NR + row]);
           if (live && top > m + lazy) {
             f = ex2((m - top) * sl2);
             l *= f;
             m = top;
-            grow = 1;
           }
-        }
-        if (tid < NR) fac[(u & 1) * NR + tid] = f;
-        // a row's maximum grew, or a wait gave up: then the group leaves together
-        const uint32_t any = bar_or(1, grow | (ok ? 0u : 1u));
-        if (any && bar_or(1, ok ? 0u : 1u)) {
-          ok = false;
-          break;
-        }
-        if (j > 0) {  // P's buffer is free, and the accumulator complete, once the last product is
-          if (!bounded_wait_warp(smem_u32(&ms.pv_done), (u - 1) & 1, p.wait_ns, abort_flag)) ok = false;
-          tc_fence_after();
-        }
-        if (ok && any && j > 0) {
-          const float* fr = fac + (u & 1) * NR;
+          bar_softmax();
+          if (half == 0 && row < NR) xch[row] = f;
+          bar_softmax();
+          if (j > 0) {
 #pragma unroll 1
-          for (int c = 0; c < v_chunks; ++c) {
-            if (c * 128 + warp * 32 >= p.Dv) break;
+            for (int c = 0; c < v_chunks; ++c) {
+              if (c * 128 + quad * 32 >= p.Dv) break;
 #pragma unroll 1
-            for (int col = 0; col < w.rows; col += 8) {
-              const uint32_t at = tmem + lane_base + kSCols + c * NR + col;
-              uint32_t o[8];
-              tmem_ld_x8(at, o);
-              tmem_ld_wait();
+              for (int col = half * 8; col < w.rows; col += 16) {
+                const uint32_t at = tmem + lane_base + kSCols + c * NR + col;
+                uint32_t o[8];
+                tmem_ld_x8(at, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr[col + e]);
-              tmem_st_x8(at, o);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * xch[col + e]);
+                tmem_st_x8(at, o);
+              }
             }
+            tmem_st_wait();
           }
-          tmem_st_wait();
         }
         if (ok && rows_here) {
           const float neg = m == neg_inf() ? 0.f : -m * sl2;
-          const float2 sc = make_float2(sl2, sl2), ng = make_float2(neg, neg);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint8_t* prow = smem + p.off_p + tid * 128;
+          uint32_t x[16];
+          exp_batch<!P16>(s, make_float2(sl2, sl2), make_float2(neg, neg), acc, x);
+          if (live) {
+            uint8_t* prow = smem + p.off_p + row * 128;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[16];
-            exp_batch<!P16>(s + 32 * h, sc, ng, acc, x);
-            if (live)
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(prow + (((4 * h + c) ^ (tid & 7)) << 4)) =
-                    make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(prow + (((4 * half + c) ^ (row & 7)) << 4)) =
+                  make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
           }
           const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l += sum.x + sum.y;
         }
-        if (ok && p.vq == 0) {
-          const uint64_t valid = ms.valid[u % kValidRing];
-          if (valid != ~0ull) {  // zero the value rows that do not exist, two threads per row
-            const int key = tid >> 1;
-            if (!((valid >> key) & 1)) {
-              uint8_t* vrow = smem + p.off_ring + kv.stage * p.stage_bytes + key * 128 + (tid & 1) * 64;
-              for (int c = 0; c < p.vslabs; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  *reinterpret_cast<uint4*>(vrow + c * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+        if (p.vq == 0 && valid != ~0ull) {  // zero the value rows that do not exist, four threads per row
+          const int key = tid >> 2;
+          if (!((valid >> key) & 1)) {
+            uint8_t* vrow = smem + p.off_ring + kv.stage * p.stage_bytes + key * 128 + (tid & 3) * 32;
+            for (int c = 0; c < p.vslabs; ++c) {
+              *reinterpret_cast<uint4*>(vrow + c * kSlab) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(vrow + c * kSlab + 16) = make_uint4(0, 0, 0, 0);
             }
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(smem_u32(&ms.p_ready));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready));
         kv.next(p.ns);
       }
       if (ok && n > 0) ok = bounded_wait_warp(smem_u32(&ms.pv_done), (jt + n - 1) & 1, p.wait_ns, abort_flag);
-      ok = bar_or(1, ok ? 0u : 1u) == 0;
+      if (row < NR) xch[half * NR + row] = l;
+      ok = bar_or(ok ? 0u : 1u) == 0;
       if (!ok) break;
       tc_fence_after();
       jt += n;
 
       // ---- epilogue: final rows, or the piece's statistics and accumulator
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1);
-      if (tid < NR) inv_sum[tid] = l > 0.f ? 1.f / l : 0.f;
-      if (live) {
-        if (w.whole()) {
-          if (p.lse)
-            p.lse[out_row[tid]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + (k_quant ? row_const[tid] : 0.f) : neg_inf();
-        } else {
-          p.stats[slot * NR + tid] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, k_quant && n > 0 ? row_const[tid] : 0.f, 0.f);
-        }
-      }
-      if (piece == 0 && tid == 0) {
-        // the block behind the first cut through an item joins the item's pieces
-        const int64_t item0 = start - w.t0;
-        const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
-        int32_t* mt = p.meta + 8 * blockIdx.x;
-        mt[1] = first;
-        mt[2] = last;
-        mt[3] = w.rows;
-        mt[4] = w.q_start + w.tok;
-        mt[5] = w.n;
-        mt[6] = w.head;
-        mt[0] = w.t0 > 0 && first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
-      }
-      bar_128(1);
-      // Rolled loops over eight rows at a time: this code runs once a piece, and each line of
-      // it comes from L2 (unrolled over 16 rows it took 21k cycles, now NEW_EPI).
       const bool whole = w.whole();
+      if (half == 0 && row < NR) {
+        l += xch[NR + row];
+        inv_sum[row] = l > 0.f ? 1.f / l : 0.f;
+        const float shift = k_quant && n > 0 && live ? row_const[row] : 0.f;
+        if (live && whole && p.lse)
+          p.lse[out_row[row]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
+        if (live && !whole) p.join.stats[slot * NR + row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
+      }
+      bar_softmax();
+      // Rolled loops over eight rows at a time: this code runs once a piece, and each line of
+      // it comes from L2 (unrolled over 16 rows it took 26k cycles for 64 rows of 512).
 #pragma unroll 1
       for (int c = 0; c < v_chunks; ++c) {
-        const int ch = c * 128 + tid;                 // this lane's channel
-        if (c * 128 + warp * 32 >= p.Dv) break;
+        const int ch = c * 128 + row;                 // this lane's channel
+        if (c * 128 + quad * 32 >= p.Dv) break;
         float2 so = make_float2(1.f, 0.f);
         if (whole && p.vq) so = value_quant(p, w.n, min(ch, p.Dv - 1));
         const float inv_s = 1.f / so.x;
-        float* part = p.parts + slot * NR * p.Dv + ch;
+        float* part = p.join.parts + slot * NR * p.Dv + ch;
 #pragma unroll 1
-        for (int col = 0; col < w.rows; col += 8) {
+        for (int col = half * 8; col < w.rows; col += 16) {
           uint32_t o[8];
           if (n > 0) {
             tmem_ld_x8(tmem + lane_base + kSCols + c * NR + col, o);
@@ -881,102 +841,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   tc_fence_after();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-}
-
-// Joins the pieces of the items that a cut runs through.  Blocks (x, *) take the x-th,
-// x + gridDim.x-th, ... block of the main kernel that says so in `meta`.  A unit is a row's
-// 128 channels: a warp sums an item of few pieces, the block's eight warps every eighth
-// piece of one with many, and their sums are added in a fixed order.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinFew = 12;                // pieces up to which a warp takes a unit alone
-constexpr int kJoinLoads = (kMaxBlocks + 31) / 32;
-template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Params p, int32_t blocks) {
-  __shared__ float4 sum[kJoinWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int NR = p.NR, slices = (p.Dv + 127) / 128;
-  int32_t skip = blockIdx.x;                // items before this block's next one
-  for (int32_t c0 = 0; c0 < blocks; c0 += 32) {
-    uint32_t has = __ballot_sync(0xffffffffu, c0 + lane < blocks && p.meta[8 * (c0 + lane)] != 0);
-    while (has) {
-      const int32_t c = c0 + __ffs(has) - 1;
-      has &= has - 1;
-      if (skip-- != 0) continue;
-      skip += gridDim.x;
-      const int32_t* mt = p.meta + 8 * c;
-      const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3], kv_head = mt[5];
-      const bool few = n <= kJoinFew;
-      // the item's piece is the last of its first block, the first of the others
-      auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-      const int32_t units = rows * slices, group = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
-      const int32_t groups = few ? gridDim.y * kJoinWarps : gridDim.y;
-      for (int32_t unit = group; unit < units; unit += groups) {
-        const int32_t r = unit / slices, ch = (unit - r * slices) * 128 + lane * 4;
-        const int32_t t = r / p.hb;
-        const int64_t row = static_cast<int64_t>(mt[4] + t) * p.heads + mt[6] + (r - t * p.hb);
-        // every lane holds the statistics of pieces lane, lane + 32, ...
-        float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
-        float4 st[kJoinLoads];
-#pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
-          if (32 * i < n && 32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + r];
-          m = fmaxf(m, st[i].x);
-          if (st[i].y > 0.f) k0 = st[i].z;  // the same in every piece that saw a key
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
-        }
-#pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
-          l = fmaf(st[i].y, wt[i], l);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          if (32 * i >= n) break;
-#pragma unroll 4
-          for (int e = few ? 0 : warp; e < 32; e += few ? 1 : kJoinWarps) {
-            const float weight = __shfl_sync(0xffffffffu, wt[i], e);
-            if (weight == 0.f || ch >= p.Dv) continue;  // a piece that saw nothing stored no accumulator
-            const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + r) * p.Dv + ch);
-            acc.x = fmaf(x.x, weight, acc.x);
-            acc.y = fmaf(x.y, weight, acc.y);
-            acc.z = fmaf(x.z, weight, acc.z);
-            acc.w = fmaf(x.w, weight, acc.w);
-          }
-        }
-        if (!few) {
-          sum[warp][lane] = acc;
-          __syncthreads();
-          acc = sum[0][lane];
-#pragma unroll
-          for (int i = 1; i < kJoinWarps; ++i) {
-            const float4 x = sum[i][lane];
-            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
-          }
-          __syncthreads();
-        }
-        if (few || warp == 0) {
-          if (lane == 0 && ch < 128 && p.lse) p.lse[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          const float y[4] = {acc.x, acc.y, acc.z, acc.w};
-          if (ch < p.Dv) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 so = value_quant(p, kv_head, ch + e);
-              p.out[row * p.Dv + ch + e] = to_half<F16>(l > 0.f ? (y[e] * inv - so.y) / so.x : 0.f);
-            }
-          }
-        }
-      }
-    }
-  }
 }
 
 struct Plan {
@@ -1038,41 +902,6 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   return true;
 }
 
-// A cache's rows as a 3-D map: PA (channels, heads, slots), the others (channels, 1, rows);
-// boxes of 64 channels x box_rows rows, swizzled like an MMA operand unless they are codes
-bool make_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32_t width, int32_t quant, int32_t box_rows) {
-  auto enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  const uint64_t row = static_cast<uint64_t>(width) * (quant ? 1 : 2);
-  const bool pa = L.mode == kModePa;
-  const uint64_t slots = L.mode == kModeNorm ? static_cast<uint64_t>(L.B) * L.cache_seq
-                                             : static_cast<uint64_t>(L.block_num) * L.block_size;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), pa ? static_cast<cuuint64_t>(L.N) : 1, pa ? slots : slots * L.N};
-  cuuint64_t strides[2] = {row, pa ? row * L.N : row};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
-             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// q as (channels, heads, tokens), boxes of one row tile's 64 channels
-bool make_q_map(CUtensorMap* m, const PagedLaunch& L, const Plan& pl) {
-  auto enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(L.Dkv), static_cast<cuuint64_t>(L.heads), static_cast<cuuint64_t>(L.total_q)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(L.Dkv) * 2, static_cast<cuuint64_t>(L.Dkv) * 2 * L.heads};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(pl.hb), static_cast<cuuint32_t>(pl.tb)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(L.q), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-size_t meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
-size_t stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
-
 template <bool F16, bool P16>
 cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
@@ -1087,33 +916,30 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
   }
   kernel<<<blocks, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || blocks == 1) return e;
-  // cuts there are, at most; and blocks for each that fill the SMs about twice
-  const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), units = p.NR * ((p.Dv + 127) / 128);
-  const int y = std::max(1, std::min(units, (2 * device_sm_count() + cuts - 1) / cuts));
-  paged_join_kernel<F16><<<dim3(cuts, y), kJoinThreads, 0, stream>>>(p, blocks);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join(p.join, F16, blocks, items, stream);
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(const PagedLaunch& L) {
+  if (paged_tile_serves(L)) return kAttnHeader + paged_tile_workspace(L);
   Plan pl;
   if (!plan(L, &pl)) return 0;
-  return kAttnHeader + meta_bytes(pl.G) + stats_bytes(pl.G, pl.NR) +
-         static_cast<size_t>(pl.G) * 2 * pl.NR * L.Dv * sizeof(float);
+  return kAttnHeader + join_bytes(pl.G, pl.NR, L.Dv);
 }
 
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why) {
+  if (paged_tile_serves(L)) return launch_paged_tile(L, stream, why);
   Plan pl;
   if (!plan(L, &pl)) {
     *why = "no tile shape fits";
     return cudaErrorInvalidValue;
   }
-  uint8_t* const stats = L.partials + meta_bytes(pl.G);
-  uint8_t* const parts = stats + stats_bytes(pl.G, pl.NR);
-  pl.G = std::min(pl.G, device_sm_count());
   Params p{};
+  p.join.NR = p.join.sub = pl.NR;
+  join_place(&p.join, L.partials, pl.G);
+  pl.G = std::min(pl.G, device_sm_count());
   p.q = L.q;
   p.out = L.out;
   p.lse = L.lse;
@@ -1128,9 +954,18 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.table = L.table;
   p.err_count = L.err_count;
   p.status = L.status;
-  p.meta = reinterpret_cast<int32_t*>(L.partials);
-  p.stats = reinterpret_cast<float4*>(stats);
-  p.parts = reinterpret_cast<float*>(parts);
+  p.join.out = L.out;
+  p.join.lse = L.lse;
+  p.join.v_scale = L.v_scale;
+  p.join.v_offset = L.v_offset;
+  p.join.o_hs = L.Dv;
+  p.join.o_ts = static_cast<int64_t>(L.Dv) * L.heads;
+  p.join.heads = L.heads;
+  p.join.hb = pl.hb;
+  p.join.tb = pl.tb;
+  p.join.Dv = L.Dv;
+  p.join.per_head = L.variant == 2;
+  p.join.v_scalar = L.v_scalar;
   p.table_stride = L.table_stride;
   const int64_t room = L.mode == kModeNorm ? L.cache_seq : L.table_stride * L.block_size;
   p.cap = std::min<int64_t>(room, L.max_seq_len);
@@ -1162,7 +997,7 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.hblocks = pl.hblocks;
   p.box_rows = L.mode == kModeNorm || L.block_size % 64 == 0 ? 64 : L.block_size % 32 == 0 ? 32 : 16;
   p.box_shift = p.box_rows == 64 ? 6 : p.box_rows == 32 ? 5 : 4;
-  if (!make_q_map(&p.tq, L, pl) || !make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
+  if (!make_q_map(&p.tq, L, pl.hb, pl.tb) || !make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

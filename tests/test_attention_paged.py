@@ -203,3 +203,46 @@ def test_equal_tokens_without_starts():
 
 def test_large_scores():
     run_case(19, variant=2, lens=[900], news=[40], heads=4, N=2, std=20.0)
+
+
+# ---------------------------------------------------------------- many rows per sequence and kv head
+@pytest.mark.parametrize("dims", [(64, 64, 32), (96, 80, 32), (128, 128, 64), (160, 48, 64), (192, 128, 64), (16, 16, 8)])
+@pytest.mark.parametrize("kt", ["bf16", "int8", "e4m3", "e5m2"])
+def test_chunk_widths_and_types(dims, kt):
+    run_case(20, variant=2, lens=[300, 90, 0], news=[150, 90, 3], heads=4, N=2, Dkv=dims[0], Dv=dims[1], R=dims[2], kt=kt, vt=kt)
+
+
+@pytest.mark.parametrize("mode,bs", [("PA", 16), ("PA", 96), ("PA_BNSD", 32), ("PA_BNSD", 64), ("PA_BNSD", 128), ("PA_BNSD", 160),
+                                     ("PA_BNSD", 256), ("Norm", 0)])
+@pytest.mark.parametrize("kt,Dkv", [("bf16", 128), ("bf16", 192), ("int8", 128), ("int8", 192)])
+def test_chunk_pages(mode, bs, kt, Dkv):
+    if kt == "int8" and bs == 16:
+        bs = 32
+    run_case(21, variant=2, lens=[400, 129], news=[100, 129], heads=6, N=2, Dkv=Dkv, mode=mode, bs=bs or 32, kt=kt, vt=kt)
+
+
+@pytest.mark.parametrize("g", [1, 3, 7, 64, 100, 128, 130])
+def test_chunk_groups(g):
+    run_case(22, variant=2, lens=[200, 40], news=[80 if g < 8 else 5, 40 if g < 8 else 3], heads=2 * g, N=2)
+
+
+@pytest.mark.parametrize("kt", ["bf16", "int8"])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+def test_chunk_split_over_blocks(kt, causal):
+    run_case(23, variant=2, lens=[4500, 0, 70, 1], news=[40, 2, 70, 9], heads=2, N=1, kt=kt, vt=kt, tail=5, causal=causal)
+
+
+@pytest.mark.parametrize("kt", ["bf16", "e4m3"])
+def test_chunk_bad_pages(kt):
+    run_case(24, variant=2, lens=[300, 200], news=[80, 70], heads=4, N=2, kt=kt, vt=kt, bad_pages=[(0, 1, -1), (0, 4, 1 << 20), (1, 0, -3)])
+
+
+def test_chunk_more_queries_than_keys():
+    run_case(25, variant=2, lens=[60, 0, 3], news=[300, 100, 90], heads=2, N=1)
+
+
+def test_chunk_fp16_and_far_scales():
+    run_case(26, variant=2, lens=[200], news=[100], heads=4, N=2, dtype="fp16", kt="fp16", vt="fp16")
+    run_case(27, variant=2, lens=[200], news=[100], heads=4, N=2, dtype="fp16", kt="int8", vt="e4m3")
+    run_case(28, variant=2, lens=[200], news=[100], heads=4, N=2, kt="int8", vt="int8", scale_range=(2e4, 9e4), std=30.0)
+    run_case(29, variant=2, lens=[200], news=[100], heads=4, N=2, kt="int8", vt="int8", offsets=False)
