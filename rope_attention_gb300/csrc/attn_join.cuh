@@ -58,107 +58,180 @@ __device__ __forceinline__ float2 channel_quant(const float* scale, const float*
 }
 
 // Blocks (x, *) take the x-th, x + gridDim.x-th, ... block of the main kernel that says in
-// `meta` that an item's first cut lies before it.  A unit is a row's 128 channels: a warp
-// sums an item of few pieces, the block's eight warps every eighth piece of one with many,
-// and their sums are added in a fixed order.
+// `meta` that an item's first cut lies before it.  An item of few pieces: a warp takes four
+// rows' 128 channels at once, the rows' statistics side by side in its lanes, so that the
+// loads of four rows are in flight.  One with many: the block's eight warps take every
+// eighth piece of one row's 128 channels, and their sums are added in a fixed order.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinFew = 12;                // pieces up to which a warp takes a unit alone
+constexpr int kJoinFew = 8;                 // pieces up to which a warp takes rows alone
 constexpr int kJoinLoads = (kMaxBlocks + 31) / 32;
+
+struct JoinRow {
+  int32_t part;                             // row of a part
+  int64_t token, head;
+};
+__device__ __forceinline__ JoinRow join_row(const JoinParams& p, const int32_t* mt, int32_t r) {
+  const int32_t rows0 = mt[3], in = r < rows0 ? r : r - rows0;      // row of its subtile
+  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(in) / static_cast<uint32_t>(p.hb));
+  return JoinRow{r < rows0 ? r : p.sub + in, mt[5] + (r < rows0 ? 0 : p.tb) + t, mt[6] + in - t * p.hb};
+}
+template <bool F16>
+__device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& row, int32_t kv_head, int32_t ch, float4 acc,
+                                           float l) {
+  const float inv = l > 0.f ? rcp(l) : 0.f;
+  float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  if (p.v_scale) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 so = channel_quant(p.v_scale, p.v_offset, (p.per_head ? kv_head * p.Dv : 0) + ch + e, p.v_scalar);
+      y[e] = l > 0.f ? (y[e] - so.y) * rcp(so.x) : 0.f;
+    }
+  }
+  *reinterpret_cast<uint2*>(p.out + row.token * p.o_ts + row.head * p.o_hs + ch) =
+      make_uint2(pack_half2<!F16>(y[0], y[1]), pack_half2<!F16>(y[2], y[3]));
+}
+__device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row, float m, float l, float k0) {
+  p.lse[row.token * p.heads + row.head] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
+}
+
 template <bool F16>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t blocks) {
   __shared__ float4 sum[kJoinWarps][32];
   grid_dependency_wait();                   // launched while the main kernel's last blocks still run
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NR = p.NR, slices = (p.Dv + 127) / 128;
-  int32_t skip = blockIdx.x;                // items before this block's next one
-  for (int32_t c0 = 0; c0 < blocks; c0 += 32) {
-    uint32_t has = __ballot_sync(0xffffffffu, c0 + lane < blocks && p.meta[8 * (c0 + lane)] != 0);
-    while (has) {
-      const int32_t c = c0 + __ffs(has) - 1;
-      has &= has - 1;
-      if (skip-- != 0) continue;
-      skip += gridDim.x;
-      const int32_t* mt = p.meta + 8 * c;
-      const int32_t first = mt[1], n = mt[2] - first + 1, rows0 = mt[3], rows1 = mt[4], kv_head = mt[7];
-      const bool few = n <= kJoinFew;
-      auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-      const int32_t units = (rows0 + rows1) * slices, group = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
-      const int32_t groups = few ? gridDim.y * kJoinWarps : gridDim.y;
-      for (int32_t unit = group; unit < units; unit += groups) {
-        int32_t r = unit / slices;
-        const int32_t ch = (unit - r * slices) * 128 + lane * 4;
-        const int32_t in = r < rows0 ? r : r - rows0;      // row of its subtile
-        const int32_t t = in / p.hb, h = in - t * p.hb;
-        const int64_t token = mt[5] + (r < rows0 ? 0 : p.tb) + t, head = mt[6] + h;
-        r = r < rows0 ? r : p.sub + in;
-        // every lane holds the statistics of pieces lane, lane + 32, ...
-        float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
-        float4 st[kJoinLoads];
+  uint32_t has[kJoinLoads];
 #pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
-          if (32 * i < n && 32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + r];
-          m = fmaxf(m, st[i].x);
-          if (st[i].y > 0.f) k0 = st[i].z;  // the same in every piece that saw a key
-        }
+  for (int i = 0; i < kJoinLoads; ++i) has[i] = 32 * i + lane < blocks && p.meta[8 * (32 * i + lane)] != 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+  for (int i = 0; i < kJoinLoads; ++i) has[i] = __ballot_sync(0xffffffffu, has[i]);
+  for (int32_t x = blockIdx.x;; x += gridDim.x) {
+    int32_t c = -1, skip = x;               // the x-th flagged block
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      const int32_t here = __popc(has[i]);
+      if (c < 0 && skip < here) c = 32 * i + __fns(has[i], 0, skip + 1);
+      skip -= here;
+    }
+    if (c < 0) return;
+    const int32_t* mt = p.meta + 8 * c;
+    const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3] + mt[4], kv_head = mt[7];
+    auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+    if (n <= kJoinFew) {
+      const int32_t units = (rows + 3) / 4 * slices;
+      for (int32_t unit = blockIdx.y * kJoinWarps + warp; unit < units; unit += gridDim.y * kJoinWarps) {
+        const int32_t r0 = unit / slices * 4, ch = (unit % slices) * 128 + lane * 4;
+        const int32_t mine = r0 + (lane >> 3), piece = lane & 7;
+        float4 st = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+        JoinRow row = join_row(p, mt, min(mine, rows - 1));
+        if (mine < rows && piece < n) st = p.stats[slot(piece) * NR + row.part];
+        float m = st.x, k0 = st.y > 0.f ? st.z : neg_inf();  // the same in every piece that saw a key
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
         }
+        const float wt = st.y > 0.f ? ex2(st.x - m) : 0.f;
+        float l = st.y * wt;
 #pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
-          l = fmaf(st[i].y, wt[i], l);
-        }
+        for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (piece == 0 && mine < rows && unit % slices == 0 && p.lse) join_lse(p, row, m, l, k0);
+        float4 acc[4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int32_t i = 0; i < n; ++i) {
+          float4 v[4];
+          float w[4];
 #pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          if (32 * i >= n) break;
-#pragma unroll 4
-          for (int e = few ? 0 : warp; e < 32; e += few ? 1 : kJoinWarps) {
-            const float weight = __shfl_sync(0xffffffffu, wt[i], e);
-            if (weight == 0.f || ch >= p.Dv) continue;  // a piece that saw nothing stored no accumulator
-            const float4 x = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + r) * p.Dv + ch);
-            acc.x = fmaf(x.x, weight, acc.x);
-            acc.y = fmaf(x.y, weight, acc.y);
-            acc.z = fmaf(x.z, weight, acc.z);
-            acc.w = fmaf(x.w, weight, acc.w);
+          for (int t = 0; t < 4; ++t) {
+            w[t] = __shfl_sync(0xffffffffu, wt, 8 * t + i);
+            const int32_t part = __shfl_sync(0xffffffffu, row.part, 8 * t);
+            v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[t] != 0.f && ch < p.Dv)   // a piece that saw nothing stored no accumulator
+              v[t] = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + part) * p.Dv + ch);
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            acc[t].x = fmaf(v[t].x, w[t], acc[t].x);
+            acc[t].y = fmaf(v[t].y, w[t], acc[t].y);
+            acc[t].z = fmaf(v[t].z, w[t], acc[t].z);
+            acc[t].w = fmaf(v[t].w, w[t], acc[t].w);
           }
         }
-        if (!few) {
-          sum[warp][lane] = acc;
-          __syncthreads();
-          acc = sum[0][lane];
 #pragma unroll
-          for (int i = 1; i < kJoinWarps; ++i) {
-            const float4 x = sum[i][lane];
-            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
-          }
-          __syncthreads();
-        }
-        if (few || warp == 0) {
-          if (lane == 0 && ch < 128 && p.lse)
-            p.lse[token * p.heads + head] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-          if (ch < p.Dv) {
-            if (p.v_scale) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 so = channel_quant(p.v_scale, p.v_offset, (p.per_head ? kv_head * p.Dv : 0) + ch + e, p.v_scalar);
-                y[e] = l > 0.f ? (y[e] - so.y) / so.x : 0.f;
-              }
-            }
-            uint2 w;
-            w.x = pack_half2<!F16>(y[0], y[1]);
-            w.y = pack_half2<!F16>(y[2], y[3]);
-            *reinterpret_cast<uint2*>(p.out + token * p.o_ts + head * p.o_hs + ch) = w;
-          }
+        for (int t = 0; t < 4; ++t) {
+          const float lt = __shfl_sync(0xffffffffu, l, 8 * t);
+          JoinRow rt;
+          rt.token = __shfl_sync(0xffffffffu, row.token, 8 * t);
+          rt.head = __shfl_sync(0xffffffffu, row.head, 8 * t);
+          if (r0 + t < rows && ch < p.Dv) join_store<F16>(p, rt, kv_head, ch, acc[t], lt);
         }
       }
+      continue;
+    }
+    for (int32_t unit = blockIdx.y; unit < rows * slices; unit += gridDim.y) {
+      const int32_t ch = (unit % slices) * 128 + lane * 4;
+      const JoinRow row = join_row(p, mt, unit / slices);
+      // every lane holds the statistics of pieces lane, lane + 32, ...
+      float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
+      float4 st[kJoinLoads];
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+        if (32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + row.part];
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        m = fmaxf(m, st[i].x);
+        if (st[i].y > 0.f) k0 = st[i].z;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
+        l = fmaf(st[i].y, wt[i], l);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        if (32 * i >= n) break;
+        float4 v[4];
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = warp + kJoinWarps * k;
+          w[k] = __shfl_sync(0xffffffffu, wt[i], e);
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w[k] != 0.f && ch < p.Dv)
+            v[k] = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + row.part) * p.Dv + ch);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc.x = fmaf(v[k].x, w[k], acc.x);
+          acc.y = fmaf(v[k].y, w[k], acc.y);
+          acc.z = fmaf(v[k].z, w[k], acc.z);
+          acc.w = fmaf(v[k].w, w[k], acc.w);
+        }
+      }
+      sum[warp][lane] = acc;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int i = 1; i < kJoinWarps; ++i) {
+          const float4 v = sum[i][lane];
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        if (lane == 0 && ch < 128 && p.lse) join_lse(p, row, m, l, k0);
+        if (ch < p.Dv) join_store<F16>(p, row, kv_head, ch, acc, l);
+      }
+      __syncthreads();
     }
   }
 }

@@ -14,6 +14,8 @@
 namespace ra {
 namespace {
 
+constexpr int64_t kKeysInL2 = 48 << 20;     // of the 126 MB
+
 // [tokens, heads, d] with any strides as a 3-D map of 64 x 128-token boxes; the axis with
 // the smaller stride comes second
 bool make_view_map(CUtensorMap* m, const uint16_t* base, int64_t tokens, int64_t heads, int32_t d, int64_t ts, int64_t hs,
@@ -76,10 +78,15 @@ cudaError_t launch_packed_attention(const PackedLaunch& L, cudaStream_t stream, 
   p.total_q = static_cast<int32_t>(L.total_q);
   p.total_k = static_cast<int32_t>(L.total_k);
   p.items = L.nq;
+  // Keys and values that stay in L2: the heads of a row block one after another, so that its
+  // rows of q and out, a token's heads side by side, pass HBM in long stretches.  Otherwise
+  // the row blocks of a head, which share its keys.
+  p.heads_first = L.total_k * L.nkv * L.d * 4 <= kKeysInL2;
   p.g = L.nq / L.nkv;
   p.Dk = L.d;
   p.ksteps = L.d / 16;
   p.causal = L.causal;
+  p.out32 = (reinterpret_cast<uintptr_t>(L.out) & 31u) == 0 && p.join.o_ts % 16 == 0 && p.join.o_hs % 16 == 0;
   p.scale = L.scale;
   p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);

@@ -81,6 +81,7 @@ cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const c
   p.box_rows = 1 << p.box_shift;
   p.kq = L.kq;
   p.vq = L.vq;
+  p.out32 = (reinterpret_cast<uintptr_t>(L.out) & 31u) == 0 && p.join.o_ts % 16 == 0 && p.join.o_hs % 16 == 0;
   p.scale = L.scale;
   p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);

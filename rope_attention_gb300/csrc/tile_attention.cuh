@@ -13,7 +13,9 @@
 //   their O (128 each).
 //
 // Warps 0-3 and 4-7: softmax of the two row tiles, one row per thread, which also rescale
-// and write O; warp 8: TMA; warp 9: MMA; with quantised caches warps 12-15 convert codes.
+// and write O; warp 8: TMA; warp 9: MMA; warp 10 finds the block's pieces (a walk over the
+// sequences' lengths, full of loads and divisions) ahead of the others and hands them over
+// in shared memory; with quantised caches warps 12-15 convert codes.
 // The running maximum follows only when a tile exceeds it by 2^kLazy (the factor cancels
 // between the weighted sum and the sum of weights), so O is rescaled in the first few tiles
 // of a piece and hardly ever after.  Quantised keys and values enter the products as codes,
@@ -41,6 +43,18 @@ constexpr float kTileLazy = 8.f;            // log2 of how far a tile may exceed
 constexpr uint64_t kTileDrainNs = 200000000ull;
 constexpr int kTileValid = 16;              // > key tiles between the loads and the softmax
 constexpr int kTileMinRun = 4;              // key tiles per block below which a cut costs more than it gives
+constexpr int kTilePieces = 4;              // pieces handed over ahead
+// What an item costs beside its key tiles (its queries' arrival, its rows' way out), in key
+// tiles: they stand at the item's start in the line.
+constexpr int kTileExtra = 2;
+// Items per block from which blocks take whole items: at most about a 16th is lost to uneven
+// ends, and nothing is joined.  With few sequences they take every G-th item, so that the
+// blocks are at one head or two at a time and read its keys from L2 together (480p
+// self-attention: STRIDED ms; 17.3 with runs cut anywhere, whose blocks stream 40 heads' keys
+// from HBM, which costs the tensor core power as well as time); over many sequences, each of
+// which a strided walk would have to look up, they take consecutive ones.
+constexpr int kTileWholeItems = 16, kTileStrideSeqs = 64;
+enum TileRuns : int32_t { kRunsCut = 0, kRunsWhole = 1, kRunsStrided = 2 };
 
 struct TileParams {
   CUtensorMap tq, tk, tv;
@@ -53,11 +67,14 @@ struct TileParams {
   int64_t table_stride, cap, block_num, cache_seq;
   int32_t B, total_q, total_k;
   int32_t items;                            // heads an item can have: query heads (packed), kv heads (paged)
+  int32_t heads_first;                      // the line's order within a sequence: heads within row blocks (1), or
+                                            // row blocks within heads (0)
   int32_t g;                                // query heads per kv head
   int32_t Dk, ksteps;
   int32_t causal, mode, block_size, bs_shift, box_rows, box_shift;
   int32_t q_swap, k_swap, v_swap;           // packed: the map's axes are (channels, tokens, heads)
   int32_t kq, vq;
+  int32_t out32;                            // every row of out starts on 32 bytes
   float scale, sl2;                         // softmax scale, and with log2(e)
   uint64_t wait_ns;
   int32_t stall_loads;
@@ -84,19 +101,6 @@ struct TileShape {
   static constexpr int kOffMisc = kOffCode + kNsg * kCode;
   static_assert(kNk >= 1 && kNv >= 1, "shared memory budget");
 };
-struct TileMisc {
-  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], c_full[2], c_empty[2];
-  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_ready[2], o_done[2], drain;
-  uint64_t valid[kTileValid][2];
-  int64_t scan[16], scan_items[16];
-  int64_t start_off;
-  int32_t start_b;
-  uint32_t tmem;
-  int32_t abort;
-  int32_t pad;
-  float inv_scale[2][192];                  // 1 / the key's scales, for each softmax group
-};
-
 __device__ __forceinline__ void tile_span(const int32_t* cu, int32_t b, int32_t B, int32_t total, int32_t& start,
                                           int32_t& len) {
   if (cu == nullptr) {
@@ -110,22 +114,27 @@ __device__ __forceinline__ void tile_span(const int32_t* cu, int32_t b, int32_t 
 }
 
 // Key tiles that block b of a sequence's rows counts for in the line: q0 + step (b + 1)
-// between 1 and most (step 0: most).  Packed causal prompts have step 2: 256 rows see 256
+// between 1 and most (step 0: most), and kTileExtra.  Packed causal prompts have step 2: 256 rows see 256
 // keys more than the 256 before them.
 struct TileCount {
   int32_t blocks, q0, step, most;
-  __device__ __forceinline__ int32_t of(int32_t b) const { return step == 0 ? most : max(1, min(most, q0 + step * (b + 1))); }
+  __device__ __forceinline__ int32_t of(int32_t b) const {
+    return kTileExtra + (step == 0 ? most : max(1, min(most, q0 + step * (b + 1))));
+  }
   // of the first n blocks
   __device__ int64_t sum(int32_t n) const {
-    if (step == 0) return static_cast<int64_t>(n) * most;
+    const int64_t extra = static_cast<int64_t>(n) * kTileExtra;
+    if (step == 0) return extra + static_cast<int64_t>(n) * most;
     const int32_t lo = min(n, max(0, (1 - q0 + step - 1) / step - 1));       // blocks that count 1
     const int32_t hi = max(lo, min(n, max(0, (most - q0 + step - 1) / step - 1)));  // and those below `most`
     const int64_t mid = hi - lo;
-    return lo + mid * q0 + step * ((static_cast<int64_t>(lo) + 1 + hi) * mid / 2) + static_cast<int64_t>(n - hi) * most;
+    return extra + lo + mid * q0 + step * ((static_cast<int64_t>(lo) + 1 + hi) * mid / 2) + static_cast<int64_t>(n - hi) * most;
   }
 };
 
 struct TilePiece {
+  int32_t end;                              // there is no further piece
+  int32_t first;                            // the first of its block
   int32_t b, head, kv_head, tok, q_start, Lq, k_start, Lk;
   int32_t rows[2];                          // of the two row tiles
   int32_t t0, take, T;                      // tiles [t0, t0 + take) of the item's T in the line
@@ -134,10 +143,28 @@ struct TilePiece {
   __device__ __forceinline__ int32_t n(int i) const { return max(0, tb[i] - ta); }
 };
 
+struct TileMisc {
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], c_full[2], c_empty[2];
+  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t piece_full[kTilePieces], piece_empty[kTilePieces];
+  uint64_t valid[kTileValid][2];
+  TilePiece pieces[kTilePieces];
+  int64_t scan[16], scan_items[16];
+  int64_t start_off;
+  int32_t start_b;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t pad;
+  float inv_scale[2][192];                  // 1 / the key's scales, for each softmax group
+};
+
 template <int KT, bool PAGED>
 struct TileWalk {
   int32_t b, item, blk, t;                  // next: sequence, head, row block, key tile
   int64_t rem;
+  TilePiece w;                              // of the sequence that c is of: its spans
+  TileCount c;
+  int32_t runs;                             // TileRuns
 
   __device__ static TileCount count(const TileParams& p, int32_t b, TilePiece& w) {
     tile_span(p.cu_q, b, p.B, p.total_q, w.q_start, w.Lq);
@@ -155,70 +182,125 @@ struct TileWalk {
     c.q0 = w.Lk >= w.Lq ? (w.Lk - w.Lq + KT - 1) / KT : -((w.Lq - w.Lk) / KT);
     return c;
   }
-  __device__ static int64_t work(const TileParams& p, int32_t b, int64_t* items = nullptr) {
+  __device__ static int64_t work(const TileParams& p, int32_t b, int64_t* items) {
     TilePiece w;
     const TileCount c = count(p, b, w);
-    if (items) *items += static_cast<int64_t>(c.blocks) * p.items;
+    *items += static_cast<int64_t>(c.blocks) * p.items;
     return c.sum(c.blocks) * p.items;
   }
-  // to offset `off` of sequence b
-  __device__ void seek(const TileParams& p, int32_t seq, int64_t off, int64_t run) {
-    TilePiece w;
+  // to offset `off` of sequence b, for `run` tiles
+  __device__ void seek(const TileParams& p, int32_t seq, int64_t off, int64_t run, int32_t kind) {
     b = seq;
     rem = run;
-    const TileCount c = count(p, b, w);
-    const int64_t per_head = c.sum(c.blocks);
-    item = static_cast<int32_t>(off / per_head);
-    off -= item * per_head;
+    runs = kind;
+    if (runs == kRunsStrided) {             // the block's first item is item blockIdx.x of all
+      b = 0;
+      rem = 1;
+      t = item = blk = 0;
+      c = count(p, b, w);
+      skip(p, blockIdx.x);
+      return;
+    }
+    c = count(p, b, w);
+    const int64_t per_head = c.sum(c.blocks), each = p.heads_first ? p.items : 1;
+    if (!p.heads_first) {
+      item = static_cast<int32_t>(off / per_head);
+      off -= item * per_head;
+    }
     int32_t lo = 0, hi = c.blocks - 1;      // the last block that begins at or before off
     while (lo < hi) {
       const int32_t mid = (lo + hi + 1) / 2;
-      if (c.sum(mid) <= off) lo = mid;
+      if (c.sum(mid) * each <= off) lo = mid;
       else hi = mid - 1;
     }
     blk = lo;
-    t = static_cast<int32_t>(off - c.sum(lo));
-  }
-  __device__ bool next(const TileParams& p, TilePiece& w) {
-    while (rem > 0 && b < p.B) {
-      const TileCount c = count(p, b, w);
-      if (c.blocks == 0) {
-        ++b;
-        continue;
-      }
-      const int32_t T = c.of(blk);
-      w.b = b;
-      w.T = T;
-      w.t0 = t;
-      w.take = static_cast<int32_t>(min(static_cast<int64_t>(T - t), rem));
-      w.kv_head = PAGED ? item : item / p.g;
-      w.head = PAGED ? item * p.g : item;
-      w.tok = blk * 2 * p.join.tb;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int32_t first = w.tok + i * p.join.tb, tokens = max(0, min(p.join.tb, w.Lq - first));
-        const int32_t seen = p.causal ? min(w.Lk, max(0, first + tokens + w.Lk - w.Lq)) : w.Lk;
-        w.rows[i] = tokens * p.join.hb;
-        w.tb[i] = tokens == 0 ? 0 : min(w.t0 + w.take, (seen + KT - 1) / KT);
-      }
-      w.ta = w.t0;
-      rem -= w.take;
-      t += w.take;
-      if (t == T) {
-        t = 0;
-        if (++blk == c.blocks) {
-          blk = 0;
-          if (++item == p.items) {
-            item = 0;
-            ++b;
-          }
-        }
-      }
-      return true;
+    off -= c.sum(lo) * each;
+    if (p.heads_first) {
+      item = static_cast<int32_t>(off / c.of(blk));
+      off -= static_cast<int64_t>(item) * c.of(blk);
     }
-    return false;
+    t = static_cast<int32_t>(off);
+    if (runs == kRunsWhole && t > 0) {      // an item that the block before began
+      rem -= c.of(blk) - t;
+      advance(p);
+    }
+  }
+  // n items on
+  __device__ void skip(const TileParams& p, int64_t n) {
+    n += p.heads_first ? static_cast<int64_t>(blk) * p.items + item : static_cast<int64_t>(item) * c.blocks + blk;
+    while (n >= static_cast<int64_t>(p.items) * c.blocks) {
+      n -= static_cast<int64_t>(p.items) * c.blocks;
+      if (++b >= p.B) return;
+      c = count(p, b, w);
+    }
+    const uint32_t inner = p.heads_first ? p.items : c.blocks;  // n < items * blocks < 2^31
+    const int32_t outer = static_cast<int32_t>(static_cast<uint32_t>(n) / inner);
+    const int32_t rest = static_cast<int32_t>(n - static_cast<int64_t>(outer) * inner);
+    blk = p.heads_first ? outer : rest;
+    item = p.heads_first ? rest : outer;
+  }
+  __device__ void advance(const TileParams& p) {
+    t = 0;
+    if (runs == kRunsStrided) {
+      skip(p, gridDim.x);
+      return;
+    }
+    if (p.heads_first) {
+      if (++item < p.items) return;
+      item = 0;
+      if (++blk < c.blocks) return;
+      blk = 0;
+    } else {
+      if (++blk < c.blocks) return;
+      blk = 0;
+      if (++item < p.items) return;
+      item = 0;
+    }
+    do {
+      if (++b >= p.B) return;
+      c = count(p, b, w);
+    } while (c.blocks == 0);
+  }
+  // the next piece into w
+  __device__ bool next(const TileParams& p) {
+    if (rem <= 0 || b >= p.B) return false;
+    const int32_t T = c.of(blk);
+    w.b = b;
+    w.T = T;
+    w.t0 = t;
+    w.take = runs != kRunsCut ? T : static_cast<int32_t>(min(static_cast<int64_t>(T - t), rem));
+    w.kv_head = PAGED ? item : static_cast<int32_t>(static_cast<uint32_t>(item) / static_cast<uint32_t>(p.g));
+    w.head = PAGED ? item * p.g : item;
+    w.tok = blk * 2 * p.join.tb;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t first = w.tok + i * p.join.tb, tokens = max(0, min(p.join.tb, w.Lq - first));
+      const int32_t seen = p.causal ? min(w.Lk, max(0, first + tokens + w.Lk - w.Lq)) : w.Lk;
+      w.rows[i] = tokens * p.join.hb;
+      w.tb[i] = tokens == 0 ? 0 : min(w.t0 + w.take - kTileExtra, (seen + KT - 1) / KT);
+    }
+    w.ta = max(0, w.t0 - kTileExtra);
+    if (runs != kRunsStrided) rem -= w.take;
+    t += w.take;
+    return true;
+  }
+  __device__ void done(const TileParams& p) {  // with the piece that next gave
+    if (t == w.T) advance(p);
   }
 };
+
+// The next piece that warp 10 handed over, for a whole warp; false at the end or when a wait
+// gave up.
+__device__ __forceinline__ bool take_piece(TileMisc& ms, Ring& ring, TilePiece& w, uint64_t limit, volatile int* abort_flag,
+                                           bool& ok) {
+  ok = ok && bounded_wait_warp(smem_u32(&ms.piece_full[ring.stage]), ring.parity, limit, abort_flag);
+  if (!ok) return false;
+  w = ms.pieces[ring.stage];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms.piece_empty[ring.stage]));
+  ring.next(kTilePieces);
+  return !w.end;
+}
 
 // whether all 128 threads of a softmax group are well
 __device__ __forceinline__ bool group_ok(uint32_t id, bool ok) {
@@ -242,9 +324,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   using SH = TileShape<KS, VS, KT, QUANT>;
   constexpr bool P16 = F16 || QUANT;
   // Registers per thread: launched with 168 (QUANT: 128) each, then moved to the softmax:
-  // 2 x 208 + 88 = 3 x 168; 2 x 192 + 64 + 64 = 4 x 128
-  constexpr int kRegsSoftmax = QUANT ? 192 : 208, kRegsRest = QUANT ? 64 : 88;
-  constexpr int kTmaWarp = 8, kMmaWarp = 9, kConvert0 = 12;
+  // 2 x 216 + 72 = 3 x 168; 2 x 192 + 64 + 64 = 4 x 128
+  constexpr int kRegsSoftmax = QUANT ? 192 : 216, kRegsRest = QUANT ? 64 : 72;
+  constexpr int kTmaWarp = 8, kMmaWarp = 9, kPieceWarp = 10, kConvert0 = 12;
   extern __shared__ __align__(1024) uint8_t smem[];
   TileMisc& ms = *reinterpret_cast<TileMisc*>(smem + SH::kOffMisc);
   const uint32_t s0 = smem_u32(smem);
@@ -286,6 +368,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       mbar_init(smem_u32(&ms.p_ready[i]), 4);
       mbar_init(smem_u32(&ms.o_done[i]), 1);
     }
+    for (int i = 0; i < kTilePieces; ++i) {
+      mbar_init(smem_u32(&ms.piece_full[i]), 1);
+      mbar_init(smem_u32(&ms.piece_empty[i]), QUANT ? 14 : 10);  // the warps that read a piece
+    }
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
     fence_mbar_init();
@@ -307,6 +393,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   const int64_t G = gridDim.x;
   int64_t per = (W + G - 1) / G;
   if (per < kTileMinRun && items > 0) per = max(per, min(static_cast<int64_t>(kTileMinRun), (W + items - 1) / items));
+  const int32_t runs = items < kTileWholeItems * G ? kRunsCut : p.B <= kTileStrideSeqs ? kRunsStrided : kRunsWhole;
   const int64_t start = per * blockIdx.x;
   grid_launch_dependents();
   if (threadIdx.x == 0) p.join.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
@@ -314,7 +401,8 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   if (before <= start && start < before + mine) {
     int32_t b = b_lo;
     int64_t off = start - before;
-    for (int64_t w; b < b_hi && off >= (w = Walk::work(p, b)); ++b) off -= w;
+    int64_t unused = 0;
+    for (int64_t w; b < b_hi && off >= (w = Walk::work(p, b, &unused)); ++b) off -= w;
     ms.start_b = b;
     ms.start_off = off;
   }
@@ -327,13 +415,31 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
   volatile int* abort_flag = &ms.abort;
-  Walk walk;
-  walk.seek(p, ms.start_b, ms.start_off, min(per, W - start));
   TilePiece w{};
+  Ring pieces;
 
   if (warp >= 8 && warp < 12) {
     set_max_regs_dec<kRegsRest>();
-    if (warp == kTmaWarp && !p.stall_loads) {
+    if (warp == kPieceWarp) {
+      // ------------------------------------------------------------ pieces
+      Walk walk;
+      walk.seek(p, ms.start_b, ms.start_off, min(per, W - start), runs);
+      bool more = true, first = true;
+      while (more) {
+        more = walk.next(p);
+        walk.w.end = more ? 0 : 1;
+        walk.w.first = first ? 1 : 0;
+        first = false;
+        if (!bounded_wait_warp(smem_u32(&ms.piece_empty[pieces.stage]), pieces.parity ^ 1u, p.wait_ns, abort_flag)) break;
+        if (lane == 0) {
+          ms.pieces[pieces.stage] = walk.w;
+          mbar_arrive(smem_u32(&ms.piece_full[pieces.stage]));
+        }
+        __syncwarp();
+        pieces.next(kTilePieces);
+        if (more) walk.done(p);
+      }
+    } else if (warp == kTmaWarp && !p.stall_loads) {
       // ------------------------------------------------------------ loads
       const int groups = PAGED ? KT >> p.box_shift : 1;
       const int per_trip = PAGED ? 32 / groups * groups : 32;
@@ -346,26 +452,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         armed |= 1u << st;
         par = (par & ~(1u << st)) | (parity << st);
       };
-      while (ok && walk.next(p, w)) {
+      while (take_piece(ms, pieces, w, p.wait_ns, abort_flag, ok)) {
         const int32_t t_end = max(w.tb[0], w.tb[1]);
         if (w.ta >= t_end) continue;
-        for (int i = 0; ok && i < 2; ++i) {
-          if (w.n(i) == 0) continue;
-          ok = bounded_wait_warp(smem_u32(&ms.q_empty[i]), q_par[i] ^ 1u, p.wait_ns, abort_flag);
-          if (!ok) break;
-          if (elect_one()) {
-            const uint32_t bar = smem_u32(&ms.q_full[i]);
-            const int32_t tok = w.q_start + w.tok + i * p.join.tb;
-            mbar_arrive_expect_tx(bar, KS * p.join.tb * p.join.hb * 128);
-#pragma unroll
-            for (int c = 0; c < KS; ++c)
-              tma_load_3d(s0 + i * SH::kQTile + c * kTileRows * 128, &p.tq, bar, 64 * c, p.q_swap ? tok : w.head,
-                          p.q_swap ? w.head : tok);
-          }
-          __syncwarp();
-          mark(armed_q, par_q, i, q_par[i]);
-          q_par[i] ^= 1u;
-        }
         // Cache rows: lane i holds where group `base + i` of the piece starts, per_trip groups
         // of box_rows keys per trip to the block table.
         int64_t row = -1;
@@ -398,6 +487,28 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           // 0: the key tile, 1: the value tile
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
+            if (side == 1 && t == w.ta) {
+              // the queries, once the products of the last ones are through with them: behind the
+              // first key tile, whose place in the ring is free earlier
+              for (int i = 0; ok && i < 2; ++i) {
+                if (w.n(i) == 0) continue;
+                ok = bounded_wait_warp(smem_u32(&ms.q_empty[i]), q_par[i] ^ 1u, p.wait_ns, abort_flag);
+                if (!ok) break;
+                if (elect_one()) {
+                  const uint32_t bar = smem_u32(&ms.q_full[i]);
+                  const int32_t tok = w.q_start + w.tok + i * p.join.tb;
+                  mbar_arrive_expect_tx(bar, KS * p.join.tb * p.join.hb * 128);
+      #pragma unroll
+                  for (int c = 0; c < KS; ++c)
+                    tma_load_3d(s0 + i * SH::kQTile + c * kTileRows * 128, &p.tq, bar, 64 * c, p.q_swap ? tok : w.head,
+                                p.q_swap ? w.head : tok);
+                }
+                __syncwarp();
+                mark(armed_q, par_q, i, q_par[i]);
+                q_par[i] ^= 1u;
+              }
+              if (!ok) break;
+            }
             const int st = side ? vr.stage : kr.stage;
             const uint32_t par = side ? vr.parity : kr.parity;
             if (QUANT)
@@ -494,7 +605,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         tc_commit(smem_u32(&ms.s_full[i]));
         if (last) tc_commit(smem_u32(&ms.q_empty[i]));
       };
-      while (ok && walk.next(p, w)) {
+      while (take_piece(ms, pieces, w, p.wait_ns, abort_flag, ok)) {
         const int32_t n0 = w.n(0), n1 = w.n(1), n = max(n0, n1);
         if (n == 0) continue;
         if (!wait(&ms.k_full[kr.stage], kr.parity)) break;
@@ -552,7 +663,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
     Ring kr, vr, cr;
     uint32_t u = 0;
     bool ok = !p.stall_loads;
-    while (ok && walk.next(p, w)) {
+    while (take_piece(ms, pieces, w, p.wait_ns, abort_flag, ok)) {
       const int32_t t_end = max(w.tb[0], w.tb[1]);
       for (int32_t t = w.ta; ok && t < t_end; ++t, ++u) {
 #pragma unroll 1
@@ -608,15 +719,14 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
     const uint32_t s_addr = tmem + 128 * i + lane_base, o_addr = tmem + 256 + 128 * i + lane_base;
     uint32_t s_par = 0, o_par = 0, q_par = 0, u = 0;
     Ring vr;
-    int32_t piece = 0;
     bool ok = true;
-    for (; ok && walk.next(p, w); ++piece) {
+    while (take_piece(ms, pieces, w, p.wait_ns, abort_flag, ok)) {
       const int32_t n = w.n(i), n_both = max(w.n(0), w.n(1));
       const bool live = row < w.rows[i];
       const int32_t in_tile = static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.join.hb));
       const int32_t tok = w.tok + i * p.join.tb + in_tile, head = w.head + row - in_tile * p.join.hb;
       const int32_t seen = !p.causal ? w.Lk : min(w.Lk, max(0, tok + 1 + w.Lk - w.Lq));
-      if (piece == 0 && threadIdx.x == 0 && w.t0 > 0) {
+      if (w.first && threadIdx.x == 0 && w.t0 > 0) {
         // the block behind the first cut through an item joins the item's pieces
         const int64_t item0 = start - w.t0;
         const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
@@ -630,6 +740,12 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         mt[7] = w.kv_head;
         mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
       }
+      // where the row goes
+      const bool whole = w.whole();
+      const int64_t token = w.q_start + tok;
+      const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + (w.first && w.t0 > 0 ? 0 : 1)) * 2 * kTileRows + i * kTileRows + row;
+      uint16_t* const dst = p.join.out + token * p.join.o_ts + head * p.join.o_hs;
+      float* const part = p.join.parts + part_row * p.join.Dv;
       float sl2 = p.sl2, shift = 0.f;
       if (QUANT && n > 0) {
         // The row of q over the key's scales, behind a power of two that keeps its elements
@@ -794,10 +910,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       u += n_both;
 
       // ---- final rows, or the piece's statistics and accumulator
-      const bool whole = w.whole();
-      const int64_t token = w.q_start + tok;
-      const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1)) * 2 * kTileRows + i * kTileRows + row;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l > 0.f ? rcp(l) : 0.f;
       if (live) {
         if (whole) {
           if (p.join.lse)
@@ -806,8 +919,6 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           p.join.stats[part_row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
         }
       }
-      uint16_t* dst = p.join.out + token * p.join.o_ts + head * p.join.o_hs;
-      float* part = p.join.parts + part_row * p.join.Dv;
       const bool store = live && (whole || n > 0);
 #pragma unroll 1
       for (int c = 0; c < VS * 64; c += 16) {
@@ -819,9 +930,8 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         if (!store) continue;
         if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(part + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          store_32(part + c, o);
+          store_32(part + c + 8, o + 8);
           continue;
         }
         float y[16];
@@ -833,11 +943,15 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = (y[e] - (vo ? __ldg(vo + e) : 0.f)) * rcp(__ldg(vs + e));
         }
+        uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 16; e += 8)
-          *reinterpret_cast<uint4*>(dst + c + e) =
-              make_uint4(pack_half2<!F16>(y[e], y[e + 1]), pack_half2<!F16>(y[e + 2], y[e + 3]),
-                         pack_half2<!F16>(y[e + 4], y[e + 5]), pack_half2<!F16>(y[e + 6], y[e + 7]));
+        for (int e = 0; e < 8; ++e) h[e] = pack_half2<!F16>(y[2 * e], y[2 * e + 1]);
+        if (p.out32) {
+          store_32(dst + c, h);
+        } else {
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
       }
       tc_fence_before();
     }
