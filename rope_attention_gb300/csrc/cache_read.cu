@@ -9,10 +9,15 @@
 //    element (fp32; at most 2^-24 (2 |x| + 3 |offset / scale|) off, far below the rounding
 //    to 16 bits);
 //  * a warp takes 4 tokens at once and spreads their rows' 8-channel units (8 or 16 bytes
-//    in, 16 out) over its lanes: four rows fill them where one would not (72 units in a
-//    576-channel row: 9 rounds of 32 instead of 12), and the slot lookups and the index
-//    arithmetic, done by one lane per token, are a small part;
+//    in, 16 out) over its lanes: four rows fill them where one would not (64 + 8 units in a
+//    latent and its rope part: 8 + 1 rounds of 32 lanes for four tokens, not 4 x 3), and the
+//    slot lookups and the index arithmetic, done by one lane per token a turn ahead, are a
+//    small part;
 //  * the loads of kBatch rounds are in flight together.
+// Measured (131072 rows of 512 int8 + 64 bf16 channels, 228 MB in all): 52 us, 4.3 TB/s, 64 %
+// of a plain copy's rate; a mapping of one row per warp took 86 us.  Half of the issue slots
+// are busy and DRAM at 40 % of its nominal rate: the latency of two dependent loads (slot,
+// then row) at four blocks an SM bounds it.  Five blocks spill and are no faster (53 us).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -27,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTokens = 4;      // tokens a warp takes at once
-constexpr int kBatch = 3;
+constexpr int kBatch = 4;
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 
 struct Side {                   // one of the two caches
   const uint8_t* cache;
@@ -36,128 +42,161 @@ struct Side {                   // one of the two caches
   int32_t width, kind, scalar, units;  // units of 8 channels per row
 };
 
-// the cache row of token (b, s) of head n; -1: none, -2: outside the cache
-__device__ __forceinline__ int64_t row_of(const ReadLaunch& L, int64_t b, int64_t n, int64_t s) {
+// quotient of two numbers that are not negative: a 64-bit division is a hundred instructions,
+// and few of these need it
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// A token's index entry, and the cache row of head n that it stands for (-1: none, -2:
+// outside the cache).
+struct Token {
+  int64_t b, s, entry;
+};
+__device__ __forceinline__ Token load_token(const ReadLaunch& L, int64_t t) {
+  Token k;
+  k.b = quotient(t, L.S);
+  k.s = t - k.b * L.S;
+  k.entry = __ldg(L.index + (L.mode == kModePaBlkBnsd ? k.b * quotient(L.S + L.block_size - 1, L.block_size) + quotient(k.s, L.block_size)
+                                                      : t));
+  return k;
+}
+__device__ __forceinline__ int64_t row_of(const ReadLaunch& L, const Token& k, int64_t n) {
   const int64_t bs = L.block_size;
-  if (L.mode == kModeNorm) {
-    const int64_t i = __ldg(L.index + b * L.S + s);
-    if (i == -1) return -1;
-    return i < 0 || i >= L.cache_seq ? -2 : (b * L.N + n) * L.cache_seq + i;
-  }
-  int64_t slot;
-  if (L.mode == kModePaBlkBnsd) {
-    const int64_t first = __ldg(L.index + b * ((L.S + bs - 1) / bs) + s / bs);
-    if (first == -1) return -1;
-    if (first < 0 || first >= L.block_num * bs) return -2;
-    slot = first + s % bs;
-  } else {
-    slot = __ldg(L.index + b * L.S + s);
-    if (slot == -1) return -1;
-  }
-  if (slot < 0 || slot >= L.block_num * bs) return -2;
-  const int64_t page = slot / bs, in = slot - page * bs;
-  return L.mode == kModePa ? slot * L.N + n : (page * L.N + n) * bs + in;
+  if (k.entry == -1) return -1;
+  if (L.mode == kModeNorm) return k.entry < 0 || k.entry >= L.cache_seq ? -2 : (k.b * L.N + n) * L.cache_seq + k.entry;
+  const int64_t slots = L.block_num * bs;
+  if (k.entry < 0 || k.entry >= slots) return -2;
+  const int64_t slot = k.entry + (L.mode == kModePaBlkBnsd ? k.s - quotient(k.s, bs) * bs : 0);
+  if (slot >= slots) return -2;
+  const int64_t page = quotient(slot, bs);
+  return L.mode == kModePa ? slot * L.N + n : (page * L.N + n) * bs + (slot - page * bs);
 }
 
 // 8 codes -> 8 floats
-__device__ __forceinline__ void codes_to_float(uint2 w, int32_t kind, float (&x)[8]) {
+__device__ __forceinline__ void codes_to_float(uint2 w, int32_t kind, float2 (&x)[4]) {
   const uint32_t v[2] = {w.x, w.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (kind == kQuantInt8) {
       // the byte code + 128 below the exponent of 2^23 is the float 2^23 + code + 128
       const uint32_t u = v[i] ^ 0x80808080u;
-      x[4 * i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.f;
-      x[4 * i + 1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.f;
-      x[4 * i + 2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.f;
-      x[4 * i + 3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.f;
+      const float2 bias = make_float2(-8388736.f, -8388736.f);
+      x[2 * i] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
+                                        __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), bias);
+      x[2 * i + 1] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
+                                            __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), bias);
     } else {
       const __nv_fp8_interpretation_t f = kind == kQuantE4m3 ? __NV_E4M3 : __NV_E5M2;
       const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v[i] & 0xFFFFu), f);
       const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v[i] >> 16), f);
-      x[4 * i] = __half2float(__ushort_as_half(lo.x));
-      x[4 * i + 1] = __half2float(__ushort_as_half(lo.y));
-      x[4 * i + 2] = __half2float(__ushort_as_half(hi.x));
-      x[4 * i + 3] = __half2float(__ushort_as_half(hi.y));
+      x[2 * i] = make_float2(__half2float(__ushort_as_half(lo.x)), __half2float(__ushort_as_half(lo.y)));
+      x[2 * i + 1] = make_float2(__half2float(__ushort_as_half(hi.x)), __half2float(__ushort_as_half(hi.y)));
     }
   }
 }
 
+// One cache's rows of a warp's tokens.  rows: per token its cache row and its row of the
+// output; place: for every (round, lane) its token (upper half) and unit; tab: the side's
+// quantisation, four arrays of a float4 per unit.
 template <bool F16>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadLaunch L,
+__device__ __forceinline__ void read_side(const Side& side, const int64_t (*rows)[2], const uint32_t* place,
+                                          const float4* tab, int lane) {
+  const int rounds = (kTokens * side.units + 31) / 32;
+  const bool codes = side.kind != kQuantNone;
+  for (int r0 = 0; r0 < rounds; r0 += kBatch) {
+    uint4 in[kBatch];
+    uint4* to[kBatch];
+    int32_t unit[kBatch];
+    bool have[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const uint32_t at = r0 + e < rounds ? place[(r0 + e) * 32 + lane] : kNowhere;
+      unit[e] = at & 0xFFFFu;
+      to[e] = nullptr;
+      have[e] = false;
+      in[e] = make_uint4(0, 0, 0, 0);
+      if (at == kNowhere) continue;
+      const longlong2 row = *reinterpret_cast<const longlong2*>(rows[at >> 16]);
+      if (row.y < 0) continue;
+      to[e] = reinterpret_cast<uint4*>(side.out + row.y * side.width) + unit[e];
+      have[e] = row.x >= 0;
+      if (!have[e]) continue;
+      if (codes) {
+        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(side.cache + row.x * side.width) + unit[e]);
+        in[e].x = x.x;
+        in[e].y = x.y;
+      } else {
+        in[e] = __ldcs(reinterpret_cast<const uint4*>(side.cache + row.x * side.width * 2) + unit[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (to[e] == nullptr) continue;
+      if (have[e] && codes) {
+        float2 x[4];
+        codes_to_float(make_uint2(in[e].x, in[e].y), side.kind, x);
+        const float4* t = tab + unit[e];
+        const float4 ra = t[0], rb = t[side.units], ta = t[2 * side.units], tb = t[3 * side.units];
+        x[0] = __ffma2_rn(x[0], make_float2(ra.x, ra.y), make_float2(ta.x, ta.y));
+        x[1] = __ffma2_rn(x[1], make_float2(ra.z, ra.w), make_float2(ta.z, ta.w));
+        x[2] = __ffma2_rn(x[2], make_float2(rb.x, rb.y), make_float2(tb.x, tb.y));
+        x[3] = __ffma2_rn(x[3], make_float2(rb.z, rb.w), make_float2(tb.z, tb.w));
+        in[e] = make_uint4(pack_half2<!F16>(x[0].x, x[0].y), pack_half2<!F16>(x[1].x, x[1].y),
+                           pack_half2<!F16>(x[2].x, x[2].y), pack_half2<!F16>(x[3].x, x[3].y));
+      }
+      __stcs(to[e], in[e]);
+    }
+  }
+}
+
+// the side's table of head n, and its places
+__device__ __forceinline__ void set_up(const Side& side, int32_t head, bool per_head, float4* tab, uint32_t* place) {
+  for (int i = threadIdx.x; side.kind != kQuantNone && i < side.width; i += kThreads) {
+    const int at = side.scalar ? 0 : (per_head ? head * side.width : 0) + i;
+    const float r = __frcp_rn(__ldg(side.scale + at));
+    float* const t = reinterpret_cast<float*>(tab + ((i >> 2) & 1) * side.units + (i >> 3)) + (i & 3);
+    t[0] = r;
+    t[8 * side.units] = side.offset ? -__ldg(side.offset + at) * r : 0.f;
+  }
+  for (int i = threadIdx.x; i < (kTokens * side.units + 31) / 32 * 32; i += kThreads) {
+    const int token = i / side.units;
+    place[i] = token < kTokens ? (token << 16) | (i - token * side.units) : kNowhere;
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_constant__ ReadLaunch L,
                                                               const __grid_constant__ Side k,
                                                               const __grid_constant__ Side v) {
-  extern __shared__ float4 table[];          // r, then t, of the k units and the v units: 2 + 2 float4 a unit
+  extern __shared__ float4 shared[];
+  __shared__ __align__(16) int64_t rows[kWarps][kTokens][2];
   const int64_t n = blockIdx.y;
-  const int units = k.units + v.units, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < units * 8; i += kThreads) {
-    const bool is_k = i < k.units * 8;
-    const Side& side = is_k ? k : v;
-    if (side.kind == kQuantNone) continue;
-    const int c = is_k ? i : i - k.units * 8;
-    const int at = side.scalar ? 0 : (L.variant == 2 ? static_cast<int>(n) * side.width : 0) + c;
-    const float r = __frcp_rn(__ldg(side.scale + at));
-    float* row = reinterpret_cast<float*>(table) + (i >> 3) * 16;
-    row[i & 7] = r;
-    row[8 + (i & 7)] = side.offset ? -__ldg(side.offset + at) * r : 0.f;
-  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float4 *const k_tab = shared, *const v_tab = k_tab + 4 * k.units;
+  uint32_t* const k_place = reinterpret_cast<uint32_t*>(v_tab + 4 * v.units);
+  uint32_t* const v_place = k_place + (kTokens * k.units + 31) / 32 * 32;
+  if (k.units) set_up(k, static_cast<int32_t>(n), L.variant == 2, k_tab, k_place);
+  if (v.units) set_up(v, static_cast<int32_t>(n), L.variant == 2, v_tab, v_place);
   __syncthreads();
   const int64_t tokens = L.B * L.S, step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
-  const int rounds = (kTokens * units + 31) / 32;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens; t0 < tokens; t0 += step) {
-    // one lane per token: its cache row and its row of the output
-    int64_t row = -1, out = -1;
-    if (lane < kTokens && t0 + lane < tokens) {
-      const int64_t t = t0 + lane, b = t / L.S, s = t - b * L.S;
-      row = row_of(L, b, n, s);
-      out = (b * L.N + n) * L.S + s;
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens;
+  Token next{0, 0, -1};                      // one lane per token; its entry is on the way a turn ahead
+  if (lane < kTokens && t0 + lane < tokens) next = load_token(L, t0 + lane);
+  for (; t0 < tokens; t0 += step) {
+    if (lane < kTokens) {
+      const Token token = next;
+      const bool real = t0 + lane < tokens;
+      const int64_t row = real ? row_of(L, token, n) : -1;
       if (row == -2 && n == 0 && L.err_count) atomicAdd(L.err_count, 1);
+      rows[warp][lane][0] = row;
+      rows[warp][lane][1] = real ? (token.b * L.N + n) * L.S + token.s : -1;
+      if (t0 + step + lane < tokens) next = load_token(L, t0 + step + lane);
     }
-    for (int r0 = 0; r0 < rounds; r0 += kBatch) {
-      uint4 in[kBatch];
-      int64_t to[kBatch];
-      int32_t unit[kBatch];
-      bool have[kBatch];
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const int i = (r0 + e) * 32 + lane, token = min(i / units, kTokens - 1);
-        unit[e] = i - token * units;
-        const int64_t from = __shfl_sync(0xffffffffu, row, token);
-        to[e] = __shfl_sync(0xffffffffu, out, token);
-        if (i >= kTokens * units) to[e] = -1;
-        in[e] = make_uint4(0, 0, 0, 0);
-        have[e] = to[e] >= 0 && from >= 0;
-        if (have[e]) {
-          const bool is_k = unit[e] < k.units;
-          const Side& side = is_k ? k : v;
-          const int64_t at = from * side.width + (is_k ? unit[e] : unit[e] - k.units) * 8;
-          if (side.kind == kQuantNone) {
-            in[e] = __ldcs(reinterpret_cast<const uint4*>(side.cache + at * 2));
-          } else {
-            const uint2 x = __ldcs(reinterpret_cast<const uint2*>(side.cache + at));
-            in[e].x = x.x;
-            in[e].y = x.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        if (to[e] < 0) continue;
-        const bool is_k = unit[e] < k.units;
-        const Side& side = is_k ? k : v;
-        if (have[e] && side.kind != kQuantNone) {
-          float x[8];
-          codes_to_float(make_uint2(in[e].x, in[e].y), side.kind, x);
-          const float4* tab = table + unit[e] * 4;
-          const float4 ra = tab[0], rb = tab[1], ta = tab[2], tb = tab[3];
-          in[e].x = pack_half2<!F16>(fmaf(x[0], ra.x, ta.x), fmaf(x[1], ra.y, ta.y));
-          in[e].y = pack_half2<!F16>(fmaf(x[2], ra.z, ta.z), fmaf(x[3], ra.w, ta.w));
-          in[e].z = pack_half2<!F16>(fmaf(x[4], rb.x, tb.x), fmaf(x[5], rb.y, tb.y));
-          in[e].w = pack_half2<!F16>(fmaf(x[6], rb.z, tb.z), fmaf(x[7], rb.w, tb.w));
-        }
-        __stcs(reinterpret_cast<uint4*>(side.out + to[e] * side.width + (is_k ? unit[e] : unit[e] - k.units) * 8), in[e]);
-      }
-    }
+    __syncwarp();
+    if (v.units) read_side<F16>(v, rows[warp], v_place, v_tab, lane);
+    if (k.units) read_side<F16>(k, rows[warp], k_place, k_tab, lane);
+    __syncwarp();
   }
 }
 
@@ -168,9 +207,10 @@ cudaError_t launch_cache_read(const ReadLaunch& L, cudaStream_t stream) {
          L.k_out ? L.kw / 8 : 0};
   Side v{static_cast<const uint8_t*>(L.v_cache), L.v_scale, L.v_offset, L.v_out, L.vw, L.vq, L.v_scalar,
          L.v_out ? L.vw / 8 : 0};
-  const int smem = (k.units + v.units) * 64;  // at most 16 KB
+  const int units = k.units + v.units;
+  const int smem = units * 64 + ((kTokens * k.units + 31) / 32 + (kTokens * v.units + 31) / 32) * 128;  // at most 20 KB
   const int64_t groups = (L.B * L.S + kWarps * kTokens - 1) / (kWarps * kTokens);
-  // four blocks an SM, or fewer than that where there is less to do
+  // four blocks an SM, or fewer where there is less to do
   const int64_t blocks = std::min(groups, std::max<int64_t>(1, 4 * static_cast<int64_t>(device_sm_count()) / L.N));
   auto kernel = L.f16 ? cache_read_kernel<true> : cache_read_kernel<false>;
   kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(L.N)), kThreads, smem, stream>>>(L, k, v);
