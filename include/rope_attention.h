@@ -411,15 +411,18 @@ typedef struct {
   int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
 } packed_attention_params;
 
-/* Workspace bytes of packed_attention (a status word and scratch).  Zero-fill it
- * once after allocation.  Calls that may overlap need workspaces of their own. */
+/* Workspace bytes of packed_attention: a status word and the partial results of
+ * rows that several blocks share (at most 64 MiB).  Zero-fill it once after
+ * allocation.  Calls that may overlap need workspaces of their own. */
 ra_status packed_attention_workspace_bytes(const packed_attention_params* p, size_t* bytes);
 
 /* One call.
  *   q, k, v       strided as above, 16-byte aligned; out likewise, no two elements of
- *                 out in one place.  Every row of q, k and v inside a sequence must be
- *                 finite; rows outside every sequence may hold anything and the
- *                 matching rows of out (and lse) are left as they were.
+ *                 out in one place.  A NaN in a row of q makes that row of out NaN; an
+ *                 infinity or NaN in a row of k or v can reach every row of its
+ *                 sequence, those that the causal mask keeps from it too.  Rows
+ *                 outside every sequence may hold anything and the matching rows of
+ *                 out (and lse) are left as they were.
  *   lse           [total_q, num_heads] fp32: log of the sum of the exponentials, or NULL.
  *   cu_seqlens_q  [B + 1] int32 on the device: sequence b has the query tokens
  *                 cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (non-decreasing, at most
@@ -450,12 +453,14 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
  * The new tokens' own rows must already be in the cache: the Lq query tokens of a
  * sequence are its last Lq positions, and with `causal` query i sees the
  * positions <= seq_len - Lq + i.  A query that sees no key gives zeros (lse -inf).
+ * Non-finite values as in packed_attention; slots that are no sequence's position may
+ * hold anything.
  * Built for V1 with Dv <= 512 (a multiple of 64) and rope_size <= 64 (a multiple
- * of 16), and V2 with Dkv <= 256 and Dv <= 256 (multiples of 16): others are
- * RA_ERR_UNSUPPORTED. */
+ * of 16), and V2 with Dkv <= 256 and Dv <= 256 (multiples of 16), and for caches of
+ * fewer than 2^31 rows (slots times N): others are RA_ERR_UNSUPPORTED. */
 typedef struct {
   int64_t B;                  /* sequences (in NORM mode the cache's B)                */
-  int64_t total_q;            /* query tokens, >= 1, < 2^31                            */
+  int64_t total_q;            /* query tokens, >= 1; total_q * num_heads < 2^31        */
   int32_t num_heads;          /* query heads; a multiple of the cache's N              */
   int32_t causal;             /* 0 or 1                                                */
   float softmax_scale;        /* finite, > 0                                           */

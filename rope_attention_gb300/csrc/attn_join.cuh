@@ -78,20 +78,20 @@ __device__ __forceinline__ JoinRow join_row(const JoinParams& p, const int32_t* 
 template <bool F16>
 __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& row, int32_t kv_head, int32_t ch, float4 acc,
                                            float l) {
-  const float inv = l > 0.f ? rcp(l) : 0.f;
+  const float inv = l != 0.f ? rcp(l) : 0.f;
   float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   if (p.v_scale) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 so = channel_quant(p.v_scale, p.v_offset, (p.per_head ? kv_head * p.Dv : 0) + ch + e, p.v_scalar);
-      y[e] = l > 0.f ? (y[e] - so.y) * rcp(so.x) : 0.f;
+      y[e] = l != 0.f ? (y[e] - so.y) * rcp(so.x) : 0.f;
     }
   }
   *reinterpret_cast<uint2*>(p.out + row.token * p.o_ts + row.head * p.o_hs + ch) =
       make_uint2(pack_half2<!F16>(y[0], y[1]), pack_half2<!F16>(y[2], y[3]));
 }
 __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row, float m, float l, float k0) {
-  p.lse[row.token * p.heads + row.head] = l > 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
+  p.lse[row.token * p.heads + row.head] = l != 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
 }
 
 template <bool F16>
@@ -125,13 +125,13 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
         float4 st = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
         JoinRow row = join_row(p, mt, min(mine, rows - 1));
         if (mine < rows && piece < n) st = p.stats[slot(piece) * NR + row.part];
-        float m = st.x, k0 = st.y > 0.f ? st.z : neg_inf();  // the same in every piece that saw a key
+        float m = st.x, k0 = st.y != 0.f ? st.z : neg_inf();  // the same in every piece that saw a key
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
         }
-        const float wt = st.y > 0.f ? ex2(st.x - m) : 0.f;
+        const float wt = st.y != 0.f ? ex2(st.x - m) : 0.f;
         float l = st.y * wt;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < kJoinLoads; ++i) {
         m = fmaxf(m, st[i].x);
-        if (st[i].y > 0.f) k0 = st[i].z;
+        if (st[i].y != 0.f) k0 = st[i].z;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
       }
 #pragma unroll
       for (int i = 0; i < kJoinLoads; ++i) {
-        wt[i] = st[i].y > 0.f ? ex2(st[i].x - m) : 0.f;
+        wt[i] = st[i].y != 0.f ? ex2(st[i].x - m) : 0.f;
         l = fmaf(st[i].y, wt[i], l);
       }
 #pragma unroll

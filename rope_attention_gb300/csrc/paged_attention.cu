@@ -30,8 +30,8 @@
 //    sequence's end and rows of absent pages are zeroed in shared memory (0 times a
 //    stray NaN is NaN) and masked in S.  Warps 0-7 are the softmax, the rescaling and the
 //    epilogue, two threads to a row of S with 32 of its 64 columns each (with one thread
-//    a 64-key tile took 1740 cycles, more than its products); warp 12 issues the MMAs, taking whichever of the next S = Q K^T and the
-//    next O^T += V^T P^T is ready first.
+//    a 64-key tile took 1740 cycles, more than its products); warp 12 issues the MMAs,
+//    taking whichever of the next S = Q K^T and the next O^T += V^T P^T is ready first.
 // Every wait is bounded in time (status word).
 #include <algorithm>
 #include <atomic>
@@ -794,10 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       const bool whole = w.whole();
       if (half == 0 && row < NR) {
         l += xch[NR + row];
-        inv_sum[row] = l > 0.f ? 1.f / l : 0.f;
+        inv_sum[row] = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is 0; a NaN stays one
         const float shift = k_quant && n > 0 && live ? row_const[row] : 0.f;
         if (live && whole && p.lse)
-          p.lse[out_row[row]] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
+          p.lse[out_row[row]] = l != 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
         if (live && !whole) p.join.stats[slot * NR + row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
       }
       bar_softmax();
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             if (r >= w.rows) break;
             if (whole) {
               const float inv = inv_sum[r];
-              const float y = inv > 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
+              const float y = inv != 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
               p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
             } else {
               part[r * p.Dv] = __uint_as_float(o[e]);

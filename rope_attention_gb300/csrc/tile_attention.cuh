@@ -50,7 +50,7 @@ constexpr int kTileExtra = 2;
 // Items per block from which blocks take whole items: at most about a 16th is lost to uneven
 // ends, and nothing is joined.  With few sequences they take every G-th item, so that the
 // blocks are at one head or two at a time and read its keys from L2 together (480p
-// self-attention: STRIDED ms; 17.3 with runs cut anywhere, whose blocks stream 40 heads' keys
+// self-attention: 14.2 ms; 17.3 with runs cut anywhere, whose blocks stream 40 heads' keys
 // from HBM, which costs the tensor core power as well as time); over many sequences, each of
 // which a strided walk would have to look up, they take consecutive ones.
 constexpr int kTileWholeItems = 16, kTileStrideSeqs = 64;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   const int64_t start = per * blockIdx.x;
   grid_launch_dependents();
   if (threadIdx.x == 0) p.join.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
-  if (start >= W) return;
+  if (start >= W && runs != kRunsStrided) return;  // (strided: every block has its 16 items and more)
   if (before <= start && start < before + mine) {
     int32_t b = b_lo;
     int64_t off = start - before;
@@ -910,11 +910,11 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       u += n_both;
 
       // ---- final rows, or the piece's statistics and accumulator
-      const float inv = l > 0.f ? rcp(l) : 0.f;
+      const float inv = l != 0.f ? rcp(l) : 0.f;  // a row that sees nothing is 0; a NaN stays one
       if (live) {
         if (whole) {
           if (p.join.lse)
-            p.join.lse[token * p.join.heads + head] = l > 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
+            p.join.lse[token * p.join.heads + head] = l != 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
         } else {
           p.join.stats[part_row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
         }
@@ -936,8 +936,8 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         float y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-        if (QUANT && l > 0.f) {
+        for (int e = 0; e < 16; ++e) y[e] = l != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+        if (QUANT && l != 0.f) {
           const float* vs = p.join.v_scale + static_cast<int64_t>(w.kv_head) * p.join.Dv + c;
           const float* vo = p.join.v_offset ? p.join.v_offset + static_cast<int64_t>(w.kv_head) * p.join.Dv + c : nullptr;
 #pragma unroll

@@ -35,7 +35,7 @@ def packed(**kw):
 
 
 def call_packed(L, p=None, **over):
-    a = dict(q=A16, k=A16, v=A16, out=A16, lse=None, cq=None, ck=None, ws=A16, n=1 << 20)
+    a = dict(q=A16, k=A16, v=A16, out=A16, lse=None, cq=None, ck=None, ws=A16, n=64 << 20)
     a.update(over)
     st = L.packed_attention(ctypes.byref(p or packed()), a["q"], a["k"], a["v"], a["out"], a["lse"], a["cq"], a["ck"],
                             a["ws"], a["n"], None)
@@ -246,21 +246,27 @@ def test_paged_and_read_binding_refusals():
 
 
 # ---------------------------------------------------------------- kernels
-def test_register_budgets(tmp_path):
-    """The packed kernel moves registers between its warpgroups: what it gives out (2 x 224 +
-    56 = 3 x 168) must be what it was launched with, or a warpgroup waits for ever."""
+@pytest.mark.parametrize("file,kernel,budget", [
+    # the tile kernel launches 384 threads (2 x 216 + 72 = 3 x 168), with converters 512 (2 x 192 + 2 x 64 = 4 x 128)
+    ("packed_attention.cu", "tile_attention_kernel", {168: 4}),
+    ("paged_tile.cu", "tile_attention_kernel", {168: 4, 128: 4}),
+    ("paged_attention.cu", "paged_attention_kernel", {128: 3}),   # 2 x 160 + 120 + 72 = 4 x 128
+    ("cache_read.cu", "cache_read_kernel", {64: 2}),              # four blocks of 256 threads an SM
+])
+def test_register_budgets(file, kernel, budget, tmp_path):
+    """The attention kernels move registers between their warpgroups: what they give out must
+    be what they were launched with, or a warpgroup waits for ever."""
     try:
         build.nvcc()
     except RuntimeError:
         pytest.skip("nvcc not available")
-    rep = ptxas_report("packed_attention.cu", str(tmp_path))
-    hits = {n: v for n, v in rep.items() if "packed_attention_kernel" in n}
-    assert len(hits) == 4
-    for n, (regs, spill) in hits.items():
-        assert regs == 168, n
-        assert spill <= 128, n
-    for n, (regs, spill) in ptxas_report("paged_attention.cu", str(tmp_path)).items():
-        assert regs <= 168 and spill <= 64, n
+    rep = ptxas_report(file, str(tmp_path))
+    hits = [v for n, v in rep.items() if kernel in n]
+    assert {r: sum(h[0] == r for h in hits) for r in {h[0] for h in hits}} == budget, hits
+    # the softmax warps run with more registers than ptxas was given: a few words that live
+    # across their loops may spill
+    assert all(spill <= (320 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
+    assert all(regs <= 128 and spill == 0 for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
 
 
 # ---------------------------------------------------------------- the oracle
