@@ -201,8 +201,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // issues in order, and with each used at once 64 elements took 827 cycles (one warp per
 // scheduler; 882 for two), against 353 (615) in batches of 32, near the rate of the
 // exponential unit (8 lanes a cycle: 256, 512).
-template <bool BF16>
-__device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float2 neg, float2 (&acc)[4], uint32_t* w) {
+// LO (fp16): what the rounding left, rounded itself, in lo.
+template <bool BF16, bool LO = false>
+__device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float2 neg, float2 (&acc)[4], uint32_t* w,
+                                          uint32_t* lo = nullptr) {
+  static_assert(!(BF16 && LO), "");
   float2 t[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
@@ -219,6 +222,10 @@ __device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float
       asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t[i].y), "f"(t[i].x));
     else
       asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t[i].y), "f"(t[i].x));
+    if constexpr (LO) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[i]) : "f"(t[i].y - h.y), "f"(t[i].x - h.x));
+    }
   }
 }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(static_cast<int>(0xff800000u)); }

@@ -314,7 +314,9 @@ __device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows
 }
 
 // F16: q, out and 16-bit caches are fp16, not bf16; P16: P is fp16 (V's operand is)
-template <bool F16, bool P16>
+// PLO: fp16 results over codes.  q / s is rounded to 11 bits, like the result; so that P's
+// rounding does not add a third error of that size, P goes in as two fp16 numbers (hi + lo).
+template <bool F16, bool P16, bool PLO>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + p.off_misc);
@@ -562,6 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             const uint64_t va = v_desc + static_cast<uint64_t>(st_o * (p.stage_bytes >> 4));
             for (int c = 0; c < v_chunks; ++c)
               mma4_f16_ss<128, 2>(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4), p_desc, id_o, pv > 0, 4);
+            if (PLO)
+              for (int c = 0; c < v_chunks; ++c)
+                mma4_f16_ss<128, 2>(tmem + kSCols + c * NR, va + c * (2 * kSlab >> 4), p_desc + (NR * 128 >> 4), id_o, true, 4);
             tc_commit(smem_u32(&ms.kv_empty[st_o]));
             tc_commit(smem_u32(&ms.pv_done));
           }
@@ -754,14 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (ok && rows_here) {
           const float neg = m == neg_inf() ? 0.f : -m * sl2;
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint32_t x[16];
-          exp_batch<!P16>(s, make_float2(sl2, sl2), make_float2(neg, neg), acc, x);
+          uint32_t x[16], lo[16];
+          exp_batch<!P16, PLO>(s, make_float2(sl2, sl2), make_float2(neg, neg), acc, x, lo);
           if (live) {
             uint8_t* prow = smem + p.off_p + row * 128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(prow + (((4 * half + c) ^ (row & 7)) << 4)) =
-                  make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) {
+              const int at = ((4 * half + c) ^ (row & 7)) << 4;
+              *reinterpret_cast<uint4*>(prow + at) = make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+              if (PLO) *reinterpret_cast<uint4*>(prow + NR * 128 + at) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
           }
           const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l += sum.x + sum.y;
@@ -850,6 +857,9 @@ struct Plan {
   int32_t vslabs, kslabs, qslabs, kslab0, stage, staging, off_p, off_ring, off_staging, off_misc, smem;
 };
 
+bool p_in_two(const PagedLaunch& L) { return L.f16 && (L.kq != 0 || L.vq != 0); }
+int p_bytes(const PagedLaunch& L, int nr) { return nr * 128 * (p_in_two(L) ? 2 : 1); }
+
 // The rows of a tile: as many as a sequence's tokens and heads fill on average, so that a
 // decode step does not pay for 128, within what shared memory leaves for two stages.
 bool plan(const PagedLaunch& L, Plan* pl) {
@@ -868,7 +878,7 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   for (;; nr >>= 1) {
     if (nr < 16) return false;
     if (kSCols + chunks * nr > 512) continue;
-    const int fixed = pl->qslabs * nr * 128 + nr * 128 + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
+    const int fixed = pl->qslabs * nr * 128 + p_bytes(L, nr) + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
     const int left = kSmemMax - fixed;
     if (!staged) {
       pl->nsg = 0;
@@ -885,7 +895,7 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   }
   pl->NR = nr;
   pl->off_p = pl->qslabs * nr * 128;
-  pl->off_ring = pl->off_p + nr * 128;
+  pl->off_ring = pl->off_p + p_bytes(L, nr);
   pl->off_staging = pl->off_ring + pl->ns * pl->stage;
   pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
@@ -902,13 +912,13 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   return true;
 }
 
-template <bool F16, bool P16>
+template <bool F16, bool P16, bool PLO>
 cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto kernel = paged_attention_kernel<F16, P16>;
+  auto kernel = paged_attention_kernel<F16, P16, PLO>;
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
@@ -1018,8 +1028,11 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);
   p.stall_loads = L.stall_loads;
 
-  if (L.f16) return launch<true, true>(p, pl.G, pl.items, pl.smem, stream);
-  return L.vq ? launch<false, true>(p, pl.G, pl.items, pl.smem, stream) : launch<false, false>(p, pl.G, pl.items, pl.smem, stream);
+  if (L.f16)
+    return p_in_two(L) ? launch<true, true, true>(p, pl.G, pl.items, pl.smem, stream)
+                       : launch<true, true, false>(p, pl.G, pl.items, pl.smem, stream);
+  return L.vq ? launch<false, true, false>(p, pl.G, pl.items, pl.smem, stream)
+              : launch<false, false, false>(p, pl.G, pl.items, pl.smem, stream);
 }
 
 }  // namespace ra

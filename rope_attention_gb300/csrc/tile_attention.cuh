@@ -323,6 +323,10 @@ template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED>
 __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(const __grid_constant__ TileParams p) {
   using SH = TileShape<KS, VS, KT, QUANT>;
   constexpr bool P16 = F16 || QUANT;
+  // fp16 results over codes: q / s is rounded to 11 bits, like the result; so that P's rounding
+  // does not add a third error of that size, P goes in as two fp16 numbers (hi + lo).  The
+  // products of a tile cost half as much again, which the softmax hides for the most part.
+  constexpr bool kPLo = F16 && QUANT;
   // Registers per thread: launched with 168 (QUANT: 128) each, then moved to the softmax:
   // 2 x 216 + 72 = 3 x 168; 2 x 192 + 64 + 64 = 4 x 128
   constexpr int kRegsSoftmax = QUANT ? 192 : 216, kRegsRest = QUANT ? 64 : 72;
@@ -636,6 +640,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 #pragma unroll
               for (int k = 0; k < KT / 16; ++k)
                 mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, bd + 128 * k, id_o, j > 0 || k > 0);
+              if (kPLo)
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                  mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + KT / 2 + 8 * k, bd + 128 * k, id_o, true);
               if (j + 1 < ni) issue_s(i, kr.stage, j + 2 == ni);
               else tc_commit(smem_u32(&ms.o_done[i]));
             }
@@ -869,9 +877,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < KT / 32; ++h) {
-          uint32_t x[16];
-          exp_batch<!P16>(s + 32 * h, sl, ng, acc, x);
+          uint32_t x[16], lo[16];
+          exp_batch<!P16, kPLo>(s + 32 * h, sl, ng, acc, x, lo);
           tmem_st_x16(s_addr + 16 * h, x);  // P takes the place of S: KT / 2 columns of pairs
+          if (kPLo) tmem_st_x16(s_addr + KT / 2 + 16 * h, lo);
         }
         const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l += sum.x + sum.y;

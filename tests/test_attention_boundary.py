@@ -250,7 +250,7 @@ def test_paged_and_read_binding_refusals():
     # the tile kernel launches 384 threads (2 x 216 + 72 = 3 x 168), with converters 512 (2 x 192 + 2 x 64 = 4 x 128)
     ("packed_attention.cu", "tile_attention_kernel", {168: 4}),
     ("paged_tile.cu", "tile_attention_kernel", {168: 4, 128: 4}),
-    ("paged_attention.cu", "paged_attention_kernel", {128: 3}),   # 2 x 160 + 120 + 72 = 4 x 128
+    ("paged_attention.cu", "paged_attention_kernel", {128: 4}),   # 2 x 160 + 120 + 72 = 4 x 128
     ("cache_read.cu", "cache_read_kernel", {64: 2}),              # four blocks of 256 threads an SM
 ])
 def test_register_budgets(file, kernel, budget, tmp_path):
@@ -265,7 +265,7 @@ def test_register_budgets(file, kernel, budget, tmp_path):
     assert {r: sum(h[0] == r for h in hits) for r in {h[0] for h in hits}} == budget, hits
     # the softmax warps run with more registers than ptxas was given: a few words that live
     # across their loops may spill
-    assert all(spill <= (320 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
+    assert all(spill <= (384 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
     assert all(regs <= 128 and spill == 0 for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
 
 
