@@ -3,7 +3,8 @@
 Each translation unit is compiled by its own nvcc process (in parallel), then
 linked into one shared library with the CUDA runtime linked statically, so the
 library loads on a machine without a GPU driver (calls then fail with
-RA_ERR_CUDA) and needs no libcudart at run time.
+RA_ERR_CUDA) and needs no libcudart at run time.  Beside it, _torch_calls.so: the
+attention calls with torch tensors, for this interpreter and its torch.
 
     python -m rope_attention_gb300.build            # build if out of date
     python -m rope_attention_gb300.build --force    # rebuild
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -23,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "librope_attention.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+CALLS_PATH = os.path.join(PKG, "_torch_calls.so")  # the calls with torch tensors, linked to the library
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "qkv_project.cu", "qk_norm_rope.cu", "kv_cache.cu", "noalloc.cu", "row_quant.cu",
            "packed_attention.cu", "paged_attention.cu", "paged_tile.cu", "cache_read.cu"]
@@ -43,9 +46,9 @@ def _inputs() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -63,11 +66,42 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_calls() -> str:
+    """csrc/torch_calls.cpp, against this interpreter's torch."""
+    import torch  # the library itself needs none
+
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", cuda]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc(), "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static", "-lpthread", "-ldl", "-lrt"]
@@ -75,6 +109,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_calls(calls.result())
     return LIB_PATH
 
 

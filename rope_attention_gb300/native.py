@@ -5,18 +5,22 @@ dtype, contiguity and size, turns tensors into raw pointers and calls the C
 entry point of the same name on the current CUDA stream.  The C ABI takes bare
 pointers, so it cannot see how large a buffer is; the binding refuses a tensor
 smaller than the extent the call reads or writes through it (``qkv_extents``,
-``kv_extents``) before anything reaches the device.  All arithmetic happens in
+``kv_extents``) before anything reaches the device.  The attention calls and the
+cache read, which a decode step makes once a layer, do all this in a compiled
+module (``csrc/torch_calls.cpp``).  All arithmetic happens in
 the library's CUDA kernels; there is no CPU fallback.  ``load()`` raises if
 the library has not been built (``python -m rope_attention_gb300.build``).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
-from .build import LIB_PATH
+from .build import CALLS_PATH, LIB_PATH
 
 RA_OK = 0
 STATUS_NAMES = {0: "RA_OK", -1: "RA_ERR_INVALID_ARG", -2: "RA_ERR_UNSUPPORTED",
@@ -132,6 +136,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
         fn.argtypes = args
     _LIB = lib
     return lib
+
+
+_CALLS = None
+
+
+def _calls():
+    """The module of the calls that take tensors whole (csrc/torch_calls.cpp), loaded once."""
+    global _CALLS
+    if _CALLS is None:
+        load()
+        if not os.path.exists(CALLS_PATH):
+            raise FileNotFoundError(f"{CALLS_PATH} is missing: build it with `python -m rope_attention_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("rope_attention_gb300._torch_calls", CALLS_PATH)
+        spec = importlib.util.spec_from_loader(loader.name, loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _CALLS = module
+    return _CALLS
 
 
 def _check(status: int) -> None:
@@ -408,38 +430,9 @@ def row_quantize_e4m3_packed(x: torch.Tensor, packed: torch.Tensor, stream=None)
 
 
 # ---------------------------------------------------------------- attention and the cache read
-_I32, _I64, _F32, _U8 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.uint8,)
-_STORED = {RA_BF16: (torch.bfloat16,), RA_FP16: (torch.float16,), RA_INT8: (torch.int8,),
-           RA_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), RA_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
-
-
 def ra_test_stall_next_attention() -> None:
     """Test hook: the next packed or paged attention issues no loads, so its waits time out."""
     load().ra_test_stall_next_attention()
-
-
-def _arg(t: torch.Tensor | None, nbytes: int, dtypes, name: str) -> int | None:
-    """Pointer of a contiguous tensor of one of ``dtypes`` and of at least ``nbytes`` bytes."""
-    if t is None:
-        return None
-    size = t.numel() * t.element_size()
-    if size < nbytes:
-        raise ValueError(f"{name}: the call needs {nbytes} bytes, the tensor holds {size}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {dtypes[-1]}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _place(**tensors) -> None:
-    """The calls run on the current device's stream: every tensor has to be there."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            if not t.is_cuda:
-                raise ValueError(f"{name}: expected a CUDA tensor")
-            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{dev}")
 
 
 def packed_attention_params(q, k, v, out, *, B: int = 1, causal: bool = False,
@@ -448,48 +441,7 @@ def packed_attention_params(q, k, v, out, *, B: int = 1, causal: bool = False,
     token and head strides: views of a qkv_cte_mx output, for example
     ``qkv.view(T, heads, d)[:, :num_heads]`` (BSD) or ``planes[:num_heads].transpose(0, 1)``
     (NBSd).  softmax_scale defaults to head_dim ** -0.5."""
-    qs, ks = q.shape, k.shape
-    for name, t, want in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)):
-        if t.dim() != 3:
-            raise ValueError(f"{name}: expected [tokens, heads, head_dim]")
-        if t.shape != want or want[2] != qs[2]:
-            raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {tuple(want if t.shape != want else qs)}")
-        if t.dtype != q.dtype:
-            raise ValueError(f"{name}: expected {q.dtype}, got {t.dtype}")
-        if want[2] > 1 and t.stride(2) != 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-    code = RA_BF16 if q.dtype == torch.bfloat16 else RA_FP16 if q.dtype == torch.float16 else None
-    if code is None:
-        raise ValueError(f"q: expected bfloat16 or float16, got {q.dtype}")
-    d = qs[2]
-    return PackedAttentionParams(B, qs[0], ks[0], qs[1], ks[1], d, code, 1 if causal else 0,
-                                 d ** -0.5 if softmax_scale is None else softmax_scale,
-                                 *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
-
-
-def packed_extents(p: PackedAttentionParams) -> dict[str, int]:
-    """Bytes that each tensor argument of packed_attention spans, from its first element:
-    the strided extent of q, k, v and out, and [total_q, num_heads], [B + 1] for the others."""
-    def span(tokens, heads, ts, hs):
-        return ((max(tokens, 1) - 1) * ts + (max(heads, 1) - 1) * hs + p.head_dim) * 2
-    return {"q": span(p.total_q, p.num_heads, p.q_token_stride, p.q_head_stride),
-            "k": span(p.total_k, p.num_kv_heads, p.k_token_stride, p.k_head_stride),
-            "v": span(p.total_k, p.num_kv_heads, p.v_token_stride, p.v_head_stride),
-            "out": span(p.total_q, p.num_heads, p.out_token_stride, p.out_head_stride),
-            "lse": p.total_q * p.num_heads * 4, "cu_seqlens_q": (p.B + 1) * 4, "cu_seqlens_k": (p.B + 1) * 4}
-
-
-def _strided_arg(t: torch.Tensor, tokens: int, heads: int, d: int, ts: int, hs: int, dtypes, name: str) -> int:
-    """Pointer of a strided 16-bit tensor [tokens, heads, d]: one with these sizes and strides
-    holds what the call addresses, any other has to in its storage."""
-    if t.shape != (tokens, heads, d) or t.stride() != (ts, hs, 1):
-        need = ((max(tokens, 1) - 1) * ts + (max(heads, 1) - 1) * hs + d) * 2
-        held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
-        if held < need:
-            raise ValueError(f"{name}: the call needs {need} bytes, the tensor's storage holds {held}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {dtypes[-1]}, got {t.dtype}")
-    return t.data_ptr()
+    return PackedAttentionParams.from_buffer_copy(_calls().packed_params(q, k, v, out, B, causal, softmax_scale))
 
 
 def packed_attention_workspace_bytes(params: PackedAttentionParams) -> int:
@@ -502,35 +454,7 @@ def packed_attention(params, q, k, v, out, workspace, lse=None, cu_seqlens_q=Non
                      stream=None) -> None:
     """Attention over packed prompts (header: packed_attention); q, k, v and out as the
     tensors that ``packed_attention_params`` was given, or others with the same strides."""
-    p, half = params, _STORED.get(params.dtype, (torch.bfloat16, torch.float16))
-    tq, tk, nq, nk, d, cu = p.total_q, p.total_k, p.num_heads, p.num_kv_heads, p.head_dim, (p.B + 1) * 4
-    args = (_strided_arg(q, tq, nq, d, p.q_token_stride, p.q_head_stride, half, "q"),
-            _strided_arg(k, tk, nk, d, p.k_token_stride, p.k_head_stride, half, "k"),
-            _strided_arg(v, tk, nk, d, p.v_token_stride, p.v_head_stride, half, "v"),
-            _strided_arg(out, tq, nq, d, p.out_token_stride, p.out_head_stride, half, "out"),
-            _arg(lse, tq * nq * 4, _F32, "lse"), _arg(cu_seqlens_q, cu, _I32, "cu_seqlens_q"),
-            _arg(cu_seqlens_k, cu, _I32, "cu_seqlens_k"), _arg(workspace, 0, _U8, "workspace"))
-    _place(q=q, k=k, v=v, out=out, lse=lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, workspace=workspace)
-    _check(load().packed_attention(ctypes.byref(p), *args, workspace.numel(), _stream(stream)))
-
-
-def _cache_extents(p: KvRmsNormRopeCacheParams) -> dict[str, int]:
-    """The part of kv_extents that a reader of the caches shares with their writer."""
-    v1, N = p.variant == 1, p.N
-    kw, cw = (p.rope_size, p.Dkv - p.rope_size) if v1 else (p.Dkv, p.Dv)
-    rows = (p.B * p.cache_seq_len if p.cache_mode == RA_CACHE_NORM else p.block_num * p.block_size) * N
-    qk, qv = (1 if p.k_quant_scalar else kw, 1 if p.c_kv_quant_scalar else cw) if v1 else (N * kw, N * cw)
-    return {"k_cache": rows * kw * _CACHE_BYTES.get(p.k_cache_dtype, 1),
-            "ckv_cache": rows * cw * _CACHE_BYTES.get(p.ckv_cache_dtype, 1),
-            "k_rope_scale": qk * 4, "k_rope_offset": qk * 4, "c_kv_scale": qv * 4, "c_kv_offset": qv * 4}
-
-
-def paged_extents(cache: KvRmsNormRopeCacheParams, p: PagedAttentionParams) -> dict[str, int]:
-    """Bytes that each tensor argument of paged_attention spans, from the call's parameters."""
-    rows = max(p.total_q, 0) * max(p.num_heads, 0)
-    return {"q": rows * max(cache.Dkv, 0) * 2, "out": rows * max(cache.Dv, 0) * 2, "lse": rows * 4,
-            "seq_lens": p.B * 4, "block_table": p.B * p.block_table_stride * 4, "cu_seqlens_q": (p.B + 1) * 4,
-            "dev_error_count": 4, **_cache_extents(cache)}
+    _check(_calls().packed_attention(params, q, k, v, out, workspace, lse, cu_seqlens_q, cu_seqlens_k, stream))
 
 
 def paged_attention_workspace_bytes(cache: KvRmsNormRopeCacheParams, params: PagedAttentionParams) -> int:
@@ -545,25 +469,8 @@ def paged_attention(cache, params, q, k_cache, ckv_cache, seq_lens, out, workspa
     """Attention of new tokens over the caches of kv_rms_norm_rope_cache (header:
     paged_attention).  ``cache`` is that call's parameter struct; block_table is [B, pages],
     and its width is taken as ``block_table_stride`` where that is 0."""
-    if block_table is not None:
-        if block_table.dim() != 2 or block_table.shape[0] != params.B:
-            raise ValueError(f"block_table: expected [{params.B}, pages], got {tuple(block_table.shape)}")
-        if params.block_table_stride == 0:
-            params = PagedAttentionParams(params.B, params.total_q, params.num_heads, params.causal,
-                                          params.softmax_scale, params.reserved, params.max_seq_len,
-                                          block_table.shape[1])
-    ext, half = paged_extents(cache, params), _STORED.get(cache.kv_dtype)
-    arg = lambda t, name, dtypes: None if t is None else _arg(t, ext[name], dtypes, name)
-    args = (arg(q, "q", half), arg(k_cache, "k_cache", _STORED.get(cache.k_cache_dtype)),
-            arg(ckv_cache, "ckv_cache", _STORED.get(cache.ckv_cache_dtype)), arg(seq_lens, "seq_lens", _I32),
-            arg(block_table, "block_table", _I32), arg(cu_seqlens_q, "cu_seqlens_q", _I32),
-            arg(k_rope_scale, "k_rope_scale", _F32), arg(c_kv_scale, "c_kv_scale", _F32),
-            arg(k_rope_offset, "k_rope_offset", _F32), arg(c_kv_offset, "c_kv_offset", _F32), arg(out, "out", half),
-            arg(lse, "lse", _F32), arg(dev_error_count, "dev_error_count", _I32), _arg(workspace, 0, _U8, "workspace"))
-    _place(q=q, k_cache=k_cache, ckv_cache=ckv_cache, seq_lens=seq_lens, block_table=block_table,
-           cu_seqlens_q=cu_seqlens_q, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale, k_rope_offset=k_rope_offset,
-           c_kv_offset=c_kv_offset, out=out, lse=lse, dev_error_count=dev_error_count, workspace=workspace)
-    _check(load().paged_attention(ctypes.byref(cache), ctypes.byref(params), *args, workspace.numel(), _stream(stream)))
+    _check(_calls().paged_attention(cache, params, q, k_cache, ckv_cache, seq_lens, out, workspace, block_table, cu_seqlens_q,
+                                    k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse, dev_error_count, stream))
 
 
 def attention_status(workspace: torch.Tensor, stream=None) -> int:
@@ -575,27 +482,9 @@ def attention_status(workspace: torch.Tensor, stream=None) -> int:
     return v.value
 
 
-def read_extents(p: KvRmsNormRopeCacheParams) -> dict[str, int]:
-    """Bytes that each tensor argument of kv_cache_read spans, from the call's parameters."""
-    kw, cw = (p.rope_size, p.Dkv - p.rope_size) if p.variant == 1 else (p.Dkv, p.Dv)
-    rows, bs = p.B * p.N * p.S, max(p.block_size, 1)
-    n_index = p.B * (-(-p.S // bs)) if p.cache_mode == RA_CACHE_PA_BLK_BNSD else p.B * p.S
-    return {"k_out": rows * kw * 2, "c_kv_out": rows * cw * 2, "index": n_index * 8, "dev_error_count": 4,
-            **_cache_extents(p)}
-
-
 def kv_cache_read(params, index, k_cache, ckv_cache, k_out=None, c_kv_out=None, k_rope_scale=None,
                   c_kv_scale=None, k_rope_offset=None, c_kv_offset=None, dev_error_count=None,
                   stream=None) -> None:
     """Rows of the caches of kv_rms_norm_rope_cache read back (header: kv_cache_read)."""
-    ext, half = read_extents(params), _STORED.get(params.kv_dtype)
-    arg = lambda t, name, dtypes: None if t is None else _arg(t, ext[name], dtypes, name)
-    args = (arg(index, "index", _I64), arg(k_cache, "k_cache", _STORED.get(params.k_cache_dtype)),
-            arg(ckv_cache, "ckv_cache", _STORED.get(params.ckv_cache_dtype)), arg(k_rope_scale, "k_rope_scale", _F32),
-            arg(c_kv_scale, "c_kv_scale", _F32), arg(k_rope_offset, "k_rope_offset", _F32),
-            arg(c_kv_offset, "c_kv_offset", _F32), arg(k_out, "k_out", half), arg(c_kv_out, "c_kv_out", half),
-            arg(dev_error_count, "dev_error_count", _I32))
-    _place(index=index, k_cache=k_cache, ckv_cache=ckv_cache, k_rope_scale=k_rope_scale, c_kv_scale=c_kv_scale,
-           k_rope_offset=k_rope_offset, c_kv_offset=c_kv_offset, k_out=k_out, c_kv_out=c_kv_out,
-           dev_error_count=dev_error_count)
-    _check(load().kv_cache_read(ctypes.byref(params), *args, _stream(stream)))
+    _check(_calls().kv_cache_read(params, index, k_cache, ckv_cache, k_out, c_kv_out, k_rope_scale, c_kv_scale, k_rope_offset,
+                                  c_kv_offset, dev_error_count, stream))

@@ -190,8 +190,12 @@ def test_packed_params_from_projection_views():
     nbsd = torch.zeros(nq + 2 * nk, T, d, dtype=torch.bfloat16).transpose(0, 1)
     p = native.packed_attention_params(nbsd[:, :nq], nbsd[:, nq:nq + nk], nbsd[:, nq + nk:], out)
     assert (p.k_token_stride, p.k_head_stride) == (64, T * 64)
-    ext = native.packed_extents(p)
-    assert ext["q"] == ((T - 1) * 64 + (nq - 1) * T * 64 + 64) * 2 and ext["out"] == out.numel() * 2
+    # a storage one element short of what those strides address
+    ws = torch.zeros(256, dtype=torch.uint8)
+    need = ((T - 1) * 64 + (nq - 1) * T * 64 + 64) * 2
+    short = torch.zeros(need // 2 - 1, dtype=torch.bfloat16).view(1, 1, -1)
+    with pytest.raises(ValueError, match=f"^q: the call needs {need} bytes, the tensor's storage holds {need - 2}"):
+        native.packed_attention(p, short, nbsd[:, nq:nq + nk], nbsd[:, nq + nk:], out, ws)
 
 
 def test_packed_binding_refusals():
@@ -216,6 +220,12 @@ def test_packed_binding_refusals():
         native.packed_attention(p, *good, ws, cu_seqlens_k=torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match=r"expected a CUDA tensor"):
         native.packed_attention(p, *good, ws)
+    with pytest.raises(TypeError, match="^v: expected a tensor"):
+        native.packed_attention(p, *good[:2], None, good[3], ws)
+    with pytest.raises(TypeError, match="^params: "):
+        native.packed_attention(cache(), *good, ws)
+    with pytest.raises(TypeError):
+        native.packed_attention_params(*good, B="two")
 
 
 def test_paged_and_read_binding_refusals():
