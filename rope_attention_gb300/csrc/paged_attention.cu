@@ -60,6 +60,10 @@ constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kValidRing = 16;            // > tiles between the loads and the softmax
 constexpr int kMaxStages = 6;
 constexpr int kMinTiles = 4;              // tiles per block below which a split costs more than it gives
+// Tiles of the longest sequence up to which items are not cut: the join that a cut needs costs
+// about what three tiles do (one token, 8 heads: 333 positions 16.6 us whole and 18.7 cut, 450
+// positions 18.6 and 16.9).
+constexpr int kWholeTiles = 6;
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSmemMax = 232448;
@@ -90,6 +94,7 @@ struct Params {
   int32_t off_p, off_ring, off_staging, off_misc;
   float sl2, scale;
   uint64_t wait_ns;
+  int32_t whole;                // blocks take whole items
   int32_t stall_loads;
 };
 
@@ -125,11 +130,24 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len) { return max(1, (len + 
 __device__ __forceinline__ int32_t row_tiles_of(const Params& p, int32_t lq) {
   return p.hblocks > 1 ? lq * p.hblocks : static_cast<int32_t>(static_cast<uint32_t>(lq + p.tb - 1) / static_cast<uint32_t>(p.tb));
 }
-__device__ __forceinline__ int64_t seq_work(const Params& p, int32_t b) {
-  int32_t s, lq;
-  q_span(p, b, s, lq);
-  return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * tiles_of(seq_len_of(p, b));
+// what a sequence counts for in the line: its items' tiles, or its items
+__device__ __forceinline__ int64_t seq_work(const Params& p, int32_t lq, int32_t len) {
+  return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * (p.whole ? 1 : tiles_of(len));
 }
+
+// The spans of 32 sequences, one to a lane: a walk over them waits for memory once.
+struct Spans {
+  int32_t base, start, lq, len;
+  __device__ __forceinline__ void load(const Params& p, int32_t from) {
+    base = from;
+    const int32_t b = from + static_cast<int32_t>(threadIdx.x & 31);
+    start = lq = len = 0;
+    if (b < p.B) {
+      q_span(p, b, start, lq);
+      len = seq_len_of(p, b);
+    }
+  }
+};
 
 // One block's share of an item: key tiles [ta, tb) of row tile rt of (b, n).
 struct Piece {
@@ -138,28 +156,31 @@ struct Piece {
   int32_t ta, tb;               // those that any of its rows sees
   __device__ bool whole() const { return take == T; }
 };
-// Walks the pieces of a run of tiles.
+// Walks the pieces of a run of tiles (p.whole: of items), a whole warp at once.
 struct Walker {
   int32_t b;
   int64_t off, rem;             // position inside sequence b, tiles left
+  Spans spans;
   __device__ bool next(const Params& p, Piece& w) {
     while (rem > 0 && b < p.B) {
-      int32_t qs, lq;
-      q_span(p, b, qs, lq);
-      const int32_t len = seq_len_of(p, b), T = tiles_of(len);
+      if (b >= spans.base + 32) spans.load(p, b);
+      const int32_t qs = __shfl_sync(0xffffffffu, spans.start, b - spans.base);
+      const int32_t lq = __shfl_sync(0xffffffffu, spans.lq, b - spans.base);
+      const int32_t len = __shfl_sync(0xffffffffu, spans.len, b - spans.base);
+      const int32_t T = tiles_of(len), each = p.whole ? 1 : T;
       const int32_t rts = row_tiles_of(p, lq);
-      const int64_t work = static_cast<int64_t>(rts) * p.N * T;
+      const int64_t work = static_cast<int64_t>(rts) * p.N * each;
       if (off >= work) {
         off -= work;
         ++b;
         continue;
       }
       // (a 64-bit division is a hundred instructions: only for what needs it)
-      const int64_t item = work >> 32 ? off / T : static_cast<int64_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(T));
+      const int64_t item = work >> 32 ? off / each : static_cast<int64_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each));
       w.b = b;
-      w.t0 = static_cast<int32_t>(off - item * T);
+      w.t0 = static_cast<int32_t>(off - item * each);
       w.T = T;
-      w.take = static_cast<int32_t>(min(static_cast<int64_t>(T - w.t0), rem));
+      w.take = p.whole ? T : static_cast<int32_t>(min(static_cast<int64_t>(T - w.t0), rem));
       w.n = static_cast<int32_t>(static_cast<uint32_t>(item) / static_cast<uint32_t>(rts));  // item < rts * N <= 2^31
       const int32_t rt = static_cast<int32_t>(item - static_cast<int64_t>(w.n) * rts);
       if (p.hblocks > 1) {
@@ -180,8 +201,8 @@ struct Walker {
       const int32_t vt = (seen + kKeys - 1) / kKeys;
       w.ta = min(w.t0, vt);
       w.tb = min(w.t0 + w.take, vt);
-      off += w.take;
-      rem -= w.take;
+      off += p.whole ? 1 : w.take;
+      rem -= p.whole ? 1 : w.take;
       return true;
     }
     return false;
@@ -329,19 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- this block's run of tiles
-  const int32_t chunk = (p.B + kThreads - 1) / kThreads;
-  const int32_t b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk), b_hi = min(p.B, b_lo + chunk);
-  int64_t mine = 0;
-  for (int32_t b = b_lo; b < b_hi; ++b) mine += seq_work(p, b);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) ms.scan[warp] = incl;
-  if (threadIdx.x == 0) {
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ms.tmem), 512);
+    tmem_relinquish();
+  } else if (threadIdx.x == kSoftmax) {
     for (int s = 0; s < p.ns; ++s) {
       // one arrival with the bytes of a 16-bit cache, one from each warp that converts codes
       mbar_init(smem_u32(&ms.kv_full[s]), (p.vq == 0 || p.kq == 0 ? 1 : 0) + (p.nsg != 0 ? kConvertWarps : 0));
@@ -361,42 +373,90 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
     fence_mbar_init();
+    p.join.meta[8 * blockIdx.x] = 0;         // nothing to join, unless the first piece says so below
+  } else if (threadIdx.x == 32 * kLoadWarp) {
     prefetch_tensormap(&p.tq);
     prefetch_tensormap(&p.tk);
     prefetch_tensormap(&p.tv);
   }
-  __syncthreads();
-  int64_t before = incl - mine, W = 0;
+  grid_launch_dependents();
+
+  // ---- this block's run of tiles.  Up to 32 sequences every warp finds it for itself, beside
+  // the set-up above (a block-wide scan behind it cost a short decode step 2.5k cycles more).
+  Walker walk;
+  walk.b = p.B;
+  walk.off = 0;
+  walk.spans.load(p, 0);
+  const bool few = p.B <= 32;
+  int64_t mine = 0;
+  int32_t b_lo = lane, b_hi = lane;
+  if (few) {
+    mine = seq_work(p, walk.spans.lq, walk.spans.len);
+  } else {
+    const int32_t chunk = (p.B + kThreads - 1) / kThreads;
+    b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
+    b_hi = min(p.B, b_lo + chunk);
+    for (int32_t b = b_lo; b < b_hi; ++b) {
+      int32_t qs, lq;
+      q_span(p, b, qs, lq);
+      mine += seq_work(p, lq, seq_len_of(p, b));
+    }
+  }
+  int64_t incl = mine;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t t = ms.scan[w];
-    if (w < warp) before += t;
-    W += t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  int64_t before = incl - mine, W = 0;
+  if (few) {
+    W = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    if (lane == 31) ms.scan[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int64_t t = ms.scan[w];
+      if (w < warp) before += t;
+      W += t;
+    }
   }
   const int64_t G = gridDim.x;
-  const int64_t per = max((W + G - 1) / G, static_cast<int64_t>(kMinTiles));
+  const int64_t even = W >> 31 ? (W + G - 1) / G : static_cast<int64_t>((static_cast<uint32_t>(W) + static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(G));
+  const int64_t per = max(even, static_cast<int64_t>(p.whole ? 1 : kMinTiles));
   const int64_t start = per * blockIdx.x;
-  grid_launch_dependents();
-  if (threadIdx.x == 0) p.join.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
-  if (start >= W) return;
-  if (before <= start && start < before + mine) {
+  walk.rem = max(static_cast<int64_t>(0), min(per, W - start));  // none: the block has nothing to do
+  const bool here = before <= start && start < before + mine;
+  if (few) {
+    const uint32_t at = __ballot_sync(0xffffffffu, here);
+    if (at) {
+      walk.b = __ffs(at) - 1;
+      walk.off = start - __shfl_sync(0xffffffffu, before, walk.b);
+    }
+  } else if (here) {
     int32_t b = b_lo;
     int64_t off = start - before;
-    for (int64_t w; b < b_hi && off >= (w = seq_work(p, b)); ++b) off -= w;
+    for (; b < b_hi; ++b) {
+      int32_t qs, lq;
+      q_span(p, b, qs, lq);
+      const int64_t w = seq_work(p, lq, seq_len_of(p, b));
+      if (off < w) break;
+      off -= w;
+    }
     ms.start_b = b;
     ms.start_off = off;
-  }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&ms.tmem), 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!few && walk.rem > 0) {
+    walk.b = ms.start_b;
+    walk.off = ms.start_off;
+    walk.spans.load(p, walk.b);
+  }
   const uint32_t tmem = ms.tmem;
   const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
   volatile int* abort_flag = &ms.abort;
-  Walker walk{ms.start_b, ms.start_off, min(per, W - start)};
   Piece w{};
 
   if (warp >= kMmaWarp) {
@@ -413,18 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     bool ok = !p.stall_loads;
     while (ok && walk.next(p, w)) {
       if (w.ta >= w.tb) continue;
-      // the row tile of Q, once the products of the last one are through with it
-      ok = bounded_wait_warp(smem_u32(&ms.q_empty), (pieces & 1) ^ 1u, p.wait_ns, abort_flag);
-      if (!ok) break;
-      if (elect_one()) {
-        const uint32_t bar = smem_u32(&ms.q_full);
-        mbar_arrive_expect_tx(bar, p.qslabs * p.hb * p.tb * 128);
-        for (int c = 0; c < p.qslabs; ++c) tma_load_3d(s0 + c * NR * 128, &p.tq, bar, 64 * c, w.head, w.q_start + w.tok);
-      }
-      __syncwarp();
-      armed[2] = 1;
-      armed_parity[2] = pieces & 1;
-      ++pieces;
       // Cache rows.  Lane i holds where group `base + i` of the piece starts: 32 groups of
       // box_rows keys per trip to the block table.
       const int32_t g_end = w.tb * groups, head = p.mode == kModePa ? w.n : 0;
@@ -448,6 +496,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 atomicAdd(p.err_count, 1);
             }
           }
+        }
+        if (t == w.ta) {  // the row tile of Q, once the products of the last one are through with it
+          ok = bounded_wait_warp(smem_u32(&ms.q_empty), (pieces & 1) ^ 1u, p.wait_ns, abort_flag);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t bar = smem_u32(&ms.q_full);
+            mbar_arrive_expect_tx(bar, p.qslabs * p.hb * p.tb * 128);
+            for (int c = 0; c < p.qslabs; ++c) tma_load_3d(s0 + c * NR * 128, &p.tq, bar, 64 * c, w.head, w.q_start + w.tok);
+          }
+          __syncwarp();
+          armed[2] = 1;
+          armed_parity[2] = pieces & 1;
+          ++pieces;
         }
         const int st = kv.stage, sg = code.stage;
         const uint32_t par_d = kv.parity, par_s = code.parity;
@@ -476,17 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           if (direct) mbar_arrive_expect_tx(bar_d, live * direct_bytes);
           if (staged) mbar_arrive_expect_tx(bar_s, live * staged_bytes);
           const uint32_t operand = s0 + p.off_ring + st * p.stage_bytes, codes = s0 + p.off_staging + sg * p.staging_bytes;
-          const uint32_t k_codes = codes + (p.vq ? p.vslabs : 0) * kCodeSlab;
+          // (lean loops: the copies of a tile go out one after the other from here)
+          const uint32_t to_v = p.vq ? codes : operand, to_k = p.kq ? codes + (p.vq ? p.vslabs : 0) * kCodeSlab : operand + p.vslabs * kSlab;
+          const uint32_t bar_v = p.vq ? bar_s : bar_d, bar_k = p.kq ? bar_s : bar_d;
+          const uint32_t slab_v = p.vq ? kCodeSlab : kSlab, slab_k = p.kq ? kCodeSlab : kSlab;
+          const int32_t end_v = 64 * p.vslabs, end_k = 64 * p.kslabs;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (at[i] < 0) continue;
-            const uint32_t od = (i << p.box_shift) * 128, cd = (i << p.box_shift) * 64;
-            for (int c = 0; c < p.vslabs; ++c)
-              tma_load_3d(p.vq ? codes + cd + c * kCodeSlab : operand + od + c * kSlab, &p.tv, p.vq ? bar_s : bar_d, 64 * c,
-                          head, at[i]);
-            for (int c = 0; c < p.kslabs; ++c)
-              tma_load_3d(p.kq ? k_codes + cd + c * kCodeSlab : operand + od + (p.vslabs + c) * kSlab, &p.tk,
-                          p.kq ? bar_s : bar_d, 64 * c, head, at[i]);
+            uint32_t to = to_v + (i << p.box_shift) * (slab_v / kKeys);
+#pragma unroll 2
+            for (int32_t x = 0; x < end_v; x += 64, to += slab_v) tma_load_3d(to, &p.tv, bar_v, x, head, at[i]);
+            to = to_k + (i << p.box_shift) * (slab_k / kKeys);
+#pragma unroll 2
+            for (int32_t x = 0; x < end_k; x += 64, to += slab_k) tma_load_3d(to, &p.tk, bar_k, x, head, at[i]);
           }
         }
         __syncwarp();
@@ -614,26 +678,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         const uint64_t valid = ms.valid[u % kValidRing];
         // 64 keys x 4 chunks of 16 codes per slab, two rounds of 128 threads; two slabs' loads
         // are in flight together
-        for (int sl = sl0; sl < sl1; sl += 2) {
-          uint4 x[4];
+        const int key0 = tid >> 2, c = tid & 3;
+        const bool have[2] = {((valid >> key0) & 1) != 0, ((valid >> (key0 + 32)) & 1) != 0};
+        auto convert = [&](auto kind, int lo, int hi) {
+          constexpr int K = decltype(kind)::value;
+#pragma unroll 1
+          for (int sl = lo; sl < hi; sl += 2) {
+            uint4 x[4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int key = (tid >> 2) + 32 * (h & 1), c = tid & 3;
-            x[h] = make_uint4(0, 0, 0, 0);
-            if (sl + (h >> 1) < sl1 && ((valid >> key) & 1))
-              x[h] = *reinterpret_cast<const uint4*>(from + (sl - sl0 + (h >> 1)) * kCodeSlab + key * 64 + c * 16);
-          }
+            for (int h = 0; h < 4; ++h) {
+              x[h] = make_uint4(0, 0, 0, 0);
+              if (have[h & 1] && sl + (h >> 1) < hi)
+                x[h] = *reinterpret_cast<const uint4*>(from + (sl - sl0 + (h >> 1)) * kCodeSlab + (key0 + 32 * (h & 1)) * 64 + c * 16);
+            }
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            if (sl + (h >> 1) >= sl1) break;
-            const int key = (tid >> 2) + 32 * (h & 1), c = tid & 3;
-            const int32_t kind = sl + (h >> 1) < p.vslabs ? p.vq : p.kq;
-            const uint2 a = codes_to_half(x[h].x, kind), b = codes_to_half(x[h].y, kind);
-            const uint2 d = codes_to_half(x[h].z, kind), e = codes_to_half(x[h].w, kind);
-            uint8_t* dst = stage + (sl + (h >> 1)) * kSlab + key * 128;
-            *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+            for (int h = 0; h < 4; ++h)
+              if (h < 2 || sl + 1 < hi) store_codes<K>(stage + (sl + (h >> 1)) * kSlab + (key0 + 32 * (h & 1)) * 128, key0, c, x[h]);
           }
+        };
+        for (int lo = sl0; lo < sl1;) {      // slabs of one kind: all of them, or the value's and then the key's
+          const int32_t kind = lo < p.vslabs ? p.vq : p.kq;
+          const int hi = lo < p.vslabs && p.kq != p.vq ? p.vslabs : sl1;
+          with_kind(kind, [&](auto k) { convert(k, lo, hi); });
+          lo = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -852,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
 struct Plan {
   int32_t NR, G, hb, tb, hblocks;
+  int32_t whole;
   int64_t items;                // at most
   int32_t ns, nsg;
   int32_t vslabs, kslabs, qslabs, kslab0, stage, staging, off_p, off_ring, off_staging, off_misc, smem;
@@ -907,7 +975,8 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
   pl->items = rts * L.N;
   const int64_t T = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
-  const int64_t runs = (rts * L.N * T + kMinTiles - 1) / kMinTiles;
+  pl->whole = T <= kWholeTiles;
+  const int64_t runs = pl->whole ? pl->items : (rts * L.N * T + kMinTiles - 1) / kMinTiles;
   pl->G = static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs)));
   return true;
 }
@@ -927,7 +996,7 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
   kernel<<<blocks, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join(p.join, F16, blocks, items, stream);
+  return p.whole ? cudaSuccess : launch_join(p.join, F16, blocks, items, stream);
 }
 
 }  // namespace
@@ -936,7 +1005,7 @@ size_t paged_attention_workspace(const PagedLaunch& L) {
   if (paged_tile_serves(L)) return kAttnHeader + paged_tile_workspace(L);
   Plan pl;
   if (!plan(L, &pl)) return 0;
-  return kAttnHeader + join_bytes(pl.G, pl.NR, L.Dv);
+  return kAttnHeader + (pl.whole ? join_meta_bytes(pl.G) : join_bytes(pl.G, pl.NR, L.Dv));
 }
 
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why) {
@@ -1026,6 +1095,7 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.scale = L.scale;
   p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);
+  p.whole = pl.whole;
   p.stall_loads = L.stall_loads;
 
   if (L.f16)

@@ -683,31 +683,28 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           if (!ok) break;
           uint8_t* stage = smem + (side ? SH::kOffV + r.stage * SH::kV : SH::kOffK + r.stage * SH::kK);
           const uint8_t* from = smem + SH::kOffCode + cr.stage * SH::kCode;
-          const int32_t kind = side ? p.vq : p.kq;
           const uint64_t valid[2] = {ms.valid[u % kTileValid][0], ms.valid[u % kTileValid][1]};
           // KT keys x 4 chunks of 16 codes per slab, 32 keys a round of the 128 threads
           const int c = tid & 3, rounds = (side ? VS : KS) * (KT / 32);
+          with_kind(side ? p.vq : p.kq, [&](auto kind) {
+            constexpr int K = decltype(kind)::value;
 #pragma unroll 1
-          for (int h0 = 0; h0 < rounds; h0 += 4) {
-            uint4 x[4];
+            for (int h0 = 0; h0 < rounds; h0 += 4) {
+              uint4 x[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int sl = (h0 + h) / (KT / 32), key = (tid >> 2) + 32 * ((h0 + h) % (KT / 32));
-              x[h] = make_uint4(0, 0, 0, 0);
-              if (h0 + h < rounds && (valid[key >> 6] >> (key & 63)) & 1)
-                x[h] = *reinterpret_cast<const uint4*>(from + sl * KT * 64 + key * 64 + c * 16);
-            }
+              for (int h = 0; h < 4; ++h) {
+                const int sl = (h0 + h) / (KT / 32), key = (tid >> 2) + 32 * ((h0 + h) % (KT / 32));
+                x[h] = make_uint4(0, 0, 0, 0);
+                if (h0 + h < rounds && (valid[key >> 6] >> (key & 63)) & 1)
+                  x[h] = *reinterpret_cast<const uint4*>(from + sl * KT * 64 + key * 64 + c * 16);
+              }
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              if (h0 + h >= rounds) break;
-              const int sl = (h0 + h) / (KT / 32), key = (tid >> 2) + 32 * ((h0 + h) % (KT / 32));
-              const uint2 a = codes_to_half(x[h].x, kind), b = codes_to_half(x[h].y, kind);
-              const uint2 d = codes_to_half(x[h].z, kind), e = codes_to_half(x[h].w, kind);
-              uint8_t* dst = stage + sl * SH::kSlab + key * 128;
-              *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-              *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (key & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+              for (int h = 0; h < 4; ++h) {
+                const int sl = (h0 + h) / (KT / 32), key = (tid >> 2) + 32 * ((h0 + h) % (KT / 32));
+                if (h0 + h < rounds) store_codes<K>(stage + sl * SH::kSlab + key * 128, key, c, x[h]);
+              }
             }
-          }
+          });
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
