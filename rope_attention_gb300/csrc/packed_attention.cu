@@ -93,11 +93,14 @@ cudaError_t launch_packed_attention(const PackedLaunch& L, cudaStream_t stream, 
   p.stall_loads = L.stall_loads;
   const int n = std::min(blocks, device_sm_count());
   const int64_t items = most_items(L);
+  // equal lengths without a mask: all items count alike, and whether one is cut is known here
+  const bool cuts = L.cu_q || L.cu_k || L.causal ||
+                    tile_runs_cut(items, kTileExtra + std::max<int64_t>(1, (L.total_k / L.B + kTileRows - 1) / kTileRows), n);
   if (L.d <= 64)
-    return L.f16 ? launch_tile<1, 1, 128, true, false, false>(p, n, items, stream)
-                 : launch_tile<1, 1, 128, false, false, false>(p, n, items, stream);
-  return L.f16 ? launch_tile<2, 2, 128, true, false, false>(p, n, items, stream)
-               : launch_tile<2, 2, 128, false, false, false>(p, n, items, stream);
+    return L.f16 ? launch_tile<1, 1, 128, true, false, false>(p, n, items, cuts, stream)
+                 : launch_tile<1, 1, 128, false, false, false>(p, n, items, cuts, stream);
+  return L.f16 ? launch_tile<2, 2, 128, true, false, false>(p, n, items, cuts, stream)
+               : launch_tile<2, 2, 128, false, false, false>(p, n, items, cuts, stream);
 }
 
 }  // namespace ra

@@ -95,16 +95,16 @@ cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const c
   const int64_t items = most_items(L);
   if (L.kq) {
     if (L.Dkv <= 128)
-      return L.f16 ? launch_tile<2, 2, kKeys, true, true, true>(p, n, items, stream)
-                   : launch_tile<2, 2, kKeys, false, true, true>(p, n, items, stream);
-    return L.f16 ? launch_tile<3, 2, kKeysWideCodes, true, true, true>(p, n, items, stream)
-                 : launch_tile<3, 2, kKeysWideCodes, false, true, true>(p, n, items, stream);
+      return L.f16 ? launch_tile<2, 2, kKeys, true, true, true>(p, n, items, true, stream)
+                   : launch_tile<2, 2, kKeys, false, true, true>(p, n, items, true, stream);
+    return L.f16 ? launch_tile<3, 2, kKeysWideCodes, true, true, true>(p, n, items, true, stream)
+                 : launch_tile<3, 2, kKeysWideCodes, false, true, true>(p, n, items, true, stream);
   }
   if (L.Dkv <= 128)
-    return L.f16 ? launch_tile<2, 2, kKeys, true, false, true>(p, n, items, stream)
-                 : launch_tile<2, 2, kKeys, false, false, true>(p, n, items, stream);
-  return L.f16 ? launch_tile<3, 2, kKeysWide, true, false, true>(p, n, items, stream)
-               : launch_tile<3, 2, kKeysWide, false, false, true>(p, n, items, stream);
+    return L.f16 ? launch_tile<2, 2, kKeys, true, false, true>(p, n, items, true, stream)
+                 : launch_tile<2, 2, kKeys, false, false, true>(p, n, items, true, stream);
+  return L.f16 ? launch_tile<3, 2, kKeysWide, true, false, true>(p, n, items, true, stream)
+               : launch_tile<3, 2, kKeysWide, false, false, true>(p, n, items, true, stream);
 }
 
 }  // namespace ra

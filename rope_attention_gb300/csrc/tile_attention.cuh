@@ -139,6 +139,7 @@ struct TilePiece {
   int32_t rows[2];                          // of the two row tiles
   int32_t t0, take, T;                      // tiles [t0, t0 + take) of the item's T in the line
   int32_t ta, tb[2];                        // those that a row of either tile sees: [ta, tb[i])
+  int32_t from, to;                         // blocks that share the item, where the block before began it
   __device__ __forceinline__ bool whole() const { return take == T; }
   __device__ __forceinline__ int32_t n(int i) const { return max(0, tb[i] - ta); }
 };
@@ -158,6 +159,48 @@ struct TileMisc {
   float inv_scale[2][192];                  // 1 / the key's scales, for each softmax group
 };
 
+// a / b of numbers that are not negative: a 64-bit division is a hundred instructions
+__device__ __forceinline__ int64_t tile_quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// The spans of 32 sequences, one to a lane: a walk over them waits for memory once.
+template <int KT, bool PAGED>
+struct TileSpans {
+  int32_t base, q_start, Lq, k_start, Lk;
+  __device__ void one(const TileParams& p, int32_t b) {
+    tile_span(p.cu_q, b, p.B, p.total_q, q_start, Lq);
+    if (PAGED) {
+      k_start = 0;
+      Lk = static_cast<int32_t>(min(static_cast<int64_t>(max(__ldg(p.cu_k + b), 0)), p.cap));
+    } else {
+      tile_span(p.cu_k, b, p.B, p.total_k, k_start, Lk);
+    }
+  }
+  __device__ void load(const TileParams& p, int32_t from) {
+    base = from;
+    const int32_t b = from + static_cast<int32_t>(threadIdx.x & 31);
+    q_start = Lq = k_start = Lk = 0;
+    if (b < p.B) one(p, b);
+  }
+  __device__ static TileCount count(const TileParams& p, int32_t Lq, int32_t Lk) {
+    const int32_t tokens = 2 * p.join.tb;
+    TileCount c;
+    c.blocks = static_cast<int32_t>((static_cast<uint32_t>(Lq) + tokens - 1) / static_cast<uint32_t>(tokens));
+    c.most = max(1, (Lk + KT - 1) / KT);
+    c.step = p.causal && !PAGED ? 2 * kTileRows / KT : 0;
+    c.q0 = Lk >= Lq ? (Lk - Lq + KT - 1) / KT : -((Lq - Lk) / KT);
+    return c;
+  }
+  // of the sequence that the thread holds
+  __device__ int64_t work(const TileParams& p, int64_t* items) const {
+    const TileCount c = count(p, Lq, Lk);
+    *items += static_cast<int64_t>(c.blocks) * p.items;
+    return c.sum(c.blocks) * p.items;
+  }
+};
+
+// Walks a block's pieces, a whole warp at once.
 template <int KT, bool PAGED>
 struct TileWalk {
   int32_t b, item, blk, t;                  // next: sequence, head, row block, key tile
@@ -165,28 +208,15 @@ struct TileWalk {
   TilePiece w;                              // of the sequence that c is of: its spans
   TileCount c;
   int32_t runs;                             // TileRuns
+  TileSpans<KT, PAGED> spans;
 
-  __device__ static TileCount count(const TileParams& p, int32_t b, TilePiece& w) {
-    tile_span(p.cu_q, b, p.B, p.total_q, w.q_start, w.Lq);
-    if (PAGED) {
-      w.k_start = 0;
-      w.Lk = static_cast<int32_t>(min(static_cast<int64_t>(max(__ldg(p.cu_k + b), 0)), p.cap));
-    } else {
-      tile_span(p.cu_k, b, p.B, p.total_k, w.k_start, w.Lk);
-    }
-    const int32_t tokens = 2 * p.join.tb;
-    TileCount c;
-    c.blocks = static_cast<int32_t>((static_cast<uint32_t>(w.Lq) + tokens - 1) / static_cast<uint32_t>(tokens));
-    c.most = max(1, (w.Lk + KT - 1) / KT);
-    c.step = p.causal && !PAGED ? 2 * kTileRows / KT : 0;
-    c.q0 = w.Lk >= w.Lq ? (w.Lk - w.Lq + KT - 1) / KT : -((w.Lq - w.Lk) / KT);
-    return c;
-  }
-  __device__ static int64_t work(const TileParams& p, int32_t b, int64_t* items) {
-    TilePiece w;
-    const TileCount c = count(p, b, w);
-    *items += static_cast<int64_t>(c.blocks) * p.items;
-    return c.sum(c.blocks) * p.items;
+  __device__ TileCount count(const TileParams& p, int32_t b, TilePiece& w) {
+    if (b >= spans.base + 32) spans.load(p, b);
+    w.q_start = __shfl_sync(0xffffffffu, spans.q_start, b - spans.base);
+    w.Lq = __shfl_sync(0xffffffffu, spans.Lq, b - spans.base);
+    w.k_start = __shfl_sync(0xffffffffu, spans.k_start, b - spans.base);
+    w.Lk = __shfl_sync(0xffffffffu, spans.Lk, b - spans.base);
+    return TileSpans<KT, PAGED>::count(p, w.Lq, w.Lk);
   }
   // to offset `off` of sequence b, for `run` tiles
   __device__ void seek(const TileParams& p, int32_t seq, int64_t off, int64_t run, int32_t kind) {
@@ -204,7 +234,7 @@ struct TileWalk {
     c = count(p, b, w);
     const int64_t per_head = c.sum(c.blocks), each = p.heads_first ? p.items : 1;
     if (!p.heads_first) {
-      item = static_cast<int32_t>(off / per_head);
+      item = static_cast<int32_t>(tile_quotient(off, per_head));
       off -= item * per_head;
     }
     int32_t lo = 0, hi = c.blocks - 1;      // the last block that begins at or before off
@@ -216,7 +246,7 @@ struct TileWalk {
     blk = lo;
     off -= c.sum(lo) * each;
     if (p.heads_first) {
-      item = static_cast<int32_t>(off / c.of(blk));
+      item = static_cast<int32_t>(tile_quotient(off, c.of(blk)));
       off -= static_cast<int64_t>(item) * c.of(blk);
     }
     t = static_cast<int32_t>(off);
@@ -337,23 +367,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   using Walk = TileWalk<KT, PAGED>;
 
-  // ---- this block's run of key tiles
-  const int32_t chunk = (p.B + SH::kThreads - 1) / SH::kThreads;
-  const int32_t b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk), b_hi = min(p.B, b_lo + chunk);
-  int64_t mine = 0, items = 0;
-  for (int32_t b = b_lo; b < b_hi; ++b) mine += Walk::work(p, b, &items);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-    items += __shfl_xor_sync(0xffffffffu, items, o);
-  }
-  if (lane == 31) {
-    ms.scan[warp] = incl;
-    ms.scan_items[warp] = items;
-  }
-  if (threadIdx.x == 0) {
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ms.tmem), 512);
+    tmem_relinquish();
+  } else if (threadIdx.x == 0) {
     for (int s = 0; s < SH::kNk; ++s) {
       mbar_init(smem_u32(&ms.k_full[s]), QUANT ? 4 : 1);
       mbar_init(smem_u32(&ms.k_empty[s]), 1);
@@ -379,40 +396,100 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
     fence_mbar_init();
+    p.join.meta[8 * blockIdx.x] = 0;        // nothing to join, unless the first piece says so below
+  } else if (threadIdx.x == 32 * kTmaWarp) {
     prefetch_tensormap(&p.tq);
     prefetch_tensormap(&p.tk);
     prefetch_tensormap(&p.tv);
   }
-  __syncthreads();
-  int64_t before = incl - mine, W = 0;
-  items = 0;
-#pragma unroll
-  for (int w = 0; w < SH::kThreads / 32; ++w) {
-    const int64_t t = ms.scan[w];
-    if (w < warp) before += t;
-    W += t;
-    items += ms.scan_items[w];
-  }
-  // equal runs, but of kTileMinRun tiles at least where the items have that many
-  const int64_t G = gridDim.x;
-  int64_t per = (W + G - 1) / G;
-  if (per < kTileMinRun && items > 0) per = max(per, min(static_cast<int64_t>(kTileMinRun), (W + items - 1) / items));
-  const int32_t runs = items < kTileWholeItems * G ? kRunsCut : p.B <= kTileStrideSeqs ? kRunsStrided : kRunsWhole;
-  const int64_t start = per * blockIdx.x;
   grid_launch_dependents();
-  if (threadIdx.x == 0) p.join.meta[8 * blockIdx.x] = 0;  // nothing to join, unless the first piece says so below
-  if (start >= W && runs != kRunsStrided) return;  // (strided: every block has its 16 items and more)
-  if (before <= start && start < before + mine) {
-    int32_t b = b_lo;
-    int64_t off = start - before;
-    int64_t unused = 0;
-    for (int64_t w; b < b_hi && off >= (w = Walk::work(p, b, &unused)); ++b) off -= w;
-    ms.start_b = b;
-    ms.start_off = off;
-  }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&ms.tmem), 512);
-    tmem_relinquish();
+
+  // ---- this block's run of key tiles.  Up to 32 sequences the warp that walks them finds it
+  // alone, beside the set-up above; more are counted by all threads.
+  const bool few = p.B <= 32;
+  Walk walk;
+  int64_t per = 0, start = 0;
+  if (few ? warp == kPieceWarp : true) {
+    walk.spans.load(p, 0);
+    int64_t mine = 0, items = 0;
+    int32_t b_lo = lane, b_hi = lane;
+    if (few) {
+      if (lane < p.B) mine = walk.spans.work(p, &items);
+    } else {
+      const int32_t chunk = (p.B + SH::kThreads - 1) / SH::kThreads;
+      b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
+      b_hi = min(p.B, b_lo + chunk);
+      TileSpans<KT, PAGED> one;
+      for (int32_t b = b_lo; b < b_hi; ++b) {
+        one.one(p, b);
+        mine += one.work(p, &items);
+      }
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+      items += __shfl_xor_sync(0xffffffffu, items, o);
+    }
+    int64_t before = incl - mine, W = 0;
+    if (few) {
+      W = __shfl_sync(0xffffffffu, incl, 31);
+    } else {
+      if (lane == 31) {
+        ms.scan[warp] = incl;
+        ms.scan_items[warp] = items;
+      }
+      __syncthreads();
+      items = 0;
+#pragma unroll
+      for (int w = 0; w < SH::kThreads / 32; ++w) {
+        const int64_t t = ms.scan[w];
+        if (w < warp) before += t;
+        W += t;
+        items += ms.scan_items[w];
+      }
+    }
+    // equal runs, but of kTileMinRun tiles at least where the items have that many
+    const int64_t G = gridDim.x;
+    per = tile_quotient(W + G - 1, G);
+    if (per < kTileMinRun && items > 0) per = max(per, min(static_cast<int64_t>(kTileMinRun), tile_quotient(W + items - 1, items)));
+    const int32_t runs = items < kTileWholeItems * G ? kRunsCut : p.B <= kTileStrideSeqs ? kRunsStrided : kRunsWhole;
+    start = per * blockIdx.x;
+    const bool here = before <= start && start < before + mine;
+    int32_t at_b = p.B;
+    int64_t at_off = 0;
+    if (few) {
+      const uint32_t at = __ballot_sync(0xffffffffu, here);
+      if (at) {
+        at_b = __ffs(at) - 1;
+        at_off = start - __shfl_sync(0xffffffffu, before, at_b);
+      }
+    } else {
+      if (here) {
+        TileSpans<KT, PAGED> one;
+        int32_t b = b_lo;
+        int64_t off = start - before, unused = 0;
+        for (; b < b_hi; ++b) {
+          one.one(p, b);
+          const int64_t w = one.work(p, &unused);
+          if (off < w) break;
+          off -= w;
+        }
+        ms.start_b = b;
+        ms.start_off = off;
+      }
+      __syncthreads();
+      if (start < W) {
+        at_b = ms.start_b;
+        at_off = ms.start_off;
+      }
+    }
+    if (warp == kPieceWarp) {
+      walk.b = p.B;                         // a block without a run (strided: every block has its 16 items and more)
+      walk.rem = 0;
+      if (W > 0 && (start < W || runs == kRunsStrided)) walk.seek(p, at_b, at_off, min(per, W - start), runs);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -421,18 +498,20 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   volatile int* abort_flag = &ms.abort;
   TilePiece w{};
   Ring pieces;
-
   if (warp >= 8 && warp < 12) {
     set_max_regs_dec<kRegsRest>();
     if (warp == kPieceWarp) {
       // ------------------------------------------------------------ pieces
-      Walk walk;
-      walk.seek(p, ms.start_b, ms.start_off, min(per, W - start), runs);
       bool more = true, first = true;
       while (more) {
         more = walk.next(p);
         walk.w.end = more ? 0 : 1;
         walk.w.first = first ? 1 : 0;
+        if (first && more && walk.w.t0 > 0) {
+          const int64_t item0 = start - walk.w.t0;
+          walk.w.from = static_cast<int32_t>(tile_quotient(item0, per));
+          walk.w.to = static_cast<int32_t>(tile_quotient(item0 + walk.w.T - 1, per));
+        }
         first = false;
         if (!bounded_wait_warp(smem_u32(&ms.piece_empty[pieces.stage]), pieces.parity ^ 1u, p.wait_ns, abort_flag)) break;
         if (lane == 0) {
@@ -733,17 +812,15 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       const int32_t seen = !p.causal ? w.Lk : min(w.Lk, max(0, tok + 1 + w.Lk - w.Lq));
       if (w.first && threadIdx.x == 0 && w.t0 > 0) {
         // the block behind the first cut through an item joins the item's pieces
-        const int64_t item0 = start - w.t0;
-        const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
         int32_t* mt = p.join.meta + 8 * blockIdx.x;
-        mt[1] = first;
-        mt[2] = last;
+        mt[1] = w.from;
+        mt[2] = w.to;
         mt[3] = w.rows[0];
         mt[4] = w.rows[1];
         mt[5] = w.q_start + w.tok;
         mt[6] = w.head;
         mt[7] = w.kv_head;
-        mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+        mt[0] = w.from + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
       }
       // where the row goes
       const bool whole = w.whole();
@@ -970,7 +1047,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 }
 
 template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED>
-cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, cudaStream_t stream) {
+cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cuts, cudaStream_t stream) {
   using SH = TileShape<KS, VS, KT, QUANT>;
   constexpr int smem = SH::kOffMisc + static_cast<int>(sizeof(TileMisc));
   static_assert(smem <= 232448, "shared memory budget");
@@ -987,7 +1064,16 @@ cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, cudaStre
   kernel<<<blocks, SH::kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join(p.join, F16, blocks, items, stream);
+  return cuts ? launch_join(p.join, F16, blocks, items, stream) : cudaSuccess;
+}
+
+// Whether the runs of `blocks` blocks cut items that all count for T key tiles (the kernel's own
+// arithmetic).
+inline bool tile_runs_cut(int64_t items, int64_t T, int64_t blocks) {
+  if (items >= kTileWholeItems * blocks) return false;
+  int64_t per = (items * T + blocks - 1) / blocks;
+  if (per < kTileMinRun) per = std::max(per, std::min<int64_t>(kTileMinRun, T));
+  return per % T != 0;
 }
 
 // Blocks for items of at most `tiles` key tiles: one per SM, and no more than there are items
