@@ -57,8 +57,8 @@ __device__ __forceinline__ float2 channel_quant(const float* scale, const float*
   return make_float2(__ldg(scale + i), offset ? __ldg(offset + i) : 0.f);
 }
 
-// Blocks (x, *) take the x-th, x + gridDim.x-th, ... block of the main kernel that says in
-// `meta` that an item's first cut lies before it.  An item of few pieces: a warp takes four
+// Blocks (x, *) join the item whose first cut lies before block x of the main kernel, where its
+// `meta` says that there is one.  An item of few pieces: a warp takes four
 // rows' 128 channels at once, the rows' statistics side by side in its lanes, so that the
 // loads of four rows are in flight.  One with many: the block's eight warps take every
 // eighth piece of one row's 128 channels, and their sums are added in a fixed order.
@@ -70,10 +70,10 @@ struct JoinRow {
   int32_t part;                             // row of a part
   int64_t token, head;
 };
-__device__ __forceinline__ JoinRow join_row(const JoinParams& p, const int32_t* mt, int32_t r) {
-  const int32_t rows0 = mt[3], in = r < rows0 ? r : r - rows0;      // row of its subtile
+__device__ __forceinline__ JoinRow join_row(const JoinParams& p, int32_t rows0, int32_t tok0, int32_t head0, int32_t r) {
+  const int32_t in = r < rows0 ? r : r - rows0;                     // row of its subtile
   const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(in) / static_cast<uint32_t>(p.hb));
-  return JoinRow{r < rows0 ? r : p.sub + in, mt[5] + (r < rows0 ? 0 : p.tb) + t, mt[6] + in - t * p.hb};
+  return JoinRow{r < rows0 ? r : p.sub + in, tok0 + (r < rows0 ? 0 : p.tb) + t, head0 + in - t * p.hb};
 }
 template <bool F16>
 __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& row, int32_t kv_head, int32_t ch, float4 acc,
@@ -95,144 +95,131 @@ __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t blocks) {
+__global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sum[kJoinWarps][32];
   grid_dependency_wait();                   // launched while the main kernel's last blocks still run
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NR = p.NR, slices = (p.Dv + 127) / 128;
-  uint32_t has[kJoinLoads];
+  const int4 m0 = *reinterpret_cast<const int4*>(p.meta + 8 * blockIdx.x);
+  const int4 m1 = *reinterpret_cast<const int4*>(p.meta + 8 * blockIdx.x + 4);
+  if (m0.x == 0) return;                    // no item whose first cut lies before block x
+  const int32_t first = m0.y, n = m0.z - first + 1, rows0 = m0.w, rows = m0.w + m1.x, tok0 = m1.y, head0 = m1.z, kv_head = m1.w;
+  auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+  if (n <= kJoinFew) {
+    const int32_t units = (rows + 3) / 4 * slices;
+    for (int32_t unit = blockIdx.y * kJoinWarps + warp; unit < units; unit += gridDim.y * kJoinWarps) {
+      const int32_t r0 = unit / slices * 4, ch = (unit % slices) * 128 + lane * 4;
+      const int32_t mine = r0 + (lane >> 3), piece = lane & 7;
+      float4 st = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+      JoinRow row = join_row(p, rows0, tok0, head0, min(mine, rows - 1));
+      if (mine < rows && piece < n) st = p.stats[slot(piece) * NR + row.part];
+      float m = st.x, k0 = st.y != 0.f ? st.z : neg_inf();  // the same in every piece that saw a key
 #pragma unroll
-  for (int i = 0; i < kJoinLoads; ++i) has[i] = 32 * i + lane < blocks && p.meta[8 * (32 * i + lane)] != 0;
-#pragma unroll
-  for (int i = 0; i < kJoinLoads; ++i) has[i] = __ballot_sync(0xffffffffu, has[i]);
-  for (int32_t x = blockIdx.x;; x += gridDim.x) {
-    int32_t c = -1, skip = x;               // the x-th flagged block
-#pragma unroll
-    for (int i = 0; i < kJoinLoads; ++i) {
-      const int32_t here = __popc(has[i]);
-      if (c < 0 && skip < here) c = 32 * i + __fns(has[i], 0, skip + 1);
-      skip -= here;
-    }
-    if (c < 0) return;
-    const int32_t* mt = p.meta + 8 * c;
-    const int32_t first = mt[1], n = mt[2] - first + 1, rows = mt[3] + mt[4], kv_head = mt[7];
-    auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-    if (n <= kJoinFew) {
-      const int32_t units = (rows + 3) / 4 * slices;
-      for (int32_t unit = blockIdx.y * kJoinWarps + warp; unit < units; unit += gridDim.y * kJoinWarps) {
-        const int32_t r0 = unit / slices * 4, ch = (unit % slices) * 128 + lane * 4;
-        const int32_t mine = r0 + (lane >> 3), piece = lane & 7;
-        float4 st = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
-        JoinRow row = join_row(p, mt, min(mine, rows - 1));
-        if (mine < rows && piece < n) st = p.stats[slot(piece) * NR + row.part];
-        float m = st.x, k0 = st.y != 0.f ? st.z : neg_inf();  // the same in every piece that saw a key
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
-        }
-        const float wt = st.y != 0.f ? ex2(st.x - m) : 0.f;
-        float l = st.y * wt;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (piece == 0 && mine < rows && unit % slices == 0 && p.lse) join_lse(p, row, m, l, k0);
-        float4 acc[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int32_t i = 0; i < n; ++i) {
-          float4 v[4];
-          float w[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            w[t] = __shfl_sync(0xffffffffu, wt, 8 * t + i);
-            const int32_t part = __shfl_sync(0xffffffffu, row.part, 8 * t);
-            v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w[t] != 0.f && ch < p.Dv)   // a piece that saw nothing stored no accumulator
-              v[t] = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + part) * p.Dv + ch);
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            acc[t].x = fmaf(v[t].x, w[t], acc[t].x);
-            acc[t].y = fmaf(v[t].y, w[t], acc[t].y);
-            acc[t].z = fmaf(v[t].z, w[t], acc[t].z);
-            acc[t].w = fmaf(v[t].w, w[t], acc[t].w);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float lt = __shfl_sync(0xffffffffu, l, 8 * t);
-          JoinRow rt;
-          rt.token = __shfl_sync(0xffffffffu, row.token, 8 * t);
-          rt.head = __shfl_sync(0xffffffffu, row.head, 8 * t);
-          if (r0 + t < rows && ch < p.Dv) join_store<F16>(p, rt, kv_head, ch, acc[t], lt);
-        }
-      }
-      continue;
-    }
-    for (int32_t unit = blockIdx.y; unit < rows * slices; unit += gridDim.y) {
-      const int32_t ch = (unit % slices) * 128 + lane * 4;
-      const JoinRow row = join_row(p, mt, unit / slices);
-      // every lane holds the statistics of pieces lane, lane + 32, ...
-      float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
-      float4 st[kJoinLoads];
-#pragma unroll
-      for (int i = 0; i < kJoinLoads; ++i) {
-        st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
-        if (32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + row.part];
-      }
-#pragma unroll
-      for (int i = 0; i < kJoinLoads; ++i) {
-        m = fmaxf(m, st[i].x);
-        if (st[i].y != 0.f) k0 = st[i].z;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
+      for (int o = 4; o > 0; o >>= 1) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
       }
+      const float wt = st.y != 0.f ? ex2(st.x - m) : 0.f;
+      float l = st.y * wt;
 #pragma unroll
-      for (int i = 0; i < kJoinLoads; ++i) {
-        wt[i] = st[i].y != 0.f ? ex2(st[i].x - m) : 0.f;
-        l = fmaf(st[i].y, wt[i], l);
-      }
+      for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (piece == 0 && mine < rows && unit % slices == 0 && p.lse) join_lse(p, row, m, l, k0);
+      float4 acc[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kJoinLoads; ++i) {
-        if (32 * i >= n) break;
+      for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int32_t i = 0; i < n; ++i) {
         float4 v[4];
         float w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int e = warp + kJoinWarps * k;
-          w[k] = __shfl_sync(0xffffffffu, wt[i], e);
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (w[k] != 0.f && ch < p.Dv)
-            v[k] = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + row.part) * p.Dv + ch);
+        for (int t = 0; t < 4; ++t) {
+          w[t] = __shfl_sync(0xffffffffu, wt, 8 * t + i);
+          const int32_t part = __shfl_sync(0xffffffffu, row.part, 8 * t);
+          v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w[t] != 0.f && ch < p.Dv)   // a piece that saw nothing stored no accumulator
+            v[t] = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + part) * p.Dv + ch);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          acc.x = fmaf(v[k].x, w[k], acc.x);
-          acc.y = fmaf(v[k].y, w[k], acc.y);
-          acc.z = fmaf(v[k].z, w[k], acc.z);
-          acc.w = fmaf(v[k].w, w[k], acc.w);
+        for (int t = 0; t < 4; ++t) {
+          acc[t].x = fmaf(v[t].x, w[t], acc[t].x);
+          acc[t].y = fmaf(v[t].y, w[t], acc[t].y);
+          acc[t].z = fmaf(v[t].z, w[t], acc[t].z);
+          acc[t].w = fmaf(v[t].w, w[t], acc[t].w);
         }
       }
-      sum[warp][lane] = acc;
-      __syncthreads();
-      if (warp == 0) {
 #pragma unroll
-        for (int i = 1; i < kJoinWarps; ++i) {
-          const float4 v = sum[i][lane];
-          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-        }
-        if (lane == 0 && ch < 128 && p.lse) join_lse(p, row, m, l, k0);
-        if (ch < p.Dv) join_store<F16>(p, row, kv_head, ch, acc, l);
+      for (int t = 0; t < 4; ++t) {
+        const float lt = __shfl_sync(0xffffffffu, l, 8 * t);
+        JoinRow rt;
+        rt.token = __shfl_sync(0xffffffffu, row.token, 8 * t);
+        rt.head = __shfl_sync(0xffffffffu, row.head, 8 * t);
+        if (r0 + t < rows && ch < p.Dv) join_store<F16>(p, rt, kv_head, ch, acc[t], lt);
       }
-      __syncthreads();
     }
+    return;
+  }
+  for (int32_t unit = blockIdx.y; unit < rows * slices; unit += gridDim.y) {
+    const int32_t ch = (unit % slices) * 128 + lane * 4;
+    const JoinRow row = join_row(p, rows0, tok0, head0, unit / slices);
+    // every lane holds the statistics of pieces lane, lane + 32, ...
+    float m = neg_inf(), l = 0.f, k0 = neg_inf(), wt[kJoinLoads];
+    float4 st[kJoinLoads];
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      st[i] = make_float4(neg_inf(), 0.f, neg_inf(), 0.f);
+      if (32 * i + lane < n) st[i] = p.stats[slot(32 * i + lane) * NR + row.part];
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      m = fmaxf(m, st[i].x);
+      if (st[i].y != 0.f) k0 = st[i].z;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      wt[i] = st[i].y != 0.f ? ex2(st[i].x - m) : 0.f;
+      l = fmaf(st[i].y, wt[i], l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      if (32 * i >= n) break;
+      float4 v[4];
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = warp + kJoinWarps * k;
+        w[k] = __shfl_sync(0xffffffffu, wt[i], e);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[k] != 0.f && ch < p.Dv)
+          v[k] = *reinterpret_cast<const float4*>(p.parts + (slot(32 * i + e) * NR + row.part) * p.Dv + ch);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc.x = fmaf(v[k].x, w[k], acc.x);
+        acc.y = fmaf(v[k].y, w[k], acc.y);
+        acc.z = fmaf(v[k].z, w[k], acc.z);
+        acc.w = fmaf(v[k].w, w[k], acc.w);
+      }
+    }
+    sum[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 1; i < kJoinWarps; ++i) {
+        const float4 v = sum[i][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      if (lane == 0 && ch < 128 && p.lse) join_lse(p, row, m, l, k0);
+      if (ch < p.Dv) join_store<F16>(p, row, kv_head, ch, acc, l);
+    }
+    __syncthreads();
   }
 }
 
@@ -240,11 +227,11 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
 // place while that kernel still runs (programmatic stream serialisation).
 inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
-  // the cuts that there can be, and blocks for each that fill the SMs
+  // the cuts that there can be, and blocks for each that fill the SMs, four on each, once
   const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), units = p.NR * ((p.Dv + 127) / 128);
-  const int y = std::max(1, std::min(units, (8 * device_sm_count() + cuts - 1) / cuts));
+  const int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(cuts, y);
+  cfg.gridDim = dim3(blocks, y);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -252,8 +239,8 @@ inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, p, static_cast<int32_t>(blocks))
-             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, p, static_cast<int32_t>(blocks));
+  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, p)
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, p);
 }
 
 inline size_t join_meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }

@@ -223,8 +223,8 @@ __device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float
     else
       asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t[i].y), "f"(t[i].x));
     if constexpr (LO) {
-      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[i]) : "f"(t[i].y - h.y), "f"(t[i].x - h.x));
+      const float2 rest = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&w[i])), make_float2(-1.f, -1.f), t[i]);
+      asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo[i]) : "f"(rest.y), "f"(rest.x));
     }
   }
 }

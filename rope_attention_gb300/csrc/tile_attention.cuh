@@ -149,6 +149,7 @@ struct TileMisc {
   uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_ready[2], o_done[2], drain;
   uint64_t piece_full[kTilePieces], piece_empty[kTilePieces];
   uint64_t valid[kTileValid][2];
+  uint32_t holes[kTileValid];               // whether a page before the sequence's end is absent
   TilePiece pieces[kTilePieces];
   int64_t scan[16], scan_items[16];
   int64_t start_off;
@@ -618,6 +619,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               if (lane == 0) {
                 ms.valid[u % kTileValid][0] = lo;
                 ms.valid[u % kTileValid][1] = hi;
+                ms.holes[u % kTileValid] = live != min(groups, (w.Lk - t * KT + p.box_rows - 1) >> p.box_shift);
               }
               __syncwarp();
             }
@@ -905,8 +907,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           for (int c = 0; c < KT; ++c)
             if (c >= nv) s[c] = __float_as_uint(neg_inf());
         }
+        const bool holes = PAGED && ms.holes[(u + j) % kTileValid] != 0;
         uint64_t gap[2] = {0, 0};           // keys before the end that do not exist (bad pages)
-        if (PAGED) {
+        if (holes) {
           const int32_t end = w.Lk - t * KT;
           const uint64_t* v = ms.valid[(u + j) % kTileValid];
           gap[0] = ~v[0] & (end >= 64 ? ~0ull : (1ull << end) - 1);
@@ -914,11 +917,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             const int32_t keys = min(end, KT) - 64;
             gap[1] = keys <= 0 ? 0ull : ~v[1] & (keys >= 64 ? ~0ull : (1ull << keys) - 1);
           }
-          if ((gap[0] | gap[1]) != 0) {
 #pragma unroll
-            for (int c = 0; c < KT; ++c)
-              if ((gap[c >> 6] >> (c & 63)) & 1) s[c] = __float_as_uint(neg_inf());
-          }
+          for (int c = 0; c < KT; ++c)
+            if ((gap[c >> 6] >> (c & 63)) & 1) s[c] = __float_as_uint(neg_inf());
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -958,7 +959,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l += sum.x + sum.y;
-        if (!QUANT && ((t + 1) * KT > w.Lk || (gap[0] | gap[1]) != 0)) {
+        if (!QUANT && ((t + 1) * KT > w.Lk || holes)) {
           // value rows that are no key's meet P = 0, but 0 times a stray NaN or infinity is
           // NaN: zero them in shared memory
           const int32_t end = w.Lk - t * KT;
