@@ -276,7 +276,8 @@ def test_register_budgets(file, kernel, budget, tmp_path):
     # the softmax warps run with more registers than ptxas was given: a few words that live
     # across their loops may spill
     assert all(spill <= (384 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
-    assert all(regs <= 128 and spill == 0 for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
+    # four blocks of 256 threads an SM
+    assert all(regs <= 64 and spill <= 128 for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
 
 
 # ---------------------------------------------------------------- the oracle

@@ -169,8 +169,8 @@ def test_on_a_stream_behind_the_writer(name):
     torch.cuda.synchronize()
     if isinstance(x, Paged):
         x.kv.run(s.cuda_stream)
-    for _ in range(2):  # the second call reuses the workspace that the first one's join reads
-        x.run(s.cuda_stream)
+    for stream in (s.cuda_stream, s):  # the second call reuses the workspace that the first one's join reads
+        x.run(stream)
     s.synchronize()
     assert x.status() == 0
     x.check("on its own stream")
