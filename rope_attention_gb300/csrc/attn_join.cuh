@@ -246,13 +246,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 // place while that kernel still runs (programmatic stream serialisation).
 inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
-  // the cuts that there can be, and blocks for each that fill the SMs, four on each, once
-  const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), units = p.NR * ((p.Dv + 127) / 128);
-  const int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
-  cudaLaunchConfig_t cfg{};
+  const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), slices = (p.Dv + 127) / 128;
   // (MLA decode, 8 items over 152 blocks: 61 us with the search, 74 with 144 empty blocks a row;
   // 151 cuts: 159 us without it, 168 with)
   const bool search = cuts * 4 < blocks;
+  // blocks for each cut that there can be, as many as fill the SMs, four on each, once, and have
+  // something to do: of few pieces a warp joins four rows, of many the block one
+  const int units = search ? p.NR * slices : ((p.NR + 3) / 4 * slices + kJoinWarps - 1) / kJoinWarps;
+  const int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
+  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(search ? cuts : blocks, y);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
