@@ -5,6 +5,10 @@
 // gets a part of an item stores the part's (max, sum, accumulator) in the workspace; the
 // second kernel here joins an item's parts in the order of the blocks, so results do not
 // depend on which block finished first.
+//
+// The join is bound by latency: a chain of dependent loads (the cut, the statistics, the parts)
+// behind a launch, 7 to 13 us of 44 to 160 where every item is cut (40 MB of parts, mostly from
+// L2).  Where the host knows that nothing is cut it is not launched.
 #pragma once
 
 #include <algorithm>
@@ -94,8 +98,10 @@ __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row
   p.lse[row.token * p.heads + row.head] = l != 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
 }
 
-template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t search) {
+// RESIDENT blocks an SM: four for few pieces (64 registers), two for many, whose statistics the
+// block holds in registers.
+template <bool F16, int RESIDENT>
+__global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t search) {
   __shared__ float4 sum[kJoinWarps][32];
   grid_dependency_wait();                   // launched while the main kernel's last blocks still run
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
   const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), slices = (p.Dv + 127) / 128;
-  // (MLA decode, 8 items over 152 blocks: 61 us with the search, 74 with 144 empty blocks a row;
+  // (MLA decode, 8 items over 152 blocks: 59 us with the search, 74 with 144 empty blocks a row;
   // 151 cuts: 159 us without it, 168 with)
   const bool search = cuts * 4 < blocks;
   // blocks for each cut that there can be, as many as fill the SMs, four on each, once, and have
@@ -263,8 +269,11 @@ inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, p, search ? blocks : 0)
-             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, p, search ? blocks : 0);
+  if (search)
+    return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 2>, p, blocks)
+               : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 2>, p, blocks);
+  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 4>, p, 0)
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 4>, p, 0);
 }
 
 inline size_t join_meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }

@@ -125,7 +125,7 @@ def test_paged_accepts(L):
     ({}, {}, dict(q=None), -1), ({}, {}, dict(kc=None), -1), ({}, {}, dict(vc=None), -1), ({}, {}, dict(lens=None), -1),
     ({}, {}, dict(table=None), -1), ({}, {}, dict(out=None), -1), ({}, {}, dict(ws=None), -1), ({}, {}, dict(q=A16 + 8), -3),
     ({}, {}, dict(kc=A16 + 8), -3), ({}, {}, dict(lens=A16 + 2), -3), ({}, {}, dict(err=A16 + 1), -3),
-    ({}, {}, dict(ws=A16 + 8), -3), ({}, {}, dict(n=4096), -4),
+    ({}, {}, dict(ws=A16 + 8), -3), ({}, {}, dict(n=300), -4), ({}, dict(max_seq_len=1000), dict(n=4096), -4),
     (dict(cache_mode=native.RA_CACHE_NORM, cache_seq_len=64, B=3), dict(block_table_stride=0), dict(table=None), -1),
     (dict(cache_mode=native.RA_CACHE_NORM, cache_seq_len=64), dict(block_table_stride=0), {}, -1),
     (dict(cache_mode=native.RA_CACHE_NORM, cache_seq_len=0), dict(block_table_stride=0), dict(table=None), -1),
@@ -276,8 +276,9 @@ def test_register_budgets(file, kernel, budget, tmp_path):
     # the softmax warps run with more registers than ptxas was given: a few words that live
     # across their loops may spill
     assert all(spill <= (384 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
-    # four blocks of 256 threads an SM
-    assert all(regs <= 64 and spill <= 128 for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
+    # four blocks of 256 threads an SM, or two
+    assert all((regs <= 64 and spill <= 128) if "Li4" in n else (regs <= 128 and spill == 0)
+               for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
 
 
 # ---------------------------------------------------------------- the oracle

@@ -331,3 +331,44 @@ def test_a_second_call_gives_the_same_bits(name):
         x.out.fill_(7.0)
         x.run()
         assert torch.equal(x.out.view(torch.int16), first.view(torch.int16)) and torch.equal(x.lse, lse)
+
+
+@pytest.mark.parametrize("name", ["decode", "chunk_int8"])
+def test_blockwise_written_caches_have_the_bnsd_layout(name):
+    x = CASES[name](13)
+    write_cache(x)
+    x.run()
+    first = x.out.clone()
+    x.out.fill_(7.0)
+    x.kv.params.cache_mode = native.RA_CACHE_PA_BLK_BNSD
+    x.run()
+    assert torch.equal(x.out.view(torch.int16), first.view(torch.int16))
+
+
+def test_two_threads_call_at_once():
+    """Two host threads, each with its own stream, workspace and case."""
+    import threading
+
+    cases, errors = [CASES["decode"](14), CASES["chunk_int8"](15)], []
+    for c in cases:
+        write_cache(c)
+    torch.cuda.synchronize()
+
+    def work(c):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                c.run(s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001 -- reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for c in cases:
+        assert c.status() == 0
+        c.check("beside another thread")
