@@ -67,7 +67,7 @@ __device__ __forceinline__ float2 channel_quant(const float* scale, const float*
 // loads of four rows are in flight.  One with many: the block's eight warps take every
 // eighth piece of one row's 128 channels, and their sums are added in a fixed order.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinFew = 8;                 // pieces up to which a warp takes rows alone
+constexpr int kJoinFew = 8, kJoinFewItems = 4;  // pieces up to which a warp takes rows alone; where few items are cut
 constexpr int kJoinLoads = (kMaxBlocks + 31) / 32;
 
 struct JoinRow {
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
   if (m0.x == 0) return;                    // no item whose first cut lies before block x
   const int32_t first = m0.y, n = m0.z - first + 1, rows0 = m0.w, rows = m0.w + m1.x, tok0 = m1.y, head0 = m1.z, kv_head = m1.w;
   auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-  if (n <= kJoinFew) {
+  if (n <= (RESIDENT == 2 ? kJoinFewItems : kJoinFew)) {
     const int32_t units = (rows + 3) / 4 * slices;
     for (int32_t unit = blockIdx.y * kJoinWarps + warp; unit < units; unit += gridDim.y * kJoinWarps) {
       const int32_t r0 = unit / slices * 4, ch = (unit % slices) * 128 + lane * 4;

@@ -18,7 +18,7 @@
 namespace ra {
 namespace {
 
-constexpr int64_t kKeysInL2 = 48 << 20;     // of the 126 MB
+constexpr int64_t kKeysInL2 = 48 << 20;     // of the 129 MB
 
 // [tokens, heads, d] with any strides as a 3-D map of 64 x 128-token boxes; the axis with
 // the smaller stride comes second

@@ -65,11 +65,11 @@ constexpr int kSoftmax = 256, kSoftmaxWarps = kSoftmax / 32, kConvertWarps = 4;
 constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kValidRing = 16;            // > tiles between the loads and the softmax
 constexpr int kMaxStages = 6;
-constexpr int kMinTiles = 4;              // tiles per block below which a split costs more than it gives
-// Tiles of the longest sequence up to which items are not cut: the join that a cut needs costs
-// about what three tiles do (one token, 8 heads: 333 positions 16.6 us whole and 18.7 cut, 450
-// positions 18.6 and 16.9).
-constexpr int kWholeTiles = 6;
+// Items are cut where that saves a block more tiles than the join costs: kJoinTiles, and up to
+// kJoinAll more the more blocks have a cut.  (V2, one sequence, 2 kv heads: 200 positions 12.6 us
+// whole and 14.5 cut, 333 15.6 and 12.6, 450 18.6 and 12.6; 64 items: 600 positions 20.7 whole and
+// 25.1 cut, 1000 26 and 29, 2000 39 and 33.  V1, 4 items: 333 positions 27 and 23.)
+constexpr int kJoinTiles = 4, kJoinAll = 10;
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSmemMax = 232448;
@@ -429,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   }
   const int64_t G = gridDim.x;
   const int64_t even = W >> 31 ? (W + G - 1) / G : static_cast<int64_t>((static_cast<uint32_t>(W) + static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(G));
-  const int64_t per = max(even, static_cast<int64_t>(p.whole ? 1 : kMinTiles));
-  const int64_t start = per * blockIdx.x;
+  const int64_t per = max(even, static_cast<int64_t>(1)), start = per * blockIdx.x;
   walk.rem = max(static_cast<int64_t>(0), min(per, W - start));  // none: the block has nothing to do
   const bool here = before <= start && start < before + mine;
   if (few) {
@@ -973,7 +972,7 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   pl->off_staging = pl->off_ring + pl->ns * pl->stage;
   pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
-  // one block per SM, and no more than there are runs of kMinTiles at the largest lengths
+  // one block per SM, and no more than there are tiles at the largest lengths
   pl->hb = std::min(g, nr);
   pl->tb = nr / pl->hb;
   pl->hblocks = g > nr ? (g + nr - 1) / nr : 1;
@@ -981,8 +980,9 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
   pl->items = rts * L.N;
   const int64_t T = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
-  pl->whole = T <= kWholeTiles;
-  const int64_t runs = pl->whole ? pl->items : (rts * L.N * T + kMinTiles - 1) / kMinTiles;
+  const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
+  pl->whole = (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
+  const int64_t runs = pl->whole ? pl->items : pl->items * T;
   pl->G = static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs)));
   return true;
 }
