@@ -37,7 +37,7 @@
 // a 64-key tile for V2 int8 (TMA issue 700, conversion 1400, softmax 1600, overlapped), 4900 for
 // V1 (74 KB a tile; 36 + 16 products).  Measured: 8 sequences of 4096 positions, 64 heads over 8,
 // int8: 43 us (55 MB, 1.3 TB/s); 32 sequences of the 576-wide latent, 128 heads, bf16: 77 us (296
-// TFLOP/s); one of 333 positions: 15 us, of which 6 are the block's start.
+// TFLOP/s); one of 333 positions, 8 heads over 2: 12 us, of which 5 are the block's start.
 // Every wait is bounded in time (status word).
 #include <algorithm>
 #include <atomic>
@@ -68,7 +68,7 @@ constexpr int kMaxStages = 6;
 // Items are cut where that saves a block more tiles than the join costs: kJoinTiles, and up to
 // kJoinAll more the more blocks have a cut.  (V2, one sequence, 2 kv heads: 200 positions 12.6 us
 // whole and 14.5 cut, 333 15.6 and 12.6, 450 18.6 and 12.6; 64 items: 600 positions 20.7 whole and
-// 25.1 cut, 1000 26 and 29, 2000 39 and 33.  V1, 4 items: 333 positions 27 and 23.)
+// 25.1 cut, 1000 26.3 and 29.0.  V1, 4 items: 333 positions 27.0 and 22.9.)
 constexpr int kJoinTiles = 4, kJoinAll = 10;
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
 constexpr uint64_t kDrainNs = 200000000ull;
