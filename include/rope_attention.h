@@ -418,7 +418,7 @@ ra_status packed_attention_workspace_bytes(const packed_attention_params* p, siz
 
 /* One call.
  *   q, k, v       strided as above, 16-byte aligned; out likewise, no two elements of
- *                 out in one place.  A NaN in a row of q makes that row of out NaN; an
+ *                 out in one place and none in one with an input's.  A NaN in a row of q makes that row of out NaN; an
  *                 infinity or NaN in a row of k or v can reach every row of its
  *                 sequence, those that the causal mask keeps from it too.  Rows
  *                 outside every sequence may hold anything and the matching rows of
@@ -487,7 +487,7 @@ ra_status paged_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* c
  *   cu_seqlens_q  [B + 1] int32 as in packed_attention; NULL: total_q / B tokens each.
  *   k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset  as given to
  *                 kv_rms_norm_rope_cache.
- *   out           [total_q, num_heads, Dv] kv_dtype, 16-byte aligned.
+ *   out           [total_q, num_heads, Dv] kv_dtype, 16-byte aligned; not on q.
  *   lse           [total_q, num_heads] fp32, or NULL.
  *   dev_error_count  optional int32 device counter, raised when a page number that a
  *                 sequence needs is outside [0, block_num): that page's keys are left out.

@@ -394,14 +394,6 @@ ra_status check_packed(const packed_attention_params* p) {
   return RA_OK;
 }
 
-// Makes the device's context current to a host thread that has made no CUDA call yet: tensor
-// maps are encoded by the driver, which does not do that by itself.
-cudaError_t bind_device() {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  return e == cudaSuccess ? cudaSetDevice(dev) : e;
-}
-
 ra_status check_attn_workspace(const void* workspace, size_t have, size_t need) {
   if (!workspace) return fail(RA_ERR_INVALID_ARG, "workspace is required");
   if (!aligned16(workspace)) return fail(RA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
@@ -844,8 +836,7 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
   L.wait_ns = g_wait_ns.load();
   L.stall_loads = g_stall_next_attn.exchange(0);
   const char* why = "launch failed";
-  cudaError_t e = bind_device();
-  if (e == cudaSuccess) e = ra::launch_packed_attention(L, static_cast<cudaStream_t>(stream), &why);
+  const cudaError_t e = ra::launch_packed_attention(L, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "packed_attention: %s (%s)", why, cudaGetErrorString(e));
   return ok();
 }
@@ -909,8 +900,7 @@ ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const page
   L.wait_ns = g_wait_ns.load();
   L.stall_loads = g_stall_next_attn.exchange(0);
   const char* why = "launch failed";
-  cudaError_t e = bind_device();
-  if (e == cudaSuccess) e = ra::launch_paged_attention(L, static_cast<cudaStream_t>(stream), &why);
+  const cudaError_t e = ra::launch_paged_attention(L, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "paged_attention: %s (%s)", why, cudaGetErrorString(e));
   return ok();
 }

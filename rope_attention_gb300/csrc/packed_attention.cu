@@ -57,9 +57,11 @@ size_t packed_attention_workspace(const PackedLaunch& L) { return kAttnHeader + 
 
 cudaError_t launch_packed_attention(const PackedLaunch& L, cudaStream_t stream, const char** why) {
   TileParams p{};
-  if (!make_view_map(&p.tq, L.q, L.total_q, L.nq, L.d, L.q_ts, L.q_hs, &p.q_swap) ||
-      !make_view_map(&p.tk, L.k, L.total_k, L.nkv, L.d, L.k_ts, L.k_hs, &p.k_swap) ||
-      !make_view_map(&p.tv, L.v, L.total_k, L.nkv, L.d, L.v_ts, L.v_hs, &p.v_swap)) {
+  if (!encode_maps([&] {
+        return make_view_map(&p.tq, L.q, L.total_q, L.nq, L.d, L.q_ts, L.q_hs, &p.q_swap) &&
+               make_view_map(&p.tk, L.k, L.total_k, L.nkv, L.d, L.k_ts, L.k_hs, &p.k_swap) &&
+               make_view_map(&p.tv, L.v, L.total_k, L.nkv, L.d, L.v_ts, L.v_hs, &p.v_swap);
+      })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

@@ -1082,7 +1082,10 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.hblocks = pl.hblocks;
   p.box_rows = L.mode == kModeNorm || L.block_size % 64 == 0 ? 64 : L.block_size % 32 == 0 ? 32 : 16;
   p.box_shift = p.box_rows == 64 ? 6 : p.box_rows == 32 ? 5 : 4;
-  if (!make_q_map(&p.tq, L, pl.hb, pl.tb) || !make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) || !make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows)) {
+  if (!encode_maps([&] {
+        return make_q_map(&p.tq, L, pl.hb, pl.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
+               make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows);
+      })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

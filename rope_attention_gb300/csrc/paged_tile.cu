@@ -91,8 +91,10 @@ cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const c
   p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
   p.wait_ns = static_cast<uint64_t>(L.wait_ns);
   p.stall_loads = L.stall_loads;
-  if (!make_q_map(&p.tq, L, p.join.hb, p.join.tb) || !make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) ||
-      !make_map(&p.tk, L.k_cache, L, L.Dkv, L.kq, p.box_rows)) {
+  if (!encode_maps([&] {
+        return make_q_map(&p.tq, L, p.join.hb, p.join.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
+               make_map(&p.tk, L.k_cache, L, L.Dkv, L.kq, p.box_rows);
+      })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

@@ -118,7 +118,7 @@ class Args {
              std::to_string(c10::cuda::current_device()));
     }
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev_).stream();
-    PyObject* held = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : Py_NewRef(o);
+    PyObject* held = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Index(o);
     if (held == nullptr) throw Refused{};
     void* s = PyLong_AsVoidPtr(held);
     Py_DECREF(held);
