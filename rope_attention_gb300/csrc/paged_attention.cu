@@ -78,10 +78,8 @@ constexpr int kSCols = 2 * kKeys;         // TMEM: two S buffers, then O^T
 struct Params {
   CUtensorMap tk, tv;           // the caches' rows: 64 channels x 1 x box_rows boxes
   CUtensorMap tq;               // (channels, heads, tokens): boxes of 64 x hb x tb, a row tile
-  const uint16_t* q;
   uint16_t* out;
   float* lse;
-  const uint8_t *k_cache, *v_cache;
   const float *k_scale, *k_offset, *v_scale, *v_offset;
   const int32_t *cu_q, *seq_lens, *table;
   int32_t* err_count;
@@ -1025,11 +1023,8 @@ cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, co
   p.join.NR = p.join.sub = pl.NR;
   join_place(&p.join, L.partials, pl.G);
   pl.G = std::min(pl.G, device_sm_count());
-  p.q = L.q;
   p.out = L.out;
   p.lse = L.lse;
-  p.k_cache = static_cast<const uint8_t*>(L.k_cache);
-  p.v_cache = static_cast<const uint8_t*>(L.v_cache);
   p.k_scale = L.k_scale;
   p.k_offset = L.k_offset;
   p.v_scale = L.v_scale;

@@ -89,7 +89,7 @@ struct TileShape {
   static constexpr int kSlab = KT * 128;
   static constexpr int kK = KS * kSlab, kV = VS * kSlab;
   static constexpr int kCode = (KS > VS ? KS : VS) * KT * 64;   // a staging slot: a tile's codes of either cache
-  static constexpr int kFree = 232448 - 2 * kQTile - 3072;
+  static constexpr int kFree = 232448 - 2 * kQTile - (3 << 10);  // TileMisc takes less than 3 KB
   static constexpr int kNsg = QUANT ? 2 : 0;
   static constexpr int kPairs = (kFree - kNsg * kCode) / (kK + kV);
   static constexpr int kNv = kPairs > 5 ? 5 : kPairs;
