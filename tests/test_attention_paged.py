@@ -246,3 +246,12 @@ def test_chunk_fp16_and_far_scales():
     run_case(27, variant=2, lens=[200], news=[100], heads=4, N=2, dtype="fp16", kt="int8", vt="e4m3")
     run_case(28, variant=2, lens=[200], news=[100], heads=4, N=2, kt="int8", vt="int8", scale_range=(2e4, 9e4), std=30.0)
     run_case(29, variant=2, lens=[200], news=[100], heads=4, N=2, kt="int8", vt="int8", offsets=False)
+
+
+@pytest.mark.parametrize("kt", ["bf16", "int8"])
+def test_cut_runs_over_more_sequences_than_a_warp_holds(kt):
+    rng = np.random.default_rng(1)
+    lens = [int(x) for x in rng.integers(0, 1500, 70)]
+    run_case(30, variant=2, lens=lens, news=[1] * 70, heads=2, N=1, Dkv=64, Dv=64, R=32, kt=kt, vt=kt, max_len=5000)
+    news = [int(min(n, x)) for n, x in zip(lens, rng.integers(0, 120, 70))]
+    run_case(31, variant=2, lens=lens, news=news, heads=4, N=2, Dkv=64, Dv=64, R=32, kt=kt, vt=kt, tail=2)

@@ -242,10 +242,11 @@ def test_prompt_then_decode_over_the_cache(variant, quant):
 
 @pytest.mark.parametrize("lens,nq,causal", [
     ([40] * 20, 128, True),                # strided whole items: 16 or more for each block
+    ([40] * 37 + [0] * 5 + [300], 64, True),  # the same over more sequences than a warp holds
     ([9, 300, 0, 33] * 30, 32, True),      # whole items in consecutive runs, over many sequences
     ([9, 300, 0, 33] * 30, 32, False),
     ([1] * 300, 16, False),
-], ids=["strided", "runs_causal", "runs_full", "single_tokens"])
+], ids=["strided", "strided_more", "runs_causal", "runs_full", "single_tokens"])
 def test_many_items_per_block(lens, nq, causal):
     x = Packed(7, lens, nq, max(1, nq // 4), 64, causal)
     x.run()
@@ -372,3 +373,53 @@ def test_two_threads_call_at_once():
     for c in cases:
         assert c.status() == 0
         c.check("beside another thread")
+
+
+def test_rows_and_strides_past_32_bits():
+    """Pages and heads more than 2^32 bytes into their tensors."""
+    Dk, Dv, bs, pages = 192, 128, 128, 90000        # 4.4 GB of keys, 2.9 GB of values
+    kc = torch.empty(pages, 1, bs, Dk, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty(pages, 1, bs, Dv, dtype=torch.bfloat16, device="cuda")
+    table = np.array([[pages - 1, 3, pages - 2]], np.int32)
+    (kb, kv), (vb, vv) = (half_values(16, i, (3, 1, bs, w), "bf16") for i, w in enumerate((Dk, Dv)))
+    at = torch.from_numpy(table[0].astype(np.int64)).cuda()
+    kc[at] = torch.from_numpy(kb.view(np.int16)).cuda().view(torch.bfloat16)
+    vc[at] = torch.from_numpy(vb.view(np.int16)).cuda().view(torch.bfloat16)
+    cache = native.KvRmsNormRopeCacheParams(B=1, N=1, S=300, Dkv=Dk, Dv=Dv, rope_size=64, variant=2,
+                                            cache_mode=native.RA_CACHE_PA_BNSD, block_num=pages, block_size=bs,
+                                            kv_dtype=native.RA_BF16, k_cache_dtype=native.RA_BF16,
+                                            ckv_cache_dtype=native.RA_BF16, epsilon=1e-5)
+    lens = torch.tensor([300], dtype=torch.int32, device="cuda")
+    keys, values = kv.transpose(0, 2, 1, 3).reshape(-1, 1, Dk)[:300], vv.transpose(0, 2, 1, 3).reshape(-1, 1, Dv)[:300]
+    for new in (1, 90):
+        qb, qv = half_values(16, 5, (new, 2, Dk), "bf16")
+        q = torch.from_numpy(qb.view(np.int16)).cuda().view(torch.bfloat16)
+        out, lse = torch.empty(new, 2, Dv, dtype=torch.bfloat16, device="cuda"), torch.empty(new, 2, device="cuda")
+        p = native.PagedAttentionParams(B=1, total_q=new, num_heads=2, causal=1, softmax_scale=Dk ** -0.5, max_seq_len=300,
+                                        block_table_stride=3)
+        ws = torch.zeros(native.paged_attention_workspace_bytes(cache, p), dtype=torch.uint8, device="cuda")
+        native.paged_attention(cache, p, q, kc, vc, lens, out, ws, torch.from_numpy(table).cuda(), lse=lse)
+        ref = oracle.attention.packed_attention(qv, keys, values, starts_q=[0, new], starts_k=[0, 300], scale=p.softmax_scale,
+                                                causal=True)
+        check_attention(out, lse, ref, "far pages", dtype="bf16", Dk=Dk)
+    index = torch.from_numpy((table[0][:, None].astype(np.int64) * bs + np.arange(bs)).reshape(-1)[:300].copy()).cuda()
+    ko = torch.empty(1, 1, 300, Dk, dtype=torch.bfloat16, device="cuda")
+    native.kv_cache_read(cache, index, kc, vc, ko, None)
+    assert np.array_equal(ko[0, 0].double().cpu().numpy(), keys[:, 0])
+    del kc, vc
+
+    # two heads 2^31 + 64 elements apart, inputs and output
+    far = 2 ** 31 + 64
+    buf = torch.empty(far + 4 * 200 * 64, dtype=torch.bfloat16, device="cuda")
+    x = Packed(17, [200], 2, 2, 64, True)
+    views = []
+    for i, t in enumerate((x.q, x.k, x.v, x.out)):
+        v = buf[i * 200 * 64:].as_strided((200, 2, 64), (64, far, 1))
+        v.copy_(t)
+        views.append(v)
+    p = native.packed_attention_params(*views, causal=True)
+    ws = torch.zeros(native.packed_attention_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    native.packed_attention(p, *views, ws, x.lse)
+    torch.cuda.synchronize()
+    x.out = views[3].contiguous()
+    x.check("heads far apart")
