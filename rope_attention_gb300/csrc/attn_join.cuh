@@ -276,13 +276,17 @@ inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_
              : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 4>, p, 0);
 }
 
+// Parts leave the tile kernel as 32-byte stores, and a workspace may start on any 16 bytes: a join
+// is placed on the next 32, in room that is sized for the step there.
+constexpr size_t kJoinAlign = 32, kJoinSlack = kJoinAlign - 16;
 inline size_t join_meta_bytes(int G) { return (static_cast<size_t>(G) * 32 + 255) / 256 * 256; }
 inline size_t join_stats_bytes(int G, int NR) { return static_cast<size_t>(G) * 2 * NR * sizeof(float4); }
 inline size_t join_bytes(int G, int NR, int Dv) {
-  return join_meta_bytes(G) + join_stats_bytes(G, NR) + static_cast<size_t>(G) * 2 * NR * Dv * sizeof(float);
+  return kJoinSlack + join_meta_bytes(G) + join_stats_bytes(G, NR) + static_cast<size_t>(G) * 2 * NR * Dv * sizeof(float);
 }
 // sets the pointers of a join whose workspace was sized for G blocks
 inline void join_place(JoinParams* j, uint8_t* at, int G) {
+  at += (0 - reinterpret_cast<uintptr_t>(at)) % kJoinAlign;
   j->meta = reinterpret_cast<int32_t*>(at);
   j->stats = reinterpret_cast<float4*>(at + join_meta_bytes(G));
   j->parts = reinterpret_cast<float*>(at + join_meta_bytes(G) + join_stats_bytes(G, j->NR));

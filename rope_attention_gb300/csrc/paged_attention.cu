@@ -1009,7 +1009,7 @@ size_t paged_attention_workspace(const PagedLaunch& L) {
   if (paged_tile_serves(L)) return kAttnHeader + paged_tile_workspace(L);
   Plan pl;
   if (!plan(L, &pl)) return 0;
-  return kAttnHeader + (pl.whole ? join_meta_bytes(pl.G) : join_bytes(pl.G, pl.NR, L.Dv));
+  return kAttnHeader + (pl.whole ? kJoinSlack + join_meta_bytes(pl.G) : join_bytes(pl.G, pl.NR, L.Dv));
 }
 
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why) {

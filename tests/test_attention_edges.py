@@ -1,0 +1,53 @@
+"""Calls of the attention operators at the edge of what the header allows, on the CPU: where
+the pieces of a cut item lie in a workspace, whatever 16 bytes it starts on."""
+import os
+import subprocess
+
+import pytest
+
+from rope_attention_gb300 import build
+
+PLACES = r"""
+#include <cstdio>
+#include "attn_join.cuh"
+int main() {
+  for (int G : {1, 7, 152, 160})
+    for (int NR : {16, 64, 256})
+      for (int Dv : {16, 48, 128, 512})
+        for (uintptr_t base : {0x10000u, 0x10010u}) {
+          ra::JoinParams j{};
+          j.NR = NR;
+          ra::join_place(&j, reinterpret_cast<uint8_t*>(base), G);
+          const uintptr_t meta = reinterpret_cast<uintptr_t>(j.meta), stats = reinterpret_cast<uintptr_t>(j.stats),
+                          parts = reinterpret_cast<uintptr_t>(j.parts);
+          const uintptr_t end = parts + static_cast<uintptr_t>(G) * 2 * NR * Dv * 4;
+          const bool apart = base <= meta && meta + G * 32 <= stats && stats + G * 2 * NR * 16 <= parts;
+          printf("%d %d %d %d\n", apart, static_cast<int>(stats % 16), static_cast<int>(parts % 32),
+                 end <= base + ra::join_bytes(G, NR, Dv));
+        }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def nvcc():
+    try:
+        return build.nvcc()
+    except RuntimeError:
+        pytest.skip("nvcc not available")
+
+
+def host_program(nvcc, tmp_path, source):
+    """The lines that a host program over the kernels' headers prints."""
+    src, exe = os.path.join(tmp_path, "t.cu"), os.path.join(tmp_path, "t")
+    with open(src, "w") as f:
+        f.write(source)
+    r = subprocess.run([nvcc, src, "-o", exe, "-std=c++17", *build.ARCH, "-I", build.INCLUDE, "-I", build.CSRC, "-cudart", "static"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    return subprocess.run([exe], capture_output=True, text=True, check=True).stdout.splitlines()
+
+
+def test_pieces_lie_on_32_bytes_in_a_workspace_on_any_16(nvcc, tmp_path):
+    lines = host_program(nvcc, tmp_path, PLACES)
+    assert len(lines) == 96 and set(lines) == {"1 0 0 1"}
