@@ -569,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         code.next(p.nsg);
       }
     }
-    if (!p.stall_loads && (!ok || *abort_flag)) {  // let every copy in flight land before the block leaves
+    // Let every copy in flight land before the block leaves: whoever waits for the last ones may give
+    // up only after this warp has come through, so it asks no flag.
+    if (!p.stall_loads) {
       for (int i = 0; i < kMaxStages; ++i) {
         // (a stage that converters share may stay open for them: then nothing is in flight after the limit)
         if (armed[0] & (1u << i)) bounded_drain(smem_u32(&ms.kv_full[i]), (armed_parity[0] >> i) & 1u, kDrainNs);

@@ -658,13 +658,14 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           }
         }
       }
-      if (!ok || *abort_flag)  // let every copy in flight land before the block leaves
-        for (int i = 0; i < 5; ++i) {
-          if (armed_k >> i & 1) bounded_drain(smem_u32(&ms.k_full[i]), par_k >> i & 1, kTileDrainNs);
-          if (armed_v >> i & 1) bounded_drain(smem_u32(&ms.v_full[i]), par_v >> i & 1, kTileDrainNs);
-          if (armed_c >> i & 1) bounded_drain(smem_u32(&ms.c_full[i]), par_c >> i & 1, kTileDrainNs);
-          if (armed_q >> i & 1) bounded_drain(smem_u32(&ms.q_full[i]), par_q >> i & 1, kTileDrainNs);
-        }
+      // Let every copy in flight land before the block leaves: whoever waits for the last ones may
+      // give up only after this warp has come through, so it asks no flag.
+      for (int i = 0; i < 5; ++i) {
+        if (armed_k >> i & 1) bounded_drain(smem_u32(&ms.k_full[i]), par_k >> i & 1, kTileDrainNs);
+        if (armed_v >> i & 1) bounded_drain(smem_u32(&ms.v_full[i]), par_v >> i & 1, kTileDrainNs);
+        if (armed_c >> i & 1) bounded_drain(smem_u32(&ms.c_full[i]), par_c >> i & 1, kTileDrainNs);
+        if (armed_q >> i & 1) bounded_drain(smem_u32(&ms.q_full[i]), par_q >> i & 1, kTileDrainNs);
+      }
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
@@ -964,6 +965,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           // NaN: zero them in shared memory
           const int32_t end = w.Lk - t * KT;
           if (!bounded_wait_warp(smem_u32(&ms.v_full[vr.stage]), vr.parity, p.wait_ns, abort_flag)) {
+            tmem_st_wait();                 // of P: tensor memory is freed only behind its stores
             ok = false;
             break;
           }
