@@ -320,19 +320,6 @@ struct TileWalk {
   }
 };
 
-// The next piece that warp 10 handed over, for a whole warp; false at the end or when a wait
-// gave up.
-__device__ __forceinline__ bool take_piece(TileMisc& ms, Ring& ring, TilePiece& w, uint64_t limit, volatile int* abort_flag,
-                                           bool& ok) {
-  ok = ok && bounded_wait_warp(smem_u32(&ms.piece_full[ring.stage]), ring.parity, limit, abort_flag);
-  if (!ok) return false;
-  w = ms.pieces[ring.stage];
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms.piece_empty[ring.stage]));
-  ring.next(kTilePieces);
-  return !w.end;
-}
-
 // whether all 128 threads of a softmax group are well
 __device__ __forceinline__ bool group_ok(uint32_t id, bool ok) {
   uint32_t bad;
@@ -342,6 +329,22 @@ __device__ __forceinline__ bool group_ok(uint32_t id, bool ok) {
       : "r"(ok ? 0u : 1u), "r"(id)
       : "memory");
   return bad == 0;
+}
+
+// The next piece that warp 10 handed over, for a whole warp; false at the end or when a wait
+// gave up.  GROUP: over codes the softmax groups meet at barriers in a piece, which have no time
+// limit, so the warps of a group (barrier `id`) take a piece, or leave, together.
+template <bool GROUP = false>
+__device__ __forceinline__ bool take_piece(TileMisc& ms, Ring& ring, TilePiece& w, uint64_t limit, volatile int* abort_flag,
+                                           bool& ok, uint32_t id = 0) {
+  ok = ok && bounded_wait_warp(smem_u32(&ms.piece_full[ring.stage]), ring.parity, limit, abort_flag);
+  if (GROUP) ok = group_ok(id, ok);
+  if (!ok) return false;
+  w = ms.pieces[ring.stage];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms.piece_empty[ring.stage]));
+  ring.next(kTilePieces);
+  return !w.end;
 }
 
 template <bool F16>
@@ -515,6 +518,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         first = false;
         if (!bounded_wait_warp(smem_u32(&ms.piece_empty[pieces.stage]), pieces.parity ^ 1u, p.wait_ns, abort_flag)) break;
+        if (__any_sync(0xffffffffu, *abort_flag)) break;  // no piece for those that are about to leave
         if (lane == 0) {
           ms.pieces[pieces.stage] = walk.w;
           mbar_arrive(smem_u32(&ms.piece_full[pieces.stage]));
@@ -807,7 +811,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
     uint32_t s_par = 0, o_par = 0, q_par = 0, u = 0;
     Ring vr;
     bool ok = true;
-    while (take_piece(ms, pieces, w, p.wait_ns, abort_flag, ok)) {
+    while (take_piece<QUANT>(ms, pieces, w, p.wait_ns, abort_flag, ok, 1 + i)) {
       const int32_t n = w.n(i), n_both = max(w.n(0), w.n(1));
       const bool live = row < w.rows[i];
       const int32_t in_tile = static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.join.hb));

@@ -37,6 +37,8 @@ SHORT_WAITS = {
     "decode_v1": lambda: Paged(8, [700, 90, 333] * 8, [1, 2, 1] * 8, 16, variant=1),
     "decode_v1_int8": lambda: Paged(9, [700, 90, 333] * 8, [1, 2, 1] * 8, 16, variant=1, quant=True),
     "chunk": lambda: Paged(10, [700, 90, 333] * 8, [80, 90, 33] * 8, 8, N=4),
+    "chunk_int8": lambda: Paged(11, [700, 90, 333] * 8, [80, 90, 33] * 8, 8, N=4, quant=True),
+    "chunk_int8_short": lambda: Paged(12, [90, 40, 65] * 20, [90, 40, 33] * 20, 64, N=8, quant=True),
 }
 
 
