@@ -519,8 +519,8 @@ void ra_test_stall_next_attention(void);
 /* Reads rows back from the caches of kv_rms_norm_rope_cache: token (b, s) comes
  * from the slot that a call with the same parameters and index would write it to,
  *   k_out[b, n, s, :] = k_cache row,  c_kv_out[b, n, s, :] = ckv_cache row,
- * as kv_dtype; a quantised element x as (code - offset) / scale in fp32, rounded
- * once.  Of `p` the call uses B, N, S, Dkv, Dv, rope_size, variant, the cache
+ * as kv_dtype; a quantised element x as (code - offset) * (1 / scale), each of the
+ * three rounded to fp32, then to kv_dtype (a code equal to its offset gives 0).  Of `p` the call uses B, N, S, Dkv, Dv, rope_size, variant, the cache
  * fields, the dtypes and the scalar flags.
  *   index         as in kv_rms_norm_rope_cache (here a slot may come several times).
  *                 A token whose index is -1 gives zeros; so does one whose slot is

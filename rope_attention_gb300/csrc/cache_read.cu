@@ -5,9 +5,10 @@
 // An HBM stream of short scattered rows (1 or 2 bytes read, 2 written per element), so the
 // mapping spends few instructions per byte and keeps loads in flight:
 //  * a block serves one head, whose quantisation it turns once into a table in shared
-//    memory: x = code * r + t, r = 1 / scale, t = -offset * r, one fused multiply-add an
-//    element (fp32; at most 2^-24 (2 |x| + 3 |offset / scale|) off, far below the rounding
-//    to 16 bits);
+//    memory: x = (code - offset) * r, r = 1 / scale.  The difference, r and the product are each
+//    rounded to fp32, at most 3 * 2^-24 of x in all, and a code equal to its offset is 0.
+//    (code * r - offset * r as one multiply-add is off by 2^-24 of offset / scale, however
+//    small x is, and takes as long: 53 us both);
 //  * a warp takes 4 tokens at once and spreads their rows' 8-channel units (8 or 16 bytes
 //    in, 16 out) over its lanes: four rows fill them where one would not (64 + 8 units in a
 //    latent and its rope part: 8 + 1 rounds of 32 lanes for four tokens, not 4 x 3), and the
@@ -98,7 +99,7 @@ __device__ __forceinline__ void codes_to_float(uint2 w, int32_t kind, float2 (&x
 
 // One cache's rows of a warp's tokens.  rows: per token its cache row and its row of the
 // output; place: for every (round, lane) its token (upper half) and unit; tab: the side's
-// quantisation, four arrays of a float4 per unit.
+// quantisation, four arrays of a float4 per unit: 1 / scale (two), -offset (two).
 template <bool F16>
 __device__ __forceinline__ void read_side(const Side& side, const int64_t (*rows)[2], const uint32_t* place,
                                           const float4* tab, int lane) {
@@ -138,10 +139,10 @@ __device__ __forceinline__ void read_side(const Side& side, const int64_t (*rows
         codes_to_float(make_uint2(in[e].x, in[e].y), side.kind, x);
         const float4* t = tab + unit[e];
         const float4 ra = t[0], rb = t[side.units], ta = t[2 * side.units], tb = t[3 * side.units];
-        x[0] = __ffma2_rn(x[0], make_float2(ra.x, ra.y), make_float2(ta.x, ta.y));
-        x[1] = __ffma2_rn(x[1], make_float2(ra.z, ra.w), make_float2(ta.z, ta.w));
-        x[2] = __ffma2_rn(x[2], make_float2(rb.x, rb.y), make_float2(tb.x, tb.y));
-        x[3] = __ffma2_rn(x[3], make_float2(rb.z, rb.w), make_float2(tb.z, tb.w));
+        x[0] = __fmul2_rn(__fadd2_rn(x[0], make_float2(ta.x, ta.y)), make_float2(ra.x, ra.y));
+        x[1] = __fmul2_rn(__fadd2_rn(x[1], make_float2(ta.z, ta.w)), make_float2(ra.z, ra.w));
+        x[2] = __fmul2_rn(__fadd2_rn(x[2], make_float2(tb.x, tb.y)), make_float2(rb.x, rb.y));
+        x[3] = __fmul2_rn(__fadd2_rn(x[3], make_float2(tb.z, tb.w)), make_float2(rb.z, rb.w));
         in[e] = make_uint4(pack_half2<!F16>(x[0].x, x[0].y), pack_half2<!F16>(x[1].x, x[1].y),
                            pack_half2<!F16>(x[2].x, x[2].y), pack_half2<!F16>(x[3].x, x[3].y));
       }
@@ -154,10 +155,9 @@ __device__ __forceinline__ void read_side(const Side& side, const int64_t (*rows
 __device__ __forceinline__ void set_up(const Side& side, int32_t head, bool per_head, float4* tab, uint32_t* place) {
   for (int i = threadIdx.x; side.kind != kQuantNone && i < side.width; i += kThreads) {
     const int at = side.scalar ? 0 : (per_head ? head * side.width : 0) + i;
-    const float r = __frcp_rn(__ldg(side.scale + at));
     float* const t = reinterpret_cast<float*>(tab + ((i >> 2) & 1) * side.units + (i >> 3)) + (i & 3);
-    t[0] = r;
-    t[8 * side.units] = side.offset ? -__ldg(side.offset + at) * r : 0.f;
+    t[0] = __frcp_rn(__ldg(side.scale + at));
+    t[8 * side.units] = side.offset ? -__ldg(side.offset + at) : 0.f;
   }
   for (int i = threadIdx.x; i < (kTokens * side.units + 31) / 32 * 32; i += kThreads) {
     const int token = i / side.units;

@@ -1,12 +1,18 @@
 """Calls of the attention operators at the edge of what the header allows, on the GPU:
-workspaces that start on any 16 bytes, waits of the shortest time limit."""
+workspaces that start on any 16 bytes, waits of the shortest time limit, codes beside their
+zero point."""
+import numpy as np
 import pytest
 import torch
 
+from attention_util import TORCH
 from rope_attention_gb300 import native
 from test_attention_use import DEFAULT_WAIT_NS, Packed, Paged
 
 pytestmark = pytest.mark.gpu
+
+CODE = {"bf16": native.RA_BF16, "fp16": native.RA_FP16, "int8": native.RA_INT8, "e4m3": native.RA_FP8_E4M3,
+        "e5m2": native.RA_FP8_E5M2}
 
 
 @pytest.mark.parametrize("at", [0, 16])
@@ -66,3 +72,43 @@ def test_waits_that_run_out_anywhere(name):
     finally:
         native.ra_set_wait_timeout_ns(DEFAULT_WAIT_NS)
     x.check(f"behind {gave_up} calls that gave up")
+
+
+def rounded_between(x, slack, dtype):
+    """The 16-bit numbers that x (1 - slack) and x (1 + slack) round to, in order."""
+    a, b = (torch.from_numpy(x * f).to(TORCH[dtype]).double().numpy() for f in (1 - slack, 1 + slack))
+    return np.minimum(a, b), np.maximum(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind", ["int8", "e4m3", "e5m2"])
+def test_read_near_the_zero_point(kind, dtype):
+    """Codes at and beside their offset: (code - offset) / scale as one difference, one
+    reciprocal and one product in fp32, at most 3 half steps (and their products) of the
+    result, then one rounding.  A code equal to its offset is zero."""
+    B, N, S, D, bs = 2, 2, 64, 64, 32
+    g = np.random.default_rng(21)
+    codes = g.integers(-128, 128, (4, N, bs, D)).astype(np.float64)
+    if kind != "int8":
+        t = torch.from_numpy(codes).to({"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}[kind])
+        codes = t.double().numpy()
+    scale = g.uniform(10, 40, (N, D)).astype(np.float32)
+    offset = codes[0, :, 0].astype(np.float32)                     # integers, each some code's value
+    offset[:, ::3] += np.float32(0.37)                              # and numbers beside one
+    codes[:, :, ::2] = codes[0, :, 0][None, :, None]                # every second row: the offset's own code
+    cache = torch.from_numpy(codes.astype(np.int8)).cuda() if kind == "int8" else \
+        torch.from_numpy(codes).to({"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}[kind]).cuda()
+    p = native.KvRmsNormRopeCacheParams(B=B, N=N, S=S, Dkv=D, Dv=D, rope_size=32, variant=2, cache_mode=native.RA_CACHE_PA_BNSD,
+                                        block_num=4, block_size=bs, kv_dtype=CODE[dtype], k_cache_dtype=CODE[kind],
+                                        ckv_cache_dtype=CODE[kind], epsilon=1e-5)
+    sd, od = torch.from_numpy(scale).cuda(), torch.from_numpy(offset).cuda()
+    outs = [torch.full((B, N, S, D), 7.0, dtype=TORCH[dtype], device="cuda") for _ in range(2)]
+    native.kv_cache_read(p, torch.arange(B * S, device="cuda"), cache, cache, *outs, sd, sd, od, od)
+    rows = codes.reshape(B, 2, N, bs, D).transpose(0, 2, 1, 3, 4).reshape(B, N, S, D)
+    want = (rows - offset.astype(np.float64)[None, :, None]) / scale.astype(np.float64)[None, :, None]
+    lo, hi = rounded_between(want, 3.01 * 2.0 ** -24, dtype)
+    assert (want == 0).mean() > 0.25
+    for out in outs:
+        got = out.double().cpu().numpy()
+        assert (got[want == 0] == 0).all()
+        assert ((lo <= got) & (got <= hi)).all(), float(((got < lo) | (got > hi)).mean())
