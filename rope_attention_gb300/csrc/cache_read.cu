@@ -139,10 +139,10 @@ __device__ __forceinline__ void read_side(const Side& side, const int64_t (*rows
         codes_to_float(make_uint2(in[e].x, in[e].y), side.kind, x);
         const float4* t = tab + unit[e];
         const float4 ra = t[0], rb = t[side.units], ta = t[2 * side.units], tb = t[3 * side.units];
-        x[0] = __fmul2_rn(__fadd2_rn(x[0], make_float2(ta.x, ta.y)), make_float2(ra.x, ra.y));
-        x[1] = __fmul2_rn(__fadd2_rn(x[1], make_float2(ta.z, ta.w)), make_float2(ra.z, ra.w));
-        x[2] = __fmul2_rn(__fadd2_rn(x[2], make_float2(tb.x, tb.y)), make_float2(rb.x, rb.y));
-        x[3] = __fmul2_rn(__fadd2_rn(x[3], make_float2(tb.z, tb.w)), make_float2(rb.z, rb.w));
+        x[0] = __fmul2_rn(make_float2(x[0].x + ta.x, x[0].y + ta.y), make_float2(ra.x, ra.y));
+        x[1] = __fmul2_rn(make_float2(x[1].x + ta.z, x[1].y + ta.w), make_float2(ra.z, ra.w));
+        x[2] = __fmul2_rn(make_float2(x[2].x + tb.x, x[2].y + tb.y), make_float2(rb.x, rb.y));
+        x[3] = __fmul2_rn(make_float2(x[3].x + tb.z, x[3].y + tb.w), make_float2(rb.z, rb.w));
         in[e] = make_uint4(pack_half2<!F16>(x[0].x, x[0].y), pack_half2<!F16>(x[1].x, x[1].y),
                            pack_half2<!F16>(x[2].x, x[2].y), pack_half2<!F16>(x[3].x, x[3].y));
       }
