@@ -201,6 +201,11 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// log2 of what fp16 probabilities are held with.  The largest is 2^0 to 2^8 (the maximum follows
+// only when a tile exceeds it by that), fp16 ends at 2^16 and its least number is 2^-24: without
+// the factor a key 2^-25 below a row's largest left the weighted sum, but not the sum of weights
+// (300 keys 2^-25.2 below one sink: all of their share lost), with it one 2^-32 below.
+constexpr float kHalfLift = 7.f;
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   if constexpr (BF16) return pack_bf16x2(lo, hi);

@@ -343,6 +343,7 @@ __device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows
 // rounding does not add a third error of that size, P goes in as two fp16 numbers (hi + lo).
 template <bool F16, bool P16, bool PLO>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+  constexpr float kLift = P16 ? kHalfLift : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + p.off_misc);
   const int NR = p.NR;
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           }
         }
         if (ok && rows_here) {
-          const float neg = m == neg_inf() ? 0.f : -m * sl2;
+          const float neg = m == neg_inf() ? kLift : fmaf(-m, sl2, kLift);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t x[16], lo[16];
           exp_batch<!P16, PLO>(s, make_float2(sl2, sl2), make_float2(neg, neg), acc, x, lo);
@@ -876,8 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         inv_sum[row] = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is 0; a NaN stays one
         const float shift = k_quant && n > 0 && live ? row_const[row] : 0.f;
         if (live && whole && p.lse)
-          p.lse[out_row[row]] = l != 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
-        if (live && !whole) p.join.stats[slot * NR + row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
+          p.lse[out_row[row]] = l != 0.f ? fmaf(m, sl2, -kLift) * 0.6931471805599453f + logf(l) + shift : neg_inf();
+        if (live && !whole) p.join.stats[slot * NR + row] = make_float4(m == neg_inf() ? neg_inf() : fmaf(m, sl2, -kLift), l, shift, 0.f);
       }
       bar_softmax();
       // Rolled loops over eight rows at a time: this code runs once a piece, and each line of

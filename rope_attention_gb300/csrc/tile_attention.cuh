@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   // does not add a third error of that size, P goes in as two fp16 numbers (hi + lo).  The
   // products of a tile cost half as much again, which the softmax hides for the most part.
   constexpr bool kPLo = F16 && QUANT;
+  constexpr float kLift = P16 ? kHalfLift : 0.f;
   // Registers per thread: launched with 168 (QUANT: 128) each, then moved to the softmax:
   // 2 x 216 + 72 = 3 x 168; 2 x 192 + 64 + 64 = 4 x 128
   constexpr int kRegsSoftmax = QUANT ? 192 : 216, kRegsRest = QUANT ? 64 : 72;
@@ -952,7 +953,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             }
           }
         }
-        const float neg = m == neg_inf() ? 0.f : -m * sl2;
+        const float neg = m == neg_inf() ? kLift : fmaf(-m, sl2, kLift);
         const float2 sl = make_float2(sl2, sl2), ng = make_float2(neg, neg);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1004,9 +1005,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       if (live) {
         if (whole) {
           if (p.join.lse)
-            p.join.lse[token * p.join.heads + head] = l != 0.f ? m * sl2 * 0.6931471805599453f + logf(l) + shift : neg_inf();
+            p.join.lse[token * p.join.heads + head] = l != 0.f ? fmaf(m, sl2, -kLift) * 0.6931471805599453f + logf(l) + shift : neg_inf();
         } else {
-          p.join.stats[part_row] = make_float4(m == neg_inf() ? neg_inf() : m * sl2, l, shift, 0.f);
+          p.join.stats[part_row] = make_float4(m == neg_inf() ? neg_inf() : fmaf(m, sl2, -kLift), l, shift, 0.f);
         }
       }
       const bool store = live && (whole || n > 0);

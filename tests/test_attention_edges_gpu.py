@@ -1,11 +1,11 @@
 """Calls of the attention operators at the edge of what the header allows, on the GPU:
 workspaces that start on any 16 bytes, waits of the shortest time limit, codes beside their
-zero point."""
+zero point, weights far below a row's largest."""
 import numpy as np
 import pytest
 import torch
 
-from attention_util import TORCH
+from attention_util import HALF_STEP, TORCH
 from rope_attention_gb300 import native
 from test_attention_use import DEFAULT_WAIT_NS, Packed, Paged
 
@@ -112,3 +112,81 @@ def test_read_near_the_zero_point(kind, dtype):
         got = out.double().cpu().numpy()
         assert (got[want == 0] == 0).all()
         assert ((lo <= got) & (got <= hi)).all(), float(((got < lo) | (got > hi)).mean())
+
+
+def one_cache(lens, kt, dtype, variant=2):
+    """Zeroed caches of one kv head in pages of 64, their parameters, the table and, over codes,
+    scales of 2 for keys and 1 for values.  Keys and values 64 wide, V1's with 16 rotated channels."""
+    bs, pages = 64, [-(-n // 64) for n in lens]
+    n_pages = sum(pages)
+    Dkv, Dv, R = (64, 64, 32) if variant == 2 else (80, 64, 16)
+    kw = Dkv if variant == 2 else R
+    tt = {**TORCH, "int8": torch.int8, "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}[kt]
+    kc = torch.zeros(n_pages, 1, bs, kw, device="cuda").to(tt)
+    vc = torch.zeros(n_pages, 1, bs, Dv, device="cuda").to(tt)
+    table = torch.full((len(lens), max(pages)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(pages):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    quant = kt not in TORCH
+    p = native.KvRmsNormRopeCacheParams(B=len(lens), N=1, S=1, Dkv=Dkv, Dv=Dv, rope_size=R, variant=variant,
+                                        cache_mode=native.RA_CACHE_PA_BNSD, block_num=n_pages, block_size=bs,
+                                        kv_dtype=CODE[dtype], k_cache_dtype=CODE[kt], ckv_cache_dtype=CODE[kt], epsilon=1e-5)
+    scales = dict(k_rope_scale=torch.full((1, kw) if variant == 2 else (kw,), 2.0, device="cuda"),
+                  c_kv_scale=torch.full((1, Dv) if variant == 2 else (Dv,), 1.0, device="cuda")) if quant else {}
+    return p, kc, vc, table.cuda(), scales
+
+
+def attend_cache(p, kc, vc, table, scales, q, lens, scale, causal=0):
+    params = native.PagedAttentionParams(B=len(lens), total_q=q.shape[0], num_heads=q.shape[1], causal=causal, softmax_scale=scale,
+                                         max_seq_len=max(lens), block_table_stride=table.shape[1])
+    out = torch.full((q.shape[0], q.shape[1], p.Dv), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    ws = torch.zeros(native.paged_attention_workspace_bytes(p, params), dtype=torch.uint8, device="cuda")
+    native.paged_attention(p, params, q, kc, vc, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, ws, table, lse=lse, **scales)
+    torch.cuda.synchronize()
+    assert native.attention_status(ws) == 0
+    return out, lse
+
+
+def attend_prompt(q, k, v, scale):
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    p = native.packed_attention_params(q, k, v, out, softmax_scale=scale)
+    ws = torch.zeros(native.packed_attention_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    native.packed_attention(p, q, k, v, out, ws, lse)
+    torch.cuda.synchronize()
+    assert native.attention_status(ws) == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("new", [1, 90], ids=["step", "chunk"])
+@pytest.mark.parametrize("kt,dtype,variant", [("fp16", "fp16", 2), ("int8", "bf16", 2), ("e4m3", "bf16", 2), ("int8", "fp16", 2),
+                                              ("int8", "bf16", 1), ("int8", "fp16", 1), ("prompt", "fp16", 0)])
+def test_a_tail_far_below_a_sink(kt, dtype, variant, new):
+    """One key holds nearly all of the weight and has the value 0; 299 keys 17.5 nats (2^-25.2)
+    below it have the value 100 (E4M3, of three bits: 18 and 96).  What is left of them is the result.  An fp16 weight is held
+    with 2^7 (the largest one between 2^7 and 2^15), so each is off by half of fp16's least
+    number at most: 2^-25 / 2^7 of the largest one."""
+    n = 300
+    q = torch.zeros(new, 2, 80 if variant == 1 else 64, dtype=TORCH[dtype], device="cuda")
+    if kt == "prompt":
+        q[..., 0] = 1
+        k, v = torch.zeros(n, 1, 64, dtype=q.dtype, device="cuda"), torch.full((n, 1, 64), 100.0, dtype=q.dtype, device="cuda")
+        k[0, 0, 0], v[0] = 17.5, 0
+        out, lse = attend_prompt(q, k, v, 1.0)
+    else:
+        p, kc, vc, table, scales = one_cache([n], kt, dtype, variant)
+        q[..., 64 if variant == 1 else 0] = 1  # (V1's latent channels, a part of the key, meet zeros)
+        kc[0, 0, 0, 0] = torch.tensor({"int8": 35.0, "e4m3": 36.0}.get(kt, 17.5), device="cuda").to(kc.dtype)
+        vc.copy_(torch.full(vc.shape, 96.0 if kt == "e4m3" else 100.0, device="cuda").to(vc.dtype))
+        vc[0, 0, 0] = torch.zeros(vc.shape[-1], device="cuda").to(vc.dtype)
+        out, lse = attend_cache(p, kc, vc, table, scales, q, [n], 1.0)
+    top, value = (18.0, 96.0) if kt == "e4m3" else (17.5, 100.0)
+    total = 1 + (n - 1) * np.exp(-top)
+    want = (n - 1) * np.exp(-top) * value / total
+    tol = (n - 1) * 2.0 ** -32 * value + 2 * HALF_STEP[dtype] * want
+    err = (out.double() - want).abs().max().item()
+    assert err <= tol, (err / want, tol / want)
+    assert (lse.double() - (top + np.log(total))).abs().max() <= 2.0 ** -17 * (1 + top)
