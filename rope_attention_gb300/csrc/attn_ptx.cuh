@@ -243,6 +243,9 @@ __device__ __forceinline__ void exp_batch(const uint32_t* s, float2 scale, float
     }
   }
 }
+// How far a row's scores may pass its maximum before that follows, from log2 to scores of that
+// scale; finite, so that a first score passes -inf + slack whatever the scale.
+__device__ __forceinline__ float lazy_slack(float log2, float scale) { return fminf(log2 / scale, 3e38f); }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(static_cast<int>(0xff800000u)); }
 
 }  // namespace ra

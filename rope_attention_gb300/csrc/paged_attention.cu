@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         ++loaded;
       }
       const float sl2 = live && k_quant && n > 0 ? row_scale[row] : p.sl2;
-      const float lazy = kLazy / sl2;
+      const float lazy = lazy_slack(kLazy, sl2);
       const int32_t seen = p.causal && live ? min(w.len, max(0, w.len - w.Lq + my_tok + 1)) : w.len;
       const bool rows_here = quad * 32 < w.rows;     // uniform in the warp
       float m = neg_inf(), l = 0.f;

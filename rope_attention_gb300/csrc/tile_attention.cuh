@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         if (!ok) break;
         if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[i]));
       }
-      const float lazy = kTileLazy / sl2;
+      const float lazy = lazy_slack(kTileLazy, sl2);
       float m = neg_inf(), l = 0.f;
       for (int32_t j = 0; j < n; ++j) {
         if (!bounded_wait_warp(smem_u32(&ms.s_full[i]), s_par, p.wait_ns, abort_flag)) {

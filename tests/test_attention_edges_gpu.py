@@ -1,6 +1,7 @@
 """Calls of the attention operators at the edge of what the header allows, on the GPU:
 workspaces that start on any 16 bytes, waits of the shortest time limit, codes beside their
-zero point, weights far below a row's largest."""
+zero point, weights far below a row's largest, scales
+near the least."""
 import numpy as np
 import pytest
 import torch
@@ -190,3 +191,33 @@ def test_a_tail_far_below_a_sink(kt, dtype, variant, new):
     err = (out.double() - want).abs().max().item()
     assert err <= tol, (err / want, tol / want)
     assert (lse.double() - (top + np.log(total))).abs().max() <= 2.0 ** -17 * (1 + top)
+
+
+@pytest.mark.parametrize("new", [1, 90], ids=["step", "chunk"])
+@pytest.mark.parametrize("kt,variant", [("bf16", 2), ("int8", 2), ("int8", 1), ("bf16", 1), ("prompt", 0)])
+@pytest.mark.parametrize("scale,zero_q", [(1e-38, False), (1e-9, True)], ids=["least_scale", "zero_queries"])
+def test_scores_that_are_all_alike(scale, zero_q, kt, variant, new):
+    """A softmax scale near fp32's least normal number, or queries of zeros under a small one:
+    every weight is alike, the result is the mean of the values and the lse log(n); with an
+    item in one piece (n = 50) and in many (n = 5000)."""
+    for n in (50, 5000):
+        g = torch.Generator(device="cuda").manual_seed(22)
+        Dk = 80 if variant == 1 else 64
+        q = torch.randn(new, 2, Dk, device="cuda", generator=g).bfloat16()
+        if zero_q:
+            q.zero_()
+        rnd = lambda shape: torch.randint(-100, 100, shape, device="cuda", generator=g).float()
+        if kt == "prompt":
+            k, v = rnd((n, 1, 64)).bfloat16(), rnd((n, 1, 64)).bfloat16()
+            values = v[:, 0]
+            out, lse = attend_prompt(q, k, v, scale)
+        else:
+            p, kc, vc, table, scales = one_cache([n], kt, "bf16", variant)
+            kc.copy_(rnd(kc.shape).to(kc.dtype))
+            vc.copy_(rnd(vc.shape).to(vc.dtype))
+            values = vc[:, 0].reshape(-1, 64)[:n]
+            out, lse = attend_cache(p, kc, vc, table, scales, q, [n], scale)
+        values = values.double()
+        mean, spread = values.mean(0), values.abs().mean(0)
+        assert ((out.double() - mean).abs() <= HALF_STEP["bf16"] * (mean.abs() + spread) + 2.0 ** -17 * spread).all()
+        assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -17 * (1 + np.log(n))
