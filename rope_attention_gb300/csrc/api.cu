@@ -310,6 +310,7 @@ ra_status check_cache(const kv_rms_norm_rope_cache_params* p, const float* k_sca
   if (mode == RA_CACHE_NORM) {
     if (p->cache_seq_len < 1 || p->cache_seq_len > (1LL << 31))
       return fail(RA_ERR_INVALID_ARG, "NORM mode needs cache_seq_len in [1, 2^31]");
+    if (p->B > (1LL << 40) / p->cache_seq_len) return fail(RA_ERR_INVALID_ARG, "too many cache slots");
     if (p->variant == 1 && (k_scale || v_scale))
       return fail(RA_ERR_INVALID_ARG, "V1 in NORM mode takes no quantisation parameters");
   } else {
@@ -933,7 +934,8 @@ ra_status kv_cache_read(const kv_rms_norm_rope_cache_params* p, const int64_t* i
   const ra_status st = check_cache(p, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, &s);
   if (st != RA_OK) return st;
   if (p->B < 1 || p->S < 1) return fail(RA_ERR_INVALID_ARG, "empty tensors are not supported");
-  if (p->S > (1LL << 31) || p->B > (1LL << 31) || p->B * p->N * p->S > (1LL << 40)) return fail(RA_ERR_INVALID_ARG, "too many rows");
+  if (p->S > (1LL << 31) || p->B > (1LL << 31) || p->B * p->S > (1LL << 40) / p->N)  // no product passes 2^62
+    return fail(RA_ERR_INVALID_ARG, "too many rows");
   if (!index || (!k_out && !c_kv_out) || (k_out && !k_cache) || (c_kv_out && !ckv_cache))
     return fail(RA_ERR_INVALID_ARG, "index, and an output with its cache, are required");
   if ((reinterpret_cast<uintptr_t>(index) & 7u) != 0 || !aligned16(k_cache) || !aligned16(ckv_cache) ||

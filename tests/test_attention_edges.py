@@ -1,11 +1,12 @@
 """Calls of the attention operators at the edge of what the header allows, on the CPU: where
 the pieces of a cut item lie in a workspace, whatever 16 bytes it starts on."""
+import ctypes
 import os
 import subprocess
 
 import pytest
 
-from rope_attention_gb300 import build
+from rope_attention_gb300 import build, native
 
 PLACES = r"""
 #include <cstdio>
@@ -51,3 +52,36 @@ def host_program(nvcc, tmp_path, source):
 def test_pieces_lie_on_32_bytes_in_a_workspace_on_any_16(nvcc, tmp_path):
     lines = host_program(nvcc, tmp_path, PLACES)
     assert len(lines) == 96 and set(lines) == {"1 0 0 1"}
+
+
+# ---------------------------------------------------------------- sizes whose products pass 64 bits
+A16 = 0x10000  # 16-byte aligned placeholder address (never dereferenced)
+
+
+@pytest.fixture()
+def validating():
+    build.build()
+    lib = native.load()
+    lib.ra_test_validate_only(1)
+    yield lib
+    lib.ra_test_validate_only(0)
+
+
+def read_params(**kw):
+    base = dict(B=2, N=2, S=5, Dkv=192, Dv=128, rope_size=64, variant=2, cache_mode=native.RA_CACHE_PA_BNSD, block_num=8,
+                block_size=32, kv_dtype=native.RA_BF16, k_cache_dtype=native.RA_BF16, ckv_cache_dtype=native.RA_BF16, epsilon=1e-5)
+    return native.KvRmsNormRopeCacheParams(**{**base, **kw})
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 31, S=1 << 31, N=8),             # B * N * S = 2^65
+    dict(B=1 << 31, S=1 << 31, N=4), dict(B=1 << 31, S=1 << 10, N=1),
+    # a NORM cache of 2^60 rows, whose bytes wrap to nothing: an empty tensor would hold it
+    dict(B=1 << 29, S=1, N=1, cache_mode=native.RA_CACHE_NORM, cache_seq_len=1 << 31, rope_size=8, Dkv=8, Dv=8),
+    dict(B=1 << 20, S=1, N=1, cache_mode=native.RA_CACHE_NORM, cache_seq_len=(1 << 20) + 1),
+])
+def test_read_refuses_sizes_beyond_2_to_the_40(validating, kw):
+    p = read_params(**kw)
+    st = validating.kv_cache_read(ctypes.byref(p), A16, A16, A16, None, None, None, None, A16, A16, None, None)
+    assert st == -1 and "too many" in validating.ra_last_error().decode()
+    assert validating.kv_cache_read(ctypes.byref(read_params()), A16, A16, A16, None, None, None, None, A16, A16, None, None) == 0
