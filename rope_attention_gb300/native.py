@@ -20,6 +20,7 @@ import os
 
 import torch
 
+from . import build
 from .build import CALLS_PATH, LIB_PATH
 
 RA_OK = 0
@@ -147,7 +148,9 @@ def _calls():
     if _CALLS is None:
         load()
         if not os.path.exists(CALLS_PATH):
-            raise FileNotFoundError(f"{CALLS_PATH} is missing: build it with `python -m rope_attention_gb300.build`")
+            why = build.calls_missing()
+            raise FileNotFoundError(f"{CALLS_PATH} is missing: build it with `python -m rope_attention_gb300.build`"
+                                    + (f" (which cannot here: {why})" if why else ""))
         loader = importlib.machinery.ExtensionFileLoader("rope_attention_gb300._torch_calls", CALLS_PATH)
         spec = importlib.util.spec_from_loader(loader.name, loader)
         module = importlib.util.module_from_spec(spec)

@@ -1,5 +1,6 @@
 """Calls of the attention operators at the edge of what the header allows, on the CPU: where
-the pieces of a cut item lie in a workspace, whatever 16 bytes it starts on."""
+the pieces of a cut item lie in a workspace, whatever 16 bytes it starts on, sizes that pass
+64 bits, and the build without torch's headers or beside another torch."""
 import ctypes
 import os
 import subprocess
@@ -85,3 +86,44 @@ def test_read_refuses_sizes_beyond_2_to_the_40(validating, kw):
     st = validating.kv_cache_read(ctypes.byref(p), A16, A16, A16, None, None, None, None, A16, A16, None, None)
     assert st == -1 and "too many" in validating.ra_last_error().decode()
     assert validating.kv_cache_read(ctypes.byref(read_params()), A16, A16, A16, None, None, None, None, A16, A16, None, None) == 0
+
+
+# ---------------------------------------------------------------- the build
+def test_the_library_builds_without_the_headers_of_the_binding(monkeypatch, tmp_path, capsys):
+    """nvcc alone makes the library: what only the binding needs may be missing."""
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / build.LIB_NAME))
+    monkeypatch.setattr(build, "CALLS_PATH", str(tmp_path / "calls.so"))
+    monkeypatch.setattr(build.shutil, "which", lambda name: None if name == "g++" else "/bin/" + name)
+    monkeypatch.setattr(build, "nvcc", lambda: "nvcc")
+    ran = []
+
+    def run(cmd, **kw):
+        if cmd[0] == "g++":
+            raise FileNotFoundError("g++")
+        ran.append(cmd[0])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    assert build.build() == build.LIB_PATH and os.path.exists(build.LIB_PATH) and not os.path.exists(build.CALLS_PATH)
+    assert len(ran) == len(build.SOURCES) + 1 and "g++" in capsys.readouterr().err
+    assert build.up_to_date()
+    build.build()
+    assert len(ran) == len(build.SOURCES) + 1
+
+
+def test_a_binding_built_for_another_torch_is_not_taken():
+    """The module's name holds the interpreter and the torch that it was compiled for."""
+    import torch
+
+    assert torch.__version__ in os.path.basename(build.CALLS_PATH)
+
+
+def test_a_missing_binding_says_what_its_build_lacks(monkeypatch):
+    build.build()
+    monkeypatch.setattr(native, "_CALLS", None)
+    monkeypatch.setattr(native, "CALLS_PATH", "/nowhere/calls.so")
+    monkeypatch.setattr(build, "calls_missing", lambda: "no headers here", raising=False)
+    with pytest.raises(FileNotFoundError, match="no headers here"):
+        native.packed_attention_params(None, None, None, None)
