@@ -470,7 +470,8 @@ typedef struct {
 } paged_attention_params;
 
 /* Workspace bytes of paged_attention: a status word and the partial results of
- * sequences that several blocks share (at most 64 MiB).  Zero-fill it once after
+ * sequences that several blocks share (at most 64 MiB).  With as many new tokens a
+ * sequence, fewer or shorter sequences never need more.  Zero-fill it once after
  * allocation.  Calls that may overlap need workspaces of their own. */
 ra_status paged_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache,
                                           const paged_attention_params* p, size_t* bytes);

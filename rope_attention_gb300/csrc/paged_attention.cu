@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
 struct Plan {
   int32_t NR, G, hb, tb, hblocks;
-  int32_t whole;
+  int32_t whole, room;          // room: blocks that the workspace is sized for
   int64_t items;                // at most
   int32_t ns, nsg;
   int32_t vslabs, kslabs, qslabs, kslab0, stage, staging, off_p, off_ring, off_staging, off_misc, smem;
@@ -983,8 +983,11 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   const int64_t T = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
   const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
   pl->whole = (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
-  const int64_t runs = pl->whole ? pl->items : pl->items * T;
-  pl->G = static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs)));
+  const auto blocks = [](int64_t runs) { return static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs))); };
+  pl->G = blocks(pl->whole ? pl->items : pl->items * T);
+  // as if items were cut always: a workspace that is sized at the largest batch, which may take
+  // whole items, serves the smaller ones, which cut theirs
+  pl->room = blocks(pl->items * T);
   return true;
 }
 
@@ -1012,7 +1015,7 @@ size_t paged_attention_workspace(const PagedLaunch& L) {
   if (paged_tile_serves(L)) return kAttnHeader + paged_tile_workspace(L);
   Plan pl;
   if (!plan(L, &pl)) return 0;
-  return kAttnHeader + (pl.whole ? kJoinSlack + join_meta_bytes(pl.G) : join_bytes(pl.G, pl.NR, L.Dv));
+  return kAttnHeader + join_bytes(pl.room, pl.NR, L.Dv);
 }
 
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why) {

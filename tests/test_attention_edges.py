@@ -1,6 +1,7 @@
 """Calls of the attention operators at the edge of what the header allows, on the CPU: where
 the pieces of a cut item lie in a workspace, whatever 16 bytes it starts on, sizes that pass
-64 bits, and the build without torch's headers or beside another torch."""
+64 bits, workspaces sized at the largest call, and the build without torch's headers or beside
+another torch."""
 import ctypes
 import os
 import subprocess
@@ -86,6 +87,28 @@ def test_read_refuses_sizes_beyond_2_to_the_40(validating, kw):
     st = validating.kv_cache_read(ctypes.byref(p), A16, A16, A16, None, None, None, None, A16, A16, None, None)
     assert st == -1 and "too many" in validating.ra_last_error().decode()
     assert validating.kv_cache_read(ctypes.byref(read_params()), A16, A16, A16, None, None, None, None, A16, A16, None, None) == 0
+
+
+# ---------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("variant,N,heads,new", [(2, 8, 64, 1), (2, 2, 8, 1), (2, 8, 64, 40), (2, 1, 128, 3), (1, 1, 128, 1),
+                                                 (1, 1, 16, 2)])
+def test_a_workspace_of_the_largest_batch_serves_the_smaller_ones(validating, variant, N, heads, new):
+    """The same new tokens a sequence: fewer sequences, or shorter ones, need no more."""
+    n = ctypes.c_size_t()
+
+    def need(B, longest):
+        c = read_params(variant=variant, N=N, block_num=1 << 16, **(dict(Dkv=576, Dv=512) if variant == 1 else {}))
+        p = native.PagedAttentionParams(B=B, total_q=B * new, num_heads=heads, causal=1, softmax_scale=0.1, max_seq_len=longest,
+                                        block_table_stride=1 << 12)
+        assert validating.paged_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(p), ctypes.byref(n)) == 0
+        return n.value
+
+    for longest in (0, 1, 64, 333, 500, 4096, 20000, 131072):
+        sizes = [need(B, longest) for B in range(1, 200)]
+        assert sizes == sorted(sizes) and sizes[-1] <= 64 << 20, longest
+    for B in (1, 3, 19, 20, 38, 40, 160, 1000):
+        sizes = [need(B, longest) for longest in (0, 1, 64, 200, 333, 450, 600, 1000, 4096, 20000, 131072)]
+        assert sizes == sorted(sizes), B
 
 
 # ---------------------------------------------------------------- the build
