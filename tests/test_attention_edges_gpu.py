@@ -1,11 +1,12 @@
 """Calls of the attention operators at the edge of what the header allows, on the GPU:
 workspaces that start on any 16 bytes, waits of the shortest time limit, codes beside their
-zero point, weights far below a row's largest, scales
-near the least."""
+zero point, weights far below a row's largest, scales near the least, and batches of very
+different lengths."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 from attention_util import HALF_STEP, TORCH
 from rope_attention_gb300 import native
 from test_attention_use import DEFAULT_WAIT_NS, Packed, Paged
@@ -115,6 +116,29 @@ def test_read_near_the_zero_point(kind, dtype):
         assert ((lo <= got) & (got <= hi)).all(), float(((got < lo) | (got > hi)).mean())
 
 
+@pytest.mark.parametrize("variant,quant", [(2, False), (2, True), (1, False), (1, True)])
+def test_rows_of_a_serving_cache_read_back(variant, quant):
+    """Every row of a cache that the writer filled and attention reads: the bytes that are there,
+    dequantised, within three half steps of fp32 and the last rounding."""
+    x = Paged(23, [130, 130], [100, 100], 4, variant=variant, quant=quant)
+    x.kv.run()
+    x.run()
+    c = x.kv.case
+    read = [torch.full((c.B, c.N, c.S, w), 7.0, dtype=torch.bfloat16, device="cuda") for w in (c.k_width, c.ckv_width)]
+    native.kv_cache_read(x.kv.params, x.kv.index, x.kv.k_cache, x.kv.ckv_cache, *read, x.kv.k_scale, x.kv.v_scale,
+                         x.kv.k_offset, x.kv.v_offset)
+    torch.cuda.synchronize()
+    for got, cache, scale, offset, kind in ((read[0], x.kv.k_cache, c.k_scale, c.k_offset, c.k_qtype),
+                                            (read[1], x.kv.ckv_cache, c.v_scale, c.v_offset, c.v_qtype)):
+        host = cache.cpu().numpy() if quant else cache.view(torch.int16).cpu().numpy().view(np.uint16)
+        want, bad = oracle.attention.kv_cache_read(c.index, host, B=c.B, N=c.N, S=c.S, cache_mode=c.cache_mode,
+                                                   block_size=c.block_size, stored=kind if quant else "bf16", scale=scale,
+                                                   offset=offset)
+        lo, hi = rounded_between(want, 3.01 * 2.0 ** -24 if quant else 0.0, "bf16")
+        got = got.double().cpu().numpy()
+        assert bad == 0 and np.abs(want).mean() > 0.1 and ((lo <= got) & (got <= hi)).all()
+
+
 def one_cache(lens, kt, dtype, variant=2):
     """Zeroed caches of one kv head in pages of 64, their parameters, the table and, over codes,
     scales of 2 for keys and 1 for values.  Keys and values 64 wide, V1's with 16 rotated channels."""
@@ -221,3 +245,18 @@ def test_scores_that_are_all_alike(scale, zero_q, kt, variant, new):
         mean, spread = values.mean(0), values.abs().mean(0)
         assert ((out.double() - mean).abs() <= HALF_STEP["bf16"] * (mean.abs() + spread) + 2.0 ** -17 * spread).all()
         assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -17 * (1 + np.log(n))
+
+
+@pytest.mark.parametrize("lens,heads,N,variant,quant", [
+    ([900, 3, 64, 700, 1, 128, 450, 65, 333, 899] * 2, 8, 8, 2, False),        # one whole item a block
+    ([900, 3, 64, 700, 1, 128, 450, 65, 333, 899] * 4, 8, 8, 2, True),         # whole items, two or three a block
+    ([9000] + [130] * 30, 8, 1, 1, False),                                     # one cut into many pieces among whole ones
+    ([9000] + [130] * 30, 16, 8, 2, True),
+], ids=["whole", "whole_int8", "long_v1", "long_int8"])
+def test_decode_batches_of_very_different_lengths(lens, heads, N, variant, quant):
+    x = Paged(24, lens, [1] * len(lens), heads, N=N, variant=variant, quant=quant)
+    x.kv.run()
+    x.run()
+    torch.cuda.synchronize()
+    assert x.status() == 0
+    x.check("lengths")
