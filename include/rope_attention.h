@@ -46,9 +46,10 @@
  *  - bf16 values are passed as their 16-bit patterns (uint16_t).
  *  - qkv_cte_mx, qkv_cte_mx_project, qkv_cte_mx_norm_rope, row_quantize_e4m3,
  *    row_quantize_e4m3_packed, qkv_cte_mx_pack_weight, kv_rms_norm_rope_cache,
- *    packed_attention, paged_attention and kv_cache_read launch kernels only (no allocation, no synchronisation), so after one
- *    eager call per device they can be captured into a CUDA graph and
- *    replayed; the status readers synchronise and cannot be captured.
+ *    packed_attention, paged_attention and kv_cache_read launch kernels only
+ *    (no allocation, no synchronisation), so after one eager call per device
+ *    they can be captured into a CUDA graph and replayed; the status readers
+ *    synchronise and cannot be captured.
  */
 #ifndef ROPE_ATTENTION_H_
 #define ROPE_ATTENTION_H_
@@ -418,11 +419,14 @@ ra_status packed_attention_workspace_bytes(const packed_attention_params* p, siz
 
 /* One call.
  *   q, k, v       strided as above, 16-byte aligned; out likewise, no two elements of
- *                 out in one place and none in one with an input's.  A NaN in a row of q makes that row of out NaN; an
- *                 infinity or NaN in a row of k or v can reach every row of its
- *                 sequence, those that the causal mask keeps from it too.  Rows
- *                 outside every sequence may hold anything and the matching rows of
- *                 out (and lse) are left as they were.
+ *                 out in one place and none in one with an input's.  A NaN in a row of
+ *                 q makes that row of out NaN; an infinity or NaN in a row of k or v
+ *                 can reach every row of its sequence, those that the causal mask
+ *                 keeps from it too.  Rows outside every sequence may hold anything
+ *                 and the matching rows of out (and lse) are left as they were.
+ * Scores, maxima, sums and accumulators are fp32.  The probabilities are rounded to
+ * the type of v for the second product: half a step of it (bf16 2^-8, fp16 2^-11)
+ * relative to each; in fp16 those below 2^-32 of a row's largest may become 0.
  *   lse           [total_q, num_heads] fp32: log of the sum of the exponentials, or NULL.
  *   cu_seqlens_q  [B + 1] int32 on the device: sequence b has the query tokens
  *                 cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (non-decreasing, at most
@@ -454,7 +458,9 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
  * sequence are its last Lq positions, and with `causal` query i sees the
  * positions <= seq_len - Lq + i.  A query that sees no key gives zeros (lse -inf).
  * Non-finite values as in packed_attention; slots that are no sequence's position may
- * hold anything.
+ * hold anything.  Roundings as in packed_attention; where the cache holds codes, q / scale
+ * and the probabilities that meet them are rounded to fp16 (the probabilities as two
+ * fp16 numbers where kv_dtype is fp16), and the codes enter exactly.
  * Built for V1 with Dv <= 512 (a multiple of 64) and rope_size <= 64 (a multiple
  * of 16), and V2 with Dkv <= 256 and Dv <= 256 (multiples of 16), and for caches of
  * fewer than 2^31 rows (slots times N): others are RA_ERR_UNSUPPORTED. */
@@ -525,7 +531,8 @@ void ra_test_stall_next_attention(void);
  * fields, the dtypes and the scalar flags.
  *   index         as in kv_rms_norm_rope_cache (here a slot may come several times).
  *                 A token whose index is -1 gives zeros; so does one whose slot is
- *                 outside the cache, which dev_error_count (optional) counts.
+ *                 outside the cache, which dev_error_count (optional) counts.  At
+ *                 most 2^40 rows B * S * N, and in NORM mode 2^40 slots.
  *   k_out         [B, N, S, k_w], c_kv_out [B, N, S, c_w], 16-byte aligned (k_w, c_w: the
  *                 caches' row widths); either may be NULL, and is then not read.
  * Asynchronous on `stream`, allocates nothing. */

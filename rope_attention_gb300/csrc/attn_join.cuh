@@ -1,7 +1,8 @@
 // Work shared out in runs of key tiles, and the joining of what a run cuts in two.
 //
 // Both attention kernels lay the key tiles of all their work items end to end and give
-// each block an equal run, so blocks finish together whatever the lengths.  A block that
+// each block an equal run, so blocks finish together whatever the lengths (or, where items are
+// many or a cut would save too little, runs of whole items).  A block that
 // gets a part of an item stores the part's (max, sum, accumulator) in the workspace; the
 // second kernel here joins an item's parts in the order of the blocks, so results do not
 // depend on which block finished first.
@@ -257,7 +258,9 @@ inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_
   // 151 cuts: 159 us without it, 168 with)
   const bool search = cuts * 4 < blocks;
   // blocks for each cut that there can be, as many as fill the SMs, four on each, once, and have
-  // something to do: of few pieces a warp joins four rows, of many the block one
+  // something to do: of few pieces a warp joins four rows, of many the block one.  (Without the
+  // search the grid is that of joins of few pieces: one long item among many short ones, cut into
+  // many, has its rows joined by the same few blocks.)
   const int units = search ? p.NR * slices : ((p.NR + 3) / 4 * slices + kJoinWarps - 1) / kJoinWarps;
   const int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
   cudaLaunchConfig_t cfg{};

@@ -15,7 +15,7 @@
 //    slot lookups and the index arithmetic, done by one lane per token a turn ahead, are a
 //    small part;
 //  * the loads of kBatch rounds are in flight together.
-// Measured (131072 rows of 512 + 64 int8 channels, 228 MB in all): 52 us, 4.3 TB/s, 64 %
+// Measured (131072 rows of 512 + 64 int8 channels, 228 MB in all): 53 us, 4.3 TB/s, 63 %
 // of a plain copy's rate; a mapping of one row per warp took 86 us.  Half of the issue slots
 // are busy and DRAM at 40 % of its nominal rate: the latency of two dependent loads (slot,
 // then row) at four blocks an SM bounds it.  Five blocks spill and are no faster (53 us).

@@ -8,14 +8,18 @@
 // the second sum does not depend on j and leaves the softmax (it enters the lse), and
 //   out_c = (sum_j p_j code_jc / sum_j p_j - o_c) / s_c.
 // The codes themselves (int8, E4M3, E5M2: all exact in fp16) are the tensor core's
-// operands; q / s is rounded to fp16 behind a power of two per row that brings the row's
-// largest element to [2^9, 2^10), so it keeps 11 bits whatever the scales.
+// operands; q / s is rounded to fp16 behind a power of two per row that keeps the row's
+// elements below 2^15, counted from its largest |q| and the head's largest 1 / s.  Elements
+// down to 2^-29 of that bound keep 11 bits.
 //
 // GB300 mapping.  A work item is one row tile of a sequence and kv head: NR rows, a row
 // being (token, head of the group), against all the sequence's keys in 64-key tiles.
 // The tiles of all items, laid end to end, are cut into equal runs, one per block, so
 // blocks finish together whatever the lengths; an item cut in two or more has its pieces'
-// (max, sum, accumulator) joined by a second kernel, in a fixed order.
+// (max, sum, accumulator) joined by a second kernel, in a fixed order.  Where a cut would save
+// less than its join costs, counted at the largest length (plan()), blocks take runs of whole
+// items instead; those are equal in items, not in tiles, so there they finish together only if
+// the lengths are alike.
 //  * The rows are few (one token: 1..128 heads), so the second product is transposed:
 //    O^T[channel, row] += V^T P^T puts the channels on the MMA's 128 rows and the NR rows
 //    on its N, which costs tensor time and TMEM for NR columns instead of 128.  The
@@ -69,6 +73,7 @@ constexpr int kMaxStages = 6;
 // kJoinAll more the more blocks have a cut.  (V2, one sequence, 2 kv heads: 200 positions 12.6 us
 // whole and 14.5 cut, 333 15.6 and 12.6, 450 18.6 and 12.6; 64 items: 600 positions 20.7 whole and
 // 25.1 cut, 1000 26.3 and 29.0.  V1, 4 items: 333 positions 27.0 and 22.9.)
+// Rounds are counted over kMaxBlocks, the blocks that the workspace has room for.
 constexpr int kJoinTiles = 4, kJoinAll = 10;
 constexpr float kLazy = 8.f;              // log2 of how far a tile may exceed the running maximum
 constexpr uint64_t kDrainNs = 200000000ull;

@@ -1,7 +1,7 @@
 // paged_attention for many rows per sequence and kv head (chunks of new tokens): the caches
 // behind tile_attention.cuh's kernel.  Measured: 512 new tokens a sequence
 // over 4 bf16 sequences of up to 16384 positions, 32 heads over 8, 400 us (1090 TFLOP/s); an fp16 one over an FP8 cache of 2 x 8192 positions,
-// 777 tokens and 32 heads, 337 us (590 TFLOP/s; 265 without the second half of P, whose
+// 777 tokens and 32 heads, 335 us (590 TFLOP/s; 265 without the second half of P, whose
 // results are 1.8 times as far off as fp16's own rounding).
 #include "paged_maps.cuh"
 #include "tile_attention.cuh"
