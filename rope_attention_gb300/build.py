@@ -60,8 +60,12 @@ def _torch_version() -> str:
     root = _torch_root()
     if root is None:
         return "none"
-    with open(os.path.join(root, "version.py")) as f:
-        return re.search(r"__version__ = ['\"]([^'\"]+)", f.read()).group(1)
+    try:
+        with open(os.path.join(root, "version.py")) as f:
+            found = re.search(r"^__version__\b[^=\n]*= *['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        found = None
+    return found.group(1) if found else "unknown"
 
 
 # the calls with torch tensors, linked to the library

@@ -143,6 +143,15 @@ def test_a_binding_built_for_another_torch_is_not_taken():
     assert torch.__version__ in os.path.basename(build.CALLS_PATH)
 
 
+@pytest.mark.parametrize("text,version", [("__version__ = '2.9.1+cu130'\n", "2.9.1+cu130"),
+                                          ('x = 1\n__version__: str = "3.0"\n', "3.0"), ("", "unknown"), (None, "unknown")])
+def test_a_torch_without_a_plain_version_file_stops_nothing(monkeypatch, tmp_path, text, version):
+    if text is not None:
+        (tmp_path / "version.py").write_text(text)
+    monkeypatch.setattr(build, "_torch_root", lambda: str(tmp_path))
+    assert build._torch_version() == version
+
+
 def test_a_missing_binding_says_what_its_build_lacks(monkeypatch):
     build.build()
     monkeypatch.setattr(native, "_CALLS", None)
