@@ -2,7 +2,7 @@
  * rope_attention.h -- C ABI of librope_attention.so, the GB300 (sm_103a)
  * attention-prologue hot path.
  *
- * Two operators of the prologue, and (c) - (e) the attention that follows it:
+ * Two operators of the prologue, and (c) - (g) the attention that follows it:
  *
  *  (a) qkv_cte_mx: the fused QKV projection of the AWS Neuron page "Kernel
  *      reference: qkv_cte -- Wan2.2 additions to the NKI Library QKV CTE MXFP8
@@ -27,6 +27,12 @@
  *      caches gathered by slot and dequantised.  The pages end at the prologue;
  *      these three take the layouts, dtypes and parameters of (a) and (b).
  *
+ *  (f) packed_window_attention, paged_window_attention: (c) and (d) where a query
+ *      sees the last keys up to its own and a few first ones.
+ *      paged_prefix_attention: (d) for sequences that share their first tokens.
+ *  (g) kv_cache_extend, kv_cache_slots, kv_cache_truncate: the pages of the caches,
+ *      from the requests' lengths.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Tensor pointers are DEVICE pointers owned by the caller, dense and
@@ -46,7 +52,8 @@
  *  - bf16 values are passed as their 16-bit patterns (uint16_t).
  *  - qkv_cte_mx, qkv_cte_mx_project, qkv_cte_mx_norm_rope, row_quantize_e4m3,
  *    row_quantize_e4m3_packed, qkv_cte_mx_pack_weight, kv_rms_norm_rope_cache,
- *    packed_attention, paged_attention and kv_cache_read launch kernels only
+ *    packed_attention, paged_attention, kv_cache_read and the calls of (f) and (g)
+ *    that take a stream launch kernels only
  *    (no allocation, no synchronisation), so after one eager call per device
  *    they can be captured into a CUDA graph and replayed; the status readers
  *    synchronise and cannot be captured.
@@ -540,6 +547,136 @@ ra_status kv_cache_read(const kv_rms_norm_rope_cache_params* p, const int64_t* i
                         const void* ckv_cache, const float* k_rope_scale, const float* c_kv_scale,
                         const float* k_rope_offset, const float* c_kv_offset, uint16_t* k_out,
                         uint16_t* c_kv_out, int32_t* dev_error_count, void* stream);
+
+/* ========================================================================
+ * (f) windows with sinks; shared prefixes
+ * ======================================================================== */
+
+/* A query at position P among its sequence's keys (the last query at the last key:
+ * P = Lk - Lq + i) sees the keys j <= P with
+ *   j > P - window, or j < sinks.
+ * Values above 2^31 - 256 count as that. */
+typedef struct {
+  int64_t window;             /* >= 1                                                  */
+  int64_t sinks;              /* >= 0; 0: none                                         */
+} attention_window;
+
+/* packed_attention with a window: arguments, precision and workspace are that call's
+ * (packed_attention_workspace_bytes); `causal` must be 1.  The time goes with the keys
+ * that are seen, not with all. */
+ra_status packed_window_attention(const packed_attention_params* p, const attention_window* window,
+                                  const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* out,
+                                  float* lse, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* paged_attention with a window: arguments, precision and workspace are that call's
+ * (paged_attention_workspace_bytes); `causal` must be 1.  Entries of block_table whose
+ * pages hold no position that some query of the call sees may be anything (-1, or a
+ * page that another sequence has meanwhile): they are not counted as errors, and their
+ * rows are not used.  Rows of a page that holds such a position must be finite up to the
+ * sequence's end. */
+ra_status paged_window_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                                 const attention_window* window, const uint16_t* q, const void* k_cache,
+                                 const void* ckv_cache, const int32_t* seq_lens, const int32_t* block_table,
+                                 const int32_t* cu_seqlens_q, const float* k_rope_scale,
+                                 const float* c_kv_scale, const float* k_rope_offset,
+                                 const float* c_kv_offset, uint16_t* out, float* lse,
+                                 int32_t* dev_error_count, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Bounds of a prefix that all sequences of a call share. */
+typedef struct {
+  int64_t max_prefix_len;     /* the prefix is not longer (a larger length is clamped) */
+  int64_t table_entries;      /* entries of prefix_table, >= 1                         */
+} attention_prefix;
+
+/* Workspace bytes of paged_prefix_attention: beside what paged_attention needs twice,
+ * fp32 rows [total_q, num_heads, Dv].  With as many sequences and query tokens, shorter
+ * sequences and prefixes never need more.  Zero-fill it once after allocation.  Calls
+ * that may overlap need workspaces of their own. */
+ra_status paged_prefix_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache,
+                                                 const paged_attention_params* p,
+                                                 const attention_prefix* prefix, size_t* bytes);
+
+/* paged_attention of sequences behind a shared prefix, whose keys are read once for the
+ * rows of all of them.  The keys of sequence b are the prefix's positions, which every
+ * query of the call sees, then its own: seq_lens, max_seq_len and block_table count and
+ * hold its own positions alone, of which its queries see those that paged_attention
+ * lets them see.
+ *   prefix_len    [1] int32 on the device: positions of the prefix; 0 allowed.
+ *   prefix_table  [table_entries] int32: position j of the prefix is in page
+ *                 prefix_table[j / block_size] at j % block_size.  The page behind its
+ *                 last position may be partly filled.
+ * The other arguments are those of paged_attention, and so are roundings (the two
+ * results of a row are joined in fp32) and non-finite values.  cu_seqlens_q must be
+ * non-decreasing.  PA modes only: NORM has no pages (RA_ERR_UNSUPPORTED). */
+ra_status paged_prefix_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                                 const attention_prefix* prefix, const uint16_t* q, const void* k_cache,
+                                 const void* ckv_cache, const int32_t* prefix_len,
+                                 const int32_t* prefix_table, const int32_t* seq_lens,
+                                 const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                 const float* k_rope_scale, const float* c_kv_scale,
+                                 const float* k_rope_offset, const float* c_kv_offset, uint16_t* out,
+                                 float* lse, int32_t* dev_error_count, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ========================================================================
+ * (g) paging
+ * ======================================================================== */
+
+/* The pages of a paged cache (PA, PA_BNSD), shared out to requests on the device.
+ *   block_table   [B, block_table_stride] int32: a request's pages in order, as
+ *                 paged_attention takes it.
+ *   free_pages    [block_num] int32: a stack of pages that no request has, the first
+ *                 *free_count entries of it; the last of these is taken first.
+ * Requests' lengths are clamped to [0, block_table_stride * block_size] and *free_count
+ * to [0, block_num]. */
+typedef struct {
+  int64_t B;                  /* requests, 1 .. 16384                                  */
+  int64_t block_num;          /* pages of the cache                                    */
+  int64_t block_size;         /* slots per page                                        */
+  int64_t block_table_stride; /* entries per row of block_table; B times this < 2^31   */
+  int64_t max_tokens;         /* entries of index, <= 2^30 (kv_cache_truncate: any)    */
+} kv_cache_paging_params;
+
+/* Makes room for new_tokens[b] more tokens of each request b (below 0: none), in the
+ * order of the requests: takes the pages it needs from the free list, writes them behind
+ * those it has, and gives the slot of every new token, request after request.
+ *   index         [max_tokens] int64: the tokens' slots (page * block_size + offset), as
+ *                 kv_rms_norm_rope_cache takes them; -1 behind the last.
+ *   cu_seqlens    [B + 1] int32: where each request's tokens start (clamped to max_tokens).
+ *   new_seq_lens  [B] int32: the lengths with the new tokens; may be seq_lens itself.
+ *   new_free_count  [1] int32; may be free_count itself.
+ * A request is refused, whole, whose pages would take more than the free list and the
+ * requests before it leave, whose length would pass its row of the table, or whose
+ * tokens would pass max_tokens: its length stays, its tokens' slots are -1, no page is
+ * taken.  (Requests behind one that was refused for pages get none either unless they need
+ * none.)  A token whose page is outside [0, block_num) gets -1.  dev_error_count
+ * (optional) counts refused requests and such tokens. */
+ra_status kv_cache_extend(const kv_cache_paging_params* p, const int32_t* new_tokens, const int32_t* seq_lens,
+                          int32_t* block_table, const int32_t* free_pages, const int32_t* free_count,
+                          int64_t* index, int32_t* cu_seqlens, int32_t* new_seq_lens,
+                          int32_t* new_free_count, int32_t* dev_error_count, void* stream);
+
+/* The slots of the positions starts[b] .. starts[b] + counts[b] - 1 of each request
+ * (starts NULL: from 0; numbers below 0 count as 0), request after request: index and
+ * cu_seqlens as in kv_cache_extend (entries that do not fit into max_tokens are left
+ * out).  A position behind the table's row or in a page outside [0, block_num) gets -1
+ * and is counted.  With them kv_cache_read reads whole contexts. */
+ra_status kv_cache_slots(const kv_cache_paging_params* p, const int32_t* starts, const int32_t* counts,
+                         const int32_t* block_table, int64_t* index, int32_t* cu_seqlens,
+                         int32_t* dev_error_count, void* stream);
+
+/* Cuts requests back to their first keep[b] tokens (clamped to their length; keep NULL:
+ * all of them end) and puts the pages behind those on the free list, so that
+ * kv_cache_extend takes them in the same order again.  new_seq_lens and new_free_count may
+ * be seq_lens and free_count themselves; block_table is left as it is (entries behind a
+ * sequence's end are not read).  Entries outside [0, block_num) are left out, and so are
+ * pages that the list has no room for; dev_error_count (optional) counts both. */
+ra_status kv_cache_truncate(const kv_cache_paging_params* p, const int32_t* keep, const int32_t* seq_lens,
+                            const int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                            int32_t* new_seq_lens, int32_t* new_free_count, int32_t* dev_error_count,
+                            void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,14 +19,15 @@ qkv_cte   : fused QKV projection + across-heads RMSNorm + rotate-half RoPE
 kv_cache  : KvRmsNormRopeCache (CANN ops-transformer "KvRmsNormRopeCache",
             formulas (1)-(5)).
 attention : packed and paged attention, and rows read back from the caches (the
-            definitions in include/rope_attention.h (c) - (e)).
+            definitions in include/rope_attention.h (c) - (f)).
+paging    : pages, block tables and slots from the requests' lengths (its (g)).
 row_quant : row FP8 quantisation of the activation into the row-packed layout
             (AWS Neuron "Kernel reference: qkv_cte", Interface).
 
 Every function is pinned by ``tests/test_oracle_pins.py``; no function here is
 "parity unpinned".
 """
-from . import attention  # noqa: F401
+from . import attention, paging  # noqa: F401
 from .codes import decode_bf16, decode_e4m3, decode_ue8m0  # noqa: F401
 from .kv_cache import kv_rms_norm_rope_cache  # noqa: F401
 from .qkv_cte import qkv_cte_mx  # noqa: F401

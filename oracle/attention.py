@@ -13,6 +13,10 @@ j % block_size; Norm mode: row j of sequence b), the Lq query tokens being the s
 last positions.  V1's key is the ckv row followed by the k row, its value the ckv row.
 A page outside the cache is left out.
 
+With ``window`` (and causal) a query at position P = i + Lk - Lq sees of the keys j <= P those
+with j > P - window or j < sinks.  paged_prefix_attention: every sequence's keys are the
+prefix's, which all of its queries see, then its own as in paged_attention.
+
 kv_cache_read: rows gathered by the slots of kv_rms_norm_rope_cache's index (-1 and slots
 outside the cache give zeros).
 
@@ -32,15 +36,18 @@ _DECODE = {"bf16": decode_bf16, "fp16": decode_fp16, "e4m3": decode_e4m3, "e5m2"
            "int8": lambda x: np.asarray(x, np.float64)}
 
 
-def attend(q, k, v, scale, causal, hidden=None):
+def attend(q, k, v, scale, causal, hidden=None, window=None, sinks=0, shared=0):
     """One sequence and head: q [Lq, Dk], k [Lk, Dk], v [Lk, Dv] float64.  ``hidden``
-    marks keys that no query sees.  Returns out [Lq, Dv], lse [Lq], spread [Lq, Dv]."""
+    marks keys that no query sees; the first ``shared`` keys are seen by all.  Returns out
+    [Lq, Dv], lse [Lq], spread [Lq, Dv]."""
     Lq, Lk = q.shape[0], k.shape[0]
     out, spread = np.zeros((Lq, v.shape[1])), np.zeros((Lq, v.shape[1]))
     lse = np.full(Lq, -np.inf)
     for i in range(Lq):
-        n = min(Lk, max(0, i + Lk - Lq + 1)) if causal else Lk
+        n = min(Lk, max(shared, i + Lk - Lq + 1)) if causal else Lk
         keep = np.arange(n) if hidden is None else np.nonzero(~hidden[:n])[0]
+        if window is not None:
+            keep = keep[(keep > i + Lk - Lq - window) | (keep < sinks)]
         if keep.size == 0:
             continue
         s = k[keep] @ q[i] * scale
@@ -53,7 +60,7 @@ def attend(q, k, v, scale, causal, hidden=None):
     return out, lse, spread
 
 
-def packed_attention(q, k, v, *, starts_q, starts_k, scale, causal) -> dict:
+def packed_attention(q, k, v, *, starts_q, starts_k, scale, causal, window=None, sinks=0) -> dict:
     """q [Tq, heads, d], k and v [Tk, kv_heads, d] float64; starts [B + 1].  Rows outside
     every sequence are NaN in the results."""
     g = q.shape[1] // k.shape[1]
@@ -62,7 +69,7 @@ def packed_attention(q, k, v, *, starts_q, starts_k, scale, causal) -> dict:
     for b in range(len(starts_q) - 1):
         a, z = slice(starts_q[b], starts_q[b + 1]), slice(starts_k[b], starts_k[b + 1])
         for h in range(q.shape[1]):
-            o, l, s = attend(q[a, h], k[z, h // g], v[z, h // g], scale, causal)
+            o, l, s = attend(q[a, h], k[z, h // g], v[z, h // g], scale, causal, window=window, sinks=sinks)
             res["out"][a, h], res["lse"][a, h], res["spread"][a, h] = o, l, s
             if k[z].shape[0] and q[a].shape[0]:
                 res["reach"][a, h] = (np.abs(q[a, h]) @ np.abs(k[z, h // g]).T).max(axis=1) * scale
@@ -96,8 +103,9 @@ def _rows(cache, cache_mode, block_size, b, n, L, table):
 
 def paged_attention(q, k_cache, ckv_cache, *, variant, seq_lens, starts_q, scale, causal, cache_mode="PA_BNSD",
                     block_size=0, table=None, k_type="bf16", v_type="bf16", k_scale=None, k_offset=None,
-                    v_scale=None, v_offset=None) -> dict:
-    """q [Tq, heads, Dk] float64; caches as stored (bit patterns, codes)."""
+                    v_scale=None, v_offset=None, window=None, sinks=0, prefix_len=0, prefix_table=None) -> dict:
+    """q [Tq, heads, Dk] float64; caches as stored (bit patterns, codes).  With prefix_len the
+    keys of every sequence are those of prefix_table [pages], then its own."""
     kc, vc = _DECODE[k_type](k_cache), _DECODE[v_type](ckv_cache)
     N = kc.shape[2] if cache_mode == "PA" else kc.shape[1]
     g, Dv = q.shape[1] // N, vc.shape[-1]
@@ -108,6 +116,10 @@ def paged_attention(q, k_cache, ckv_cache, *, variant, seq_lens, starts_q, scale
         for n in range(N):
             ks, bad = _rows(kc, cache_mode, block_size, b, n, L, table)
             vs, _ = _rows(vc, cache_mode, block_size, b, n, L, table)
+            if prefix_len:
+                first, missing = _rows(kc, cache_mode, block_size, 0, n, prefix_len, [prefix_table])
+                ks, bad = np.concatenate([first, ks]), np.concatenate([missing, bad])
+                vs = np.concatenate([_rows(vc, cache_mode, block_size, 0, n, prefix_len, [prefix_table])[0], vs])
             k = _dequantise(ks, k_scale, k_offset, n)
             v = _dequantise(vs, v_scale, v_offset, n)
             one = lambda s, w: np.ones(w) if s is None else np.broadcast_to(np.asarray(s)[n] if np.ndim(s) == 2 else s, w)
@@ -117,9 +129,9 @@ def paged_attention(q, k_cache, ckv_cache, *, variant, seq_lens, starts_q, scale
                 stored = np.concatenate([vs, ks], axis=1)
                 div = np.concatenate([one(v_scale, vs.shape[1]), div])
             for h in range(n * g, (n + 1) * g):
-                o, l, s = attend(q[a, h], k, v, scale, causal, bad)
+                o, l, s = attend(q[a, h], k, v, scale, causal, bad, window, sinks, prefix_len)
                 res["out"][a, h], res["lse"][a, h], res["spread"][a, h] = o, l, s
-                if L and q[a].shape[0]:
+                if ks.shape[0] and q[a].shape[0]:
                     res["reach"][a, h] = (np.abs(q[a, h] / div) @ np.abs(np.where(bad[:, None], 0, stored)).T).max(axis=1) * scale
     return res
 

@@ -4,10 +4,12 @@
 #include <cstdarg>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
 
 #include "rope_attention.h"
 #include "attention.h"
+#include "cache_paging.h"
 #include "internal.h"
 #include "kv_cache.h"
 #include "row_quant.h"
@@ -336,6 +338,32 @@ ra_status check_cache(const kv_rms_norm_rope_cache_params* p, const float* k_sca
   return RA_OK;
 }
 
+// where the scales are not at hand: a quantised dtype stands for its scale
+ra_status check_cache_alone(const kv_rms_norm_rope_cache_params* p, CacheShape* s) {
+  if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "cache params is NULL");
+  const float* given = reinterpret_cast<const float*>(uintptr_t{16});
+  return check_cache(p, quant_kind(p->k_cache_dtype) > 0 ? given : nullptr, quant_kind(p->ckv_cache_dtype) > 0 ? given : nullptr,
+                     nullptr, nullptr, s);
+}
+
+ra_status check_window(const attention_window* w, int32_t causal) {
+  if (w->window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1");
+  if (w->sinks < 0) return fail(RA_ERR_INVALID_ARG, "sinks must be >= 0");
+  if (causal != 1) return fail(RA_ERR_INVALID_ARG, "a window needs causal = 1");
+  return RA_OK;
+}
+
+ra_status check_prefix(const kv_rms_norm_rope_cache_params* c, const attention_prefix* x) {
+  if (x == nullptr) return fail(RA_ERR_INVALID_ARG, "prefix is NULL");
+  if (c->cache_mode == RA_CACHE_NORM)
+    return fail(RA_ERR_UNSUPPORTED, "NORM mode has no pages for sequences to share");
+  if (x->max_prefix_len < 0 || x->max_prefix_len > ra::kMostPositions)
+    return fail(RA_ERR_INVALID_ARG, "max_prefix_len must be in [0, 2^31 - 256]");
+  if (x->table_entries < 1 || x->table_entries > (1LL << 31))
+    return fail(RA_ERR_INVALID_ARG, "table_entries must be in [1, 2^31]");
+  return RA_OK;
+}
+
 ra::PackedLaunch packed_launch(const packed_attention_params* p) {
   ra::PackedLaunch L{};
   L.B = p->B;
@@ -455,7 +483,38 @@ ra::PagedLaunch paged_launch(const kv_rms_norm_rope_cache_params* c, const paged
   L.block_size = c->cache_mode == RA_CACHE_NORM ? 1 : c->block_size;
   L.cache_seq = c->cache_seq_len;
   L.table_stride = p->block_table_stride;
+  L.cu_step = 1;
   return L;
+}
+
+// the call over the prefix: the tokens of all sequences as one's
+ra::PagedLaunch over_prefix(const ra::PagedLaunch& L, const attention_prefix* x) {
+  ra::PagedLaunch P = L;
+  P.cu_step = static_cast<int32_t>(L.B);
+  P.B = 1;
+  P.causal = 0;
+  P.max_seq_len = x->max_prefix_len;
+  P.table_stride = x->table_entries;
+  return P;
+}
+
+// The workspace of paged_prefix_attention: the header and the parts of the call over the prefix, the
+// other call's, the fp32 rows that go from one to the other, and their statistics.
+struct PrefixPlan {
+  size_t partials, rows, stats, bytes;
+};
+size_t next_256(size_t n) { return (n + 255) / 256 * 256; }
+uint8_t* aligned_in(uint8_t* ws, size_t at) {  // the step from any 16 bytes to the next 32 has room
+  return ws + at + (0 - reinterpret_cast<uintptr_t>(ws + at)) % 32;
+}
+PrefixPlan prefix_plan(const ra::PagedLaunch& L, const attention_prefix* x) {
+  const size_t rows = static_cast<size_t>(L.total_q) * L.heads;
+  PrefixPlan p;
+  p.partials = next_256(ra::paged_attention_workspace(over_prefix(L, x)));
+  p.rows = p.partials + next_256(ra::paged_attention_workspace(L) - ra::kAttnHeader);
+  p.stats = p.rows + next_256(rows * L.Dv * sizeof(float) + 32);
+  p.bytes = p.stats + next_256(rows * sizeof(float2) + 32);
+  return p;
 }
 
 }  // namespace
@@ -806,10 +865,12 @@ ra_status packed_attention_workspace_bytes(const packed_attention_params* p, siz
   return ok();
 }
 
-ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, const uint16_t* k,
-                           const uint16_t* v, uint16_t* out, float* lse, const int32_t* cu_seqlens_q,
-                           const int32_t* cu_seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
+// packed_attention, or with `w` packed_window_attention
+static ra_status packed_call(const packed_attention_params* p, const attention_window* w, const uint16_t* q, const uint16_t* k,
+                             const uint16_t* v, uint16_t* out, float* lse, const int32_t* cu_seqlens_q,
+                             const int32_t* cu_seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
   ra_status st = check_packed(p);
+  if (st == RA_OK && w) st = check_window(w, p->causal);
   if (st != RA_OK) return st;
   if (!q || !k || !v || !out) return fail(RA_ERR_INVALID_ARG, "q, k, v and out are required");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
@@ -837,55 +898,80 @@ ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, 
   L.wait_ns = g_wait_ns.load();
   L.stall_loads = g_stall_next_attn.exchange(0);
   const char* why = "launch failed";
-  const cudaError_t e = ra::launch_packed_attention(L, static_cast<cudaStream_t>(stream), &why);
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "packed_attention: %s (%s)", why, cudaGetErrorString(e));
+  if (w) {
+    L.window = w->window;
+    L.sinks = w->sinks;
+  }
+  const cudaError_t e = w ? ra::launch_packed_window(L, static_cast<cudaStream_t>(stream), &why)
+                          : ra::launch_packed_attention(L, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess)
+    return fail(RA_ERR_CUDA, "%s: %s (%s)", w ? "packed_window_attention" : "packed_attention", why, cudaGetErrorString(e));
   return ok();
+}
+
+ra_status packed_attention(const packed_attention_params* p, const uint16_t* q, const uint16_t* k,
+                           const uint16_t* v, uint16_t* out, float* lse, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
+  return packed_call(p, nullptr, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, workspace, workspace_bytes, stream);
+}
+
+ra_status packed_window_attention(const packed_attention_params* p, const attention_window* window, const uint16_t* q,
+                                  const uint16_t* k, const uint16_t* v, uint16_t* out, float* lse,
+                                  const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!window) return fail(RA_ERR_INVALID_ARG, "window is NULL");
+  return packed_call(p, window, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, workspace, workspace_bytes, stream);
 }
 
 ra_status paged_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache,
                                           const paged_attention_params* p, size_t* bytes) {
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
-  if (cache == nullptr) return fail(RA_ERR_INVALID_ARG, "cache params is NULL");
-  // the scales are not at hand: a quantised dtype stands for its scale
-  const float* given = reinterpret_cast<const float*>(uintptr_t{16});
   CacheShape s;
-  ra_status st = check_cache(cache, quant_kind(cache->k_cache_dtype) > 0 ? given : nullptr,
-                             quant_kind(cache->ckv_cache_dtype) > 0 ? given : nullptr, nullptr, nullptr, &s);
+  ra_status st = check_cache_alone(cache, &s);
   if (st == RA_OK) st = check_paged(cache, p, s);
   if (st != RA_OK) return st;
   *bytes = ra::paged_attention_workspace(paged_launch(cache, p, s));
   return ok();
 }
 
-ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
-                          const uint16_t* q, const void* k_cache, const void* ckv_cache,
-                          const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
-                          const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
-                          const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+// paged_attention; with `w` paged_window_attention, with `x` and its two tensors paged_prefix_attention
+static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                            const attention_window* w, const attention_prefix* x, const int32_t* prefix_len,
+                            const int32_t* prefix_table, const uint16_t* q, const void* k_cache, const void* ckv_cache,
+                            const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                            const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
+                            const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
+                            void* workspace, size_t workspace_bytes, void* stream) {
   CacheShape s;
   ra_status st = check_cache(cache, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, &s);
   if (st == RA_OK) st = check_paged(cache, p, s);
+  if (st == RA_OK && w) st = check_window(w, p->causal);
+  if (st == RA_OK && x) st = check_prefix(cache, x);
   if (st != RA_OK) return st;
   if (!q || !k_cache || !ckv_cache || !seq_lens || !out)
     return fail(RA_ERR_INVALID_ARG, "q, k_cache, ckv_cache, seq_lens and out are required");
+  if (x && (!prefix_len || !prefix_table)) return fail(RA_ERR_INVALID_ARG, "prefix_len and prefix_table are required");
   if ((cache->cache_mode == RA_CACHE_NORM) != (block_table == nullptr))
     return fail(RA_ERR_INVALID_ARG, "the PA modes need a block_table, NORM mode takes none");
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(ckv_cache) || !aligned16(out))
     return fail(RA_ERR_ALIGNMENT, "q, out and the caches must be 16-byte aligned");
   if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(seq_lens) |
         reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
-        reinterpret_cast<uintptr_t>(dev_error_count)) & 3u) != 0)
-    return fail(RA_ERR_ALIGNMENT, "lse, seq_lens, block_table, cu_seqlens_q and dev_error_count must be 4-byte aligned");
+        reinterpret_cast<uintptr_t>(dev_error_count) | reinterpret_cast<uintptr_t>(prefix_len) |
+        reinterpret_cast<uintptr_t>(prefix_table)) & 3u) != 0)
+    return fail(RA_ERR_ALIGNMENT, "lse, lengths, block tables, cu_seqlens_q and dev_error_count must be 4-byte aligned");
   if (!cu_seqlens_q && p->total_q % p->B != 0)
     return fail(RA_ERR_INVALID_ARG, "without cu_seqlens_q, total_q must be a multiple of B");
   ra::PagedLaunch L = paged_launch(cache, p, s);
-  st = check_attn_workspace(workspace, workspace_bytes, ra::paged_attention_workspace(L));
+  PrefixPlan plan{};
+  if (x) plan = prefix_plan(L, x);
+  st = check_attn_workspace(workspace, workspace_bytes, x ? plan.bytes : ra::paged_attention_workspace(L));
   if (st != RA_OK) return st;
   if (validate_only()) return ok();
   L.q = q;
   L.out = out;
   L.lse = lse;
+  L.shifts = lse != nullptr;
   L.k_cache = k_cache;
   L.v_cache = ckv_cache;
   L.k_scale = k_rope_scale;
@@ -901,9 +987,79 @@ ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const page
   L.wait_ns = g_wait_ns.load();
   L.stall_loads = g_stall_next_attn.exchange(0);
   const char* why = "launch failed";
-  const cudaError_t e = ra::launch_paged_attention(L, static_cast<cudaStream_t>(stream), &why);
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "paged_attention: %s (%s)", why, cudaGetErrorString(e));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (w) {
+    L.window = w->window;
+    L.sinks = w->sinks;
+  }
+  if (x) {
+    // the prefix's keys for the rows of all sequences, then each sequence's own, which join those
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    ra::PagedLaunch P = over_prefix(L, x);
+    P.seq_lens = prefix_len;
+    P.table = prefix_table;
+    P.lse = nullptr;
+    P.rows_out = reinterpret_cast<float*>(aligned_in(ws, plan.rows));
+    P.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
+    L.prior = P.rows_out;
+    L.prior_stats = P.stats_out;
+    L.partials = ws + plan.partials;
+    e = ra::launch_paged_extended(P, cs, &why);
+  }
+  if (e == cudaSuccess) e = w || x ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
+  if (e != cudaSuccess)
+    return fail(RA_ERR_CUDA, "%s: %s (%s)", x ? "paged_prefix_attention" : w ? "paged_window_attention" : "paged_attention", why,
+                cudaGetErrorString(e));
   return ok();
+}
+
+ra_status paged_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                          const uint16_t* q, const void* k_cache, const void* ckv_cache,
+                          const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                          const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
+                          const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_call(cache, p, nullptr, nullptr, nullptr, nullptr, q, k_cache, ckv_cache, seq_lens, block_table, cu_seqlens_q,
+                    k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, out, lse, dev_error_count, workspace,
+                    workspace_bytes, stream);
+}
+
+ra_status paged_window_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                                 const attention_window* window, const uint16_t* q, const void* k_cache,
+                                 const void* ckv_cache, const int32_t* seq_lens, const int32_t* block_table,
+                                 const int32_t* cu_seqlens_q, const float* k_rope_scale, const float* c_kv_scale,
+                                 const float* k_rope_offset, const float* c_kv_offset, uint16_t* out, float* lse,
+                                 int32_t* dev_error_count, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!window) return fail(RA_ERR_INVALID_ARG, "window is NULL");
+  return paged_call(cache, p, window, nullptr, nullptr, nullptr, q, k_cache, ckv_cache, seq_lens, block_table, cu_seqlens_q,
+                    k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, out, lse, dev_error_count, workspace,
+                    workspace_bytes, stream);
+}
+
+ra_status paged_prefix_attention_workspace_bytes(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                                                 const attention_prefix* prefix, size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  CacheShape s;
+  ra_status st = check_cache_alone(cache, &s);
+  if (st == RA_OK) st = check_paged(cache, p, s);
+  if (st == RA_OK) st = check_prefix(cache, prefix);
+  if (st != RA_OK) return st;
+  *bytes = prefix_plan(paged_launch(cache, p, s), prefix).bytes;
+  return ok();
+}
+
+ra_status paged_prefix_attention(const kv_rms_norm_rope_cache_params* cache, const paged_attention_params* p,
+                                 const attention_prefix* prefix, const uint16_t* q, const void* k_cache,
+                                 const void* ckv_cache, const int32_t* prefix_len, const int32_t* prefix_table,
+                                 const int32_t* seq_lens, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                 const float* k_rope_scale, const float* c_kv_scale, const float* k_rope_offset,
+                                 const float* c_kv_offset, uint16_t* out, float* lse, int32_t* dev_error_count,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!prefix) return fail(RA_ERR_INVALID_ARG, "prefix is NULL");
+  return paged_call(cache, p, nullptr, prefix, prefix_len, prefix_table, q, k_cache, ckv_cache, seq_lens, block_table,
+                    cu_seqlens_q, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, out, lse, dev_error_count, workspace,
+                    workspace_bytes, stream);
 }
 
 ra_status attention_status(void* workspace, void* stream, int32_t* device_status) {
@@ -923,6 +1079,108 @@ ra_status attention_status(void* workspace, void* stream, int32_t* device_status
   if (e != cudaSuccess) return cuda_fail(e, "attention status read");
   *device_status = v;
   if (v != 0) return fail(RA_ERR_TIMEOUT, "an attention pipeline wait ran out of time (status %d)", v);
+  return ok();
+}
+
+static ra_status check_paging(const kv_cache_paging_params* p) {
+  if (p == nullptr) return fail(RA_ERR_INVALID_ARG, "params is NULL");
+  if (p->B < 1 || p->max_tokens < 1) return fail(RA_ERR_INVALID_ARG, "B and max_tokens must be >= 1 (no empty tensors)");
+  if (p->block_num < 1 || p->block_num > 0x7fffffffLL || p->block_size < 1 || p->block_size > 0x7fffffffLL)
+    return fail(RA_ERR_INVALID_ARG, "block_num and block_size must be in [1, 2^31)");
+  if (p->block_table_stride < 1 || p->block_table_stride > 0x7fffffffLL)
+    return fail(RA_ERR_INVALID_ARG, "block_table_stride must be in [1, 2^31)");
+  if (p->B > ra::kPagingRequests) return fail(RA_ERR_UNSUPPORTED, "the paging calls are built for up to 16384 requests");
+  if (p->B * p->block_table_stride > 0x7fffffffLL || p->max_tokens > ra::kPagingTokens)
+    return fail(RA_ERR_UNSUPPORTED, "the paging calls are built for block tables below 2^31 entries and up to 2^30 tokens");
+  return RA_OK;
+}
+static bool aligned4(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return false;
+  return true;
+}
+static ra::PagingLaunch paging_launch(const kv_cache_paging_params* p) {
+  ra::PagingLaunch L{};
+  L.B = p->B;
+  L.block_num = p->block_num;
+  L.block_size = p->block_size;
+  L.table_stride = p->block_table_stride;
+  L.max_tokens = p->max_tokens;
+  return L;
+}
+
+ra_status kv_cache_extend(const kv_cache_paging_params* p, const int32_t* new_tokens, const int32_t* seq_lens,
+                          int32_t* block_table, const int32_t* free_pages, const int32_t* free_count, int64_t* index,
+                          int32_t* cu_seqlens, int32_t* new_seq_lens, int32_t* new_free_count, int32_t* dev_error_count,
+                          void* stream) {
+  const ra_status st = check_paging(p);
+  if (st != RA_OK) return st;
+  if (!new_tokens || !seq_lens || !block_table || !free_pages || !free_count || !index || !cu_seqlens || !new_seq_lens ||
+      !new_free_count)
+    return fail(RA_ERR_INVALID_ARG, "every tensor but dev_error_count is required");
+  if ((reinterpret_cast<uintptr_t>(index) & 7u) || !aligned4({new_tokens, seq_lens, block_table, free_pages, free_count, cu_seqlens,
+                                                              new_seq_lens, new_free_count, dev_error_count}))
+    return fail(RA_ERR_ALIGNMENT, "index must be 8-byte aligned, the other tensors 4-byte");
+  if (validate_only()) return ok();
+  ra::PagingLaunch L = paging_launch(p);
+  L.counts = new_tokens;
+  L.seq_lens = seq_lens;
+  L.table = block_table;
+  L.free_pages = const_cast<int32_t*>(free_pages);  // only read
+  L.free_count = free_count;
+  L.index = index;
+  L.cu = cu_seqlens;
+  L.new_lens = new_seq_lens;
+  L.new_free_count = new_free_count;
+  L.err_count = dev_error_count;
+  const cudaError_t e = ra::launch_cache_extend(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_extend launch");
+  return ok();
+}
+
+ra_status kv_cache_slots(const kv_cache_paging_params* p, const int32_t* starts, const int32_t* counts,
+                         const int32_t* block_table, int64_t* index, int32_t* cu_seqlens, int32_t* dev_error_count,
+                         void* stream) {
+  const ra_status st = check_paging(p);
+  if (st != RA_OK) return st;
+  if (!counts || !block_table || !index || !cu_seqlens)
+    return fail(RA_ERR_INVALID_ARG, "counts, block_table, index and cu_seqlens are required");
+  if ((reinterpret_cast<uintptr_t>(index) & 7u) || !aligned4({starts, counts, block_table, cu_seqlens, dev_error_count}))
+    return fail(RA_ERR_ALIGNMENT, "index must be 8-byte aligned, the other tensors 4-byte");
+  if (validate_only()) return ok();
+  ra::PagingLaunch L = paging_launch(p);
+  L.counts = counts;
+  L.starts = starts;
+  L.table = const_cast<int32_t*>(block_table);  // only read
+  L.index = index;
+  L.cu = cu_seqlens;
+  L.err_count = dev_error_count;
+  const cudaError_t e = ra::launch_cache_slots(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_slots launch");
+  return ok();
+}
+
+ra_status kv_cache_truncate(const kv_cache_paging_params* p, const int32_t* keep, const int32_t* seq_lens,
+                            const int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                            int32_t* new_seq_lens, int32_t* new_free_count, int32_t* dev_error_count, void* stream) {
+  const ra_status st = check_paging(p);
+  if (st != RA_OK) return st;
+  if (!seq_lens || !block_table || !free_pages || !free_count || !new_seq_lens || !new_free_count)
+    return fail(RA_ERR_INVALID_ARG, "every tensor but keep and dev_error_count is required");
+  if (!aligned4({keep, seq_lens, block_table, free_pages, free_count, new_seq_lens, new_free_count, dev_error_count}))
+    return fail(RA_ERR_ALIGNMENT, "the tensors must be 4-byte aligned");
+  if (validate_only()) return ok();
+  ra::PagingLaunch L = paging_launch(p);
+  L.counts = keep;
+  L.seq_lens = seq_lens;
+  L.table = const_cast<int32_t*>(block_table);  // only read
+  L.free_pages = free_pages;
+  L.free_count = free_count;
+  L.new_lens = new_seq_lens;
+  L.new_free_count = new_free_count;
+  L.err_count = dev_error_count;
+  const cudaError_t e = ra::launch_cache_truncate(L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_truncate launch");
   return ok();
 }
 

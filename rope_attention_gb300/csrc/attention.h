@@ -1,4 +1,4 @@
-// Internal interface of the attention kernels (packed_attention.cu, paged_attention.cu)
+// Internal interface of the attention kernels (packed_attention.cuh, paged_rows.cuh, paged_tile.cuh)
 // and of the cache read (cache_read.cu) for the C-ABI layer.
 #pragma once
 
@@ -9,6 +9,7 @@
 namespace ra {
 
 constexpr size_t kAttnHeader = 256;  // workspace: status word + padding, ahead of the partial results
+constexpr int64_t kMostPositions = 0x7fffff00;  // of a sequence: tile coordinates stay within 31 bits
 
 struct PackedLaunch {
   const uint16_t *q, *k, *v;   // bf16 or fp16 bit patterns
@@ -19,6 +20,7 @@ struct PackedLaunch {
   int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;  // token and head strides, in elements
   int32_t nq, nkv, d;
   int32_t causal, f16;
+  int64_t window, sinks;       // keys that a query sees: the last `window` up to its own, and the first `sinks`; 0: all
   float scale;
   int32_t* status;
   uint8_t* partials;           // workspace behind the header
@@ -28,6 +30,7 @@ struct PackedLaunch {
 // Bytes of workspace (header included) of any call with these sizes.
 size_t packed_attention_workspace(const PackedLaunch& L);
 cudaError_t launch_packed_attention(const PackedLaunch& L, cudaStream_t stream, const char** why);
+cudaError_t launch_packed_window(const PackedLaunch& L, cudaStream_t stream, const char** why);  // with a window
 
 struct PagedLaunch {
   const uint16_t* q;           // [total_q, heads, Dk] bf16 or fp16 bit patterns
@@ -42,6 +45,16 @@ struct PagedLaunch {
   int32_t f16, kq, vq;         // 16-bit type; KvQuant of the two caches
   int32_t k_scalar, v_scalar;
   int32_t causal;
+  int64_t window, sinks;       // as above
+  // Two calls make one over a shared prefix.  The first, over the prefix, takes the tokens of all
+  // sequences for one's (cu_step: cu_q[0] .. cu_q[cu_step]) and leaves its rows in fp32 (rows_out)
+  // with their statistics; the second joins its own with those (prior).
+  int32_t cu_step;             // entries of cu_q to a sequence's end: 1 but in the first call
+  float* rows_out;             // [total_q, heads, Dv], or null
+  float2* stats_out;           // [total_q, heads]: (log2 of the sum, the lse's share of the key offsets)
+  const float* prior;
+  const float2* prior_stats;
+  int32_t shifts;              // the second call writes the lse: that share is wanted
   float scale;
   int64_t max_seq_len;
   int32_t* status;
@@ -52,11 +65,14 @@ struct PagedLaunch {
 // Bytes of workspace (header included) of any call with these sizes.
 size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
-// The kernel for many rows per sequence and kv head (paged_tile.cu): whether it takes the
+// with a window, rows_out or prior
+cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
+// The kernel for many rows per sequence and kv head (paged_tile.cuh): whether it takes the
 // call, its part of the workspace, and the launch.
 bool paged_tile_serves(const PagedLaunch& L);
 size_t paged_tile_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why);
+cudaError_t launch_paged_tile_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
 struct ReadLaunch {
   const int64_t* index;

@@ -14,6 +14,7 @@
 
 #include <algorithm>
 
+#include "attention.h"
 #include "attn_ptx.cuh"
 #include "internal.h"
 
@@ -35,6 +36,68 @@ struct Ring {
   }
 };
 
+// What a query sees of the keys up to its own position: the last `window` of them and the first
+// `sinks`.  Key tiles that no row of a row tile sees are left out of the line: its tiles are the
+// sink tiles, then those from the first row's window on (`skip` tiles further).
+struct Window {
+  int32_t window, sinks;                    // window 0: every key
+  int32_t tiles;                            // tiles that the sinks take
+  int32_t most;                             // tiles that a row tile's rows can see
+};
+// the first position of the window that ends at `pos` (negative: there is none)
+__device__ __forceinline__ int32_t window_from(const Window& w, int32_t pos) {
+  return w.window > 0 && pos >= w.window ? pos - w.window + 1 : 0;
+}
+// For rows of `tokens` tokens and key tiles of `keys`: seen positions from window_from(first) to the
+// last token's are window + tokens - 1 at most, anywhere in their first tile.
+inline Window make_window(int64_t window, int64_t sinks, int64_t tokens, int64_t keys) {
+  Window w{};
+  if (window <= 0) {
+    w.most = 0x7fffffff;
+    return w;
+  }
+  w.window = static_cast<int32_t>(std::min<int64_t>(window, kMostPositions));
+  w.sinks = static_cast<int32_t>(std::min<int64_t>(sinks, kMostPositions));
+  w.tiles = static_cast<int32_t>((w.sinks + keys - 1) / keys);
+  w.most = static_cast<int32_t>(std::min<int64_t>(0x7fffffff, w.tiles + (w.window + tokens + 2 * keys - 3) / keys));
+  return w;
+}
+
+// Rows that another call's rows join (attention.h, PagedLaunch): its results in fp32, with log2 of
+// their sums of exponentials and the lse's share of the key offsets.
+struct Prior {
+  float* rows_out;
+  float2* stats_out;
+  const float* rows;
+  const float2* stats;
+};
+// Shares of a row's two results, in x (its own) and y (the prior's), and log2 of the sum of both.
+// A side that saw nothing has -inf; a NaN on either side makes the row NaN.
+__device__ __forceinline__ float prior_shares(float own, float prior, float2& share) {
+  if (own == neg_inf() && prior == neg_inf()) {
+    share = make_float2(0.f, 0.f);
+    return own;
+  }
+  const float m = fmaxf(own, prior);
+  const float a = ex2(own - m), b = ex2(prior - m), sum = a + b;
+  share = make_float2(a / sum, b / sum);
+  return m + log2f(sum);
+}
+
+// The end of row `at`: m (log2) and l its statistics, k0 the lse's share of the key offsets (0 where
+// l is).  They go out, or the prior's are weighed with them.
+__device__ __forceinline__ void prior_end(const Prior& p, int64_t at, float m, float l, float k0, bool writes, float* lse,
+                                          float2& share) {
+  const float own = l != 0.f ? m + log2f(l) : neg_inf();
+  if (p.stats_out) {
+    if (writes) p.stats_out[at] = make_float2(own, k0);
+    return;
+  }
+  const float2 o = p.stats[at];
+  const float sum = prior_shares(own, o.x, share);
+  if (writes && lse) lse[at] = sum != neg_inf() ? sum * 0.6931471805599453f + (l != 0.f ? k0 : o.y) : neg_inf();
+}
+
 // A part of block c is its first piece (slot 2 c) where the item began before the block's
 // run, else its last (2 c + 1).
 struct JoinParams {
@@ -49,6 +112,7 @@ struct JoinParams {
   int32_t heads, hb, tb;        // a subtile: tb tokens x hb heads
   int32_t Dv, NR, sub;          // rows of a part, rows of a subtile (NR or NR / 2)
   int32_t per_head, v_scalar;   // the value's quantisation: [N, Dv], or [Dv] ([1])
+  Prior prior;
 };
 
 template <bool F16>
@@ -80,9 +144,10 @@ __device__ __forceinline__ JoinRow join_row(const JoinParams& p, int32_t rows0, 
   const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(in) / static_cast<uint32_t>(p.hb));
   return JoinRow{r < rows0 ? r : p.sub + in, tok0 + (r < rows0 ? 0 : p.tb) + t, head0 + in - t * p.hb};
 }
-template <bool F16>
+// share: of the row's own result and of the prior's (EXT)
+template <bool F16, bool EXT>
 __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& row, int32_t kv_head, int32_t ch, float4 acc,
-                                           float l) {
+                                           float l, float2 share) {
   const float inv = l != 0.f ? rcp(l) : 0.f;
   float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   if (p.v_scale) {
@@ -92,16 +157,45 @@ __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& r
       y[e] = l != 0.f ? (y[e] - so.y) * rcp(so.x) : 0.f;
     }
   }
+  if constexpr (EXT) {
+    const int64_t at = (row.token * p.heads + row.head) * p.Dv + ch;
+    if (p.prior.rows_out) {
+      *reinterpret_cast<float4*>(p.prior.rows_out + at) = make_float4(y[0], y[1], y[2], y[3]);
+      return;
+    }
+    if (p.prior.rows) {
+      const float4 o = *reinterpret_cast<const float4*>(p.prior.rows + at);
+      y[0] = fmaf(y[0], share.x, o.x * share.y);
+      y[1] = fmaf(y[1], share.x, o.y * share.y);
+      y[2] = fmaf(y[2], share.x, o.z * share.y);
+      y[3] = fmaf(y[3], share.x, o.w * share.y);
+    }
+  }
   *reinterpret_cast<uint2*>(p.out + row.token * p.o_ts + row.head * p.o_hs + ch) =
       make_uint2(pack_half2<!F16>(y[0], y[1]), pack_half2<!F16>(y[2], y[3]));
 }
 __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row, float m, float l, float k0) {
   p.lse[row.token * p.heads + row.head] = l != 0.f ? m * 0.6931471805599453f + logf(l) + k0 : neg_inf();
 }
+// The end of a row's statistics: m and k0 as in the parts, l their sum.  EXT: what joins it is
+// looked up and weighed (share); `writes` in the thread that writes them.
+template <bool EXT>
+__device__ __forceinline__ float2 join_row_end(const JoinParams& p, const JoinRow& row, float m, float l, float k0, bool writes) {
+  float2 share = make_float2(1.f, 0.f);
+  if constexpr (EXT) {
+    if (p.prior.stats_out || p.prior.stats) {
+      prior_end(p.prior, row.token * p.heads + row.head, m, l, l != 0.f ? k0 : 0.f, writes, p.lse, share);
+      return share;
+    }
+  }
+  if (writes && p.lse) join_lse(p, row, m, l, k0);
+  return share;
+}
 
 // RESIDENT blocks an SM: four for few pieces (64 registers), two for many, whose statistics the
 // block holds in registers.
-template <bool F16, int RESIDENT>
+// EXT: the rows go to another call, or join another's (Prior).
+template <bool F16, int RESIDENT, bool EXT>
 __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t search) {
   __shared__ float4 sum[kJoinWarps][32];
   grid_dependency_wait();                   // launched while the main kernel's last blocks still run
@@ -149,7 +243,7 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
       float l = st.y * wt;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (piece == 0 && mine < rows && unit % slices == 0 && p.lse) join_lse(p, row, m, l, k0);
+      const float2 share = join_row_end<EXT>(p, row, m, l, k0, piece == 0 && mine < rows && unit % slices == 0);
       float4 acc[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -179,7 +273,12 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
         JoinRow rt;
         rt.token = __shfl_sync(0xffffffffu, row.token, 8 * t);
         rt.head = __shfl_sync(0xffffffffu, row.head, 8 * t);
-        if (r0 + t < rows && ch < p.Dv) join_store<F16>(p, rt, kv_head, ch, acc[t], lt);
+        float2 st = share;
+        if constexpr (EXT) {
+          st.x = __shfl_sync(0xffffffffu, share.x, 8 * t);
+          st.y = __shfl_sync(0xffffffffu, share.y, 8 * t);
+        }
+        if (r0 + t < rows && ch < p.Dv) join_store<F16, EXT>(p, rt, kv_head, ch, acc[t], lt, st);
       }
     }
     return;
@@ -242,8 +341,8 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
         const float4 v = sum[i][lane];
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
       }
-      if (lane == 0 && ch < 128 && p.lse) join_lse(p, row, m, l, k0);
-      if (ch < p.Dv) join_store<F16>(p, row, kv_head, ch, acc, l);
+      const float2 share = join_row_end<EXT>(p, row, m, l, k0, lane == 0 && ch < 128);
+      if (ch < p.Dv) join_store<F16, EXT>(p, row, kv_head, ch, acc, l, share);
     }
     __syncthreads();
   }
@@ -251,7 +350,8 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
 
 // The join behind a main kernel of `blocks` blocks over at most `items` items; it is put in
 // place while that kernel still runs (programmatic stream serialisation).
-inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
+template <bool EXT = false>
+cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
   const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), slices = (p.Dv + 127) / 128;
   // (MLA decode, 8 items over 152 blocks: 59 us with the search, 74 with 144 empty blocks a row;
@@ -273,10 +373,10 @@ inline cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (search)
-    return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 2>, p, blocks)
-               : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 2>, p, blocks);
-  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 4>, p, 0)
-             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 4>, p, 0);
+    return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 2, EXT>, p, blocks)
+               : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 2, EXT>, p, blocks);
+  return f16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, 4, EXT>, p, 0)
+             : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, 4, EXT>, p, 0);
 }
 
 // Parts leave the tile kernel as 32-byte stores, and a workspace may start on any 16 bytes: a join

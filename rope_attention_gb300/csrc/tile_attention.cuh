@@ -1,6 +1,6 @@
 // The attention kernel for many query rows: two 128-row tiles of queries against a stream
-// of key tiles, for packed prompts (packed_attention.cu) and for chunks of new tokens over
-// paged caches (paged_tile.cu).
+// of key tiles, for packed prompts (packed_attention.cuh) and for chunks of new tokens over
+// paged caches (paged_tile.cuh).
 //
 // A work item is two row tiles of one head (packed) or of one kv head's group of heads
 // (paged: a row is a (token, head) pair), against the keys of one sequence.  The key tiles
@@ -21,7 +21,7 @@
 // The running maximum follows only when a tile exceeds it by 2^kLazy (the factor cancels
 // between the weighted sum and the sum of weights), so O is rescaled in the first few tiles
 // of a piece and hardly ever after.  Quantised keys and values enter the products as codes,
-// as in paged_attention.cu.  Every wait on an mbarrier is bounded in time (status word); the
+// as in paged_rows.cuh.  Every wait on an mbarrier is bounded in time (status word); the
 // groups of softmax warps that meet at other barriers leave a piece, and the loop, together.
 #pragma once
 
@@ -81,6 +81,9 @@ struct TileParams {
   float scale, sl2;                         // softmax scale, and with log2(e)
   uint64_t wait_ns;
   int32_t stall_loads;
+  // EXT
+  Window window;
+  int32_t cu_step, shifts;
 };
 
 // KS, VS: 64-channel slabs of a key and a value; KT: keys per tile; QUANT: both caches hold
@@ -105,13 +108,13 @@ struct TileShape {
   static_assert(kNk >= 1 && kNv >= 1, "shared memory budget");
 };
 __device__ __forceinline__ void tile_span(const int32_t* cu, int32_t b, int32_t B, int32_t total, int32_t& start,
-                                          int32_t& len) {
+                                          int32_t& len, int32_t step = 1) {
   if (cu == nullptr) {
     len = total / B;
     start = b * len;
     return;
   }
-  const int32_t lo = min(max(__ldg(cu + b), 0), total), hi = min(max(__ldg(cu + b + 1), lo), total);
+  const int32_t lo = min(max(__ldg(cu + b), 0), total), hi = min(max(__ldg(cu + b + step), lo), total);
   start = lo;
   len = hi - lo;
 }
@@ -144,8 +147,12 @@ struct TilePiece {
   int32_t t0, take, T;                      // tiles [t0, t0 + take) of the item's T in the line
   int32_t ta, tb[2];                        // those that a row of either tile sees: [ta, tb[i])
   int32_t from, to;                         // blocks that share the item, where the block before began it
+  int32_t skip, win;                        // EXT: positions that tiles behind the sinks' lie further; the first row's window
   __device__ __forceinline__ bool whole() const { return take == T; }
   __device__ __forceinline__ int32_t n(int i) const { return max(0, tb[i] - ta); }
+  // the first position of tile t
+  template <int KT, bool EXT>
+  __device__ __forceinline__ int32_t pos(const Window& w, int32_t t) const { return t * KT + (EXT && t >= w.tiles ? skip : 0); }
 };
 
 struct TileMisc {
@@ -170,11 +177,11 @@ __device__ __forceinline__ int64_t tile_quotient(int64_t a, int64_t b) {
 }
 
 // The spans of 32 sequences, one to a lane: a walk over them waits for memory once.
-template <int KT, bool PAGED>
+template <int KT, bool PAGED, bool EXT>
 struct TileSpans {
   int32_t base, q_start, Lq, k_start, Lk;
   __device__ void one(const TileParams& p, int32_t b) {
-    tile_span(p.cu_q, b, p.B, p.total_q, q_start, Lq);
+    tile_span(p.cu_q, b, p.B, p.total_q, q_start, Lq, EXT ? p.cu_step : 1);
     if (PAGED) {
       k_start = 0;
       Lk = static_cast<int32_t>(min(static_cast<int64_t>(max(__ldg(p.cu_k + b), 0)), p.cap));
@@ -193,6 +200,7 @@ struct TileSpans {
     TileCount c;
     c.blocks = static_cast<int32_t>((static_cast<uint32_t>(Lq) + tokens - 1) / static_cast<uint32_t>(tokens));
     c.most = max(1, (Lk + KT - 1) / KT);
+    if (EXT) c.most = min(c.most, p.window.most);
     c.step = p.causal && !PAGED ? 2 * kTileRows / KT : 0;
     c.q0 = Lk >= Lq ? (Lk - Lq + KT - 1) / KT : -((Lq - Lk) / KT);
     return c;
@@ -206,14 +214,14 @@ struct TileSpans {
 };
 
 // Walks a block's pieces, a whole warp at once.
-template <int KT, bool PAGED>
+template <int KT, bool PAGED, bool EXT>
 struct TileWalk {
   int32_t b, item, blk, t;                  // next: sequence, head, row block, key tile
   int64_t rem;
   TilePiece w;                              // of the sequence that c is of: its spans
   TileCount c;
   int32_t runs;                             // TileRuns
-  TileSpans<KT, PAGED> spans;
+  TileSpans<KT, PAGED, EXT> spans;
 
   __device__ TileCount count(const TileParams& p, int32_t b, TilePiece& w) {
     if (b >= spans.base + 32) spans.load(p, b);
@@ -221,7 +229,7 @@ struct TileWalk {
     w.Lq = __shfl_sync(0xffffffffu, spans.Lq, b - spans.base);
     w.k_start = __shfl_sync(0xffffffffu, spans.k_start, b - spans.base);
     w.Lk = __shfl_sync(0xffffffffu, spans.Lk, b - spans.base);
-    return TileSpans<KT, PAGED>::count(p, w.Lq, w.Lk);
+    return TileSpans<KT, PAGED, EXT>::count(p, w.Lq, w.Lk);
   }
   // to offset `off` of sequence b, for `run` tiles
   __device__ void seek(const TileParams& p, int32_t seq, int64_t off, int64_t run, int32_t kind) {
@@ -307,12 +315,19 @@ struct TileWalk {
     w.kv_head = PAGED ? item : static_cast<int32_t>(static_cast<uint32_t>(item) / static_cast<uint32_t>(p.g));
     w.head = PAGED ? item * p.g : item;
     w.tok = blk * 2 * p.join.tb;
+    int32_t skip = 0;
+    w.skip = w.win = 0;
+    if constexpr (EXT) {
+      w.win = window_from(p.window, w.tok + w.Lk - w.Lq);
+      skip = max(0, w.win / KT - p.window.tiles);
+      w.skip = skip * KT;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int32_t first = w.tok + i * p.join.tb, tokens = max(0, min(p.join.tb, w.Lq - first));
       const int32_t seen = p.causal ? min(w.Lk, max(0, first + tokens + w.Lk - w.Lq)) : w.Lk;
       w.rows[i] = tokens * p.join.hb;
-      w.tb[i] = tokens == 0 ? 0 : min(w.t0 + w.take - kTileExtra, (seen + KT - 1) / KT);
+      w.tb[i] = tokens == 0 ? 0 : min(w.t0 + w.take - kTileExtra, (seen + KT - 1) / KT - skip);
     }
     w.ta = max(0, w.t0 - kTileExtra);
     if (runs != kRunsStrided) rem -= w.take;
@@ -357,7 +372,8 @@ __device__ __forceinline__ float tile_half(uint32_t u) {
 }
 
 // F16: q and out (and 16-bit caches) are fp16; P16: P and the value operand are
-template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED>
+// EXT: windows; rows that leave in fp32 for another call, or join another's (Prior)
+template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED, bool EXT>
 __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(const __grid_constant__ TileParams p) {
   using SH = TileShape<KS, VS, KT, QUANT>;
   constexpr bool P16 = F16 || QUANT;
@@ -374,7 +390,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   TileMisc& ms = *reinterpret_cast<TileMisc*>(smem + SH::kOffMisc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  using Walk = TileWalk<KT, PAGED>;
+  using Walk = TileWalk<KT, PAGED, EXT>;
 
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&ms.tmem), 512);
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       const int32_t chunk = (p.B + SH::kThreads - 1) / SH::kThreads;
       b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
       b_hi = min(p.B, b_lo + chunk);
-      TileSpans<KT, PAGED> one;
+      TileSpans<KT, PAGED, EXT> one;
       for (int32_t b = b_lo; b < b_hi; ++b) {
         one.one(p, b);
         mine += one.work(p, &items);
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       }
     } else {
       if (here) {
-        TileSpans<KT, PAGED> one;
+        TileSpans<KT, PAGED, EXT> one;
         int32_t b = b_lo;
         int64_t off = start - before, unused = 0;
         for (; b < b_hi; ++b) {
@@ -557,9 +573,14 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           if (PAGED) {
             if (t * groups >= base + per_trip) {
               base += per_trip;
-              const int32_t pos = (base + lane) << p.box_shift;
+              int32_t pos = (base + lane) << p.box_shift;
+              bool hidden = false;          // a group that no row sees: its page may be gone
+              if constexpr (EXT) {
+                if (base + lane >= p.window.tiles * groups) pos += w.skip;
+                hidden = pos + p.box_rows <= w.win && pos >= p.window.sinks;
+              }
               row = -1;
-              if (lane < per_trip && base + lane < t_end * groups && pos < w.Lk) {
+              if (lane < per_trip && base + lane < t_end * groups && pos < w.Lk && !hidden) {
                 if (p.mode == kModeNorm) {
                   row = (static_cast<int64_t>(w.b) * p.items + w.kv_head) * p.cache_seq + pos;
                 } else {
@@ -576,6 +597,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             have = (__ballot_sync(0xffffffffu, row >= 0) >> (t * groups - base)) & ((1u << groups) - 1);
           }
           const uint32_t live = __popc(have);
+          const int32_t pos0 = w.template pos<KT, EXT>(p.window, t);
           const int32_t y = PAGED ? (p.mode == kModePa ? w.kv_head : 0) : w.kv_head;
           // 0: the key tile, 1: the value tile
 #pragma unroll
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             if (side == 0 && PAGED) {
               uint64_t lo = 0, hi = 0;      // which of the tile's keys exist
               for (int g = 0; g < groups; ++g) {
-                const int32_t at = g << p.box_shift, keys = min(p.box_rows, w.Lk - (t * KT + at));
+                const int32_t at = g << p.box_shift, keys = min(p.box_rows, w.Lk - (pos0 + at));
                 if (!((have >> g) & 1)) continue;
                 const uint64_t bits = keys >= 64 ? ~0ull : (1ull << keys) - 1;
                 if (at < 64) lo |= bits << at;
@@ -628,7 +650,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               if (lane == 0) {
                 ms.valid[u % kTileValid][0] = lo;
                 ms.valid[u % kTileValid][1] = hi;
-                ms.holes[u % kTileValid] = live != min(groups, (w.Lk - t * KT + p.box_rows - 1) >> p.box_shift);
+                ms.holes[u % kTileValid] = live != min(groups, (w.Lk - pos0 + p.box_rows - 1) >> p.box_shift);
               }
               __syncwarp();
             }
@@ -647,7 +669,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               }
             } else {
               if (elect_one()) {
-                const int32_t z = w.k_start + t * KT, swap = side ? p.v_swap : p.k_swap;
+                const int32_t z = w.k_start + pos0, swap = side ? p.v_swap : p.k_swap;
                 mbar_arrive_expect_tx(bar, side ? SH::kV : SH::kK);
 #pragma unroll
                 for (int c = 0; c < slabs; ++c) tma_load_3d(dst + c * SH::kSlab, map, bar, 64 * c, swap ? z : y, swap ? y : z);
@@ -822,6 +844,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       const int32_t in_tile = static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.join.hb));
       const int32_t tok = w.tok + i * p.join.tb + in_tile, head = w.head + row - in_tile * p.join.hb;
       const int32_t seen = !p.causal ? w.Lk : min(w.Lk, max(0, tok + 1 + w.Lk - w.Lq));
+      const int32_t from = EXT ? window_from(p.window, tok + w.Lk - w.Lq) : 0;  // of the row's window
       if (w.first && threadIdx.x == 0 && w.t0 > 0) {
         // the block behind the first cut through an item joins the item's pieces
         int32_t* mt = p.join.meta + 8 * blockIdx.x;
@@ -870,7 +893,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         const int k = max(-100, min(100, -(scale_exponent(tile_half<F16>(big)) + scale_exponent(top) + 15)));
         const float up = exp2_int(k);
         sl2 = p.sl2 * exp2_int(-k);
-        if (p.join.lse && p.k_offset) {
+        if ((EXT ? p.shifts != 0 : p.join.lse != nullptr) && p.k_offset) {
           const float* ko = p.k_offset + static_cast<int64_t>(w.kv_head) * p.Dk;
 #pragma unroll 1
           for (int c = 0; c < nck; ++c) {
@@ -906,21 +929,29 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         s_par ^= 1u;
         tc_fence_after();
-        const int32_t t = w.ta + j;
+        const int32_t pos0 = w.template pos<KT, EXT>(p.window, w.ta + j);
         uint32_t s[KT];
 #pragma unroll
         for (int c = 0; c < KT; c += 32) tmem_ld_x32(s_addr + c, s + c);
         tmem_ld_wait();
-        const int32_t nv = seen - t * KT;  // keys of this tile that the row sees
+        const int32_t nv = seen - pos0;  // keys of this tile that the row sees
         if (__any_sync(0xffffffffu, nv < KT)) {
 #pragma unroll
           for (int c = 0; c < KT; ++c)
             if (c >= nv) s[c] = __float_as_uint(neg_inf());
         }
+        if constexpr (EXT) {
+          const int32_t lo = max(p.window.sinks - pos0, 0), hi = from - pos0;  // [lo, hi) lie before the row's window
+          if (__any_sync(0xffffffffu, hi > lo && lo < KT)) {
+#pragma unroll
+            for (int c = 0; c < KT; ++c)
+              if (c >= lo && c < hi) s[c] = __float_as_uint(neg_inf());
+          }
+        }
         const bool holes = PAGED && ms.holes[(u + j) % kTileValid] != 0;
         uint64_t gap[2] = {0, 0};           // keys before the end that do not exist (bad pages)
         if (holes) {
-          const int32_t end = w.Lk - t * KT;
+          const int32_t end = w.Lk - pos0;
           const uint64_t* v = ms.valid[(u + j) % kTileValid];
           gap[0] = ~v[0] & (end >= 64 ? ~0ull : (1ull << end) - 1);
           if (KT > 64) {
@@ -969,10 +1000,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l += sum.x + sum.y;
-        if (!QUANT && ((t + 1) * KT > w.Lk || holes)) {
+        if (!QUANT && (pos0 + KT > w.Lk || holes)) {
           // value rows that are no key's meet P = 0, but 0 times a stray NaN or infinity is
           // NaN: zero them in shared memory
-          const int32_t end = w.Lk - t * KT;
+          const int32_t end = w.Lk - pos0;
           if (!bounded_wait_warp(smem_u32(&ms.v_full[vr.stage]), vr.parity, p.wait_ns, abort_flag)) {
             tmem_st_wait();                 // of P: tensor memory is freed only behind its stores
             ok = false;
@@ -1006,8 +1037,12 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 
       // ---- final rows, or the piece's statistics and accumulator
       const float inv = l != 0.f ? rcp(l) : 0.f;  // a row that sees nothing is 0; a NaN stays one
+      float2 share = make_float2(1.f, 0.f);
+      const int64_t at = EXT ? token * p.join.heads + head : 0;
       if (live) {
-        if (whole) {
+        if (EXT && whole && (p.join.prior.stats_out || p.join.prior.stats)) {
+          prior_end(p.join.prior, at, fmaf(m, sl2, -kLift), l, l != 0.f ? shift : 0.f, true, p.join.lse, share);
+        } else if (whole) {
           if (p.join.lse)
             p.join.lse[token * p.join.heads + head] = l != 0.f ? fmaf(m, sl2, -kLift) * 0.6931471805599453f + logf(l) + shift : neg_inf();
         } else {
@@ -1038,6 +1073,28 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = (y[e] - (vo ? __ldg(vo + e) : 0.f)) * rcp(__ldg(vs + e));
         }
+        if constexpr (EXT) {
+          if (p.join.prior.rows_out) {
+            float* const to = p.join.prior.rows_out + at * p.join.Dv + c;
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(y[e]);
+            store_32(to, u);
+            store_32(to + 8, u + 8);
+            continue;
+          }
+          if (p.join.prior.rows) {
+            const float4* o4 = reinterpret_cast<const float4*>(p.join.prior.rows + at * p.join.Dv + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 x = o4[e];
+              y[4 * e] = fmaf(y[4 * e], share.x, x.x * share.y);
+              y[4 * e + 1] = fmaf(y[4 * e + 1], share.x, x.y * share.y);
+              y[4 * e + 2] = fmaf(y[4 * e + 2], share.x, x.z * share.y);
+              y[4 * e + 3] = fmaf(y[4 * e + 3], share.x, x.w * share.y);
+            }
+          }
+        }
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = pack_half2<!F16>(y[2 * e], y[2 * e + 1]);
@@ -1058,7 +1115,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED>
+template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED, bool EXT = false>
 cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cuts, cudaStream_t stream) {
   using SH = TileShape<KS, VS, KT, QUANT>;
   constexpr int smem = SH::kOffMisc + static_cast<int>(sizeof(TileMisc));
@@ -1067,7 +1124,7 @@ cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cut
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto kernel = tile_attention_kernel<KS, VS, KT, F16, QUANT, PAGED>;
+  auto kernel = tile_attention_kernel<KS, VS, KT, F16, QUANT, PAGED, EXT>;
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1076,7 +1133,7 @@ cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cut
   kernel<<<blocks, SH::kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return cuts ? launch_join(p.join, F16, blocks, items, stream) : cudaSuccess;
+  return cuts ? launch_join<EXT>(p.join, F16, blocks, items, stream) : cudaSuccess;
 }
 
 // Whether the runs of `blocks` blocks cut items that all count for T key tiles (the kernel's own

@@ -1,4 +1,4 @@
-// packed_attention, paged_attention and kv_cache_read called with torch tensors: the checks of
+// The attention calls, kv_cache_read and the paging calls with torch tensors: the checks of
 // the binding's other calls (placement, dtype, contiguity, size) and the C call behind them.
 //
 // One decode step's attention runs for about 10 us on the device; the same checks written with
@@ -243,11 +243,17 @@ PyObject* packed_params(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return nullptr;
 }
 
-// (params, q, k, v, out, workspace, lse, cu_seqlens_q, cu_seqlens_k, stream)
+// (params, [window,] q, k, v, out, workspace, lse, cu_seqlens_q, cu_seqlens_k, stream)
+template <bool WINDOW>
 PyObject* packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_ok(n, 10)) return nullptr;
+  if (!count_ok(n, WINDOW ? 11 : 10)) return nullptr;
   return guarded([&] {
     const auto p = params_of<packed_attention_params>(a[0], "PackedAttentionParams");
+    attention_window window{};
+    if (WINDOW) {
+      window = params_of<attention_window>(a[1], "AttentionWindow");
+      ++a;                      // the tensors stand as in packed_attention
+    }
     const Types half = p.dtype == RA_FP16 ? one(at::kHalf) : p.dtype == RA_BF16 ? one(at::kBFloat16) : Types{at::kBFloat16, at::kHalf, false};
     Args args;
     auto* q = static_cast<uint16_t*>(args.strided(a[1], "q", p.total_q, p.num_heads, p.head_dim, p.q_token_stride, p.q_head_stride, half));
@@ -262,19 +268,40 @@ PyObject* packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = args.stream(a[9]);
     ra_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = packed_attention(&p, q, k, v, out, lse, cq, ck, ws, room, stream);
+    st = WINDOW ? packed_window_attention(&p, &window, q, k, v, out, lse, cq, ck, ws, room, stream)
+                : packed_attention(&p, q, k, v, out, lse, cq, ck, ws, room, stream);
     Py_END_ALLOW_THREADS
     return static_cast<long>(st);
   });
 }
 
 // (cache, params, q, k_cache, ckv_cache, seq_lens, out, workspace, block_table, cu_seqlens_q,
-//  k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse, dev_error_count, stream)
-PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_ok(n, 17)) return nullptr;
+//  k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse, dev_error_count, stream);
+// with a window that comes third; with a prefix
+// (cache, params, prefix, q, k_cache, ckv_cache, prefix_len, prefix_table, seq_lens, block_table, out,
+//  workspace, cu_seqlens_q, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse, dev_error_count, stream)
+enum Paged { kPlain, kWindow, kPrefix };
+template <Paged FORM>
+PyObject* paged(PyObject*, PyObject* const* given, Py_ssize_t n) {
+  if (!count_ok(n, FORM == kPrefix ? 20 : FORM == kWindow ? 18 : 17)) return nullptr;
   return guarded([&] {
+    // the arguments in the order of paged_attention, and what a form has beside them
+    PyObject* a[17];
+    static constexpr int from_prefix[17] = {0, 1, 3, 4, 5, 8, 10, 11, 9, 12, 13, 14, 15, 16, 17, 18, 19};
+    for (int i = 0; i < 17; ++i) a[i] = given[FORM == kPrefix ? from_prefix[i] : FORM == kWindow && i > 1 ? i + 1 : i];
     const auto c = params_of<kv_rms_norm_rope_cache_params>(a[0], "KvRmsNormRopeCacheParams");
     auto p = params_of<paged_attention_params>(a[1], "PagedAttentionParams");
+    attention_window window{};
+    attention_prefix prefix{};
+    Args args;
+    const int32_t *prefix_len = nullptr, *prefix_table = nullptr;
+    if (FORM == kWindow) window = params_of<attention_window>(given[2], "AttentionWindow");
+    if (FORM == kPrefix) {
+      prefix = params_of<attention_prefix>(given[2], "AttentionPrefix");
+      if (prefix.table_entries == 0) prefix.table_entries = tensor_of(given[7], "prefix_table")->numel();
+      prefix_len = static_cast<int32_t*>(args.flat(given[6], "prefix_len", 4, one(at::kInt)));
+      prefix_table = static_cast<int32_t*>(args.flat(given[7], "prefix_table", times(prefix.table_entries, 4), one(at::kInt)));
+    }
     if (const at::Tensor* t = tensor_of(a[8], "block_table", true)) {
       if (t->dim() != 2 || t->size(0) != p.B) {
         std::string shape;
@@ -286,7 +313,6 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Types half = half_type(c.kv_dtype);
     const CacheBytes x = cache_bytes(c);
     const int64_t rows = times(p.total_q, p.num_heads);
-    Args args;
     auto* q = static_cast<uint16_t*>(args.flat(a[2], "q", times(rows, c.Dkv, 2), half));
     void* kc = args.flat(a[3], "k_cache", x.k, stored_type(c.k_cache_dtype));
     void* vc = args.flat(a[4], "ckv_cache", x.ckv, stored_type(c.ckv_cache_dtype));
@@ -305,7 +331,13 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = args.stream(a[16]);
     ra_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = paged_attention(&c, &p, q, kc, vc, lens, table, cq, ks, vs, ko, vo, out, lse, err, ws, room, stream);
+    if (FORM == kPrefix)
+      st = paged_prefix_attention(&c, &p, &prefix, q, kc, vc, prefix_len, prefix_table, lens, table, cq, ks, vs, ko, vo, out, lse,
+                                  err, ws, room, stream);
+    else if (FORM == kWindow)
+      st = paged_window_attention(&c, &p, &window, q, kc, vc, lens, table, cq, ks, vs, ko, vo, out, lse, err, ws, room, stream);
+    else
+      st = paged_attention(&c, &p, q, kc, vc, lens, table, cq, ks, vs, ko, vo, out, lse, err, ws, room, stream);
     Py_END_ALLOW_THREADS
     return static_cast<long>(st);
   });
@@ -341,13 +373,99 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// the tensors that the paging calls share
+struct Paging {
+  kv_cache_paging_params p;
+  Args args;
+  explicit Paging(PyObject* params) : p(params_of<kv_cache_paging_params>(params, "KvCachePagingParams")) {}
+  int32_t* ints(PyObject* o, const char* name, int64_t n, bool optional = false) {
+    return static_cast<int32_t*>(args.flat(o, name, times(n, 4), one(at::kInt), optional));
+  }
+  int32_t* table(PyObject* o) { return ints(o, "block_table", times(p.B, p.block_table_stride)); }
+  int64_t* index(PyObject* o) { return static_cast<int64_t*>(args.flat(o, "index", times(p.max_tokens, 8), one(at::kLong))); }
+};
+
+// (params, new_tokens, seq_lens, block_table, free_pages, free_count, index, cu_seqlens, new_seq_lens,
+//  new_free_count, dev_error_count, stream)
+PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 12)) return nullptr;
+  return guarded([&] {
+    Paging x(a[0]);
+    auto* add = x.ints(a[1], "new_tokens", x.p.B);
+    auto* lens = x.ints(a[2], "seq_lens", x.p.B);
+    auto* table = x.table(a[3]);
+    auto* pages = x.ints(a[4], "free_pages", x.p.block_num);
+    auto* count = x.ints(a[5], "free_count", 1);
+    auto* index = x.index(a[6]);
+    auto* cu = x.ints(a[7], "cu_seqlens", x.p.B + 1);
+    auto* new_lens = x.ints(a[8], "new_seq_lens", x.p.B);
+    auto* new_count = x.ints(a[9], "new_free_count", 1);
+    auto* err = x.ints(a[10], "dev_error_count", 1, true);
+    void* stream = x.args.stream(a[11]);
+    ra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kv_cache_extend(&x.p, add, lens, table, pages, count, index, cu, new_lens, new_count, err, stream);
+    Py_END_ALLOW_THREADS
+    return static_cast<long>(st);
+  });
+}
+
+// (params, counts, block_table, index, cu_seqlens, starts, dev_error_count, stream)
+PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 8)) return nullptr;
+  return guarded([&] {
+    Paging x(a[0]);
+    auto* counts = x.ints(a[1], "counts", x.p.B);
+    auto* table = x.table(a[2]);
+    auto* index = x.index(a[3]);
+    auto* cu = x.ints(a[4], "cu_seqlens", x.p.B + 1);
+    auto* starts = x.ints(a[5], "starts", x.p.B, true);
+    auto* err = x.ints(a[6], "dev_error_count", 1, true);
+    void* stream = x.args.stream(a[7]);
+    ra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kv_cache_slots(&x.p, starts, counts, table, index, cu, err, stream);
+    Py_END_ALLOW_THREADS
+    return static_cast<long>(st);
+  });
+}
+
+// (params, seq_lens, block_table, free_pages, free_count, new_seq_lens, new_free_count, keep,
+//  dev_error_count, stream)
+PyObject* truncate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 10)) return nullptr;
+  return guarded([&] {
+    Paging x(a[0]);
+    auto* lens = x.ints(a[1], "seq_lens", x.p.B);
+    auto* table = x.table(a[2]);
+    auto* pages = x.ints(a[3], "free_pages", x.p.block_num);
+    auto* count = x.ints(a[4], "free_count", 1);
+    auto* new_lens = x.ints(a[5], "new_seq_lens", x.p.B);
+    auto* new_count = x.ints(a[6], "new_free_count", 1);
+    auto* keep = x.ints(a[7], "keep", x.p.B, true);
+    auto* err = x.ints(a[8], "dev_error_count", 1, true);
+    void* stream = x.args.stream(a[9]);
+    ra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = kv_cache_truncate(&x.p, keep, lens, table, pages, count, new_lens, new_count, err, stream);
+    Py_END_ALLOW_THREADS
+    return static_cast<long>(st);
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyCFunction fast() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F));
 }
 PyMethodDef methods[] = {{"packed_params", fast<packed_params>(), METH_FASTCALL, nullptr},
-                         {"packed_attention", fast<packed>(), METH_FASTCALL, nullptr},
-                         {"paged_attention", fast<paged>(), METH_FASTCALL, nullptr},
+                         {"packed_attention", fast<packed<false>>(), METH_FASTCALL, nullptr},
+                         {"packed_window_attention", fast<packed<true>>(), METH_FASTCALL, nullptr},
+                         {"paged_attention", fast<paged<kPlain>>(), METH_FASTCALL, nullptr},
+                         {"paged_window_attention", fast<paged<kWindow>>(), METH_FASTCALL, nullptr},
+                         {"paged_prefix_attention", fast<paged<kPrefix>>(), METH_FASTCALL, nullptr},
+                         {"kv_cache_extend", fast<extend>(), METH_FASTCALL, nullptr},
+                         {"kv_cache_slots", fast<slots>(), METH_FASTCALL, nullptr},
+                         {"kv_cache_truncate", fast<truncate>(), METH_FASTCALL, nullptr},
                          {"kv_cache_read", fast<read>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -40,7 +40,9 @@ EXPORTS = ["ra_last_error", "ra_abi_version", "ra_set_wait_timeout_ns", "ra_test
            "ra_test_stall_next_kv_cache", "ra_test_stall_next_norm_rope", "row_quantize_e4m3",
            "row_quantize_e4m3_packed", "ra_test_validate_only", "packed_attention_workspace_bytes",
            "packed_attention", "paged_attention_workspace_bytes", "paged_attention", "attention_status",
-           "ra_test_stall_next_attention", "kv_cache_read"]
+           "ra_test_stall_next_attention", "kv_cache_read", "packed_window_attention", "paged_window_attention",
+           "paged_prefix_attention_workspace_bytes", "paged_prefix_attention", "kv_cache_extend", "kv_cache_slots",
+           "kv_cache_truncate"]
 
 
 class RAError(RuntimeError):
@@ -86,6 +88,19 @@ class PagedAttentionParams(ctypes.Structure):
                 ("max_seq_len", ctypes.c_int64), ("block_table_stride", ctypes.c_int64)]
 
 
+class AttentionWindow(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int64), ("sinks", ctypes.c_int64)]
+
+
+class AttentionPrefix(ctypes.Structure):
+    _fields_ = [("max_prefix_len", ctypes.c_int64), ("table_entries", ctypes.c_int64)]
+
+
+class KvCachePagingParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("block_num", ctypes.c_int64), ("block_size", ctypes.c_int64),
+                ("block_table_stride", ctypes.c_int64), ("max_tokens", ctypes.c_int64)]
+
+
 _LIB = None
 P = ctypes.c_void_p
 
@@ -128,6 +143,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "paged_attention": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), ctypes.POINTER(PagedAttentionParams),
                                   P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
         "attention_status": (i32, [P, P, ctypes.POINTER(i32)]),
+        "packed_window_attention": (i32, [ctypes.POINTER(PackedAttentionParams), ctypes.POINTER(AttentionWindow),
+                                          P, P, P, P, P, P, P, P, sz, P]),
+        "paged_window_attention": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), ctypes.POINTER(PagedAttentionParams),
+                                         ctypes.POINTER(AttentionWindow), P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "paged_prefix_attention_workspace_bytes": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams),
+                                                         ctypes.POINTER(PagedAttentionParams),
+                                                         ctypes.POINTER(AttentionPrefix), ctypes.POINTER(sz)]),
+        "paged_prefix_attention": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), ctypes.POINTER(PagedAttentionParams),
+                                         ctypes.POINTER(AttentionPrefix), P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P,
+                                         sz, P]),
+        "kv_cache_extend": (i32, [ctypes.POINTER(KvCachePagingParams), P, P, P, P, P, P, P, P, P, P, P]),
+        "kv_cache_slots": (i32, [ctypes.POINTER(KvCachePagingParams), P, P, P, P, P, P, P]),
+        "kv_cache_truncate": (i32, [ctypes.POINTER(KvCachePagingParams), P, P, P, P, P, P, P, P, P]),
         "ra_test_stall_next_attention": (None, []),
         "kv_cache_read": (i32, [ctypes.POINTER(KvRmsNormRopeCacheParams), P, P, P, P, P, P, P, P, P, P, P]),
     }
@@ -476,6 +504,42 @@ def paged_attention(cache, params, q, k_cache, ckv_cache, seq_lens, out, workspa
                                     k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse, dev_error_count, stream))
 
 
+def packed_window_attention(params, window, q, k, v, out, workspace, lse=None, cu_seqlens_q=None, cu_seqlens_k=None,
+                            stream=None) -> None:
+    """packed_attention in a sliding window with sinks (header: packed_window_attention);
+    ``window`` is an ``AttentionWindow``, the workspace packed_attention's."""
+    _check(_calls().packed_window_attention(params, window, q, k, v, out, workspace, lse, cu_seqlens_q, cu_seqlens_k, stream))
+
+
+def paged_window_attention(cache, params, window, q, k_cache, ckv_cache, seq_lens, out, workspace, block_table=None,
+                           cu_seqlens_q=None, k_rope_scale=None, c_kv_scale=None, k_rope_offset=None,
+                           c_kv_offset=None, lse=None, dev_error_count=None, stream=None) -> None:
+    """paged_attention in a sliding window with sinks (header: paged_window_attention);
+    ``window`` is an ``AttentionWindow``, the workspace paged_attention's."""
+    _check(_calls().paged_window_attention(cache, params, window, q, k_cache, ckv_cache, seq_lens, out, workspace, block_table,
+                                           cu_seqlens_q, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, lse,
+                                           dev_error_count, stream))
+
+
+def paged_prefix_attention_workspace_bytes(cache: KvRmsNormRopeCacheParams, params: PagedAttentionParams,
+                                           prefix: AttentionPrefix) -> int:
+    n = ctypes.c_size_t()
+    _check(load().paged_prefix_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(params), ctypes.byref(prefix),
+                                                         ctypes.byref(n)))
+    return n.value
+
+
+def paged_prefix_attention(cache, params, prefix, q, k_cache, ckv_cache, prefix_len, prefix_table, seq_lens, block_table,
+                           out, workspace, cu_seqlens_q=None, k_rope_scale=None, c_kv_scale=None, k_rope_offset=None,
+                           c_kv_offset=None, lse=None, dev_error_count=None, stream=None) -> None:
+    """paged_attention of sequences behind a shared prefix (header: paged_prefix_attention).
+    ``prefix`` is an ``AttentionPrefix``, whose table_entries are taken from prefix_table
+    where they are 0; seq_lens and block_table are of the sequences' own positions."""
+    _check(_calls().paged_prefix_attention(cache, params, prefix, q, k_cache, ckv_cache, prefix_len, prefix_table, seq_lens,
+                                           block_table, out, workspace, cu_seqlens_q, k_rope_scale, c_kv_scale, k_rope_offset,
+                                           c_kv_offset, lse, dev_error_count, stream))
+
+
 def attention_status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronises the stream; returns the workspace's status word (0 = fine) and clears it."""
     v = ctypes.c_int32()
@@ -491,3 +555,25 @@ def kv_cache_read(params, index, k_cache, ckv_cache, k_out=None, c_kv_out=None, 
     """Rows of the caches of kv_rms_norm_rope_cache read back (header: kv_cache_read)."""
     _check(_calls().kv_cache_read(params, index, k_cache, ckv_cache, k_out, c_kv_out, k_rope_scale, c_kv_scale, k_rope_offset,
                                   c_kv_offset, dev_error_count, stream))
+
+
+# ---------------------------------------------------------------- paging
+def kv_cache_extend(params, new_tokens, seq_lens, block_table, free_pages, free_count, index, cu_seqlens, new_seq_lens,
+                    new_free_count, dev_error_count=None, stream=None) -> None:
+    """Pages, block table entries and slots for the requests' new tokens (header:
+    kv_cache_extend).  new_seq_lens may be seq_lens, and new_free_count free_count."""
+    _check(_calls().kv_cache_extend(params, new_tokens, seq_lens, block_table, free_pages, free_count, index, cu_seqlens,
+                                    new_seq_lens, new_free_count, dev_error_count, stream))
+
+
+def kv_cache_slots(params, counts, block_table, index, cu_seqlens, starts=None, dev_error_count=None, stream=None) -> None:
+    """The slots of spans of the requests' positions (header: kv_cache_slots)."""
+    _check(_calls().kv_cache_slots(params, counts, block_table, index, cu_seqlens, starts, dev_error_count, stream))
+
+
+def kv_cache_truncate(params, seq_lens, block_table, free_pages, free_count, new_seq_lens, new_free_count, keep=None,
+                      dev_error_count=None, stream=None) -> None:
+    """Requests cut back to ``keep`` tokens each (None: ended), their pages given back
+    (header: kv_cache_truncate)."""
+    _check(_calls().kv_cache_truncate(params, seq_lens, block_table, free_pages, free_count, new_seq_lens, new_free_count,
+                                      keep, dev_error_count, stream))
