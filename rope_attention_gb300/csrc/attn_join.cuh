@@ -113,6 +113,7 @@ struct JoinParams {
   int32_t Dv, NR, sub;          // rows of a part, rows of a subtile (NR or NR / 2)
   int32_t per_head, v_scalar;   // the value's quantisation: [N, Dv], or [Dv] ([1])
   Prior prior;
+  int32_t split;                // EXT: warps that share a row's many pieces
 };
 
 template <bool F16>
@@ -283,6 +284,83 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
     }
     return;
   }
+  if constexpr (EXT) {
+    // `split` warps to a row's 128 channels, so that few rows fill the SMs as well as many.  (8 kv
+    // heads of 256 rows in 20 pieces each: 18.4 us with eight warps to a row, 10.3 with one.)
+    __shared__ float weights[kJoinWarps][kMaxBlocks];
+    const int S = p.split, part = warp & (S - 1), group = warp / S, groups = kJoinWarps / S;
+    constexpr int kBatch = RESIDENT == 2 ? 8 : 4;
+    for (int32_t unit0 = blockIdx.y * groups; unit0 < rows * slices; unit0 += gridDim.y * groups) {
+      const int32_t unit = min(unit0 + group, rows * slices - 1);
+      const bool mine = unit0 + group < rows * slices;
+      const int32_t ch = (unit % slices) * 128 + lane * 4;
+      const JoinRow row = join_row(p, rows0, tok0, head0, unit / slices);
+      float m = neg_inf(), l = 0.f, k0 = neg_inf();
+      float2 st[kJoinLoads];
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        st[i] = make_float2(neg_inf(), 0.f);
+        if (32 * i + lane < n) {
+          const float4 x = p.stats[slot(32 * i + lane) * NR + row.part];
+          st[i] = make_float2(x.x, x.y);
+          if (x.y != 0.f) k0 = x.z;
+          m = fmaxf(m, x.x);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, k0, o));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        const float w = st[i].y != 0.f ? ex2(st[i].x - m) : 0.f;
+        if (32 * i + lane < n) weights[warp][32 * i + lane] = w;
+        l = fmaf(st[i].y, w, l);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      __syncwarp();
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int32_t i0 = part; i0 < n; i0 += kBatch * S) {
+        float4 v[kBatch];
+        float w[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int32_t i = i0 + k * S;
+          w[k] = i < n ? weights[warp][i] : 0.f;
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w[k] != 0.f && ch < p.Dv)   // a piece that saw nothing stored no accumulator
+            v[k] = *reinterpret_cast<const float4*>(p.parts + (slot(i) * NR + row.part) * p.Dv + ch);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          acc.x = fmaf(v[k].x, w[k], acc.x);
+          acc.y = fmaf(v[k].y, w[k], acc.y);
+          acc.z = fmaf(v[k].z, w[k], acc.z);
+          acc.w = fmaf(v[k].w, w[k], acc.w);
+        }
+      }
+      if (S > 1) {
+        sum[warp][lane] = acc;
+        __syncthreads();
+        if (part == 0) {
+          for (int i = 1; i < S; ++i) {
+            const float4 v = sum[warp + i][lane];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+          }
+        }
+      }
+      if (part == 0 && mine) {
+        const float2 share = join_row_end<EXT>(p, row, m, l, k0, lane == 0 && ch < 128);
+        if (ch < p.Dv) join_store<F16, EXT>(p, row, kv_head, ch, acc, l, share);
+      }
+      if (S > 1) __syncthreads();
+    }
+    return;
+  }
   for (int32_t unit = blockIdx.y; unit < rows * slices; unit += gridDim.y) {
     const int32_t ch = (unit % slices) * 128 + lane * 4;
     const JoinRow row = join_row(p, rows0, tok0, head0, unit / slices);
@@ -351,8 +429,9 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
 // The join behind a main kernel of `blocks` blocks over at most `items` items; it is put in
 // place while that kernel still runs (programmatic stream serialisation).
 template <bool EXT = false>
-cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items, cudaStream_t stream) {
+cudaError_t launch_join(const JoinParams& given, bool f16, int blocks, int64_t items, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
+  JoinParams p = given;
   const int cuts = static_cast<int>(std::min<int64_t>(blocks - 1, items)), slices = (p.Dv + 127) / 128;
   // (MLA decode, 8 items over 152 blocks: 59 us with the search, 74 with 144 empty blocks a row;
   // 151 cuts: 159 us without it, 168 with)
@@ -362,7 +441,15 @@ cudaError_t launch_join(const JoinParams& p, bool f16, int blocks, int64_t items
   // search the grid is that of joins of few pieces: one long item among many short ones, cut into
   // many, has its rows joined by the same few blocks.)
   const int units = search ? p.NR * slices : ((p.NR + 3) / 4 * slices + kJoinWarps - 1) / kJoinWarps;
-  const int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
+  int y = std::max(1, std::min(units, (4 * device_sm_count() + cuts - 1) / cuts));
+  if (EXT) {
+    // warps that fill the SMs twice over, 16 on each; and one round of blocks
+    const int64_t rows = static_cast<int64_t>(cuts) * p.NR * slices, warps = 32 * static_cast<int64_t>(device_sm_count());
+    p.split = kJoinWarps;
+    while (p.split > 1 && search && p.split * rows > warps) p.split /= 2;
+    y = search ? std::max(1, std::min(static_cast<int>((p.NR * slices * p.split + kJoinWarps - 1) / kJoinWarps), (4 * device_sm_count() + cuts - 1) / cuts))
+               : std::max(1, std::min(units, 4 * device_sm_count() / blocks));
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(search ? cuts : blocks, y);
   cfg.blockDim = dim3(kJoinThreads);

@@ -951,6 +951,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             tmem_ld_wait();
           }
           if (ch >= p.Dv || (!whole && n == 0)) continue;
+          float prior[8];
+          if (EXT && whole && p.join.prior.rows) {   // all on their way before the first is used
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              prior[e] = col + e < w.rows ? p.join.prior.rows[static_cast<int64_t>(out_row[col + e]) * p.Dv + ch] : 0.f;
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int r = col + e;
@@ -959,12 +965,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
               const float inv = inv_sum[r];
               float y = inv != 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
               if constexpr (EXT) {
-                const int64_t at = static_cast<int64_t>(out_row[r]) * p.Dv + ch;
                 if (p.join.prior.rows_out) {
-                  p.join.prior.rows_out[at] = y;
+                  p.join.prior.rows_out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = y;
                   continue;
                 }
-                if (p.join.prior.rows) y = fmaf(y, xch[NR + r], p.join.prior.rows[at] * xch[r]);
+                if (p.join.prior.rows) y = fmaf(y, xch[NR + r], prior[e] * xch[r]);
               }
               p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
             } else {
