@@ -33,7 +33,7 @@ LIB_NAME = "librope_attention.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "qkv_project.cu", "qk_norm_rope.cu", "kv_cache.cu", "noalloc.cu", "row_quant.cu",
-           "packed_attention.cu", "packed_window.cu", "paged_attention.cu", "paged_extended.cu", "paged_tile.cu",
+           "packed_attention.cu", "packed_window.cu", "paged_attention.cu", "paged_extended.cu", "paged_tokens.cu", "paged_tile.cu",
            "paged_tile_extended.cu", "cache_read.cu", "cache_paging.cu"]
 
 

@@ -74,6 +74,12 @@ size_t paged_tile_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why);
 cudaError_t launch_paged_tile_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
+// The kernel for up to 16 rows per sequence and kv head of the calls with a window or a prefix
+// (paged_tokens.cu).  Its parts never need more room than those of the kernel that serves
+// paged_attention for the same sizes.
+bool paged_tokens_serves(const PagedLaunch& L);
+cudaError_t launch_paged_tokens(const PagedLaunch& L, cudaStream_t stream, const char** why);
+
 struct ReadLaunch {
   const int64_t* index;
   const void *k_cache, *v_cache;

@@ -359,8 +359,7 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
       }
       if (S > 1) __syncthreads();
     }
-    return;
-  }
+  } else {
   for (int32_t unit = blockIdx.y; unit < rows * slices; unit += gridDim.y) {
     const int32_t ch = (unit % slices) * 128 + lane * 4;
     const JoinRow row = join_row(p, rows0, tok0, head0, unit / slices);
@@ -423,6 +422,7 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
       if (ch < p.Dv) join_store<F16, EXT>(p, row, kv_head, ch, acc, l, share);
     }
     __syncthreads();
+  }
   }
 }
 

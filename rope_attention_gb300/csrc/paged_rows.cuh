@@ -112,16 +112,22 @@ struct Params {
   // EXT
   Window window;
   int32_t cu_step, shifts;
+  const uint16_t* q;            // paged_tokens.cu, which does without tq
 };
 
+// What the threads of a block tell each other to find its run.
+template <int THREADS>
+struct RunScan {
+  int64_t scan[THREADS / 32];
+  int64_t start_off;
+  int32_t start_b;
+};
 struct Misc {                   // behind the tiles in shared memory
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t code_full[kMaxStages], code_empty[kMaxStages];
   uint64_t s_full[2], p_ready, pv_done, q_full, q_ready, q_empty, drain;
   uint64_t valid[kValidRing];
-  int64_t scan[kThreads / 32];
-  int64_t start_off;
-  int32_t start_b;
+  RunScan<kThreads> run;
   uint32_t tmem;
   int32_t abort;
   // followed by per-row arrays of NR: int32 out_row, float row_scale, row_const, xch[2], inv_sum
@@ -245,6 +251,85 @@ struct Walker {
     return false;
   }
 };
+
+// The block's run: `per` tiles (p.whole: items) from `start`, for every warp's walk.  Up to 32
+// sequences every warp finds it for itself, beside the set-up of the block (a block-wide scan
+// behind it cost a short decode step 2.5k cycles more).  start_run ends it, behind a __syncthreads.
+template <bool EXT, int THREADS, int ROOM>
+__device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, RunScan<ROOM>& ms, int64_t& per, int64_t& start) {
+  static_assert(THREADS <= ROOM, "");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  walk.b = p.B;
+  walk.off = 0;
+  walk.spans.load(p, 0);
+  const bool few = p.B <= 32;
+  int64_t mine = 0;
+  int32_t b_lo = lane, b_hi = lane;
+  if (few) {
+    mine = seq_work<EXT>(p, walk.spans.lq, walk.spans.len);
+  } else {
+    const int32_t chunk = (p.B + THREADS - 1) / THREADS;
+    b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
+    b_hi = min(p.B, b_lo + chunk);
+    for (int32_t b = b_lo; b < b_hi; ++b) {
+      int32_t qs, lq;
+      q_span<EXT>(p, b, qs, lq);
+      mine += seq_work<EXT>(p, lq, seq_len_of(p, b));
+    }
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  int64_t before = incl - mine, W = 0;
+  if (few) {
+    W = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    if (lane == 31) ms.scan[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int64_t t = ms.scan[w];
+      if (w < warp) before += t;
+      W += t;
+    }
+  }
+  const int64_t G = gridDim.x;
+  const int64_t even = W >> 31 ? (W + G - 1) / G : static_cast<int64_t>((static_cast<uint32_t>(W) + static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(G));
+  per = max(even, static_cast<int64_t>(1));
+  start = per * blockIdx.x;
+  walk.rem = max(static_cast<int64_t>(0), min(per, W - start));  // none: the block has nothing to do
+  const bool here = before <= start && start < before + mine;
+  if (few) {
+    const uint32_t at = __ballot_sync(0xffffffffu, here);
+    if (at) {
+      walk.b = __ffs(at) - 1;
+      walk.off = start - __shfl_sync(0xffffffffu, before, walk.b);
+    }
+  } else if (here) {
+    int32_t b = b_lo;
+    int64_t off = start - before;
+    for (; b < b_hi; ++b) {
+      int32_t qs, lq;
+      q_span<EXT>(p, b, qs, lq);
+      const int64_t w = seq_work<EXT>(p, lq, seq_len_of(p, b));
+      if (off < w) break;
+      off -= w;
+    }
+    ms.start_b = b;
+    ms.start_off = off;
+  }
+}
+template <bool EXT, int ROOM>
+__device__ __forceinline__ void start_run(const Params& p, Walker<EXT>& walk, const RunScan<ROOM>& ms) {
+  if (p.B > 32 && walk.rem > 0) {
+    walk.b = ms.start_b;
+    walk.off = ms.start_off;
+    walk.spans.load(p, walk.b);
+  }
+}
 
 // over the softmax warps
 __device__ __forceinline__ uint32_t bar_or(uint32_t pred) {
@@ -420,78 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   }
   grid_launch_dependents();
 
-  // ---- this block's run of tiles.  Up to 32 sequences every warp finds it for itself, beside
-  // the set-up above (a block-wide scan behind it cost a short decode step 2.5k cycles more).
+  // ---- this block's run of tiles
   Walker<EXT> walk;
-  walk.b = p.B;
-  walk.off = 0;
-  walk.spans.load(p, 0);
-  const bool few = p.B <= 32;
-  int64_t mine = 0;
-  int32_t b_lo = lane, b_hi = lane;
-  if (few) {
-    mine = seq_work<EXT>(p, walk.spans.lq, walk.spans.len);
-  } else {
-    const int32_t chunk = (p.B + kThreads - 1) / kThreads;
-    b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
-    b_hi = min(p.B, b_lo + chunk);
-    for (int32_t b = b_lo; b < b_hi; ++b) {
-      int32_t qs, lq;
-      q_span<EXT>(p, b, qs, lq);
-      mine += seq_work<EXT>(p, lq, seq_len_of(p, b));
-    }
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  int64_t before = incl - mine, W = 0;
-  if (few) {
-    W = __shfl_sync(0xffffffffu, incl, 31);
-  } else {
-    if (lane == 31) ms.scan[warp] = incl;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int64_t t = ms.scan[w];
-      if (w < warp) before += t;
-      W += t;
-    }
-  }
-  const int64_t G = gridDim.x;
-  const int64_t even = W >> 31 ? (W + G - 1) / G : static_cast<int64_t>((static_cast<uint32_t>(W) + static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(G));
-  const int64_t per = max(even, static_cast<int64_t>(1)), start = per * blockIdx.x;
-  walk.rem = max(static_cast<int64_t>(0), min(per, W - start));  // none: the block has nothing to do
-  const bool here = before <= start && start < before + mine;
-  if (few) {
-    const uint32_t at = __ballot_sync(0xffffffffu, here);
-    if (at) {
-      walk.b = __ffs(at) - 1;
-      walk.off = start - __shfl_sync(0xffffffffu, before, walk.b);
-    }
-  } else if (here) {
-    int32_t b = b_lo;
-    int64_t off = start - before;
-    for (; b < b_hi; ++b) {
-      int32_t qs, lq;
-      q_span<EXT>(p, b, qs, lq);
-      const int64_t w = seq_work<EXT>(p, lq, seq_len_of(p, b));
-      if (off < w) break;
-      off -= w;
-    }
-    ms.start_b = b;
-    ms.start_off = off;
-  }
+  int64_t per, start;
+  find_run<EXT, kThreads>(p, walk, ms.run, per, start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (!few && walk.rem > 0) {
-    walk.b = ms.start_b;
-    walk.off = ms.start_off;
-    walk.spans.load(p, walk.b);
-  }
+  start_run(p, walk, ms.run);
   const uint32_t tmem = ms.tmem;
   const bool k_quant = p.kq != 0 || (p.v1 && p.vq != 0);
   volatile int* abort_flag = &ms.abort;
@@ -1000,6 +1021,28 @@ struct Plan {
 bool p_in_two(const PagedLaunch& L) { return L.f16 && (L.kq != 0 || L.vq != 0); }
 int p_bytes(const PagedLaunch& L, int nr) { return nr * 128 * (p_in_two(L) ? 2 : 1); }
 
+// The row tiles of NR rows, and the blocks that share their key tiles: one per SM, and no more than there
+// are tiles at the largest lengths.
+void share_out(const PagedLaunch& L, Plan* pl) {
+  const int g = L.heads / static_cast<int32_t>(L.N), nr = pl->NR;
+  pl->hb = std::min(g, nr);
+  pl->tb = nr / pl->hb;
+  pl->hblocks = g > nr ? (g + nr - 1) / nr : 1;
+  if (pl->hblocks > 1) pl->tb = 1;
+  const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
+  pl->items = rts * L.N;
+  const int64_t all = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
+  pl->window = make_window(L.window, L.sinks, pl->tb, kKeys);
+  const int64_t T = std::min<int64_t>(all, pl->window.most);
+  const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
+  pl->whole = (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
+  const auto blocks = [](int64_t runs) { return static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs))); };
+  pl->G = blocks(pl->whole ? pl->items : pl->items * T);
+  // as if items were cut always: a workspace that is sized at the largest batch, which may take
+  // whole items, serves the smaller ones, which cut theirs
+  pl->room = blocks(pl->items * all);
+}
+
 // The rows of a tile: as many as a sequence's tokens and heads fill on average, so that a
 // decode step does not pay for 128, within what shared memory leaves for two stages.
 bool plan(const PagedLaunch& L, Plan* pl) {
@@ -1039,23 +1082,7 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   pl->off_staging = pl->off_ring + pl->ns * pl->stage;
   pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
-  // one block per SM, and no more than there are tiles at the largest lengths
-  pl->hb = std::min(g, nr);
-  pl->tb = nr / pl->hb;
-  pl->hblocks = g > nr ? (g + nr - 1) / nr : 1;
-  if (pl->hblocks > 1) pl->tb = 1;
-  const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
-  pl->items = rts * L.N;
-  const int64_t all = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
-  pl->window = make_window(L.window, L.sinks, pl->tb, kKeys);
-  const int64_t T = std::min<int64_t>(all, pl->window.most);
-  const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
-  pl->whole = (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
-  const auto blocks = [](int64_t runs) { return static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs))); };
-  pl->G = blocks(pl->whole ? pl->items : pl->items * T);
-  // as if items were cut always: a workspace that is sized at the largest batch, which may take
-  // whole items, serves the smaller ones, which cut theirs
-  pl->room = blocks(pl->items * all);
+  share_out(L, pl);
   return true;
 }
 
@@ -1077,17 +1104,11 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
   return p.whole ? cudaSuccess : launch_join<EXT>(p.join, F16, blocks, items, stream);
 }
 
-template <bool EXT>
-cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** why) {
-  Plan pl;
-  if (!plan(L, &pl)) {
-    *why = "no tile shape fits";
-    return cudaErrorInvalidValue;
-  }
+// what a launch's kernel takes from the call and its plan
+Params row_params(const PagedLaunch& L, const Plan& pl) {
   Params p{};
   p.join.NR = p.join.sub = pl.NR;
   join_place(&p.join, L.partials, pl.G);
-  pl.G = std::min(pl.G, device_sm_count());
   p.out = L.out;
   p.lse = L.lse;
   p.k_scale = L.k_scale;
@@ -1142,6 +1163,27 @@ cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** 
   p.hblocks = pl.hblocks;
   p.box_rows = L.mode == kModeNorm || L.block_size % 64 == 0 ? 64 : L.block_size % 32 == 0 ? 32 : 16;
   p.box_shift = p.box_rows == 64 ? 6 : p.box_rows == 32 ? 5 : 4;
+  p.scale = L.scale;
+  p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
+  p.wait_ns = static_cast<uint64_t>(L.wait_ns);
+  p.whole = pl.whole;
+  p.stall_loads = L.stall_loads;
+  p.window = pl.window;
+  p.cu_step = L.cu_step;
+  p.shifts = L.shifts;
+  p.join.prior = Prior{L.rows_out, L.stats_out, L.prior, L.prior_stats};
+  return p;
+}
+
+template <bool EXT>
+cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** why) {
+  Plan pl;
+  if (!plan(L, &pl)) {
+    *why = "no tile shape fits";
+    return cudaErrorInvalidValue;
+  }
+  Params p = row_params(L, pl);
+  pl.G = std::min(pl.G, device_sm_count());
   if (!encode_maps([&] {
         return make_q_map(&p.tq, L, pl.hb, pl.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
                make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows);
@@ -1161,15 +1203,6 @@ cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** 
   p.off_ring = pl.off_ring;
   p.off_staging = pl.off_staging;
   p.off_misc = pl.off_misc;
-  p.scale = L.scale;
-  p.sl2 = static_cast<float>(static_cast<double>(L.scale) * 1.4426950408889634);
-  p.wait_ns = static_cast<uint64_t>(L.wait_ns);
-  p.whole = pl.whole;
-  p.stall_loads = L.stall_loads;
-  p.window = pl.window;
-  p.cu_step = L.cu_step;
-  p.shifts = L.shifts;
-  p.join.prior = Prior{L.rows_out, L.stats_out, L.prior, L.prior_stats};
 
   if (L.f16)
     return p_in_two(L) ? launch<true, true, true, EXT>(p, pl.G, pl.items, pl.smem, stream)

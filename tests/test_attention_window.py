@@ -161,7 +161,9 @@ def test_fp16_and_large_scores():
 
 
 def test_a_window_that_hides_nothing_is_paged_attention():
-    for variant, news, kt in ((2, [1, 1], "bf16"), (2, [100, 60], "int8"), (1, [2, 1], "int8")):
+    # to the bit where both calls run the same kernel (V2 with up to 16 rows has one of its own here, which
+    # sums in another order: the other tests hold it to the oracle)
+    for variant, news, kt in ((2, [100, 60], "int8"), (1, [2, 1], "int8")):
         dims = dict(Dkv=576, Dv=512, N=1) if variant == 1 else dict(N=2)
         c = Case(35, variant=variant, lens=[333, 150], news=news, heads=8, kt=kt, vt=kt, window=1 << 33, sinks=0, **dims)
         c.run_and_check()

@@ -223,6 +223,7 @@ def test_binding_refuses_bad_forms():
     ("packed_window.cu", "tile_attention_kernel", {168: 4}),
     ("paged_tile_extended.cu", "tile_attention_kernel", {168: 4, 128: 4}),
     ("paged_extended.cu", "paged_attention_kernel", {128: 4}),
+    ("paged_tokens.cu", "paged_tokens_kernel", {168: 16}),        # half of them with 2 x 216 + 72 = 3 x 168
 ])
 def test_register_budgets(file, kernel, budget, tmp_path):
     """As for the calls without a window or prefix: what the warpgroups give out is what they were
@@ -234,7 +235,7 @@ def test_register_budgets(file, kernel, budget, tmp_path):
     rep = ptxas_report(file, str(tmp_path))
     hits = [v for n, v in rep.items() if kernel in n]
     assert {r: sum(h[0] == r for h in hits) for r in {h[0] for h in hits}} == budget, hits
-    assert all(spill <= (384 if 128 in budget and 168 in budget else 160) for _, spill in hits), hits
+    assert all(spill <= (384 if 128 in budget and 168 in budget else 192) for _, spill in hits), hits
     assert all((regs <= 64 and spill <= 128) if "Li4" in n else (regs <= 128 and spill == 0)
                for n, (regs, spill) in rep.items() if "attention_join_kernel" in n)
 
