@@ -87,13 +87,13 @@ __device__ __forceinline__ float prior_shares(float own, float prior, float2& sh
 // The end of row `at`: m (log2) and l its statistics, k0 the lse's share of the key offsets (0 where
 // l is).  They go out, or the prior's are weighed with them.
 __device__ __forceinline__ void prior_end(const Prior& p, int64_t at, float m, float l, float k0, bool writes, float* lse,
-                                          float2& share) {
+                                          float2& share, const float2* have = nullptr) {
   const float own = l != 0.f ? m + log2f(l) : neg_inf();
   if (p.stats_out) {
     if (writes) p.stats_out[at] = make_float2(own, k0);
     return;
   }
-  const float2 o = p.stats[at];
+  const float2 o = have ? *have : p.stats[at];
   const float sum = prior_shares(own, o.x, share);
   if (writes && lse) lse[at] = sum != neg_inf() ? sum * 0.6931471805599453f + (l != 0.f ? k0 : o.y) : neg_inf();
 }
@@ -145,10 +145,10 @@ __device__ __forceinline__ JoinRow join_row(const JoinParams& p, int32_t rows0, 
   const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(in) / static_cast<uint32_t>(p.hb));
   return JoinRow{r < rows0 ? r : p.sub + in, tok0 + (r < rows0 ? 0 : p.tb) + t, head0 + in - t * p.hb};
 }
-// share: of the row's own result and of the prior's (EXT)
+// share: of the row's own result and of the prior's (EXT); have: the prior's, where it has been fetched
 template <bool F16, bool EXT>
 __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& row, int32_t kv_head, int32_t ch, float4 acc,
-                                           float l, float2 share) {
+                                           float l, float2 share, const float4* have = nullptr) {
   const float inv = l != 0.f ? rcp(l) : 0.f;
   float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   if (p.v_scale) {
@@ -165,7 +165,7 @@ __device__ __forceinline__ void join_store(const JoinParams& p, const JoinRow& r
       return;
     }
     if (p.prior.rows) {
-      const float4 o = *reinterpret_cast<const float4*>(p.prior.rows + at);
+      const float4 o = have ? *have : *reinterpret_cast<const float4*>(p.prior.rows + at);
       y[0] = fmaf(y[0], share.x, o.x * share.y);
       y[1] = fmaf(y[1], share.x, o.y * share.y);
       y[2] = fmaf(y[2], share.x, o.z * share.y);
@@ -181,11 +181,12 @@ __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row
 // The end of a row's statistics: m and k0 as in the parts, l their sum.  EXT: what joins it is
 // looked up and weighed (share); `writes` in the thread that writes them.
 template <bool EXT>
-__device__ __forceinline__ float2 join_row_end(const JoinParams& p, const JoinRow& row, float m, float l, float k0, bool writes) {
+__device__ __forceinline__ float2 join_row_end(const JoinParams& p, const JoinRow& row, float m, float l, float k0, bool writes,
+                                               const float2* have = nullptr) {
   float2 share = make_float2(1.f, 0.f);
   if constexpr (EXT) {
     if (p.prior.stats_out || p.prior.stats) {
-      prior_end(p.prior, row.token * p.heads + row.head, m, l, l != 0.f ? k0 : 0.f, writes, p.lse, share);
+      prior_end(p.prior, row.token * p.heads + row.head, m, l, l != 0.f ? k0 : 0.f, writes, p.lse, share, have);
       return share;
     }
   }

@@ -6,17 +6,18 @@
 // Here the work is the reading of the cache: a key of 320 codes meets 8 to 16 rows, 16 to 32 operations
 // a byte where the tensor core does some 280 a byte of HBM, so the products go through warp-level MMAs
 // on registers, and what counts is a short way from shared memory to the result.
-//  * A tile is 64 keys.  Four warps take it, 16 keys each; the other four the next one.  A warp keeps its
+//  * A tile is 64 keys.  Four warps take it, 16 keys each; the next four the next one.  A warp keeps its
 //    own maximum, sum and accumulator, so nothing is exchanged before the end of a piece.
 //  * M is the keys (then the channels) and N the rows, eight at a time: 8 rows cost half of what 16
 //    would in the usual order.  S^T leaves the MMA as P^T's operand up to a transposition of 8 x 8
 //    blocks within the warp.
 //  * Codes become fp16 in registers.  The contraction's order is free as long as both operands have
 //    the same: a lane takes 16 neighbouring channels of its keys for four steps (q is laid out to match), and
-//    of the values 16 neighbouring channels of four keys, whose bytes it interleaves.  For that the
-//    keys of a block stand in the order kOrder, with which neither load has bank conflicts.
-//  * A ninth warp walks the block table and issues TMA boxes of 64 bytes (16-bit values: 128) x 16 to
-//    64 keys, four to nine tiles ahead.
+//    of the values 16 neighbouring channels of four keys, whose bytes it interleaves.  Rows of 192 and
+//    64 bytes, and of 128 with the swizzle, then have no bank conflicts.
+//  * Another warp walks the block table and issues TMA boxes of 16 to 64 keys, four to nine tiles ahead:
+//    whole rows of codes, 128 bytes of 16-bit ones.  A third walks the pieces ahead of the others and
+//    lays out their queries.
 // The runs of tiles, their parts and the join are paged_rows.cuh's.  The maximum follows only when a
 // tile exceeds it by 2^kLazy.  Every wait on an mbarrier is bounded in time (status word); the warps meet
 // at the end of a piece and leave it, or the loop, together.
@@ -25,24 +26,32 @@
 namespace ra {
 namespace {
 
-constexpr int kTokenWarps = 8, kTileWarps = 4;
-// 16 rows: the warps that compute take registers from a third warpgroup, one warp of which loads
-// (2 x 216 + 72 = 3 x 168; with 288 threads ptxas has 168 for each and spills 280 bytes)
-__host__ __device__ constexpr int token_threads(int nt) { return nt == 1 ? 32 * (kTokenWarps + 1) : 384; }
-constexpr int kRegsCompute = 216, kRegsLoad = 72;
+// Two teams of four warps compute; of a third warpgroup, whose registers they take (2 x 208 + 88 = 3 x 168),
+// one warp loads tiles and one prepares pieces.  (Three teams, for 8 rows: no gain.)
+constexpr int kTokenWarps = 8, kTileWarps = 4, kTeams = kTokenWarps / kTileWarps, kTokenThreads = 32 * kTokenWarps + 128;
+constexpr int kTokenLoad = kTokenWarps, kTokenPieces = kTokenWarps + 1;
+constexpr int kRegsCompute = 208, kRegsOther = 88;
 constexpr int kTokenStages = 12;          // at most
-constexpr int kBoxSlab = kKeys * 64;      // 64 keys x 64 bytes
 constexpr int kTokenRow = 132;            // floats of a row where the warps' results meet
 constexpr int kTokenDk = 192, kTokenDv = 128;
-// key of place m among 8: lanes m / 4 take two of them with a load of K, lanes m % 4 four with one of V
-constexpr uint32_t kOrder = 0x65742130u;
 
+// A piece as its warp hands it over.
+struct TokenPiece {
+  int32_t end;                            // there is no further piece
+  int32_t rows, kv_head, ta, n, skip, whole;
+  int32_t slot;                           // of its part
+  int32_t seen_least, from_most;
+  int32_t seen[16], from[16];             // what each row sees: positions below, and from its window on
+  int2 row[16];                           // token and head
+  float row_scale[16], row_const[16];     // of the scores; the lse's share of the key offsets
+};
 struct TokenMisc {
   uint64_t full[kTokenStages], empty[kTokenStages];
+  uint64_t piece_full[2], piece_empty[2];
   uint64_t valid[kValidRing];
-  RunScan<384> run;
+  RunScan<kTokenThreads> run;
   float2 stats[kTokenWarps][16];          // (max, sum) of each warp's rows
-  float row_scale[16], row_const[16];
+  TokenPiece pieces[2];
   int32_t abort;
 };
 
@@ -73,61 +82,65 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Rows g and g + 8 of the piece's queries as the second operand of S^T: for codes over the key's scales
-// and behind a power of two per row (paged_rows.cuh, scale_q), which row_scale undoes.
-//   16-bit keys: slab j (32 channels), lane t of a row's four: channels 32 j + 8 t .. + 7, two steps
-//   codes:       slab j (64 channels): channels 64 j + 16 t .. + 15, four steps
+// The chunk (16 bytes of a key's row) that lane t takes for its j-th load.  Eight lanes load at once, four
+// chunks of two neighbouring keys: in rows of 128 bytes with the swizzle the even chunks of one
+// meet the odd banks of the other, and so on.
+template <bool KQ>
+__device__ __forceinline__ int key_chunk(const Params& p, int j, int t) {
+  if (!KQ || p.kslab0) return 8 * (j >> 1) + 2 * t + (j & 1);
+  return 4 * j + t;
+}
+
+// Rows g (+ 8) of a piece's queries as the second operand of S^T, in to[nt][24][lane]: for codes over the
+// key's scales and behind a power of two per row (paged_rows.cuh, scale_q), which row_scale undoes.
+// Lane t of a row's four has its 16-byte chunks key_chunk(p, j, t): of 16-bit keys 8 channels each, two
+// steps; of codes 16 channels, four steps.  One warp; rolled loops, as every line of code comes
+// from L2 at the start of a block.
 template <bool F16, bool KQ, int NT>
-__device__ __forceinline__ void load_q(const Params& p, const Piece& w, int64_t q_row0, uint32_t (&qf)[NT][24], float (&scale)[NT],
-                                       TokenMisc& ms, int warp, int lane) {
-  constexpr int kSlabs = KQ ? 3 : 6, kWide = KQ ? 16 : 8;
+__device__ __forceinline__ void prepare_q(const Params& p, TokenPiece& w, uint32_t* to, int lane) {
+  constexpr int kChunks = KQ ? 3 : 6, kWide = KQ ? 16 : 8;
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll 1
+  for (int nt = 0; nt < NT; ++nt, to += 24 * 32) {
     const int r = g + 8 * nt;
     const bool live = r < w.rows;
-    const int32_t tok = p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.hb));
-    const uint16_t* q = p.q + (q_row0 + static_cast<int64_t>(tok) * p.heads + (r - tok * p.hb)) * p.Dk;
-    uint32_t x[24];
+    const uint16_t* q = p.q + (static_cast<int64_t>(w.row[r].x) * p.heads + w.row[r].y) * p.Dk;
+    uint32_t big = 0;           // |q| as bits orders like the value in either type
+    uint4 x[6];
 #pragma unroll
-    for (int j = 0; j < kSlabs; ++j) {
-      const int c = j * 4 * kWide + t * kWide;
-#pragma unroll
-      for (int h = 0; h < kWide / 8; ++h) {
-        const uint4 v = live && c + 8 * h < p.Dk ? __ldg(reinterpret_cast<const uint4*>(q + c + 8 * h)) : make_uint4(0, 0, 0, 0);
-        const int at = j * kWide / 2 + 4 * h;
-        x[at] = v.x, x[at + 1] = v.y, x[at + 2] = v.z, x[at + 3] = v.w;
-      }
+    for (int i = 0; i < 6; ++i) {
+      const int c = key_chunk<KQ>(p, i * 4 / (kWide / 2), t) * kWide + (KQ ? 8 * (i & 1) : 0);
+      x[i] = live && c < p.Dk ? __ldg(reinterpret_cast<const uint4*>(q + c)) : make_uint4(0, 0, 0, 0);
     }
-    if constexpr (!KQ) {
+    float least = 3e38f, shift = 0.f;
+    const float* ks = KQ ? p.k_scale + static_cast<int64_t>(w.kv_head) * p.Dk : nullptr;
+    if constexpr (KQ) {
 #pragma unroll
-      for (int i = 0; i < 24; ++i) qf[nt][i] = x[i];
-      scale[nt] = p.sl2;
-    } else {
-      const float* ks = p.k_scale + static_cast<int64_t>(w.n) * p.Dk;
-      const float* ko = p.k_offset ? p.k_offset + static_cast<int64_t>(w.n) * p.Dk : nullptr;
-      uint32_t big = 0;         // |q| as bits orders like the value in either type
-      float top = 0.f, shift = 0.f;
-#pragma unroll
-      for (int i = 0; i < 24; ++i) big = __vmaxu2(big, x[i] & 0x7FFF7FFFu);
-      big = max(big & 0xFFFFu, big >> 16);
-      float inv[48];
-#pragma unroll
-      for (int j = 0; j < 3; ++j)
+      for (int j = 0; j < kChunks; ++j)
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const int c = 64 * j + 16 * t + 4 * h;
-          const float4 s = c < p.Dk ? __ldg(reinterpret_cast<const float4*>(ks + c)) : make_float4(1.f, 1.f, 1.f, 1.f);
-          const float4 o = ko && p.shifts && c < p.Dk ? __ldg(reinterpret_cast<const float4*>(ko + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float s4[4] = {s.x, s.y, s.z, s.w}, o4[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 16 * j + 4 * h + e;
-            inv[i] = c < p.Dk ? rcp(s4[e]) : 0.f;
-            top = fmaxf(top, fabsf(inv[i]));
-            if (p.shifts) shift += half_to_float<F16>((x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu) / s4[e] * o4[e];
-          }
+          const int c = 16 * key_chunk<KQ>(p, j, t) + 4 * h;
+          const float4 v = c < p.Dk ? __ldg(reinterpret_cast<const float4*>(ks + c)) : make_float4(3e38f, 3e38f, 3e38f, 3e38f);
+          least = fminf(fminf(fminf(least, fabsf(v.x)), fminf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        to[(4 * i + e) * 32 + lane] = u[e];
+        big = __vmaxu2(big, u[e] & 0x7FFF7FFFu);
+      }
+    }
+    if constexpr (KQ) {
+      big = max(big & 0xFFFFu, big >> 16);
+      float top = rcp(least);
+      if (p.shifts && p.k_offset) {
+        const float* ko = p.k_offset + static_cast<int64_t>(w.kv_head) * p.Dk;
+#pragma unroll 1
+        for (int c = t; c < p.Dk && live; c += 4) shift += half_to_float<F16>(__ldg(q + c)) / __ldg(ks + c) * __ldg(ko + c);
+      }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -136,26 +149,38 @@ __device__ __forceinline__ void load_q(const Params& p, const Piece& w, int64_t 
       }
       const int k = max(-100, min(100, -(scale_exponent(half_to_float<F16>(big)) + scale_exponent(top) + 15)));
       const float up = exp2_int(k);
+#pragma unroll 1
+      for (int j = 0; j < kChunks; ++j) {
+        const int c = 16 * key_chunk<KQ>(p, j, t);
+        if (c >= p.Dk) continue;
 #pragma unroll
-      for (int i = 0; i < 24; ++i)
-        qf[nt][i] = pack_f16x2(half_to_float<F16>(x[i] & 0xFFFFu) * (inv[2 * i] * up), half_to_float<F16>(x[i] >> 16) * (inv[2 * i + 1] * up));
-      scale[nt] = p.sl2 * exp2_int(-k);
-      if (warp == 0 && t == 0) {            // for the end of the piece
-        ms.row_scale[r] = scale[nt];
-        ms.row_const[r] = -shift * p.scale;
+        for (int h = 0; h < 4; ++h) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(ks + c + 4 * h));
+          uint32_t* const at = to + (8 * j + 2 * h) * 32 + lane;
+          const uint32_t u0 = at[0], u1 = at[32];
+          at[0] = pack_f16x2(half_to_float<F16>(u0 & 0xFFFFu) * (rcp(v.x) * up), half_to_float<F16>(u0 >> 16) * (rcp(v.y) * up));
+          at[32] = pack_f16x2(half_to_float<F16>(u1 & 0xFFFFu) * (rcp(v.z) * up), half_to_float<F16>(u1 >> 16) * (rcp(v.w) * up));
+        }
       }
+      if (t == 0) {
+        w.row_scale[r] = p.sl2 * exp2_int(-k);
+        w.row_const[r] = -shift * p.scale;
+      }
+    } else if (t == 0) {
+      w.row_scale[r] = p.sl2;
+      w.row_const[r] = 0.f;
     }
   }
 }
 
 // F16: q, out and 16-bit caches are fp16, not bf16.  KQ, VQ: keys, values are codes.  NT: rows / 8.
 template <bool F16, bool KQ, bool VQ, int NT>
-__global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __grid_constant__ Params p) {
   constexpr bool K16 = F16 || KQ, P16 = F16 || VQ, PLO = F16 && (KQ || VQ);   // as in paged_rows.cuh
   constexpr float kLift = P16 ? kHalfLift : 0.f;
-  constexpr int kVSlab = VQ ? kBoxSlab : kSlab;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* meet = reinterpret_cast<float*>(smem + p.off_p);            // [warp][row][kTokenRow]
+  uint32_t* queries = reinterpret_cast<uint32_t*>(meet + kTokenWarps * 8 * NT * kTokenRow);  // [2][NT][24][32]
   TokenMisc& ms = *reinterpret_cast<TokenMisc*>(smem + p.off_misc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,31 +189,91 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
       mbar_init(smem_u32(&ms.full[s]), 1);
       mbar_init(smem_u32(&ms.empty[s]), kTileWarps);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&ms.piece_full[s]), 1);
+      mbar_init(smem_u32(&ms.piece_empty[s]), kTokenWarps);
+    }
     ms.abort = 0;
     fence_mbar_init();
     p.join.meta[8 * blockIdx.x] = 0;      // nothing to join, unless the first piece says so below
-  } else if (threadIdx.x == 32 * kTokenWarps) {
+  } else if (threadIdx.x == 32 * kTokenLoad) {
     prefetch_tensormap(&p.tk);
     prefetch_tensormap(&p.tv);
   }
   grid_launch_dependents();
   Walker<true> walk;
   int64_t per, start;
-  find_run<true, token_threads(NT)>(p, walk, ms.run, per, start);
+  if (p.B > 32 || warp >= kTokenWarps) find_run<true, kTokenThreads>(p, walk, ms.run, per, start);  // (B > 32: with a barrier)
   __syncthreads();
-  start_run(p, walk, ms.run);
   volatile int* abort_flag = &ms.abort;
   Piece w{};
-  Ring ring;
+  Ring ring, pieces;
   bool ok = true;
 
   if (warp >= kTokenWarps) {
-    if (NT == 2) set_max_regs_dec<kRegsLoad>();
+    set_max_regs_dec<kRegsOther>();
+    start_run(p, walk, ms.run);
   }
-  if (warp == kTokenWarps) {
+  if (warp == kTokenPieces) {
+    // ------------------------------------------------------------ pieces
+    bool more = true;
+    for (int32_t piece = 0; more; ++piece) {
+      more = walk.next(p, w);
+      if (!bounded_wait_warp(smem_u32(&ms.piece_empty[pieces.stage]), pieces.parity ^ 1u, p.wait_ns, abort_flag)) break;
+      if (__any_sync(0xffffffffu, *abort_flag)) break;  // no piece for those that are about to leave
+      TokenPiece& to = ms.pieces[pieces.stage];
+      if (more) {
+        const bool began = piece == 0 && w.t0 > 0;      // an item that the block before began
+        if (began && lane == 0) {
+          // the block behind the first cut through an item joins the item's pieces
+          const int64_t item0 = start - w.t0;
+          const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
+          int32_t* mt = p.join.meta + 8 * blockIdx.x;
+          mt[1] = first;
+          mt[2] = last;
+          mt[3] = w.rows;
+          mt[4] = 0;
+          mt[5] = w.q_start + w.tok;
+          mt[6] = w.head;
+          mt[7] = w.n;
+          mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+        }
+        // row `lane`: its token and head (rows behind the last stand for it), and what it sees
+        const int32_t r = min(lane, w.rows - 1);
+        const int32_t tok = p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.hb));
+        const int32_t at = w.len - w.Lq + w.tok + tok;
+        const int32_t seen = p.causal ? min(w.len, max(0, at + 1)) : w.len, from = window_from(p.window, at);
+        const int32_t seen_least = __reduce_min_sync(0xffffffffu, seen), from_most = __reduce_max_sync(0xffffffffu, from);
+        if (lane < 16) {
+          to.row[lane] = make_int2(w.q_start + w.tok + tok, w.head + r - tok * p.hb);
+          to.seen[lane] = seen;
+          to.from[lane] = from;
+        }
+        if (lane == 0) {
+          to.rows = w.rows;
+          to.kv_head = w.n;
+          to.ta = w.ta;
+          to.n = max(0, w.tb - w.ta);
+          to.skip = w.skip;
+          to.whole = w.whole();
+          to.slot = 2 * static_cast<int32_t>(blockIdx.x) + (began ? 0 : 1);
+          to.seen_least = seen_least;
+          to.from_most = from_most;
+        }
+        __syncwarp();
+        if (w.tb > w.ta) prepare_q<F16, KQ, NT>(p, to, queries + pieces.stage * NT * 24 * 32, lane);
+        else if (lane < 16) to.row_scale[lane] = p.sl2, to.row_const[lane] = 0.f;
+      }
+      if (lane == 0) to.end = more ? 0 : 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms.piece_full[pieces.stage]));
+      pieces.next(2);
+    }
+  } else if (warp == kTokenLoad) {
     // ------------------------------------------------------------ loads
     const int groups = kKeys >> p.box_shift;
-    const uint32_t group_bytes = p.box_rows * (p.kslabs * 64 + p.vslabs * (VQ ? 64 : 128));
+    const int32_t v_row = VQ ? p.Dv : 128, k_row = KQ ? p.Dk : 128;  // bytes of a box's row
+    const uint32_t group_bytes = p.box_rows * (p.kslabs * k_row + p.vslabs * v_row);
     uint32_t armed = 0, armed_parity = 0;  // copies in flight
     int32_t u = 0;
     ok = !p.stall_loads;
@@ -244,10 +329,10 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (at[i] < 0) continue;
-            uint32_t to = stage + (i << p.box_shift) * (VQ ? 64 : 128);
-            for (int32_t c = 0; c < p.vslabs; ++c, to += kVSlab) tma_load_3d(to, &p.tv, bar, 64 * c, head, at[i]);
-            to = stage + p.vslabs * kVSlab + (i << p.box_shift) * 64;
-            for (int32_t c = 0; c < p.kslabs; ++c, to += kBoxSlab) tma_load_3d(to, &p.tk, bar, (KQ ? 64 : 32) * c, head, at[i]);
+            uint32_t to = stage + (i << p.box_shift) * v_row;
+            for (int32_t c = 0; c < (VQ ? 1 : p.vslabs); ++c, to += kSlab) tma_load_3d(to, &p.tv, bar, 64 * c, head, at[i]);
+            to = stage + p.off_staging + (i << p.box_shift) * k_row;
+            for (int32_t c = 0; c < (KQ ? 1 : p.kslabs); ++c, to += kSlab) tma_load_3d(to, &p.tk, bar, 64 * c, head, at[i]);
           }
         }
         __syncwarp();
@@ -262,82 +347,86 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
         if (armed & (1u << i)) bounded_drain(smem_u32(&ms.full[i]), (armed_parity >> i) & 1u, kDrainNs);
     __syncwarp();
   } else if (warp < kTokenWarps) {
-    if (NT == 2) set_max_regs_inc<kRegsCompute>();
+    set_max_regs_inc<kRegsCompute>();
     // ------------------------------------------------------------ products and softmax
-    const int g = lane >> 2, t = lane & 3, quarter = warp & 3, tile_half = warp >> 2;
-    const int32_t key_a = 16 * quarter + ((kOrder >> (4 * g)) & 7);   // and key_a + 8: the lane's keys of S^T
-    // keys of a value operand: two and two more 8 further
-    const int32_t key_v0 = 16 * quarter + ((kOrder >> (8 * t)) & 7), key_v1 = 16 * quarter + ((kOrder >> (8 * t + 4)) & 7);
-    const int32_t key_m = 16 * quarter + ((kOrder >> (4 * (lane & 7))) & 7) + (lane & 16 ? 8 : 0);  // ldmatrix: the lane's key
-    int32_t u = 0, piece = 0;
-    for (; ok && walk.next(p, w); ++piece) {
-      const int32_t n = w.tb - w.ta;
-      const int64_t q_row0 = static_cast<int64_t>(w.q_start + w.tok) * p.heads + w.head;
-      if (piece == 0 && threadIdx.x == 0 && w.t0 > 0) {
-        // the block behind the first cut through an item joins the item's pieces
-        const int64_t item0 = start - w.t0;
-        const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
-        int32_t* mt = p.join.meta + 8 * blockIdx.x;
-        mt[1] = first;
-        mt[2] = last;
-        mt[3] = w.rows;
-        mt[4] = 0;
-        mt[5] = w.q_start + w.tok;
-        mt[6] = w.head;
-        mt[7] = w.n;
-        mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+    const int g = lane >> 2, t = lane & 3, quarter = warp & 3, team = warp >> 2;
+    const int32_t key_a = 16 * quarter + g;          // and key_a + 8, which swizzles alike: the lane's keys of S^T
+    const int32_t k_row = KQ ? p.Dk : 128, v_row = p.Dv;  // bytes of a row of codes (or of a slab's)
+    // where the lane's chunks lie in a stage: of codes three of a key, and of four values; of 16-bit rows
+    // the two of a slab, and its channels' (ldmatrix)
+    uint32_t k_at[KQ ? 3 : 2], v_at[VQ ? 4 : 1];
+    if constexpr (KQ) {
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const int chunk = key_chunk<KQ>(p, c, t);
+        k_at[c] = p.off_staging + key_a * k_row + ((p.kslab0 ? chunk ^ (key_a & 7) : chunk) << 4);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) k_at[c] = p.off_staging + key_a * 128 + (((2 * t + c) ^ (key_a & 7)) << 4);
+    }
+    if constexpr (VQ) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {      // (beyond a short row: channels that nobody has)
+        const int key = 16 * quarter + 2 * t + (i & 1) + 8 * (i >> 1);
+        v_at[i] = key * v_row + ((v_row == 128 ? g ^ (key & 7) : g) << 4);
+      }
+    } else {
+      const int key = 16 * quarter + (lane & 7) + (lane & 16 ? 8 : 0);
+      v_at[0] = key * 128 + (((lane & 8 ? 1 : 0) ^ (key & 7)) << 4);
+    }
+    int32_t u = 0;
+    while (true) {
+      ok = ok && bounded_wait_warp(smem_u32(&ms.piece_full[pieces.stage]), pieces.parity, p.wait_ns, abort_flag);
+      // together, and only when the last piece's results are read
+      if (bar_or(ok ? 0u : 1u)) {
+        ok = false;
+        break;
+      }
+      const TokenPiece& w = ms.pieces[pieces.stage];
+      if (w.end) break;
+      const int32_t n = w.n, ta = w.ta, skip = w.skip;
+      // the rows of another call that this one's join: on their way from here
+      float4 prior[NT];
+      float2 prior_stats[NT];
+      if (p.join.prior.rows && w.whole) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const int2 row = w.row[warp + kTokenWarps * i];
+          const int64_t at = static_cast<int64_t>(row.x) * p.heads + row.y;
+          prior[i] = *reinterpret_cast<const float4*>(p.join.prior.rows + at * p.Dv + min(4 * lane, p.Dv - 4));
+          prior_stats[i] = p.join.prior.stats[at];
+        }
       }
       uint32_t qf[NT][24];
-      float q_scale[NT];                    // of row g + 8 nt
-      if (n > 0) load_q<F16, KQ, NT>(p, w, q_row0, qf, q_scale, ms, warp, lane);
-      // The lane's rows: 8 nt + 2 t + e.  What they see, and the scale of their scores.
-      int32_t seen[NT][2], from[NT][2], seen_least = 0x7fffffff, from_most = 0;
-      float m[NT][2], l[NT][2], sl2[NT][2], lazy[NT][2];
+      // The lane's rows: 8 nt + 2 t + e.
+      float m[NT][2], l[NT][2], sl2[NT][2], lazy[NT][2], neg[NT][2];
       float acc[8][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 24; ++i) qf[nt][i] = queries[((pieces.stage * NT + nt) * 24 + i) * 32 + lane];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * t + e;
-          const int32_t tok = p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(min(r, w.rows - 1)) / static_cast<uint32_t>(p.hb));
-          const int32_t at = w.len - w.Lq + w.tok + tok;
-          seen[nt][e] = p.causal ? min(w.len, max(0, at + 1)) : w.len;
-          from[nt][e] = window_from(p.window, at);
-          seen_least = min(seen_least, seen[nt][e]);
-          from_most = max(from_most, from[nt][e]);
           m[nt][e] = neg_inf();
+          neg[nt][e] = kLift;
           l[nt][e] = 0.f;
-          sl2[nt][e] = p.sl2;
+          sl2[nt][e] = w.row_scale[8 * nt + 2 * t + e];
+          lazy[nt][e] = lazy_slack(kLazy, sl2[nt][e]);
         }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        seen_least = min(seen_least, __shfl_xor_sync(0xffffffffu, seen_least, o));
-        from_most = max(from_most, __shfl_xor_sync(0xffffffffu, from_most, o));
       }
-      if (KQ && n > 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) sl2[nt][e] = __shfl_sync(0xffffffffu, q_scale[nt], 4 * (2 * t + e));
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) lazy[nt][e] = lazy_slack(kLazy, sl2[nt][e]);
 
       for (int32_t j = 0; j < n; ++j, ++u, ring.next(p.ns)) {
-        if ((j & 1) != tile_half) continue;
+        if ((j & (kTeams - 1)) != team) continue;
         if (!bounded_wait_warp(smem_u32(&ms.full[ring.stage]), ring.parity, p.wait_ns, abort_flag)) {
           ok = false;
           break;
         }
-        const uint32_t stage = s0 + ring.stage * p.stage_bytes, k_base = stage + p.vslabs * kVSlab;
+        const uint32_t stage = s0 + ring.stage * p.stage_bytes;
         // ---- S^T
         float s[2][NT][4];
 #pragma unroll
@@ -346,14 +435,17 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
-        const uint32_t ka = k_base + key_a * 64 + t * 16;
         if constexpr (KQ) {
           with_kind(p.kq, [&](auto kind) {
             constexpr int K = decltype(kind)::value;
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
-              if (c >= p.kslabs) break;
-              const uint4 xa = lds_128(ka + c * kBoxSlab), xb = lds_128(ka + c * kBoxSlab + 8 * 64);
+              if (64 * c >= p.Dk) break;
+              uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+              if (16 * key_chunk<KQ>(p, c, t) < p.Dk) {    // (beyond the row lies another, which may be anything)
+                xa = lds_128(stage + k_at[c]);
+                xb = lds_128(stage + k_at[c] + 8 * k_row);
+              }
               const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -367,8 +459,9 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
         } else {
 #pragma unroll
           for (int c = 0; c < 6; ++c) {
-            if (c >= p.kslabs) break;
-            const uint4 a = lds_128(ka + c * kBoxSlab), b = lds_128(ka + c * kBoxSlab + 8 * 64);
+            if (64 * (c >> 1) >= p.Dk) break;
+            const uint32_t at = stage + (c >> 1) * kSlab + k_at[c & 1];
+            const uint4 a = lds_128(at), b = lds_128(at + 8 * 128);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_16816<K16>(s[0][nt], a.x, b.x, a.y, b.y, qf[nt][4 * c], qf[nt][4 * c + 1]);
@@ -377,9 +470,9 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
           }
         }
         // ---- what the rows see
-        const int32_t pos0 = w.template pos<true>(p, w.ta + j);
+        const int32_t pos0 = (ta + j) * kKeys + (ta + j >= p.window.tiles ? skip : 0);
         const uint32_t valid = static_cast<uint32_t>(ms.valid[u % kValidRing] >> (16 * quarter)) & 0xFFFFu;
-        const bool edge = valid != 0xFFFFu || pos0 + kKeys > seen_least || (from_most > pos0 && pos0 + kKeys > p.window.sinks);
+        const bool edge = valid != 0xFFFFu || pos0 + kKeys > w.seen_least || (w.from_most > pos0 && pos0 + kKeys > p.window.sinks);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -393,7 +486,10 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (!there || pos >= seen[nt][e] || (pos < from[nt][e] && pos >= p.window.sinks)) s[0][nt][2 * h + e] = neg_inf();
+              {
+                const int r = 8 * nt + 2 * t + e;
+                if (!there || pos >= w.seen[r] || (pos < w.from[r] && pos >= p.window.sinks)) s[0][nt][2 * h + e] = neg_inf();
+              }
           }
         }
         // ---- the running maximum
@@ -413,6 +509,7 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
               if (top > m[nt][e] + lazy[nt][e]) {
                 const float f = ex2((m[nt][e] - top) * sl2[nt][e]);
                 m[nt][e] = top;
+                neg[nt][e] = fmaf(-top, sl2[nt][e], kLift);
                 l[nt][e] *= f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -428,10 +525,7 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float neg = m[nt][e & 1] == neg_inf() ? kLift : fmaf(-m[nt][e & 1], sl2[nt][e & 1], kLift);
-            pr[e] = ex2(fmaf(s[0][nt][e], sl2[nt][e & 1], neg));
-          }
+          for (int e = 0; e < 4; ++e) pr[e] = ex2(fmaf(s[0][nt][e], sl2[nt][e & 1], neg[nt][e & 1]));
           l[nt][0] += pr[0] + pr[2];
           l[nt][1] += pr[1] + pr[3];
 #pragma unroll
@@ -446,23 +540,20 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
         }
         // ---- value rows that do not exist meet P = 0, but 0 times a stray NaN is NaN
         if (valid != 0xFFFFu) {
-          constexpr int kParts = VQ ? 4 : 8;
-          for (int i = lane; i < 16 * kParts; i += 32) {
-            const int key = i / kParts;
+          uint8_t* const rows = smem + ring.stage * p.stage_bytes;
+          for (int key = lane & 15; key < 16; key += 16) {  // two lanes to a key
             if ((valid >> key) & 1) continue;
-            for (int c = 0; c < p.vslabs; ++c)
-              *reinterpret_cast<uint4*>(smem + ring.stage * p.stage_bytes + c * kVSlab + (16 * quarter + key) * (VQ ? 64 : 128) +
-                                        (i % kParts) * 16) = make_uint4(0, 0, 0, 0);
+            for (int i = lane >> 4; i < (VQ ? v_row / 16 : 8 * p.vslabs); i += 2)
+              *reinterpret_cast<uint4*>(rows + (VQ ? (16 * quarter + key) * v_row + i * 16
+                                                   : (i >> 3) * kSlab + (16 * quarter + key) * 128 + (i & 7) * 16)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();       // the next copy into this stage comes behind these
           __syncwarp();
         }
         // ---- O^T
         if constexpr (VQ) {
-          // 16 bytes of a row: chunk g of two slabs of four, swizzled by 64 bytes
-          const uint32_t vb = stage + (g >> 2) * kBoxSlab;
-          auto row = [&](int32_t key) { return lds_128(vb + key * 64 + (((g & 3) ^ ((key >> 1) & 3)) << 4)); };
-          const uint4 r0 = row(key_v0), r1 = row(key_v1), r2 = row(key_v0 + 8), r3 = row(key_v1 + 8);
+          const uint4 r0 = lds_128(stage + v_at[0]), r1 = lds_128(stage + v_at[1]), r2 = lds_128(stage + v_at[2]),
+                      r3 = lds_128(stage + v_at[3]);
           with_kind(p.vq, [&](auto kind) {
             constexpr int K = decltype(kind)::value;
             const uint32_t x0[4] = {r0.x, r0.y, r0.z, r0.w}, x1[4] = {r1.x, r1.y, r1.z, r1.w};
@@ -485,8 +576,7 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
           for (int i = 0; i < 8; ++i) {
             if (16 * i >= p.Dv) break;
             uint32_t a[4];
-            const int chunk = 2 * (i & 3) + (lane & 8 ? 1 : 0);
-            ldmatrix_x4_trans(stage + (i >> 2) * kSlab + key_m * 128 + ((chunk ^ (key_m & 7)) << 4), a);
+            ldmatrix_x4_trans(stage + (i >> 2) * kSlab + (v_at[0] ^ ((i & 3) << 5)), a);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_16816<P16>(acc[i][nt], a[0], a[1], a[2], a[3], hi[nt][0], hi[nt][1]);
@@ -507,8 +597,10 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
           for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
           if (g == 0) ms.stats[warp][8 * nt + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
         }
-      ok = bar_or(ok ? 0u : 1u) == 0;
-      if (!ok) break;
+      if (bar_or(ok ? 0u : 1u)) {
+        ok = false;
+        break;
+      }
       float* const mine = meet + warp * 8 * NT * kTokenRow;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -536,13 +628,11 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
         }
       bar_softmax();
       // ---- final rows, or the piece's statistics and accumulator: a lane has four channels of a row
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1);
-      const bool whole = w.whole();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + warp, ch = 4 * lane;
+      for (int k = 0; k < NT; ++k) {
+        const int r = warp + kTokenWarps * k, ch = 4 * lane;
         if (r < w.rows) {
-          const float scale = KQ && n > 0 ? ms.row_scale[r] : p.sl2, off = KQ && n > 0 ? ms.row_const[r] : 0.f;
+          const float scale = w.row_scale[r], off = w.row_const[r];
           float top = neg_inf(), sum = 0.f;
 #pragma unroll
           for (int i = 0; i < kTokenWarps; ++i) top = fmaxf(top, ms.stats[i][r].x);
@@ -555,54 +645,60 @@ __global__ void __launch_bounds__(token_threads(NT), 1) paged_tokens_kernel(cons
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
           }
           const float top2 = top == neg_inf() ? neg_inf() : fmaf(top, scale, -kLift);
-          const int32_t tok = p.hblocks > 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.hb));
-          JoinRow row;
-          row.part = r;
-          row.token = w.q_start + w.tok + tok;
-          row.head = w.head + r - tok * p.hb;
-          if (whole) {
-            const float2 share = join_row_end<true>(p.join, row, top2, sum, off, lane == 0);
-            if (ch < p.Dv) join_store<F16, true>(p.join, row, w.n, ch, o, sum, share);
+          const JoinRow row{r, w.row[r].x, w.row[r].y};
+          if (w.whole) {
+            const float2 share = join_row_end<true>(p.join, row, top2, sum, off, lane == 0, &prior_stats[k]);
+            if (ch < p.Dv) join_store<F16, true>(p.join, row, w.kv_head, ch, o, sum, share, &prior[k]);
           } else {
-            if (lane == 0) p.join.stats[slot * p.NR + r] = make_float4(top2, sum, off, 0.f);
-            if (ch < p.Dv && n > 0) *reinterpret_cast<float4*>(p.join.parts + (slot * p.NR + r) * p.Dv + ch) = o;
+            const int64_t at = static_cast<int64_t>(w.slot) * p.NR + r;
+            if (lane == 0) p.join.stats[at] = make_float4(top2, sum, off, 0.f);
+            if (ch < p.Dv && n > 0) *reinterpret_cast<float4*>(p.join.parts + at * p.Dv + ch) = o;
           }
         }
       }
-      bar_softmax();                      // stats, scales and results may be written again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms.piece_empty[pieces.stage]));
+      pieces.next(2);
     }
   }
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
 }
 
-// K as 64-byte boxes without a swizzle; V of codes swizzled by 64 bytes, else like an MMA operand
-bool make_box_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32_t width, int32_t quant, int32_t box_rows, bool swizzle) {
+// Codes as boxes of whole rows, swizzled where they have 128 bytes; 16-bit rows as make_map's
+bool make_rows_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32_t width, int32_t quant, int32_t box_rows) {
+  if (quant == 0) return make_map(m, base, L, width, 0, box_rows);
   auto enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  const uint64_t row = static_cast<uint64_t>(width) * (quant ? 1 : 2);
+  const uint64_t row = static_cast<uint64_t>(width);
   const bool pa = L.mode == kModePa;
   const uint64_t slots = L.mode == kModeNorm ? static_cast<uint64_t>(L.B) * L.cache_seq
                                              : static_cast<uint64_t>(L.block_num) * L.block_size;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), pa ? static_cast<cuuint64_t>(L.N) : 1, pa ? slots : slots * L.N};
+  cuuint64_t dims[3] = {row, pa ? static_cast<cuuint64_t>(L.N) : 1, pa ? slots : slots * L.N};
   cuuint64_t strides[2] = {row, pa ? row * L.N : row};
-  cuuint32_t box[3] = {quant ? 64u : 32u, 1, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(width), 1, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
-             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 void plan_tokens(const PagedLaunch& L, Plan* pl) {
   const int g = L.heads / static_cast<int32_t>(L.N);
   pl->NR = (L.total_q + L.B - 1) / L.B * g <= 8 ? 8 : 16;
-  pl->vslabs = (L.Dv + 63) / 64;
-  pl->kslabs = (L.Dkv * (L.kq ? 1 : 2) + 63) / 64;
-  pl->stage = pl->kslabs * kBoxSlab + pl->vslabs * (L.vq ? kBoxSlab : kSlab);
-  const int fixed = kTokenWarps * pl->NR * kTokenRow * 4 + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
+  // a stage: the value rows, then the key rows, each on 1024 bytes (the swizzle's period); codes count as one slab
+  const auto bytes = [](int quant, int width) { return quant ? (kKeys * width + 1023) / 1024 * 1024 : (width + 63) / 64 * kSlab; };
+  pl->vslabs = L.vq ? 1 : (L.Dv + 63) / 64;
+  pl->kslabs = L.kq ? 1 : (L.Dkv + 63) / 64;
+  pl->kslab0 = L.kq && L.Dkv == 128;            // whether codes of keys are swizzled
+  pl->off_staging = bytes(L.vq, L.Dv);          // of the keys in a stage
+  pl->stage = pl->off_staging + bytes(L.kq, L.Dkv);
+  // where the warps' results meet, and two pieces' queries
+  const int meet = kTokenWarps * pl->NR * kTokenRow * 4 + 2 * pl->NR / 8 * 24 * 32 * 4;
+  const int fixed = meet + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
   pl->ns = std::min(kTokenStages, (kSmemMax - fixed) / pl->stage);
   pl->off_p = pl->ns * pl->stage;
-  pl->off_misc = pl->off_p + kTokenWarps * pl->NR * kTokenRow * 4;
+  pl->off_misc = pl->off_p + meet;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
   share_out(L, pl);
 }
@@ -619,8 +715,8 @@ cudaError_t launch_tokens(const Params& p, const Plan& pl, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  if (pl.NR == 8) paged_tokens_kernel<F16, KQ, VQ, 1><<<pl.G, token_threads(1), pl.smem, stream>>>(p);
-  else paged_tokens_kernel<F16, KQ, VQ, 2><<<pl.G, token_threads(2), pl.smem, stream>>>(p);
+  if (pl.NR == 8) paged_tokens_kernel<F16, KQ, VQ, 1><<<pl.G, kTokenThreads, pl.smem, stream>>>(p);
+  else paged_tokens_kernel<F16, KQ, VQ, 2><<<pl.G, kTokenThreads, pl.smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return p.whole ? cudaSuccess : launch_join<true>(p.join, F16, pl.G, pl.items, stream);
@@ -639,16 +735,18 @@ cudaError_t launch_paged_tokens(const PagedLaunch& L, cudaStream_t stream, const
   pl.G = std::min(pl.G, device_sm_count());
   p.q = L.q;
   if (!encode_maps([&] {
-        return make_box_map(&p.tk, L.k_cache, L, L.Dkv, L.kq, p.box_rows, false) &&
-               (L.vq ? make_box_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows, true) : make_map(&p.tv, L.v_cache, L, L.Dv, 0, p.box_rows));
+        return make_rows_map(&p.tk, L.k_cache, L, L.Dkv, L.kq, p.box_rows) &&
+               make_rows_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows);
       })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
   p.vslabs = pl.vslabs;
   p.kslabs = pl.kslabs;
+  p.kslab0 = pl.kslab0;
   p.ns = pl.ns;
   p.stage_bytes = pl.stage;
+  p.off_staging = pl.off_staging;
   p.off_p = pl.off_p;
   p.off_misc = pl.off_misc;
   p.whole = pl.whole;

@@ -568,6 +568,28 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         // of box_rows keys per trip to the block table.
         int64_t row = -1;
         int32_t base = w.ta * groups - per_trip;
+        // the queries, once the products of the last ones are through with them
+        auto load_q = [&] {
+          for (int i = 0; ok && i < 2; ++i) {
+            if (w.n(i) == 0) continue;
+            ok = bounded_wait_warp(smem_u32(&ms.q_empty[i]), q_par[i] ^ 1u, p.wait_ns, abort_flag);
+            if (!ok) break;
+            if (elect_one()) {
+              const uint32_t bar = smem_u32(&ms.q_full[i]);
+              const int32_t tok = w.q_start + w.tok + i * p.join.tb;
+              mbar_arrive_expect_tx(bar, KS * p.join.tb * p.join.hb * 128);
+#pragma unroll
+              for (int c = 0; c < KS; ++c)
+                tma_load_3d(s0 + i * SH::kQTile + c * kTileRows * 128, &p.tq, bar, 64 * c, p.q_swap ? tok : w.head,
+                            p.q_swap ? w.head : tok);
+            }
+            __syncwarp();
+            mark(armed_q, par_q, i, q_par[i]);
+            q_par[i] ^= 1u;
+          }
+        };
+        // A block's first queries go first: with codes their scaling stands before the first product.
+        if (EXT && w.first) load_q();
         for (int32_t t = w.ta; ok && t < t_end; ++t, ++u) {
           uint32_t have = 1;                // which of the tile's groups exist
           if (PAGED) {
@@ -602,26 +624,9 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
           // 0: the key tile, 1: the value tile
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
-            if (side == 1 && t == w.ta) {
-              // the queries, once the products of the last ones are through with them: behind the
-              // first key tile, whose place in the ring is free earlier
-              for (int i = 0; ok && i < 2; ++i) {
-                if (w.n(i) == 0) continue;
-                ok = bounded_wait_warp(smem_u32(&ms.q_empty[i]), q_par[i] ^ 1u, p.wait_ns, abort_flag);
-                if (!ok) break;
-                if (elect_one()) {
-                  const uint32_t bar = smem_u32(&ms.q_full[i]);
-                  const int32_t tok = w.q_start + w.tok + i * p.join.tb;
-                  mbar_arrive_expect_tx(bar, KS * p.join.tb * p.join.hb * 128);
-      #pragma unroll
-                  for (int c = 0; c < KS; ++c)
-                    tma_load_3d(s0 + i * SH::kQTile + c * kTileRows * 128, &p.tq, bar, 64 * c, p.q_swap ? tok : w.head,
-                                p.q_swap ? w.head : tok);
-                }
-                __syncwarp();
-                mark(armed_q, par_q, i, q_par[i]);
-                q_par[i] ^= 1u;
-              }
+            if (side == 1 && t == w.ta && !(EXT && w.first)) {
+              // behind the first key tile, whose place in the ring is free earlier
+              load_q();
               if (!ok) break;
             }
             const int st = side ? vr.stage : kr.stage;
@@ -883,7 +888,8 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         auto at = [&](int c) { return mine_row + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4); };
         uint32_t big = 0;  // |q| as bits orders like the value in either type
         const int nck = p.Dk / 8;
-#pragma unroll 2
+        constexpr int kAtOnce = EXT ? 8 : 2;  // loads on their way (a row's two passes: 6.5k cycles with two, XX with eight)
+#pragma unroll kAtOnce
         for (int c = 0; c < nck; ++c) {
           const uint4 x = *reinterpret_cast<const uint4*>(at(c));
           big = __vmaxu2(__vmaxu2(big, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
@@ -904,7 +910,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               shift -= tile_half<F16>((z4[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) / __ldg(ks + 8 * c + e) * __ldg(ko + 8 * c + e) * p.scale;
           }
         }
-#pragma unroll 2
+#pragma unroll kAtOnce
         for (int c = 0; c < nck; ++c) {
           const uint4 z = *reinterpret_cast<const uint4*>(at(c));
           const float4 a = *reinterpret_cast<const float4*>(inv + 8 * c), b = *reinterpret_cast<const float4*>(inv + 8 * c + 4);
