@@ -1,5 +1,6 @@
 // C-ABI entry points of librope_attention.so (declared in include/rope_attention.h).
 // Host-side validation happens here, before anything is launched.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cmath>
@@ -498,8 +499,19 @@ ra::PagedLaunch over_prefix(const ra::PagedLaunch& L, const attention_prefix* x)
   return P;
 }
 
+// the one call with the prefix ahead of every sequence's own positions
+ra::PagedLaunch behind_prefix(const ra::PagedLaunch& L, const attention_prefix* x, const int32_t* len, const int32_t* table) {
+  ra::PagedLaunch C = L;
+  C.prefix_len = len;
+  C.prefix_table = table;
+  C.prefix_entries = x->table_entries;
+  C.max_prefix_len = x->max_prefix_len;
+  return C;
+}
+
 // The workspace of paged_prefix_attention: the header and the parts of the call over the prefix, the
-// other call's, the fp32 rows that go from one to the other, and their statistics.
+// other call's, the fp32 rows that go from one to the other, and their statistics; or the one
+// call's parts.
 struct PrefixPlan {
   size_t partials, rows, stats, bytes;
 };
@@ -509,14 +521,15 @@ uint8_t* aligned_in(uint8_t* ws, size_t at) {  // the step from any 16 bytes to 
 }
 PrefixPlan prefix_plan(const ra::PagedLaunch& L, const attention_prefix* x) {
   const size_t rows = static_cast<size_t>(L.total_q) * L.heads;
+  static const int32_t given = 0;              // sizes alone: the pointers are not looked at
   PrefixPlan p;
   p.partials = next_256(ra::paged_attention_workspace(over_prefix(L, x)));
-  p.rows = p.partials + next_256(ra::paged_attention_workspace(L) - ra::kAttnHeader);
+  p.rows = std::max(p.partials + next_256(ra::paged_attention_workspace(L) - ra::kAttnHeader),
+                    next_256(ra::paged_attention_workspace(behind_prefix(L, x, &given, &given))));
   p.stats = p.rows + next_256(rows * L.Dv * sizeof(float) + 32);
   p.bytes = p.stats + next_256(rows * sizeof(float2) + 32);
   return p;
 }
-
 }  // namespace
 
 namespace ra {
@@ -993,7 +1006,9 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
     L.window = w->window;
     L.sinks = w->sinks;
   }
-  if (x) {
+  if (x && !ra::prefix_is_shared(over_prefix(L, x), behind_prefix(L, x, prefix_len, prefix_table))) {
+    L = behind_prefix(L, x, prefix_len, prefix_table);
+  } else if (x) {
     // the prefix's keys for the rows of all sequences, then each sequence's own, which join those
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     ra::PagedLaunch P = over_prefix(L, x);

@@ -46,7 +46,8 @@ struct PagedLaunch {
   int32_t k_scalar, v_scalar;
   int32_t causal;
   int64_t window, sinks;       // as above
-  // Two calls make one over a shared prefix.  The first, over the prefix, takes the tokens of all
+  // A shared prefix, in one of two ways.  One call has it ahead of every sequence's own positions
+  // (prefix_len and so on), or two calls make one: the first, over the prefix, takes the tokens of all
   // sequences for one's (cu_step: cu_q[0] .. cu_q[cu_step]) and leaves its rows in fp32 (rows_out)
   // with their statistics; the second joins its own with those (prior).
   int32_t cu_step;             // entries of cu_q to a sequence's end: 1 but in the first call
@@ -55,6 +56,8 @@ struct PagedLaunch {
   const float* prior;
   const float2* prior_stats;
   int32_t shifts;              // the second call writes the lse: that share is wanted
+  const int32_t *prefix_len, *prefix_table;
+  int64_t prefix_entries, max_prefix_len;
   float scale;
   int64_t max_seq_len;
   int32_t* status;
@@ -67,10 +70,14 @@ size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
 // with a window, rows_out or prior
 cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
+// Whether the two calls cost less than the one: `over` is the first of the two, `behind` the one.
+bool prefix_is_shared(const PagedLaunch& over, const PagedLaunch& behind);
 // The kernel for many rows per sequence and kv head (paged_tile.cuh): whether it takes the
 // call, its part of the workspace, and the launch.
 bool paged_tile_serves(const PagedLaunch& L);
 size_t paged_tile_workspace(const PagedLaunch& L);
+int64_t paged_tile_items(const PagedLaunch& L);   // at most, and the keys of a tile
+int paged_tile_keys(const PagedLaunch& L);
 cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why);
 cudaError_t launch_paged_tile_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
 

@@ -63,6 +63,14 @@ inline Window make_window(int64_t window, int64_t sinks, int64_t tokens, int64_t
   return w;
 }
 
+// A prefix whose positions stand before every sequence's own, in tiles of their own: the other way to
+// serve one, in a single call without sharing its reads.
+struct SharedPrefix {
+  const int32_t *len, *table;               // null: none
+  int32_t cap;                              // positions that it can have
+};
+__device__ __forceinline__ int32_t prefix_length(const SharedPrefix& x) { return x.len ? min(max(__ldg(x.len), 0), x.cap) : 0; }
+
 // Rows that another call's rows join (attention.h, PagedLaunch): its results in fp32, with log2 of
 // their sums of exponentials and the lse's share of the key offsets.
 struct Prior {

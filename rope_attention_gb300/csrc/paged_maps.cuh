@@ -2,6 +2,7 @@
 #pragma once
 
 #include "attention.h"
+#include "attn_join.cuh"
 #include "internal.h"
 #include "kv_cache.h"
 
@@ -25,6 +26,12 @@ inline bool make_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline SharedPrefix shared_prefix(const PagedLaunch& L) {
+  if (!L.prefix_len) return SharedPrefix{};
+  return SharedPrefix{L.prefix_len, L.prefix_table,
+                      static_cast<int32_t>(std::min<int64_t>(L.prefix_entries * L.block_size, L.max_prefix_len))};
 }
 
 // q as (channels, heads, tokens), boxes of one row tile's 64 channels

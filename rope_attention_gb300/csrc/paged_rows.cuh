@@ -112,6 +112,7 @@ struct Params {
   // EXT
   Window window;
   int32_t cu_step, shifts;
+  SharedPrefix prefix;
   const uint16_t* q;            // paged_tokens.cu, which does without tq
 };
 
@@ -148,10 +149,10 @@ __device__ __forceinline__ void q_span(const Params& p, int32_t b, int32_t& star
   start = lo;
   len = hi - lo;
 }
-// tiles of a sequence in the line
+// tiles of a sequence in the line, `ahead` those of a prefix
 template <bool EXT>
-__device__ __forceinline__ int32_t tiles_of(const Params& p, int32_t len) {
-  const int32_t tiles = max(1, (len + kKeys - 1) / kKeys);
+__device__ __forceinline__ int32_t tiles_of(const Params& p, int32_t len, int32_t ahead) {
+  const int32_t tiles = max(1, (len + kKeys - 1) / kKeys + (EXT ? ahead : 0));
   return EXT ? min(tiles, p.window.most) : tiles;
 }
 // row tiles of lq tokens and one kv head (lq * heads < 2^31)
@@ -160,8 +161,8 @@ __device__ __forceinline__ int32_t row_tiles_of(const Params& p, int32_t lq) {
 }
 // what a sequence counts for in the line: its items' tiles, or its items
 template <bool EXT>
-__device__ __forceinline__ int64_t seq_work(const Params& p, int32_t lq, int32_t len) {
-  return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * (p.whole ? 1 : tiles_of<EXT>(p, len));
+__device__ __forceinline__ int64_t seq_work(const Params& p, int32_t lq, int32_t len, int32_t ahead) {
+  return static_cast<int64_t>(row_tiles_of(p, lq)) * p.N * (p.whole ? 1 : tiles_of<EXT>(p, len, ahead));
 }
 
 // The spans of 32 sequences, one to a lane: a walk over them waits for memory once.
@@ -184,11 +185,16 @@ struct Piece {
   int32_t b, n, tok, head, rows, q_start, Lq, len;  // the tile's first token (of its sequence) and head
   int32_t t0, take, T;          // nominal tiles: [t0, t0 + take) of T
   int32_t ta, tb;               // those that any of its rows sees
-  int32_t skip, from;           // EXT: positions that tiles behind the sinks' lie further; the first row's window
+  // EXT: tiles of the sinks or the prefix, and how much further the others' positions are; the first row's
+  // window; positions of the prefix, whose tiles are those ahead
+  int32_t ahead, skip, from, prefix;
   template <bool EXT>
-  __device__ __forceinline__ int32_t pos(const Params& p, int32_t t) const {  // the first position of tile t
-    return t * kKeys + (EXT && t >= p.window.tiles ? skip : 0);
+  __device__ __forceinline__ int32_t pos(int32_t t) const {  // the first position of tile t
+    return t * kKeys + (EXT && t >= ahead ? skip : 0);
   }
+  // where the keys that tile t counts end; `seen` stands for the sequence's own
+  template <bool EXT>
+  __device__ __forceinline__ int32_t end_of(int32_t t, int32_t seen) const { return EXT && prefix > 0 && t < ahead ? prefix : seen; }
   __device__ bool whole() const { return take == T; }
 };
 // Walks the pieces of a run of tiles (p.whole: of items), a whole warp at once.
@@ -196,14 +202,16 @@ template <bool EXT>
 struct Walker {
   int32_t b;
   int64_t off, rem;             // position inside sequence b, tiles left
+  int32_t prefix;               // EXT: positions ahead of every sequence's own
   Spans<EXT> spans;
+  __device__ __forceinline__ int32_t ahead() const { return (prefix + kKeys - 1) / kKeys; }
   __device__ bool next(const Params& p, Piece& w) {
     while (rem > 0 && b < p.B) {
       if (b >= spans.base + 32) spans.load(p, b);
       const int32_t qs = __shfl_sync(0xffffffffu, spans.start, b - spans.base);
       const int32_t lq = __shfl_sync(0xffffffffu, spans.lq, b - spans.base);
       const int32_t len = __shfl_sync(0xffffffffu, spans.len, b - spans.base);
-      const int32_t T = tiles_of<EXT>(p, len), each = p.whole ? 1 : T;
+      const int32_t T = tiles_of<EXT>(p, len, ahead()), each = p.whole ? 1 : T;
       const int32_t rts = row_tiles_of(p, lq);
       const int64_t work = static_cast<int64_t>(rts) * p.N * each;
       if (off >= work) {
@@ -235,10 +243,12 @@ struct Walker {
       const int32_t last = p.hblocks > 1 ? w.tok : min(w.tok + p.tb, lq) - 1;
       const int32_t seen = p.causal ? min(len, max(0, len - lq + last + 1)) : len;
       int32_t vt = (seen + kKeys - 1) / kKeys;
-      w.skip = w.from = 0;
+      w.ahead = w.skip = w.from = w.prefix = 0;
       if constexpr (EXT) {
+        w.prefix = prefix;
         w.from = window_from(p.window, len - lq + w.tok);
-        const int32_t skip = max(0, w.from / kKeys - p.window.tiles);
+        w.ahead = p.prefix.len ? ahead() : p.window.tiles;
+        const int32_t skip = p.prefix.len ? -w.ahead : max(0, w.from / kKeys - w.ahead);
         w.skip = skip * kKeys;
         vt = max(0, vt - skip);
       }
@@ -261,12 +271,13 @@ __device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, Run
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   walk.b = p.B;
   walk.off = 0;
+  walk.prefix = EXT ? prefix_length(p.prefix) : 0;
   walk.spans.load(p, 0);
   const bool few = p.B <= 32;
   int64_t mine = 0;
   int32_t b_lo = lane, b_hi = lane;
   if (few) {
-    mine = seq_work<EXT>(p, walk.spans.lq, walk.spans.len);
+    mine = seq_work<EXT>(p, walk.spans.lq, walk.spans.len, walk.ahead());
   } else {
     const int32_t chunk = (p.B + THREADS - 1) / THREADS;
     b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
@@ -274,7 +285,7 @@ __device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, Run
     for (int32_t b = b_lo; b < b_hi; ++b) {
       int32_t qs, lq;
       q_span<EXT>(p, b, qs, lq);
-      mine += seq_work<EXT>(p, lq, seq_len_of(p, b));
+      mine += seq_work<EXT>(p, lq, seq_len_of(p, b), walk.ahead());
     }
   }
   int64_t incl = mine;
@@ -314,7 +325,7 @@ __device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, Run
     for (; b < b_hi; ++b) {
       int32_t qs, lq;
       q_span<EXT>(p, b, qs, lq);
-      const int64_t w = seq_work<EXT>(p, lq, seq_len_of(p, b));
+      const int64_t w = seq_work<EXT>(p, lq, seq_len_of(p, b), walk.ahead());
       if (off < w) break;
       off -= w;
     }
@@ -542,18 +553,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           base += 32;
           int32_t pos = (base + lane) << p.box_shift;
           bool hidden = false;              // a group that no row of the tile sees: its page may be gone
+          const bool own = !EXT || base + lane >= w.ahead * groups;
           if constexpr (EXT) {
-            if (base + lane >= p.window.tiles * groups) pos += w.skip;
+            if (own) pos += w.skip;
             hidden = pos + p.box_rows <= w.from && pos >= p.window.sinks;
           }
           row = -1;
-          if (base + lane < g_end && pos < w.len && !hidden) {
+          if (base + lane < g_end && pos < (EXT && !own && w.prefix > 0 ? w.prefix : w.len) && !hidden) {
             if (p.mode == kModeNorm) {
               row = (static_cast<int64_t>(w.b) * p.N + w.n) * p.cache_seq + pos;
             } else {
               const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
               const int32_t in = pos - pg * p.block_size;
-              const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
+              const int32_t* table = EXT && !own && w.prefix > 0 ? p.prefix.table : p.table + w.b * p.table_stride;
+              const int64_t page = __ldg(table + pg);
               if (page >= 0 && page < p.block_num)
                 row = p.mode == kModePa ? page * p.block_size + in : (page * p.N + w.n) * p.block_size + in;
               else if (p.err_count)
@@ -588,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           at[i] = -1;
           if (i < groups) {
             at[i] = __shfl_sync(0xffffffffu, static_cast<int32_t>(row), t * groups - base + i);
-            const int32_t have = min(p.box_rows, w.len - (w.template pos<EXT>(p, t) + (i << p.box_shift)));
+            const int32_t have = min(p.box_rows, w.template end_of<EXT>(t, w.len) - (w.template pos<EXT>(t) + (i << p.box_shift)));
             if (at[i] >= 0) {
               bits |= (~0ull >> (64 - have)) << (i << p.box_shift);
               ++live;
@@ -834,8 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (ok && rows_here) {
           tmem_ld_x32(tmem + lane_base + (u & 1) * kKeys + col0, s);
           tmem_ld_wait();
-          const int32_t pos0 = w.template pos<EXT>(p, w.ta + j) + col0;
-          const int32_t nv = seen - pos0;            // keys of these 32 that the row sees
+          const int32_t pos0 = w.template pos<EXT>(w.ta + j) + col0;
+          const int32_t nv = w.template end_of<EXT>(w.ta + j, seen) - pos0;  // keys of these 32 that the row sees
           uint32_t mask = static_cast<uint32_t>(valid >> col0);
           if (nv < 32) mask &= nv <= 0 ? 0u : (1u << nv) - 1;
           if constexpr (EXT) {
@@ -1031,7 +1044,8 @@ void share_out(const PagedLaunch& L, Plan* pl) {
   if (pl->hblocks > 1) pl->tb = 1;
   const int64_t rts = pl->hblocks > 1 ? L.total_q * pl->hblocks : std::min<int64_t>(L.total_q, L.total_q / pl->tb + L.B);
   pl->items = rts * L.N;
-  const int64_t all = std::max<int64_t>(1, (L.max_seq_len + kKeys - 1) / kKeys);
+  const int64_t ahead = L.prefix_len ? (L.max_prefix_len + kKeys - 1) / kKeys : 0;
+  const int64_t all = std::max<int64_t>(1, ahead + (L.max_seq_len + kKeys - 1) / kKeys);
   pl->window = make_window(L.window, L.sinks, pl->tb, kKeys);
   const int64_t T = std::min<int64_t>(all, pl->window.most);
   const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
@@ -1171,6 +1185,7 @@ Params row_params(const PagedLaunch& L, const Plan& pl) {
   p.window = pl.window;
   p.cu_step = L.cu_step;
   p.shifts = L.shifts;
+  p.prefix = shared_prefix(L);
   p.join.prior = Prior{L.rows_out, L.stats_out, L.prior, L.prior_stats};
   return p;
 }

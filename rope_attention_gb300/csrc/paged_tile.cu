@@ -16,6 +16,9 @@ bool paged_tile_serves(const PagedLaunch& L) {
          L.total_q * g > kRows * L.B;
 }
 
+int64_t paged_tile_items(const PagedLaunch& L) { return most_items(L); }
+int paged_tile_keys(const PagedLaunch& L) { return keys_per_tile(L); }
+
 size_t paged_tile_workspace(const PagedLaunch& L) { return join_bytes(most_blocks(L), 2 * kTileRows, L.Dv); }
 
 cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why) {

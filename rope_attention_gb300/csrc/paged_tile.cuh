@@ -23,7 +23,8 @@ int64_t most_items(const PagedLaunch& L) {
 }
 int most_blocks(const PagedLaunch& L) {
   const int keys = keys_per_tile(L);
-  return tile_blocks(most_items(L), std::max<int64_t>(1, (L.max_seq_len + keys - 1) / keys));
+  const int64_t ahead = L.prefix_len ? (L.max_prefix_len + keys - 1) / keys : 0;
+  return tile_blocks(most_items(L), std::max<int64_t>(1, ahead + (L.max_seq_len + keys - 1) / keys));
 }
 
 template <bool EXT>
@@ -82,6 +83,7 @@ cudaError_t launch_tile_over_pages(const PagedLaunch& L, cudaStream_t stream, co
   p.window = make_window(L.window, L.sinks, 2 * p.join.tb, keys);
   p.cu_step = L.cu_step;
   p.shifts = L.shifts;
+  p.prefix = shared_prefix(L);
   p.join.prior = Prior{L.rows_out, L.stats_out, L.prior, L.prior_stats};
   if (!encode_maps([&] {
         return make_q_map(&p.tq, L, p.join.hb, p.join.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&

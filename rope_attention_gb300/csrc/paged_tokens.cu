@@ -21,39 +21,10 @@
 // The runs of tiles, their parts and the join are paged_rows.cuh's.  The maximum follows only when a
 // tile exceeds it by 2^kLazy.  Every wait on an mbarrier is bounded in time (status word); the warps meet
 // at the end of a piece and leave it, or the loop, together.
-#include "paged_rows.cuh"
+#include "paged_tokens.cuh"
 
 namespace ra {
 namespace {
-
-// Two teams of four warps compute; of a third warpgroup, whose registers they take (2 x 208 + 88 = 3 x 168),
-// one warp loads tiles and one prepares pieces.  (Three teams, for 8 rows: no gain.)
-constexpr int kTokenWarps = 8, kTileWarps = 4, kTeams = kTokenWarps / kTileWarps, kTokenThreads = 32 * kTokenWarps + 128;
-constexpr int kTokenLoad = kTokenWarps, kTokenPieces = kTokenWarps + 1;
-constexpr int kRegsCompute = 208, kRegsOther = 88;
-constexpr int kTokenStages = 12;          // at most
-constexpr int kTokenRow = 132;            // floats of a row where the warps' results meet
-constexpr int kTokenDk = 192, kTokenDv = 128;
-
-// A piece as its warp hands it over.
-struct TokenPiece {
-  int32_t end;                            // there is no further piece
-  int32_t rows, kv_head, ta, n, skip, whole;
-  int32_t slot;                           // of its part
-  int32_t seen_least, from_most;
-  int32_t seen[16], from[16];             // what each row sees: positions below, and from its window on
-  int2 row[16];                           // token and head
-  float row_scale[16], row_const[16];     // of the scores; the lse's share of the key offsets
-};
-struct TokenMisc {
-  uint64_t full[kTokenStages], empty[kTokenStages];
-  uint64_t piece_full[2], piece_empty[2];
-  uint64_t valid[kValidRing];
-  RunScan<kTokenThreads> run;
-  float2 stats[kTokenWarps][16];          // (max, sum) of each warp's rows
-  TokenPiece pieces[2];
-  int32_t abort;
-};
 
 __device__ __forceinline__ uint4 lds_128(uint32_t addr) {
   uint4 v;
@@ -254,7 +225,9 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
           to.kv_head = w.n;
           to.ta = w.ta;
           to.n = max(0, w.tb - w.ta);
+          to.ahead = w.ahead;
           to.skip = w.skip;
+          to.prefix = w.prefix;
           to.whole = w.whole();
           to.slot = 2 * static_cast<int32_t>(blockIdx.x) + (began ? 0 : 1);
           to.seen_least = seen_least;
@@ -286,17 +259,18 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
       for (int32_t t = w.ta; t < w.tb; ++t, ++u) {
         if (t * groups >= base + 32) {
           base += 32;
-          int32_t pos = (base + lane) << p.box_shift;
-          if (base + lane >= p.window.tiles * groups) pos += w.skip;
+          const bool own = base + lane >= w.ahead * groups;
+          const int32_t pos = ((base + lane) << p.box_shift) + (own ? w.skip : 0);
           const bool hidden = pos + p.box_rows <= w.from && pos >= p.window.sinks;  // no row sees any: its page may be gone
           row = -1;
-          if (base + lane < g_end && pos < w.len && !hidden) {
+          if (base + lane < g_end && pos < (!own && w.prefix > 0 ? w.prefix : w.len) && !hidden) {
             if (p.mode == kModeNorm) {
               row = (static_cast<int64_t>(w.b) * p.N + w.n) * p.cache_seq + pos;
             } else {
               const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
               const int32_t in = pos - pg * p.block_size;
-              const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
+              const int32_t* table = !own && w.prefix > 0 ? p.prefix.table : p.table + w.b * p.table_stride;
+              const int64_t page = __ldg(table + pg);
               if (page >= 0 && page < p.block_num)
                 row = p.mode == kModePa ? page * p.block_size + in : (page * p.N + w.n) * p.block_size + in;
               else if (p.err_count)
@@ -315,7 +289,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
           at[i] = -1;
           if (i < groups) {
             at[i] = __shfl_sync(0xffffffffu, static_cast<int32_t>(row), t * groups - base + i);
-            const int32_t have = min(p.box_rows, w.len - (w.template pos<true>(p, t) + (i << p.box_shift)));
+            const int32_t have = min(p.box_rows, w.template end_of<true>(t, w.len) - (w.template pos<true>(t) + (i << p.box_shift)));
             if (at[i] >= 0) {
               bits |= (~0ull >> (64 - have)) << (i << p.box_shift);
               ++live;
@@ -385,7 +359,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
       }
       const TokenPiece& w = ms.pieces[pieces.stage];
       if (w.end) break;
-      const int32_t n = w.n, ta = w.ta, skip = w.skip;
+      const int32_t n = w.n, ta = w.ta, ahead = w.ahead, skip = w.skip;
       // the rows of another call that this one's join: on their way from here
       float4 prior[NT];
       float2 prior_stats[NT];
@@ -470,9 +444,10 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
           }
         }
         // ---- what the rows see
-        const int32_t pos0 = (ta + j) * kKeys + (ta + j >= p.window.tiles ? skip : 0);
+        const int32_t pos0 = (ta + j) * kKeys + (ta + j >= ahead ? skip : 0);
+        const int32_t shared = ta + j < ahead ? w.prefix : 0;  // of a tile of the prefix: where that ends
         const uint32_t valid = static_cast<uint32_t>(ms.valid[u % kValidRing] >> (16 * quarter)) & 0xFFFFu;
-        const bool edge = valid != 0xFFFFu || pos0 + kKeys > w.seen_least || (w.from_most > pos0 && pos0 + kKeys > p.window.sinks);
+        const bool edge = valid != 0xFFFFu || pos0 + kKeys > (shared > 0 ? shared : w.seen_least) || (w.from_most > pos0 && pos0 + kKeys > p.window.sinks);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -488,7 +463,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
               for (int e = 0; e < 2; ++e)
               {
                 const int r = 8 * nt + 2 * t + e;
-                if (!there || pos >= w.seen[r] || (pos < w.from[r] && pos >= p.window.sinks)) s[0][nt][2 * h + e] = neg_inf();
+                if (!there || pos >= (shared > 0 ? shared : w.seen[r]) || (pos < w.from[r] && pos >= p.window.sinks)) s[0][nt][2 * h + e] = neg_inf();
               }
           }
         }
@@ -681,26 +656,6 @@ bool make_rows_map(CUtensorMap* m, const void* base, const PagedLaunch& L, int32
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-void plan_tokens(const PagedLaunch& L, Plan* pl) {
-  const int g = L.heads / static_cast<int32_t>(L.N);
-  pl->NR = (L.total_q + L.B - 1) / L.B * g <= 8 ? 8 : 16;
-  // a stage: the value rows, then the key rows, each on 1024 bytes (the swizzle's period); codes count as one slab
-  const auto bytes = [](int quant, int width) { return quant ? (kKeys * width + 1023) / 1024 * 1024 : (width + 63) / 64 * kSlab; };
-  pl->vslabs = L.vq ? 1 : (L.Dv + 63) / 64;
-  pl->kslabs = L.kq ? 1 : (L.Dkv + 63) / 64;
-  pl->kslab0 = L.kq && L.Dkv == 128;            // whether codes of keys are swizzled
-  pl->off_staging = bytes(L.vq, L.Dv);          // of the keys in a stage
-  pl->stage = pl->off_staging + bytes(L.kq, L.Dkv);
-  // where the warps' results meet, and two pieces' queries
-  const int meet = kTokenWarps * pl->NR * kTokenRow * 4 + 2 * pl->NR / 8 * 24 * 32 * 4;
-  const int fixed = meet + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
-  pl->ns = std::min(kTokenStages, (kSmemMax - fixed) / pl->stage);
-  pl->off_p = pl->ns * pl->stage;
-  pl->off_misc = pl->off_p + meet;
-  pl->smem = pl->off_misc + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
-  share_out(L, pl);
 }
 
 template <bool F16, bool KQ, bool VQ>

@@ -84,6 +84,7 @@ struct TileParams {
   // EXT
   Window window;
   int32_t cu_step, shifts;
+  SharedPrefix prefix;
 };
 
 // KS, VS: 64-channel slabs of a key and a value; KT: keys per tile; QUANT: both caches hold
@@ -147,12 +148,17 @@ struct TilePiece {
   int32_t t0, take, T;                      // tiles [t0, t0 + take) of the item's T in the line
   int32_t ta, tb[2];                        // those that a row of either tile sees: [ta, tb[i])
   int32_t from, to;                         // blocks that share the item, where the block before began it
-  int32_t skip, win;                        // EXT: positions that tiles behind the sinks' lie further; the first row's window
+  int32_t ahead, skip, win;                 // EXT: tiles of the sinks or the prefix, and how much further the others' positions
+                                            // are; the first row's window
+  int32_t prefix;                           // positions of the prefix, whose tiles are those ahead
   __device__ __forceinline__ bool whole() const { return take == T; }
   __device__ __forceinline__ int32_t n(int i) const { return max(0, tb[i] - ta); }
   // the first position of tile t
   template <int KT, bool EXT>
-  __device__ __forceinline__ int32_t pos(const Window& w, int32_t t) const { return t * KT + (EXT && t >= w.tiles ? skip : 0); }
+  __device__ __forceinline__ int32_t pos(int32_t t) const { return t * KT + (EXT && t >= ahead ? skip : 0); }
+  // where the keys that tile t counts end; `seen` stands for the sequence's own
+  template <bool EXT>
+  __device__ __forceinline__ int32_t end_of(int32_t t, int32_t seen) const { return EXT && prefix > 0 && t < ahead ? prefix : seen; }
 };
 
 struct TileMisc {
@@ -180,6 +186,7 @@ __device__ __forceinline__ int64_t tile_quotient(int64_t a, int64_t b) {
 template <int KT, bool PAGED, bool EXT>
 struct TileSpans {
   int32_t base, q_start, Lq, k_start, Lk;
+  int32_t prefix;                           // EXT, PAGED: positions ahead of every sequence's own
   __device__ void one(const TileParams& p, int32_t b) {
     tile_span(p.cu_q, b, p.B, p.total_q, q_start, Lq, EXT ? p.cu_step : 1);
     if (PAGED) {
@@ -189,17 +196,20 @@ struct TileSpans {
       tile_span(p.cu_k, b, p.B, p.total_k, k_start, Lk);
     }
   }
+  __device__ void load_prefix(const TileParams& p) {
+    prefix = EXT && PAGED ? prefix_length(p.prefix) : 0;
+  }
   __device__ void load(const TileParams& p, int32_t from) {
     base = from;
     const int32_t b = from + static_cast<int32_t>(threadIdx.x & 31);
     q_start = Lq = k_start = Lk = 0;
     if (b < p.B) one(p, b);
   }
-  __device__ static TileCount count(const TileParams& p, int32_t Lq, int32_t Lk) {
+  __device__ TileCount count(const TileParams& p, int32_t Lq, int32_t Lk) const {
     const int32_t tokens = 2 * p.join.tb;
     TileCount c;
     c.blocks = static_cast<int32_t>((static_cast<uint32_t>(Lq) + tokens - 1) / static_cast<uint32_t>(tokens));
-    c.most = max(1, (Lk + KT - 1) / KT);
+    c.most = max(1, (Lk + KT - 1) / KT + (EXT && PAGED ? (prefix + KT - 1) / KT : 0));
     if (EXT) c.most = min(c.most, p.window.most);
     c.step = p.causal && !PAGED ? 2 * kTileRows / KT : 0;
     c.q0 = Lk >= Lq ? (Lk - Lq + KT - 1) / KT : -((Lq - Lk) / KT);
@@ -229,7 +239,7 @@ struct TileWalk {
     w.Lq = __shfl_sync(0xffffffffu, spans.Lq, b - spans.base);
     w.k_start = __shfl_sync(0xffffffffu, spans.k_start, b - spans.base);
     w.Lk = __shfl_sync(0xffffffffu, spans.Lk, b - spans.base);
-    return TileSpans<KT, PAGED, EXT>::count(p, w.Lq, w.Lk);
+    return spans.count(p, w.Lq, w.Lk);
   }
   // to offset `off` of sequence b, for `run` tiles
   __device__ void seek(const TileParams& p, int32_t seq, int64_t off, int64_t run, int32_t kind) {
@@ -316,10 +326,12 @@ struct TileWalk {
     w.head = PAGED ? item * p.g : item;
     w.tok = blk * 2 * p.join.tb;
     int32_t skip = 0;
-    w.skip = w.win = 0;
+    w.ahead = w.skip = w.win = w.prefix = 0;
     if constexpr (EXT) {
+      w.prefix = spans.prefix;
       w.win = window_from(p.window, w.tok + w.Lk - w.Lq);
-      skip = max(0, w.win / KT - p.window.tiles);
+      w.ahead = PAGED && p.prefix.len ? (w.prefix + KT - 1) / KT : p.window.tiles;
+      skip = PAGED && p.prefix.len ? -w.ahead : max(0, w.win / KT - w.ahead);
       w.skip = skip * KT;
     }
 #pragma unroll
@@ -435,6 +447,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   Walk walk;
   int64_t per = 0, start = 0;
   if (few ? warp == kPieceWarp : true) {
+    walk.spans.load_prefix(p);
     walk.spans.load(p, 0);
     int64_t mine = 0, items = 0;
     int32_t b_lo = lane, b_hi = lane;
@@ -445,6 +458,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       b_lo = min(p.B, static_cast<int32_t>(threadIdx.x) * chunk);
       b_hi = min(p.B, b_lo + chunk);
       TileSpans<KT, PAGED, EXT> one;
+      one.prefix = walk.spans.prefix;
       for (int32_t b = b_lo; b < b_hi; ++b) {
         one.one(p, b);
         mine += one.work(p, &items);
@@ -493,6 +507,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
     } else {
       if (here) {
         TileSpans<KT, PAGED, EXT> one;
+        one.prefix = walk.spans.prefix;
         int32_t b = b_lo;
         int64_t off = start - before, unused = 0;
         for (; b < b_hi; ++b) {
@@ -597,18 +612,20 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               base += per_trip;
               int32_t pos = (base + lane) << p.box_shift;
               bool hidden = false;          // a group that no row sees: its page may be gone
+              const bool own = !EXT || base + lane >= w.ahead * groups;
               if constexpr (EXT) {
-                if (base + lane >= p.window.tiles * groups) pos += w.skip;
+                if (own) pos += w.skip;
                 hidden = pos + p.box_rows <= w.win && pos >= p.window.sinks;
               }
               row = -1;
-              if (lane < per_trip && base + lane < t_end * groups && pos < w.Lk && !hidden) {
+              if (lane < per_trip && base + lane < t_end * groups && pos < (EXT && !own && w.prefix > 0 ? w.prefix : w.Lk) && !hidden) {
                 if (p.mode == kModeNorm) {
                   row = (static_cast<int64_t>(w.b) * p.items + w.kv_head) * p.cache_seq + pos;
                 } else {
                   const int32_t pg = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.block_size;
                   const int32_t in = pos - pg * p.block_size;
-                  const int64_t page = __ldg(p.table + w.b * p.table_stride + pg);
+                  const int32_t* table = EXT && !own && w.prefix > 0 ? p.prefix.table : p.table + w.b * p.table_stride;
+                  const int64_t page = __ldg(table + pg);
                   if (page >= 0 && page < p.block_num)
                     row = p.mode == kModePa ? page * p.block_size + in : (page * p.items + w.kv_head) * p.block_size + in;
                   else if (p.err_count)
@@ -619,7 +636,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             have = (__ballot_sync(0xffffffffu, row >= 0) >> (t * groups - base)) & ((1u << groups) - 1);
           }
           const uint32_t live = __popc(have);
-          const int32_t pos0 = w.template pos<KT, EXT>(p.window, t);
+          const int32_t pos0 = w.template pos<KT, EXT>(t), end = w.template end_of<EXT>(t, w.Lk);
           const int32_t y = PAGED ? (p.mode == kModePa ? w.kv_head : 0) : w.kv_head;
           // 0: the key tile, 1: the value tile
 #pragma unroll
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             if (side == 0 && PAGED) {
               uint64_t lo = 0, hi = 0;      // which of the tile's keys exist
               for (int g = 0; g < groups; ++g) {
-                const int32_t at = g << p.box_shift, keys = min(p.box_rows, w.Lk - (pos0 + at));
+                const int32_t at = g << p.box_shift, keys = min(p.box_rows, end - (pos0 + at));
                 if (!((have >> g) & 1)) continue;
                 const uint64_t bits = keys >= 64 ? ~0ull : (1ull << keys) - 1;
                 if (at < 64) lo |= bits << at;
@@ -655,7 +672,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               if (lane == 0) {
                 ms.valid[u % kTileValid][0] = lo;
                 ms.valid[u % kTileValid][1] = hi;
-                ms.holes[u % kTileValid] = live != min(groups, (w.Lk - pos0 + p.box_rows - 1) >> p.box_shift);
+                ms.holes[u % kTileValid] = live != min(groups, (end - pos0 + p.box_rows - 1) >> p.box_shift);
               }
               __syncwarp();
             }
@@ -888,8 +905,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         auto at = [&](int c) { return mine_row + (c >> 3) * kTileRows * 128 + (((c & 7) ^ (row & 7)) << 4); };
         uint32_t big = 0;  // |q| as bits orders like the value in either type
         const int nck = p.Dk / 8;
-        constexpr int kAtOnce = EXT ? 8 : 2;  // loads on their way (a row's two passes: 6.5k cycles with two, XX with eight)
-#pragma unroll kAtOnce
+#pragma unroll 2
         for (int c = 0; c < nck; ++c) {
           const uint4 x = *reinterpret_cast<const uint4*>(at(c));
           big = __vmaxu2(__vmaxu2(big, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
@@ -910,7 +926,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
               shift -= tile_half<F16>((z4[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) / __ldg(ks + 8 * c + e) * __ldg(ko + 8 * c + e) * p.scale;
           }
         }
-#pragma unroll kAtOnce
+#pragma unroll 2
         for (int c = 0; c < nck; ++c) {
           const uint4 z = *reinterpret_cast<const uint4*>(at(c));
           const float4 a = *reinterpret_cast<const float4*>(inv + 8 * c), b = *reinterpret_cast<const float4*>(inv + 8 * c + 4);
@@ -935,12 +951,12 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         s_par ^= 1u;
         tc_fence_after();
-        const int32_t pos0 = w.template pos<KT, EXT>(p.window, w.ta + j);
+        const int32_t pos0 = w.template pos<KT, EXT>(w.ta + j), keys_end = w.template end_of<EXT>(w.ta + j, w.Lk);
         uint32_t s[KT];
 #pragma unroll
         for (int c = 0; c < KT; c += 32) tmem_ld_x32(s_addr + c, s + c);
         tmem_ld_wait();
-        const int32_t nv = seen - pos0;  // keys of this tile that the row sees
+        const int32_t nv = w.template end_of<EXT>(w.ta + j, seen) - pos0;  // keys of this tile that the row sees
         if (__any_sync(0xffffffffu, nv < KT)) {
 #pragma unroll
           for (int c = 0; c < KT; ++c)
@@ -957,7 +973,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         const bool holes = PAGED && ms.holes[(u + j) % kTileValid] != 0;
         uint64_t gap[2] = {0, 0};           // keys before the end that do not exist (bad pages)
         if (holes) {
-          const int32_t end = w.Lk - pos0;
+          const int32_t end = keys_end - pos0;
           const uint64_t* v = ms.valid[(u + j) % kTileValid];
           gap[0] = ~v[0] & (end >= 64 ? ~0ull : (1ull << end) - 1);
           if (KT > 64) {
@@ -1006,10 +1022,10 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l += sum.x + sum.y;
-        if (!QUANT && (pos0 + KT > w.Lk || holes)) {
+        if (!QUANT && (pos0 + KT > keys_end || holes)) {
           // value rows that are no key's meet P = 0, but 0 times a stray NaN or infinity is
           // NaN: zero them in shared memory
-          const int32_t end = w.Lk - pos0;
+          const int32_t end = keys_end - pos0;
           if (!bounded_wait_warp(smem_u32(&ms.v_full[vr.stage]), vr.parity, p.wait_ns, abort_flag)) {
             tmem_st_wait();                 // of P: tensor memory is freed only behind its stores
             ok = false;

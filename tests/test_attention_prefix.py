@@ -1,6 +1,8 @@
 """paged_prefix_attention on the GPU against the fp64 oracle: prefixes around the key tiles and pages
 (none at all among them), every stored type of both variants, single tokens and chunks, sequences
-without positions or tokens of their own, bad pages, and rows outside every sequence."""
+without positions or tokens of their own, bad pages, and rows outside every sequence.  Short prefixes
+and few sequences are served by one call with the prefix ahead of each sequence, many rows behind a
+longer one by two that share its reads: the tests from `MANY` on have sizes of the second sort."""
 import numpy as np
 import pytest
 import torch
@@ -106,3 +108,49 @@ def test_a_longer_bound_and_a_wider_table_change_nothing():
     b.run()
     torch.cuda.synchronize()
     assert torch.equal(first.view(torch.int16), b.out.view(torch.int16))
+
+
+# ---------------------------------------------------------------- many rows behind one prefix
+MANY = dict(variant=2, lens=[(7 * i) % 40 for i in range(96)], news=[1] * 96, heads=16, N=8, prefix=1100)
+
+
+def tokens_of(lens, most):
+    return [min(max(n, 1), 1 + i % most) for i, n in enumerate(lens)]
+
+
+@pytest.mark.parametrize("mode", ["PA", "PA_BNSD"])
+@pytest.mark.parametrize("kt,vt", [("bf16", "bf16"), ("int8", "int8"), ("e4m3", "e5m2"), ("int8", "bf16"), ("bf16", "e4m3")])
+def test_many_sequences_share_v2(mode, kt, vt):
+    Case(21, mode=mode, kt=kt, vt=vt, tail=3, **MANY).run_and_check()
+
+
+@pytest.mark.parametrize("kt", ["bf16", "int8"])
+def test_many_sequences_share_other_widths_and_tokens(kt):
+    for dims in ((64, 64, 32), (96, 80, 32), (128, 128, 64), (256, 208, 64)):
+        case = {**MANY, "Dkv": dims[0], "Dv": dims[1], "R": dims[2], "kt": kt, "vt": kt, "news": tokens_of(MANY["lens"], 3)}
+        Case(22, **case).run_and_check()
+    # one row tile for the batch's rows of a kv head, and chunks
+    Case(23, variant=2, lens=[3, 0], news=[1, 1], heads=8, N=8, prefix=40000, kt=kt, vt=kt).run_and_check()
+    Case(24, variant=2, lens=[40] * 40, news=[18] * 40, heads=16, N=8, prefix=2000, kt=kt, vt=kt).run_and_check()
+
+
+@pytest.mark.parametrize("kt,vt", [("bf16", "bf16"), ("int8", "int8"), ("int8", "bf16"), ("bf16", "e5m2")])
+def test_many_sequences_share_v1(kt, vt):
+    lens = [(5 * i) % 30 for i in range(150)]
+    Case(25, variant=1, lens=lens, news=tokens_of(lens, 2), heads=16, Dkv=576, Dv=512, kt=kt, vt=vt, prefix=1100).run_and_check()
+
+
+def test_many_sequences_share_fp16_bad_pages_and_no_prefix_after_all():
+    for kt in ("fp16", "int8"):
+        Case(26, dtype="fp16", kt=kt, vt=kt, **MANY).run_and_check()
+    Case(27, bad_pages=[(5, 0, -1)], bad_prefix=[(2, 1 << 20), (30, -4)], **MANY).run_and_check()
+    Case(28, causal=False, given_starts=False, std=8.0, **MANY).run_and_check()
+    # sized for a long prefix, called with a short one and with none
+    c = Case(29, spare=1100, **{**MANY, "prefix": 1})
+    c.run_and_check()
+    c.prefix_len.fill_(0)
+    c.ref_args["prefix_len"] = 0
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    c.check("no prefix")
