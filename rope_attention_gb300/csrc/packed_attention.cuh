@@ -100,9 +100,18 @@ cudaError_t launch_packed(const PackedLaunch& L, cudaStream_t stream, const char
   p.cu_step = 1;
   const int n = std::min(blocks, device_sm_count());
   const int64_t items = most_items(L);
-  // equal lengths without a mask: all items count alike, and whether one is cut is known here
-  const bool cuts = L.cu_q || L.cu_k || L.causal ||
-                    tile_runs_cut(items, kTileExtra + std::max<int64_t>(1, (L.total_k / L.B + kTileRows - 1) / kTileRows), n);
+  // Equal lengths, without a mask or with one row block each: all items count alike, and whether one is
+  // cut is known here.
+  const int64_t lq = L.total_q / L.B, tiles = std::max<int64_t>(1, (L.total_k / L.B + kTileRows - 1) / kTileRows);
+  bool cuts = L.cu_q || L.cu_k || (L.causal && !(EXT && lq <= 2 * kTileRows));
+  if (!cuts) {
+    int64_t T = std::min<int64_t>(tiles, p.window.most);
+    if (L.causal) {                         // (TileCount's, of a sequence's first and only block)
+      const int64_t lk = L.total_k / L.B, q0 = lk >= lq ? (lk - lq + kTileRows - 1) / kTileRows : -((lq - lk) / kTileRows);
+      T = std::max<int64_t>(1, std::min<int64_t>(T, q0 + 2));
+    }
+    cuts = tile_runs_cut(items, kTileExtra + T, n);
+  }
   if (L.d <= 64)
     return L.f16 ? launch_tile<1, 1, 128, true, false, false, EXT>(p, n, items, cuts, stream)
                  : launch_tile<1, 1, 128, false, false, false, EXT>(p, n, items, cuts, stream);
