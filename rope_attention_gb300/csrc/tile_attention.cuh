@@ -166,7 +166,8 @@ struct TileMisc {
   uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_ready[2], o_done[2], drain;
   uint64_t piece_full[kTilePieces], piece_empty[kTilePieces];
   uint64_t valid[kTileValid][2];
-  uint32_t holes[kTileValid];               // whether a page before the sequence's end is absent
+  uint32_t holes[kTileValid];               // whether keys before the sequence's end are absent: a page is (EXT: 2), or
+                                            // no row sees them (1)
   TilePiece pieces[kTilePieces];
   int64_t scan[16], scan_items[16];
   int64_t start_off;
@@ -383,6 +384,26 @@ __device__ __forceinline__ float tile_half(uint32_t u) {
   return F16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u))) : __uint_as_float(u << 16);
 }
 
+// Hides a row's keys from nv on and those of [lo, hi), 32 columns at a time: a choice for each element only
+// where some row of the warp does not see all of them.  (A comparison and a choice for each of 128 columns,
+// on a pipe of half the rate, took 1600 cycles of a masked tile's 3200: 9001 tokens of 7 prompts in a
+// window of 1024 166 us, XX with this.)
+template <int KT>
+__device__ __forceinline__ void hide_keys(uint32_t (&s)[KT], int32_t nv, int32_t lo, int32_t hi) {
+  if (!__any_sync(0xffffffffu, nv < KT || (hi > lo && lo < KT))) return;
+#pragma unroll
+  for (int c = 0; c < KT; c += 32) {
+    uint32_t seen = nv - c >= 32 ? ~0u : nv <= c ? 0u : (1u << (nv - c)) - 1;
+    const int32_t from = max(lo - c, 0), to = min(hi - c, 32);
+    if (to > from) seen &= ~((~0u >> (32 - to)) & (~0u << from));
+    if (__any_sync(0xffffffffu, seen != ~0u)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!((seen >> e) & 1)) s[c + e] = __float_as_uint(neg_inf());
+    }
+  }
+}
+
 // F16: q and out (and 16-bit caches) are fp16; P16: P and the value operand are
 // EXT: windows; rows that leave in fp32 for another call, or join another's (Prior)
 template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED, bool EXT>
@@ -582,6 +603,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         // Cache rows: lane i holds where group `base + i` of the piece starts, per_trip groups
         // of box_rows keys per trip to the block table.
         int64_t row = -1;
+        bool hidden = false;                // EXT: no row sees the group, and its page may be gone
         int32_t base = w.ta * groups - per_trip;
         // the queries, once the products of the last ones are through with them
         auto load_q = [&] {
@@ -611,7 +633,6 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             if (t * groups >= base + per_trip) {
               base += per_trip;
               int32_t pos = (base + lane) << p.box_shift;
-              bool hidden = false;          // a group that no row sees: its page may be gone
               const bool own = !EXT || base + lane >= w.ahead * groups;
               if constexpr (EXT) {
                 if (own) pos += w.skip;
@@ -669,10 +690,14 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
                 else hi |= bits << (at - 64);
                 if (keys > 64) hi |= keys >= 128 ? ~0ull : (1ull << (keys - 64)) - 1;
               }
+              const uint32_t absent = min(groups, (end - pos0 + p.box_rows - 1) >> p.box_shift) - live;
+              uint32_t unseen = 0;
+              if constexpr (EXT)
+                unseen = __popc(__ballot_sync(0xffffffffu, hidden && lane >= t * groups - base && lane < (t + 1) * groups - base));
               if (lane == 0) {
                 ms.valid[u % kTileValid][0] = lo;
                 ms.valid[u % kTileValid][1] = hi;
-                ms.holes[u % kTileValid] = live != min(groups, (end - pos0 + p.box_rows - 1) >> p.box_shift);
+                ms.holes[u % kTileValid] = absent == 0 ? 0 : EXT && absent == unseen ? 1 : 2;
               }
               __syncwarp();
             }
@@ -957,20 +982,15 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         for (int c = 0; c < KT; c += 32) tmem_ld_x32(s_addr + c, s + c);
         tmem_ld_wait();
         const int32_t nv = w.template end_of<EXT>(w.ta + j, seen) - pos0;  // keys of this tile that the row sees
-        if (__any_sync(0xffffffffu, nv < KT)) {
+        if constexpr (EXT) {
+          hide_keys<KT>(s, nv, max(p.window.sinks - pos0, 0), from - pos0);
+        } else if (__any_sync(0xffffffffu, nv < KT)) {
 #pragma unroll
           for (int c = 0; c < KT; ++c)
             if (c >= nv) s[c] = __float_as_uint(neg_inf());
         }
-        if constexpr (EXT) {
-          const int32_t lo = max(p.window.sinks - pos0, 0), hi = from - pos0;  // [lo, hi) lie before the row's window
-          if (__any_sync(0xffffffffu, hi > lo && lo < KT)) {
-#pragma unroll
-            for (int c = 0; c < KT; ++c)
-              if (c >= lo && c < hi) s[c] = __float_as_uint(neg_inf());
-          }
-        }
-        const bool holes = PAGED && ms.holes[(u + j) % kTileValid] != 0;
+        const uint32_t hole = PAGED ? ms.holes[(u + j) % kTileValid] : 0;
+        const bool holes = hole != 0;
         uint64_t gap[2] = {0, 0};           // keys before the end that do not exist (bad pages)
         if (holes) {
           const int32_t end = keys_end - pos0;
@@ -980,9 +1000,11 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             const int32_t keys = min(end, KT) - 64;
             gap[1] = keys <= 0 ? 0ull : ~v[1] & (keys >= 64 ? ~0ull : (1ull << keys) - 1);
           }
+          if (!EXT || hole == 2) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c)
-            if ((gap[c >> 6] >> (c & 63)) & 1) s[c] = __float_as_uint(neg_inf());
+            for (int c = 0; c < KT; ++c)
+              if ((gap[c >> 6] >> (c & 63)) & 1) s[c] = __float_as_uint(neg_inf());
+          }
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
