@@ -1009,18 +1009,22 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
   if (x && !ra::prefix_is_shared(over_prefix(L, x), behind_prefix(L, x, prefix_len, prefix_table))) {
     L = behind_prefix(L, x, prefix_len, prefix_table);
   } else if (x) {
-    // the prefix's keys for the rows of all sequences, then each sequence's own, which join those
+    // each sequence's own keys, then the prefix's for the rows of all sequences, which join those
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
-    ra::PagedLaunch P = over_prefix(L, x);
-    P.seq_lens = prefix_len;
-    P.table = prefix_table;
-    P.lse = nullptr;
-    P.rows_out = reinterpret_cast<float*>(aligned_in(ws, plan.rows));
-    P.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
-    L.prior = P.rows_out;
-    L.prior_stats = P.stats_out;
-    L.partials = ws + plan.partials;
-    e = ra::launch_paged_extended(P, cs, &why);
+    ra::PagedLaunch own = L;
+    own.lse = nullptr;
+    own.rows_out = reinterpret_cast<float*>(aligned_in(ws, plan.rows));
+    own.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
+    own.partials = ws + plan.partials;
+    e = ra::launch_paged_extended(own, cs, &why);
+    const int taken = ra::paged_extended_blocks(own), sms = ra::device_sm_count();
+    L = over_prefix(L, x);
+    L.seq_lens = prefix_len;
+    L.table = prefix_table;
+    L.prior = own.rows_out;
+    L.prior_stats = own.stats_out;
+    // SMs that the first call leaves are enough when they are half of all; else it takes turns with it
+    L.most_blocks = taken <= sms / 2 ? sms - taken : 0;
   }
   if (e == cudaSuccess) e = w || x ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
   if (e != cudaSuccess)

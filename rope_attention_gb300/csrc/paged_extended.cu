@@ -9,6 +9,13 @@ cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, con
   return launch_rows<true>(L, stream, why);
 }
 
+int paged_extended_blocks(const PagedLaunch& L) {
+  if (paged_tile_serves(L)) return paged_tile_blocks(L);
+  if (paged_tokens_serves(L)) return paged_tokens_blocks(L);
+  Plan pl{};
+  return plan(L, &pl) ? std::min(pl.G, launch_blocks(L)) : 0;
+}
+
 namespace {
 // Cycles of a call's blocks for `keys` keys of every sequence, roughly: the tiles shared out, at what one of
 // its kernel takes (measured over prefixes of 2000 to 20000 positions).

@@ -18,6 +18,7 @@ bool paged_tile_serves(const PagedLaunch& L) {
 
 int64_t paged_tile_items(const PagedLaunch& L) { return most_items(L); }
 int paged_tile_keys(const PagedLaunch& L) { return keys_per_tile(L); }
+int paged_tile_blocks(const PagedLaunch& L) { return std::min(most_blocks(L), device_sm_count()); }
 
 size_t paged_tile_workspace(const PagedLaunch& L) { return join_bytes(most_blocks(L), 2 * kTileRows, L.Dv); }
 

@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
       float4 prior[NT];
       float2 prior_stats[NT];
       if (p.join.prior.rows && w.whole) {
+        grid_dependency_wait();
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const int2 row = w.row[warp + kTokenWarps * i];
@@ -637,6 +638,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
     }
   }
   __syncthreads();
+  if (p.join.prior.rows) grid_dependency_wait();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
 }
 
@@ -670,9 +672,8 @@ cudaError_t launch_tokens(const Params& p, const Plan& pl, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  if (pl.NR == 8) paged_tokens_kernel<F16, KQ, VQ, 1><<<pl.G, kTokenThreads, pl.smem, stream>>>(p);
-  else paged_tokens_kernel<F16, KQ, VQ, 2><<<pl.G, kTokenThreads, pl.smem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_main(pl.NR == 8 ? paged_tokens_kernel<F16, KQ, VQ, 1> : paged_tokens_kernel<F16, KQ, VQ, 2>, p, pl.G, kTokenThreads,
+                  pl.smem, p.join.prior.rows != nullptr, stream);
   if (e != cudaSuccess) return e;
   return p.whole ? cudaSuccess : launch_join<true>(p.join, F16, pl.G, pl.items, stream);
 }
@@ -683,11 +684,17 @@ bool paged_tokens_serves(const PagedLaunch& L) {
   return L.variant == 2 && L.Dkv <= kTokenDk && L.Dv <= kTokenDv && (L.total_q + L.B - 1) / L.B * (L.heads / L.N) <= 16;
 }
 
+int paged_tokens_blocks(const PagedLaunch& L) {
+  Plan pl{};
+  plan_tokens(L, &pl);
+  return std::min(pl.G, launch_blocks(L));
+}
+
 cudaError_t launch_paged_tokens(const PagedLaunch& L, cudaStream_t stream, const char** why) {
   Plan pl{};
   plan_tokens(L, &pl);
   Params p = row_params(L, pl);
-  pl.G = std::min(pl.G, device_sm_count());
+  pl.G = std::min(pl.G, launch_blocks(L));
   p.q = L.q;
   if (!encode_maps([&] {
         return make_rows_map(&p.tk, L.k_cache, L, L.Dkv, L.kq, p.box_rows) &&

@@ -1085,6 +1085,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       const int64_t at = EXT ? token * p.join.heads + head : 0;
       if (live) {
         if (EXT && whole && (p.join.prior.stats_out || p.join.prior.stats)) {
+          if (p.join.prior.stats) grid_dependency_wait();
           prior_end(p.join.prior, at, fmaf(m, sl2, -kLift), l, l != 0.f ? shift : 0.f, true, p.join.lse, share);
         } else if (whole) {
           if (p.join.lse)
@@ -1155,6 +1156,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (EXT && p.join.prior.rows) grid_dependency_wait();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
@@ -1174,8 +1176,7 @@ cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cut
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  kernel<<<blocks, SH::kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_main(kernel, p, blocks, SH::kThreads, smem, EXT && p.join.prior.rows, stream);
   if (e != cudaSuccess) return e;
   return cuts ? launch_join<EXT>(p.join, F16, blocks, items, stream) : cudaSuccess;
 }
