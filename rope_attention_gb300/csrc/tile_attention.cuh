@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "attention.h"
 #include "attn_join.cuh"
@@ -140,7 +141,17 @@ struct TileCount {
   }
 };
 
-struct TilePiece {
+// What a piece of a call with a window or a prefix has beside the rest: tiles of the sinks or the prefix, and how
+// much further the others' positions are; the first row's window; positions of the prefix, whose
+// tiles are those ahead.
+struct TileAhead {
+  int32_t ahead, skip, win, prefix;
+};
+struct TileNoneAhead {
+  static constexpr int32_t ahead = 0, skip = 0, win = 0, prefix = 0;
+};
+template <bool EXT>
+struct TilePiece : std::conditional_t<EXT, TileAhead, TileNoneAhead> {
   int32_t end;                              // there is no further piece
   int32_t first;                            // the first of its block
   int32_t b, head, kv_head, tok, q_start, Lq, k_start, Lk;
@@ -148,19 +159,18 @@ struct TilePiece {
   int32_t t0, take, T;                      // tiles [t0, t0 + take) of the item's T in the line
   int32_t ta, tb[2];                        // those that a row of either tile sees: [ta, tb[i])
   int32_t from, to;                         // blocks that share the item, where the block before began it
-  int32_t ahead, skip, win;                 // EXT: tiles of the sinks or the prefix, and how much further the others' positions
-                                            // are; the first row's window
-  int32_t prefix;                           // positions of the prefix, whose tiles are those ahead
   __device__ __forceinline__ bool whole() const { return take == T; }
   __device__ __forceinline__ int32_t n(int i) const { return max(0, tb[i] - ta); }
   // the first position of tile t
-  template <int KT, bool EXT>
-  __device__ __forceinline__ int32_t pos(int32_t t) const { return t * KT + (EXT && t >= ahead ? skip : 0); }
+  template <int KT>
+  __device__ __forceinline__ int32_t pos(int32_t t) const { return t * KT + (EXT && t >= this->ahead ? this->skip : 0); }
   // where the keys that tile t counts end; `seen` stands for the sequence's own
-  template <bool EXT>
-  __device__ __forceinline__ int32_t end_of(int32_t t, int32_t seen) const { return EXT && prefix > 0 && t < ahead ? prefix : seen; }
+  __device__ __forceinline__ int32_t end_of(int32_t t, int32_t seen) const {
+    return EXT && this->prefix > 0 && t < this->ahead ? this->prefix : seen;
+  }
 };
 
+template <bool EXT>
 struct TileMisc {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], c_full[2], c_empty[2];
   uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_ready[2], o_done[2], drain;
@@ -168,7 +178,7 @@ struct TileMisc {
   uint64_t valid[kTileValid][2];
   uint32_t holes[kTileValid];               // whether keys before the sequence's end are absent: a page is (EXT: 2), or
                                             // no row sees them (1)
-  TilePiece pieces[kTilePieces];
+  TilePiece<EXT> pieces[kTilePieces];
   int64_t scan[16], scan_items[16];
   int64_t start_off;
   int32_t start_b;
@@ -229,12 +239,12 @@ template <int KT, bool PAGED, bool EXT>
 struct TileWalk {
   int32_t b, item, blk, t;                  // next: sequence, head, row block, key tile
   int64_t rem;
-  TilePiece w;                              // of the sequence that c is of: its spans
+  TilePiece<EXT> w;                         // of the sequence that c is of: its spans
   TileCount c;
   int32_t runs;                             // TileRuns
   TileSpans<KT, PAGED, EXT> spans;
 
-  __device__ TileCount count(const TileParams& p, int32_t b, TilePiece& w) {
+  __device__ TileCount count(const TileParams& p, int32_t b, TilePiece<EXT>& w) {
     if (b >= spans.base + 32) spans.load(p, b);
     w.q_start = __shfl_sync(0xffffffffu, spans.q_start, b - spans.base);
     w.Lq = __shfl_sync(0xffffffffu, spans.Lq, b - spans.base);
@@ -327,7 +337,6 @@ struct TileWalk {
     w.head = PAGED ? item * p.g : item;
     w.tok = blk * 2 * p.join.tb;
     int32_t skip = 0;
-    w.ahead = w.skip = w.win = w.prefix = 0;
     if constexpr (EXT) {
       w.prefix = spans.prefix;
       w.win = window_from(p.window, w.tok + w.Lk - w.Lq);
@@ -366,8 +375,8 @@ __device__ __forceinline__ bool group_ok(uint32_t id, bool ok) {
 // The next piece that warp 10 handed over, for a whole warp; false at the end or when a wait
 // gave up.  GROUP: over codes the softmax groups meet at barriers in a piece, which have no time
 // limit, so the warps of a group (barrier `id`) take a piece, or leave, together.
-template <bool GROUP = false>
-__device__ __forceinline__ bool take_piece(TileMisc& ms, Ring& ring, TilePiece& w, uint64_t limit, volatile int* abort_flag,
+template <bool GROUP = false, bool EXT>
+__device__ __forceinline__ bool take_piece(TileMisc<EXT>& ms, Ring& ring, TilePiece<EXT>& w, uint64_t limit, volatile int* abort_flag,
                                            bool& ok, uint32_t id = 0) {
   ok = ok && bounded_wait_warp(smem_u32(&ms.piece_full[ring.stage]), ring.parity, limit, abort_flag);
   if (GROUP) ok = group_ok(id, ok);
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   constexpr int kRegsSoftmax = QUANT ? 192 : 216, kRegsRest = QUANT ? 64 : 72;
   constexpr int kTmaWarp = 8, kMmaWarp = 9, kPieceWarp = 10, kConvert0 = 12;
   extern __shared__ __align__(1024) uint8_t smem[];
-  TileMisc& ms = *reinterpret_cast<TileMisc*>(smem + SH::kOffMisc);
+  TileMisc<EXT>& ms = *reinterpret_cast<TileMisc<EXT>*>(smem + SH::kOffMisc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   using Walk = TileWalk<KT, PAGED, EXT>;
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
   volatile int* abort_flag = &ms.abort;
-  TilePiece w{};
+  TilePiece<EXT> w{};
   Ring pieces;
   if (warp >= 8 && warp < 12) {
     set_max_regs_dec<kRegsRest>();
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
             have = (__ballot_sync(0xffffffffu, row >= 0) >> (t * groups - base)) & ((1u << groups) - 1);
           }
           const uint32_t live = __popc(have);
-          const int32_t pos0 = w.template pos<KT, EXT>(t), end = w.template end_of<EXT>(t, w.Lk);
+          const int32_t pos0 = w.template pos<KT>(t), end = w.end_of(t, w.Lk);
           const int32_t y = PAGED ? (p.mode == kModePa ? w.kv_head : 0) : w.kv_head;
           // 0: the key tile, 1: the value tile
 #pragma unroll
@@ -976,12 +985,12 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
         }
         s_par ^= 1u;
         tc_fence_after();
-        const int32_t pos0 = w.template pos<KT, EXT>(w.ta + j), keys_end = w.template end_of<EXT>(w.ta + j, w.Lk);
+        const int32_t pos0 = w.template pos<KT>(w.ta + j), keys_end = w.end_of(w.ta + j, w.Lk);
         uint32_t s[KT];
 #pragma unroll
         for (int c = 0; c < KT; c += 32) tmem_ld_x32(s_addr + c, s + c);
         tmem_ld_wait();
-        const int32_t nv = w.template end_of<EXT>(w.ta + j, seen) - pos0;  // keys of this tile that the row sees
+        const int32_t nv = w.end_of(w.ta + j, seen) - pos0;  // keys of this tile that the row sees
         if constexpr (EXT) {
           hide_keys<KT>(s, nv, max(p.window.sinks - pos0, 0), from - pos0);
         } else if (__any_sync(0xffffffffu, nv < KT)) {
@@ -1164,7 +1173,7 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
 template <int KS, int VS, int KT, bool F16, bool QUANT, bool PAGED, bool EXT = false>
 cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cuts, cudaStream_t stream) {
   using SH = TileShape<KS, VS, KT, QUANT>;
-  constexpr int smem = SH::kOffMisc + static_cast<int>(sizeof(TileMisc));
+  constexpr int smem = SH::kOffMisc + static_cast<int>(sizeof(TileMisc<EXT>));
   static_assert(smem <= 232448, "shared memory budget");
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
