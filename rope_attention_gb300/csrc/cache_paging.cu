@@ -13,7 +13,8 @@
 // Every block sums over all requests for itself (they are in L2, a few thousand at most) and then
 // takes its share of the tokens, whose request it finds by bisection in shared memory.  extend and
 // truncate are one cluster: lengths and the count of free pages may be written where they were
-// read, once every block of the cluster has read them, and no second launch is needed.
+// read, once every block of the cluster has read them, and no second launch is needed.  An extend by
+// more tokens than a cluster writes as fast as all SMs is two launches: the tokens, then the state.
 // Bound by latency: a launch, three dependent loads and a scan.  Measured: 256 requests and a token each
 // 5.1 us; 36000 tokens for 16 requests 8.3 (12.3 with four blocks, 8.2 with sixteen); 18700 pages of 300 requests
 // back 8.2.
@@ -90,7 +91,9 @@ __device__ __forceinline__ int32_t last_not_above(const int32_t* v, int32_t n, i
 // Shared memory: where each request's tokens start, its first position, and its first page among
 // those taken (-1: it gets none of what it asks for).
 // AT_ONCE: tokens of a thread whose loads are on their way together, 1 where no thread has more.
-template <bool EXTEND, int AT_ONCE>
+// PART: both in one cluster; or the tokens by any number of blocks, and the lengths and the count by one.
+enum SlotsPart { kBoth, kTokens, kState };
+template <bool EXTEND, int AT_ONCE, SlotsPart PART>
 __global__ void __launch_bounds__(kMostThreads, 1) slots_kernel(const __grid_constant__ Params p) {
   extern __shared__ int32_t shared[];
   __shared__ Sums sums;
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) slots_kernel(const __grid_con
     if (EXTEND && n <= p.cap - at) need += pages_of(p, at + n) - pages_of(p, at);
   }
   __syncwarp();
-  if (EXTEND) cluster_arrive();             // this block has read lengths and count
+  if (EXTEND && PART == kBoth) cluster_arrive();  // this block has read lengths and count
   block_scan(before, need, sums, total, all);
   int32_t refused = 0;
   for (int32_t b = b0; b < b1; ++b) {
@@ -134,14 +137,14 @@ __global__ void __launch_bounds__(kMostThreads, 1) slots_kernel(const __grid_con
       if (!served && n > 0) ++refused;
     }
   }
-  if (EXTEND && blockIdx.x == 0 && refused > 0 && L.err_count) atomicAdd(L.err_count, refused);
+  if (EXTEND && PART != kState && blockIdx.x == 0 && refused > 0 && L.err_count) atomicAdd(L.err_count, refused);
   __syncthreads();
 
   // ---- tokens
   const int32_t rows = static_cast<int32_t>(min(total, static_cast<int64_t>(max_tokens)));
   int32_t bad = 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * threads;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * threads + tid; t0 < max_tokens; t0 += AT_ONCE * stride) {
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * threads + tid; PART != kState && t0 < max_tokens; t0 += AT_ONCE * stride) {
     // where each token's page stands: in the table, or on the free list (and then in the table as well)
     const int32_t* from[AT_ONCE];
     int32_t* to[AT_ONCE];
@@ -180,19 +183,19 @@ __global__ void __launch_bounds__(kMostThreads, 1) slots_kernel(const __grid_con
     }
   }
   if (bad > 0 && L.err_count) atomicAdd(L.err_count, bad);
-  if (EXTEND) cluster_wait();               // every block has read lengths and count
+  if (EXTEND && PART == kBoth) cluster_wait();  // every block has read lengths and count
   if (blockIdx.x != 0) return;
   for (int32_t b = tid; b < B; b += threads) {
-    L.cu[b] = cu[b];
-    if (EXTEND) {
+    if (PART != kState) L.cu[b] = cu[b];
+    if (EXTEND && PART != kTokens) {
       // (a request's tokens, of which pages[b] says whether it gets them: what its successor starts behind)
       const int32_t n = (b + 1 < B ? cu[b + 1] : rows) - cu[b];
       L.new_lens[b] = first[b] + (pages[b] >= 0 ? n : 0);
     }
   }
   if (tid == 0) {
-    L.cu[B] = rows;
-    if (EXTEND) *L.new_free_count = avail - most_taken;
+    if (PART != kState) L.cu[B] = rows;
+    if (EXTEND && PART != kTokens) *L.new_free_count = avail - most_taken;
   }
 }
 
@@ -325,14 +328,22 @@ int64_t cluster_for(int64_t n) {
 }  // namespace
 
 cudaError_t launch_cache_extend(const PagingLaunch& L, cudaStream_t stream) {
+  // (a cluster writes 1 us more for each 8000 tokens; the second launch takes 3)
+  constexpr int64_t kOneCluster = 1 << 16;
+  const Params p = make_params(L);
+  if (L.max_tokens > kOneCluster) {
+    const cudaError_t e = launch(slots_kernel<true, 4, kTokens>, p, device_sm_count(), kMostThreads, false, stream);
+    return e != cudaSuccess ? e : launch(slots_kernel<true, 1, kState>, p, 1, threads_for(1, L.B), false, stream);
+  }
   const int64_t c = cluster_for(L.max_tokens);
   const int threads = threads_for((L.max_tokens + c - 1) / c, L.B);
-  return launch(c * threads >= L.max_tokens ? slots_kernel<true, 1> : slots_kernel<true, 4>, make_params(L), c, threads, true, stream);
+  return launch(c * threads >= L.max_tokens ? slots_kernel<true, 1, kBoth> : slots_kernel<true, 4, kBoth>, p, c, threads, true, stream);
 }
 cudaError_t launch_cache_slots(const PagingLaunch& L, cudaStream_t stream) {
   const int threads = threads_for(L.max_tokens, L.B);
   const int64_t blocks = std::min<int64_t>(device_sm_count(), (L.max_tokens + threads - 1) / threads);
-  return launch(slots_kernel<false, 1>, make_params(L), blocks, threads, false, stream);
+  return launch(blocks * threads >= L.max_tokens ? slots_kernel<false, 1, kBoth> : slots_kernel<false, 4, kBoth>, make_params(L),
+                blocks, threads, false, stream);
 }
 cudaError_t launch_cache_truncate(const PagingLaunch& L, cudaStream_t stream) {
   const int64_t n = std::min(L.block_num, L.B * L.table_stride), c = cluster_for(n);

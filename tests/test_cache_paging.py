@@ -93,11 +93,30 @@ def test_page_sizes(bs, in_place):
     assert p.count == p.block_num and sorted(p.free) == list(range(p.block_num))
 
 
-@pytest.mark.parametrize("tokens", [2047, 2048, 2049, 5000, 9000, 20000, 70000])
+@pytest.mark.parametrize("tokens", [2047, 2048, 2049, 5000, 9000, 20000, 65430, 70000, 400000])
 def test_long_prompts(tokens):
     p = Pages(3, [100, 0, 33], tokens // 16 + 20, 16, tokens // 16 + 40)
     p.extend([tokens // 3, tokens - tokens // 3 - 1, 1], tokens + 100)
     p.truncate([50, 0, 34])
+
+
+def test_long_prompts_in_place_and_refused():
+    p = Pages(15, [100, 0, 33, 7], 5000, 16, 6000)
+    # 1875 and 3750 pages of 6000; the third's 1250 are not there, the last needs none
+    want = p.extend([30000, 60000, 20000, 3], 150000, in_place=True)
+    assert want["new_seq_lens"].tolist() == [30100, 60000, 33, 10] and want["errors"] == 1
+    p.extend([1, 1, 1, 1], 100000, in_place=True)
+
+
+@pytest.mark.parametrize("B", [3, 16384])
+def test_slots_of_long_contexts(B):
+    lens = [300000, 0, 77] if B == 3 else [20] * B
+    p = Pages(16, lens, max(lens) // 16 + 2, 16, 3)
+    total = sum(lens)
+    want = oracle.paging.slots(None, lens, p.table, block_num=p.block_num, block_size=16, max_tokens=total)
+    index, cu = torch.empty(total, dtype=torch.int64, device="cuda"), torch.empty(B + 1, dtype=torch.int32, device="cuda")
+    native.kv_cache_slots(p.params(total), dev(lens), dev(p.table), index, cu)
+    assert np.array_equal(index.cpu().numpy(), want["index"]) and np.array_equal(cu.cpu().numpy(), want["cu_seqlens"])
 
 
 def test_free_list_that_runs_out():
