@@ -123,7 +123,7 @@ struct RunScan {
   int64_t start_off;
   int32_t start_b;
 };
-struct Misc {                   // behind the tiles in shared memory
+struct alignas(16) Misc {       // behind the tiles in shared memory
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t code_full[kMaxStages], code_empty[kMaxStages];
   uint64_t s_full[2], p_ready, pv_done, q_full, q_ready, q_empty, drain;
@@ -465,6 +465,61 @@ __device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows
     }
   }
   return true;
+}
+
+// Eight rows of O^T from column `col` on, a lane's channel ch of each, to where they go (EXT).  Nothing
+// depends on the row before: the rows' words come from shared memory four at a time, and pairs of
+// lanes swap halves so that each writes two channels of four rows.  (Row by row, with a
+// branch out of the loop and two bytes to a store, 64 rows of 512 channels took 25k cycles, XX so.)
+template <bool F16>
+__device__ __forceinline__ void write_rows(const Params& p, const Piece& w, bool whole, int32_t n, int col, int ch, const uint32_t (&o)[8],
+                                           float offset, float inv_s, const int32_t* out_row, const float* inv_sum, const float* xch,
+                                           float* part, int lane) {
+  const bool there = ch < p.Dv;
+  if (!whole) {
+    if (there && n > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < w.rows) part[(col + e) * p.Dv] = __uint_as_float(o[e]);
+    }
+    return;
+  }
+  const int4 r0 = *reinterpret_cast<const int4*>(out_row + col), r1 = *reinterpret_cast<const int4*>(out_row + col + 4);
+  const int32_t row[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};    // -1: none
+  const float4 i0 = *reinterpret_cast<const float4*>(inv_sum + col), i1 = *reinterpret_cast<const float4*>(inv_sum + col + 4);
+  const float inv[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = inv[e] != 0.f ? (__uint_as_float(o[e]) * inv[e] - offset) * inv_s : 0.f;
+  if (p.join.prior.rows_out) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (there && row[e] >= 0) p.join.prior.rows_out[static_cast<int64_t>(row[e]) * p.Dv + ch] = y[e];
+    return;
+  }
+  if (p.join.prior.rows) {
+    float prior[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      prior[e] = there && row[e] >= 0 ? p.join.prior.rows[static_cast<int64_t>(row[e]) * p.Dv + ch] : 0.f;
+    const float4 a0 = *reinterpret_cast<const float4*>(xch + p.NR + col), a1 = *reinterpret_cast<const float4*>(xch + p.NR + col + 4);
+    const float4 b0 = *reinterpret_cast<const float4*>(xch + col), b1 = *reinterpret_cast<const float4*>(xch + col + 4);
+    const float own[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, other[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], own[e], prior[e] * other[e]);
+  }
+  const bool odd = lane & 1;              // odd lanes take the last four rows
+  const uint32_t h0 = pack_half2<!F16>(y[0], y[1]), h1 = pack_half2<!F16>(y[2], y[3]);
+  const uint32_t h2 = pack_half2<!F16>(y[4], y[5]), h3 = pack_half2<!F16>(y[6], y[7]);
+  const uint32_t x0 = __shfl_xor_sync(0xffffffffu, odd ? h0 : h2, 1), x1 = __shfl_xor_sync(0xffffffffu, odd ? h1 : h3, 1);
+  const uint32_t lo[2] = {odd ? x0 : h0, odd ? x1 : h1}, hi[2] = {odd ? h2 : x0, odd ? h3 : x1};  // even channel, odd channel
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int32_t at = odd ? row[e + 4] : row[e];
+    if (there && at >= 0)
+      *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(at) * p.Dv + (ch & ~1)) =
+          __byte_perm(lo[e >> 1], hi[e >> 1], e & 1 ? 0x7632 : 0x5410);
+  }
 }
 
 // F16: q, out and 16-bit caches are fp16, not bf16; P16: P is fp16 (V's operand is)
@@ -985,27 +1040,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             tmem_ld_x8(tmem + lane_base + kSCols + c * NR + col, o);
             tmem_ld_wait();
           }
-          if (ch >= p.Dv || (!whole && n == 0)) continue;
-          float prior[8];
-          if (EXT && whole && p.join.prior.rows) {   // all on their way before the first is used
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              prior[e] = col + e < w.rows ? p.join.prior.rows[static_cast<int64_t>(out_row[col + e]) * p.Dv + ch] : 0.f;
+          if constexpr (EXT) {
+            write_rows<F16>(p, w, whole, n, col, ch, o, so.y, inv_s, out_row, inv_sum, xch, part, lane);
+            continue;
           }
+          if (ch >= p.Dv || (!whole && n == 0)) continue;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int r = col + e;
             if (r >= w.rows) break;
             if (whole) {
               const float inv = inv_sum[r];
-              float y = inv != 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
-              if constexpr (EXT) {
-                if (p.join.prior.rows_out) {
-                  p.join.prior.rows_out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = y;
-                  continue;
-                }
-                if (p.join.prior.rows) y = fmaf(y, xch[NR + r], prior[e] * xch[r]);
-              }
+              const float y = inv != 0.f ? (__uint_as_float(o[e]) * inv - so.y) * inv_s : 0.f;
               p.out[static_cast<int64_t>(out_row[r]) * p.Dv + ch] = to_half<F16>(y);
             } else {
               part[r * p.Dv] = __uint_as_float(o[e]);
