@@ -86,8 +86,7 @@ cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const c
 cudaError_t launch_paged_tile_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
 // The kernel for up to 16 rows per sequence and kv head of the calls with a window or a prefix
-// (paged_tokens.cu).  Its parts never need more room than those of the kernel that serves
-// paged_attention for the same sizes.
+// (paged_tokens.cu).  Its workspace is paged_attention's for the same sizes.
 bool paged_tokens_serves(const PagedLaunch& L);
 int paged_tokens_blocks(const PagedLaunch& L);
 cudaError_t launch_paged_tokens(const PagedLaunch& L, cudaStream_t stream, const char** why);

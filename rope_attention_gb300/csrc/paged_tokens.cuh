@@ -54,6 +54,9 @@ inline void plan_tokens(const PagedLaunch& L, Plan* pl) {
   pl->off_misc = pl->off_p + meet;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
   share_out(L, pl);
+  // the workspace is sized for paged_attention's kernel, whose row tiles hold more rows
+  const size_t have = paged_attention_workspace(L) - kAttnHeader;
+  while (pl->G > 1 && join_bytes(pl->G, pl->NR, L.Dv) > have) --pl->G;
 }
 
 }  // namespace

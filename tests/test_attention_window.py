@@ -170,3 +170,17 @@ def test_a_window_that_hides_nothing_is_paged_attention():
         want, lse = torch.empty_like(c.out), torch.empty_like(c.lse)
         native.paged_attention(c.cache, c.params, c.q, c.kd, c.vd, c.lens_d, want, c.ws, lse=lse, **c.args)
         assert torch.equal(want.view(torch.int16), c.out.view(torch.int16)) and torch.equal(lse, c.lse)
+
+
+@pytest.mark.parametrize("at", [0, 16])
+@pytest.mark.parametrize("heads,N,B,new,Dv", [(6, 2, 1, 2, 16), (3, 1, 2, 2, 48), (13, 1, 1, 1, 128), (6, 1, 3, 1, 32), (5, 1, 1, 3, 16),
+                                              (24, 8, 2, 2, 16)])
+def test_small_items_stay_in_their_workspace(at, heads, N, B, new, Dv):
+    c = Case(36, variant=2, lens=[512] * B, news=[new] * B, heads=heads, N=N, Dkv=32, Dv=Dv, R=16, window=500, sinks=2)
+    n = c.ws.numel()
+    room = torch.zeros(at + n + 4096, dtype=torch.uint8, device="cuda")
+    room[at + n:] = 77
+    room[:at] = 77
+    c.ws = room[at:at + n]
+    c.run_and_check()
+    assert (room[:at] == 77).all() and (room[at + n:] == 77).all()
