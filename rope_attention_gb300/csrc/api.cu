@@ -1017,14 +1017,12 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
     own.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
     own.partials = ws + plan.partials;
     e = ra::launch_paged_extended(own, cs, &why);
-    const int taken = ra::paged_extended_blocks(own), sms = ra::device_sm_count();
     L = over_prefix(L, x);
     L.seq_lens = prefix_len;
     L.table = prefix_table;
     L.prior = own.rows_out;
     L.prior_stats = own.stats_out;
-    // SMs that the first call leaves are enough when they are half of all; else it takes turns with it
-    L.most_blocks = taken <= sms / 2 ? sms - taken : 0;
+    L.most_blocks = ra::prefix_blocks(own, L);
   }
   if (e == cudaSuccess) e = w || x ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
   if (e != cudaSuccess)

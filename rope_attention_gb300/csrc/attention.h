@@ -72,7 +72,7 @@ size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
 // with a window, rows_out or prior
 cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
-int paged_extended_blocks(const PagedLaunch& L);  // that such a call launches
+int prefix_blocks(const PagedLaunch& own, const PagedLaunch& over);  // most_blocks of the second of two calls
 // Whether the two calls cost less than the one: `over` is the first of the two, `behind` the one.
 bool prefix_is_shared(const PagedLaunch& over, const PagedLaunch& behind);
 // The kernel for many rows per sequence and kv head (paged_tile.cuh): whether it takes the

@@ -1082,9 +1082,13 @@ struct Plan {
 bool p_in_two(const PagedLaunch& L) { return L.f16 && (L.kq != 0 || L.vq != 0); }
 int p_bytes(const PagedLaunch& L, int nr) { return nr * 128 * (p_in_two(L) ? 2 : 1); }
 
+// blocks that a call may have
+int launch_blocks(const PagedLaunch& L) { return L.most_blocks > 0 ? L.most_blocks : device_sm_count(); }
+
 // The row tiles of NR rows, and the blocks that share their key tiles: one per SM, and no more than there
-// are tiles at the largest lengths.
-void share_out(const PagedLaunch& L, Plan* pl) {
+// are tiles at the largest lengths.  whole(T): whether items of T tiles at most are not cut.
+template <class Whole>
+void share_out(const PagedLaunch& L, Plan* pl, Whole&& whole) {
   const int g = L.heads / static_cast<int32_t>(L.N), nr = pl->NR;
   pl->hb = std::min(g, nr);
   pl->tb = nr / pl->hb;
@@ -1096,8 +1100,7 @@ void share_out(const PagedLaunch& L, Plan* pl) {
   const int64_t all = std::max<int64_t>(1, ahead + (L.max_seq_len + kKeys - 1) / kKeys);
   pl->window = make_window(L.window, L.sinks, pl->tb, kKeys);
   const int64_t T = std::min<int64_t>(all, pl->window.most);
-  const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
-  pl->whole = (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
+  pl->whole = whole(T);
   const auto blocks = [](int64_t runs) { return static_cast<int32_t>(std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, runs))); };
   pl->G = blocks(pl->whole ? pl->items : pl->items * T);
   // as if items were cut always: a workspace that is sized at the largest batch, which may take
@@ -1144,7 +1147,10 @@ bool plan(const PagedLaunch& L, Plan* pl) {
   pl->off_staging = pl->off_ring + pl->ns * pl->stage;
   pl->off_misc = pl->off_staging + pl->nsg * pl->staging;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(Misc)) + 15) & ~15) + row_arrays_bytes(nr) + 16;
-  share_out(L, pl);
+  share_out(L, pl, [&](int64_t T) {
+    const double share = static_cast<double>(pl->items) / kMaxBlocks, rounds = std::ceil(share);  // rounds of whole items
+    return (rounds - share) * static_cast<double>(T) <= kJoinTiles + kJoinAll * std::min(share, 1.0);
+  });
   return true;
 }
 
@@ -1164,9 +1170,6 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
   if (e != cudaSuccess) return e;
   return p.whole ? cudaSuccess : launch_join<EXT>(p.join, F16, blocks, items, stream);
 }
-
-// blocks that a call may have
-int launch_blocks(const PagedLaunch& L) { return L.most_blocks > 0 ? L.most_blocks : device_sm_count(); }
 
 // what a launch's kernel takes from the call and its plan
 Params row_params(const PagedLaunch& L, const Plan& pl) {

@@ -53,7 +53,13 @@ inline void plan_tokens(const PagedLaunch& L, Plan* pl) {
   pl->off_p = pl->ns * pl->stage;
   pl->off_misc = pl->off_p + meet;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
-  share_out(L, pl);
+  // Items are cut where that saves a block more tiles than the join costs, 5 to 17 of this kernel's.  (int8, in a
+  // window: 8 items of 9 tiles 14.1 us whole and 14.4 cut, of 15 16.4 and 14.4; 64 items of 15 18.5 and 22.0, of 28
+  // 24.6 and 24.6; 256 items of 28 43 and 48, of 53 70 and 70.)
+  share_out(L, pl, [&](int64_t T) {
+    const double share = static_cast<double>(pl->items) / launch_blocks(L), rounds = std::ceil(share);
+    return (rounds - share) * static_cast<double>(T) <= 5 + 12 * std::min(4 * share, 1.0);
+  });
   // the workspace is sized for paged_attention's kernel, whose row tiles hold more rows
   const size_t have = paged_attention_workspace(L) - kAttnHeader;
   while (pl->G > 1 && join_bytes(pl->G, pl->NR, L.Dv) > have) --pl->G;
