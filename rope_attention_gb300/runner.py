@@ -140,9 +140,11 @@ class KvRun:
 
 class PackedAttentionRun:
     """packed_attention on the output of a QkvRun: its Q, K and V columns as they lie, each
-    batch element one sequence (or ``starts``, the first token of each and the total)."""
+    batch element one sequence (or ``starts``, the first token of each and the total).  With a
+    ``window`` (a native.AttentionWindow) packed_window_attention, which is causal."""
 
-    def __init__(self, qkv: QkvRun, causal: bool = False, starts: list[int] | None = None, scale: float | None = None):
+    def __init__(self, qkv: QkvRun, causal: bool = False, starts: list[int] | None = None, scale: float | None = None,
+                 window: native.AttentionWindow | None = None):
         c = qkv.case
         nq, nkv, d = c.num_heads, c.num_kv_heads, c.head_dim
         if qkv.params.output_layout == native.RA_LAYOUT_BSD:
@@ -154,15 +156,19 @@ class PackedAttentionRun:
         self.out = torch.empty(c.T, nq, d, dtype=torch.bfloat16, device=device)
         self.lse = torch.empty(c.T, nq, dtype=torch.float32, device=device)
         self.starts = None if starts is None else torch.tensor(starts, dtype=torch.int32, device=device)
+        self.window = window
         self.params = native.packed_attention_params(self.q, self.k, self.v, self.out,
-                                                     B=c.B if starts is None else len(starts) - 1, causal=causal,
-                                                     softmax_scale=scale)
+                                                     B=c.B if starts is None else len(starts) - 1,
+                                                     causal=causal or window is not None, softmax_scale=scale)
         self.workspace = torch.zeros(native.packed_attention_workspace_bytes(self.params), dtype=torch.uint8,
                                      device=device)
 
     def run(self, stream=None) -> None:
-        native.packed_attention(self.params, self.q, self.k, self.v, self.out, self.workspace, self.lse,
-                                self.starts, self.starts, stream)
+        tensors = (self.q, self.k, self.v, self.out, self.workspace, self.lse, self.starts, self.starts, stream)
+        if self.window is not None:
+            native.packed_window_attention(self.params, self.window, *tensors)
+        else:
+            native.packed_attention(self.params, *tensors)
 
     def status(self, stream=None) -> int:
         return native.attention_status(self.workspace, stream)
@@ -170,10 +176,13 @@ class PackedAttentionRun:
 
 class PagedAttentionRun:
     """paged_attention of query tokens q [total_q, heads, Dkv] over the caches of a KvRun.
-    ``table`` [B, pages] int32 (None in Norm mode), ``lens`` [B] and ``starts`` [B + 1] lists."""
+    ``table`` [B, pages] int32 (None in Norm mode), ``lens`` [B] and ``starts`` [B + 1] lists.
+    With a ``window`` (a native.AttentionWindow) paged_window_attention; with a ``prefix``
+    (its length and its pages' table) paged_prefix_attention, behind that prefix."""
 
     def __init__(self, kv: KvRun, q: torch.Tensor, lens: list[int], table=None, starts: list[int] | None = None,
-                 causal: bool = True, scale: float | None = None):
+                 causal: bool = True, scale: float | None = None, window: native.AttentionWindow | None = None,
+                 prefix: tuple | None = None):
         c, device = kv.case, q.device
         self.kv, self.q = kv, q
         i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).to(device)
@@ -186,14 +195,28 @@ class PagedAttentionRun:
             B=len(lens), total_q=q.shape[0], num_heads=q.shape[1], causal=1 if causal else 0,
             softmax_scale=c.Dkv ** -0.5 if scale is None else scale, max_seq_len=max(lens),
             block_table_stride=0 if table is None else self.table.shape[1])
-        self.workspace = torch.zeros(native.paged_attention_workspace_bytes(kv.params, self.params),
-                                     dtype=torch.uint8, device=device)
+        self.window, self.prefix = window, None
+        if prefix is not None:
+            self.prefix_len, self.prefix_table = i32([prefix[0]]), i32(prefix[1])
+            self.prefix = native.AttentionPrefix(max_prefix_len=prefix[0], table_entries=self.prefix_table.numel())
+            n = native.paged_prefix_attention_workspace_bytes(kv.params, self.params, self.prefix)
+        else:
+            n = native.paged_attention_workspace_bytes(kv.params, self.params)
+        self.workspace = torch.zeros(n, dtype=torch.uint8, device=device)
 
     def run(self, stream=None) -> None:
         k = self.kv
-        native.paged_attention(k.params, self.params, self.q, k.k_cache, k.ckv_cache, self.lens, self.out,
-                               self.workspace, self.table, self.starts, k.k_scale, k.v_scale, k.k_offset,
-                               k.v_offset, self.lse, self.err, stream)
+        rest = (self.starts, k.k_scale, k.v_scale, k.k_offset, k.v_offset, self.lse, self.err, stream)
+        if self.prefix is not None:
+            native.paged_prefix_attention(k.params, self.params, self.prefix, self.q, k.k_cache, k.ckv_cache,
+                                          self.prefix_len, self.prefix_table, self.lens, self.table, self.out,
+                                          self.workspace, *rest)
+        elif self.window is not None:
+            native.paged_window_attention(k.params, self.params, self.window, self.q, k.k_cache, k.ckv_cache,
+                                          self.lens, self.out, self.workspace, self.table, *rest)
+        else:
+            native.paged_attention(k.params, self.params, self.q, k.k_cache, k.ckv_cache, self.lens, self.out,
+                                   self.workspace, self.table, *rest)
 
     def status(self, stream=None) -> int:
         return native.attention_status(self.workspace, stream)
