@@ -586,7 +586,8 @@ ra_status paged_window_attention(const kv_rms_norm_rope_cache_params* cache, con
 
 /* Bounds of a prefix that all sequences of a call share. */
 typedef struct {
-  int64_t max_prefix_len;     /* the prefix is not longer (a larger length is clamped) */
+  int64_t max_prefix_len;     /* the prefix is not longer (a larger length is clamped);
+                                 with max_seq_len at most 2^31 - 256                   */
   int64_t table_entries;      /* entries of prefix_table, >= 1                         */
 } attention_prefix;
 

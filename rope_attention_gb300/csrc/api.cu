@@ -354,12 +354,15 @@ ra_status check_window(const attention_window* w, int32_t causal) {
   return RA_OK;
 }
 
-ra_status check_prefix(const kv_rms_norm_rope_cache_params* c, const attention_prefix* x) {
+ra_status check_prefix(const kv_rms_norm_rope_cache_params* c, const paged_attention_params* p, const attention_prefix* x) {
   if (x == nullptr) return fail(RA_ERR_INVALID_ARG, "prefix is NULL");
   if (c->cache_mode == RA_CACHE_NORM)
     return fail(RA_ERR_UNSUPPORTED, "NORM mode has no pages for sequences to share");
   if (x->max_prefix_len < 0 || x->max_prefix_len > ra::kMostPositions)
     return fail(RA_ERR_INVALID_ARG, "max_prefix_len must be in [0, 2^31 - 256]");
+  // one call lays a prefix's tiles ahead of a sequence's own
+  if (x->max_prefix_len + p->max_seq_len > ra::kMostPositions)
+    return fail(RA_ERR_INVALID_ARG, "max_prefix_len + max_seq_len must be at most 2^31 - 256");
   if (x->table_entries < 1 || x->table_entries > (1LL << 31))
     return fail(RA_ERR_INVALID_ARG, "table_entries must be in [1, 2^31]");
   return RA_OK;
@@ -959,7 +962,7 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
   ra_status st = check_cache(cache, k_rope_scale, c_kv_scale, k_rope_offset, c_kv_offset, &s);
   if (st == RA_OK) st = check_paged(cache, p, s);
   if (st == RA_OK && w) st = check_window(w, p->causal);
-  if (st == RA_OK && x) st = check_prefix(cache, x);
+  if (st == RA_OK && x) st = check_prefix(cache, p, x);
   if (st != RA_OK) return st;
   if (!q || !k_cache || !ckv_cache || !seq_lens || !out)
     return fail(RA_ERR_INVALID_ARG, "q, k_cache, ckv_cache, seq_lens and out are required");
@@ -1060,7 +1063,7 @@ ra_status paged_prefix_attention_workspace_bytes(const kv_rms_norm_rope_cache_pa
   CacheShape s;
   ra_status st = check_cache_alone(cache, &s);
   if (st == RA_OK) st = check_paged(cache, p, s);
-  if (st == RA_OK) st = check_prefix(cache, prefix);
+  if (st == RA_OK) st = check_prefix(cache, p, prefix);
   if (st != RA_OK) return st;
   *bytes = prefix_plan(paged_launch(cache, p, s), prefix).bytes;
   return ok();

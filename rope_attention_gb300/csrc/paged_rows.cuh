@@ -470,7 +470,7 @@ __device__ __forceinline__ bool scale_q(const Params& p, int32_t n, int32_t rows
 // Eight rows of O^T from column `col` on, a lane's channel ch of each, to where they go (EXT).  Nothing
 // depends on the row before: the rows' words come from shared memory four at a time, and pairs of
 // lanes swap halves so that each writes two channels of four rows.  (Row by row, with a
-// branch out of the loop and two bytes to a store, 64 rows of 512 channels took 25k cycles, XX so.)
+// branch out of the loop and two bytes to a store, 64 rows of 512 channels took 25k cycles, 13k so.)
 template <bool F16>
 __device__ __forceinline__ void write_rows(const Params& p, const Piece& w, bool whole, int32_t n, int col, int ch, const uint32_t (&o)[8],
                                            float offset, float inv_s, const int32_t* out_row, const float* inv_sum, const float* xch,

@@ -95,6 +95,12 @@ def test_prefixes_rejected(L, x, c, over, code):
     assert st == code and msg
 
 
+def test_a_prefix_and_what_follows_stay_within_31_bits(L):
+    for n, code in ((1000, 0), (1001, -1), ((1 << 31) - 256, -1)):
+        st, msg = call_prefix(L, X(n), p=paged(max_seq_len=(1 << 31) - 1256))
+        assert st == code and (st == 0) == (msg == "")
+
+
 def test_a_prefix_needs_pages(L):
     st, msg = call_prefix(L, c=cache(**NORM), p=paged(block_table_stride=0), table=None)
     assert st == -2 and "NORM" in msg
