@@ -1009,23 +1009,23 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
     L.window = w->window;
     L.sinks = w->sinks;
   }
-  if (x && !ra::prefix_is_shared(over_prefix(L, x), behind_prefix(L, x, prefix_len, prefix_table))) {
-    L = behind_prefix(L, x, prefix_len, prefix_table);
-  } else if (x) {
+  if (x) {
     // each sequence's own keys, then the prefix's for the rows of all sequences, which join those
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
-    ra::PagedLaunch own = L;
+    ra::PagedLaunch own = L, over = over_prefix(L, x);
     own.lse = nullptr;
     own.rows_out = reinterpret_cast<float*>(aligned_in(ws, plan.rows));
     own.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
     own.partials = ws + plan.partials;
-    e = ra::launch_paged_extended(own, cs, &why);
-    L = over_prefix(L, x);
-    L.seq_lens = prefix_len;
-    L.table = prefix_table;
-    L.prior = own.rows_out;
-    L.prior_stats = own.stats_out;
-    L.most_blocks = ra::prefix_blocks(own, L);
+    over.seq_lens = prefix_len;
+    over.table = prefix_table;
+    over.prior = own.rows_out;
+    over.prior_stats = own.stats_out;
+    L = behind_prefix(L, x, prefix_len, prefix_table);
+    if (ra::prefix_is_shared(own, over, L)) {
+      e = ra::launch_paged_extended(own, cs, &why);
+      L = over;
+    }
   }
   if (e == cudaSuccess) e = w || x ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
   if (e != cudaSuccess)

@@ -49,14 +49,12 @@ struct PagedLaunch {
   // A shared prefix, in one of two ways.  One call has it ahead of every sequence's own positions
   // (prefix_len and so on), or two calls make one: the first, over the sequences' own positions, leaves its
   // rows in fp32 (rows_out) with their statistics; the second, over the prefix, takes the tokens of all
-  // sequences for one's (cu_step: cu_q[0] .. cu_q[cu_step]) and joins its rows with those (prior).  It
-  // starts while the first still runs.
+  // sequences for one's (cu_step: cu_q[0] .. cu_q[cu_step]) and joins its rows with those (prior).
   int32_t cu_step;             // entries of cu_q to a sequence's end: 1 but in the second call
   float* rows_out;             // [total_q, heads, Dv], or null
   float2* stats_out;           // [total_q, heads]: (log2 of the sum, the lse's share of the key offsets)
   const float* prior;
   const float2* prior_stats;
-  int32_t most_blocks;         // of the second call: SMs that the first leaves; 0: all
   int32_t shifts;              // the second call writes the lse: that share is wanted
   const int32_t *prefix_len, *prefix_table;
   int64_t prefix_entries, max_prefix_len;
@@ -72,23 +70,21 @@ size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
 // with a window, rows_out or prior
 cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
-int prefix_blocks(const PagedLaunch& own, const PagedLaunch& over);  // most_blocks of the second of two calls
-// Whether the two calls cost less than the one: `over` is the first of the two, `behind` the one.
-bool prefix_is_shared(const PagedLaunch& over, const PagedLaunch& behind);
+// Whether sequences behind a shared prefix are served in two calls (`own` positions, then `over` the prefix) or in
+// one (`behind` it).
+bool prefix_is_shared(const PagedLaunch& own, const PagedLaunch& over, const PagedLaunch& behind);
 // The kernel for many rows per sequence and kv head (paged_tile.cuh): whether it takes the
 // call, its part of the workspace, and the launch.
 bool paged_tile_serves(const PagedLaunch& L);
 size_t paged_tile_workspace(const PagedLaunch& L);
-int64_t paged_tile_items(const PagedLaunch& L);   // at most, and the keys of a tile
+int64_t paged_tile_tokens(const PagedLaunch& L);  // of an item, and the keys of a tile
 int paged_tile_keys(const PagedLaunch& L);
-int paged_tile_blocks(const PagedLaunch& L);
 cudaError_t launch_paged_tile(const PagedLaunch& L, cudaStream_t stream, const char** why);
 cudaError_t launch_paged_tile_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
 // The kernel for up to 16 rows per sequence and kv head of the calls with a window or a prefix
 // (paged_tokens.cu).  Its workspace is paged_attention's for the same sizes.
 bool paged_tokens_serves(const PagedLaunch& L);
-int paged_tokens_blocks(const PagedLaunch& L);
 cudaError_t launch_paged_tokens(const PagedLaunch& L, cudaStream_t stream, const char** why);
 
 struct ReadLaunch {

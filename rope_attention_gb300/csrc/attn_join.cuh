@@ -72,9 +72,7 @@ struct SharedPrefix {
 __device__ __forceinline__ int32_t prefix_length(const SharedPrefix& x) { return x.len ? min(max(__ldg(x.len), 0), x.cap) : 0; }
 
 // Rows that another call's rows join (attention.h, PagedLaunch): its results in fp32, with log2 of
-// their sums of exponentials and the lse's share of the key offsets.  The call that reads them was launched
-// while the one that writes them ran: its kernel waits for that before it reads them, and every
-// block before it ends, so that whatever waits for this kernel has waited for both.
+// their sums of exponentials and the lse's share of the key offsets.
 struct Prior {
   float* rows_out;
   float2* stats_out;
@@ -210,7 +208,6 @@ __device__ __forceinline__ float2 join_row_end(const JoinParams& p, const JoinRo
 template <bool F16, int RESIDENT, bool EXT>
 __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(const __grid_constant__ JoinParams p, int32_t search) {
   __shared__ float4 sum[kJoinWarps][32];
-  if (EXT) grid_launch_dependents();
   grid_dependency_wait();                   // launched while the main kernel's last blocks still run
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NR = p.NR, slices = (p.Dv + 127) / 128;
@@ -436,22 +433,6 @@ __global__ void __launch_bounds__(kJoinThreads, RESIDENT) attention_join_kernel(
     __syncthreads();
   }
   }
-}
-
-// Launches a call's kernel; one whose rows join another's (Prior) while that still runs.
-template <class P>
-cudaError_t launch_main(void (*kernel)(P), const P& p, int blocks, int threads, int smem, bool early, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // The join behind a main kernel of `blocks` blocks over at most `items` items; it is put in

@@ -10,53 +10,55 @@ cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, con
 }
 
 namespace {
-// blocks that a call launches
-int paged_extended_blocks(const PagedLaunch& L) {
-  if (paged_tile_serves(L)) return paged_tile_blocks(L);
-  if (paged_tokens_serves(L)) return paged_tokens_blocks(L);
-  Plan pl{};
-  return plan(L, &pl) ? std::min(pl.G, launch_blocks(L)) : 0;
-}
-
-// Cycles of a call's blocks for `keys` keys of every sequence, roughly: the tiles shared out, at what one of
-// its kernel takes (measured over prefixes of 2000 to 20000 positions).
-double call_cycles(const PagedLaunch& L, int64_t keys) {
-  double tiles, each;
+// What a call over `keys` keys of every sequence takes, roughly, in cycles: items of so many tiles, whole or
+// shared out and joined, what a tile of its kernel takes, an item's beginning and end, and a block's start (launch
+// included).  Fitted to calls over 500 to 20000 positions on 8 to 152 SMs.
+constexpr double kJoinCycles = 15000;
+struct CallCost {
+  double items, each, start, end, tiles;
+  bool whole;
+  double cycles(int blocks) const {
+    const double most = std::ceil(items / blocks);
+    return start + most * end + (whole ? most * tiles * each : std::ceil(items * tiles / blocks) * each + kJoinCycles);
+  }
+};
+CallCost call_cost(const PagedLaunch& L, int64_t keys) {
+  CallCost c{};
+  int kt = kKeys;
+  const int64_t mean = (L.total_q + L.B - 1) / L.B;     // tokens of a sequence
+  const auto items = [&](const Plan& pl) {
+    return static_cast<double>((pl.hblocks > 1 ? L.total_q * pl.hblocks : L.B * ((mean + pl.tb - 1) / pl.tb)) * L.N);
+  };
   if (paged_tile_serves(L)) {
-    const int kt = paged_tile_keys(L);
-    tiles = static_cast<double>(paged_tile_items(L)) * ((keys + kt - 1) / kt);
-    each = 3500;
+    kt = paged_tile_keys(L);
+    const int64_t tokens = paged_tile_tokens(L);
+    const bool half = 2 * mean <= tokens;     // one of an item's two row tiles
+    c = CallCost{static_cast<double>(L.B * ((mean + tokens - 1) / tokens) * L.N), half ? 2700. : 3500., half ? 20000. : 30000.,
+                 half ? 12000. : 17000., 0, false};
   } else {
     Plan pl{};
-    const bool tokens = paged_tokens_serves(L);
-    if (tokens) plan_tokens(L, &pl);
-    else if (!plan(L, &pl)) return 0;
-    tiles = static_cast<double>(pl.items) * ((keys + kKeys - 1) / kKeys);
-    each = tokens ? 1150 : L.variant == 1 ? 4000 : 3300;
+    if (paged_tokens_serves(L)) {
+      plan_tokens(L, &pl);
+      c = CallCost{items(pl), 1150, 17000, 3000, 0, pl.whole != 0};
+    } else if (plan(L, &pl)) {
+      c = CallCost{items(pl), L.variant == 1 ? 4000. : 3300., 30000, L.kq || L.vq ? 16000. : 4000., 0, pl.whole != 0};
+    }
   }
-  return std::ceil(tiles / device_sm_count()) * each;
+  c.tiles = static_cast<double>((keys + kt - 1) / kt);
+  return c;
 }
 }  // namespace
 
-// Sharing the prefix's reads takes a second call (its start, its join, and the fp32 rows on their way from
-// one to the other), and pays where that many tiles need not be read again.  (64 heads over 8, int8,
-// sequences of 512, one call and two: 16 of them behind 2000 positions 31 and 40 us, 32 of them 53 and 45,
-// behind 8192 141 and 59, 61 of them 258 and 91; the latent under 16 heads, 32 sequences: 500 27 and
-// 28, 2000 37 and 34, 8192 76 and 46; under 128 heads, whose tiles one sequence fills, 20000 300 and 488.)
-bool prefix_is_shared(const PagedLaunch& over, const PagedLaunch& behind) {
-  const double second = over.variant == 1 ? 14000 : paged_tokens_serves(over) ? 16000 : 26000;
+// The second call costs a launch, a start, a join and the fp32 rows on their way to it, and pays where that many
+// tiles need not be read again.  (us in one call and in two: 64 heads over 8, int8, sequences of 512: 16 of them behind
+// 1500 positions 27 and 44, behind 8192 78 and 49; 32 of them behind 1500 47 and 50, behind 20000 312 and 94.  The latent
+// under 16 heads, 32 sequences behind 1500 33 and 44, 8192 75 and 61; under 128 heads, whose tiles one sequence fills,
+// behind 20000 300 and 322.  Chunks of up to 64 tokens, 32 heads over 4, 32 sequences behind 4000 143 and 168, 20000 493 and 439.)
+bool prefix_is_shared(const PagedLaunch& own, const PagedLaunch& over, const PagedLaunch& behind) {
+  const int sms = device_sm_count();
   const double rows = static_cast<double>(over.total_q) * over.heads * over.Dv * sizeof(float) / 700;  // bytes a cycle, there and back
-  return call_cycles(behind, behind.max_prefix_len) > call_cycles(over, over.max_seq_len) + second + rows;
-}
-
-// Blocks for the call over the prefix, 0 for all: the SMs that the sequences' own call leaves, where those take
-// less longer over it than waiting for the others would (its start and its end beside its tiles).
-int prefix_blocks(const PagedLaunch& own, const PagedLaunch& over) {
-  constexpr double kStartAndEnd = 25000;
-  const int sms = device_sm_count(), taken = paged_extended_blocks(own);
-  if (taken >= sms) return 0;
-  const double later = call_cycles(own, own.max_seq_len) + kStartAndEnd;
-  return call_cycles(over, over.max_seq_len) * taken / (sms - taken) < later && 2 * taken <= sms ? sms - taken : 0;
+  const double two = call_cost(own, own.max_seq_len).cycles(sms) + call_cost(over, over.max_seq_len).cycles(sms) + rows;
+  return two < call_cost(behind, behind.max_prefix_len + own.max_seq_len).cycles(sms);
 }
 
 }  // namespace ra

@@ -1006,7 +1006,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       // ---- epilogue: final rows, or the piece's statistics and accumulator
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1);
       const bool whole = w.whole();
-      if (EXT && whole && p.join.prior.rows) grid_dependency_wait();
       if (half == 0 && row < NR) {
         l += xch[NR + row];
         inv_sum[row] = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is 0; a NaN stays one
@@ -1065,7 +1064,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (EXT && p.join.prior.rows) grid_dependency_wait();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
@@ -1081,9 +1079,6 @@ struct Plan {
 
 bool p_in_two(const PagedLaunch& L) { return L.f16 && (L.kq != 0 || L.vq != 0); }
 int p_bytes(const PagedLaunch& L, int nr) { return nr * 128 * (p_in_two(L) ? 2 : 1); }
-
-// blocks that a call may have
-int launch_blocks(const PagedLaunch& L) { return L.most_blocks > 0 ? L.most_blocks : device_sm_count(); }
 
 // The row tiles of NR rows, and the blocks that share their key tiles: one per SM, and no more than there
 // are tiles at the largest lengths.  whole(T): whether items of T tiles at most are not cut.
@@ -1166,7 +1161,8 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  e = launch_main(kernel, p, blocks, kThreads, smem, EXT && p.join.prior.rows, stream);
+  kernel<<<blocks, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return p.whole ? cudaSuccess : launch_join<EXT>(p.join, F16, blocks, items, stream);
 }
@@ -1251,7 +1247,7 @@ cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** 
     return cudaErrorInvalidValue;
   }
   Params p = row_params(L, pl);
-  pl.G = std::min(pl.G, launch_blocks(L));
+  pl.G = std::min(pl.G, device_sm_count());
   if (!encode_maps([&] {
         return make_q_map(&p.tq, L, pl.hb, pl.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
                make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows);

@@ -16,9 +16,8 @@ bool paged_tile_serves(const PagedLaunch& L) {
          L.total_q * g > kRows * L.B;
 }
 
-int64_t paged_tile_items(const PagedLaunch& L) { return most_items(L); }
+int64_t paged_tile_tokens(const PagedLaunch& L) { return 2 * (kTileRows / (L.heads / static_cast<int32_t>(L.N))); }
 int paged_tile_keys(const PagedLaunch& L) { return keys_per_tile(L); }
-int paged_tile_blocks(const PagedLaunch& L) { return std::min(most_blocks(L), device_sm_count()); }
 
 size_t paged_tile_workspace(const PagedLaunch& L) { return join_bytes(most_blocks(L), 2 * kTileRows, L.Dv); }
 

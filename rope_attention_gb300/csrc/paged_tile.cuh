@@ -92,7 +92,7 @@ cudaError_t launch_tile_over_pages(const PagedLaunch& L, cudaStream_t stream, co
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
-  const int n = std::min(blocks, L.most_blocks > 0 ? L.most_blocks : device_sm_count());
+  const int n = std::min(blocks, device_sm_count());
   const int64_t items = most_items(L);
   if (L.kq) {
     if (L.Dkv <= 128)

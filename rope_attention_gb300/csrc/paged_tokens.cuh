@@ -57,7 +57,7 @@ inline void plan_tokens(const PagedLaunch& L, Plan* pl) {
   // window: 8 items of 9 tiles 14.1 us whole and 14.4 cut, of 15 16.4 and 14.4; 64 items of 15 18.5 and 22.0, of 28
   // 24.6 and 24.6; 256 items of 28 43 and 48, of 53 70 and 70.)
   share_out(L, pl, [&](int64_t T) {
-    const double share = static_cast<double>(pl->items) / launch_blocks(L), rounds = std::ceil(share);
+    const double share = static_cast<double>(pl->items) / device_sm_count(), rounds = std::ceil(share);
     return (rounds - share) * static_cast<double>(T) <= 5 + 12 * std::min(4 * share, 1.0);
   });
   // the workspace is sized for paged_attention's kernel, whose row tiles hold more rows

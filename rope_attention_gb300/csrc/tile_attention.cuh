@@ -396,7 +396,7 @@ __device__ __forceinline__ float tile_half(uint32_t u) {
 // Hides a row's keys from nv on and those of [lo, hi), 32 columns at a time: a choice for each element only
 // where some row of the warp does not see all of them.  (A comparison and a choice for each of 128 columns,
 // on a pipe of half the rate, took 1600 cycles of a masked tile's 3200: 9001 tokens of 7 prompts in a
-// window of 1024 166 us, XX with this.)
+// window of 1024 166 us, 162 with this.)
 template <int KT>
 __device__ __forceinline__ void hide_keys(uint32_t (&s)[KT], int32_t nv, int32_t lo, int32_t hi) {
   if (!__any_sync(0xffffffffu, nv < KT || (hi > lo && lo < KT))) return;
@@ -1094,7 +1094,6 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
       const int64_t at = EXT ? token * p.join.heads + head : 0;
       if (live) {
         if (EXT && whole && (p.join.prior.stats_out || p.join.prior.stats)) {
-          if (p.join.prior.stats) grid_dependency_wait();
           prior_end(p.join.prior, at, fmaf(m, sl2, -kLift), l, l != 0.f ? shift : 0.f, true, p.join.lse, share);
         } else if (whole) {
           if (p.join.lse)
@@ -1165,7 +1164,6 @@ __global__ void __launch_bounds__(QUANT ? 512 : 384, 1) tile_attention_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (EXT && p.join.prior.rows) grid_dependency_wait();
   if (threadIdx.x == 0 && *abort_flag) *p.status = 1;
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
@@ -1185,7 +1183,8 @@ cudaError_t launch_tile(const TileParams& p, int blocks, int64_t items, bool cut
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  e = launch_main(kernel, p, blocks, SH::kThreads, smem, EXT && p.join.prior.rows, stream);
+  kernel<<<blocks, SH::kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return cuts ? launch_join<EXT>(p.join, F16, blocks, items, stream) : cudaSuccess;
 }

@@ -134,10 +134,12 @@ def test_many_sequences_share_other_widths_and_tokens(kt):
     Case(24, variant=2, lens=[40] * 40, news=[18] * 40, heads=16, N=8, prefix=2000, kt=kt, vt=kt).run_and_check()
 
 
+@pytest.mark.parametrize("prefix", [1100, 4000])
 @pytest.mark.parametrize("kt,vt", [("bf16", "bf16"), ("int8", "int8"), ("int8", "bf16"), ("bf16", "e5m2")])
-def test_many_sequences_share_v1(kt, vt):
+def test_many_sequences_share_v1(kt, vt, prefix):
     lens = [(5 * i) % 30 for i in range(150)]
-    Case(25, variant=1, lens=lens, news=tokens_of(lens, 2), heads=16, Dkv=576, Dv=512, kt=kt, vt=vt, prefix=1100).run_and_check()
+    Case(25, variant=1, lens=lens, news=tokens_of(lens, 2), heads=16, Dkv=576, Dv=512, kt=kt, vt=vt,
+         prefix=prefix).run_and_check()
 
 
 def test_many_sequences_share_fp16_bad_pages_and_no_prefix_after_all():

@@ -49,7 +49,7 @@ CASES = {
     "prefix_v1": lambda s: Case(s, lens=[90, 77], news=[1, 2], prefix=300, **V1),
     "prefix_chunk_int8": lambda s: Case(s, lens=[200, 150], news=[120, 120], prefix=300, kt="int8", vt="int8", **FEW),
     "prefix_shared": lambda s: Case(s, kt="int8", vt="int8", **SHARED),
-    "prefix_shared_v1": lambda s: Case(s, lens=[(5 * i) % 30 for i in range(150)], news=[1] * 150, prefix=1100, **V1),
+    "prefix_shared_v1": lambda s: Case(s, lens=[(5 * i) % 30 for i in range(150)], news=[1] * 150, prefix=4000, **V1),
 }
 
 
