@@ -1021,13 +1021,10 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
     over.table = prefix_table;
     over.prior = own.rows_out;
     over.prior_stats = own.stats_out;
-    L = behind_prefix(L, x, prefix_len, prefix_table);
-    if (ra::prefix_is_shared(own, over, L)) {
-      e = ra::launch_paged_extended(own, cs, &why);
-      L = over;
-    }
+    e = ra::launch_paged_prefix(own, over, behind_prefix(L, x, prefix_len, prefix_table), cs, &why);
+  } else {
+    e = w ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
   }
-  if (e == cudaSuccess) e = w || x ? ra::launch_paged_extended(L, cs, &why) : ra::launch_paged_attention(L, cs, &why);
   if (e != cudaSuccess)
     return fail(RA_ERR_CUDA, "%s: %s (%s)", x ? "paged_prefix_attention" : w ? "paged_window_attention" : "paged_attention", why,
                 cudaGetErrorString(e));

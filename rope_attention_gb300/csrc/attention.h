@@ -70,9 +70,10 @@ size_t paged_attention_workspace(const PagedLaunch& L);
 cudaError_t launch_paged_attention(const PagedLaunch& L, cudaStream_t stream, const char** why);
 // with a window, rows_out or prior
 cudaError_t launch_paged_extended(const PagedLaunch& L, cudaStream_t stream, const char** why);
-// Whether sequences behind a shared prefix are served in two calls (`own` positions, then `over` the prefix) or in
-// one (`behind` it).
-bool prefix_is_shared(const PagedLaunch& own, const PagedLaunch& over, const PagedLaunch& behind);
+// Sequences behind a shared prefix, in one call (`behind` it) or in two (their `own` positions, then `over` the
+// prefix, whose rows join the own).
+cudaError_t launch_paged_prefix(const PagedLaunch& own, const PagedLaunch& over, const PagedLaunch& behind, cudaStream_t stream,
+                                const char** why);
 // The kernel for many rows per sequence and kv head (paged_tile.cuh): whether it takes the
 // call, its part of the workspace, and the launch.
 bool paged_tile_serves(const PagedLaunch& L);

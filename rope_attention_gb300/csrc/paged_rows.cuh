@@ -113,8 +113,31 @@ struct Params {
   Window window;
   int32_t cu_step, shifts;
   SharedPrefix prefix;
+  int32_t join_all;             // of two calls in one launch: the rows of items that no cut goes through are joined too
   const uint16_t* q;            // paged_tokens.cu, which does without tq
 };
+
+// A launch: one call, or (EXT) two on blocks of their own, whose results the join behind both puts together.
+template <bool EXT>
+struct Calls {
+  Params a;
+};
+template <>
+struct Calls<true> {
+  Params a, b;
+  int32_t split;                // blocks of the first
+};
+__device__ __forceinline__ const Params& call_of(const Calls<false>& c, int32_t& block, int32_t& blocks) {
+  block = blockIdx.x;
+  blocks = gridDim.x;
+  return c.a;
+}
+__device__ __forceinline__ const Params& call_of(const Calls<true>& c, int32_t& block, int32_t& blocks) {
+  const bool second = static_cast<int32_t>(blockIdx.x) >= c.split;
+  block = second ? blockIdx.x - c.split : blockIdx.x;
+  blocks = second ? gridDim.x - c.split : c.split;
+  return second ? c.b : c.a;
+}
 
 // What the threads of a block tell each other to find its run.
 template <int THREADS>
@@ -266,7 +289,8 @@ struct Walker {
 // sequences every warp finds it for itself, beside the set-up of the block (a block-wide scan
 // behind it cost a short decode step 2.5k cycles more).  start_run ends it, behind a __syncthreads.
 template <bool EXT, int THREADS, int ROOM>
-__device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, RunScan<ROOM>& ms, int64_t& per, int64_t& start) {
+__device__ __forceinline__ void find_run(const Params& p, int32_t block, int32_t blocks, Walker<EXT>& walk, RunScan<ROOM>& ms,
+                                         int64_t& per, int64_t& start) {
   static_assert(THREADS <= ROOM, "");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   walk.b = p.B;
@@ -307,10 +331,10 @@ __device__ __forceinline__ void find_run(const Params& p, Walker<EXT>& walk, Run
       W += t;
     }
   }
-  const int64_t G = gridDim.x;
+  const int64_t G = blocks;
   const int64_t even = W >> 31 ? (W + G - 1) / G : static_cast<int64_t>((static_cast<uint32_t>(W) + static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(G));
   per = max(even, static_cast<int64_t>(1));
-  start = per * blockIdx.x;
+  start = per * block;
   walk.rem = max(static_cast<int64_t>(0), min(per, W - start));  // none: the block has nothing to do
   const bool here = before <= start && start < before + mine;
   if (few) {
@@ -527,7 +551,9 @@ __device__ __forceinline__ void write_rows(const Params& p, const Piece& w, bool
 // rounding does not add a third error of that size, P goes in as two fp16 numbers (hi + lo).
 // EXT: windows; rows that leave in fp32 for another call, or join another's (Prior).
 template <bool F16, bool P16, bool PLO, bool EXT>
-__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Calls<EXT> calls) {
+  int32_t block, blocks;
+  const Params& p = call_of(calls, block, blocks);
   constexpr float kLift = P16 ? kHalfLift : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + p.off_misc);
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     mbar_init(smem_u32(&ms.drain), 1);
     ms.abort = 0;
     fence_mbar_init();
-    p.join.meta[8 * blockIdx.x] = 0;         // nothing to join, unless the first piece says so below
+    p.join.meta[8 * block] = 0;         // nothing to join, unless the first piece says so below
   } else if (threadIdx.x == 32 * kLoadWarp) {
     prefetch_tensormap(&p.tq);
     prefetch_tensormap(&p.tk);
@@ -574,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   // ---- this block's run of tiles
   Walker<EXT> walk;
   int64_t per, start;
-  find_run<EXT, kThreads>(p, walk, ms.run, per, start);
+  find_run<EXT, kThreads>(p, block, blocks, walk, ms.run, per, start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -868,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         // the block behind the first cut through an item joins the item's pieces
         const int64_t item0 = start - w.t0;
         const int32_t first = static_cast<int32_t>(item0 / per), last = static_cast<int32_t>((item0 + w.T - 1) / per);
-        int32_t* mt = p.join.meta + 8 * blockIdx.x;
+        int32_t* mt = p.join.meta + 8 * block;
         mt[1] = first;
         mt[2] = last;
         mt[3] = w.rows;
@@ -876,7 +902,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         mt[5] = w.q_start + w.tok;
         mt[6] = w.head;
         mt[7] = w.n;
-        mt[0] = first + 1 == static_cast<int32_t>(blockIdx.x) ? 1 : 0;
+        mt[0] = first + 1 == block ? 1 : 0;
+      }
+      if (EXT && p.join_all && tid == 0 && w.whole()) {
+        // a part by itself (more blocks than items: the only piece of the block)
+        int32_t* mt = p.join.meta + 8 * block;
+        mt[1] = mt[2] = block;
+        mt[3] = w.rows;
+        mt[4] = 0;
+        mt[5] = w.q_start + w.tok;
+        mt[6] = w.head;
+        mt[7] = w.n;
+        mt[0] = 1;
       }
       if (k_quant && n > 0) {
         ok = scale_q<F16, EXT>(p, w.n, w.rows, smem, row_scale, row_const, warp, lane, smem_u32(&ms.q_full), loaded & 1, abort_flag);
@@ -1004,8 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       jt += n;
 
       // ---- epilogue: final rows, or the piece's statistics and accumulator
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece == 0 && w.t0 > 0 ? 0 : 1);
-      const bool whole = w.whole();
+      const int64_t slot = 2 * static_cast<int64_t>(block) + (piece == 0 && w.t0 > 0 ? 0 : 1);
+      const bool whole = w.whole() && !(EXT && p.join_all);
       if (half == 0 && row < NR) {
         l += xch[NR + row];
         inv_sum[row] = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is 0; a NaN stays one
@@ -1150,7 +1187,7 @@ bool plan(const PagedLaunch& L, Plan* pl) {
 }
 
 template <bool F16, bool P16, bool PLO, bool EXT>
-cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStream_t stream) {
+cudaError_t launch(const Calls<EXT>& calls, int blocks, int smem, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1161,10 +1198,14 @@ cudaError_t launch(const Params& p, int blocks, int64_t items, int smem, cudaStr
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  kernel<<<blocks, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return p.whole ? cudaSuccess : launch_join<EXT>(p.join, F16, blocks, items, stream);
+  kernel<<<blocks, kThreads, smem, stream>>>(calls);
+  return cudaGetLastError();
+}
+template <bool EXT>
+cudaError_t launch_calls(const PagedLaunch& L, const Calls<EXT>& calls, int blocks, int smem, cudaStream_t stream) {
+  if (L.f16)
+    return p_in_two(L) ? launch<true, true, true, EXT>(calls, blocks, smem, stream) : launch<true, true, false, EXT>(calls, blocks, smem, stream);
+  return L.vq ? launch<false, true, false, EXT>(calls, blocks, smem, stream) : launch<false, false, false, EXT>(calls, blocks, smem, stream);
 }
 
 // what a launch's kernel takes from the call and its plan
@@ -1239,40 +1280,45 @@ Params row_params(const PagedLaunch& L, const Plan& pl) {
   return p;
 }
 
-template <bool EXT>
-cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** why) {
-  Plan pl;
-  if (!plan(L, &pl)) {
+// the parameters of a call and its plan
+bool prepare_rows(const PagedLaunch& L, Plan* pl, Params* to, const char** why) {
+  if (!plan(L, pl)) {
     *why = "no tile shape fits";
-    return cudaErrorInvalidValue;
+    return false;
   }
-  Params p = row_params(L, pl);
-  pl.G = std::min(pl.G, device_sm_count());
+  Params& p = *to;
+  p = row_params(L, *pl);
   if (!encode_maps([&] {
-        return make_q_map(&p.tq, L, pl.hb, pl.tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
+        return make_q_map(&p.tq, L, pl->hb, pl->tb) && make_map(&p.tv, L.v_cache, L, L.Dv, L.vq, p.box_rows) &&
                make_map(&p.tk, L.k_cache, L, p.Dko, L.kq, p.box_rows);
       })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
-    return cudaErrorInvalidValue;
+    return false;
   }
-  p.vslabs = pl.vslabs;
-  p.kslabs = pl.kslabs;
-  p.qslabs = pl.qslabs;
-  p.kslab0 = pl.kslab0;
-  p.ns = pl.ns;
-  p.nsg = pl.nsg;
-  p.stage_bytes = pl.stage;
-  p.staging_bytes = pl.staging;
-  p.off_p = pl.off_p;
-  p.off_ring = pl.off_ring;
-  p.off_staging = pl.off_staging;
-  p.off_misc = pl.off_misc;
+  p.vslabs = pl->vslabs;
+  p.kslabs = pl->kslabs;
+  p.qslabs = pl->qslabs;
+  p.kslab0 = pl->kslab0;
+  p.ns = pl->ns;
+  p.nsg = pl->nsg;
+  p.stage_bytes = pl->stage;
+  p.staging_bytes = pl->staging;
+  p.off_p = pl->off_p;
+  p.off_ring = pl->off_ring;
+  p.off_staging = pl->off_staging;
+  p.off_misc = pl->off_misc;
+  return true;
+}
 
-  if (L.f16)
-    return p_in_two(L) ? launch<true, true, true, EXT>(p, pl.G, pl.items, pl.smem, stream)
-                       : launch<true, true, false, EXT>(p, pl.G, pl.items, pl.smem, stream);
-  return L.vq ? launch<false, true, false, EXT>(p, pl.G, pl.items, pl.smem, stream)
-              : launch<false, false, false, EXT>(p, pl.G, pl.items, pl.smem, stream);
+template <bool EXT>
+cudaError_t launch_rows(const PagedLaunch& L, cudaStream_t stream, const char** why) {
+  Plan pl;
+  Calls<EXT> calls{};
+  if (!prepare_rows(L, &pl, &calls.a, why)) return cudaErrorInvalidValue;
+  const int blocks = std::min(pl.G, device_sm_count());
+  if constexpr (EXT) calls.split = blocks;
+  const cudaError_t e = launch_calls<EXT>(L, calls, blocks, pl.smem, stream);
+  return e != cudaSuccess || pl.whole ? e : launch_join<EXT>(calls.a.join, L.f16, blocks, pl.items, stream);
 }
 
 }  // namespace

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
   grid_launch_dependents();
   Walker<true> walk;
   int64_t per, start;
-  if (p.B > 32 || warp >= kTokenWarps) find_run<true, kTokenThreads>(p, walk, ms.run, per, start);  // (B > 32: with a barrier)
+  if (p.B > 32 || warp >= kTokenWarps) find_run<true, kTokenThreads>(p, blockIdx.x, gridDim.x, walk, ms.run, per, start);  // (B > 32: with a barrier)
   __syncthreads();
   volatile int* abort_flag = &ms.abort;
   Piece w{};

@@ -156,3 +156,20 @@ def test_many_sequences_share_fp16_bad_pages_and_no_prefix_after_all():
     torch.cuda.synchronize()
     assert c.status() == 0
     c.check("no prefix")
+
+
+@pytest.mark.parametrize("kt", ["bf16", "int8"])
+def test_two_calls_in_one_launch_sized_for_a_longer_prefix(kt):
+    # the latent: each of the prefix's row tiles is cut over many blocks, or is one block's where it is short
+    for B, prefix in ((150, 1), (8, 65), (9, 16000), (5, 130), (61, 64)):
+        lens = [(11 * i) % 90 for i in range(B)]
+        c = Case(30, variant=1, lens=lens, news=tokens_of(lens, 2), heads=16, Dkv=576, Dv=512, kt=kt, vt=kt, prefix=prefix,
+                 spare=20000 - prefix, tail=2)
+        c.run_and_check()
+        c.prefix_len.fill_(0)
+        c.ref_args["prefix_len"] = 0
+        c.run()
+        torch.cuda.synchronize()
+        assert c.status() == 0
+        c.check("no prefix")
+    Case(31, variant=2, lens=[40] * 61, news=[1] * 61, heads=16, N=4, Dkv=256, Dv=208, R=64, kt=kt, vt=kt, prefix=9000).run_and_check()
