@@ -636,7 +636,8 @@ typedef struct {
   int64_t B;                  /* requests, 1 .. 16384                                  */
   int64_t block_num;          /* pages of the cache                                    */
   int64_t block_size;         /* slots per page                                        */
-  int64_t block_table_stride; /* entries per row of block_table; B times this < 2^31   */
+  int64_t block_table_stride; /* entries per row of block_table; with B rows at most
+                                 2^31 - 256                                            */
   int64_t max_tokens;         /* entries of index, <= 2^30 (kv_cache_truncate: any)    */
 } kv_cache_paging_params;
 

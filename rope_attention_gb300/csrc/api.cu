@@ -1107,8 +1107,8 @@ static ra_status check_paging(const kv_cache_paging_params* p) {
   if (p->block_table_stride < 1 || p->block_table_stride > 0x7fffffffLL)
     return fail(RA_ERR_INVALID_ARG, "block_table_stride must be in [1, 2^31)");
   if (p->B > ra::kPagingRequests) return fail(RA_ERR_UNSUPPORTED, "the paging calls are built for up to 16384 requests");
-  if (p->B * p->block_table_stride > 0x7fffffffLL || p->max_tokens > ra::kPagingTokens)
-    return fail(RA_ERR_UNSUPPORTED, "the paging calls are built for block tables below 2^31 entries and up to 2^30 tokens");
+  if (p->B * p->block_table_stride > ra::kPagingEntries || p->max_tokens > ra::kPagingTokens)
+    return fail(RA_ERR_UNSUPPORTED, "the paging calls are built for block tables of up to 2^31 - 256 entries and up to 2^30 tokens");
   return RA_OK;
 }
 static bool aligned4(std::initializer_list<const void*> ptrs) {

@@ -8,6 +8,7 @@ namespace ra {
 
 constexpr int64_t kPagingRequests = 16384;     // of a call: three words of shared memory each
 constexpr int64_t kPagingTokens = 1LL << 30;
+constexpr int64_t kPagingEntries = 0x7fffff00;   // of a block table: indexes a little behind its end stay within 31 bits
 
 struct PagingLaunch {
   int64_t B, block_num, block_size, table_stride, max_tokens;

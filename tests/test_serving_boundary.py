@@ -304,3 +304,10 @@ def test_oracle_paging_by_hand():
     assert back["free_pages"][:3].tolist() == [9, 8, 6] and back["new_free_count"] == 3
     s = oracle.paging.slots([14], [4], np.array([[2, 11]]), block_num=10, block_size=16, max_tokens=5)
     assert s["index"].tolist() == [46, 47, -1, -1, -1] and s["errors"] == 2 and s["cu_seqlens"].tolist() == [0, 4]
+
+
+def test_block_tables_stay_within_31_bits(L):
+    for stride, code in (((1 << 31) - 256, 0), ((1 << 31) - 255, -2), ((1 << 31) - 1, -2)):
+        for name in ("kv_cache_extend", "kv_cache_slots", "kv_cache_truncate"):
+            st, msg = call_paging(L, name, paging(B=1, block_table_stride=stride))
+            assert st == code and (st == 0) == (msg == "")
