@@ -600,7 +600,7 @@ ra_status paged_prefix_attention_workspace_bytes(const kv_rms_norm_rope_cache_pa
                                                  const attention_prefix* prefix, size_t* bytes);
 
 /* paged_attention of sequences behind a shared prefix, whose keys are read once for the
- * rows of all of them.  The keys of sequence b are the prefix's positions, which every
+ * rows of all of them where that takes less time.  The keys of sequence b are the prefix's positions, which every
  * query of the call sees, then its own: seq_lens, max_seq_len and block_table count and
  * hold its own positions alone, of which its queries see those that paged_attention
  * lets them see.
