@@ -49,7 +49,11 @@ inline void plan_tokens(const PagedLaunch& L, Plan* pl) {
   // where the warps' results meet, and two pieces' queries
   const int meet = kTokenWarps * pl->NR * kTokenRow * 4 + 2 * pl->NR / 8 * 24 * 32 * 4;
   const int fixed = meet + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
-  pl->ns = std::min(kTokenStages, (kSmemMax - fixed) / pl->stage);
+  // As many for each team: a stage then is always one team's, which waits for its uses one after the other.  (A
+  // wait knows a use of a stage from the one before by a parity alone.  With an odd number the teams take turns on
+  // a stage, and one could come to it while the copy of the other's tile, issued earlier, had still not landed,
+  // and take that for its own.)
+  pl->ns = std::min(kTokenStages, (kSmemMax - fixed) / pl->stage) / kTeams * kTeams;
   pl->off_p = pl->ns * pl->stage;
   pl->off_misc = pl->off_p + meet;
   pl->smem = pl->off_misc + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);

@@ -173,3 +173,19 @@ def test_two_calls_in_one_launch_sized_for_a_longer_prefix(kt):
         assert c.status() == 0
         c.check("no prefix")
     Case(31, variant=2, lens=[40] * 61, news=[1] * 61, heads=16, N=4, Dkv=256, Dv=208, R=64, kt=kt, vt=kt, prefix=9000).run_and_check()
+
+
+@pytest.mark.parametrize("kt,heads,window", [("bf16", 8, None), ("int8", 16, None), ("bf16", 8, 2500), ("int8", 16, 3000), ("bf16", 32, 2000)])
+def test_many_passes_give_the_same_bits(kt, heads, window):
+    # long runs of tiles from pages all over the cache, whose copies land in any order
+    lens = [(397 * i) % 3000 + 1 for i in range(61)]
+    form = dict(window=window, sinks=4) if window else dict(prefix=9000)
+    c = Case(32, variant=2, lens=lens, news=[1] * 61, heads=heads, N=2, Dkv=128, Dv=128, bs=128, kt=kt, vt=kt, **form)
+    c.run_and_check()
+    out = torch.full_like(c.out, 7.0)
+    for _ in range(20):
+        for _ in range(150):
+            c.run(out=out, lse=None)
+        torch.cuda.synchronize()
+        assert c.status() == 0
+        assert torch.equal(out.view(torch.int16), c.out.view(torch.int16))
