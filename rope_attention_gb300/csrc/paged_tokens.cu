@@ -15,7 +15,7 @@
 //    the same: a lane takes 16 neighbouring channels of its keys for four steps (q is laid out to match), and
 //    of the values 16 neighbouring channels of four keys, whose bytes it interleaves.  Rows of 192 and
 //    64 bytes, and of 128 with the swizzle, then have no bank conflicts.
-//  * Another warp walks the block table and issues TMA boxes of 16 to 64 keys, two to eight tiles ahead and more:
+//  * Another warp walks the block table and issues TMA boxes of 16 to 64 keys, two to twelve tiles ahead:
 //    whole rows of codes, 128 bytes of 16-bit ones.  A third walks the pieces ahead of the others and
 //    lays out their queries.
 // The runs of tiles, their parts and the join are paged_rows.cuh's.  The maximum follows only when a
