@@ -294,11 +294,12 @@ Params make_params(const PagingLaunch& L) {
   return p;
 }
 
-cudaError_t launch(void (*kernel)(Params), Params p, int64_t blocks, int threads, bool cluster, cudaStream_t stream) {
+template <auto KERNEL>
+cudaError_t launch(Params p, int64_t blocks, int threads, bool cluster, cudaStream_t stream) {
   const int smem = static_cast<int>(p.L.B) * 12;
   p.per_thread = static_cast<int32_t>((p.L.B + threads - 1) / threads);
   cudaError_t e = cudaSuccess;
-  if (smem > 40 << 10) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 40 << 10) e = allow_all_shared_memory<KERNEL>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -310,7 +311,7 @@ cudaError_t launch(void (*kernel)(Params), Params p, int64_t blocks, int threads
   attr.val.clusterDim = {static_cast<unsigned>(blocks), 1, 1};
   cfg.attrs = &attr;
   cfg.numAttrs = cluster && blocks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
 // threads of a block for so many items of its own and so many requests: fewer warps meet sooner
@@ -332,22 +333,24 @@ cudaError_t launch_cache_extend(const PagingLaunch& L, cudaStream_t stream) {
   constexpr int64_t kOneCluster = 1 << 16;
   const Params p = make_params(L);
   if (L.max_tokens > kOneCluster) {
-    const cudaError_t e = launch(slots_kernel<true, 4, kTokens>, p, device_sm_count(), kMostThreads, false, stream);
-    return e != cudaSuccess ? e : launch(slots_kernel<true, 1, kState>, p, 1, threads_for(1, L.B), false, stream);
+    const cudaError_t e = launch<slots_kernel<true, 4, kTokens>>(p, device_sm_count(), kMostThreads, false, stream);
+    return e != cudaSuccess ? e : launch<slots_kernel<true, 1, kState>>(p, 1, threads_for(1, L.B), false, stream);
   }
   const int64_t c = cluster_for(L.max_tokens);
   const int threads = threads_for((L.max_tokens + c - 1) / c, L.B);
-  return launch(c * threads >= L.max_tokens ? slots_kernel<true, 1, kBoth> : slots_kernel<true, 4, kBoth>, p, c, threads, true, stream);
+  return c * threads >= L.max_tokens ? launch<slots_kernel<true, 1, kBoth>>(p, c, threads, true, stream)
+                                     : launch<slots_kernel<true, 4, kBoth>>(p, c, threads, true, stream);
 }
 cudaError_t launch_cache_slots(const PagingLaunch& L, cudaStream_t stream) {
   const int threads = threads_for(L.max_tokens, L.B);
   const int64_t blocks = std::min<int64_t>(device_sm_count(), (L.max_tokens + threads - 1) / threads);
-  return launch(blocks * threads >= L.max_tokens ? slots_kernel<false, 1, kBoth> : slots_kernel<false, 4, kBoth>, make_params(L),
-                blocks, threads, false, stream);
+  const Params p = make_params(L);
+  return blocks * threads >= L.max_tokens ? launch<slots_kernel<false, 1, kBoth>>(p, blocks, threads, false, stream)
+                                          : launch<slots_kernel<false, 4, kBoth>>(p, blocks, threads, false, stream);
 }
 cudaError_t launch_cache_truncate(const PagingLaunch& L, cudaStream_t stream) {
   const int64_t n = std::min(L.block_num, L.B * L.table_stride), c = cluster_for(n);
-  return launch(truncate_kernel, make_params(L), c, threads_for(n / c, L.B), true, stream);
+  return launch<truncate_kernel>(make_params(L), c, threads_for(n / c, L.B), true, stream);
 }
 
 }  // namespace ra

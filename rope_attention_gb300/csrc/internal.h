@@ -3,6 +3,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -85,6 +86,25 @@ struct NormRopeLaunch {
 cudaError_t launch_qk_norm_rope(const NormRopeLaunch& L, cudaStream_t stream);
 
 int device_sm_count();
+
+// Lets KERNEL take all the shared memory that a block can have, once per device.  The limit belongs to the
+// kernel and not to a call: one that calls set to what each needs could be lowered by another host thread's
+// between a call's setting and its launch, which is then refused.
+template <auto KERNEL>
+cudaError_t allow_all_shared_memory() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (ready.load() >> dev & 1)) return cudaSuccess;
+  cudaFuncAttributes own{};
+  e = cudaFuncGetAttributes(&own, KERNEL);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(own.sharedSizeBytes));
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+  return e;
+}
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (null if unavailable)
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

@@ -1,0 +1,86 @@
+"""Calls of one kernel from two host threads at a time, of sizes that need different amounts of shared
+memory, each thread on a stream and on tensors of its own: every call is accepted, whatever the other
+thread launches between its checks and its launch, and the results are the oracle's."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from rope_attention_gb300 import native
+from test_cache_paging import Pages, dev
+
+pytestmark = pytest.mark.gpu
+
+
+def beside_one_another(calls, times):
+    """Each of `calls` (of a stream) `times` times, in a thread of its own."""
+    start, errors = threading.Barrier(len(calls)), []
+
+    def work(call):
+        stream = torch.cuda.Stream()
+        start.wait()
+        try:
+            for i in range(times):
+                call(stream)
+                if i % 100 == 99:
+                    stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+        finally:
+            stream.synchronize()
+
+    for c in calls:                      # what a first call sets up
+        c(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+
+
+class Paging:
+    """extend, slots and truncate of B requests, none of them in place."""
+
+    def __init__(self, seed, B):
+        rng = np.random.default_rng(seed)
+        p = self.p = Pages(seed, rng.integers(0, 60, B), 8, 16, 2 * B)
+        self.new, self.keep = rng.integers(0, 3, B), rng.integers(0, 60, B)
+        self.T = int(self.new.sum()) + 5
+        self.params = p.params(self.T)
+        self.lens, self.count, self.free = dev(p.lens), dev([p.count]), dev(p.free)
+        self.table, self.full, self.back = dev(p.table), dev(p.table), dev(p.free)
+        self.new_d, self.keep_d = dev(self.new), dev(self.keep)
+        out = lambda n: torch.full((n,), 77, dtype=torch.int32, device="cuda")
+        index = lambda: torch.full((self.T,), 77, dtype=torch.int64, device="cuda")
+        self.extended = index(), out(B + 1), out(B), out(1)
+        self.slots = index(), out(B + 1)
+        self.cut = out(B), out(1)
+
+    def __call__(self, stream):
+        native.kv_cache_extend(self.params, self.new_d, self.lens, self.full, self.free, self.count, *self.extended, stream=stream)
+        native.kv_cache_slots(self.params, self.new_d, self.table, *self.slots, stream=stream)
+        native.kv_cache_truncate(self.params, self.lens, self.table, self.back, self.count, *self.cut, keep=self.keep_d, stream=stream)
+
+    def check(self):
+        p = self.p
+        size = dict(block_num=p.block_num, block_size=p.bs)
+        e = oracle.paging.extend(self.new, p.lens, p.table, p.free, p.count, max_tokens=self.T, **size)
+        s = oracle.paging.slots(None, self.new, p.table, max_tokens=self.T, **size)
+        t = oracle.paging.truncate(self.keep, p.lens, p.table, p.free, p.count, **size)
+        got = (*self.extended, self.full, *self.slots, *self.cut, self.back)
+        want = (e["index"], e["cu_seqlens"], e["new_seq_lens"], [e["new_free_count"]], e["table"], s["index"], s["cu_seqlens"],
+                t["new_seq_lens"], [t["new_free_count"]], t["free_pages"])
+        for i, (g, w) in enumerate(zip(got, want)):
+            assert np.array_equal(g.cpu().numpy(), np.asarray(w)), i
+
+
+def test_paging_calls_of_many_and_of_fewer_requests():
+    calls = [Paging(1, 16384), Paging(2, 4000)]
+    beside_one_another(calls, 2000)
+    for c in calls:
+        c.check()
