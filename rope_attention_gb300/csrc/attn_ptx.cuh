@@ -147,16 +147,6 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t
   return sdesc(saddr, mn_stride, 1024, kLayoutSwizzle128B);
 }
 
-// ---------------------------------------------------------------- tensor maps
-// f encodes a launch's maps.  The driver does that in the thread's current context, and a host
-// thread that has made no CUDA call yet has none: it gets the device's own, and f a second try.
-template <class F>
-bool encode_maps(F&& f) {
-  if (f()) return true;
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && f();
-}
-
 // ---------------------------------------------------------------- loads
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y,
                                             int32_t z) {

@@ -121,6 +121,15 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// f encodes a launch's maps.  The driver does that in the thread's current context, and a host
+// thread that has made no CUDA call yet has none: it gets the device's own, and f a second try.
+template <class F>
+bool encode_maps(F&& f) {
+  if (f()) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && f();
+}
+
 // Sets the thread-local message returned by ra_last_error() ("where: what").
 void set_last_error(int code, const char* where, const char* what);
 

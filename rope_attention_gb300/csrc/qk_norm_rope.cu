@@ -621,9 +621,11 @@ cudaError_t launch_nbsd(const NormRopeLaunch& L, const NbPlan& pl, cudaStream_t 
   cuuint32_t box[3] = {static_cast<cuuint32_t>(D), pl.tb, pl.hb};
   cuuint32_t estr[3] = {1, 1, 1};
   void* base = L.out + static_cast<size_t>(h_begin) * L.T * D;
-  if (enc(&tmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  if (!encode_maps([&] {
+        return enc(&tmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+      }))
     return cudaErrorInvalidValue;
   auto kernel = qk_norm_rope_nbsd_kernel<D, ROT>;
   const size_t smem = nb_smem(pl);

@@ -710,9 +710,11 @@ cudaError_t launch_qkv_project(const ProjLaunch& L, cudaStream_t stream, const c
   Params p{};
   const int num_n = static_cast<int>((L.I + BN - 1) / BN), num_k = static_cast<int>(L.H / BK);
   const uint64_t sf_rows = static_cast<uint64_t>(num_n) * num_k * (SF_BYTES / 256);
-  if (!make_tmap_2d(&p.tmap_a, L.a, L.H, L.T, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&p.tmap_b, L.w_t, L.H, L.I, BK, BN_HALF, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&p.tmap_sf, L.sf, 256, sf_rows, 256, 16, CU_TENSOR_MAP_SWIZZLE_NONE)) {
+  if (!encode_maps([&] {
+        return make_tmap_2d(&p.tmap_a, L.a, L.H, L.T, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) &&
+               make_tmap_2d(&p.tmap_b, L.w_t, L.H, L.I, BK, BN_HALF, CU_TENSOR_MAP_SWIZZLE_128B) &&
+               make_tmap_2d(&p.tmap_sf, L.sf, 256, sf_rows, 256, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+      })) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

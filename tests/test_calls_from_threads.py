@@ -1,6 +1,7 @@
-"""Calls of one kernel from two host threads at a time, of sizes that need different amounts of shared
-memory, each thread on a stream and on tensors of its own: every call is accepted, whatever the other
-thread launches between its checks and its launch, and the results are the oracle's."""
+"""Calls from host threads.  Two threads at a time call one kernel with sizes that need different amounts
+of shared memory, each on a stream and on tensors of its own: every call is accepted, whatever the other
+thread launches between its checks and its launch.  And a call is the first CUDA call that its thread makes.
+The results are the oracle's."""
 import threading
 
 import numpy as np
@@ -8,7 +9,8 @@ import pytest
 import torch
 
 import oracle
-from rope_attention_gb300 import native
+from parity_util import as_f64, check_qkv, qkv_reference
+from rope_attention_gb300 import native, runner, synth
 from test_cache_paging import Pages, dev
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +86,31 @@ def test_paging_calls_of_many_and_of_fewer_requests():
     beside_one_another(calls, 2000)
     for c in calls:
         c.check()
+
+
+@pytest.mark.parametrize("layout", [native.RA_LAYOUT_BSD, native.RA_LAYOUT_NBSD], ids=["bsd", "nbsd"])
+@pytest.mark.parametrize("first", ["project", "norm_rope"])
+def test_a_projection_call_is_its_threads_first(first, layout):
+    c = synth.make_qkv("threads_first", 60, S=64, H=256, num_heads=2, num_kv_heads=2, head_dim=64)
+    r = runner.QkvRun(c, layout=layout)
+    stream, errors = torch.cuda.Stream(), []
+    if first == "norm_rope":
+        r.project(stream)
+
+    def work():
+        try:
+            if first == "project":
+                r.project(stream)
+            r.norm_rope(stream)
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert r.status() == 0
+    out = r.out if layout == native.RA_LAYOUT_BSD else r.out.permute(1, 0, 2).reshape(c.T, c.I)
+    check_qkv(c, as_f64(out), qkv_reference(c), "a thread's first call")
