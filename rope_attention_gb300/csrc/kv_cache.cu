@@ -692,6 +692,7 @@ __global__ void __launch_bounds__(StagedShape<VARIANT>::THREADS, StagedShape<VAR
 #pragma unroll
     for (int step = 0; step < T::STEPS; ++step) {
       const int lr = (warp * T::STEPS + step) * T::RPG + g;  // row within the tile
+      const uint32_t row = r0 + lr;
       RowIn<T::CPL> in;
       const uint8_t* x = st + lr * T::DKV * 2;
 #pragma unroll
@@ -707,7 +708,8 @@ __global__ void __launch_bounds__(StagedShape<VARIANT>::THREADS, StagedShape<VAR
       }
       if (j < T::R / 8) {
         if (bcast) {  // cos/sin [B, N, 1, R]: the row of this (b, n), from the cache hierarchy
-          const size_t off = static_cast<size_t>(bn_s[s * T::TILE + lr]) * T::R;
+          // (rows behind the last have no entry in bn_s: what stands there may be any number)
+          const size_t off = row < rows ? static_cast<size_t>(bn_s[s * T::TILE + lr]) * T::R : 0;
           const uint16_t* cg = p.cos + off;
           const uint16_t* sg = p.sin + off;
           in.c1 = __ldg(reinterpret_cast<const uint2*>(cg + 4 * j));
@@ -726,7 +728,6 @@ __global__ void __launch_bounds__(StagedShape<VARIANT>::THREADS, StagedShape<VAR
       in.slot = slot_s[s * T::TILE + lr];
       in.n = head_s[s * T::TILE + lr];
       in.aux = GEN ? aux_s[s * T::TILE + lr] : 0;
-      const uint32_t row = r0 + lr;
       w.process(in, row, row < rows);
     }
     __syncwarp();
