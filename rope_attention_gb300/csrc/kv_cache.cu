@@ -738,11 +738,10 @@ __global__ void __launch_bounds__(StagedShape<VARIANT>::THREADS, StagedShape<VAR
 template <int VARIANT, bool F16, bool GEN>
 cudaError_t launch_staged(const KvLaunch& L, const KvAux& aux, cudaStream_t st) {
   using T = StagedShape<VARIANT>;
-  auto kernel = kv_staged_kernel<VARIANT, F16, GEN>;
+  constexpr auto kernel = kv_staged_kernel<VARIANT, F16, GEN>;
   const StagedPlan pl =
       staged_plan(static_cast<uint32_t>(quant_table_bytes(L, L.kq != 0, L.vq != 0, T::SPLIT)), T::STAGE_B, T::TILE);
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(pl.total));
+  const cudaError_t e = allow_all_shared_memory<kernel>();
   if (e != cudaSuccess) return e;
   const int64_t rows = L.B * L.N * L.S;
   const uint32_t tiles = static_cast<uint32_t>((rows + T::TILE - 1) / T::TILE);
@@ -770,11 +769,10 @@ unsigned persistent_grid(K kernel, int64_t rows, size_t smem) {
 
 template <int VARIANT, int LPR, int CPL, bool F16, bool GEN>
 cudaError_t launch_one(const KvLaunch& L, const KvAux& aux, cudaStream_t st) {
-  auto kernel = kv_rms_norm_rope_cache_kernel<VARIANT, LPR, CPL, F16, GEN>;
+  constexpr auto kernel = kv_rms_norm_rope_cache_kernel<VARIANT, LPR, CPL, F16, GEN>;
   const size_t smem = quant_table_bytes(L, L.kq != 0, L.vq != 0, true);
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_all_shared_memory<kernel>();
     if (e != cudaSuccess) return e;
   }
   const unsigned grid = persistent_grid(kernel, L.B * L.N * L.S, smem);

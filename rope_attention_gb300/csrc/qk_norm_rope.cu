@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kStThreads, 2)
 
 template <int D, bool ROT>
 cudaError_t launch_staged(const NormRopeLaunch& L, const StagePlan& pl, cudaStream_t st) {
-  auto kernel = qk_norm_rope_staged_kernel<D, ROT>;
+  constexpr auto kernel = qk_norm_rope_staged_kernel<D, ROT>;
   const size_t smem = static_cast<size_t>(kSt) * pl.bytes + 3 * kSt * 8 + 16;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_all_shared_memory<kernel>();
   if (e != cudaSuccess) return e;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kStThreads, smem) != cudaSuccess || per_sm < 1)
@@ -627,9 +627,9 @@ cudaError_t launch_nbsd(const NormRopeLaunch& L, const NbPlan& pl, cudaStream_t 
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
       }))
     return cudaErrorInvalidValue;
-  auto kernel = qk_norm_rope_nbsd_kernel<D, ROT>;
+  constexpr auto kernel = qk_norm_rope_nbsd_kernel<D, ROT>;
   const size_t smem = nb_smem(pl);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_all_shared_memory<kernel>();
   if (e != cudaSuccess) return e;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kNbThreads, smem) != cudaSuccess || per_sm < 1)

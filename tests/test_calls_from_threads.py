@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from parity_util import as_f64, check_qkv, qkv_reference
+from parity_util import as_f64, check_kv, check_qkv, qkv_reference
 from rope_attention_gb300 import native, runner, synth
 from test_cache_paging import Pages, dev
 
@@ -114,3 +114,34 @@ def test_a_projection_call_is_its_threads_first(first, layout):
     assert r.status() == 0
     out = r.out if layout == native.RA_LAYOUT_BSD else r.out.permute(1, 0, 2).reshape(c.T, c.I)
     check_qkv(c, as_f64(out), qkv_reference(c), "a thread's first call")
+
+
+KV = dict(variant=2, B=2, block_size=32, skip_frac=0.1)
+KV_PAIRS = {
+    "pipelined": (dict(N=8, S=21, Dkv=192, Dv=128, quant_k=True, quant_v=True), dict(N=8, S=21, Dkv=192, Dv=128)),
+    "register": (dict(N=8, S=9, Dkv=512, Dv=512, quant_k=True, quant_v=True), dict(N=8, S=9, Dkv=512, Dv=256, quant_k=True, quant_v=True)),
+}
+
+
+@pytest.mark.parametrize("name", KV_PAIRS)
+def test_cache_writers_of_wide_and_of_narrow_tables(name):
+    cases = [synth.make_kv(f"threads_{name}_{i}", 40 + i, **KV, **kw) for i, kw in enumerate(KV_PAIRS[name])]
+    runs = [runner.KvRun(c) for c in cases]
+    beside_one_another([r.run for r in runs], 4000)
+    assert native.kv_rms_norm_rope_cache_status() == 0
+    for c, r in zip(cases, runs):
+        r.err.zero_()
+        r.run()
+        torch.cuda.synchronize()
+        check_kv(c, r, name)
+
+
+@pytest.mark.parametrize("layout", [native.RA_LAYOUT_BSD, native.RA_LAYOUT_NBSD], ids=["bsd", "nbsd"])
+def test_norm_passes_of_many_and_of_few_heads(layout):
+    cases = [synth.make_qkv(f"threads_{n}", 50 + n, S=64, H=256, num_heads=n, num_kv_heads=n, head_dim=64) for n in (12, 2)]
+    runs = [runner.QkvRun(c, layout=layout) for c in cases]
+    beside_one_another([r.run for r in runs], 4000)
+    for c, r in zip(cases, runs):
+        assert r.status() == 0
+        out = r.out if layout == native.RA_LAYOUT_BSD else r.out.permute(1, 0, 2).reshape(c.T, c.I)
+        check_qkv(c, as_f64(out), qkv_reference(c), "threads")
