@@ -530,7 +530,7 @@ PrefixPlan prefix_plan(const ra::PagedLaunch& L, const attention_prefix* x) {
   p.rows = std::max(p.partials + next_256(ra::paged_attention_workspace(L) - ra::kAttnHeader),
                     next_256(ra::paged_attention_workspace(behind_prefix(L, x, &given, &given))));
   p.stats = p.rows + next_256(rows * L.Dv * sizeof(float) + 32);
-  p.bytes = p.stats + next_256(rows * sizeof(float2) + 32);
+  p.bytes = p.stats + next_256(rows * sizeof(float4) + 32);
   return p;
 }
 }  // namespace
@@ -1015,7 +1015,7 @@ static ra_status paged_call(const kv_rms_norm_rope_cache_params* cache, const pa
     ra::PagedLaunch own = L, over = over_prefix(L, x);
     own.lse = nullptr;
     own.rows_out = reinterpret_cast<float*>(aligned_in(ws, plan.rows));
-    own.stats_out = reinterpret_cast<float2*>(aligned_in(ws, plan.stats));
+    own.stats_out = reinterpret_cast<float4*>(aligned_in(ws, plan.stats));
     own.partials = ws + plan.partials;
     over.seq_lens = prefix_len;
     over.table = prefix_table;

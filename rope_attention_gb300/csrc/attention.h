@@ -52,9 +52,10 @@ struct PagedLaunch {
   // sequences for one's (cu_step: cu_q[0] .. cu_q[cu_step]) and joins its rows with those (prior).
   int32_t cu_step;             // entries of cu_q to a sequence's end: 1 but in the second call
   float* rows_out;             // [total_q, heads, Dv], or null
-  float2* stats_out;           // [total_q, heads]: (log2 of the sum, the lse's share of the key offsets)
+  float4* stats_out;           // [total_q, heads]: (log2 of the largest weight, the sum of the weights over it, the
+                               // lse's share of the key offsets, 0)
   const float* prior;
-  const float2* prior_stats;
+  const float4* prior_stats;
   int32_t shifts;              // the second call writes the lse: that share is wanted
   const int32_t *prefix_len, *prefix_table;
   int64_t prefix_entries, max_prefix_len;

@@ -71,39 +71,31 @@ struct SharedPrefix {
 };
 __device__ __forceinline__ int32_t prefix_length(const SharedPrefix& x) { return x.len ? min(max(__ldg(x.len), 0), x.cap) : 0; }
 
-// Rows that another call's rows join (attention.h, PagedLaunch): its results in fp32, with log2 of
-// their sums of exponentials and the lse's share of the key offsets.
+// Rows that another call's rows join (attention.h, PagedLaunch): its results in fp32, with their
+// statistics.
 struct Prior {
   float* rows_out;
-  float2* stats_out;
+  float4* stats_out;
   const float* rows;
-  const float2* stats;
+  const float4* stats;
 };
-// Shares of a row's two results, in x (its own) and y (the prior's), and log2 of the sum of both.
-// A side that saw nothing has -inf; a NaN on either side makes the row NaN.
-__device__ __forceinline__ float prior_shares(float own, float prior, float2& share) {
-  if (own == neg_inf() && prior == neg_inf()) {
-    share = make_float2(0.f, 0.f);
-    return own;
-  }
-  const float m = fmaxf(own, prior);
-  const float a = ex2(own - m), b = ex2(prior - m), sum = a + b;
-  share = make_float2(a / sum, b / sum);
-  return m + log2f(sum);
-}
 
 // The end of row `at`: m (log2) and l its statistics, k0 the lse's share of the key offsets (0 where
-// l is).  They go out, or the prior's are weighed with them.
+// l is).  They go out, or the prior's are weighed with them: share.x is the row's own, share.y the prior's.
+// The maxima go from one call to the other by themselves: their difference is exact, where log2 of a whole sum,
+// m + log2 l, is rounded by up to |m| 2^-24, which for large scores is more than the rows' own rounding.
+// A side that saw nothing has l = 0 (and counts for nothing whatever its m); a NaN on either side makes the row NaN.
 __device__ __forceinline__ void prior_end(const Prior& p, int64_t at, float m, float l, float k0, bool writes, float* lse,
-                                          float2& share, const float2* have = nullptr) {
-  const float own = l != 0.f ? m + log2f(l) : neg_inf();
+                                          float2& share, const float4* have = nullptr) {
   if (p.stats_out) {
-    if (writes) p.stats_out[at] = make_float2(own, k0);
+    if (writes) p.stats_out[at] = make_float4(m, l, k0, 0.f);
     return;
   }
-  const float2 o = have ? *have : p.stats[at];
-  const float sum = prior_shares(own, o.x, share);
-  if (writes && lse) lse[at] = sum != neg_inf() ? sum * 0.6931471805599453f + (l != 0.f ? k0 : o.y) : neg_inf();
+  const float4 o = have ? *have : p.stats[at];
+  const float own_m = l != 0.f ? m : neg_inf(), prior_m = o.y != 0.f ? o.x : neg_inf(), top = fmaxf(own_m, prior_m);
+  const float own = l != 0.f ? l * ex2(own_m - top) : 0.f, prior = o.y != 0.f ? o.y * ex2(prior_m - top) : 0.f, sum = own + prior;
+  share = sum != 0.f ? make_float2(own / sum, prior / sum) : make_float2(0.f, 0.f);
+  if (writes && lse) lse[at] = sum != 0.f ? top * 0.6931471805599453f + logf(sum) + (l != 0.f ? k0 : o.z) : neg_inf();
 }
 
 // A part of block c is its first piece (slot 2 c) where the item began before the block's
@@ -190,7 +182,7 @@ __device__ __forceinline__ void join_lse(const JoinParams& p, const JoinRow& row
 // looked up and weighed (share); `writes` in the thread that writes them.
 template <bool EXT>
 __device__ __forceinline__ float2 join_row_end(const JoinParams& p, const JoinRow& row, float m, float l, float k0, bool writes,
-                                               const float2* have = nullptr) {
+                                               const float4* have = nullptr) {
   float2 share = make_float2(1.f, 0.f);
   if constexpr (EXT) {
     if (p.prior.stats_out || p.prior.stats) {

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kTokenThreads, 1) paged_tokens_kernel(const __
       const int32_t n = w.n, ta = w.ta, ahead = w.ahead, skip = w.skip;
       // the rows of another call that this one's join: on their way from here
       float4 prior[NT];
-      float2 prior_stats[NT];
+      float4 prior_stats[NT];
       if (p.join.prior.rows && w.whole) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
