@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) slots_kernel(const __grid_con
     }
   }
   if (bad > 0 && L.err_count) atomicAdd(L.err_count, bad);
+  __syncwarp();                             // (lanes leave the loop after different turns; the wait is the warp's)
   if (EXTEND && PART == kBoth) cluster_wait();  // every block has read lengths and count
   if (blockIdx.x != 0) return;
   for (int32_t b = tid; b < B; b += threads) {
