@@ -178,11 +178,14 @@ class PagedAttentionRun:
     """paged_attention of query tokens q [total_q, heads, Dkv] over the caches of a KvRun.
     ``table`` [B, pages] int32 (None in Norm mode), ``lens`` [B] and ``starts`` [B + 1] lists.
     With a ``window`` (a native.AttentionWindow) paged_window_attention; with a ``prefix``
-    (its length and its pages' table) paged_prefix_attention, behind that prefix."""
+    (its length and its pages' table) paged_prefix_attention, behind that prefix.  There is no
+    call with both (ValueError)."""
 
     def __init__(self, kv: KvRun, q: torch.Tensor, lens: list[int], table=None, starts: list[int] | None = None,
                  causal: bool = True, scale: float | None = None, window: native.AttentionWindow | None = None,
                  prefix: tuple | None = None):
+        if window is not None and prefix is not None:
+            raise ValueError("window and prefix: no call has a window behind a shared prefix")
         c, device = kv.case, q.device
         self.kv, self.q = kv, q
         i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).to(device)
