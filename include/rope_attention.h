@@ -630,15 +630,17 @@ ra_status paged_prefix_attention(const kv_rms_norm_rope_cache_params* cache, con
  *                 paged_attention takes it.
  *   free_pages    [block_num] int32: a stack of pages that no request has, the first
  *                 *free_count entries of it; the last of these is taken first.
- * Requests' lengths are clamped to [0, block_table_stride * block_size] and *free_count
- * to [0, block_num]. */
+ * Requests' lengths are clamped to what a row of the table holds, block_table_stride *
+ * block_size positions and at most 2^31 - 256 (as the attention calls take), and
+ * *free_count to [0, block_num]. */
 typedef struct {
   int64_t B;                  /* requests, 1 .. 16384                                  */
   int64_t block_num;          /* pages of the cache                                    */
   int64_t block_size;         /* slots per page                                        */
   int64_t block_table_stride; /* entries per row of block_table; with B rows at most
                                  2^31 - 256                                            */
-  int64_t max_tokens;         /* entries of index, <= 2^30 (kv_cache_truncate: any)    */
+  int64_t max_tokens;         /* entries of index, 1 .. 2^30 (kv_cache_truncate, which
+                                 has no index, checks it all the same)                 */
 } kv_cache_paging_params;
 
 /* Makes room for new_tokens[b] more tokens of each request b (below 0: none), in the
@@ -674,7 +676,11 @@ ra_status kv_cache_slots(const kv_cache_paging_params* p, const int32_t* starts,
  * kv_cache_extend takes them in the same order again.  new_seq_lens and new_free_count may
  * be seq_lens and free_count themselves; block_table is left as it is (entries behind a
  * sequence's end are not read).  Entries outside [0, block_num) are left out, and so are
- * pages that the list has no room for; dev_error_count (optional) counts both. */
+ * pages that the list has no room for; dev_error_count (optional) counts both.
+ * Every other entry goes on the list, whoever has the page: entries of pages that were
+ * given away before (paged_window_attention lets a request do without those that left its
+ * window) must be outside [0, block_num) by then, -1 for example, or a page that another
+ * request has would be handed out a second time.  Those -1 are counted too. */
 ra_status kv_cache_truncate(const kv_cache_paging_params* p, const int32_t* keep, const int32_t* seq_lens,
                             const int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
                             int32_t* new_seq_lens, int32_t* new_free_count, int32_t* dev_error_count,
