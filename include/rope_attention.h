@@ -562,8 +562,10 @@ typedef struct {
 } attention_window;
 
 /* packed_attention with a window: arguments, precision and workspace are that call's
- * (packed_attention_workspace_bytes); `causal` must be 1.  The time goes with the keys
- * that are seen, not with all. */
+ * (packed_attention_workspace_bytes); `causal` must be 1.  Tiles of 128 keys that no query
+ * of 256 sees are left out, and those at both edges of a window, and of the sinks, are
+ * computed whole: long prompts in short windows take less time than without, prompts of
+ * few windows' length do not. */
 ra_status packed_window_attention(const packed_attention_params* p, const attention_window* window,
                                   const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* out,
                                   float* lse, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
@@ -600,7 +602,9 @@ ra_status paged_prefix_attention_workspace_bytes(const kv_rms_norm_rope_cache_pa
                                                  const attention_prefix* prefix, size_t* bytes);
 
 /* paged_attention of sequences behind a shared prefix, whose keys are read once for the
- * rows of all of them where that takes less time.  The keys of sequence b are the prefix's positions, which every
+ * rows of all of them where that takes less time (as the host counts it, from B, total_q
+ * and the bounds max_prefix_len and max_seq_len, not from the lengths on the device: a
+ * step captured with bounds for a full cache has the choice for full lengths).  The keys of sequence b are the prefix's positions, which every
  * query of the call sees, then its own: seq_lens, max_seq_len and block_table count and
  * hold its own positions alone, of which its queries see those that paged_attention
  * lets them see.

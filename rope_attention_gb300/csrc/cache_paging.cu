@@ -16,8 +16,8 @@
 // read, once every block of the cluster has read them, and no second launch is needed.  An extend by
 // more tokens than a cluster writes as fast as all SMs is two launches: the tokens, then the state.
 // Bound by latency: a launch, three dependent loads and a scan.  Measured: 256 requests and a token each
-// 5.1 us; 36000 tokens for 16 requests 8.3 (12.3 with four blocks, 8.2 with sixteen); 18700 pages of 300 requests
-// back 8.2.
+// 5.1 to 6.2 us; 33000 tokens for 16 requests 8.5 to 9.7 (12.3 with four blocks; sixteen are no faster); 18700 pages of
+// 300 requests back 8.2, 3000 requests of up to 9000 tokens in pages of 16 99.
 #include <algorithm>
 
 #include "cache_paging.h"

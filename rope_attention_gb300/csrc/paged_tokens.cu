@@ -15,15 +15,17 @@
 //    the same: a lane takes 16 neighbouring channels of its keys for four steps (q is laid out to match), and
 //    of the values 16 neighbouring channels of four keys, whose bytes it interleaves.  Rows of 192 and
 //    64 bytes, and of 128 with the swizzle, then have no bank conflicts.
-//  * Another warp walks the block table and issues TMA boxes of 16 to 64 keys, two to twelve tiles ahead:
-//    whole rows of codes, 128 bytes of 16-bit ones.  A third walks the pieces ahead of the others and
-//    lays out their queries.
+//  * Another warp walks the block table and issues TMA boxes of 16 to 64 keys into two to twelve stages:
+//    whole rows of codes, 128 bytes of 16-bit ones.  (Two, one for each team, are what 16-bit rows of 192 + 128
+//    channels and 9 to 16 rows leave room for: a team's next tile is on its way only when it has freed the
+//    last.)  A third walks the pieces ahead of the others and lays out their queries.
 // The runs of tiles, their parts and the join are paged_rows.cuh's.  The maximum follows only when a
 // tile exceeds it by 2^kLazy.  Every wait on an mbarrier is bounded in time (status word); the warps meet
 // at the end of a piece and leave it, or the loop, together.
 // Measured: 8 sequences, 64 heads over 8, int8, 4096 positions in the window and 64 sinks 35 us, of which 28 tiles a
 // block are 15 (5.6 TB/s while they run), a block's start 6 and the join 7 (57 us in paged_rows.cuh's kernel); 16 rows
-// of 541 bf16 positions 14 us.  Bound by latency: the start, the join, and a tile's chain of loads, conversion, S, softmax and O.
+// of 541 bf16 positions 14 us.  The same window over bf16 rows: 64 heads (four stages) 41 us, 4.1 TB/s; 128 heads, two stages,
+// 51 us, 3.4 TB/s.  Bound by latency: the start, the join, and a tile's chain of loads, conversion, S, softmax and O.
 #include "paged_tokens.cuh"
 
 namespace ra {

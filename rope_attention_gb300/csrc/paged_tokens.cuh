@@ -49,10 +49,13 @@ inline void plan_tokens(const PagedLaunch& L, Plan* pl) {
   // where the warps' results meet, and two pieces' queries
   const int meet = kTokenWarps * pl->NR * kTokenRow * 4 + 2 * pl->NR / 8 * 24 * 32 * 4;
   const int fixed = meet + ((static_cast<int>(sizeof(TokenMisc)) + 15) & ~15);
-  // As many for each team: a stage then is always one team's, which waits for its uses one after the other.  (A
-  // wait knows a use of a stage from the one before by a parity alone.  With an odd number the teams take turns on
-  // a stage, and one could come to it while the copy of the other's tile, issued earlier, had still not landed,
-  // and take that for its own.)
+  // As many for each team: within a piece a stage then is always one team's, which waits for its uses one after the
+  // other.  (A wait knows a use of a stage from the one before by a parity alone.  With an odd number the teams take
+  // turns on a stage, and one could come to it while the copy of the other's tile, issued earlier, had still not
+  // landed, and take that for its own.)  From one piece to the next the teams may change places, as the team goes
+  // by the tile's number in its piece and the stage by the running one: behind a piece with an odd number of
+  // tiles they do.  Both teams meet at the end of a piece (bar_or), where every copy of it has landed and been used; a team
+  // that went on without that would bring the fault back.
   pl->ns = std::min(kTokenStages, (kSmemMax - fixed) / pl->stage) / kTeams * kTeams;
   pl->off_p = pl->ns * pl->stage;
   pl->off_misc = pl->off_p + meet;
